@@ -64,8 +64,10 @@ typedef enum {
 #define RLK_DEVERR_TARGET_RANGE 0x1u   /* an active row's target id is outside [0, V) */
 #define RLK_DEVERR_WAIT_TIMEOUT 0x2u   /* a pipeline wait gave up (the results are invalid) */
 #define RLK_DEVERR_ROW_RANGE 0x4u      /* an entry of a row-index list is outside [0, N) */
+#define RLK_DEVERR_LOGITS 0x8u         /* an active row's logits hold NaN or +inf, or only -inf */
+#define RLK_DEVERR_SAMPLE_PARAM 0x10u  /* an active row's sampling setting is out of its range */
 
-/* element type of rlk_logp_from_logits' logits */
+/* element type of logits, norm rows and norm parameters */
 #define RLK_DTYPE_F32 0
 #define RLK_DTYPE_BF16 1
 
@@ -507,6 +509,107 @@ rlk_status_t rlk_dlogp_audit_ext(const float* logp_new, const float* logp_old,
 rlk_status_t rlk_dlogp_audit_noalloc(const float* logp_new, const float* logp_old,
                                      const uint8_t* active_mask, int64_t N,
                                      rlk_audit_result_t* result_dev, cudaStream_t stream);
+
+/*
+ * Layer norm and RMS norm, forward and backward: the norm that makes the LM head's hidden
+ * states and takes dhidden back.  "RL-Kernel Roadmap (2026)", WS1: batch-invariant RMSNorm
+ * forward and backward next to the batch-invariant log-prob.  Per row of x [N,H]:
+ *
+ *   mean = sum x / H,  rstd = 1 / sqrt( sum (x - mean)^2 / H + eps )
+ *   y = (x - mean) rstd w + b                     (RMS norm: mean = 0, no b)
+ *   dx = rstd (g - mean_H(g) - xh mean_H(g xh)),  g = dy w, xh = (x - mean) rstd
+ *   dw = sum_t dy xh,  db = sum_t dy              (RMS norm: no mean_H(g), no db)
+ *
+ *   x, dy, y, dx   x_dtype (fp32 or bf16), rows contiguous, row strides in elements
+ *               (>= H); aligned to their element, 16-byte rows are read faster.  Outputs
+ *               must not overlap inputs.
+ *   weight, bias   [H], w_dtype (fp32 or bf16, independent of x's); bias may be NULL
+ *   active_mask [N] uint8 or NULL: rows of mask 0 are never read; their y and dx rows and
+ *               statistics are 0, and they add nothing to dweight and dbias
+ *   eps         finite, >= 0
+ *   mean_out, rstd_out  [N] fp32 or NULL: what the backward takes back
+ *   dweight, dbias [H] w_dtype, overwritten; either may be NULL
+ *   workspace   rlk_*_norm_bwd_workspace_bytes(N, H), 256-aligned (needed when dweight or
+ *               dbias is asked for); its contents on entry do not matter
+ * 1 <= H <= 2^24, any value; 0 <= N <= 2^31 - 2^16.  N = 0: the forward enqueues nothing,
+ * the backward writes dweight = dbias = 0.  Arithmetic is fp32 with one rounding to the
+ * output type; a row's y, dx and statistics do not depend on the batch it is in, on its
+ * position or on alignment, and dweight and dbias are bitwise reproducible (no atomics).
+ * Rows up to 16384 columns are read once; wider ones once for each step.
+ */
+rlk_status_t rlk_layer_norm_fwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                                const void* weight, const void* bias, int32_t w_dtype,
+                                const uint8_t* active_mask, int64_t N, int64_t H, double eps,
+                                void* y, int64_t y_stride, float* mean_out, float* rstd_out,
+                                cudaStream_t stream);
+size_t rlk_layer_norm_bwd_workspace_bytes(int64_t N, int64_t H);
+rlk_status_t rlk_layer_norm_bwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                                const void* weight, int32_t w_dtype, const void* dy,
+                                int64_t dy_stride, const float* mean, const float* rstd,
+                                const uint8_t* active_mask, int64_t N, int64_t H, void* dx,
+                                int64_t dx_stride, void* dweight, void* dbias, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+rlk_status_t rlk_rms_norm_fwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                              const void* weight, int32_t w_dtype, const uint8_t* active_mask,
+                              int64_t N, int64_t H, double eps, void* y, int64_t y_stride,
+                              float* rstd_out, cudaStream_t stream);
+size_t rlk_rms_norm_bwd_workspace_bytes(int64_t N, int64_t H);
+rlk_status_t rlk_rms_norm_bwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                              const void* weight, int32_t w_dtype, const void* dy,
+                              int64_t dy_stride, const float* rstd, const uint8_t* active_mask,
+                              int64_t N, int64_t H, void* dx, int64_t dx_stride, void* dweight,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Settings of rlk_sample_logits (a host structure, read during the call).  A *_rows member
+ * is a device array with one value a row, or NULL: then the scalar holds for every row. */
+typedef struct {
+    const float* temperature_rows;
+    const int32_t* top_k_rows;
+    const float* top_p_rows;
+    const float* min_p_rows;
+    double temperature;   /* 1e-6 .. 1e6 */
+    int64_t top_k;        /* >= 0; 0 or >= V: off */
+    double top_p;         /* > 0; >= 1: off */
+    double min_p;         /* 0 .. 1; 0: off */
+} rlk_sample_params_t;
+
+/*
+ * Sampling from logits with given random numbers: the rollout's draw, and the logp it is
+ * audited against ("RL-Kernel integration roadmap for vime", Consistency Contract: old
+ * logp at the rollout temperature).  For an active row x_v with uniform u in [0, 1):
+ *
+ *   w_v  = exp((x_v - max x) / T);  order: x descending, lowest index first among equals
+ *   n_k  = top_k (V when off);  S_n = sum of the order's first n weights
+ *   n_p  = min{ n : S_n >= top_p S_{n_k} } (n_k when off);  n_m = #{ v : w_v >= min_p }
+ *   kept = the order's first min(n_k, n_p, n_m)
+ *   token = the first kept v, in index order, whose running sum of kept weights exceeds
+ *           u times their total
+ *   logp = x_token/T - log sum_v exp(x_v/T)        (all v: rlk_logp_from_logits' value)
+ *   kept_logp = the same with the sum over the kept tokens (the truncated distribution's)
+ *
+ * Greedy decoding is top_k = 1.  -inf entries (banned tokens) are never drawn.
+ *
+ *   logits      [N, row_stride] (V <= row_stride used), fp32 or bf16, aligned to the element
+ *   uniforms    [N] fp32
+ *   active_mask [N] uint8 or NULL; inactive rows give token -1, logp 0, and are never read
+ *   tokens_out  [N] int64; logp_out, kept_logp_out [N] fp32 or NULL
+ *   workspace   rlk_sample_logits_workspace_bytes(N, V) bytes, 256-aligned (may be NULL when
+ *               that is 0); its contents on entry do not matter
+ * Sums of weights are 64-bit integers of about 40 correct bits, so the token is that of
+ * exact arithmetic unless u times the total lies within about 1e-12 of a border, and it
+ * depends on the row alone (not on the batch, the mask or alignment).  V <= 2^22
+ * (RLK_ERR_UNSUPPORTED above).  A row with NaN or +inf, or with nothing above -inf, gives
+ * token -1, logp NaN and RLK_DEVERR_LOGITS; a row whose own settings or uniform are out of
+ * range gives the same with RLK_DEVERR_SAMPLE_PARAM.  Scalar settings out of range are
+ * RLK_ERR_INVALID_VALUE.
+ */
+size_t rlk_sample_logits_workspace_bytes(int64_t N, int64_t V);
+rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                               int64_t row_stride, const float* uniforms,
+                               const uint8_t* active_mask, const rlk_sample_params_t* params,
+                               int64_t* tokens_out, float* logp_out, float* kept_logp_out,
+                               void* workspace, size_t workspace_bytes,
+                               uint32_t* device_error_word, cudaStream_t stream);
 
 /* Build fingerprint and the fixed numeric contract (tile shapes, chunk widths,
  * accumulation and rounding points).  Static string, never NULL. */

@@ -28,6 +28,8 @@ RLK_OK, RLK_ERR_INVALID_VALUE, RLK_ERR_UNSUPPORTED, RLK_ERR_WORKSPACE, RLK_ERR_L
 RLK_DEVERR_TARGET_RANGE = 0x1
 RLK_DEVERR_WAIT_TIMEOUT = 0x2
 RLK_DEVERR_ROW_RANGE = 0x4
+RLK_DEVERR_LOGITS = 0x8
+RLK_DEVERR_SAMPLE_PARAM = 0x10
 RLK_DTYPE_F32, RLK_DTYPE_BF16 = 0, 1
 RLK_AUDIT_NOALLOC_MAX_N = 1 << 27
 
@@ -84,6 +86,20 @@ class GrpoResult(ctypes.Structure):
 
 
 GRPO_RESULT_BYTES = ctypes.sizeof(GrpoResult)
+
+
+class SampleParams(ctypes.Structure):
+    """Mirror of rlk_sample_params_t (a host structure)."""
+    _fields_ = [
+        ("temperature_rows", ctypes.c_void_p),
+        ("top_k_rows", ctypes.c_void_p),
+        ("top_p_rows", ctypes.c_void_p),
+        ("min_p_rows", ctypes.c_void_p),
+        ("temperature", ctypes.c_double),
+        ("top_k", ctypes.c_int64),
+        ("top_p", ctypes.c_double),
+        ("min_p", ctypes.c_double),
+    ]
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -166,6 +182,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                         _vp, _sz, _vp]
     lib.rlk_dlogp_audit_noalloc.restype = ctypes.c_int
     lib.rlk_dlogp_audit_noalloc.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp]
+    i32, f64 = ctypes.c_int32, ctypes.c_double
+    for name, args in (
+            ("rlk_layer_norm_fwd", [_vp, i32, _i64, _vp, _vp, i32, _vp, _i64, _i64, f64, _vp,
+                                    _i64, _vp, _vp, _vp]),
+            ("rlk_layer_norm_bwd", [_vp, i32, _i64, _vp, i32, _vp, _i64, _vp, _vp, _vp, _i64,
+                                    _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+            ("rlk_rms_norm_fwd", [_vp, i32, _i64, _vp, i32, _vp, _i64, _i64, f64, _vp, _i64, _vp,
+                                  _vp]),
+            ("rlk_rms_norm_bwd", [_vp, i32, _i64, _vp, i32, _vp, _i64, _vp, _vp, _i64, _i64, _vp,
+                                  _i64, _vp, _vp, _sz, _vp]),
+            ("rlk_sample_logits", [_vp, i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _sz, _vp, _vp])):
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name).argtypes = args
+    for name in ("rlk_layer_norm_bwd_workspace_bytes", "rlk_rms_norm_bwd_workspace_bytes",
+                 "rlk_sample_logits_workspace_bytes"):
+        getattr(lib, name).restype = _sz
+        getattr(lib, name).argtypes = [_i64, _i64]
     lib.rlk_contract_string.restype = ctypes.c_char_p
     lib.rlk_contract_string.argtypes = []
     lib.rlk_status_string.restype = ctypes.c_char_p
@@ -215,6 +249,18 @@ def rlk_dlogp_audit_ext_workspace_bytes(N: int) -> int:
 
 def rlk_grpo_clip_loss_workspace_bytes(N: int) -> int:
     return int(load().rlk_grpo_clip_loss_workspace_bytes(N))
+
+
+def rlk_layer_norm_bwd_workspace_bytes(N: int, H: int) -> int:
+    return int(load().rlk_layer_norm_bwd_workspace_bytes(N, H))
+
+
+def rlk_rms_norm_bwd_workspace_bytes(N: int, H: int) -> int:
+    return int(load().rlk_rms_norm_bwd_workspace_bytes(N, H))
+
+
+def rlk_sample_logits_workspace_bytes(N: int, V: int) -> int:
+    return int(load().rlk_sample_logits_workspace_bytes(N, V))
 
 
 # ----------------------------------------------------------------------------- marshalling
@@ -620,6 +666,156 @@ def rlk_grpo_clip_loss(logp_new, logp_old, advantages, active_mask, eps_low, eps
     _check("rlk_grpo_clip_loss", st)
 
 
+def _dtype_code(t, name):
+    if t.dtype == torch.float32:
+        return RLK_DTYPE_F32
+    if t.dtype == torch.bfloat16:
+        return RLK_DTYPE_BF16
+    raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+
+
+def _need_rows(t, name, shape=None, dtype=None):
+    """Row stride of a 2-D CUDA tensor with contiguous rows (any stride between them)."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError("%s must be a 2-D CUDA tensor" % name)
+    n, h = t.shape
+    if shape is not None and (n, h) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), (n, h)))
+    if h > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    stride = t.stride(0) if n > 1 else h          # a single row has no stride of its own
+    if stride < h:
+        raise ValueError("%s must not have overlapping rows" % name)
+    return stride
+
+
+def _need_norm(x, weight, active_mask):
+    """(n, h, x's row stride) of the arguments that every norm call has."""
+    stride = _need_rows(x, "x")
+    n, h = x.shape
+    _need(weight, weight.dtype, "weight", (h,))
+    if active_mask is not None:
+        _need(active_mask, torch.uint8, "active_mask", (n,))
+    return n, h, stride
+
+
+def _need_stats(n, **stats):
+    for name, t in stats.items():
+        if t is not None:
+            _need(t, torch.float32, name, (n,))
+
+
+def rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd, stream=None):
+    """Enqueue the layer norm of x [N, H]; bias, active_mask, mean and rstd may be None.  See
+    include/rlk.h."""
+    n, h, sx = _need_norm(x, weight, active_mask)
+    if bias is not None:
+        _need(bias, weight.dtype, "bias", (h,))
+    sy = _need_rows(y, "y", (n, h), x.dtype)
+    _need_stats(n, mean=mean, rstd=rstd)
+    st = load().rlk_layer_norm_fwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight), _ptr(bias),
+                                   _dtype_code(weight, "weight"), _ptr(active_mask), n, h,
+                                   float(eps), _ptr(y), sy, _ptr(mean), _ptr(rstd),
+                                   _stream(stream))
+    _check("rlk_layer_norm_fwd", st)
+
+
+def rlk_layer_norm_bwd(x, weight, dy, mean, rstd, active_mask, dx, dweight, dbias, workspace,
+                       stream=None):
+    """Enqueue the layer norm's backward; dweight and dbias may be None.  See include/rlk.h."""
+    n, h, sx = _need_norm(x, weight, active_mask)
+    sg = _need_rows(dy, "dy", (n, h), x.dtype)
+    sd = _need_rows(dx, "dx", (n, h), x.dtype)
+    _need(mean, torch.float32, "mean", (n,))
+    _need(rstd, torch.float32, "rstd", (n,))
+    for t, name in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            _need(t, weight.dtype, name, (h,))
+    _need(workspace, torch.uint8, "workspace")
+    st = load().rlk_layer_norm_bwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight),
+                                   _dtype_code(weight, "weight"), _ptr(dy), sg, _ptr(mean),
+                                   _ptr(rstd), _ptr(active_mask), n, h, _ptr(dx), sd,
+                                   _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                   workspace.numel(), _stream(stream))
+    _check("rlk_layer_norm_bwd", st)
+
+
+def rlk_rms_norm_fwd(x, weight, active_mask, eps, y, rstd, stream=None):
+    """Enqueue the RMS norm of x [N, H]; active_mask and rstd may be None.  See include/rlk.h."""
+    n, h, sx = _need_norm(x, weight, active_mask)
+    sy = _need_rows(y, "y", (n, h), x.dtype)
+    _need_stats(n, rstd=rstd)
+    st = load().rlk_rms_norm_fwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight),
+                                 _dtype_code(weight, "weight"), _ptr(active_mask), n, h,
+                                 float(eps), _ptr(y), sy, _ptr(rstd), _stream(stream))
+    _check("rlk_rms_norm_fwd", st)
+
+
+def rlk_rms_norm_bwd(x, weight, dy, rstd, active_mask, dx, dweight, workspace, stream=None):
+    """Enqueue the RMS norm's backward; dweight may be None.  See include/rlk.h."""
+    n, h, sx = _need_norm(x, weight, active_mask)
+    sg = _need_rows(dy, "dy", (n, h), x.dtype)
+    sd = _need_rows(dx, "dx", (n, h), x.dtype)
+    _need(rstd, torch.float32, "rstd", (n,))
+    if dweight is not None:
+        _need(dweight, weight.dtype, "dweight", (h,))
+    _need(workspace, torch.uint8, "workspace")
+    st = load().rlk_rms_norm_bwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight),
+                                 _dtype_code(weight, "weight"), _ptr(dy), sg, _ptr(rstd),
+                                 _ptr(active_mask), n, h, _ptr(dx), sd, _ptr(dweight),
+                                 _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("rlk_rms_norm_bwd", st)
+
+
+def _sample_params(n, temperature, top_k, top_p, min_p):
+    """rlk_sample_params_t of four settings, each a number or a CUDA tensor [n]."""
+    p = SampleParams(None, None, None, None, 1.0, 0, 1.0, 0.0)
+    if isinstance(temperature, torch.Tensor):
+        _need(temperature, torch.float32, "temperature", (n,))
+        p.temperature_rows = temperature.data_ptr()
+    else:
+        p.temperature = float(temperature)
+    if isinstance(top_k, torch.Tensor):
+        _need(top_k, torch.int32, "top_k", (n,))
+        p.top_k_rows = top_k.data_ptr()
+    else:
+        p.top_k = int(top_k)
+    if isinstance(top_p, torch.Tensor):
+        _need(top_p, torch.float32, "top_p", (n,))
+        p.top_p_rows = top_p.data_ptr()
+    else:
+        p.top_p = float(top_p)
+    if isinstance(min_p, torch.Tensor):
+        _need(min_p, torch.float32, "min_p", (n,))
+        p.min_p_rows = min_p.data_ptr()
+    else:
+        p.min_p = float(min_p)
+    return p
+
+
+def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, min_p, tokens,
+                      logp, kept_logp, workspace, device_error_word=None, stream=None):
+    """Draw one token a row of logits [N, V] (fp32 or bf16, rows contiguous, any row stride).
+    temperature, top_p, min_p: a number or a float32 tensor [N]; top_k: a number or an int32
+    tensor [N].  active_mask, logp, kept_logp may be None.  See include/rlk.h."""
+    stride = _need_rows(logits, "logits")
+    n, v = logits.shape
+    _need(uniforms, torch.float32, "uniforms", (n,))
+    if active_mask is not None:
+        _need(active_mask, torch.uint8, "active_mask", (n,))
+    _need(tokens, torch.int64, "tokens", (n,))
+    _need_stats(n, logp=logp, kept_logp=kept_logp)
+    _need(workspace, torch.uint8, "workspace")
+    params = _sample_params(n, temperature, top_k, top_p, min_p)
+    st = load().rlk_sample_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
+                                  _ptr(uniforms), _ptr(active_mask), ctypes.byref(params),
+                                  _ptr(tokens), _ptr(logp), _ptr(kept_logp), _ptr(workspace),
+                                  workspace.numel(), _ptr(device_error_word), _stream(stream))
+    _check("rlk_sample_logits", st)
+
+
 # ----------------------------------------------------------------------------- conveniences
 
 def _workspace(nbytes, device):
@@ -752,6 +948,59 @@ def dlogp_audit_ext(logp_new, logp_old, active_mask=None, seq_offsets=None, clip
     return {f: getattr(r, f) for f, _ in AuditExtResult._fields_}
 
 
+def layer_norm_fwd(x, weight, bias=None, eps=1e-6, active_mask=None):
+    """(y [N,H], mean [N], rstd [N]) of x [N,H]."""
+    n, h = x.shape
+    y = torch.empty(n, h, dtype=x.dtype, device=x.device)
+    mean, rstd = (torch.empty(n, dtype=torch.float32, device=x.device) for _ in range(2))
+    rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, weight, dy, mean, rstd, active_mask=None, with_bias=True):
+    """(dx [N,H], dweight [H], dbias [H] or None)."""
+    n, h = x.shape
+    dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(weight) if with_bias else None
+    ws = _workspace(rlk_layer_norm_bwd_workspace_bytes(n, h), x.device)
+    rlk_layer_norm_bwd(x, weight, dy, mean, rstd, active_mask, dx, dw, db, ws)
+    return dx, dw, db
+
+
+def rms_norm_fwd(x, weight, eps=1e-6, active_mask=None):
+    """(y [N,H], rstd [N]) of x [N,H]."""
+    n, h = x.shape
+    y = torch.empty(n, h, dtype=x.dtype, device=x.device)
+    rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+    rlk_rms_norm_fwd(x, weight, active_mask, eps, y, rstd)
+    return y, rstd
+
+
+def rms_norm_bwd(x, weight, dy, rstd, active_mask=None):
+    """(dx [N,H], dweight [H])."""
+    n, h = x.shape
+    dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(weight)
+    ws = _workspace(rlk_rms_norm_bwd_workspace_bytes(n, h), x.device)
+    rlk_rms_norm_bwd(x, weight, dy, rstd, active_mask, dx, dw, ws)
+    return dx, dw
+
+
+def sample_logits(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                  active_mask=None, error_word=None):
+    """(tokens [N] int64, logp [N], kept_logp [N]): the draw from each row's truncated
+    distribution with the given uniforms, its log-probability under the whole distribution
+    (the old logp that the audit compares) and under the truncated one."""
+    n, v = logits.shape
+    tokens = torch.empty(n, dtype=torch.int64, device=logits.device)
+    logp, kept = (torch.empty(n, dtype=torch.float32, device=logits.device) for _ in range(2))
+    ws = _workspace(rlk_sample_logits_workspace_bytes(n, v), logits.device)
+    rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, min_p, tokens,
+                      logp, kept, ws, error_word)
+    return tokens, logp, kept
+
+
 class LinearLogp(torch.autograd.Function):
     """logp = LinearLogp.apply(hidden, weight, targets, active_mask, temperature)."""
 
@@ -831,3 +1080,73 @@ def linear_kl(hidden, weight, hidden_ref, weight_ref, active_mask=None, temperat
     temperature_ref = temperature if temperature_ref is None else temperature_ref
     return LinearKl.apply(hidden, weight, hidden_ref.detach(), weight_ref.detach(), active_mask,
                           temperature, temperature_ref)
+
+
+def _as_rows(t, like=None):
+    """[..., H] as [N, H] rows that the kernels take (copied only if they cannot be a view)."""
+    if like is not None:
+        t = t.to(like.dtype)
+    rows = t.reshape(-1, t.shape[-1])
+    n, h = rows.shape
+    if (h > 1 and rows.stride(1) != 1) or (n > 1 and rows.stride(0) < h):
+        rows = rows.contiguous()                  # an expanded gradient, for instance
+    return rows
+
+
+class LayerNorm(torch.autograd.Function):
+    """y = LayerNorm.apply(x, weight, bias, eps, active_mask)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, active_mask):
+        rows = _as_rows(x)
+        y, mean, rstd = layer_norm_fwd(rows, weight, bias, eps, active_mask)
+        ctx.save_for_backward(rows, weight, mean, rstd, active_mask)
+        return y.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, weight, mean, rstd, active_mask = ctx.saved_tensors
+        n, h = x.shape
+        dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
+        dw = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
+        db = torch.empty_like(weight) if ctx.needs_input_grad[2] else None
+        ws = _workspace(rlk_layer_norm_bwd_workspace_bytes(n, h), x.device)
+        rlk_layer_norm_bwd(x, weight, _as_rows(grad, x), mean, rstd, active_mask, dx, dw, db, ws)
+        return dx.view(grad.shape), dw, db, None, None
+
+
+def layer_norm(x, weight, bias=None, eps=1e-6, active_mask=None):
+    """Differentiable layer norm over the last axis of x [..., H]; active_mask: uint8, one byte
+    a row, in the order of x's leading axes.
+
+    A training step can be captured in a CUDA graph.  As for every autograd operator, an eager
+    graph of the same leaves that is still alive then has to come from the captured stream:
+    autograd joins a leaf's gradient on the stream of the first live graph that used it, and a
+    join with a stream outside the capture ends the capture."""
+    return LayerNorm.apply(x, weight, bias, eps, active_mask)
+
+
+class RmsNorm(torch.autograd.Function):
+    """y = RmsNorm.apply(x, weight, eps, active_mask)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, eps, active_mask):
+        rows = _as_rows(x)
+        y, rstd = rms_norm_fwd(rows, weight, eps, active_mask)
+        ctx.save_for_backward(rows, weight, rstd, active_mask)
+        return y.view(x.shape)
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, weight, rstd, active_mask = ctx.saved_tensors
+        n, h = x.shape
+        dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
+        dw = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
+        ws = _workspace(rlk_rms_norm_bwd_workspace_bytes(n, h), x.device)
+        rlk_rms_norm_bwd(x, weight, _as_rows(grad, x), rstd, active_mask, dx, dw, ws)
+        return dx.view(grad.shape), dw, None, None
+
+
+def rms_norm(x, weight, eps=1e-6, active_mask=None):
+    """Differentiable RMS norm over the last axis of x [..., H]."""
+    return RmsNorm.apply(x, weight, eps, active_mask)

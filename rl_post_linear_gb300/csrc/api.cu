@@ -699,6 +699,185 @@ rlk_status_t rlk_dlogp_audit_noalloc(const float* logp_new, const float* logp_ol
     return RLK_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The checks that the four norm entry points share, in NormArgs' terms.
+rlk_status_t check_norm(int32_t x_dtype, int32_t w_dtype, int64_t N, int64_t H, int64_t x_stride,
+                        int64_t out_stride) {
+    if (x_dtype != RLK_DTYPE_F32 && x_dtype != RLK_DTYPE_BF16) return RLK_ERR_UNSUPPORTED;
+    if (w_dtype != RLK_DTYPE_F32 && w_dtype != RLK_DTYPE_BF16) return RLK_ERR_UNSUPPORTED;
+    if (N < 0 || N > kMaxDim || H < 1) return RLK_ERR_INVALID_VALUE;
+    if (H > (int64_t(1) << 24)) return RLK_ERR_UNSUPPORTED;
+    if (x_stride < H || out_stride < H) return RLK_ERR_INVALID_VALUE;
+    return RLK_OK;
+}
+
+bool rows_vec(const void* p, int64_t stride, size_t esize) {
+    return aligned(p, 16) && (static_cast<size_t>(stride) * esize) % 16 == 0;
+}
+
+rlk_status_t norm_fwd(bool center, const void* x, int32_t x_dtype, int64_t x_stride,
+                      const void* weight, const void* bias, int32_t w_dtype, const uint8_t* mask,
+                      int64_t N, int64_t H, double eps, void* y, int64_t y_stride, float* mean_out,
+                      float* rstd_out, cudaStream_t stream) {
+    RLK_TRY(check_norm(x_dtype, w_dtype, N, H, x_stride, y_stride));
+    if (!(std::isfinite(eps) && eps >= 0.0)) return RLK_ERR_INVALID_VALUE;
+    if (N == 0) return RLK_OK;
+    const size_t es = x_dtype == RLK_DTYPE_F32 ? 4 : 2, wes = w_dtype == RLK_DTYPE_F32 ? 4 : 2;
+    if (x == nullptr || weight == nullptr || y == nullptr) return RLK_ERR_INVALID_VALUE;
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, wes) || !aligned(bias, wes))
+        return RLK_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    rlk::NormArgs a{};
+    a.x = x, a.weight = weight, a.bias = bias, a.mask = mask, a.out = y;
+    a.mean_out = mean_out, a.rstd_out = rstd_out;
+    a.x_stride = x_stride, a.out_stride = y_stride;
+    a.N = static_cast<int>(N), a.H = static_cast<int>(H), a.eps = static_cast<float>(eps);
+    a.bf16 = x_dtype == RLK_DTYPE_BF16, a.w_bf16 = w_dtype == RLK_DTYPE_BF16;
+    a.in_vec = rows_vec(x, x_stride, es);
+    a.out_vec = rows_vec(y, y_stride, es);
+    a.w_vec = aligned(weight, 16) && aligned(bias, 16);
+    RLK_CUDA(rlk::launch_norm_fwd(a, center, stream));
+    return RLK_OK;
+}
+
+rlk_status_t norm_bwd(bool center, const void* x, int32_t x_dtype, int64_t x_stride,
+                      const void* weight, int32_t w_dtype, const void* dy, int64_t dy_stride,
+                      const float* mean, const float* rstd, const uint8_t* mask, int64_t N,
+                      int64_t H, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                      void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    RLK_TRY(check_norm(x_dtype, w_dtype, N, H, x_stride, dx_stride));
+    if (dy_stride < H) return RLK_ERR_INVALID_VALUE;
+    const bool params = dweight != nullptr || dbias != nullptr;
+    if (N == 0 && !params) return RLK_OK;
+    const size_t es = x_dtype == RLK_DTYPE_F32 ? 4 : 2, wes = w_dtype == RLK_DTYPE_F32 ? 4 : 2;
+    if (N > 0 && (x == nullptr || weight == nullptr || dy == nullptr || dx == nullptr ||
+                  rstd == nullptr || (center && mean == nullptr)))
+        return RLK_ERR_INVALID_VALUE;
+    if (!aligned(x, es) || !aligned(dy, es) || !aligned(dx, es) || !aligned(weight, wes) ||
+        !aligned(dweight, wes) || !aligned(dbias, wes))
+        return RLK_ERR_INVALID_VALUE;
+    if (params && (workspace == nullptr || !aligned(workspace, 256) ||
+                   workspace_bytes < rlk::norm_bwd_workspace(N, H, center)))
+        return RLK_ERR_WORKSPACE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    rlk::NormArgs a{};
+    a.x = x, a.dy = dy, a.weight = weight, a.mask = mask, a.mean = mean, a.rstd = rstd;
+    a.out = dx, a.dweight = dweight, a.dbias = dbias, a.workspace = workspace;
+    a.x_stride = x_stride, a.dy_stride = dy_stride, a.out_stride = dx_stride;
+    a.N = static_cast<int>(N), a.H = static_cast<int>(H);
+    a.bf16 = x_dtype == RLK_DTYPE_BF16, a.w_bf16 = w_dtype == RLK_DTYPE_BF16;
+    a.in_vec = rows_vec(x, x_stride, es) && rows_vec(dy, dy_stride, es);
+    a.out_vec = rows_vec(dx, dx_stride, es);
+    a.w_vec = aligned(weight, 16);
+    RLK_CUDA(rlk::launch_norm_bwd(a, center, stream));
+    return RLK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rlk_status_t rlk_layer_norm_fwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                                const void* weight, const void* bias, int32_t w_dtype,
+                                const uint8_t* active_mask, int64_t N, int64_t H, double eps,
+                                void* y, int64_t y_stride, float* mean_out, float* rstd_out,
+                                cudaStream_t stream) {
+    return norm_fwd(true, x, x_dtype, x_stride, weight, bias, w_dtype, active_mask, N, H, eps, y,
+                    y_stride, mean_out, rstd_out, stream);
+}
+
+rlk_status_t rlk_rms_norm_fwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                              const void* weight, int32_t w_dtype, const uint8_t* active_mask,
+                              int64_t N, int64_t H, double eps, void* y, int64_t y_stride,
+                              float* rstd_out, cudaStream_t stream) {
+    return norm_fwd(false, x, x_dtype, x_stride, weight, nullptr, w_dtype, active_mask, N, H, eps,
+                    y, y_stride, nullptr, rstd_out, stream);
+}
+
+size_t rlk_layer_norm_bwd_workspace_bytes(int64_t N, int64_t H) {
+    if (N < 0 || H < 1) return 0;
+    return rlk::norm_bwd_workspace(N, H, true);
+}
+
+size_t rlk_rms_norm_bwd_workspace_bytes(int64_t N, int64_t H) {
+    if (N < 0 || H < 1) return 0;
+    return rlk::norm_bwd_workspace(N, H, false);
+}
+
+rlk_status_t rlk_layer_norm_bwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                                const void* weight, int32_t w_dtype, const void* dy,
+                                int64_t dy_stride, const float* mean, const float* rstd,
+                                const uint8_t* active_mask, int64_t N, int64_t H, void* dx,
+                                int64_t dx_stride, void* dweight, void* dbias, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+    return norm_bwd(true, x, x_dtype, x_stride, weight, w_dtype, dy, dy_stride, mean, rstd,
+                    active_mask, N, H, dx, dx_stride, dweight, dbias, workspace, workspace_bytes,
+                    stream);
+}
+
+rlk_status_t rlk_rms_norm_bwd(const void* x, int32_t x_dtype, int64_t x_stride,
+                              const void* weight, int32_t w_dtype, const void* dy,
+                              int64_t dy_stride, const float* rstd, const uint8_t* active_mask,
+                              int64_t N, int64_t H, void* dx, int64_t dx_stride, void* dweight,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    return norm_bwd(false, x, x_dtype, x_stride, weight, w_dtype, dy, dy_stride, nullptr, rstd,
+                    active_mask, N, H, dx, dx_stride, dweight, nullptr, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t rlk_sample_logits_workspace_bytes(int64_t N, int64_t V) {
+    if (N < 0 || V < 1) return 0;
+    return rlk::sample_workspace(N, V);
+}
+
+rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                               int64_t row_stride, const float* uniforms,
+                               const uint8_t* active_mask, const rlk_sample_params_t* params,
+                               int64_t* tokens_out, float* logp_out, float* kept_logp_out,
+                               void* workspace, size_t workspace_bytes,
+                               uint32_t* device_error_word, cudaStream_t stream) {
+    if (dtype != RLK_DTYPE_F32 && dtype != RLK_DTYPE_BF16) return RLK_ERR_UNSUPPORTED;
+    if (N < 0 || N > kMaxDim || V < 1 || row_stride < V) return RLK_ERR_INVALID_VALUE;
+    if (V > (int64_t(1) << 22)) return RLK_ERR_UNSUPPORTED;
+    if (params == nullptr) return RLK_ERR_INVALID_VALUE;
+    const rlk_sample_params_t& p = *params;
+    if (p.temperature_rows == nullptr &&
+        !(p.temperature >= rlk::kSampleMinT && p.temperature <= rlk::kSampleMaxT))
+        return RLK_ERR_INVALID_VALUE;
+    if (p.top_k_rows == nullptr && p.top_k < 0) return RLK_ERR_INVALID_VALUE;
+    if (p.top_p_rows == nullptr && !(p.top_p > 0.0)) return RLK_ERR_INVALID_VALUE;
+    if (p.min_p_rows == nullptr && !(p.min_p >= 0.0 && p.min_p <= 1.0))
+        return RLK_ERR_INVALID_VALUE;
+    if (N == 0) return RLK_OK;
+    if (logits == nullptr || uniforms == nullptr || tokens_out == nullptr)
+        return RLK_ERR_INVALID_VALUE;
+    const size_t es = dtype == RLK_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, es)) return RLK_ERR_INVALID_VALUE;
+    const size_t need = rlk::sample_workspace(N, V);
+    if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
+        return RLK_ERR_WORKSPACE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    rlk::SampleArgs a{};
+    a.uniforms = uniforms, a.mask = active_mask;
+    a.temperature_rows = p.temperature_rows, a.top_k_rows = p.top_k_rows;
+    a.top_p_rows = p.top_p_rows, a.min_p_rows = p.min_p_rows;
+    a.temperature = p.temperature, a.top_k = p.top_k, a.top_p = p.top_p, a.min_p = p.min_p;
+    a.stride = row_stride, a.N = static_cast<int>(N), a.V = static_cast<int>(V);
+    a.bits = 46;
+    while ((int64_t(1) << (64 - a.bits)) <= V) --a.bits;      // V 2^bits < 2^64
+    a.vec_ok = rows_vec(logits, row_stride, es);
+    a.tokens = tokens_out, a.logp = logp_out, a.kept_logp = kept_logp_out;
+    a.workspace = workspace, a.err = device_error_word;
+    RLK_CUDA(rlk::launch_sample(logits, dtype == RLK_DTYPE_BF16, a, stream));
+    return RLK_OK;
+}
+
 #define RLK_STR2(x) #x
 #define RLK_STR(x) RLK_STR2(x)
 

@@ -277,6 +277,54 @@ cudaError_t launch_audit_ext(const float* logp_new, const float* logp_old, const
                              rlk_audit_ext_t* result, void* workspace, bool vec_ok, int sms,
                              cudaStream_t stream);
 
+// Layer norm / RMS norm.  *_vec: the rows' starts allow 16-byte accesses.
+struct NormArgs {
+    const void* x;
+    const void* dy;            // backward only
+    const void* weight;
+    const void* bias;          // forward only, or nullptr
+    const uint8_t* mask;
+    const float* mean;         // backward only (layer norm)
+    const float* rstd;         // backward only
+    void* out;                 // y, or dx
+    float* mean_out;           // forward only, or nullptr
+    float* rstd_out;
+    void* dweight;             // backward only, or nullptr
+    void* dbias;
+    void* workspace;           // backward only
+    int64_t x_stride, dy_stride, out_stride;
+    int N, H;
+    float eps;
+    bool bf16, w_bf16, in_vec, w_vec, out_vec;
+};
+size_t norm_bwd_workspace(int64_t N, int64_t H, bool center);
+cudaError_t launch_norm_fwd(const NormArgs& args, bool center, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormArgs& args, bool center, cudaStream_t stream);
+
+// Sampling.  *_rows: one value a row, or nullptr (then the scalar holds for all).
+constexpr double kSampleMinT = 1e-6, kSampleMaxT = 1e6;
+struct SampleArgs {
+    const float* uniforms;
+    const uint8_t* mask;
+    const float* temperature_rows;
+    const int32_t* top_k_rows;
+    const float* top_p_rows;
+    const float* min_p_rows;
+    double temperature, top_p, min_p;
+    int64_t top_k, stride;
+    int N, V;
+    int bits;                  // weights are scaled by 2^bits; V 2^bits < 2^64
+    bool vec_ok;               // rows start on 16 bytes
+    int64_t* tokens;
+    float* logp;               // or nullptr
+    float* kept_logp;          // or nullptr
+    void* workspace;
+    uint32_t* err;
+};
+size_t sample_workspace(int64_t N, int64_t V);
+cudaError_t launch_sample(const void* logits, bool bf16, const SampleArgs& args,
+                          cudaStream_t stream);
+
 // Device address (current device and context) of the library-owned audit scratch.
 cudaError_t audit_noalloc_scratch(void** parts);
 
