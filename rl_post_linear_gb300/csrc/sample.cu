@@ -18,24 +18,26 @@
 // is sorted.  Sums that decide are integers (weight_exp.cuh), so the token depends on the
 // row alone: not on the batch, on how the row is split, or on the alignment.
 //
-// A cluster of up to 8 blocks takes one row; a warp takes a chunk of 512 columns.
+// Two launches.  The scan: a cluster of up to 8 blocks a row, a warp a chunk of 512
+// columns; per chunk its maximum and an fp32 sum of 2^((x - chunk max) c), c = log2(e)/T,
+// go to the workspace.  This is the only pass over HBM.  The cluster's block 0 then forms
+// the chunks' weights as integers, in the same order whatever the split, and finishes the
+// rows that need no further pass over all columns:
 //
-// Scan (the only pass over HBM).  Per chunk its maximum and an fp32 sum of
-// 2^((x - chunk max) c), c = log2(e)/T.  Through distributed shared memory every block
-// gets all chunks' pairs and forms the chunks' weights as integers, in the same order
-// whatever the split.
+//   no truncation: the chunk and the element that u times the total falls on come from the
+//   fast weights, together with a bound on their error (kFastErr); only when the target lies
+//   within it of a border of the running sums -- some percent of the rows at V ~ 150k --
+//   does the row go on to the search, which weighs it exactly.
 //
-// Draw without truncation.  The chunk and the element that u times the total falls on come
-// from these weights, together with a bound on their error (kFastErr).  Only when the
-// target lies within that bound of a border of the running sums -- some percent of the
-// rows at V ~ 150k -- are the row's weights formed again as exact integers.
+//   truncation: elements from some value on are gathered from the chunks whose maximum
+//   reaches it, and their order is counted out in place.  The value is one that K chunk
+//   maxima reach (top_k), that chunk maxima of top_p of the total reach, or min_p's own; in
+//   rows in no particular order few other elements reach it.
 //
-// Truncated draws.  The K-th largest chunk maximum is below at least K elements and, in
-// rows in no particular order, above nearly all the others: the elements from it on are
-// gathered into a list, where the boundary is found by radix selection.  Where that cannot
-// work (a large top_k, a wide nucleus, a row sorted by token) histograms of 2048 bins of
-// the scaled distance from the maximum, then of the keys inside the remaining window, close
-// in on the boundary until its window fits the list or is a single value.  Block 0 of the
+// The search takes the rows that are left (a wide nucleus, a large top_k, a row sorted by
+// token, a target near a border), again a cluster a row: histograms of 2048 bins of the
+// scaled distance from the maximum, then of the keys inside the remaining window, close in
+// on the boundary until its window fits a list or is a single value.  Block 0 of the
 // cluster decides each step; the blocks work on their own chunks in between.
 #include <cuda_bf16.h>
 
@@ -54,7 +56,9 @@ typedef unsigned long long u64;
 constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
-constexpr int kList = 1024;              // elements of a list
+constexpr int kList = 1024;              // elements of the search's list
+constexpr int kShort = 512;              // of the scan's list, counted out in place
+constexpr int kThreads = 256;
 constexpr float kRange = 48.f;           // weights below 2^-48 round to 0 (bits <= 46)
 constexpr int kMaxSteps = 32;            // far more than any row takes
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
@@ -197,6 +201,34 @@ struct Cmd {
     int list;         // kCollect: 1 lists the elements inside, 0 counts them per chunk
 };
 
+// Shared memory of the scan.
+struct Shared0 {
+    u64 table[kExpEntries];
+    u64 w[kShort];
+    uint32_t key[kShort], idx[kShort];
+    u64 part[32];
+    uint32_t part_n[32];
+    u64 at_w;
+    uint32_t n_list, n_ids, flag;
+    int at;
+};
+
+// Workspace: a header a row, then the chunks' maxima and sums.
+enum : uint32_t { kRowDone, kRowSearch };
+struct RowHeader {
+    u64 all;                             // fast total of the weights
+    float m;                             // maximum
+    uint32_t mode;
+};
+__host__ __device__ constexpr size_t stats_offset(int64_t N) {
+    return (size_t(N) * sizeof(RowHeader) + 255) / 256 * 256;
+}
+__device__ __forceinline__ float2* row_stats(const SampleArgs& a, int64_t row, int nch) {
+    return reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + stats_offset(a.N)) +
+           row * nch;
+}
+
+// Shared memory of the search.
 struct Shared {
     u64 table[kExpEntries];
     u64 w[kList];                        // block 0: the merged list
@@ -213,8 +245,6 @@ struct Shared {
     u64 at_w;
     uint32_t at_n, at_n2;
     int at, at2;
-    uint32_t flag;
-    float value;
     Cmd cmd;
 };
 
@@ -234,7 +264,8 @@ struct Block {
     static constexpr int kWarps = THREADS / 32;
 
     // exclusive prefix of v and n over the block's threads; totals in tv, tn
-    __device__ static void scan(u64& v, uint32_t& n, u64& tv, uint32_t& tn, Shared& sh) {
+    template <typename S>
+    __device__ static void scan(u64& v, uint32_t& n, u64& tv, uint32_t& tn, S& sh) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         u64 iv = v;
         uint32_t in = n;
@@ -444,28 +475,12 @@ __device__ __forceinline__ void write_drawn(const SampleArgs& a, int64_t row, in
               static_cast<float>(z - log_of(kept, bits)));
 }
 
-// Order statistic: the k-th largest (k >= 1, from 1) of the chunk maxima.
-template <int THREADS>
-__device__ float kth_max(const float* cmax, int nch, int k, Shared& sh) {
-    for (int c = threadIdx.x; c < nch; c += THREADS) {
-        const float v = cmax[c];
-        int above = 0;
-        for (int j = 0; j < nch; ++j) above += (cmax[j] > v || (cmax[j] == v && j < c)) ? 1 : 0;
-        if (above == k - 1) sh.value = v;
-    }
-    __syncthreads();
-    const float r = sh.value;
-    __syncthreads();
-    return r;
-}
-
 // What block 0 carries from step to step (uniform over its threads).
 struct Search {
     bool want_k, want_p;       // boundaries still to be found
     bool draw;                 // the next kCollect is the last
     bool sum;                  // the next kCollect is the exact total
     bool exact;                // s_lo == s_hi is the exact weight that top_p refers to
-    bool tried;                // the guess from the chunk maxima has been used
     int level;                 // histograms of this search so far
     u64 n_above;               // count above the window (want_k)
     u64 s_lo, s_hi;            // bounds of the total that top_p refers to
@@ -901,21 +916,19 @@ struct Sampler {
     }
 };
 
-// The draw without truncation from the fast weights.  Every block of the cluster does the
-// same; returns false where the weights' error leaves the token open.
-template <typename T, int THREADS>
+// The draw without truncation from the fast weights; false where their error leaves the
+// token open.
+template <typename T>
 __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64 all, float u,
-                          const SampleArgs& a, int64_t row_i, double temp, bool writes,
-                          Shared& sh) {
-    typedef Block<THREADS> B;
+                          const SampleArgs& a, int64_t row_i, double temp, Shared0& sh) {
     const int tid = threadIdx.x;
     const u64 target = part_of(static_cast<double>(u), all, false);
-    const int each = (r.nch + THREADS - 1) / THREADS;
+    const int each = (r.nch + kThreads - 1) / kThreads;
     const int c0 = min(r.nch, tid * each), c1 = min(r.nch, c0 + each);
     u64 w = 0, tw;
     uint32_t n = 0, tn;
     for (int c = c0; c < c1; ++c) w += cw[c];
-    B::scan(w, n, tw, tn, sh);
+    Block<kThreads>::scan(w, n, tw, tn, sh);
     if (tid == 0) sh.flag = 0, sh.at = 0, sh.at_w = 0;
     __syncthreads();
     for (int c = c0; c < c1; ++c) {
@@ -956,9 +969,8 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
                 at += we[e];
                 if ((lo == 0 || lo + err <= target) && target + err < at && lo <= target) {
                     sure = true;
-                    if (writes)
-                        write_drawn(a, row_i, Chunk<T>::column(chunk, j, tid) + e,
-                                    c.get(j * VEC + e), r.ws.m, temp, all, all, r.bits);
+                    write_drawn(a, row_i, Chunk<T>::column(chunk, j, tid) + e,
+                                c.get(j * VEC + e), r.ws.m, temp, all, all, r.bits);
                 }
             }
         }
@@ -968,48 +980,30 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
     return sh.flag != 0;
 }
 
-// Floats and integers behind Shared in dynamic shared memory, for nch chunks of which a
-// block owns `own`.
-__host__ __device__ constexpr size_t smem_bytes(int nch, int own) {
-    return sizeof(Shared) + size_t(nch) * 16 + size_t(own) * 16 + 16;
+// A row's settings.
+struct Settings {
+    double temp, top_p, min_p;
+    int64_t top_k;
+    float u;
+    bool ok;
+};
+__device__ __forceinline__ Settings read_settings(const SampleArgs& a, int64_t row) {
+    Settings s;
+    s.temp = a.temperature_rows != nullptr ? a.temperature_rows[row] : a.temperature;
+    s.top_k = a.top_k_rows != nullptr ? a.top_k_rows[row] : a.top_k;
+    s.top_p = a.top_p_rows != nullptr ? a.top_p_rows[row] : a.top_p;
+    s.min_p = a.min_p_rows != nullptr ? a.min_p_rows[row] : a.min_p;
+    s.u = a.uniforms[row];
+    s.ok = s.temp >= kSampleMinT && s.temp <= kSampleMaxT && s.top_k >= 0 && s.top_p > 0.0 &&
+           s.min_p >= 0.0 && s.min_p <= 1.0 && s.u >= 0.f && s.u < 1.f;
+    return s;
 }
 
-template <typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS) sample_kernel(const T* __restrict__ logits,
-                                                         const SampleArgs a, int nch, int own,
-                                                         int ranks) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem);
-    u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared));     // all chunks: weight
-    u64* own_w = cw + nch;                                       // own chunks
-    float* cmax = reinterpret_cast<float*>(own_w + own);         // all chunks: maximum
-    uint32_t* cn = reinterpret_cast<uint32_t*>(cmax + nch);      //             ties
-    float* own_max = reinterpret_cast<float*>(cn + nch);
-    uint32_t* own_n = reinterpret_cast<uint32_t*>(own_max + own);   // sums (scan), counts
-
-    const int64_t row_i = blockIdx.x / ranks;
-    const uint32_t rank = blockIdx.x % ranks;        // = the block's rank in its cluster
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (a.mask != nullptr && a.mask[row_i] == 0) {
-        if (rank == 0 && tid == 0) write_row(a, row_i, -1, 0.f, 0.f);
-        return;
-    }
-    const double temp = a.temperature_rows != nullptr ? a.temperature_rows[row_i] : a.temperature;
-    const int64_t top_k = a.top_k_rows != nullptr ? a.top_k_rows[row_i] : a.top_k;
-    const double top_p = a.top_p_rows != nullptr ? a.top_p_rows[row_i] : a.top_p;
-    const double min_p = a.min_p_rows != nullptr ? a.min_p_rows[row_i] : a.min_p;
-    const float u = a.uniforms[row_i];
-    const bool params_ok = temp >= kSampleMinT && temp <= kSampleMaxT && top_k >= 0 &&
-                           top_p > 0.0 && min_p >= 0.0 && min_p <= 1.0 && u >= 0.f && u < 1.f;
-    if (!params_ok) {
-        if (rank == 0 && tid == 0) {
-            write_row(a, row_i, -1, quiet_nan(), quiet_nan());
-            if (a.err != nullptr) atomicOr(a.err, RLK_DEVERR_SAMPLE_PARAM);
-        }
-        return;
-    }
+template <typename T>
+__device__ __forceinline__ Row<T> make_row(const T* logits, const SampleArgs& a, int64_t row,
+                                           double temp, int nch, int own, int rank) {
     Row<T> r;
-    r.x = logits + row_i * a.stride;
+    r.x = logits + row * a.stride;
     r.V = a.V;
     r.nch = nch;
     r.own = own;
@@ -1018,153 +1012,424 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const T* __restrict__ l
     r.vec = a.vec_ok;
     r.bits = a.bits;
     const double c = 1.4426950408889634074 / temp;
+    r.ws.m = 0.f;
     r.ws.ch = static_cast<float>(c);
     r.ws.cl = static_cast<float>(c - static_cast<double>(r.ws.ch));
     r.ws.shift = 62 - a.bits;
     r.scale = r.ws.ch * (kBins / kRange);
+    return r;
+}
 
-    // ---- scan
-    for (int i = tid; i < kExpEntries; i += THREADS) sh.table[i] = kExpTable.v[i];
+// the key of the smallest float x with x >= max + T log(min_p); 0 without min_p
+__device__ __forceinline__ uint32_t min_p_key(const Settings& s, float m) {
+    if (!(s.min_p > 0.0)) return 0;
+    const double at = static_cast<double>(m) + s.temp * log(s.min_p);
+    const float f = static_cast<float>(at);
+    return order_key(f) + (static_cast<double>(f) < at ? 1u : 0u);
+}
+
+// bounds of the exact total from the fast one
+__device__ __forceinline__ void total_bounds(u64 all, u64& lo, u64& hi) {
+    const u64 err = static_cast<u64>(static_cast<float>(all) * (kFastErr + 1.5e-11f)) + 8192;
+    lo = all > err ? all - err : 1;
+    hi = all + err;
+}
+
+// A value that enough chunk maxima reach: at least `count` of them, or (need > 0) maxima of
+// a weight of at least `need`.  Between the maximum and `low`, by bisection with a warp a
+// trial: 4 rounds leave 1/6561 of the range.  `low` itself if that is not enough, with
+// found = false.
+template <typename T>
+__device__ float reach_value(const Row<T>& r, const float* cmax, int count, float need, float low,
+                             bool& found, Shared0& sh) {
+    constexpr int kWarps = kThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float hi = r.ws.m, lo = low;
+    found = true;
+    for (int round = 0; round < 4; ++round) {
+        // warp w tries the (w + 1)-th of 9 parts below hi; the first round also tries low
+        const float step = (hi - lo) / (kWarps + 1);
+        const float x = round == 0 && warp == kWarps - 1 ? low : hi - step * (warp + 1);
+        int n = 0;
+        float w = 0.f;
+        for (int c = lane; c < r.nch; c += 32) {
+            const float v = cmax[c];
+            if (v < x) continue;
+            ++n;
+            if (need > 0.f) w += ex2_approx((v - r.ws.m) * r.ws.ch);
+        }
+        const bool enough =
+            need > 0.f ? warp_sum(w) >= need : __reduce_add_sync(0xffffffffu, n) >= count;
+        __syncthreads();
+        if (lane == 0) sh.part_n[warp] = enough ? 1u : 0u;
+        __syncthreads();
+        int first = 0;                               // the highest trial that is enough
+        while (first < kWarps && sh.part_n[first] == 0) ++first;
+        if (round == 0) {
+            if (first == kWarps) {
+                found = false;
+                return low;
+            }
+            if (first == kWarps - 1) {               // only low itself
+                hi = hi - step * (kWarps - 1);
+                continue;
+            }
+        }
+        const float top = hi;
+        if (first > 0) hi = top - step * first;
+        if (first < kWarps) lo = top - step * (first + 1);
+    }
+    return lo;
+}
+
+// Draws from the elements at or above a value, if they settle the boundary and are few.
+// Block 0 of the scan.
+template <typename T>
+__device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax, uint16_t* ids,
+                           u64 all, const SampleArgs& a, int64_t row_i, Shared0& sh) {
+    typedef Block<kThreads> B;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool want_k = s.top_k > 0 && s.top_k < r.V, want_p = s.top_p < 1.0;
+    const uint32_t key_m = min_p_key(s, r.ws.m);
+    uint32_t tau = kKeyNegInf + 1;
+    if (r.V > kShort && (want_k || want_p)) {
+        // between the maximum and 48 powers of two below it: what is lower weighs nothing
+        const float low = static_cast<float>(
+            fmax(static_cast<double>(r.ws.m) - kRange / static_cast<double>(r.ws.ch),
+                 -3.4028234663852886e38));
+        const float need = static_cast<float>(s.top_p * 1.00001 * static_cast<double>(all) /
+                                              static_cast<double>(u64(1) << r.bits));
+        if (want_k && s.top_k > r.nch * 9 / 10) return false;
+        bool found;
+        const float x = reach_value(r, cmax, static_cast<int>(s.top_k), want_k ? 0.f : need, low,
+                                    found, sh);
+        if (!found && !want_k) return false;         // a wide nucleus
+        tau = max(tau, order_key(x));
+    }
+    // what min_p cuts is needed only where top_p counts it
+    if (!want_p) tau = max(tau, key_m);
+    if (tid == 0) sh.n_list = 0, sh.n_ids = 0;
+    __syncthreads();
+    for (int c = tid; c < r.nch; c += kThreads)
+        if (order_key(cmax[c]) >= tau) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
+    __syncthreads();
+    const int n_ids = sh.n_ids;
     constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
-    for (int i0 = warp; i0 < r.mine; i0 += kAhead * (THREADS / 32)) {
+    for (int i0 = warp; i0 < n_ids; i0 += kAhead * (kThreads / 32)) {
         Chunk<T> ch[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * (THREADS / 32);
-            if (i < r.mine) ch[q].load(r.x, r.V, r.first + i, lane, r.vec);
+            const int i = i0 + q * (kThreads / 32);
+            if (i < n_ids) ch[q].load(r.x, r.V, ids[i], lane, r.vec);
         }
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * (THREADS / 32);
-            if (i >= r.mine) break;
-            float m = ch[q].get(0);
+            const int i = i0 + q * (kThreads / 32);
+            if (i >= n_ids) break;
 #pragma unroll
-            for (int e = 1; e < kLane; ++e) m = fmaxf(m, ch[q].get(e));
-            m = warp_max(m);
-            // a chunk of -inf has sum 0; NaN or +inf make it NaN
-            const float mm = fmaxf(m, -3.402823466e38f);
-            float s[kLane];
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) s[e] = ex2_approx((ch[q].get(e) - mm) * r.ws.ch);
-#pragma unroll
-            for (int w = kLane / 2; w > 0; w >>= 1)
-#pragma unroll
-                for (int e = 0; e < w; ++e) s[e] += s[e + w];
-            const float sum = warp_sum(s[0]);
-            if (lane == 0) own_max[i] = m, own_n[i] = __float_as_uint(sum);
+            for (int e = 0; e < kLane; ++e) {
+                const float x = ch[q].get(e);
+                const uint32_t k = order_key(x);
+                if (k < tau) continue;
+                const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                if (at < kShort) {
+                    sh.w[at] = fixed_weight(x, r.ws, sh.table);
+                    sh.key[at] = k;
+                    sh.idx[at] = Chunk<T>::column(ids[i], e / Chunk<T>::VEC, lane) +
+                                 e % Chunk<T>::VEC;
+                }
+            }
         }
     }
-    cluster_join();
+    __syncthreads();
+    const uint32_t n = sh.n_list;
+    if (n > kShort) return false;
+    // each element's place in the order, and the weight before it
+    constexpr int kPer = kShort / kThreads;
+    uint32_t place[kPer];
+    u64 before[kPer], list_w = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t i = tid + q * kThreads;
+        place[q] = 0;
+        before[q] = 0;
+        if (i >= n) continue;
+        const uint32_t k = sh.key[i], v = sh.idx[i];
+        for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t kj = sh.key[j];
+            if (kj > k || (kj == k && sh.idx[j] < v)) ++place[q], before[q] += sh.w[j];
+        }
+        list_w += sh.w[i];
+    }
+    u64 dummy_w = list_w;
+    uint32_t dummy = 0, tn;
+    B::scan(dummy_w, dummy, list_w, tn, sh);
+    u64 need_lo = ~u64(0), need_hi = ~u64(0);
+    u64 top_k = ~u64(0);
+    if (want_k) {
+        top_k = static_cast<u64>(s.top_k);
+        if (tid == 0) sh.at_w = list_w;              // fewer elements than top_k: all of them
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const uint32_t i = tid + q * kThreads;
+            if (i < n && place[q] == top_k - 1) sh.at_w = before[q] + sh.w[i];
+        }
+        __syncthreads();
+        if (want_p) need_lo = need_hi = max(u64(1), part_of(s.top_p, sh.at_w, true));
+    } else if (want_p) {
+        u64 lo, hi;
+        total_bounds(all, lo, hi);
+        need_lo = max(u64(1), part_of(s.top_p, lo, true));
+        need_hi = max(u64(1), part_of(s.top_p, hi, true));
+        if (need_hi > list_w && r.V > kShort) return false;
+        if (r.V <= kShort) need_lo = need_hi = max(u64(1), part_of(s.top_p, list_w, true));
+    }
+    // kept, by each bound of the total: where the two differ the search decides
+    bool keep[kPer], open = false;
+    u64 kept = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t i = tid + q * kThreads;
+        keep[q] = i < n && place[q] < top_k && before[q] < need_lo && sh.key[i] >= key_m;
+        open |= i < n && place[q] < top_k && before[q] >= need_lo && before[q] < need_hi &&
+                sh.key[i] >= key_m;
+        if (keep[q]) kept += sh.w[i];
+    }
+    if (__syncthreads_or(open)) return false;
+    // cut elements weigh nothing from here on
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t i = tid + q * kThreads;
+        if (i < n && !keep[q]) sh.w[i] = 0;
+    }
+    u64 kept_all;
+    dummy_w = kept;
+    B::scan(dummy_w, dummy, kept_all, tn, sh);
+    const u64 target = part_of(static_cast<double>(s.u), kept_all, false);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t i = tid + q * kThreads;
+        if (i >= n || !keep[q]) continue;
+        const uint32_t v = sh.idx[i];
+        u64 run = 0;
+        for (uint32_t j = 0; j < n; ++j)
+            if (sh.idx[j] < v) run += sh.w[j];
+        if (run <= target && target < run + sh.w[i])
+            write_drawn(a, row_i, v, key_value(sh.key[i]), r.ws.m, s.temp, max(all, kept_all),
+                        kept_all, r.bits);
+    }
+    return true;
+}
 
-    // ---- every block: all chunks' maxima and weights
+__host__ __device__ constexpr size_t scan_smem(int nch) {
+    return sizeof(Shared0) + size_t(nch) * 8 + size_t(nch) * 4 + size_t(nch) * 2 + 16;
+}
+
+// Maximum and sum of a chunk: the sum of 2^((x - max) c) without one element of the
+// maximum (sign bit set) where `apart`, else of all.  A row's total is a sum of such parts
+// plus the maximum's own weight, so a logp near 0 keeps its digits.
+template <typename T>
+__device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float& best) {
+    float ml = c.get(0);
+#pragma unroll
+    for (int e = 1; e < kLane; ++e) ml = fmaxf(ml, c.get(e));
+    const float m = warp_max(ml);
+    // a chunk of -inf has sum 0; NaN or +inf make it NaN
+    const float mm = fmaxf(m, -3.402823466e38f);
+    float s[kLane];
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) s[e] = ex2_approx((c.get(e) - mm) * ch);
+    // only a chunk that holds the warp's largest so far can hold the row's maximum
+    const bool apart = m >= best && m < INFINITY && m > -INFINITY;
+    if (apart) {
+        best = m;
+        bool lead = (threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, ml == m)) - 1;
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) {
+            const bool hit = lead && c.get(e) == m;
+            s[e] = hit ? 0.f : s[e];
+            lead = lead && !hit;
+        }
+    }
+#pragma unroll
+    for (int w = kLane / 2; w > 0; w >>= 1)
+#pragma unroll
+        for (int e = 0; e < w; ++e) s[e] += s[e + w];
+    const float sum = warp_sum(s[0]);
+    return make_float2(m, apart ? -sum : sum);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
+    sample_scan_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
+                       int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared0& sh = *reinterpret_cast<Shared0*>(smem);
+    u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared0));
+    float* cmax = reinterpret_cast<float*>(cw + nch);
+    uint16_t* ids = reinterpret_cast<uint16_t*>(cmax + nch);
+    const int64_t row_i = blockIdx.x / ranks;
+    const int rank = blockIdx.x % ranks;             // = the block's rank in its cluster
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    RowHeader* head = static_cast<RowHeader*>(a.workspace) + row_i;
+    float2* stats = row_stats(a, row_i, nch);
+    if (a.mask != nullptr && a.mask[row_i] == 0) {
+        if (rank == 0 && tid == 0) {
+            write_row(a, row_i, -1, 0.f, 0.f);
+            head->mode = kRowDone;
+        }
+        return;
+    }
+    const Settings s = read_settings(a, row_i);
+    if (!s.ok) {
+        if (rank == 0 && tid == 0) {
+            write_row(a, row_i, -1, quiet_nan(), quiet_nan());
+            if (a.err != nullptr) atomicOr(a.err, RLK_DEVERR_SAMPLE_PARAM);
+            head->mode = kRowDone;
+        }
+        return;
+    }
+    Row<T> r = make_row(logits, a, row_i, s.temp, nch, own, rank);
+    float best = -INFINITY;
+    constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
+    for (int i0 = warp; i0 < r.mine; i0 += kAhead * (kThreads / 32)) {
+        Chunk<T> c[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int i = i0 + q * (kThreads / 32);
+            if (i < r.mine) c[q].load(r.x, r.V, r.first + i, lane, r.vec);
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int i = i0 + q * (kThreads / 32);
+            if (i >= r.mine) break;
+            const float2 st = chunk_stats(c[q], r.ws.ch, best);
+            if (lane == 0) stats[r.first + i] = st;
+        }
+    }
+    // the other blocks are done once their part is out
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    for (int i = tid; i < kExpEntries; i += kThreads) sh.table[i] = kExpTable.v[i];
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+
     float m = -INFINITY;
     bool bad = false;
-    for (int i = tid; i < nch; i += THREADS) {
-        const int k = i / own, j = i - k * own;
-        const float v = peer(own_max, k)[j];
-        const uint32_t s = peer(own_n, k)[j];
-        cmax[i] = v;
-        cn[i] = s;
-        m = fmaxf(m, v);
-        bad |= __uint_as_float(s) != __uint_as_float(s);
+    for (int i = tid; i < nch; i += kThreads) {
+        const float2 st = stats[i];
+        cmax[i] = st.x;
+        m = fmaxf(m, st.x);
+        bad |= st.y != st.y;
     }
     m = warp_max(m);
     if (lane == 0) sh.part_n[warp] = __float_as_uint(m);
     bad = __syncthreads_or(bad);
-    for (int i = 0; i < THREADS / 32; ++i) m = fmaxf(m, __uint_as_float(sh.part_n[i]));
-    // the blocks' scan results are overwritten only after every block has read them
-    cluster_join();
+    for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, __uint_as_float(sh.part_n[i]));
     if (bad || m == -INFINITY) {
-        if (rank == 0 && tid == 0) {
+        if (tid == 0) {
             write_row(a, row_i, -1, quiet_nan(), quiet_nan());
             if (a.err != nullptr) atomicOr(a.err, RLK_DEVERR_LOGITS);
+            head->mode = kRowDone;
         }
         return;
     }
     r.ws.m = m;
     u64 mine = 0, all;
     uint32_t dummy = 0, tn;
-    for (int i = tid; i < nch; i += THREADS) {
-        const float s = __uint_as_float(cn[i]);
-        const u64 w = s == 0.f ? 0 : scale_weight(s, fixed_weight(cmax[i], r.ws, sh.table));
+    for (int i = tid; i < nch; i += kThreads) {
+        const float2 st = stats[i];
+        u64 w = 0;
+        if (st.x > -INFINITY) {
+            const u64 top = fixed_weight(st.x, r.ws, sh.table);
+            w = scale_weight(fabsf(st.y), top) + (__float_as_uint(st.y) >> 31 ? top : 0);
+        }
         cw[i] = w;
         mine += w;
     }
-    Block<THREADS>::scan(mine, dummy, all, tn, sh);     // its barriers also publish cw
-    all = max(all, u64(1) << a.bits);                   // the maximum's own weight
+    Block<kThreads>::scan(mine, dummy, all, tn, sh);     // its barriers also publish cw
+    const bool cut = (s.top_k > 0 && s.top_k < a.V) || s.top_p < 1.0 || s.min_p > 0.0;
+    const bool done = cut ? short_draw(r, s, cmax, ids, all, a, row_i, sh)
+                          : fast_draw(r, cmax, cw, all, s.u, a, row_i, s.temp, sh);
+    if (tid == 0) {
+        head->all = all;
+        head->m = m;
+        head->mode = done ? kRowDone : kRowSearch;
+    }
+}
 
-    // ---- the first step, the same in every block
+// Floats and integers behind Shared in dynamic shared memory, for nch chunks of which a
+// block owns `own`.
+__host__ __device__ constexpr size_t search_smem(int nch, int own) {
+    return sizeof(Shared) + size_t(nch) * 16 + size_t(own) * 12 + 16;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3)
+    sample_search_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
+                         int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared));     // all chunks: weight
+    u64* own_w = cw + nch;                                       // own chunks
+    float* cmax = reinterpret_cast<float*>(own_w + own);         // all chunks: maximum
+    uint32_t* cn = reinterpret_cast<uint32_t*>(cmax + nch);      //             ties
+    uint32_t* own_n = cn + nch;
+    const int64_t row_i = blockIdx.x / ranks;
+    const int rank = blockIdx.x % ranks;
+    const int tid = threadIdx.x;
+    // the scan's results (also of earlier calls that shared the workspace) are complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const RowHeader* head = static_cast<const RowHeader*>(a.workspace) + row_i;
+    if (head->mode != kRowSearch) return;
+    const Settings s = read_settings(a, row_i);
+    Row<T> r = make_row(logits, a, row_i, s.temp, nch, own, rank);
+    r.ws.m = head->m;
+    u64 all = head->all;
+    const float2* stats = row_stats(a, row_i, nch);
+    for (int i = tid; i < nch; i += kThreads) cmax[i] = stats[i].x;
+    for (int i = tid; i < kExpEntries; i += kThreads) sh.table[i] = kExpTable.v[i];
+    __syncthreads();
+
     Search P;
-    P.want_k = top_k > 0 && top_k < a.V;
-    P.want_p = top_p < 1.0;
+    P.want_k = s.top_k > 0 && s.top_k < a.V;
+    P.want_p = s.top_p < 1.0;
     P.draw = P.sum = P.exact = false;
     P.level = 0;
     P.n_above = 0;
-    const u64 err = static_cast<u64>(static_cast<float>(all) * (kFastErr + 1.5e-11f)) + 8192;
-    P.s_lo = all > err ? all - err : 1;
-    P.s_hi = all + err;
+    total_bounds(all, P.s_lo, P.s_hi);
     P.key = kKeyNegInf;
     P.ties = 0;
-    P.key_m = 0;
-    if (min_p > 0.0) {
-        // the key of the smallest float x with x >= max + T log(min_p)
-        const double at = static_cast<double>(m) + temp * log(min_p);
-        const float f = static_cast<float>(at);
-        P.key_m = order_key(f) + (static_cast<double>(f) < at ? 1u : 0u);
-    }
+    P.key_m = min_p_key(s, r.ws.m);
     Cmd cmd;
     if (!P.want_k && !P.want_p) {
-        if (P.key_m <= kKeyNegInf &&
-            fast_draw<T, THREADS>(r, cmax, cw, all, u, a, row_i, temp, rank == 0, sh))
-            return;
-        Sampler<T, THREADS>::finish(P, cmd);
+        Sampler<T, kThreads>::finish(P, cmd);
+    } else if (a.V <= kList) {
+        cmd = Cmd{kCollect, 0, 2 * kBins, kKeyNegInf + 1, 0xffffffffu, 0, 0, 1};
     } else {
-        // elements from a high chunk maximum on: few, if the row is in no particular order
-        int guess = 0;
-        if (a.V <= kList)
-            guess = nch;
-        else if (nch <= 1024 && P.want_k)
-            guess = top_k <= nch * 9 / 10 ? static_cast<int>(top_k) : 0;
-        else if (nch <= 1024)
-            guess = max(1, nch * 7 / 10);
-        float tau = -INFINITY;
-        if (guess > 0 && a.V > kList) {
-            tau = kth_max<THREADS>(cmax, nch, guess, sh);
-            if (!P.want_k) {
-                // a nucleus far wider than what the maxima alone weigh goes to the histogram
-                u64 up = 0, captured;
-                for (int i = tid; i < nch; i += THREADS)
-                    if (cmax[i] >= tau) up += fixed_weight(cmax[i], r.ws, sh.table);
-                Block<THREADS>::scan(up, dummy, captured, tn, sh);
-                if (captured < part_of(top_p, all, false) / 2) guess = 0;
-            }
-        }
-        if (guess > 0) {
-            cmd = Cmd{kCollect, 0, 2 * kBins, max(kKeyNegInf + 1, order_key(tau)), 0xffffffffu,
-                      0, 0, 1};
-        } else {
-            P.level = 1;
-            cmd = make_hist0(!P.want_k);
-        }
+        P.level = 1;
+        cmd = make_hist0(!P.want_k);
     }
 
-    // ---- steps: the blocks work on their chunks, block 0 decides what comes next
+    // the blocks work on their chunks, block 0 decides what comes next
     for (int step = 0; step < kMaxSteps; ++step) {
         if (cmd.type == kHist)
-            step_hist<T, THREADS>(r, cmd, cmax, sh);
+            step_hist<T, kThreads>(r, cmd, cmax, sh);
         else
-            step_collect<T, THREADS>(r, cmd, cmax, own_w, own_n, sh);
+            step_collect<T, kThreads>(r, cmd, cmax, own_w, own_n, sh);
         cluster_join();
         if (rank == 0) {
             bool done = false;
             if (cmd.type == kHist)
-                Sampler<T, THREADS>::after_hist(r, P, cmd, top_p, static_cast<u64>(top_k), ranks,
-                                                sh);
+                Sampler<T, kThreads>::after_hist(r, P, cmd, s.top_p, static_cast<u64>(s.top_k),
+                                                 ranks, sh);
             else
-                done = Sampler<T, THREADS>::after_collect(r, P, cmd, top_p,
-                                                          static_cast<u64>(top_k), cw, cn, own_w,
-                                                          own_n, ranks, a, row_i, u, temp, all,
-                                                          sh);
+                done = Sampler<T, kThreads>::after_collect(r, P, cmd, s.top_p,
+                                                           static_cast<u64>(s.top_k), cw, cn,
+                                                           own_w, own_n, ranks, a, row_i, s.u,
+                                                           s.temp, all, sh);
             if (done) cmd.type = kDone;
             if (!done && step == kMaxSteps - 1 && tid == 0) {
                 write_row(a, row_i, -1, quiet_nan(), quiet_nan());
@@ -1180,27 +1445,29 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const T* __restrict__ l
     cluster_join();          // block 0's shared memory is read until here
 }
 
-template <typename T, int THREADS>
-cudaError_t launch_rows(const T* logits, const SampleArgs& a, int nch, int ranks,
-                        cudaStream_t stream) {
+template <typename T>
+cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int),
+                        const T* logits, const SampleArgs& a, int nch, int ranks, size_t smem,
+                        bool dependent, cudaStream_t stream) {
     const int own = (nch + ranks - 1) / ranks;
-    const size_t smem = smem_bytes(nch, own);
-    auto kernel = sample_kernel<T, THREADS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.N) * ranks);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, logits, a, nch, own, ranks);
 }
 
@@ -1209,16 +1476,17 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int nch = (a.V + kChunk - 1) / kChunk;
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (int64_t(a.N) * ranks <= 152) return launch_rows<T, 1024>(logits, a, nch, ranks, stream);
-    return launch_rows<T, 256>(logits, a, nch, ranks, stream);
+    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, scan_smem(nch), false,
+                                stream);
+    if (e != cudaSuccess) return e;
+    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks,
+                       search_smem(nch, (nch + ranks - 1) / ranks), true, stream);
 }
 
 }  // namespace
 
 size_t sample_workspace(int64_t N, int64_t V) {
-    (void)N;
-    (void)V;
-    return 0;
+    return stats_offset(N) + size_t(N) * size_t((V + kChunk - 1) / kChunk) * sizeof(float2);
 }
 
 cudaError_t launch_sample(const void* logits, bool bf16, const SampleArgs& args,
