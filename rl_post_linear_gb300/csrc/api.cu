@@ -867,7 +867,25 @@ rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int
     a.uniforms = uniforms, a.mask = active_mask;
     a.temperature_rows = p.temperature_rows, a.top_k_rows = p.top_k_rows;
     a.top_p_rows = p.top_p_rows, a.min_p_rows = p.min_p_rows;
-    a.temperature = p.temperature, a.top_k = p.top_k, a.top_p = p.top_p, a.min_p = p.min_p;
+    a.temperature = p.temperature, a.top_k = p.top_k, a.min_p = p.min_p;
+    if (p.temperature_rows == nullptr) {
+        const double c = 1.4426950408889634074 / p.temperature;
+        a.ch = static_cast<float>(c);
+        a.cl = static_cast<float>(c - static_cast<double>(a.ch));
+    }
+    a.top_p_value = 1.f;
+    if (p.top_p_rows == nullptr && p.top_p < 1.0) {
+        // mant 2^-shift exactly; a value that rounds to 1 stays on
+        int e;
+        const double m = std::frexp(p.top_p, &e);              // top_p = m 2^e, 1/2 <= m < 1
+        a.top_p.mant = static_cast<unsigned long long>(std::ldexp(m, 53));
+        a.top_p.shift = 53 - e;
+        a.top_p_value = std::min(static_cast<float>(p.top_p), 0.99999994f);
+    }
+    if (p.min_p_rows == nullptr && p.min_p > 0.0) {
+        a.min_p_value = std::max(static_cast<float>(p.min_p), 1e-45f);
+        a.min_p_offset = p.temperature * std::log(p.min_p);
+    }
     a.stride = row_stride, a.N = static_cast<int>(N), a.V = static_cast<int>(V);
     a.bits = 46;
     while ((int64_t(1) << (64 - a.bits)) <= V) --a.bits;      // V 2^bits < 2^64

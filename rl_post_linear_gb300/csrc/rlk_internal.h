@@ -303,6 +303,10 @@ cudaError_t launch_norm_bwd(const NormArgs& args, bool center, cudaStream_t stre
 
 // Sampling.  *_rows: one value a row, or nullptr (then the scalar holds for all).
 constexpr double kSampleMinT = 1e-6, kSampleMaxT = 1e6;
+struct SampleFraction {
+    unsigned long long mant;   // mant 2^-shift, shift >= 1
+    int shift;
+};
 struct SampleArgs {
     const float* uniforms;
     const uint8_t* mask;
@@ -310,7 +314,11 @@ struct SampleArgs {
     const int32_t* top_k_rows;
     const float* top_p_rows;
     const float* min_p_rows;
-    double temperature, top_p, min_p;
+    double temperature, min_p;
+    float ch, cl;              // log2(e) / temperature in two floats
+    float top_p_value, min_p_value;   // >= 1 / 0: off
+    SampleFraction top_p;      // exactly, where it is on
+    double min_p_offset;       // temperature log(min_p), where both are scalars
     int64_t top_k, stride;
     int N, V;
     int bits;                  // weights are scaled by 2^bits; V 2^bits < 2^64

@@ -54,20 +54,27 @@ struct WeightScale {
     int shift;      // 62 - bits
 };
 
-// table: the 1024 entries (shared memory).  x <= m, both finite or x = -inf.
-__device__ __forceinline__ unsigned long long fixed_weight(float x, const WeightScale& s,
-                                                           const unsigned long long* table) {
+// t = th + tl of an x <= m; x = -inf gives th = inf (and no meaning to tl)
+__device__ __forceinline__ void scaled_distance(float x, const WeightScale& s, float& th,
+                                                float& tl) {
     // d = dh + dl exactly (two-sum)
     const float dh = s.m - x;
     const float bb = dh - s.m;
     const float dl = (s.m - (dh - bb)) + (-x - bb);
-    const float th = dh * s.ch;
-    if (!(th < 62.f)) return 0;                        // below half a unit; also x = -inf
-    const float tl = fmaf(dh, s.cl, fmaf(dl, s.ch, fmaf(dh, s.ch, -th)));
+    th = __fmul_rn(dh, s.ch);
+    tl = fmaf(dh, s.cl, fmaf(dl, s.ch, fmaf(dh, s.ch, -th)));
+}
+
+// table: the 1024 entries (shared memory).  x <= m, both finite or x = -inf.
+__device__ __forceinline__ unsigned long long fixed_weight(float x, const WeightScale& s,
+                                                           const unsigned long long* table) {
+    float th, tl;
+    scaled_distance(x, s, th, tl);
+    th = fminf(th, 63.f);                              // below half a unit from 62 on
     const float big = th + 12288.f;                    // ulp 2^-10: rounds t to j / 1024
     const int idx = __float_as_int(big) - __float_as_int(12288.f);
     const float r = th - (big - 12288.f);              // exact, |r| <= 2^-11
-    // y and a = y ln 2 scaled by 2^41 (|a| < 2^30)
+    // y and a = y ln 2 scaled by 2^41 (|a| < 2^30); a tl without meaning ends at w = 0
     const int y = __float2int_rn(r * 2199023255552.f) + __float2int_rn(tl * 2199023255552.f);
     const int a = static_cast<int>((static_cast<long long>(y) * 2977044472LL + (1LL << 31)) >> 32);
     const int a2 = __mulhi(a, a);                      // a^2 2^50
@@ -77,7 +84,7 @@ __device__ __forceinline__ unsigned long long fixed_weight(float x, const Weight
     const unsigned long long w =
         t62 - ((static_cast<long long>(q) * static_cast<int>((t62 + (1ULL << 31)) >> 32)) >> 9);
     const int sh = (idx >> 10) + s.shift;              // 1 <= sh
-    return sh > 63 ? 0 : ((w >> (sh - 1)) + 1) >> 1;
+    return sh > 62 ? 0 : ((w >> (sh - 1)) + 1) >> 1;
 }
 
 }  // namespace rlk
