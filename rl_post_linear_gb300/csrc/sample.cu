@@ -53,8 +53,9 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;            // of a scan block
 constexpr int kWarps = kThreads / 32;
+constexpr int kSearch = 512;             // of a search block
 constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
@@ -144,19 +145,6 @@ __device__ __forceinline__ float warp_max(float v) {
     return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 
-// Exclusive prefix over the warp; `total` in every lane.
-__device__ __forceinline__ u64 warp_scan(u64 v, u64& total) {
-    const int lane = threadIdx.x & 31;
-    u64 in = v;
-#pragma unroll 1
-    for (int off = 1; off < 32; off <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, in, off);
-        if (lane >= off) in += o;
-    }
-    total = __shfl_sync(0xffffffffu, in, 31);
-    return in - v;
-}
-
 // Exclusive prefix of v and n over the block's threads, and the totals.  Not inlined, like
 // the other serial parts of a row: they run once, and fetching their code is much of their
 // time.
@@ -164,6 +152,7 @@ struct Scanned {
     u64 v, tv;
     uint32_t n, tn;
 };
+template <int THREADS>
 __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_t* part_n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 iv = v;
@@ -179,7 +168,7 @@ __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_
     __syncthreads();
     Scanned r{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         if (i == warp) r.v = r.tv, r.n = r.tn;
         r.tv += part[i], r.tn += part_n[i];
     }
@@ -355,7 +344,7 @@ __device__ __noinline__ void write_drawn(const SampleArgs& a, int64_t row, int v
 // Shared memory of the scan.
 struct Shared0 {
     u64 table[kExpEntries];
-    u64 order[kShort], w[kShort];
+    u64 order[kShort], w[kShort];        // the list, then sorted
     u64 part[kWarps];
     uint32_t part_n[kWarps];
     u64 at_w;
@@ -423,7 +412,7 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
     const int c0 = min(r.nch, tid * each), c1 = min(r.nch, c0 + each);
     u64 w = 0;
     for (int c = c0; c < c1; ++c) w += cw[c];
-    w = block_scan(w, 0, sh.part, sh.part_n).v;
+    w = block_scan<kThreads>(w, 0, sh.part, sh.part_n).v;
     if (tid == 0) sh.flag = 0, sh.at = 0, sh.at_w = 0;
     __syncthreads();
     for (int c = c0; c < c1; ++c) {
@@ -431,31 +420,23 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
         w += cw[c];
     }
     __syncthreads();
-    if (tid < 32) {
-        const float part = 2.f * s.u_value * (1.f - s.u_value) * kFastErr + 1.5e-11f;
-        const u64 err = static_cast<u64>(static_cast<float>(all) * part) + 8192;
-        const int chunk = sh.at;
-        const float m = cmax[chunk];
-        const u64 top = fixed_weight(m, r.ws, sh.table);
-        u64 run = sh.at_w;
-        // lane l takes columns 32 j + l, 16 steps
-        int v = -1;
-        float xv = 0.f;
-#pragma unroll 1
-        for (int j = 0; j < kLane; ++j) {
-            const int col = chunk * kChunk + j * 32 + tid;
-            const float x = col < r.V ? load_one(r.x + col) : -INFINITY;
-            const u64 we = scale_weight(ex2_approx((x - m) * r.ws.ch), top);
-            u64 sum;
-            const u64 lo = run + warp_scan(we, sum), hi = lo + we;
-            run += sum;
-            if (lo <= target && (lo == 0 || lo + err <= target) && target + err < hi)
-                v = col, xv = x;
-        }
-        if (v >= 0) {
-            write_drawn(a, row_i, v, xv, r.ws, all, all);
-            sh.flag = 1;
-        }
+    // the chunk's columns in order, two a thread
+    const int chunk = sh.at, col = chunk * kChunk + 2 * tid;
+    const float x0 = col < r.V ? load_one(r.x + col) : -INFINITY;
+    const float x1 = col + 1 < r.V ? load_one(r.x + col + 1) : -INFINITY;
+    const float m = cmax[chunk];
+    const u64 top = fixed_weight(m, r.ws, sh.table);
+    const u64 w0 = scale_weight(ex2_approx((x0 - m) * r.ws.ch), top);
+    const u64 w1 = scale_weight(ex2_approx((x1 - m) * r.ws.ch), top);
+    const u64 lo = sh.at_w + block_scan<kThreads>(w0 + w1, 0, sh.part, sh.part_n).v;
+    const u64 mid = lo + w0, hi = mid + w1;
+    const float part = 2.f * s.u_value * (1.f - s.u_value) * kFastErr + 1.5e-11f;
+    const u64 err = static_cast<u64>(static_cast<float>(all) * part) + 8192;
+    const bool hit0 = lo <= target && (lo == 0 || lo + err <= target) && target + err < mid;
+    const bool hit1 = mid <= target && (mid == 0 || mid + err <= target) && target + err < hi;
+    if (hit0 || hit1) {
+        write_drawn(a, row_i, hit0 ? col : col + 1, hit0 ? x0 : x1, r.ws, all, all);
+        sh.flag = 1;
     }
     __syncthreads();
     return sh.flag != 0;
@@ -463,7 +444,7 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
 
 // A value that enough chunk maxima reach: at least `count` of them, or (need > 0) maxima of
 // a weight of at least `need`.  Between the maximum and `low`, by bisection with a warp a
-// trial: 4 rounds leave 1/6561 of the range.  `low` itself if that is not enough, with
+// trial: 3 rounds leave 1/729 of the range.  `low` itself if that is not enough, with
 // found = false.
 template <typename T>
 __device__ float reach_value(const Row<T>& r, const float* cmax, int count, float need, float low,
@@ -472,12 +453,13 @@ __device__ float reach_value(const Row<T>& r, const float* cmax, int count, floa
     float hi = r.ws.m, lo = low;
     found = true;
 #pragma unroll 1
-    for (int round = 0; round < 4; ++round) {
+    for (int round = 0; round < 3; ++round) {
         // warp w tries the (w + 1)-th of 9 parts below hi; the first round also tries low
-        const float step = (hi - lo) / (kWarps + 1);
+        const float step = (hi - lo) * (1.f / (kWarps + 1));
         const float x = round == 0 && warp == kWarps - 1 ? low : hi - step * (warp + 1);
         int n = 0;
         float w = 0.f;
+#pragma unroll 4
         for (int c = lane; c < r.nch; c += 32) {
             const float v = cmax[c];
             n += v >= x ? 1 : 0;
@@ -503,31 +485,37 @@ __device__ float reach_value(const Row<T>& r, const float* cmax, int count, floa
     return lo;
 }
 
-// Sorts the first n of (order, w) by descending order (all different): bitonic, a pair a
-// thread; strides below 64 stay inside a warp's 64 elements.  Places up to the next power
-// of two are filled with 0.
+// Sorts the first n <= kShort of (order, w) by descending order (all different), each
+// element's place counted out by a thread: at these lengths quicker than a sorting network,
+// whose steps each wait for the one before.  `order` is padded to a multiple of 4.
 __device__ __noinline__ void sort_list(uint32_t n, u64* order, u64* w) {
-    uint32_t size = 64;
-    while (size < n) size *= 2;
-    for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) order[i] = w[i] = 0;
+    constexpr int kPer = kShort / kThreads;
+    const uint32_t padded = (n + 3) / 4 * 4;
+    if (threadIdx.x < padded - n) order[n + threadIdx.x] = 0;
     __syncthreads();
-    const uint32_t t = threadIdx.x;
-#pragma unroll 1
-    for (uint32_t k = 2; k <= size; k *= 2)
-#pragma unroll 1
-        for (uint32_t stride = k / 2; stride > 0; stride /= 2) {
-            if (2 * t < size) {
-                const uint32_t i = 2 * t - (t & (stride - 1)), j = i + stride;
-                const u64 oi = order[i], oj = order[j];
-                if ((oi < oj) == ((i & k) == 0)) {
-                    const u64 wi = w[i], wj = w[j];
-                    order[i] = oj, order[j] = oi;
-                    w[i] = wj, w[j] = wi;
-                }
+    u64 me[kPer], mw[kPer];
+    uint32_t place[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const uint32_t i = threadIdx.x + q * kThreads;
+        me[q] = i < n ? order[i] : 0;
+        mw[q] = i < n ? w[i] : 0;
+        place[q] = 0;
+        // warps without elements of their own have nothing to count
+        if ((i & ~31u) < n) {
+#pragma unroll 2
+            for (uint32_t j = 0; j < padded; j += 4) {
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(order + j);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(order + j + 2);
+                place[q] += (a.x > me[q] ? 1u : 0u) + (a.y > me[q] ? 1u : 0u) +
+                            (b.x > me[q] ? 1u : 0u) + (b.y > me[q] ? 1u : 0u);
             }
-            if (stride > 32 || (stride == 1 && k >= 64)) __syncthreads();
-            else __syncwarp();
         }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+        if (threadIdx.x + q * kThreads < n) order[place[q]] = me[q], w[place[q]] = mw[q];
     __syncthreads();
 }
 
@@ -562,7 +550,7 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
         if (cmax[c] >= tau_x) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
     __syncthreads();
     const int n_ids = sh.n_ids;
-    constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
+    constexpr int kAhead = sizeof(T) == 4 ? 3 : 4;
 #pragma unroll 1
     for (int i0 = warp; i0 < n_ids; i0 += kAhead * kWarps) {
         Chunk<T> ch[kAhead];
@@ -601,7 +589,7 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     // thread t holds elements 2 t and 2 t + 1 of the order
     const uint32_t i0 = 2 * tid, i1 = i0 + 1;
     const u64 w0 = i0 < n ? sh.w[i0] : 0, w1 = i1 < n ? sh.w[i1] : 0;
-    const Scanned sum = block_scan(w0 + w1, 0, sh.part, sh.part_n);
+    const Scanned sum = block_scan<kThreads>(w0 + w1, 0, sh.part, sh.part_n);
     const u64 b0 = sum.v, b1 = b0 + w0;
     uint32_t keep = n;
     u64 s_k = sum.tv;                                // fewer elements than top_k: all of them
@@ -646,7 +634,7 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     __syncthreads();
     sort_list(keep, sh.order, sh.w);
     const u64 v0 = i0 < keep ? sh.w[i0] : 0, v1 = i1 < keep ? sh.w[i1] : 0;
-    const u64 c0 = block_scan(v0 + v1, 0, sh.part, sh.part_n).v, c1 = c0 + v0;
+    const u64 c0 = block_scan<kThreads>(v0 + v1, 0, sh.part, sh.part_n).v, c1 = c0 + v0;
     const bool hit0 = c0 <= target && target < c1, hit1 = c1 <= target && target < c1 + v1;
     if (hit0 || hit1) {
         const u64 o = sh.order[hit0 ? i0 : i1];
@@ -690,6 +678,12 @@ __global__ void __launch_bounds__(kThreads, 4)
         return;
     }
     Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
+    if (rank == 0)
+        for (int i = tid; i < kExpEntries / 2; i += kThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(sh.table + 2 * i)),
+                         "l"(kExpTable.v + 2 * i)
+                         : "memory");
     float best = -INFINITY;
     constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
 #pragma unroll 1
@@ -712,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     if (rank != 0) return;
-    for (int i = tid; i < kExpEntries; i += kThreads) sh.table[i] = kExpTable.v[i];
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
@@ -746,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         cw[i] = w;
         mine += w;
     }
-    const u64 all = block_scan(mine, 0, sh.part, sh.part_n).tv;   // its barriers publish cw
+    const u64 all = block_scan<kThreads>(mine, 0, sh.part, sh.part_n).tv;   // its barriers publish cw
     const bool done = s.want_k || s.want_p || s.want_m
                           ? short_draw(r, s, cmax, ids, all, a, row_i, sh)
                           : fast_draw(r, cmax, cw, all, s, a, row_i, sh);
@@ -769,6 +763,7 @@ struct Cmd {
     int shift;        // kHist: bins of the keys, (khi - key) >> shift; -1: of the distance
     int by_weight;    // kHist: 12-bit weights instead of counts
     int list;         // kCollect: 1 lists the elements inside, 0 counts them per chunk
+    int total;        // also the exact weight of all elements
 };
 
 // Shared memory of the search.
@@ -779,9 +774,9 @@ struct Shared {
     uint32_t own_key[kList], own_idx[kList];   // this block's part of it
     uint32_t hist[kBins];
     uint32_t cnt[256], lo[256], hi[256];
-    u64 part[kWarps];
-    uint32_t part_n[kWarps];
-    u64 own_above;                       // exact weight above the window, all own chunks
+    u64 part[kSearch / 32];
+    uint32_t part_n[kSearch / 32];
+    u64 own_above, own_total;            // exact weights, all own chunks
     uint32_t own_count;
     uint32_t n_list, key_m;
     // results of block-wide searches
@@ -797,23 +792,56 @@ __device__ __forceinline__ float distance(float x, const Row<T>& r) {
     return fminf((r.ws.m - x) * r.scale, 2.f * kBins);
 }
 
+// Which of a lane's 16 elements are above and inside the window, as bits.
+template <typename T>
+__device__ __forceinline__ void classify(const Chunk<T>& c, const Row<T>& r, const Cmd& cmd,
+                                         uint32_t& up, uint32_t& in) {
+    up = in = 0;
+    if (cmd.khi <= kKeyNegInf) {                     // all that is not -inf is above
+        up = (1u << kLane) - 1;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) {
+        const float x = c.get(e);
+        const int b = static_cast<int>(distance(x, r));
+        const uint32_t k = order_key(x);
+        const bool over = b < cmd.b1 || (b <= cmd.b2 && k > cmd.khi);
+        const bool inside = !over && b <= cmd.b2 && k >= cmd.klo && k > kKeyNegInf;
+        up |= (over ? 1u : 0u) << e;
+        in |= (inside ? 1u : 0u) << e;
+    }
+}
+
+// exact weights of a lane's elements: of those in `up`, and of all
+template <typename T>
+__device__ __forceinline__ void weigh(const Chunk<T>& c, const Row<T>& r, const u64* table,
+                                      uint32_t up, u64& above, u64& all) {
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) {
+        const u64 w = fixed_weight(c.get(e), r.ws, table);
+        all += w;
+        above += (up >> e) & 1u ? w : 0;
+    }
+}
+
 // Histogram of the window; for windows of keys also the exact weight above it.
 template <typename T>
 __device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const float* cmax,
                                        Shared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.hist[i] = 0;
-    if (threadIdx.x == 0) sh.own_above = 0;
+    for (int i = threadIdx.x; i < kBins; i += kSearch) sh.hist[i] = 0;
+    if (threadIdx.x == 0) sh.own_above = sh.own_total = 0;
     __syncthreads();
     const float unit = kRange / kBins;
     const float x_hi = key_value(cmd.khi);
-    const int last = min(cmd.b2, kBins - 1);
-    u64 above = 0;
+    u64 above = 0, all = 0;
 #pragma unroll 1
-    for (int i = warp; i < r.mine; i += kWarps) {
+    for (int i = warp; i < r.mine; i += kSearch / 32) {
         const float top = cmax[r.first + i];
-        if (static_cast<int>(distance(top, r)) > last ||
-            (cmd.shift >= 0 && order_key(top) < cmd.klo))
+        const int top_bin = static_cast<int>(distance(top, r));
+        if (top_bin >= kBins || (!cmd.total && (top_bin > cmd.b2 ||
+                                                (cmd.shift >= 0 && order_key(top) < cmd.klo))))
             continue;
         Chunk<T> c;
         c.load(r.x, r.V, r.first + i, lane, r.vec);
@@ -823,34 +851,27 @@ __device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const fl
                 const float t = distance(c.get(e), r);
                 const int b = static_cast<int>(t);
                 const float q = cmd.by_weight ? rintf(4096.f * ex2_approx((b - t) * unit)) : 1.f;
-                if (b <= last) atomicAdd(&sh.hist[b], static_cast<uint32_t>(q));
+                if (b < kBins) atomicAdd(&sh.hist[b], static_cast<uint32_t>(q));
             }
             continue;
         }
-        uint32_t up = 0;                             // elements above, inside
+        uint32_t up, in;
+        classify(c, r, cmd, up, in);
+        if (cmd.by_weight && __any_sync(0xffffffffu, cmd.total || up != 0))
+            weigh(c, r, sh.table, up, above, all);
 #pragma unroll
         for (int e = 0; e < kLane; ++e) {
             const float x = c.get(e);
-            const int b = static_cast<int>(distance(x, r));
-            const uint32_t k = order_key(x);
-            const bool over = b < cmd.b1 || (b <= last && k > cmd.khi);
-            up |= (over ? 1u : 0u) << e;
-            if (!over && b <= last && k >= cmd.klo) {
-                const float q =
-                    cmd.by_weight ? rintf(4096.f * ex2_approx((x - x_hi) * r.ws.ch)) : 1.f;
-                atomicAdd(&sh.hist[(cmd.khi - k) >> cmd.shift], static_cast<uint32_t>(q));
-            }
-        }
-        if (cmd.by_weight && __any_sync(0xffffffffu, up != 0)) {
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-                const u64 w = fixed_weight(c.get(e), r.ws, sh.table);
-                above += (up >> e) & 1u ? w : 0;
-            }
+            const float q = cmd.by_weight ? rintf(4096.f * ex2_approx((x - x_hi) * r.ws.ch)) : 1.f;
+            if ((in >> e) & 1u)
+                atomicAdd(&sh.hist[(cmd.khi - order_key(x)) >> cmd.shift],
+                          static_cast<uint32_t>(q));
         }
     }
     above = warp_sum(above);
+    all = warp_sum(all);
     if (lane == 0 && above != 0) atomicAdd(&sh.own_above, above);
+    if (lane == 0 && all != 0) atomicAdd(&sh.own_total, all);
     __syncthreads();
 }
 
@@ -859,33 +880,23 @@ template <typename T>
 __device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const float* cmax,
                                           u64* own_w, uint32_t* own_n, Shared& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) sh.own_count = 0;
+    if (threadIdx.x == 0) sh.own_count = 0, sh.own_total = 0;
     __syncthreads();
+    u64 all = 0;
 #pragma unroll 1
-    for (int i = warp; i < r.mine; i += kWarps) {
+    for (int i = warp; i < r.mine; i += kSearch / 32) {
         const float top = cmax[r.first + i];
+        const int top_bin = static_cast<int>(distance(top, r));
         u64 w = 0;
         uint32_t n = 0;
-        if (static_cast<int>(distance(top, r)) <= cmd.b2 && order_key(top) >= cmd.klo) {
+        const bool near = top_bin <= cmd.b2 && order_key(top) >= cmd.klo;
+        if (near || (cmd.total && top_bin < kBins)) {
             Chunk<T> c;
             c.load(r.x, r.V, r.first + i, lane, r.vec);
-            uint32_t up = 0, in = 0;
-#pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-                const float x = c.get(e);
-                const int b = static_cast<int>(distance(x, r));
-                const uint32_t k = order_key(x);
-                const bool over = b < cmd.b1 || (b <= cmd.b2 && k > cmd.khi);
-                const bool inside = !over && b <= cmd.b2 && k >= cmd.klo && k > kKeyNegInf;
-                up |= (over ? 1u : 0u) << e;
-                in |= (inside ? 1u : 0u) << e;
-            }
-            if (__any_sync(0xffffffffu, up != 0)) {
-#pragma unroll
-                for (int e = 0; e < kLane; ++e) {
-                    const u64 we = fixed_weight(c.get(e), r.ws, sh.table);
-                    w += (up >> e) & 1u ? we : 0;
-                }
+            uint32_t up, in;
+            classify(c, r, cmd, up, in);
+            if (__any_sync(0xffffffffu, cmd.total || up != 0)) {
+                weigh(c, r, sh.table, up, w, all);
                 w = warp_sum(w);
             }
             if (cmd.list == 0) {
@@ -907,6 +918,8 @@ __device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const
         }
         if (lane == 0) own_w[i] = w, own_n[i] = n;
     }
+    all = warp_sum(all);
+    if (lane == 0 && all != 0) atomicAdd(&sh.own_total, all);
     __syncthreads();
 }
 
@@ -922,11 +935,11 @@ __device__ __noinline__ Selected list_select(bool by_weight, u64 need, Shared& s
 #pragma unroll 1
     for (int level = 3; level >= 0; --level) {
         __syncthreads();
-        for (int i = threadIdx.x; i < 256; i += kThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+        if (threadIdx.x < 256) sh.cnt[threadIdx.x] = sh.lo[threadIdx.x] = sh.hi[threadIdx.x] = 0;
         __syncthreads();
         const uint32_t mask = level == 3 ? 0u : 0xffffffffu << (8 * (level + 1));
 #pragma unroll 1
-        for (uint32_t i = threadIdx.x; i < sh.n_list; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSearch) {
             const uint32_t k = sh.key[i];
             if ((k & mask) != prefix) continue;
             const uint32_t b = (k >> (8 * level)) & 255u;
@@ -939,13 +952,13 @@ __device__ __noinline__ Selected list_select(bool by_weight, u64 need, Shared& s
         __syncthreads();
         // thread t holds bin 255 - t, from the top down
         const int b = 255 - int(threadIdx.x);
-        const u64 w = (u64(sh.hi[b]) << 32) | sh.lo[b];
-        const uint32_t n = sh.cnt[b];
-        const Scanned s = block_scan(w, n, sh.part, sh.part_n);
+        const u64 w = b >= 0 ? (u64(sh.hi[b]) << 32) | sh.lo[b] : 0;
+        const uint32_t n = b >= 0 ? sh.cnt[b] : 0;
+        const Scanned s = block_scan<kSearch>(w, n, sh.part, sh.part_n);
         const u64 before = by_weight ? w_up + s.v : n_up + s.n;
         const u64 after = before + (by_weight ? w : u64(n));
         // the first bin to reach the need; the lowest one if none does
-        if ((before < need && after >= need) || (b == 0 && after < need)) {
+        if (b >= 0 && ((before < need && after >= need) || (b == 0 && after < need))) {
             sh.at = b;
             sh.at_w = w_up + s.v;
             sh.at_n = static_cast<uint32_t>(n_up) + s.n;
@@ -963,9 +976,7 @@ __device__ __noinline__ Selected list_select(bool by_weight, u64 need, Shared& s
 struct Search {
     bool want_k, want_p;       // boundaries still to be found
     bool draw;                 // the next kCollect is the last
-    bool sum;                  // the next kCollect is the exact total
     bool exact;                // s_lo == s_hi is the exact weight that top_p refers to
-    int level;                 // histograms of this search so far
     u64 n_above;               // count above the window (want_k)
     u64 s_lo, s_hi;            // bounds of the total that top_p refers to
     uint32_t key;              // the boundary so far
@@ -978,11 +989,11 @@ struct Search {
 };
 
 __device__ __forceinline__ Cmd make_hist0(bool by_weight) {
-    return Cmd{kHist, 0, kBins - 1, 0u, 0xffffffffu, -1, by_weight ? 1 : 0, 0};
+    return Cmd{kHist, 0, kBins - 1, 0u, 0xffffffffu, -1, by_weight ? 1 : 0, 0, 0};
 }
 // exact weights above a key, and the number of elements equal to it
 __device__ __forceinline__ Cmd make_above(uint32_t key) {
-    return Cmd{kCollect, 0, 2 * kBins, key, key, 0, 0, 0};
+    return Cmd{kCollect, 0, 2 * kBins, key, key, 0, 0, 0, 0};
 }
 
 // the boundary is known up to min_p: the last step
@@ -995,42 +1006,42 @@ __device__ __forceinline__ void ask_draw(Search& P, Cmd& cmd) {
 // the top_p search from its beginning, or the end of the search without top_p
 __device__ __forceinline__ void start_p(Search& P, Cmd& cmd) {
     if (!P.want_p) return ask_draw(P, cmd);
-    P.level = 1;
     cmd = make_hist0(true);
 }
-__device__ __forceinline__ void ask_sum(Search& P, Cmd& cmd) {
-    P.sum = true;
-    cmd = make_above(0u);
-}
-// A histogram of the window's keys.  Without the exact total its error would not let the
-// window shrink much further.
-__device__ __forceinline__ void next_hist(Search& P, Cmd& cmd) {
-    ++P.level;
-    if (!P.want_k && P.level > 2 && !P.exact) return ask_sum(P, cmd);
+// a histogram of the window's keys
+__device__ __forceinline__ void next_hist(Cmd& cmd) {
     cmd.type = kHist;
     const uint32_t span = cmd.khi - cmd.klo;
     cmd.shift = 0;
     while ((span >> cmd.shift) >= kBins) ++cmd.shift;
+}
+// the exact total, where this step formed it
+__device__ __forceinline__ void take_total(Search& P, const Cmd& cmd, int ranks, Shared& sh) {
+    if (!cmd.total) return;
+    u64 t = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += k < ranks ? *peer(&sh.own_total, k) : 0;
+    P.exact = true;
+    P.s_lo = P.s_hi = P.all = t;
 }
 
 // Narrows the window from the cluster's histograms and asks for the next step.
 template <typename T>
 __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, int ranks,
                                         Shared& sh) {
-    constexpr int kPer = kBins / kThreads;
+    constexpr int kPer = kBins / kSearch;
+    static_assert(kPer == 4, "a thread takes 16 bytes of each histogram");
     const int b0 = threadIdx.x * kPer;
-    u64 q[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) q[i] = 0;
+    u64 q[kPer] = {0, 0, 0, 0};
     u64 above = 0;
-#pragma unroll 1
-    for (int k = 0; k < ranks; ++k) {
-        const uint4* h = reinterpret_cast<const uint4*>(peer(sh.hist, k) + b0);
-        const uint4 h0 = h[0], h1 = h[1];
-        q[0] += h0.x, q[1] += h0.y, q[2] += h0.z, q[3] += h0.w;
-        q[4] += h1.x, q[5] += h1.y, q[6] += h1.z, q[7] += h1.w;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k >= ranks) break;
+        const uint4 h = *reinterpret_cast<const uint4*>(peer(sh.hist, k) + b0);
+        q[0] += h.x, q[1] += h.y, q[2] += h.z, q[3] += h.w;
         above += *peer(&sh.own_above, k);
     }
+    if (cmd.shift >= 0) take_total(P, cmd, ranks, sh);
     u64 mine = 0;
     const bool keys = cmd.shift >= 0, single = cmd.shift == 0;
     const float unit = kRange / kBins;
@@ -1056,12 +1067,14 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
             if (q[i] != 0) {
                 const float x = key_value(cmd.khi - (b0 + i));
                 const float code = rintf(4096.f * ex2_approx((x - x_hi) * r.ws.ch));
-                weight[i] = q[i] / static_cast<u64>(code) * fixed_weight(x, r.ws, sh.table);
+                // the count is below 2^22 and the quotient off by less than 2^-23 of it
+                weight[i] = __float2ull_rn(__fdiv_rn(static_cast<float>(q[i]), code)) *
+                            fixed_weight(x, r.ws, sh.table);
             }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += weight[i];
-    const u64 before = block_scan(mine, 0, sh.part, sh.part_n).v;
+    const u64 before = block_scan<kSearch>(mine, 0, sh.part, sh.part_n).v;
     // the first bins at which the running sum surely may, and surely must, have reached the
     // need
     if (threadIdx.x == 0) sh.at = sh.at2 = kBins, sh.at_w = 0;
@@ -1100,7 +1113,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
         if (b0 + i >= j1 && b0 + i <= j2) est += q[i];
-    est = block_scan(est, 0, sh.part, sh.part_n).tv;
+    est = block_scan<kSearch>(est, 0, sh.part, sh.part_n).tv;
     if (cmd.by_weight) est = est / 3600 + 1;
     if (at == kBins) {
         // fewer elements of weight > 0 than top_k: nothing is cut (a weight is reached)
@@ -1135,7 +1148,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         cmd.list = cmd.klo == cmd.khi ? 0 : 1;
         return;
     }
-    next_hist(P, cmd);
+    next_hist(cmd);
 }
 
 // Draws from the kept set: cw[c] holds the chunks' weight above the window, cn[c] the
@@ -1147,7 +1160,7 @@ __device__ __noinline__ void search_draw(const Row<T>& r, const Search& P, const
     const int tid = threadIdx.x;
     if (cmd.list) {
 #pragma unroll 1
-        for (uint32_t i = tid; i < sh.n_list; i += kThreads) {
+        for (uint32_t i = tid; i < sh.n_list; i += kSearch) {
             const int c = sh.idx[i] / kChunk;
             if (sh.key[i] > P.key) atomicAdd(&cw[c], sh.w[i]);
             else if (sh.key[i] == P.key) atomicAdd(&cn[c], 1u);
@@ -1156,12 +1169,12 @@ __device__ __noinline__ void search_draw(const Row<T>& r, const Search& P, const
     }
     const u64 wt = P.ties == 0 ? 0 : fixed_weight(key_value(P.key), r.ws, sh.table);
     const uint32_t ties = static_cast<uint32_t>(min(P.ties, u64(0xffffffffu)));
-    const int each = (r.nch + kThreads - 1) / kThreads;
+    const int each = (r.nch + kSearch - 1) / kSearch;
     const int c0 = min(r.nch, tid * each), c1 = min(r.nch, c0 + each);
     u64 w = 0;
     uint32_t n = 0;
     for (int c = c0; c < c1; ++c) w += cw[c], n += cn[c];
-    const Scanned s = block_scan(w, n, sh.part, sh.part_n);
+    const Scanned s = block_scan<kSearch>(w, n, sh.part, sh.part_n);
     w = s.v, n = s.n;
     const u64 kept = s.tv + min(s.tn, ties) * wt;
     // nothing cut: one total for both; otherwise the kept part is at most the whole
@@ -1177,30 +1190,19 @@ __device__ __noinline__ void search_draw(const Row<T>& r, const Search& P, const
         if (lo <= target && target < hi) sh.at = c, sh.at_w = w_at, sh.at_n = n_at;
     }
     __syncthreads();
-    if (tid >= 32) return;
-    // one warp goes through the chunk in index order, 32 columns at a time
-    u64 run = sh.at_w;
-    uint32_t seen = sh.at_n;
-    const int chunk = sh.at;
-    int v = -1;
-    float xv = 0.f;
-#pragma unroll 1
-    for (int j = 0; j < kLane; ++j) {
-        const int col = chunk * kChunk + j * 32 + tid;
-        const float x = col < r.V ? load_one(r.x + col) : -INFINITY;
-        const uint32_t k = order_key(x);
-        const u64 we = k > P.key ? fixed_weight(x, r.ws, sh.table) : 0;
-        const uint32_t tie = __ballot_sync(0xffffffffu, k == P.key);
-        u64 sum;
-        const u64 w_at = run + warp_scan(we, sum);
-        const uint32_t n_at = seen + __popc(tie & ((1u << tid) - 1));
-        const u64 lo = w_at + min(n_at, ties) * wt;
-        const u64 hi = w_at + we + min(n_at + ((tie >> tid) & 1u), ties) * wt;
-        if (lo <= target && target < hi) v = col, xv = x;
-        run += sum;
-        seen += __popc(tie);
-    }
-    if (v >= 0) write_drawn(a, row_i, v, xv, r.ws, all, kept);
+    // the chunk's columns in order, one a thread
+    static_assert(kSearch == kChunk, "a thread takes a column");
+    const int col = sh.at * kChunk + tid;
+    const float x = col < r.V ? load_one(r.x + col) : -INFINITY;
+    const uint32_t k = order_key(x);
+    const u64 we = k > P.key ? fixed_weight(x, r.ws, sh.table) : 0;
+    const uint32_t tie = k == P.key ? 1 : 0;
+    const u64 w_at = sh.at_w;
+    const uint32_t n_at = sh.at_n;
+    const Scanned in = block_scan<kSearch>(we, tie, sh.part, sh.part_n);
+    const u64 lo = w_at + in.v + min(n_at + in.n, ties) * wt;
+    const u64 hi = w_at + in.v + we + min(n_at + in.n + tie, ties) * wt;
+    if (lo <= target && target < hi) write_drawn(a, row_i, col, x, r.ws, all, kept);
 }
 
 // All blocks' weights and counts per chunk, and their lists as one; sums in `above`,
@@ -1212,7 +1214,7 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
     u64 mine = 0;
     uint32_t n_mine = 0;
 #pragma unroll 2
-    for (int c = threadIdx.x; c < r.nch; c += kThreads) {
+    for (int c = threadIdx.x; c < r.nch; c += kSearch) {
         const int k = c / r.own, i = c - k * r.own;
         const u64 w = peer(own_w, k)[i];
         const uint32_t n = peer(own_n, k)[i];
@@ -1221,7 +1223,7 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
         mine += w;
         n_mine += n;
     }
-    const Scanned s = block_scan(mine, n_mine, sh.part, sh.part_n);
+    const Scanned s = block_scan<kSearch>(mine, n_mine, sh.part, sh.part_n);
     above = s.tv;
     inside = s.tn;
     if (!cmd.list) return 0;
@@ -1234,7 +1236,7 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
         if (over) break;
         const uint32_t* pk = peer(sh.own_key, k);
         const uint32_t* pi = peer(sh.own_idx, k);
-        for (uint32_t i = threadIdx.x; i < m; i += kThreads) {
+        for (uint32_t i = threadIdx.x; i < m; i += kSearch) {
             const uint32_t key = pk[i];
             sh.key[n + i] = key;
             sh.idx[n + i] = pi[i];
@@ -1260,22 +1262,16 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
         search_draw(r, P, cmd, cw, cn, a, row_i, u, sh);
         return true;
     }
-    if (P.sum) {                         // the exact total: search again with it
-        P.sum = false;
-        P.exact = true;
-        P.s_lo = P.s_hi = P.all = above;
-        start_p(P, cmd);
-        return false;
-    }
+    take_total(P, cmd, ranks, sh);
     if (n == 0xffffffffu) {              // the list did not hold the window
-        next_hist(P, cmd);
+        next_hist(cmd);
         return false;
     }
     u64 list_w;
     if (cmd.list) {
         u64 mine = 0;
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads) mine += sh.w[i];
-        list_w = block_scan(mine, 0, sh.part, sh.part_n).tv;
+        for (uint32_t i = threadIdx.x; i < n; i += kSearch) mine += sh.w[i];
+        list_w = block_scan<kSearch>(mine, 0, sh.part, sh.part_n).tv;
     } else {
         list_w = inside * fixed_weight(key_value(cmd.klo), r.ws, sh.table);
     }
@@ -1307,29 +1303,19 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
         }
     }
     if (P.want_p) {
-        const u64 need_lo = P.need(P.s_lo), need_hi = P.need(P.s_hi);
-        if (need_lo <= above || need_hi > above + list_w) {
-            // the total's bounds straddle the window.  Exact sums always put the need into
-            // it; were they not to, everything is kept.
-            if (!P.exact) {
-                ask_sum(P, cmd);
-            } else {
-                P.key = kKeyNegInf;
-                P.ties = 0;
-                ask_draw(P, cmd);
-            }
+        const u64 need = P.need(P.s_lo);     // exact by now
+        if (need <= above || need > above + list_w) {
+            // cannot be: the window was drawn around every total within its bounds
+            P.key = kKeyNegInf;
+            P.ties = 0;
+            ask_draw(P, cmd);
             return false;
         }
         Selected at{cmd.klo, 0, 0};
-        if (cmd.list) at = list_select(true, need_lo - above, sh);
+        if (cmd.list) at = list_select(true, need - above, sh);
         const u64 wt = fixed_weight(key_value(at.key), r.ws, sh.table);
-        const u64 lo = need_lo - above - at.w, hi = need_hi - above - at.w;
         P.key = at.key;
-        P.ties = wt == 0 ? 0 : (lo + wt - 1) / wt;
-        if (need_hi != need_lo && (wt == 0 || (hi + wt - 1) / wt != P.ties)) {
-            ask_sum(P, cmd);             // the total's error matters here
-            return false;
-        }
+        P.ties = wt == 0 ? 0 : (need - above - at.w + wt - 1) / wt;
         P.want_p = false;
     }
     if (P.key_m > P.key) {
@@ -1352,7 +1338,7 @@ __host__ __device__ constexpr size_t search_smem(int nch, int own) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kSearch, 2)
     sample_search_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
                          int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1373,16 +1359,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
     r.ws.m = head->m;
     const float2* stats = row_stats(a, row_i, nch);
-    for (int i = tid; i < nch; i += kThreads) cmax[i] = stats[i].x;
-    for (int i = tid; i < kExpEntries; i += kThreads) sh.table[i] = kExpTable.v[i];
+    for (int i = tid; i < nch; i += kSearch) cmax[i] = stats[i].x;
+    for (int i = tid; i < kExpEntries; i += kSearch) sh.table[i] = kExpTable.v[i];
     if (tid == 0) sh.key_m = s.want_m ? min_p_key(a, row_i, r.ws.m) : 0;
     __syncthreads();
 
     Search P;
     P.want_k = s.want_k;
     P.want_p = s.want_p;
-    P.draw = P.sum = P.exact = false;
-    P.level = 0;
+    P.draw = P.exact = false;
     P.n_above = 0;
     P.all = head->all;
     total_bounds(P.all, P.s_lo, P.s_hi);
@@ -1395,13 +1380,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (!P.want_k && !P.want_p) {
         ask_draw(P, cmd);
     } else if (a.V <= kList) {           // the whole row fits the list
-        cmd = Cmd{kCollect, 0, 2 * kBins, kKeyNegInf + 1, 0xffffffffu, 0, 0, 1};
-        P.level = 1;
+        cmd = Cmd{kCollect, 0, 2 * kBins, kKeyNegInf + 1, 0xffffffffu, 0, 0, 1, 0};
     } else {
-        P.level = 1;
         cmd = make_hist0(!P.want_k);
     }
 
+    cmd.total = P.want_p && !P.want_k && cmd.type == kCollect;
     // the blocks work on their chunks, block 0 decides what comes next
     for (int step = 0; step < kMaxSteps; ++step) {
         if (cmd.type == kHist)
@@ -1416,6 +1400,9 @@ __global__ void __launch_bounds__(kThreads, 3)
             else
                 done = after_collect(r, P, cmd, cw, cn, own_w, own_n, ranks, a, row_i, s.u, sh);
             if (done) cmd.type = kDone;
+            // top_p refers to the exact total: formed on the way, in a pass that is made anyway
+            cmd.total = P.want_p && !P.want_k && !P.exact &&
+                        !(cmd.type == kHist && cmd.shift < 0);
             if (!done && step == kMaxSteps - 1 && tid == 0)
                 write_failed(a, row_i, RLK_DEVERR_WAIT_TIMEOUT);
             __syncthreads();
@@ -1430,8 +1417,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 template <typename T>
 cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int),
-                        const T* logits, const SampleArgs& a, int nch, int ranks, size_t smem,
-                        bool dependent, cudaStream_t stream) {
+                        const T* logits, const SampleArgs& a, int nch, int ranks, int threads,
+                        size_t smem, bool dependent, cudaStream_t stream) {
     const int own = (nch + ranks - 1) / ranks;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -1441,7 +1428,7 @@ cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.N) * ranks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1461,10 +1448,10 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int nch = (a.V + kChunk - 1) / kChunk;
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, scan_smem(nch), false,
-                                stream);
+    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, kThreads,
+                                scan_smem(nch), false, stream);
     if (e != cudaSuccess) return e;
-    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks,
+    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, kSearch,
                        search_smem(nch, (nch + ranks - 1) / ranks), true, stream);
 }
 

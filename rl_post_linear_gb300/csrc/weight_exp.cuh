@@ -45,7 +45,7 @@ constexpr ExpTable make_exp_table() {
     return t;
 }
 
-__device__ const ExpTable kExpTable = make_exp_table();
+__device__ const __align__(16) ExpTable kExpTable = make_exp_table();
 
 // t = d (ch + cl), d = m - x
 struct WeightScale {
@@ -74,17 +74,17 @@ __device__ __forceinline__ unsigned long long fixed_weight(float x, const Weight
     const float big = th + 12288.f;                    // ulp 2^-10: rounds t to j / 1024
     const int idx = __float_as_int(big) - __float_as_int(12288.f);
     const float r = th - (big - 12288.f);              // exact, |r| <= 2^-11
-    // y and a = y ln 2 scaled by 2^41 (|a| < 2^30); a tl without meaning ends at w = 0
+    // y = t - j / 1024 and a = y ln 2 by 2^41, |a| < 2^30 (a tl without meaning ends at w = 0)
     const int y = __float2int_rn(r * 2199023255552.f) + __float2int_rn(tl * 2199023255552.f);
-    const int a = static_cast<int>((static_cast<long long>(y) * 2977044472LL + (1LL << 31)) >> 32);
-    const int a2 = __mulhi(a, a);                      // a^2 2^50
-    const int a3 = __mulhi(a2, a);                     // a^3 2^59
+    const int a = static_cast<int>((static_cast<long long>(y) * 1488522236 + (1LL << 30)) >> 31);
+    const int a2 = __mulhi(a, a);                      // a^2 by 2^50
+    const int a3 = __mulhi(a2, a);                     // a^3 by 2^59
     const int q = a - (a2 >> 10) + (__mulhi(a3, 715827883) >> 18);
     const unsigned long long t62 = table[idx & (kExpEntries - 1)];
     const unsigned long long w =
-        t62 - ((static_cast<long long>(q) * static_cast<int>((t62 + (1ULL << 31)) >> 32)) >> 9);
-    const int sh = (idx >> 10) + s.shift;              // 1 <= sh
-    return sh > 62 ? 0 : ((w >> (sh - 1)) + 1) >> 1;
+        t62 - ((static_cast<long long>(q) * static_cast<int>(t62 >> 32)) >> 9);
+    const int sh = min((idx >> 10) + s.shift, 64);     // 16 <= sh; w < 2^62 + 2^51
+    return ((w >> (sh - 1)) + 1) >> 1;
 }
 
 }  // namespace rlk
