@@ -269,8 +269,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without building a torch Stream object (2.8 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -278,6 +284,9 @@ def _stream(stream):
 
 
 def _need(t, dtype, name, shape=None):
+    if (t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda:
@@ -666,29 +675,35 @@ def rlk_grpo_clip_loss(logp_new, logp_old, advantages, active_mask, eps_low, eps
     _check("rlk_grpo_clip_loss", st)
 
 
+_DTYPE_CODES = {torch.float32: RLK_DTYPE_F32, torch.bfloat16: RLK_DTYPE_BF16}
+
+
 def _dtype_code(t, name):
-    if t.dtype == torch.float32:
-        return RLK_DTYPE_F32
-    if t.dtype == torch.bfloat16:
-        return RLK_DTYPE_BF16
-    raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    return code
 
 
 def _need_rows(t, name, shape=None, dtype=None):
     """Row stride of a 2-D CUDA tensor with contiguous rows (any stride between them)."""
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda or t.dim() != 2:
         raise ValueError("%s must be a 2-D CUDA tensor" % name)
     n, h = t.shape
-    if shape is not None and (n, h) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), (n, h)))
-    if h > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return h                                  # also a single row, whose stride says nothing
+    sn, sh = t.stride()
+    if h > 1 and sh != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    stride = t.stride(0) if n > 1 else h          # a single row has no stride of its own
-    if stride < h:
+    if n == 1:
+        return h
+    if sn < h:
         raise ValueError("%s must not have overlapping rows" % name)
-    return stride
+    return sn
 
 
 def _need_norm(x, weight, active_mask):
@@ -701,12 +716,6 @@ def _need_norm(x, weight, active_mask):
     return n, h, stride
 
 
-def _need_stats(n, **stats):
-    for name, t in stats.items():
-        if t is not None:
-            _need(t, torch.float32, name, (n,))
-
-
 def rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd, stream=None):
     """Enqueue the layer norm of x [N, H]; bias, active_mask, mean and rstd may be None.  See
     include/rlk.h."""
@@ -714,7 +723,10 @@ def rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd, stream=
     if bias is not None:
         _need(bias, weight.dtype, "bias", (h,))
     sy = _need_rows(y, "y", (n, h), x.dtype)
-    _need_stats(n, mean=mean, rstd=rstd)
+    if mean is not None:
+        _need(mean, torch.float32, "mean", (n,))
+    if rstd is not None:
+        _need(rstd, torch.float32, "rstd", (n,))
     st = load().rlk_layer_norm_fwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight), _ptr(bias),
                                    _dtype_code(weight, "weight"), _ptr(active_mask), n, h,
                                    float(eps), _ptr(y), sy, _ptr(mean), _ptr(rstd),
@@ -746,7 +758,8 @@ def rlk_rms_norm_fwd(x, weight, active_mask, eps, y, rstd, stream=None):
     """Enqueue the RMS norm of x [N, H]; active_mask and rstd may be None.  See include/rlk.h."""
     n, h, sx = _need_norm(x, weight, active_mask)
     sy = _need_rows(y, "y", (n, h), x.dtype)
-    _need_stats(n, rstd=rstd)
+    if rstd is not None:
+        _need(rstd, torch.float32, "rstd", (n,))
     st = load().rlk_rms_norm_fwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight),
                                  _dtype_code(weight, "weight"), _ptr(active_mask), n, h,
                                  float(eps), _ptr(y), sy, _ptr(rstd), _stream(stream))
@@ -806,7 +819,10 @@ def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, 
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
     _need(tokens, torch.int64, "tokens", (n,))
-    _need_stats(n, logp=logp, kept_logp=kept_logp)
+    if logp is not None:
+        _need(logp, torch.float32, "logp", (n,))
+    if kept_logp is not None:
+        _need(kept_logp, torch.float32, "kept_logp", (n,))
     _need(workspace, torch.uint8, "workspace")
     params = _sample_params(n, temperature, top_k, top_p, min_p)
     st = load().rlk_sample_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,

@@ -735,7 +735,8 @@ rlk_status_t norm_fwd(bool center, const void* x, int32_t x_dtype, int64_t x_str
     a.x = x, a.weight = weight, a.bias = bias, a.mask = mask, a.out = y;
     a.mean_out = mean_out, a.rstd_out = rstd_out;
     a.x_stride = x_stride, a.out_stride = y_stride;
-    a.N = static_cast<int>(N), a.H = static_cast<int>(H), a.eps = static_cast<float>(eps);
+    a.N = static_cast<int>(N), a.H = static_cast<int>(H), a.sms = dev.sms;
+    a.eps = static_cast<float>(eps);
     a.bf16 = x_dtype == RLK_DTYPE_BF16, a.w_bf16 = w_dtype == RLK_DTYPE_BF16;
     a.in_vec = rows_vec(x, x_stride, es);
     a.out_vec = rows_vec(y, y_stride, es);

@@ -14,15 +14,16 @@
 //   dx = rstd ( g - mean_H(g) - xh mean_H(g xh) )     (no mean_H(g) for RMS norm)
 //   dw = sum_t dy xh      db = sum_t dy
 //
-// Both directions are bound by HBM: x in, y out; x and dy in, dx out.  A row
-// stays in the registers of its threads between its two reductions, so it is
-// read once.  Columns are dealt in groups of 8: thread j of the row's THREADS
-// owns groups j, j + THREADS, ...  and folds them in that order, then a fixed
-// shuffle tree and the warps in order.  THREADS and the groups a thread holds
-// follow from H alone, and the way a group is loaded (one or two 16-byte
-// loads, or element by element where rows are not 16-byte aligned or the
-// group crosses H) does not change the order: a row's results do not depend
-// on N, its position, the mask or the alignment.
+// Both directions are bound by HBM: x in, y out; x and dy in, dx out.  A block takes row
+// after row and holds one in registers between its reductions, so each is read once; the
+// next rows are on their way into shared memory meanwhile (cp.async, up to 4 rows ahead).
+// Each thread copies just what it reads itself, so this needs no barrier.
+//
+// Columns are dealt in groups of 8: thread j of the row's `threads` owns groups j and
+// j + threads and folds them in that order, then a fixed shuffle tree and the warps in
+// order.  The number of threads follows from H alone, and the way a group is copied (16
+// bytes at a time, 4 bytes, or element by element, as the rows are aligned) does not change
+// the order: a row's results do not depend on N, its position, the mask or the alignment.
 //
 // dw and db: block b of a fixed number of blocks takes rows b, b + blocks, ...
 // in ascending order, adds them up in registers (each thread its own columns)
@@ -32,6 +33,7 @@
 
 #include <algorithm>
 
+#include "ptx.cuh"
 #include "rlk_internal.h"
 
 namespace rlk {
@@ -165,21 +167,20 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sums of a and b over the row's THREADS threads, in every thread: lanes by a shuffle
-// tree, warps in order.  `slot` alternates between consecutive calls, so one barrier a
-// call suffices.
-template <int THREADS>
+// Sums of a and b over the block's threads, in every thread: lanes by a shuffle tree, warps
+// in order.  `slot` alternates between consecutive calls, so one barrier a call suffices.
 __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*slots)[32], int& slot) {
     a = warp_sum(a);
     b = warp_sum(b);
-    if (THREADS == 32) return make_float2(a, b);
+    if (blockDim.x == 32) return make_float2(a, b);
     float2* s = slots[slot];
     slot ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
     float2 t = s[0];
-#pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w) {
+    const int warps = blockDim.x >> 5;
+#pragma unroll 8
+    for (int w = 1; w < warps; ++w) {
         t.x += s[w].x;
         t.y += s[w].y;
     }
@@ -192,77 +193,178 @@ __host__ __device__ constexpr int64_t part_len(int64_t H, int threads) {
     return (H + threads * kGroup - 1) / (threads * kGroup) * (threads * kGroup);
 }
 
-// Rows a block of the register kernels works on side by side.
-__host__ __device__ constexpr int rows_of(int threads) { return threads == 32 ? 4 : 1; }
+// Copies of a group into shared memory: how the rows are aligned.
+enum : int { kCopy16, kCopy4, kCopyPlain };
 
-template <typename T, bool CENTER, int THREADS, int GROUPS>
-__global__ void __launch_bounds__(THREADS * rows_of(THREADS))
-    norm_fwd_kernel(const T* __restrict__ x, int64_t x_stride, bool x_vec,
-                    const void* __restrict__ weight, const void* __restrict__ bias, bool w_bf16,
-                    bool w_vec, const uint8_t* __restrict__ mask, int N, int H, float inv_h,
-                    float eps, T* __restrict__ y, int64_t y_stride, bool y_vec,
-                    float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes, bool wide) {
+    // the rest of the 16 (4) bytes is filled with zeros
+    if (wide)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                     : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest `left` groups have arrived
+__device__ __forceinline__ void cp_wait(int left) {
+    if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+constexpr int kGroups = 2;       // groups of a thread
+constexpr int kMaxStages = 4;    // rows on their way
+
+// A thread's part of a ring of rows in shared memory: `stages` slots of kGroups groups.
+// 16-byte piece p of slot s lies at (s pieces + p) threads + tid, so the threads of a warp
+// touch neighbouring pieces.
+template <typename T>
+struct Ring {
+    static constexpr int kPieces = kGroups * kGroup * sizeof(T) / 16;
+    uint4* base;
+    __device__ __forceinline__ uint4* piece(int stage, int p) const {
+        return base + (stage * kPieces + p) * blockDim.x + threadIdx.x;
+    }
+    __device__ __forceinline__ void fetch(const T* row, int stage, int H, int mode) const {
+        constexpr int kPerGroup = kPieces / kGroups, kElems = kGroup / kPerGroup;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+            const int c = (threadIdx.x + p / kPerGroup * blockDim.x) * kGroup +
+                          p % kPerGroup * kElems;
+            const int n = min(kElems, max(0, H - c));
+            const T* src = n > 0 ? row + c : row;
+            const uint32_t dst = smem_u32(piece(stage, p));
+            if (mode == kCopy16) {
+                cp_async(dst, src, n * int(sizeof(T)), true);
+            } else if (mode == kCopy4 && sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < kElems; ++e)
+                    cp_async(dst + 4 * e, e < n ? src + e : row, e < n ? 4 : 0, false);
+            } else {
+                T v[kElems];
+#pragma unroll
+                for (int e = 0; e < kElems; ++e) v[e] = e < n ? src[e] : T(0.f);
+                *piece(stage, p) = *reinterpret_cast<const uint4*>(v);
+            }
+        }
+    }
+    __device__ __forceinline__ Raw<T> group(int stage, int i) const;
+};
+template <>
+__device__ __forceinline__ Raw<__nv_bfloat16> Ring<__nv_bfloat16>::group(int stage, int i) const {
+    Raw<__nv_bfloat16> r;
+    r.a = *piece(stage, i);
+    return r;
+}
+template <>
+__device__ __forceinline__ Raw<float> Ring<float>::group(int stage, int i) const {
+    Raw<float> r;
+    r.a = *reinterpret_cast<const float4*>(piece(stage, 2 * i));
+    r.b = *reinterpret_cast<const float4*>(piece(stage, 2 * i + 1));
+    return r;
+}
+
+// What the masks of the next rows say, one load ahead of the copies that need it.
+struct Live {
+    const uint8_t* mask;
+    int64_t step, N;
+    uint32_t bits;               // bit k: the k-th next row is active
+    int next;                    // mask byte of the row after those
+    __device__ __forceinline__ int byte(int64_t row) const {
+        return row >= N ? 0 : mask == nullptr ? 1 : __ldg(mask + row);
+    }
+};
+
+template <typename T, bool CENTER, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
+    norm_fwd_kernel(const NormArgs a, int stages, int x_mode, float inv_h) {
+    extern __shared__ uint4 ring_smem[];
     __shared__ float2 slots[2][32];
     int slot = 0;
-    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = int64_t(blockIdx.x) * rows_of(THREADS) + (THREADS == 32 ? threadIdx.x >> 5 : 0);
-    if (row >= N) return;
-    T* yr = y + row * y_stride;
-    if (mask != nullptr && mask[row] == 0) {
-        const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int c = tid * kGroup; c < H; c += THREADS * kGroup) store_group(yr, c, H, y_vec, z);
+    const int tid = threadIdx.x, H = a.H;
+    const T* x = static_cast<const T*>(a.x);
+    T* y = static_cast<T*>(a.out);
+    const Ring<T> ring{ring_smem};
+    Live live{a.mask, int64_t(gridDim.x), a.N, 0, 0};
+    int64_t row = blockIdx.x;
+    // stages - 1 rows are on their way before the first is waited for
+    for (int k = 0; k < stages - 1; ++k) {
+        const int64_t r = row + k * live.step;
+        if (live.byte(r)) {
+            ring.fetch(x + r * a.x_stride, k, H, x_mode);
+            live.bits |= 1u << k;
+        }
+        cp_commit();
+    }
+    live.next = live.byte(row + (stages - 1) * live.step);
+    float w[kGroups][8], b[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const int c = (tid + i * blockDim.x) * kGroup;
+        param_group(a.weight, a.w_bf16, a.w_vec, c, H, w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[i][e] = 0.f;
+        if (a.bias != nullptr) param_group(a.bias, a.w_bf16, a.w_vec, c, H, b[i]);
+    }
+    int stage = 0;
+    for (; row < a.N; row += live.step) {
+        const int64_t ahead = row + (stages - 1) * live.step;
+        if (live.next) {
+            ring.fetch(x + ahead * a.x_stride, stage == 0 ? stages - 1 : stage - 1, H, x_mode);
+            live.bits |= 1u << (stages - 1);
+        }
+        cp_commit();
+        live.next = live.byte(ahead + live.step);
+        const bool on = live.bits & 1u;
+        live.bits >>= 1;
+        const int at = stage;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        T* yr = y + row * a.out_stride;
+        if (!on) {
+            const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int c = tid * kGroup; c < H; c += blockDim.x * kGroup)
+                store_group(yr, c, H, a.out_vec, z);
+            if (tid == 0) {
+                if (a.mean_out != nullptr) a.mean_out[row] = 0.f;
+                if (a.rstd_out != nullptr) a.rstd_out[row] = 0.f;
+            }
+            continue;
+        }
+        cp_wait(stages - 1);
+        float f[kGroups][8];
+        float mean = 0.f, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            ring.group(at, i).unpack(f[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += f[i][e];      // columns past H hold 0
+        }
+        if (CENTER) mean = row_sum(s, 0.f, slots, slot).x * inv_h;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int n = valid_cols((tid + i * blockDim.x) * kGroup, H);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[i][e] -= mean;
+                if (!CENTER || e < n) q = fmaf(f[i][e], f[i][e], q);
+            }
+        }
+        const float var = row_sum(q, 0.f, slots, slot).x * inv_h;
+        const float rstd = 1.f / sqrtf(var + a.eps);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int c = (tid + i * blockDim.x) * kGroup;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[i][e] = fmaf(f[i][e] * rstd, w[i][e], b[i][e]);
+            if (c < H) store_group(yr, c, H, a.out_vec, f[i]);
+        }
         if (tid == 0) {
-            if (mean_out != nullptr) mean_out[row] = 0.f;
-            if (rstd_out != nullptr) rstd_out[row] = 0.f;
+            if (a.mean_out != nullptr) a.mean_out[row] = mean;
+            if (a.rstd_out != nullptr) a.rstd_out[row] = rstd;
         }
-        return;
-    }
-    const T* xr = x + row * x_stride;
-    Raw<T> raw[GROUPS];
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i)
-        load_group(raw[i], xr, (tid + i * THREADS) * kGroup, H, x_vec);
-    float mean = 0.f;
-    if (CENTER) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            float f[8];
-            raw[i].unpack(f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s += f[e];     // columns past H hold 0
-        }
-        mean = row_sum<THREADS>(s, 0.f, slots, slot).x * inv_h;
-    }
-    float q = 0.f;
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        float f[8];
-        raw[i].unpack(f);
-        const int n = valid_cols((tid + i * THREADS) * kGroup, H);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = f[e] - mean;
-            if (e < n) q = fmaf(d, d, q);
-        }
-    }
-    const float var = row_sum<THREADS>(q, 0.f, slots, slot).x * inv_h;
-    const float rstd = 1.f / sqrtf(var + eps);
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        const int c = (tid + i * THREADS) * kGroup;
-        if (c >= H) break;
-        float f[8], w[8], b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        raw[i].unpack(f);
-        param_group(weight, w_bf16, w_vec, c, H, w);
-        if (bias != nullptr) param_group(bias, w_bf16, w_vec, c, H, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf((f[e] - mean) * rstd, w[e], b[e]);
-        store_group(yr, c, H, y_vec, f);
-    }
-    if (tid == 0) {
-        if (mean_out != nullptr) mean_out[row] = mean;
-        if (rstd_out != nullptr) rstd_out[row] = rstd;
     }
 }
 
@@ -294,7 +396,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += f[e];
             }
-            mean = row_sum<1024>(s, 0.f, slots, slot).x * inv_h;
+            mean = row_sum(s, 0.f, slots, slot).x * inv_h;
         }
         float q = 0.f;
         for (int c = c0; c < H; c += kStep) {
@@ -308,7 +410,7 @@ __global__ void __launch_bounds__(1024)
                 if (e < n) q = fmaf(d, d, q);
             }
         }
-        const float var = row_sum<1024>(q, 0.f, slots, slot).x * inv_h;
+        const float var = row_sum(q, 0.f, slots, slot).x * inv_h;
         rstd = 1.f / sqrtf(var + eps);
     }
     for (int c = c0; c < H; c += kStep) {
@@ -331,107 +433,98 @@ __global__ void __launch_bounds__(1024)
 
 // ----------------------------------------------------------------------------- backward
 
-template <typename T, bool CENTER, int THREADS, int GROUPS>
-__global__ void __launch_bounds__(THREADS * rows_of(THREADS))
-    norm_bwd_kernel(const T* __restrict__ x, int64_t x_stride, const T* __restrict__ dy,
-                    int64_t dy_stride, bool in_vec, const void* __restrict__ weight, bool w_bf16,
-                    bool w_vec, const float* __restrict__ mean_in,
-                    const float* __restrict__ rstd_in, const uint8_t* __restrict__ mask, int N,
-                    int H, float inv_h, T* __restrict__ dx, int64_t dx_stride, bool dx_vec,
+template <typename T, bool CENTER, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1)
+    norm_bwd_kernel(const NormArgs a, int stages, int x_mode, int dy_mode, float inv_h,
                     float* __restrict__ dw_part, float* __restrict__ db_part) {
+    extern __shared__ uint4 ring_smem[];
     __shared__ float2 slots[2][32];
     int slot = 0;
-    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int sub = THREADS == 32 ? threadIdx.x >> 5 : 0;
-    float dw[GROUPS * 8], db[CENTER ? GROUPS * 8 : 1];
-#pragma unroll
-    for (int i = 0; i < GROUPS * 8; ++i) {
-        dw[i] = 0.f;
-        if (CENTER) db[i] = 0.f;
+    const int tid = threadIdx.x, H = a.H;
+    const T* x = static_cast<const T*>(a.x);
+    const T* dy = static_cast<const T*>(a.dy);
+    T* dx = static_cast<T*>(a.out);
+    const Ring<T> rx{ring_smem}, rg{ring_smem + stages * Ring<T>::kPieces * blockDim.x};
+    Live live{a.mask, int64_t(gridDim.x), a.N, 0, 0};
+    int64_t row = blockIdx.x;
+    for (int k = 0; k < stages - 1; ++k) {
+        const int64_t r = row + k * live.step;
+        if (live.byte(r)) {
+            rx.fetch(x + r * a.x_stride, k, H, x_mode);
+            rg.fetch(dy + r * a.dy_stride, k, H, dy_mode);
+            live.bits |= 1u << k;
+        }
+        cp_commit();
     }
-    const int64_t step = int64_t(gridDim.x) * rows_of(THREADS);
-    for (int64_t row = int64_t(blockIdx.x) * rows_of(THREADS) + sub; row < N; row += step) {
-        T* dxr = dx + row * dx_stride;
-        if (mask != nullptr && mask[row] == 0) {
+    live.next = live.byte(row + (stages - 1) * live.step);
+    float w[kGroups][8], dw[kGroups][8], db[kGroups][8];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        param_group(a.weight, a.w_bf16, a.w_vec, (tid + i * blockDim.x) * kGroup, H, w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
+    }
+    int stage = 0;
+    for (; row < a.N; row += live.step) {
+        const int64_t ahead = row + (stages - 1) * live.step;
+        if (live.next) {
+            const int to = stage == 0 ? stages - 1 : stage - 1;
+            rx.fetch(x + ahead * a.x_stride, to, H, x_mode);
+            rg.fetch(dy + ahead * a.dy_stride, to, H, dy_mode);
+            live.bits |= 1u << (stages - 1);
+        }
+        cp_commit();
+        live.next = live.byte(ahead + live.step);
+        const bool on = live.bits & 1u;
+        live.bits >>= 1;
+        const int at = stage;
+        stage = stage + 1 == stages ? 0 : stage + 1;
+        T* dxr = dx + row * a.out_stride;
+        if (!on) {
             const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int c = tid * kGroup; c < H; c += THREADS * kGroup)
-                store_group(dxr, c, H, dx_vec, z);
+            for (int c = tid * kGroup; c < H; c += blockDim.x * kGroup)
+                store_group(dxr, c, H, a.out_vec, z);
             continue;
         }
-        Raw<T> rx[GROUPS], rg[GROUPS];
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            const int c = (tid + i * THREADS) * kGroup;
-            load_group(rx[i], x + row * x_stride, c, H, in_vec);
-            load_group(rg[i], dy + row * dy_stride, c, H, in_vec);
-        }
-        const float rstd = rstd_in[row];
-        const float mean = CENTER ? mean_in[row] : 0.f;
+        const float rstd = a.rstd[row];
+        const float mean = CENTER ? a.mean[row] : 0.f;
+        cp_wait(stages - 1);
+        float xh[kGroups][8], g[kGroups][8];
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            const int c = (tid + i * THREADS) * kGroup;
-            if (c >= H) break;
-            float xf[8], gf[8], w[8];
-            rx[i].unpack(xf);
-            rg[i].unpack(gf);          // dy past H is 0, so these columns add nothing
-            param_group(weight, w_bf16, w_vec, c, H, w);
+        for (int i = 0; i < kGroups; ++i) {
+            rx.group(at, i).unpack(xh[i]);
+            rg.group(at, i).unpack(g[i]);       // dy past H is 0: these columns add nothing
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = (xf[e] - mean) * rstd;
-                const float g = gf[e] * w[e];
-                if (CENTER) s1 += g;
-                s2 = fmaf(g, xh, s2);
-                dw[i * 8 + e] = fmaf(gf[e], xh, dw[i * 8 + e]);
-                if (CENTER) db[i * 8 + e] += gf[e];
+                xh[i][e] = (xh[i][e] - mean) * rstd;
+                dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
+                if (CENTER) db[i][e] += g[i][e];
+                g[i][e] *= w[i][e];
+                if (CENTER) s1 += g[i][e];
+                s2 = fmaf(g[i][e], xh[i][e], s2);
             }
         }
-        const float2 t = row_sum<THREADS>(s1, s2, slots, slot);
+        const float2 t = row_sum(s1, s2, slots, slot);
         const float m1 = t.x * inv_h, m2 = t.y * inv_h;
 #pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            const int c = (tid + i * THREADS) * kGroup;
-            if (c >= H) break;
-            float xf[8], gf[8], w[8];
-            rx[i].unpack(xf);
-            rg[i].unpack(gf);
-            param_group(weight, w_bf16, w_vec, c, H, w);
+        for (int i = 0; i < kGroups; ++i) {
+            const int c = (tid + i * blockDim.x) * kGroup;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = (xf[e] - mean) * rstd;
-                float d = fmaf(gf[e], w[e], CENTER ? -m1 : 0.f);
-                xf[e] = fmaf(-xh, m2, d) * rstd;
+                const float d = CENTER ? g[i][e] - m1 : g[i][e];
+                g[i][e] = fmaf(-xh[i][e], m2, d) * rstd;
             }
-            store_group(dxr, c, H, dx_vec, xf);
+            if (c < H) store_group(dxr, c, H, a.out_vec, g[i]);
         }
     }
-    if (dw_part == nullptr && db_part == nullptr) return;
     // the block's partial row, in the order of part_len: neighbouring threads write
-    // neighbouring floats.  Rows worked on side by side are added in order first.
-    const int64_t at = int64_t(blockIdx.x) * (THREADS * GROUPS * 8);
-    if (THREADS != 32) {
+    // neighbouring floats
+    const int64_t out = int64_t(blockIdx.x) * (blockDim.x * kGroups * 8) + tid;
 #pragma unroll
-        for (int i = 0; i < GROUPS * 8; ++i) {
-            if (dw_part != nullptr) dw_part[at + i * THREADS + tid] = dw[i];
-            if (CENTER && db_part != nullptr) db_part[at + i * THREADS + tid] = db[i];
-        }
-    } else {
-        __shared__ float acc[2][THREADS == 32 ? 32 * GROUPS * 8 : 1];
-        for (int r = 0; r < rows_of(THREADS); ++r) {
-            if (sub == r) {
-#pragma unroll
-                for (int i = 0; i < GROUPS * 8; ++i) {
-                    const int k = i * 32 + tid;
-                    acc[0][k] = r == 0 ? dw[i] : acc[0][k] + dw[i];
-                    if (CENTER) acc[1][k] = r == 0 ? db[i] : acc[1][k] + db[i];
-                }
-            }
-            __syncthreads();
-        }
-        for (int k = threadIdx.x; k < 32 * GROUPS * 8; k += blockDim.x) {
-            if (dw_part != nullptr) dw_part[at + k] = acc[0][k];
-            if (CENTER && db_part != nullptr) db_part[at + k] = acc[1][k];
-        }
+    for (int i = 0; i < kGroups * 8; ++i) {
+        if (dw_part != nullptr) dw_part[out + i * blockDim.x] = dw[i / 8][i % 8];
+        if (CENTER && db_part != nullptr) db_part[out + i * blockDim.x] = db[i / 8][i % 8];
     }
 }
 
@@ -487,7 +580,7 @@ __global__ void __launch_bounds__(1024)
                 if (CENTER && db_part != nullptr) db_part[k] += gf[e];
             }
         }
-        const float2 t = row_sum<1024>(s1, s2, slots, slot);
+        const float2 t = row_sum(s1, s2, slots, slot);
         const float m1 = t.x * inv_h, m2 = t.y * inv_h;
         for (int c = c0; c < H; c += kStep) {
             float xf[8], gf[8], w[8];
@@ -522,8 +615,18 @@ __global__ void __launch_bounds__(512)
     const int r = pos / threads;                     // the place's column: see part_len
     const int64_t c = (int64_t(r >> 3) * threads + pos % threads) * kGroup + (r & 7);
     float a = 0.f;
-    if (c < H)
-        for (int p = q; p < P; p += 16) a += part[int64_t(p) * len + pos];
+    if (c < H) {
+        // four loads at a time, added in ascending order
+        int p = q;
+        for (; p + 48 < P; p += 64) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = part[int64_t(p + 16 * k) * len + pos];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a += v[k];
+        }
+        for (; p < P; p += 16) a += part[int64_t(p) * len + pos];
+    }
     s[q][x] = a;
     __syncthreads();
     if (q != 0 || c >= H) return;
@@ -535,86 +638,117 @@ __global__ void __launch_bounds__(512)
         static_cast<float*>(out)[c] = a;
 }
 
-// The widest row that stays in registers (512 threads of 4 groups).
-constexpr int kMaxRegH = 512 * 4 * kGroup;
+// The widest row that stays in registers.
+constexpr int kMaxRegH = 1024 * kGroups * kGroup;
 
-struct BwdPlan {
-    int threads, groups, blocks;   // groups: 0 for the wide kernel
-    int64_t len;                   // floats of a partial row
+// The threads of a row follow from H alone.
+struct Plan {
+    int threads;                   // 0: the wide kernels
+    int stages;
+    size_t smem;
 };
-
-// Fixed by H and N alone.  The number of blocks fills the GPU with what the registers
-// allow (two accumulators a column) and keeps the partial rows small.
-BwdPlan bwd_plan(int64_t N, int64_t H) {
-    BwdPlan p;
-    if (H <= 1024) p = {32, H <= 256 ? 1 : H <= 512 ? 2 : 4, 608, 0};
-    else if (H <= 4096) p = {128, H <= 2048 ? 2 : 4, 608, 0};
-    else if (H <= 8192) p = {256, 4, 304, 0};
-    else if (H <= kMaxRegH) p = {512, 4, 152, 0};
-    else p = {1024, 0, 152, 0};
-    const int rows = rows_of(p.threads);
-    p.blocks = static_cast<int>(std::min<int64_t>((N + rows - 1) / rows, p.blocks));
-    p.len = p.groups > 0 ? int64_t(p.threads) * p.groups * kGroup : part_len(H, p.threads);
+// tensors: rings that a block holds; blocks: on an SM
+Plan make_plan(int64_t H, size_t esize, int tensors, int blocks) {
+    if (H > kMaxRegH) return {0, 0, 0};
+    Plan p;
+    const int64_t half = (H + kGroups * kGroup - 1) / (kGroups * kGroup);
+    p.threads = static_cast<int>((half + 31) / 32 * 32);
+    const size_t row = size_t(p.threads) * kGroups * kGroup * esize * tensors;
+    const size_t room = size_t(208) * 1024 / blocks;
+    p.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(1, room / row)));
+    p.smem = row * p.stages;
     return p;
+}
+// Blocks on an SM: the forward holds 64 registers a thread, the backward up to 128.
+int fwd_blocks_per_sm(int threads) { return std::max(1, std::min(16, 1024 / std::max(threads, 32))); }
+int bwd_blocks_per_sm(int threads) { return std::max(1, std::min(16, 512 / std::max(threads, 32))); }
+
+int threads_of(int64_t H) { return make_plan(H, 4, 1, 1).threads; }
+
+// Blocks (= partial rows) of the backward and floats of a partial row: fixed by H and N.
+struct Parts {
+    int threads, blocks;
+    int64_t len;
+};
+Parts bwd_parts(int64_t N, int64_t H) {
+    const int t = threads_of(H);
+    const int64_t most = 152 * (t == 0 ? 1 : bwd_blocks_per_sm(t));
+    return {t == 0 ? 1024 : t, static_cast<int>(std::min<int64_t>(N, most)),
+            part_len(H, t == 0 ? 1024 : t * kGroups)};
+}
+
+int copy_mode(const void* p, int64_t stride, size_t esize) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    if (a % 16 == 0 && size_t(stride) * esize % 16 == 0) return kCopy16;
+    return esize == 4 ? kCopy4 : kCopyPlain;
+}
+
+// a block's shared memory beyond 48 KB is asked for
+template <typename F>
+cudaError_t allow_smem(F kernel, size_t smem) {
+    if (smem <= 47 * 1024) return cudaSuccess;      // with the static part below 48 KB
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem));
+}
+
+template <typename T, bool CENTER, int MAXT>
+cudaError_t run_fwd(const NormArgs& a, const Plan& p, cudaStream_t stream) {
+    auto kernel = norm_fwd_kernel<T, CENTER, MAXT>;
+    const cudaError_t e = allow_smem(kernel, p.smem);
+    if (e != cudaSuccess) return e;
+    const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(p.threads));
+    kernel<<<blocks, p.threads, p.smem, stream>>>(a, p.stages, copy_mode(a.x, a.x_stride, sizeof(T)),
+                                                  1.f / static_cast<float>(a.H));
+    return cudaGetLastError();
 }
 
 template <typename T, bool CENTER>
 cudaError_t fwd_dispatch(const NormArgs& a, cudaStream_t stream) {
-    const float inv_h = 1.f / static_cast<float>(a.H);
-    const T* x = static_cast<const T*>(a.x);
-    T* y = static_cast<T*>(a.out);
-#define RLK_NORM_FWD(TH, G)                                                                       \
-    norm_fwd_kernel<T, CENTER, TH, G>                                                             \
-        <<<(a.N + rows_of(TH) - 1) / rows_of(TH), TH * rows_of(TH), 0, stream>>>(                 \
-            x, a.x_stride, a.in_vec, a.weight, a.bias, a.w_bf16, a.w_vec, a.mask, a.N, a.H,       \
-            inv_h, a.eps, y, a.out_stride, a.out_vec, a.mean_out, a.rstd_out)
-    if (a.H <= 256) RLK_NORM_FWD(32, 1);
-    else if (a.H <= 512) RLK_NORM_FWD(32, 2);
-    else if (a.H <= 1024) RLK_NORM_FWD(32, 4);
-    else if (a.H <= 2048) RLK_NORM_FWD(128, 2);
-    else if (a.H <= 4096) RLK_NORM_FWD(128, 4);
-    else if (a.H <= 8192) RLK_NORM_FWD(256, 4);
-    else if (a.H <= kMaxRegH) RLK_NORM_FWD(512, 4);
-    else
+    const int t = threads_of(a.H);
+    if (t == 0) {
         norm_fwd_wide_kernel<T, CENTER><<<a.N, 1024, 0, stream>>>(
-            x, a.x_stride, a.in_vec, a.weight, a.bias, a.w_bf16, a.w_vec, a.mask, a.N, a.H, inv_h,
-            a.eps, y, a.out_stride, a.out_vec, a.mean_out, a.rstd_out);
-#undef RLK_NORM_FWD
+            static_cast<const T*>(a.x), a.x_stride, a.in_vec, a.weight, a.bias, a.w_bf16, a.w_vec,
+            a.mask, a.N, a.H, 1.f / static_cast<float>(a.H), a.eps, static_cast<T*>(a.out),
+            a.out_stride, a.out_vec, a.mean_out, a.rstd_out);
+        return cudaGetLastError();
+    }
+    const Plan p = make_plan(a.H, sizeof(T), 1, fwd_blocks_per_sm(t));
+    return t <= 512 ? run_fwd<T, CENTER, 512>(a, p, stream) : run_fwd<T, CENTER, 1024>(a, p, stream);
+}
+
+template <typename T, bool CENTER, int MAXT>
+cudaError_t run_bwd(const NormArgs& a, const Plan& p, int blocks, float* dwp, float* dbp,
+                    cudaStream_t stream) {
+    auto kernel = norm_bwd_kernel<T, CENTER, MAXT>;
+    const cudaError_t e = allow_smem(kernel, p.smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, p.threads, p.smem, stream>>>(a, p.stages, copy_mode(a.x, a.x_stride, sizeof(T)),
+                                                  copy_mode(a.dy, a.dy_stride, sizeof(T)),
+                                                  1.f / static_cast<float>(a.H), dwp, dbp);
     return cudaGetLastError();
 }
 
 template <typename T, bool CENTER>
-cudaError_t bwd_dispatch(const NormArgs& a, const BwdPlan& p, float* dwp, float* dbp,
+cudaError_t bwd_dispatch(const NormArgs& a, int blocks, float* dwp, float* dbp,
                          cudaStream_t stream) {
-    const float inv_h = 1.f / static_cast<float>(a.H);
-    const T* x = static_cast<const T*>(a.x);
-    const T* dy = static_cast<const T*>(a.dy);
-    T* dx = static_cast<T*>(a.out);
-#define RLK_NORM_BWD(TH, G)                                                                       \
-    norm_bwd_kernel<T, CENTER, TH, G><<<p.blocks, TH * rows_of(TH), 0, stream>>>(                 \
-        x, a.x_stride, dy, a.dy_stride, a.in_vec, a.weight, a.w_bf16, a.w_vec, a.mean, a.rstd,    \
-        a.mask, a.N, a.H, inv_h, dx, a.out_stride, a.out_vec, dwp, dbp)
-    switch (p.threads * 8 + p.groups) {
-        case 32 * 8 + 1: RLK_NORM_BWD(32, 1); break;
-        case 32 * 8 + 2: RLK_NORM_BWD(32, 2); break;
-        case 32 * 8 + 4: RLK_NORM_BWD(32, 4); break;
-        case 128 * 8 + 2: RLK_NORM_BWD(128, 2); break;
-        case 128 * 8 + 4: RLK_NORM_BWD(128, 4); break;
-        case 256 * 8 + 4: RLK_NORM_BWD(256, 4); break;
-        case 512 * 8 + 4: RLK_NORM_BWD(512, 4); break;
-        default:
-            norm_bwd_wide_kernel<T, CENTER><<<p.blocks, 1024, 0, stream>>>(
-                x, a.x_stride, dy, a.dy_stride, a.in_vec, a.weight, a.w_bf16, a.w_vec, a.mean,
-                a.rstd, a.mask, a.N, a.H, inv_h, dx, a.out_stride, a.out_vec, dwp, dbp);
+    const int t = threads_of(a.H);
+    if (t == 0) {
+        norm_bwd_wide_kernel<T, CENTER><<<blocks, 1024, 0, stream>>>(
+            static_cast<const T*>(a.x), a.x_stride, static_cast<const T*>(a.dy), a.dy_stride,
+            a.in_vec, a.weight, a.w_bf16, a.w_vec, a.mean, a.rstd, a.mask, a.N, a.H,
+            1.f / static_cast<float>(a.H), static_cast<T*>(a.out), a.out_stride, a.out_vec, dwp,
+            dbp);
+        return cudaGetLastError();
     }
-#undef RLK_NORM_BWD
-    return cudaGetLastError();
+    const Plan p = make_plan(a.H, sizeof(T), 2, bwd_blocks_per_sm(t));
+    return t <= 512 ? run_bwd<T, CENTER, 512>(a, p, blocks, dwp, dbp, stream)
+                    : run_bwd<T, CENTER, 1024>(a, p, blocks, dwp, dbp, stream);
 }
 
 }  // namespace
 
 size_t norm_bwd_workspace(int64_t N, int64_t H, bool center) {
-    const BwdPlan p = bwd_plan(N, H);
+    const Parts p = bwd_parts(N, H);
     return align_up(size_t(p.blocks) * p.len * sizeof(float), 256) * (center ? 2 : 1) + 256;
 }
 
@@ -626,7 +760,7 @@ cudaError_t launch_norm_fwd(const NormArgs& a, bool center, cudaStream_t stream)
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, bool center, cudaStream_t stream) {
-    const BwdPlan p = bwd_plan(a.N, a.H);
+    const Parts p = bwd_parts(a.N, a.H);
     const size_t plane = align_up(size_t(p.blocks) * p.len * sizeof(float), 256);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     float* dwp = a.dweight != nullptr ? reinterpret_cast<float*>(ws) : nullptr;
@@ -634,11 +768,11 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool center, cudaStream_t stream)
     if (a.N > 0) {
         cudaError_t e;
         if (a.bf16)
-            e = center ? bwd_dispatch<__nv_bfloat16, true>(a, p, dwp, dbp, stream)
-                       : bwd_dispatch<__nv_bfloat16, false>(a, p, dwp, dbp, stream);
+            e = center ? bwd_dispatch<__nv_bfloat16, true>(a, p.blocks, dwp, dbp, stream)
+                       : bwd_dispatch<__nv_bfloat16, false>(a, p.blocks, dwp, dbp, stream);
         else
-            e = center ? bwd_dispatch<float, true>(a, p, dwp, dbp, stream)
-                       : bwd_dispatch<float, false>(a, p, dwp, dbp, stream);
+            e = center ? bwd_dispatch<float, true>(a, p.blocks, dwp, dbp, stream)
+                       : bwd_dispatch<float, false>(a, p.blocks, dwp, dbp, stream);
         if (e != cudaSuccess) return e;
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;

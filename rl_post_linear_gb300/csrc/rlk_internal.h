@@ -293,7 +293,7 @@ struct NormArgs {
     void* dbias;
     void* workspace;           // backward only
     int64_t x_stride, dy_stride, out_stride;
-    int N, H;
+    int N, H, sms;
     float eps;
     bool bf16, w_bf16, in_vec, w_vec, out_vec;
 };

@@ -77,11 +77,12 @@ def test_backward_only_layer_norm(lib):
 
 
 def test_workspace_queries(lib):
-    # two fp32 planes of at most 608 partial rows, a row padded to whole 8-column groups of
-    # its threads
-    assert rlk.rlk_layer_norm_bwd_workspace_bytes(8192, 4096) == 2 * 608 * 4096 * 4 + 256
-    assert rlk.rlk_rms_norm_bwd_workspace_bytes(8192, 4096) == 608 * 4096 * 4 + 256
+    # fp32 planes (two for layer norm) of at most 304 partial rows at this width, a row padded
+    # to the 16 columns of each of its threads
+    assert rlk.rlk_layer_norm_bwd_workspace_bytes(8192, 4096) == 2 * 304 * 4096 * 4 + 256
+    assert rlk.rlk_rms_norm_bwd_workspace_bytes(8192, 4096) == 304 * 4096 * 4 + 256
     assert rlk.rlk_rms_norm_bwd_workspace_bytes(3, 4096) == 3 * 4096 * 4 + 256
+    assert rlk.rlk_rms_norm_bwd_workspace_bytes(2, 4097) >= 2 * 4097 * 4
     assert rlk.rlk_layer_norm_bwd_workspace_bytes(-1, 8) == 0
     assert rlk.rlk_layer_norm_bwd_workspace_bytes(8, 0) == 0
     assert rlk.rlk_sample_logits_workspace_bytes(-1, 8) == 0
