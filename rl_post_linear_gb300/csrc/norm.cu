@@ -49,6 +49,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two columns at a time: sm_100's paired fp32 instructions, each half rounded as the single
+// instruction rounds.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // One group of 8 columns as it lies in memory.
 template <typename T>
 struct Raw;
@@ -66,6 +70,10 @@ struct Raw<__nv_bfloat16> {
         for (int e = 0; e < 8; ++e)
             if (e < n) w[e / 2] |= uint32_t(__ldcs(q + e)) << (16 * (e & 1));
         a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
+        f[0] = make_float2(bf_lo(a.x), bf_hi(a.x)), f[1] = make_float2(bf_lo(a.y), bf_hi(a.y));
+        f[2] = make_float2(bf_lo(a.z), bf_hi(a.z)), f[3] = make_float2(bf_lo(a.w), bf_hi(a.w));
     }
     __device__ __forceinline__ void unpack(float (&f)[8]) const {
         f[0] = bf_lo(a.x), f[1] = bf_hi(a.x), f[2] = bf_lo(a.y), f[3] = bf_hi(a.y);
@@ -86,6 +94,10 @@ struct Raw<float> {
         for (int e = 0; e < 8; ++e) w[e] = e < n ? __ldcs(p + e) : 0.f;
         a = make_float4(w[0], w[1], w[2], w[3]);
         b = make_float4(w[4], w[5], w[6], w[7]);
+    }
+    __device__ __forceinline__ void unpack(float2 (&f)[4]) const {
+        f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w);
+        f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
     }
     __device__ __forceinline__ void unpack(float (&f)[8]) const {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
@@ -133,6 +145,18 @@ __device__ __forceinline__ void store_group(float* row, int c, int H, bool vec,
         if (e < n) row[c + e] = f[e];
 }
 
+template <typename T>
+__device__ __forceinline__ void store_group(T* row, int c, int H, bool vec, const float2 (&f)[4]) {
+    const float v[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    store_group(row, c, H, vec, v);
+}
+template <typename T>
+__device__ __forceinline__ void zero_row(T* row, int H, bool vec) {
+    const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int c = threadIdx.x * kGroup; c < H; c += blockDim.x * kGroup)
+        store_group(row, c, H, vec, z);
+}
+
 // weight / bias group: read by every row, so kept in L1 (default caching)
 __device__ __forceinline__ void param_group(const void* p, bool bf16, bool vec, int c, int H,
                                             float (&f)[8]) {
@@ -167,24 +191,39 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sums of a and b over the block's threads, in every thread: lanes by a shuffle tree, warps
-// in order.  `slot` alternates between consecutive calls, so one barrier a call suffices.
+// Sums over the block's threads, in every thread: lanes by a shuffle tree, then the warps by
+// another one.  `slot` alternates between consecutive calls, so one barrier a call suffices.
+template <int MAXT>
+__device__ __forceinline__ float row_sum(float a, float2 (*slots)[32], int& slot) {
+    a = warp_sum(a);
+    if (blockDim.x == 32) return a;
+    float2* s = slots[slot];
+    slot ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s[threadIdx.x >> 5].x = a;
+    __syncthreads();
+    a = lane < (blockDim.x >> 5) ? s[lane].x : 0.f;
+#pragma unroll
+    for (int off = MAXT / 64; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    return __shfl_sync(0xffffffffu, a, 0);
+}
+template <int MAXT>
 __device__ __forceinline__ float2 row_sum(float a, float b, float2 (*slots)[32], int& slot) {
     a = warp_sum(a);
     b = warp_sum(b);
     if (blockDim.x == 32) return make_float2(a, b);
     float2* s = slots[slot];
     slot ^= 1;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    float2 t = s[0];
-    const int warps = blockDim.x >> 5;
-#pragma unroll 8
-    for (int w = 1; w < warps; ++w) {
-        t.x += s[w].x;
-        t.y += s[w].y;
+    float2 t = lane < (blockDim.x >> 5) ? s[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int off = MAXT / 64; off > 0; off >>= 1) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, off);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, off);
     }
-    return t;
+    return make_float2(__shfl_sync(0xffffffffu, t.x, 0), __shfl_sync(0xffffffffu, t.y, 0));
 }
 
 // A partial row of dw or db holds element e of the i-th group of thread t at place
@@ -227,8 +266,19 @@ struct Ring {
     __device__ __forceinline__ uint4* piece(int stage, int p) const {
         return base + (stage * kPieces + p) * blockDim.x + threadIdx.x;
     }
-    __device__ __forceinline__ void fetch(const T* row, int stage, int H, int mode) const {
+    // full: 16 bytes at a time, and every column of every group is there
+    __device__ __forceinline__ void fetch(const T* row, int stage, int H, int mode,
+                                          bool full) const {
         constexpr int kPerGroup = kPieces / kGroups, kElems = kGroup / kPerGroup;
+        if (full) {
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+                cp_async(smem_u32(piece(stage, p)),
+                         row + (threadIdx.x + p / kPerGroup * blockDim.x) * kGroup +
+                             p % kPerGroup * kElems,
+                         16, true);
+            return;
+        }
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int c = (threadIdx.x + p / kPerGroup * blockDim.x) * kGroup +
@@ -277,13 +327,16 @@ struct Live {
     }
 };
 
-template <typename T, bool CENTER, int MAXT>
+// FULL: H is 16 columns for each thread and every row starts on 16 bytes, so no column needs
+// a test (a third of the instructions of a row; the arithmetic is the same).
+template <typename T, bool CENTER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     norm_fwd_kernel(const NormArgs a, int stages, int x_mode, float inv_h) {
     extern __shared__ uint4 ring_smem[];
     __shared__ float2 slots[2][32];
     int slot = 0;
     const int tid = threadIdx.x, H = a.H;
+    const bool out_vec = FULL || a.out_vec;
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.out);
     const Ring<T> ring{ring_smem};
@@ -293,26 +346,32 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     for (int k = 0; k < stages - 1; ++k) {
         const int64_t r = row + k * live.step;
         if (live.byte(r)) {
-            ring.fetch(x + r * a.x_stride, k, H, x_mode);
+            ring.fetch(x + r * a.x_stride, k, H, x_mode, FULL);
             live.bits |= 1u << k;
         }
         cp_commit();
     }
     live.next = live.byte(row + (stages - 1) * live.step);
-    float w[kGroups][8], b[kGroups][8];
+    float2 w[kGroups][4], b[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         const int c = (tid + i * blockDim.x) * kGroup;
-        param_group(a.weight, a.w_bf16, a.w_vec, c, H, w[i]);
+        float v[8];
+        param_group(a.weight, a.w_bf16, a.w_vec, c, H, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[i][e] = 0.f;
-        if (a.bias != nullptr) param_group(a.bias, a.w_bf16, a.w_vec, c, H, b[i]);
+        for (int e = 0; e < 4; ++e) w[i][e] = make_float2(v[2 * e], v[2 * e + 1]), b[i][e] = both(0.f);
+        if (a.bias != nullptr) {
+            param_group(a.bias, a.w_bf16, a.w_vec, c, H, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
+        }
     }
     int stage = 0;
     for (; row < a.N; row += live.step) {
         const int64_t ahead = row + (stages - 1) * live.step;
         if (live.next) {
-            ring.fetch(x + ahead * a.x_stride, stage == 0 ? stages - 1 : stage - 1, H, x_mode);
+            ring.fetch(x + ahead * a.x_stride, stage == 0 ? stages - 1 : stage - 1, H, x_mode,
+                       FULL);
             live.bits |= 1u << (stages - 1);
         }
         cp_commit();
@@ -323,9 +382,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
         stage = stage + 1 == stages ? 0 : stage + 1;
         T* yr = y + row * a.out_stride;
         if (!on) {
-            const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int c = tid * kGroup; c < H; c += blockDim.x * kGroup)
-                store_group(yr, c, H, a.out_vec, z);
+            zero_row(yr, H, out_vec);
             if (tid == 0) {
                 if (a.mean_out != nullptr) a.mean_out[row] = 0.f;
                 if (a.rstd_out != nullptr) a.rstd_out[row] = 0.f;
@@ -333,33 +390,39 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
             continue;
         }
         cp_wait(stages - 1);
-        float f[kGroups][8];
-        float mean = 0.f, s = 0.f;
+        float2 f[kGroups][4], s = both(0.f);
+        float mean = 0.f;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             ring.group(at, i).unpack(f[i]);
+            if (CENTER)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += f[i][e];      // columns past H hold 0
+                for (int e = 0; e < 4; ++e) s = __fadd2_rn(s, f[i][e]);   // columns past H hold 0
         }
-        if (CENTER) mean = row_sum(s, 0.f, slots, slot).x * inv_h;
-        float q = 0.f;
+        if (CENTER) mean = row_sum<MAXT>(s.x + s.y, slots, slot) * inv_h;
+        float2 q = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int n = valid_cols((tid + i * blockDim.x) * kGroup, H);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                f[i][e] -= mean;
-                if (!CENTER || e < n) q = fmaf(f[i][e], f[i][e], q);
+            for (int e = 0; e < 4; ++e) {
+                if (CENTER) {
+                    f[i][e] = __fadd2_rn(f[i][e], both(-mean));
+                    if (!FULL && 2 * e >= n) f[i][e].x = 0.f;
+                    if (!FULL && 2 * e + 1 >= n) f[i][e].y = 0.f;
+                }
+                q = __ffma2_rn(f[i][e], f[i][e], q);
             }
         }
-        const float var = row_sum(q, 0.f, slots, slot).x * inv_h;
-        const float rstd = 1.f / sqrtf(var + a.eps);
+        const float var = row_sum<MAXT>(q.x + q.y, slots, slot) * inv_h;
+        const float rstd = rsqrtf(var + a.eps);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = (tid + i * blockDim.x) * kGroup;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[i][e] = fmaf(f[i][e] * rstd, w[i][e], b[i][e]);
-            if (c < H) store_group(yr, c, H, a.out_vec, f[i]);
+            for (int e = 0; e < 4; ++e)
+                f[i][e] = __ffma2_rn(__fmul2_rn(f[i][e], both(rstd)), w[i][e], b[i][e]);
+            if (FULL || c < H) store_group(yr, c, FULL ? c + kGroup : H, out_vec, f[i]);
         }
         if (tid == 0) {
             if (a.mean_out != nullptr) a.mean_out[row] = mean;
@@ -396,7 +459,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s += f[e];
             }
-            mean = row_sum(s, 0.f, slots, slot).x * inv_h;
+            mean = row_sum<1024>(s, slots, slot) * inv_h;
         }
         float q = 0.f;
         for (int c = c0; c < H; c += kStep) {
@@ -410,8 +473,8 @@ __global__ void __launch_bounds__(1024)
                 if (e < n) q = fmaf(d, d, q);
             }
         }
-        const float var = row_sum(q, 0.f, slots, slot).x * inv_h;
-        rstd = 1.f / sqrtf(var + eps);
+        const float var = row_sum<1024>(q, slots, slot) * inv_h;
+        rstd = rsqrtf(var + eps);
     }
     for (int c = c0; c < H; c += kStep) {
         float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8], b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -433,7 +496,7 @@ __global__ void __launch_bounds__(1024)
 
 // ----------------------------------------------------------------------------- backward
 
-template <typename T, bool CENTER, int MAXT>
+template <typename T, bool CENTER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, 1)
     norm_bwd_kernel(const NormArgs a, int stages, int x_mode, int dy_mode, float inv_h,
                     float* __restrict__ dw_part, float* __restrict__ db_part) {
@@ -441,6 +504,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     __shared__ float2 slots[2][32];
     int slot = 0;
     const int tid = threadIdx.x, H = a.H;
+    const bool out_vec = FULL || a.out_vec;
     const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.out);
@@ -450,27 +514,33 @@ __global__ void __launch_bounds__(MAXT, 1)
     for (int k = 0; k < stages - 1; ++k) {
         const int64_t r = row + k * live.step;
         if (live.byte(r)) {
-            rx.fetch(x + r * a.x_stride, k, H, x_mode);
-            rg.fetch(dy + r * a.dy_stride, k, H, dy_mode);
+            rx.fetch(x + r * a.x_stride, k, H, x_mode, FULL);
+            rg.fetch(dy + r * a.dy_stride, k, H, dy_mode, FULL);
             live.bits |= 1u << k;
         }
         cp_commit();
     }
     live.next = live.byte(row + (stages - 1) * live.step);
-    float w[kGroups][8], dw[kGroups][8], db[kGroups][8];
+    float2 w[kGroups][4], dw[kGroups][4], db[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        param_group(a.weight, a.w_bf16, a.w_vec, (tid + i * blockDim.x) * kGroup, H, w[i]);
+        float v[8];
+        param_group(a.weight, a.w_bf16, a.w_vec, (tid + i * blockDim.x) * kGroup, H, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+            w[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
+            dw[i][e] = db[i][e] = both(0.f);
+        }
     }
+    // the statistics of a row are read one row early
+    float rstd_next = a.rstd[row], mean_next = CENTER ? a.mean[row] : 0.f;
     int stage = 0;
     for (; row < a.N; row += live.step) {
         const int64_t ahead = row + (stages - 1) * live.step;
         if (live.next) {
             const int to = stage == 0 ? stages - 1 : stage - 1;
-            rx.fetch(x + ahead * a.x_stride, to, H, x_mode);
-            rg.fetch(dy + ahead * a.dy_stride, to, H, dy_mode);
+            rx.fetch(x + ahead * a.x_stride, to, H, x_mode, FULL);
+            rg.fetch(dy + ahead * a.dy_stride, to, H, dy_mode, FULL);
             live.bits |= 1u << (stages - 1);
         }
         cp_commit();
@@ -479,52 +549,59 @@ __global__ void __launch_bounds__(MAXT, 1)
         live.bits >>= 1;
         const int at = stage;
         stage = stage + 1 == stages ? 0 : stage + 1;
+        const float rstd = rstd_next, mean = mean_next;
+        if (row + live.step < a.N) {
+            rstd_next = a.rstd[row + live.step];
+            if (CENTER) mean_next = a.mean[row + live.step];
+        }
         T* dxr = dx + row * a.out_stride;
         if (!on) {
-            const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int c = tid * kGroup; c < H; c += blockDim.x * kGroup)
-                store_group(dxr, c, H, a.out_vec, z);
+            zero_row(dxr, H, out_vec);
             continue;
         }
-        const float rstd = a.rstd[row];
-        const float mean = CENTER ? a.mean[row] : 0.f;
         cp_wait(stages - 1);
-        float xh[kGroups][8], g[kGroups][8];
-        float s1 = 0.f, s2 = 0.f;
+        float2 xh[kGroups][4], g[kGroups][4], s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             rx.group(at, i).unpack(xh[i]);
             rg.group(at, i).unpack(g[i]);       // dy past H is 0: these columns add nothing
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[i][e] = (xh[i][e] - mean) * rstd;
-                dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
-                if (CENTER) db[i][e] += g[i][e];
-                g[i][e] *= w[i][e];
-                if (CENTER) s1 += g[i][e];
-                s2 = fmaf(g[i][e], xh[i][e], s2);
+            for (int e = 0; e < 4; ++e) {
+                if (CENTER) xh[i][e] = __fadd2_rn(xh[i][e], both(-mean));
+                xh[i][e] = __fmul2_rn(xh[i][e], both(rstd));
+                dw[i][e] = __ffma2_rn(g[i][e], xh[i][e], dw[i][e]);
+                if (CENTER) db[i][e] = __fadd2_rn(db[i][e], g[i][e]);
+                g[i][e] = __fmul2_rn(g[i][e], w[i][e]);
+                if (CENTER) s1 = __fadd2_rn(s1, g[i][e]);
+                s2 = __ffma2_rn(g[i][e], xh[i][e], s2);
             }
         }
-        const float2 t = row_sum(s1, s2, slots, slot);
+        float2 t;
+        if (CENTER)
+            t = row_sum<MAXT>(s1.x + s1.y, s2.x + s2.y, slots, slot);
+        else
+            t = make_float2(0.f, row_sum<MAXT>(s2.x + s2.y, slots, slot));
         const float m1 = t.x * inv_h, m2 = t.y * inv_h;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = (tid + i * blockDim.x) * kGroup;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float d = CENTER ? g[i][e] - m1 : g[i][e];
-                g[i][e] = fmaf(-xh[i][e], m2, d) * rstd;
+            for (int e = 0; e < 4; ++e) {
+                if (CENTER) g[i][e] = __fadd2_rn(g[i][e], both(-m1));
+                g[i][e] = __fmul2_rn(__ffma2_rn(xh[i][e], both(-m2), g[i][e]), both(rstd));
             }
-            if (c < H) store_group(dxr, c, H, a.out_vec, g[i]);
+            if (FULL || c < H) store_group(dxr, c, FULL ? c + kGroup : H, out_vec, g[i]);
         }
     }
     // the block's partial row, in the order of part_len: neighbouring threads write
     // neighbouring floats
     const int64_t out = int64_t(blockIdx.x) * (blockDim.x * kGroups * 8) + tid;
 #pragma unroll
-    for (int i = 0; i < kGroups * 8; ++i) {
-        if (dw_part != nullptr) dw_part[out + i * blockDim.x] = dw[i / 8][i % 8];
-        if (CENTER && db_part != nullptr) db_part[out + i * blockDim.x] = db[i / 8][i % 8];
+    for (int i = 0; i < kGroups * 4; ++i) {
+        const float2 vw = dw[i / 4][i % 4], vb = db[i / 4][i % 4];
+        const int64_t at = out + 2 * i * blockDim.x;
+        if (dw_part != nullptr) dw_part[at] = vw.x, dw_part[at + blockDim.x] = vw.y;
+        if (CENTER && db_part != nullptr) db_part[at] = vb.x, db_part[at + blockDim.x] = vb.y;
     }
 }
 
@@ -580,7 +657,7 @@ __global__ void __launch_bounds__(1024)
                 if (CENTER && db_part != nullptr) db_part[k] += gf[e];
             }
         }
-        const float2 t = row_sum(s1, s2, slots, slot);
+        const float2 t = row_sum<1024>(s1, s2, slots, slot);
         const float m1 = t.x * inv_h, m2 = t.y * inv_h;
         for (int c = c0; c < H; c += kStep) {
             float xf[8], gf[8], w[8];
@@ -600,16 +677,18 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-// Column sums of the partial rows: 32 places a block, 16 threads a place (each every 16th
-// partial row, ascending), then the 16 in order.  P = 0 writes zeros.
-__global__ void __launch_bounds__(512)
+// Column sums of the partial rows: 32 places a block, 32 threads a place (each every 32nd
+// partial row, ascending), then the 32 in order.  P = 0 writes zeros.  Launched early: its
+// blocks wait for the partial rows.
+__global__ void __launch_bounds__(1024)
     norm_dw_merge_kernel(const float* __restrict__ dw_part, const float* __restrict__ db_part,
                          int P, int len, int threads, int H, bool bf16,
                          void* __restrict__ dweight, void* __restrict__ dbias) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float* part = blockIdx.y == 0 ? dw_part : db_part;
     void* out = blockIdx.y == 0 ? dweight : dbias;
     if (out == nullptr) return;
-    __shared__ float s[16][33];
+    __shared__ float s[32][33];
     const int x = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int pos = blockIdx.x * 32 + x;             // len is a multiple of 32
     const int r = pos / threads;                     // the place's column: see part_len
@@ -618,20 +697,20 @@ __global__ void __launch_bounds__(512)
     if (c < H) {
         // four loads at a time, added in ascending order
         int p = q;
-        for (; p + 48 < P; p += 64) {
+        for (; p + 96 < P; p += 128) {
             float v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = part[int64_t(p + 16 * k) * len + pos];
+            for (int k = 0; k < 4; ++k) v[k] = part[int64_t(p + 32 * k) * len + pos];
 #pragma unroll
             for (int k = 0; k < 4; ++k) a += v[k];
         }
-        for (; p < P; p += 16) a += part[int64_t(p) * len + pos];
+        for (; p < P; p += 32) a += part[int64_t(p) * len + pos];
     }
     s[q][x] = a;
     __syncthreads();
     if (q != 0 || c >= H) return;
-#pragma unroll
-    for (int k = 1; k < 16; ++k) a += s[k][x];
+#pragma unroll 8
+    for (int k = 1; k < 32; ++k) a += s[k][x];
     if (bf16)
         static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(a);
     else
@@ -691,9 +770,14 @@ cudaError_t allow_smem(F kernel, size_t smem) {
                                 static_cast<int>(smem));
 }
 
+bool is_full(const NormArgs& a, const Plan& p) {
+    return a.H == p.threads * kGroups * kGroup && a.in_vec && a.out_vec;
+}
+
 template <typename T, bool CENTER, int MAXT>
 cudaError_t run_fwd(const NormArgs& a, const Plan& p, cudaStream_t stream) {
-    auto kernel = norm_fwd_kernel<T, CENTER, MAXT>;
+    auto kernel = is_full(a, p) ? norm_fwd_kernel<T, CENTER, MAXT, true>
+                                : norm_fwd_kernel<T, CENTER, MAXT, false>;
     const cudaError_t e = allow_smem(kernel, p.smem);
     if (e != cudaSuccess) return e;
     const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(p.threads));
@@ -719,7 +803,8 @@ cudaError_t fwd_dispatch(const NormArgs& a, cudaStream_t stream) {
 template <typename T, bool CENTER, int MAXT>
 cudaError_t run_bwd(const NormArgs& a, const Plan& p, int blocks, float* dwp, float* dbp,
                     cudaStream_t stream) {
-    auto kernel = norm_bwd_kernel<T, CENTER, MAXT>;
+    auto kernel = is_full(a, p) ? norm_bwd_kernel<T, CENTER, MAXT, true>
+                                : norm_bwd_kernel<T, CENTER, MAXT, false>;
     const cudaError_t e = allow_smem(kernel, p.smem);
     if (e != cudaSuccess) return e;
     kernel<<<blocks, p.threads, p.smem, stream>>>(a, p.stages, copy_mode(a.x, a.x_stride, sizeof(T)),
@@ -776,10 +861,19 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool center, cudaStream_t stream)
         if (e != cudaSuccess) return e;
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>(p.len / 32), a.dbias != nullptr ? 2 : 1);
-    norm_dw_merge_kernel<<<grid, 512, 0, stream>>>(dwp, dbp, p.blocks, static_cast<int>(p.len),
-                                                   p.threads, a.H, a.w_bf16, a.dweight, a.dbias);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.len / 32), a.dbias != nullptr ? 2 : 1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_dw_merge_kernel, static_cast<const float*>(dwp),
+                              static_cast<const float*>(dbp), a.N > 0 ? p.blocks : 0,
+                              static_cast<int>(p.len), p.threads, a.H, a.w_bf16, a.dweight,
+                              a.dbias);
 }
 
 }  // namespace rlk
