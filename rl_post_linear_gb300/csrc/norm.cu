@@ -245,16 +245,23 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int byte
                      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but the newest `left` groups have arrived
-__device__ __forceinline__ void cp_wait(int left) {
-    if (left == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+// all but the newest LEFT groups have arrived
+template <int LEFT>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-constexpr int kGroups = 2;       // groups of a thread
-constexpr int kMaxStages = 4;    // rows on their way
+// Groups of a thread: two keep the forward at 64 registers and the backward at 128 (with
+// four the backward took 84 us instead of 42 at [8192, 4096], the forward 28.8 instead of
+// 26.6).
+constexpr int kGroups = 2;
+// Rows that a block has in shared memory, the one it works on among them.  The forward gains
+// nothing from a third row (26.6 us at [8192, 4096] either way, 72 against 92 us at
+// [16384, 7168] with a fifth masked), the backward nothing from a fourth.
+template <typename T, int MAXT, int TENSORS>
+__host__ __device__ constexpr int stages_of() {
+    return TENSORS == 1 ? 2 : MAXT == 512 || sizeof(T) == 2 ? 3 : 1;
+}
 
 // A thread's part of a ring of rows in shared memory: `stages` slots of kGroups groups.
 // 16-byte piece p of slot s lies at (s pieces + p) threads + tid, so the threads of a warp
@@ -316,22 +323,17 @@ __device__ __forceinline__ Raw<float> Ring<float>::group(int stage, int i) const
     return r;
 }
 
-// What the masks of the next rows say, one load ahead of the copies that need it.
-struct Live {
-    const uint8_t* mask;
-    int64_t step, N;
-    uint32_t bits;               // bit k: the k-th next row is active
-    int next;                    // mask byte of the row after those
-    __device__ __forceinline__ int byte(int64_t row) const {
-        return row >= N ? 0 : mask == nullptr ? 1 : __ldg(mask + row);
-    }
-};
+// mask byte of a row: 0 past the end
+__device__ __forceinline__ int mask_byte(const NormArgs& a, int row) {
+    return row >= a.N ? 0 : a.mask == nullptr ? 1 : __ldg(a.mask + row);
+}
 
 // FULL: H is 16 columns for each thread and every row starts on 16 bytes, so no column needs
 // a test (a third of the instructions of a row; the arithmetic is the same).
 template <typename T, bool CENTER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
-    norm_fwd_kernel(const NormArgs a, int stages, int x_mode, float inv_h) {
+    norm_fwd_kernel(const NormArgs a, int x_mode, float inv_h) {
+    constexpr int S = stages_of<T, MAXT, 1>();
     extern __shared__ uint4 ring_smem[];
     __shared__ float2 slots[2][32];
     int slot = 0;
@@ -340,18 +342,24 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.out);
     const Ring<T> ring{ring_smem};
-    Live live{a.mask, int64_t(gridDim.x), a.N, 0, 0};
-    int64_t row = blockIdx.x;
-    // stages - 1 rows are on their way before the first is waited for
-    for (int k = 0; k < stages - 1; ++k) {
-        const int64_t r = row + k * live.step;
-        if (live.byte(r)) {
-            ring.fetch(x + r * a.x_stride, k, H, x_mode, FULL);
-            live.bits |= 1u << k;
+    // Row indices leave room for S more steps below 2^31.  S - 1 rows are on their way before
+    // the first is waited for; `bits` says which of them are active, `next` whether the row
+    // after them is.
+    const int step = gridDim.x;
+    int row = blockIdx.x, next;
+    uint32_t bits = 0;
+    const T* ahead = x + row * a.x_stride;           // the row to fetch next
+    T* yr = y + row * a.out_stride;
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+        if (mask_byte(a, row + k * step)) {
+            ring.fetch(ahead, k, H, x_mode, FULL);
+            bits |= 1u << k;
         }
         cp_commit();
+        ahead += step * a.x_stride;
     }
-    live.next = live.byte(row + (stages - 1) * live.step);
+    next = mask_byte(a, row + (S - 1) * step);
     float2 w[kGroups][4], b[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -367,20 +375,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
         }
     }
     int stage = 0;
-    for (; row < a.N; row += live.step) {
-        const int64_t ahead = row + (stages - 1) * live.step;
-        if (live.next) {
-            ring.fetch(x + ahead * a.x_stride, stage == 0 ? stages - 1 : stage - 1, H, x_mode,
-                       FULL);
-            live.bits |= 1u << (stages - 1);
+    for (; row < a.N; row += step, yr += step * a.out_stride) {
+        if (next) {
+            ring.fetch(ahead, stage == 0 ? S - 1 : stage - 1, H, x_mode, FULL);
+            bits |= 1u << (S - 1);
         }
         cp_commit();
-        live.next = live.byte(ahead + live.step);
-        const bool on = live.bits & 1u;
-        live.bits >>= 1;
+        ahead += step * a.x_stride;
+        next = mask_byte(a, row + S * step);
+        const bool on = bits & 1u;
+        bits >>= 1;
         const int at = stage;
-        stage = stage + 1 == stages ? 0 : stage + 1;
-        T* yr = y + row * a.out_stride;
+        stage = stage + 1 == S ? 0 : stage + 1;
         if (!on) {
             zero_row(yr, H, out_vec);
             if (tid == 0) {
@@ -389,7 +395,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
             }
             continue;
         }
-        cp_wait(stages - 1);
+        cp_wait<S - 1>();
         float2 f[kGroups][4], s = both(0.f);
         float mean = 0.f;
 #pragma unroll
@@ -498,8 +504,9 @@ __global__ void __launch_bounds__(1024)
 
 template <typename T, bool CENTER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, 1)
-    norm_bwd_kernel(const NormArgs a, int stages, int x_mode, int dy_mode, float inv_h,
+    norm_bwd_kernel(const NormArgs a, int x_mode, int dy_mode, float inv_h,
                     float* __restrict__ dw_part, float* __restrict__ db_part) {
+    constexpr int S = stages_of<T, MAXT, 2>();
     extern __shared__ uint4 ring_smem[];
     __shared__ float2 slots[2][32];
     int slot = 0;
@@ -508,19 +515,25 @@ __global__ void __launch_bounds__(MAXT, 1)
     const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.out);
-    const Ring<T> rx{ring_smem}, rg{ring_smem + stages * Ring<T>::kPieces * blockDim.x};
-    Live live{a.mask, int64_t(gridDim.x), a.N, 0, 0};
-    int64_t row = blockIdx.x;
-    for (int k = 0; k < stages - 1; ++k) {
-        const int64_t r = row + k * live.step;
-        if (live.byte(r)) {
-            rx.fetch(x + r * a.x_stride, k, H, x_mode, FULL);
-            rg.fetch(dy + r * a.dy_stride, k, H, dy_mode, FULL);
-            live.bits |= 1u << k;
+    const Ring<T> rx{ring_smem}, rg{ring_smem + S * Ring<T>::kPieces * blockDim.x};
+    const int step = gridDim.x;
+    int row = blockIdx.x, next;
+    uint32_t bits = 0;
+    const T* x_ahead = x + row * a.x_stride;
+    const T* g_ahead = dy + row * a.dy_stride;
+    T* dxr = dx + row * a.out_stride;
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) {
+        if (mask_byte(a, row + k * step)) {
+            rx.fetch(x_ahead, k, H, x_mode, FULL);
+            rg.fetch(g_ahead, k, H, dy_mode, FULL);
+            bits |= 1u << k;
         }
         cp_commit();
+        x_ahead += step * a.x_stride;
+        g_ahead += step * a.dy_stride;
     }
-    live.next = live.byte(row + (stages - 1) * live.step);
+    next = mask_byte(a, row + (S - 1) * step);
     float2 w[kGroups][4], dw[kGroups][4], db[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -535,31 +548,31 @@ __global__ void __launch_bounds__(MAXT, 1)
     // the statistics of a row are read one row early
     float rstd_next = a.rstd[row], mean_next = CENTER ? a.mean[row] : 0.f;
     int stage = 0;
-    for (; row < a.N; row += live.step) {
-        const int64_t ahead = row + (stages - 1) * live.step;
-        if (live.next) {
-            const int to = stage == 0 ? stages - 1 : stage - 1;
-            rx.fetch(x + ahead * a.x_stride, to, H, x_mode, FULL);
-            rg.fetch(dy + ahead * a.dy_stride, to, H, dy_mode, FULL);
-            live.bits |= 1u << (stages - 1);
+    for (; row < a.N; row += step, dxr += step * a.out_stride) {
+        if (next) {
+            const int to = stage == 0 ? S - 1 : stage - 1;
+            rx.fetch(x_ahead, to, H, x_mode, FULL);
+            rg.fetch(g_ahead, to, H, dy_mode, FULL);
+            bits |= 1u << (S - 1);
         }
         cp_commit();
-        live.next = live.byte(ahead + live.step);
-        const bool on = live.bits & 1u;
-        live.bits >>= 1;
+        x_ahead += step * a.x_stride;
+        g_ahead += step * a.dy_stride;
+        next = mask_byte(a, row + S * step);
+        const bool on = bits & 1u;
+        bits >>= 1;
         const int at = stage;
-        stage = stage + 1 == stages ? 0 : stage + 1;
+        stage = stage + 1 == S ? 0 : stage + 1;
         const float rstd = rstd_next, mean = mean_next;
-        if (row + live.step < a.N) {
-            rstd_next = a.rstd[row + live.step];
-            if (CENTER) mean_next = a.mean[row + live.step];
+        if (row + step < a.N) {
+            rstd_next = a.rstd[row + step];
+            if (CENTER) mean_next = a.mean[row + step];
         }
-        T* dxr = dx + row * a.out_stride;
         if (!on) {
             zero_row(dxr, H, out_vec);
             continue;
         }
-        cp_wait(stages - 1);
+        cp_wait<S - 1>();
         float2 xh[kGroups][4], g[kGroups][4], s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
@@ -695,16 +708,15 @@ __global__ void __launch_bounds__(1024)
     const int64_t c = (int64_t(r >> 3) * threads + pos % threads) * kGroup + (r & 7);
     float a = 0.f;
     if (c < H) {
-        // four loads at a time, added in ascending order
-        int p = q;
-        for (; p + 96 < P; p += 128) {
-            float v[4];
+        // ten loads at a time, added in ascending order
+        for (int p = q; p < P; p += 320) {
+            float v[10];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = part[int64_t(p + 32 * k) * len + pos];
+            for (int k = 0; k < 10; ++k)
+                v[k] = p + 32 * k < P ? part[int64_t(p + 32 * k) * len + pos] : 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) a += v[k];
+            for (int k = 0; k < 10; ++k) a += v[k];
         }
-        for (; p < P; p += 32) a += part[int64_t(p) * len + pos];
     }
     s[q][x] = a;
     __syncthreads();
@@ -720,29 +732,16 @@ __global__ void __launch_bounds__(1024)
 // The widest row that stays in registers.
 constexpr int kMaxRegH = 1024 * kGroups * kGroup;
 
-// The threads of a row follow from H alone.
-struct Plan {
-    int threads;                   // 0: the wide kernels
-    int stages;
-    size_t smem;
-};
-// tensors: rings that a block holds; blocks: on an SM
-Plan make_plan(int64_t H, size_t esize, int tensors, int blocks) {
-    if (H > kMaxRegH) return {0, 0, 0};
-    Plan p;
-    const int64_t half = (H + kGroups * kGroup - 1) / (kGroups * kGroup);
-    p.threads = static_cast<int>((half + 31) / 32 * 32);
-    const size_t row = size_t(p.threads) * kGroups * kGroup * esize * tensors;
-    const size_t room = size_t(208) * 1024 / blocks;
-    p.stages = static_cast<int>(std::min<size_t>(kMaxStages, std::max<size_t>(1, room / row)));
-    p.smem = row * p.stages;
-    return p;
-}
 // Blocks on an SM: the forward holds 64 registers a thread, the backward up to 128.
 int fwd_blocks_per_sm(int threads) { return std::max(1, std::min(16, 1024 / std::max(threads, 32))); }
 int bwd_blocks_per_sm(int threads) { return std::max(1, std::min(16, 512 / std::max(threads, 32))); }
 
-int threads_of(int64_t H) { return make_plan(H, 4, 1, 1).threads; }
+// The threads of a row follow from H alone; 0: the wide kernels.
+int threads_of(int64_t H) {
+    if (H > kMaxRegH) return 0;
+    const int64_t half = (H + kGroups * kGroup - 1) / (kGroups * kGroup);
+    return static_cast<int>((half + 31) / 32 * 32);
+}
 
 // Blocks (= partial rows) of the backward and floats of a partial row: fixed by H and N.
 struct Parts {
@@ -770,19 +769,20 @@ cudaError_t allow_smem(F kernel, size_t smem) {
                                 static_cast<int>(smem));
 }
 
-bool is_full(const NormArgs& a, const Plan& p) {
-    return a.H == p.threads * kGroups * kGroup && a.in_vec && a.out_vec;
+bool is_full(const NormArgs& a, int threads) {
+    return a.H == threads * kGroups * kGroup && a.in_vec && a.out_vec;
 }
 
 template <typename T, bool CENTER, int MAXT>
-cudaError_t run_fwd(const NormArgs& a, const Plan& p, cudaStream_t stream) {
-    auto kernel = is_full(a, p) ? norm_fwd_kernel<T, CENTER, MAXT, true>
+cudaError_t run_fwd(const NormArgs& a, int threads, cudaStream_t stream) {
+    auto kernel = is_full(a, threads) ? norm_fwd_kernel<T, CENTER, MAXT, true>
                                 : norm_fwd_kernel<T, CENTER, MAXT, false>;
-    const cudaError_t e = allow_smem(kernel, p.smem);
+    const size_t smem = size_t(threads) * kGroups * kGroup * sizeof(T) * stages_of<T, MAXT, 1>();
+    const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(p.threads));
-    kernel<<<blocks, p.threads, p.smem, stream>>>(a, p.stages, copy_mode(a.x, a.x_stride, sizeof(T)),
-                                                  1.f / static_cast<float>(a.H));
+    const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(threads));
+    kernel<<<blocks, threads, smem, stream>>>(a, copy_mode(a.x, a.x_stride, sizeof(T)),
+                                              1.f / static_cast<float>(a.H));
     return cudaGetLastError();
 }
 
@@ -796,20 +796,21 @@ cudaError_t fwd_dispatch(const NormArgs& a, cudaStream_t stream) {
             a.out_stride, a.out_vec, a.mean_out, a.rstd_out);
         return cudaGetLastError();
     }
-    const Plan p = make_plan(a.H, sizeof(T), 1, fwd_blocks_per_sm(t));
-    return t <= 512 ? run_fwd<T, CENTER, 512>(a, p, stream) : run_fwd<T, CENTER, 1024>(a, p, stream);
+    return t <= 512 ? run_fwd<T, CENTER, 512>(a, t, stream) : run_fwd<T, CENTER, 1024>(a, t, stream);
 }
 
 template <typename T, bool CENTER, int MAXT>
-cudaError_t run_bwd(const NormArgs& a, const Plan& p, int blocks, float* dwp, float* dbp,
+cudaError_t run_bwd(const NormArgs& a, int threads, int blocks, float* dwp, float* dbp,
                     cudaStream_t stream) {
-    auto kernel = is_full(a, p) ? norm_bwd_kernel<T, CENTER, MAXT, true>
+    auto kernel = is_full(a, threads) ? norm_bwd_kernel<T, CENTER, MAXT, true>
                                 : norm_bwd_kernel<T, CENTER, MAXT, false>;
-    const cudaError_t e = allow_smem(kernel, p.smem);
+    const size_t smem =
+        size_t(threads) * kGroups * kGroup * sizeof(T) * 2 * stages_of<T, MAXT, 2>();
+    const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, p.threads, p.smem, stream>>>(a, p.stages, copy_mode(a.x, a.x_stride, sizeof(T)),
-                                                  copy_mode(a.dy, a.dy_stride, sizeof(T)),
-                                                  1.f / static_cast<float>(a.H), dwp, dbp);
+    kernel<<<blocks, threads, smem, stream>>>(a, copy_mode(a.x, a.x_stride, sizeof(T)),
+                                              copy_mode(a.dy, a.dy_stride, sizeof(T)),
+                                              1.f / static_cast<float>(a.H), dwp, dbp);
     return cudaGetLastError();
 }
 
@@ -825,9 +826,8 @@ cudaError_t bwd_dispatch(const NormArgs& a, int blocks, float* dwp, float* dbp,
             dbp);
         return cudaGetLastError();
     }
-    const Plan p = make_plan(a.H, sizeof(T), 2, bwd_blocks_per_sm(t));
-    return t <= 512 ? run_bwd<T, CENTER, 512>(a, p, blocks, dwp, dbp, stream)
-                    : run_bwd<T, CENTER, 1024>(a, p, blocks, dwp, dbp, stream);
+    return t <= 512 ? run_bwd<T, CENTER, 512>(a, t, blocks, dwp, dbp, stream)
+                    : run_bwd<T, CENTER, 1024>(a, t, blocks, dwp, dbp, stream);
 }
 
 }  // namespace
