@@ -204,6 +204,17 @@ struct Chunk {
             }
         }
     }
+    // Four elements at a time, for loops whose code is better short: the first four, and the
+    // others moved up.
+    static constexpr int kQuads = kLane / 4;
+    __device__ __forceinline__ void take(float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = get(e);
+        uint32_t* p = reinterpret_cast<uint32_t*>(raw);
+        constexpr int kWords = LOADS * 4, kStep = kWords / kQuads;
+#pragma unroll
+        for (int w = 0; w + kStep < kWords; ++w) p[w] = p[w + kStep];
+    }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t* p = reinterpret_cast<const uint32_t*>(raw);
         if (sizeof(T) == 4) return __uint_as_float(p[i]);
@@ -528,23 +539,28 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
         sh.n_list = 0, sh.n_ids = 0;
         sh.key_m = s.want_m ? min_p_key(a, row_i, r.ws.m) : 0;
     }
+    // What min_p keeps is all that is needed where nothing refers to the weight of the first
+    // top_k elements.
+    const bool by_m = s.want_m && !(s.want_k && s.want_p);
     uint32_t tau = kKeyNegInf + 1;
-    if (r.V > kShort && (s.want_k || s.want_p)) {
-        if (s.want_k && s.top_k > r.nch * 9 / 10) return false;
+    if (r.V > kShort && (s.want_k || s.want_p) && !(by_m && s.want_p)) {
+        const bool few = s.want_k && s.top_k <= r.nch * 9 / 10;
+        if (s.want_k && !few && !by_m) return false;
         // between the maximum and what weighs nothing
         const float low = fmaxf(r.ws.m - 47.5f / r.ws.ch, -3.402823466e38f);
         const float need = s.p_value * 1.00001f * static_cast<float>(all) *
                            __uint_as_float(uint32_t(127 - r.bits) << 23);
-        bool found;
-        const float x = reach_value(r, cmax, static_cast<int>(s.top_k), s.want_k ? 0.f : need, low,
-                                    found, sh);
-        if (!found && !s.want_k) return false;       // a wide nucleus
-        tau = max(tau, order_key(x));
+        if (few || !s.want_k) {
+            bool found;
+            const float x = reach_value(r, cmax, static_cast<int>(s.top_k), s.want_k ? 0.f : need,
+                                        low, found, sh);
+            if (!found && !s.want_k) return false;   // a wide nucleus
+            tau = max(tau, order_key(x));
+        }
     }
     __syncthreads();
     const uint32_t key_m = sh.key_m;
-    // what min_p cuts is needed only where top_p counts it
-    if (!s.want_p) tau = max(tau, key_m);
+    if (by_m) tau = max(tau, key_m);
     const float tau_x = key_value(tau);
     for (int c = tid; c < r.nch; c += kThreads)
         if (cmax[c] >= tau_x) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
@@ -570,12 +586,10 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
             while (hits != 0) {
                 const int e = __ffs(hits) - 1;
                 hits &= hits - 1;
-                const int col = Chunk<T>::column(ids[i], e / Chunk<T>::VEC, lane) +
-                                e % Chunk<T>::VEC;
                 const uint32_t at = atomicAdd(&sh.n_list, 1u);
                 if (at < kShort)
-                    sh.order[at] = (u64(order_key(load_one(r.x + col))) << 32) |
-                                   (0xffffffffu - uint32_t(col));
+                    sh.order[at] = Chunk<T>::column(ids[i], e / Chunk<T>::VEC, lane) +
+                                   e % Chunk<T>::VEC;
             }
         }
     }
@@ -583,8 +597,12 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     const uint32_t n = sh.n_list;
     if (n > kShort) return false;
 #pragma unroll 1
-    for (uint32_t i = tid; i < n; i += kThreads)
-        sh.w[i] = fixed_weight(key_value(uint32_t(sh.order[i] >> 32)), r.ws, sh.table);
+    for (uint32_t i = tid; i < n; i += kThreads) {
+        const uint32_t col = static_cast<uint32_t>(sh.order[i]);
+        const float x = load_one(r.x + col);
+        sh.order[i] = (u64(order_key(x)) << 32) | (0xffffffffu - col);
+        sh.w[i] = fixed_weight(x, r.ws, sh.table);
+    }
     sort_list(n, sh.order, sh.w);
     // thread t holds elements 2 t and 2 t + 1 of the order
     const uint32_t i0 = 2 * tid, i1 = i0 + 1;
@@ -602,11 +620,11 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     }
     if (s.want_p) {
         u64 lo = s_k, hi = s_k;                      // exact, where the list holds all that counts
-        const bool whole = s.want_k || r.V <= kShort;
+        const bool whole = s.want_k || (r.V <= kShort && !by_m);
         if (!whole) total_bounds(all, lo, hi);
         const u64 need_lo = max(u64(1), part_of(s.top_p, lo, true));
         const u64 need_hi = whole ? need_lo : max(u64(1), part_of(s.top_p, hi, true));
-        if (need_hi > sum.tv) return false;
+        if (need_hi > sum.tv && !by_m) return false;
         // the order's first elements before whose sum the need is not reached
         const uint32_t n_lo = __syncthreads_count(i0 < n && b0 < need_lo) +
                               __syncthreads_count(i1 < n && b1 < need_lo);
@@ -771,8 +789,12 @@ struct Shared {
     u64 table[kExpEntries];
     u64 w[kList];                        // block 0: the merged list
     uint32_t key[kList], idx[kList];
-    uint32_t own_key[kList], own_idx[kList];   // this block's part of it
-    uint32_t hist[kBins];
+    union {                              // of one step or the other
+        uint32_t hist[kBins];
+        struct {
+            uint32_t own_key[kList], own_idx[kList];   // this block's part of the list
+        };
+    };
     uint32_t cnt[256], lo[256], hi[256];
     u64 part[kSearch / 32];
     uint32_t part_n[kSearch / 32];
@@ -792,37 +814,14 @@ __device__ __forceinline__ float distance(float x, const Row<T>& r) {
     return fminf((r.ws.m - x) * r.scale, 2.f * kBins);
 }
 
-// Which of a lane's 16 elements are above and inside the window, as bits.
+// Whether an element is above or inside the window.
 template <typename T>
-__device__ __forceinline__ void classify(const Chunk<T>& c, const Row<T>& r, const Cmd& cmd,
-                                         uint32_t& up, uint32_t& in) {
-    up = in = 0;
-    if (cmd.khi <= kKeyNegInf) {                     // all that is not -inf is above
-        up = (1u << kLane) - 1;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) {
-        const float x = c.get(e);
-        const int b = static_cast<int>(distance(x, r));
-        const uint32_t k = order_key(x);
-        const bool over = b < cmd.b1 || (b <= cmd.b2 && k > cmd.khi);
-        const bool inside = !over && b <= cmd.b2 && k >= cmd.klo && k > kKeyNegInf;
-        up |= (over ? 1u : 0u) << e;
-        in |= (inside ? 1u : 0u) << e;
-    }
-}
-
-// exact weights of a lane's elements: of those in `up`, and of all
-template <typename T>
-__device__ __forceinline__ void weigh(const Chunk<T>& c, const Row<T>& r, const u64* table,
-                                      uint32_t up, u64& above, u64& all) {
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) {
-        const u64 w = fixed_weight(c.get(e), r.ws, table);
-        all += w;
-        above += (up >> e) & 1u ? w : 0;
-    }
+__device__ __forceinline__ void classify(float x, const Row<T>& r, const Cmd& cmd, bool& up,
+                                         bool& in) {
+    const int b = static_cast<int>(distance(x, r));
+    const uint32_t k = order_key(x);
+    up = b < cmd.b1 || (b <= cmd.b2 && k > cmd.khi);
+    in = !up && b <= cmd.b2 && k >= cmd.klo && k > kKeyNegInf;
 }
 
 // Histogram of the window; for windows of keys also the exact weight above it.
@@ -855,17 +854,27 @@ __device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const fl
             }
             continue;
         }
-        uint32_t up, in;
-        classify(c, r, cmd, up, in);
-        if (cmd.by_weight && __any_sync(0xffffffffu, cmd.total || up != 0))
-            weigh(c, r, sh.table, up, above, all);
+#pragma unroll 1
+        for (int j = 0; j < Chunk<T>::kQuads; ++j) {
+            float x[4];
+            u64 w[4] = {0, 0, 0, 0};
+            c.take(x);
+            if (cmd.by_weight) {
+                fixed_weights(make_float2(x[0], x[1]), r.ws, sh.table, w[0], w[1]);
+                fixed_weights(make_float2(x[2], x[3]), r.ws, sh.table, w[2], w[3]);
+            }
 #pragma unroll
-        for (int e = 0; e < kLane; ++e) {
-            const float x = c.get(e);
-            const float q = cmd.by_weight ? rintf(4096.f * ex2_approx((x - x_hi) * r.ws.ch)) : 1.f;
-            if ((in >> e) & 1u)
-                atomicAdd(&sh.hist[(cmd.khi - order_key(x)) >> cmd.shift],
-                          static_cast<uint32_t>(q));
+            for (int e = 0; e < 4; ++e) {
+                bool up, in;
+                classify(x[e], r, cmd, up, in);
+                all += w[e];
+                above += up ? w[e] : 0;
+                const float q =
+                    cmd.by_weight ? rintf(4096.f * ex2_approx((x[e] - x_hi) * r.ws.ch)) : 1.f;
+                if (in)
+                    atomicAdd(&sh.hist[(cmd.khi - order_key(x[e])) >> cmd.shift],
+                              static_cast<uint32_t>(q));
+            }
         }
     }
     above = warp_sum(above);
@@ -893,28 +902,35 @@ __device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const
         if (near || (cmd.total && top_bin < kBins)) {
             Chunk<T> c;
             c.load(r.x, r.V, r.first + i, lane, r.vec);
-            uint32_t up, in;
-            classify(c, r, cmd, up, in);
-            if (__any_sync(0xffffffffu, cmd.total || up != 0)) {
-                weigh(c, r, sh.table, up, w, all);
-                w = warp_sum(w);
-            }
-            if (cmd.list == 0) {
-                n = __reduce_add_sync(0xffffffffu, __popc(in));
-                in = 0;
-            }
 #pragma unroll 1
-            while (in != 0) {
-                const int e = __ffs(in) - 1;
-                in &= in - 1;
-                const int col = Chunk<T>::column(r.first + i, e / Chunk<T>::VEC, lane) +
-                                e % Chunk<T>::VEC;
-                const uint32_t at = atomicAdd(&sh.own_count, 1u);
-                if (at < kList) {
-                    sh.own_key[at] = order_key(load_one(r.x + col));
-                    sh.own_idx[at] = col;
+            for (int j = 0; j < Chunk<T>::kQuads; ++j) {
+                float x[4];
+                u64 we[4];
+                c.take(x);
+                fixed_weights(make_float2(x[0], x[1]), r.ws, sh.table, we[0], we[1]);
+                fixed_weights(make_float2(x[2], x[3]), r.ws, sh.table, we[2], we[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    bool up, in;
+                    classify(x[e], r, cmd, up, in);
+                    all += we[e];
+                    w += up ? we[e] : 0;
+                    if (!in) continue;
+                    if (cmd.list == 0) {
+                        ++n;
+                        continue;
+                    }
+                    const uint32_t at = atomicAdd(&sh.own_count, 1u);
+                    if (at < kList) {
+                        const int v = j * 4 + e;
+                        sh.own_key[at] = order_key(x[e]);
+                        sh.own_idx[at] = Chunk<T>::column(r.first + i, v / Chunk<T>::VEC, lane) +
+                                         v % Chunk<T>::VEC;
+                    }
                 }
             }
+            w = warp_sum(w);
+            n = __reduce_add_sync(0xffffffffu, n);
         }
         if (lane == 0) own_w[i] = w, own_n[i] = n;
     }
@@ -929,11 +945,14 @@ struct Selected {
     uint32_t key;
     u64 n, w;
 };
-__device__ __noinline__ Selected list_select(bool by_weight, u64 need, Shared& sh) {
-    uint32_t prefix = 0;
+__device__ __noinline__ Selected list_select(bool by_weight, u64 need, const Cmd& cmd,
+                                             Shared& sh) {
+    // the window's keys differ in their low bytes alone
+    const int levels = (39 - __clz(cmd.klo ^ cmd.khi)) / 8;
+    uint32_t prefix = levels > 3 ? 0u : cmd.khi >> (8 * levels) << (8 * levels);
     u64 n_up = 0, w_up = 0;
 #pragma unroll 1
-    for (int level = 3; level >= 0; --level) {
+    for (int level = levels - 1; level >= 0; --level) {
         __syncthreads();
         if (threadIdx.x < 256) sh.cnt[threadIdx.x] = sh.lo[threadIdx.x] = sh.hi[threadIdx.x] = 0;
         __syncthreads();
@@ -1039,7 +1058,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         if (k >= ranks) break;
         const uint4 h = *reinterpret_cast<const uint4*>(peer(sh.hist, k) + b0);
         q[0] += h.x, q[1] += h.y, q[2] += h.z, q[3] += h.w;
-        above += *peer(&sh.own_above, k);
+        if (cmd.shift >= 0) above += *peer(&sh.own_above, k);
     }
     if (cmd.shift >= 0) take_total(P, cmd, ranks, sh);
     u64 mine = 0;
@@ -1227,23 +1246,25 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
     above = s.tv;
     inside = s.tn;
     if (!cmd.list) return 0;
-    uint32_t n = 0;
-    bool over = false;
+    uint32_t start[9] = {0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        start[k + 1] = start[k] + (k < ranks ? *peer(&sh.own_count, k) : 0);
+    const uint32_t n = start[8];
+    const bool over = n > kList;
+    if (!over)
 #pragma unroll 1
-    for (int k = 0; k < ranks && !over; ++k) {
-        const uint32_t m = *peer(&sh.own_count, k);
-        over = n + m > kList;
-        if (over) break;
-        const uint32_t* pk = peer(sh.own_key, k);
-        const uint32_t* pi = peer(sh.own_idx, k);
-        for (uint32_t i = threadIdx.x; i < m; i += kSearch) {
-            const uint32_t key = pk[i];
-            sh.key[n + i] = key;
-            sh.idx[n + i] = pi[i];
-            sh.w[n + i] = fixed_weight(key_value(key), r.ws, sh.table);
+        for (uint32_t i = threadIdx.x; i < n; i += kSearch) {
+            int k = 0;
+            uint32_t from = 0;
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                if (i >= start[j]) k = j, from = start[j];
+            const uint32_t key = peer(sh.own_key, k)[i - from];
+            sh.key[i] = key;
+            sh.idx[i] = peer(sh.own_idx, k)[i - from];
+            sh.w[i] = fixed_weight(key_value(key), r.ws, sh.table);
         }
-        n += m;
-    }
     if (threadIdx.x == 0) sh.n_list = over ? 0 : n;
     __syncthreads();
     return over ? 0xffffffffu : n;
@@ -1283,7 +1304,7 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
             P.ties = 0;
             up_w = list_w;
         } else if (cmd.list) {
-            const Selected at = list_select(false, left, sh);
+            const Selected at = list_select(false, left, cmd, sh);
             P.key = at.key;
             P.ties = left - at.n;
             up_w = at.w;
@@ -1312,7 +1333,7 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
             return false;
         }
         Selected at{cmd.klo, 0, 0};
-        if (cmd.list) at = list_select(true, need - above, sh);
+        if (cmd.list) at = list_select(true, need - above, cmd, sh);
         const u64 wt = fixed_weight(key_value(at.key), r.ws, sh.table);
         P.key = at.key;
         P.ties = wt == 0 ? 0 : (need - above - at.w + wt - 1) / wt;

@@ -65,17 +65,12 @@ __device__ __forceinline__ void scaled_distance(float x, const WeightScale& s, f
     tl = fmaf(dh, s.cl, fmaf(dl, s.ch, fmaf(dh, s.ch, -th)));
 }
 
-// table: the 1024 entries (shared memory).  x <= m, both finite or x = -inf.
-__device__ __forceinline__ unsigned long long fixed_weight(float x, const WeightScale& s,
-                                                           const unsigned long long* table) {
-    float th, tl;
-    scaled_distance(x, s, th, tl);
-    th = fminf(th, 63.f);                              // below half a unit from 62 on
-    const float big = th + 12288.f;                    // ulp 2^-10: rounds t to j / 1024
-    const int idx = __float_as_int(big) - __float_as_int(12288.f);
-    const float r = th - (big - 12288.f);              // exact, |r| <= 2^-11
-    // y = t - j / 1024 and a = y ln 2 by 2^41, |a| < 2^30 (a tl without meaning ends at w = 0)
-    const int y = __float2int_rn(r * 2199023255552.f) + __float2int_rn(tl * 2199023255552.f);
+// 2^bits 2^(-t) from t = th + tl split as th = k / 1024 + r (k = idx), |r| <= 2^-11
+__device__ __forceinline__ unsigned long long fixed_power(int idx, float r_scaled, float tl_scaled,
+                                                          const WeightScale& s,
+                                                          const unsigned long long* table) {
+    // y = t - k / 1024 and a = y ln 2 by 2^41, |a| < 2^30 (a tl without meaning ends at w = 0)
+    const int y = __float2int_rn(r_scaled) + __float2int_rn(tl_scaled);
     const int a = static_cast<int>((static_cast<long long>(y) * 1488522236 + (1LL << 30)) >> 31);
     const int a2 = __mulhi(a, a);                      // a^2 by 2^50
     const int a3 = __mulhi(a2, a);                     // a^3 by 2^59
@@ -86,6 +81,45 @@ __device__ __forceinline__ unsigned long long fixed_weight(float x, const Weight
     const int sh = min((idx >> 10) + s.shift, 64);     // 16 <= sh; w < 2^62 + 2^51
     return ((w >> (sh - 1)) + 1) >> 1;
 }
+
+constexpr float kTwo41 = 2199023255552.f;
+
+// table: the 1024 entries (shared memory).  x <= m, both finite or x = -inf.
+__device__ __forceinline__ unsigned long long fixed_weight(float x, const WeightScale& s,
+                                                           const unsigned long long* table) {
+    float th, tl;
+    scaled_distance(x, s, th, tl);
+    th = fminf(th, 63.f);                              // below half a unit from 62 on
+    const float big = th + 12288.f;                    // ulp 2^-10: rounds t to k / 1024
+    const float r = th - (big - 12288.f);              // exact
+    return fixed_power(__float_as_int(big) - __float_as_int(12288.f), r * kTwo41, tl * kTwo41, s,
+                       table);
+}
+
+#ifdef __CUDACC__
+// Two weights, the same values, with paired fp32 instructions.
+__device__ __forceinline__ void fixed_weights(float2 x, const WeightScale& s,
+                                              const unsigned long long* table,
+                                              unsigned long long& w0, unsigned long long& w1) {
+    const float2 m = make_float2(s.m, s.m), minus = make_float2(-1.f, -1.f);
+    const float2 dh = __ffma2_rn(x, minus, m);         // m - x, as rounded once
+    const float2 bb = __fadd2_rn(dh, make_float2(-s.m, -s.m));
+    const float2 dl = __fadd2_rn(__ffma2_rn(__ffma2_rn(bb, minus, dh), minus, m),
+                                 __ffma2_rn(x, minus, make_float2(-bb.x, -bb.y)));
+    const float2 ch = make_float2(s.ch, s.ch), cl = make_float2(s.cl, s.cl);
+    float2 th = __fmul2_rn(dh, ch);
+    const float2 tl = __ffma2_rn(
+        dh, cl, __ffma2_rn(dl, ch, __ffma2_rn(dh, ch, make_float2(-th.x, -th.y))));
+    th = make_float2(fminf(th.x, 63.f), fminf(th.y, 63.f));
+    const float2 big = __fadd2_rn(th, make_float2(12288.f, 12288.f));
+    const float2 r = __ffma2_rn(__fadd2_rn(big, make_float2(-12288.f, -12288.f)), minus, th);
+    const float2 up = make_float2(kTwo41, kTwo41);
+    const float2 rs = __fmul2_rn(r, up), ts = __fmul2_rn(tl, up);
+    constexpr int kZero = 0x46400000;                  // bits of 12288.f
+    w0 = fixed_power(__float_as_int(big.x) - kZero, rs.x, ts.x, s, table);
+    w1 = fixed_power(__float_as_int(big.y) - kZero, rs.y, ts.y, s, table);
+}
+#endif
 
 }  // namespace rlk
 
