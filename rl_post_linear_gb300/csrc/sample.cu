@@ -771,12 +771,11 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ----------------------------------------------------------------------------- search
 
-// A step that block 0 asks of all blocks.  Elements are above, inside or below a window:
-// bins [b1, b2] of the scaled distance from the maximum, and keys [klo, khi] in them.
+// A step that block 0 asks of all blocks.  Elements are above, inside or below a window of
+// values [key_value(klo), key_value(khi)].
 enum : int { kHist, kCollect, kDone };
 struct Cmd {
     int type;
-    int b1, b2;
     uint32_t klo, khi;
     int shift;        // kHist: bins of the keys, (khi - key) >> shift; -1: of the distance
     int by_weight;    // kHist: 12-bit weights instead of counts
@@ -814,34 +813,35 @@ __device__ __forceinline__ float distance(float x, const Row<T>& r) {
     return fminf((r.ws.m - x) * r.scale, 2.f * kBins);
 }
 
-// Whether an element is above or inside the window.
-template <typename T>
-__device__ __forceinline__ void classify(float x, const Row<T>& r, const Cmd& cmd, bool& up,
-                                         bool& in) {
-    const int b = static_cast<int>(distance(x, r));
-    const uint32_t k = order_key(x);
-    up = b < cmd.b1 || (b <= cmd.b2 && k > cmd.khi);
-    in = !up && b <= cmd.b2 && k >= cmd.klo && k > kKeyNegInf;
+// The window as values: above is x > hi, inside lo <= x <= hi.  With no window (khi at or
+// below -inf's key) all that is not -inf is above and nothing inside.
+__device__ __forceinline__ void window_of(const Cmd& cmd, float& lo, float& hi) {
+    const bool none = cmd.khi <= kKeyNegInf;
+    lo = none ? INFINITY : key_value(max(cmd.klo, kKeyNegInf + 1));
+    // the key between the negatives and 0 is no element's, but its value (-0) compares as 0
+    const uint32_t khi = cmd.khi == 0x7fffffffu ? 0x7ffffffeu : cmd.khi;
+    hi = none ? -INFINITY : khi > order_key(INFINITY) ? INFINITY : key_value(khi);
 }
 
 // Histogram of the window; for windows of keys also the exact weight above it.
 template <typename T>
-__device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const float* cmax,
+__device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, const float* cmax,
                                        Shared& sh) {
+    const Row<T> r = row;                    // in registers for the loops
+    const Cmd cmd = command;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kBins; i += kSearch) sh.hist[i] = 0;
     if (threadIdx.x == 0) sh.own_above = sh.own_total = 0;
     __syncthreads();
     const float unit = kRange / kBins;
     const float x_hi = key_value(cmd.khi);
+    float lo, hi;
+    window_of(cmd, lo, hi);
     u64 above = 0, all = 0;
 #pragma unroll 1
     for (int i = warp; i < r.mine; i += kSearch / 32) {
         const float top = cmax[r.first + i];
-        const int top_bin = static_cast<int>(distance(top, r));
-        if (top_bin >= kBins || (!cmd.total && (top_bin > cmd.b2 ||
-                                                (cmd.shift >= 0 && order_key(top) < cmd.klo))))
-            continue;
+        if (distance(top, r) >= kBins || (cmd.shift >= 0 && !cmd.total && top < lo)) continue;
         Chunk<T> c;
         c.load(r.x, r.V, r.first + i, lane, r.vec);
         if (cmd.shift < 0) {
@@ -863,15 +863,13 @@ __device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const fl
                 fixed_weights(make_float2(x[0], x[1]), r.ws, sh.table, w[0], w[1]);
                 fixed_weights(make_float2(x[2], x[3]), r.ws, sh.table, w[2], w[3]);
             }
+            all += (w[0] + w[1]) + (w[2] + w[3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                bool up, in;
-                classify(x[e], r, cmd, up, in);
-                all += w[e];
-                above += up ? w[e] : 0;
+                above += x[e] > hi ? w[e] : 0;
                 const float q =
                     cmd.by_weight ? rintf(4096.f * ex2_approx((x[e] - x_hi) * r.ws.ch)) : 1.f;
-                if (in)
+                if (x[e] >= lo && x[e] <= hi)
                     atomicAdd(&sh.hist[(cmd.khi - order_key(x[e])) >> cmd.shift],
                               static_cast<uint32_t>(q));
             }
@@ -886,22 +884,26 @@ __device__ __noinline__ void step_hist(const Row<T>& r, const Cmd& cmd, const fl
 
 // Exact weight above the window, per chunk, and the elements inside it.
 template <typename T>
-__device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const float* cmax,
+__device__ __noinline__ void step_collect(const Row<T>& row, const Cmd& command, const float* cmax,
                                           u64* own_w, uint32_t* own_n, Shared& sh) {
+    const Row<T> r = row;                    // in registers for the loops
+    const Cmd cmd = command;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) sh.own_count = 0, sh.own_total = 0;
     __syncthreads();
+    float lo, hi;
+    window_of(cmd, lo, hi);
+    const bool everything = hi == -INFINITY;
     u64 all = 0;
 #pragma unroll 1
     for (int i = warp; i < r.mine; i += kSearch / 32) {
         const float top = cmax[r.first + i];
-        const int top_bin = static_cast<int>(distance(top, r));
         u64 w = 0;
         uint32_t n = 0;
-        const bool near = top_bin <= cmd.b2 && order_key(top) >= cmd.klo;
-        if (near || (cmd.total && top_bin < kBins)) {
+        if (top >= lo || ((cmd.total || everything) && distance(top, r) < kBins)) {
             Chunk<T> c;
             c.load(r.x, r.V, r.first + i, lane, r.vec);
+            u64 sum = 0;
 #pragma unroll 1
             for (int j = 0; j < Chunk<T>::kQuads; ++j) {
                 float x[4];
@@ -909,17 +911,14 @@ __device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const
                 c.take(x);
                 fixed_weights(make_float2(x[0], x[1]), r.ws, sh.table, we[0], we[1]);
                 fixed_weights(make_float2(x[2], x[3]), r.ws, sh.table, we[2], we[3]);
+                sum += (we[0] + we[1]) + (we[2] + we[3]);
+                if (everything) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    bool up, in;
-                    classify(x[e], r, cmd, up, in);
-                    all += we[e];
-                    w += up ? we[e] : 0;
-                    if (!in) continue;
-                    if (cmd.list == 0) {
-                        ++n;
-                        continue;
-                    }
+                    w += x[e] > hi ? we[e] : 0;
+                    if (!(x[e] >= lo && x[e] <= hi)) continue;
+                    ++n;
+                    if (!cmd.list) continue;
                     const uint32_t at = atomicAdd(&sh.own_count, 1u);
                     if (at < kList) {
                         const int v = j * 4 + e;
@@ -929,8 +928,9 @@ __device__ __noinline__ void step_collect(const Row<T>& r, const Cmd& cmd, const
                     }
                 }
             }
-            w = warp_sum(w);
-            n = __reduce_add_sync(0xffffffffu, n);
+            all += sum;
+            w = warp_sum(everything ? sum : w);
+            n = cmd.list ? 0 : __reduce_add_sync(0xffffffffu, n);
         }
         if (lane == 0) own_w[i] = w, own_n[i] = n;
     }
@@ -1008,11 +1008,11 @@ struct Search {
 };
 
 __device__ __forceinline__ Cmd make_hist0(bool by_weight) {
-    return Cmd{kHist, 0, kBins - 1, 0u, 0xffffffffu, -1, by_weight ? 1 : 0, 0, 0};
+    return Cmd{kHist, 0u, 0xffffffffu, -1, by_weight ? 1 : 0, 0, 0};
 }
 // exact weights above a key, and the number of elements equal to it
 __device__ __forceinline__ Cmd make_above(uint32_t key) {
-    return Cmd{kCollect, 0, 2 * kBins, key, key, 0, 0, 0, 0};
+    return Cmd{kCollect, key, key, 0, 0, 0, 0};
 }
 
 // the boundary is known up to min_p: the last step
@@ -1042,6 +1042,23 @@ __device__ __forceinline__ void take_total(Search& P, const Cmd& cmd, int ranks,
     for (int k = 0; k < 8; ++k) t += k < ranks ? *peer(&sh.own_total, k) : 0;
     P.exact = true;
     P.s_lo = P.s_hi = P.all = t;
+}
+
+// The lowest key in [lo, hi] whose value lies in bin `bin` or above; hi's does.  One warp, 32
+// trials at a time.
+template <typename T>
+__device__ __noinline__ uint32_t first_key(const Row<T>& r, uint32_t lo, uint32_t hi, int bin) {
+    const uint32_t lane = threadIdx.x & 31;
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 32 + 1;
+        const uint32_t k = min(hi, lo + step * lane);
+        const bool in = static_cast<int>(distance(key_value(k), r)) <= bin;
+        const int first = __ffs(__ballot_sync(0xffffffffu, in)) - 1;
+        if (first == 0) return lo;
+        if (first > 0) hi = min(hi, lo + step * first);
+        lo = min(hi, lo + step * ((first < 0 ? 32 : first) - 1) + 1);
+    }
+    return hi;
 }
 
 // Narrows the window from the cluster's histograms and asks for the next step.
@@ -1148,14 +1165,18 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     }
     if (P.want_k) P.n_above += skipped;
     if (!keys) {
-        cmd.b1 = j1;
-        cmd.b2 = j2;
-        // keys that surely span these bins
-        const float m = r.ws.m, pad = fabsf(m) * 4.8e-7f + 1e-37f;
-        const float lo = m - ((j2 + 1) / r.scale * 1.000001f + pad);
-        const float hi = m - (j1 / r.scale * 0.999999f - pad);
-        cmd.klo = max(kKeyNegInf + 1, order_key(fmaxf(lo, -3.402823466e38f)) - 1);
-        cmd.khi = min(order_key(m), order_key(fminf(hi, 3.402823466e38f)) + 1);
+        // the keys of exactly these bins: the lowest of bin j2 or above, and the highest of
+        // bin j1 or below
+        if (threadIdx.x < 32) {
+            const uint32_t lo = first_key(r, kKeyNegInf + 1, order_key(r.ws.m), j2);
+            const uint32_t hi = j1 == 0 ? order_key(r.ws.m)
+                                        : first_key(r, lo, order_key(r.ws.m), j1 - 1) - 1;
+            if (threadIdx.x == 0) sh.at = static_cast<int>(lo), sh.at2 = static_cast<int>(hi);
+        }
+        __syncthreads();
+        cmd.klo = static_cast<uint32_t>(sh.at);
+        cmd.khi = static_cast<uint32_t>(sh.at2);
+        __syncthreads();
     } else {
         const int64_t hi = int64_t(cmd.khi) - (int64_t(j1) << cmd.shift);
         const int64_t lo = int64_t(cmd.khi) - (int64_t(j2 + 1) << cmd.shift) + 1;
@@ -1401,7 +1422,7 @@ __global__ void __launch_bounds__(kSearch, 2)
     if (!P.want_k && !P.want_p) {
         ask_draw(P, cmd);
     } else if (a.V <= kList) {           // the whole row fits the list
-        cmd = Cmd{kCollect, 0, 2 * kBins, kKeyNegInf + 1, 0xffffffffu, 0, 0, 1, 0};
+        cmd = Cmd{kCollect, kKeyNegInf + 1, 0xffffffffu, 0, 0, 1, 0};
     } else {
         cmd = make_hist0(!P.want_k);
     }

@@ -78,8 +78,8 @@ __device__ __forceinline__ unsigned long long fixed_power(int idx, float r_scale
     const unsigned long long t62 = table[idx & (kExpEntries - 1)];
     const unsigned long long w =
         t62 - ((static_cast<long long>(q) * static_cast<int>(t62 >> 32)) >> 9);
-    const int sh = min((idx >> 10) + s.shift, 64);     // 16 <= sh; w < 2^62 + 2^51
-    return ((w >> (sh - 1)) + 1) >> 1;
+    const int sh = min((idx >> 10) + s.shift - 1, 63);     // 15 <= sh; w < 2^62 + 2^51
+    return ((w >> sh) + 1) >> 1;
 }
 
 constexpr float kTwo41 = 2199023255552.f;
