@@ -60,7 +60,8 @@ constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
 constexpr int kList = 1024;              // elements of the search's list
-constexpr int kShort = 512;              // of the scan's list, sorted in place
+constexpr int kShort = 1024;             // of the scan's list, sorted in place
+constexpr int kMaxSegments = 8192;       // of a row whose truncation the scan tries itself
 constexpr float kRange = 48.f;           // weights below 2^-47 round to 0 (bits <= 46)
 constexpr int kMaxSteps = 32;            // far more than any row takes
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
@@ -179,12 +180,31 @@ __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_
 
 // ----------------------------------------------------------------------------- rows
 
+// 16 bytes of a row from column c on, -inf past its end.
+template <typename T>
+__device__ __forceinline__ uint4 load_group(const T* row, int V, int c, bool vec) {
+    constexpr int VEC = 16 / sizeof(T);
+    if (vec && c + VEC <= V) return __ldg(reinterpret_cast<const uint4*>(row + c));
+    T v[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = c + e < V ? row[c + e] : T(-INFINITY);
+    return *reinterpret_cast<const uint4*>(v);
+}
+template <typename T>
+__device__ __forceinline__ float group_value(const uint4& g, int i) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(&g);
+    if (sizeof(T) == 4) return __uint_as_float(p[i]);
+    return __uint_as_float((i & 1) ? (p[i / 2] & 0xffff0000u) : (p[i / 2] << 16));
+}
+
 // The 16 columns that a lane holds of a chunk, as they lie in memory: LOADS groups of VEC
 // consecutive ones, group j of lane l at column (32 j + l) VEC of the chunk.
 template <typename T>
 struct Chunk {
     static constexpr int VEC = 16 / sizeof(T);
     static constexpr int LOADS = kLane / VEC;
+    // columns of a segment: what one load of the warp covers
+    static constexpr int SEG = 32 * VEC;
     uint4 raw[LOADS];
 
     __device__ __forceinline__ static int column(int chunk, int j, int lane) {
@@ -192,17 +212,7 @@ struct Chunk {
     }
     __device__ __forceinline__ void load(const T* row, int V, int chunk, int lane, bool vec) {
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
-            const int c = column(chunk, j, lane);
-            if (vec && c + VEC <= V) {
-                raw[j] = __ldg(reinterpret_cast<const uint4*>(row + c));
-            } else {
-                T v[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[e] = c + e < V ? row[c + e] : T(-INFINITY);
-                raw[j] = *reinterpret_cast<const uint4*>(v);
-            }
-        }
+        for (int j = 0; j < LOADS; ++j) raw[j] = load_group(row, V, column(chunk, j, lane), vec);
     }
     // Four elements at a time, for loops whose code is better short: the first four, and the
     // others moved up.
@@ -216,9 +226,7 @@ struct Chunk {
         for (int w = 0; w + kStep < kWords; ++w) p[w] = p[w + kStep];
     }
     __device__ __forceinline__ float get(int i) const {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(raw);
-        if (sizeof(T) == 4) return __uint_as_float(p[i]);
-        return __uint_as_float((i & 1) ? (p[i / 2] & 0xffff0000u) : (p[i / 2] << 16));
+        return group_value<T>(raw[i / VEC], i % VEC);
     }
 };
 
@@ -363,30 +371,47 @@ struct Shared0 {
     int at;
 };
 
-// Workspace: a header a row, then the chunks' maxima and sums.
+// Workspace: a header a row, then the chunks' maxima and sums, then the segments' maxima
+// (room for them as if logits were fp32).
 enum : uint32_t { kRowDone, kRowSearch };
 struct RowHeader {
     u64 all;                             // fast total of the weights
     float m;                             // maximum
     uint32_t mode;
 };
+constexpr int kSegsPerChunk = kChunk / 128;
 __host__ __device__ constexpr size_t stats_offset(int64_t N) {
     return (size_t(N) * sizeof(RowHeader) + 255) / 256 * 256;
+}
+__host__ __device__ constexpr size_t segs_offset(int64_t N, int nch) {
+    return (stats_offset(N) + size_t(N) * nch * sizeof(float2) + 255) / 256 * 256;
 }
 __device__ __forceinline__ float2* row_stats(const SampleArgs& a, int64_t row, int nch) {
     return reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + stats_offset(a.N)) +
            row * nch;
 }
+__device__ __forceinline__ float* row_segs(const SampleArgs& a, int64_t row, int nch) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + segs_offset(a.N, nch)) +
+           row * nch * kSegsPerChunk;
+}
 
 // Maximum and sum of a chunk.  The sum of 2^((x - max) c) leaves out one element of the
 // maximum (and has its sign bit set) where the chunk may hold the row's maximum: a total is
 // a sum of such parts plus the maximum's own weight.
-template <typename T>
-__device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float& best) {
-    float ml = c.get(0);
+template <bool SEGMENTS, typename T>
+__device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float& best,
+                                              float (&seg)[Chunk<T>::LOADS]) {
+    constexpr int VEC = Chunk<T>::VEC, LOADS = Chunk<T>::LOADS;
+    float ml = -INFINITY, m = -INFINITY;
 #pragma unroll
-    for (int e = 1; e < kLane; ++e) ml = fmaxf(ml, c.get(e));
-    const float m = warp_max(ml);
+    for (int j = 0; j < LOADS; ++j) {
+        float v = c.get(j * VEC);
+#pragma unroll
+        for (int e = 1; e < VEC; ++e) v = fmaxf(v, c.get(j * VEC + e));
+        ml = fmaxf(ml, v);
+        if (SEGMENTS) m = fmaxf(m, seg[j] = warp_max(v));
+    }
+    if (!SEGMENTS) m = warp_max(ml);
     // a chunk of -inf has sum 0; NaN or +inf make it NaN
     const float mm = fmaxf(m, -3.402823466e38f);
     float s[kLane];
@@ -453,13 +478,13 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
     return sh.flag != 0;
 }
 
-// A value that enough chunk maxima reach: at least `count` of them, or (need > 0) maxima of
+// A value that enough segment maxima reach: at least `count` of them, or (need > 0) maxima of
 // a weight of at least `need`.  Between the maximum and `low`, by bisection with a warp a
 // trial: 3 rounds leave 1/729 of the range.  `low` itself if that is not enough, with
 // found = false.
 template <typename T>
-__device__ float reach_value(const Row<T>& r, const float* cmax, int count, float need, float low,
-                             bool& found, Shared0& sh) {
+__device__ float reach_value(const Row<T>& r, const float* smax, int nseg, int count, float need,
+                             float low, bool& found, Shared0& sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float hi = r.ws.m, lo = low;
     found = true;
@@ -470,11 +495,22 @@ __device__ float reach_value(const Row<T>& r, const float* cmax, int count, floa
         const float x = round == 0 && warp == kWarps - 1 ? low : hi - step * (warp + 1);
         int n = 0;
         float w = 0.f;
-#pragma unroll 4
-        for (int c = lane; c < r.nch; c += 32) {
-            const float v = cmax[c];
-            n += v >= x ? 1 : 0;
-            w += v >= x ? ex2_approx((v - r.ws.m) * r.ws.ch) : 0.f;
+        if (need > 0.f) {
+#pragma unroll 1
+            for (int c = lane * 4; c < nseg; c += 128) {
+                const float4 v = *reinterpret_cast<const float4*>(smax + c);
+                w += v.x >= x ? ex2_approx((v.x - r.ws.m) * r.ws.ch) : 0.f;
+                w += v.y >= x ? ex2_approx((v.y - r.ws.m) * r.ws.ch) : 0.f;
+                w += v.z >= x ? ex2_approx((v.z - r.ws.m) * r.ws.ch) : 0.f;
+                w += v.w >= x ? ex2_approx((v.w - r.ws.m) * r.ws.ch) : 0.f;
+            }
+        } else {
+#pragma unroll 2
+            for (int c = lane * 4; c < nseg; c += 128) {
+                const float4 v = *reinterpret_cast<const float4*>(smax + c);
+                n += (v.x >= x ? 1 : 0) + (v.y >= x ? 1 : 0) + (v.z >= x ? 1 : 0) +
+                     (v.w >= x ? 1 : 0);
+            }
         }
         const bool enough =
             need > 0.f ? warp_sum(w) >= need : __reduce_add_sync(0xffffffffu, n) >= count;
@@ -532,8 +568,8 @@ __device__ __noinline__ void sort_list(uint32_t n, u64* order, u64* w) {
 
 // Draws from the elements at or above a value, if they settle the boundary and are few.
 template <typename T>
-__device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax, uint16_t* ids,
-                           u64 all, const SampleArgs& a, int64_t row_i, Shared0& sh) {
+__device__ bool short_draw(const Row<T>& r, const Settings& s, const float* smax, uint16_t* ids,
+                           int nseg, u64 all, const SampleArgs& a, int64_t row_i, Shared0& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         sh.n_list = 0, sh.n_ids = 0;
@@ -544,7 +580,8 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     const bool by_m = s.want_m && !(s.want_k && s.want_p);
     uint32_t tau = kKeyNegInf + 1;
     if (r.V > kShort && (s.want_k || s.want_p) && !(by_m && s.want_p)) {
-        const bool few = s.want_k && s.top_k <= r.nch * 9 / 10;
+        // a list of about -nseg log(1 - top_k / nseg) elements, if the row is in no order
+        const bool few = s.want_k && s.top_k <= nseg / 2;
         if (s.want_k && !few && !by_m) return false;
         // between the maximum and what weighs nothing
         const float low = fmaxf(r.ws.m - 47.5f / r.ws.ch, -3.402823466e38f);
@@ -552,8 +589,8 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
                            __uint_as_float(uint32_t(127 - r.bits) << 23);
         if (few || !s.want_k) {
             bool found;
-            const float x = reach_value(r, cmax, static_cast<int>(s.top_k), s.want_k ? 0.f : need,
-                                        low, found, sh);
+            const float x = reach_value(r, smax, nseg, static_cast<int>(s.top_k),
+                                        s.want_k ? 0.f : need, low, found, sh);
             if (!found && !s.want_k) return false;   // a wide nucleus
             tau = max(tau, order_key(x));
         }
@@ -562,35 +599,41 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
     const uint32_t key_m = sh.key_m;
     if (by_m) tau = max(tau, key_m);
     const float tau_x = key_value(tau);
-    for (int c = tid; c < r.nch; c += kThreads)
-        if (cmax[c] >= tau_x) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
+    for (int c = tid; c < nseg; c += kThreads)
+        if (smax[c] >= tau_x) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
     __syncthreads();
     const int n_ids = sh.n_ids;
-    constexpr int kAhead = sizeof(T) == 4 ? 3 : 4;
+    constexpr int VEC = Chunk<T>::VEC, SEG = Chunk<T>::SEG, kAhead = 8;
 #pragma unroll 1
     for (int i0 = warp; i0 < n_ids; i0 += kAhead * kWarps) {
-        Chunk<T> ch[kAhead];
+        uint4 raw[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
             const int i = i0 + q * kWarps;
-            if (i < n_ids) ch[q].load(r.x, r.V, ids[i], lane, r.vec);
+            if (i < n_ids) raw[q] = load_group(r.x, r.V, ids[i] * SEG + lane * VEC, r.vec);
         }
+        // bit q VEC + e: element e of group q
+        u64 hits = 0;
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * kWarps;
-            if (i >= n_ids) break;
-            uint32_t hits = 0;
+        for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-            for (int e = 0; e < kLane; ++e) hits |= (ch[q].get(e) >= tau_x ? 1u : 0u) << e;
+            for (int e = 0; e < VEC; ++e)
+                hits |= u64(i0 + q * kWarps < n_ids && group_value<T>(raw[q], e) >= tau_x ? 1 : 0)
+                        << (q * VEC + e);
+        const uint32_t mine = __popcll(hits);
+        uint32_t at = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, at, off);
+            if (lane >= off) at += o;
+        }
+        uint32_t first = 0;
+        if (lane == 31) first = atomicAdd(&sh.n_list, at);
+        at += __shfl_sync(0xffffffffu, first, 31) - mine;
 #pragma unroll 1
-            while (hits != 0) {
-                const int e = __ffs(hits) - 1;
-                hits &= hits - 1;
-                const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                if (at < kShort)
-                    sh.order[at] = Chunk<T>::column(ids[i], e / Chunk<T>::VEC, lane) +
-                                   e % Chunk<T>::VEC;
-            }
+        for (; hits != 0; hits &= hits - 1, ++at) {
+            const int e = __ffsll(hits) - 1;
+            if (at < kShort) sh.order[at] = ids[i0 + e / VEC * kWarps] * SEG + lane * VEC + e % VEC;
         }
     }
     __syncthreads();
@@ -604,17 +647,23 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
         sh.w[i] = fixed_weight(x, r.ws, sh.table);
     }
     sort_list(n, sh.order, sh.w);
-    // thread t holds elements 2 t and 2 t + 1 of the order
-    const uint32_t i0 = 2 * tid, i1 = i0 + 1;
-    const u64 w0 = i0 < n ? sh.w[i0] : 0, w1 = i1 < n ? sh.w[i1] : 0;
-    const Scanned sum = block_scan<kThreads>(w0 + w1, 0, sh.part, sh.part_n);
-    const u64 b0 = sum.v, b1 = b0 + w0;
+    // thread t holds elements 4 t .. 4 t + 3 of the order
+    constexpr int kPer = kShort / kThreads;
+    const uint32_t i0 = kPer * tid;
+    u64 w[kPer], b[kPer + 1], mine = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) w[q] = i0 + q < n ? sh.w[i0 + q] : 0, mine += w[q];
+    const Scanned sum = block_scan<kThreads>(mine, 0, sh.part, sh.part_n);
+    b[0] = sum.v;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) b[q + 1] = b[q] + w[q];
     uint32_t keep = n;
     u64 s_k = sum.tv;                                // fewer elements than top_k: all of them
     if (s.want_k && static_cast<u64>(s.top_k) < n) {
         keep = static_cast<uint32_t>(s.top_k);
-        if (keep - 1 == i0) sh.at_w = b1;
-        if (keep - 1 == i1) sh.at_w = b1 + w1;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            if (keep - 1 == i0 + q) sh.at_w = b[q + 1];
         __syncthreads();
         s_k = sh.at_w;
     }
@@ -626,44 +675,60 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* cmax
         const u64 need_hi = whole ? need_lo : max(u64(1), part_of(s.top_p, hi, true));
         if (need_hi > sum.tv && !by_m) return false;
         // the order's first elements before whose sum the need is not reached
-        const uint32_t n_lo = __syncthreads_count(i0 < n && b0 < need_lo) +
-                              __syncthreads_count(i1 < n && b1 < need_lo);
-        const uint32_t n_hi = whole ? n_lo : __syncthreads_count(i0 < n && b0 < need_hi) +
-                                                 __syncthreads_count(i1 < n && b1 < need_hi);
-        if (n_lo != n_hi) return false;              // the total's error matters
-        keep = min(keep, n_lo);
+        uint32_t n_lo = 0, n_hi = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            n_lo += i0 + q < n && b[q] < need_lo ? 1u : 0u;
+            n_hi += i0 + q < n && b[q] < need_hi ? 1u : 0u;
+        }
+        const Scanned c = block_scan<kThreads>(n_hi, n_lo, sh.part, sh.part_n);
+        if (c.tn != c.tv) return false;              // the total's error matters
+        keep = min(keep, c.tn);
     }
     if (s.want_m) {
         const u64 cut = u64(key_m) << 32;
-        const uint32_t n_m = __syncthreads_count(i0 < n && sh.order[i0] >= cut) +
-                             __syncthreads_count(i1 < n && sh.order[i1] >= cut);
-        keep = min(keep, n_m);
+        uint32_t n_m = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) n_m += i0 + q < n && sh.order[i0 + q] >= cut ? 1u : 0u;
+        keep = min(keep, block_scan<kThreads>(0, n_m, sh.part, sh.part_n).tn);
     }
-    if (keep - 1 == i0) sh.at_w = b1;
-    if (keep - 1 == i1) sh.at_w = b1 + w1;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+        if (keep - 1 == i0 + q) sh.at_w = b[q + 1];
     // the kept elements by index: their order words become (~index, key)
     __syncthreads();
     const u64 kept = sh.at_w;
     const u64 target = part_of(s.u, kept, false);
-    const u64 o0 = sh.order[i0], o1 = sh.order[i1];
-    __syncthreads();
-    if (i0 < keep) sh.order[i0] = (o0 << 32) | (o0 >> 32);
-    if (i1 < keep) sh.order[i1] = (o1 << 32) | (o1 >> 32);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+        if (i0 + q < keep) {
+            const u64 o = sh.order[i0 + q];
+            sh.order[i0 + q] = (o << 32) | (o >> 32);
+        }
     __syncthreads();
     sort_list(keep, sh.order, sh.w);
-    const u64 v0 = i0 < keep ? sh.w[i0] : 0, v1 = i1 < keep ? sh.w[i1] : 0;
-    const u64 c0 = block_scan<kThreads>(v0 + v1, 0, sh.part, sh.part_n).v, c1 = c0 + v0;
-    const bool hit0 = c0 <= target && target < c1, hit1 = c1 <= target && target < c1 + v1;
-    if (hit0 || hit1) {
-        const u64 o = sh.order[hit0 ? i0 : i1];
-        write_drawn(a, row_i, int(0xffffffffu - uint32_t(o >> 32)), key_value(uint32_t(o)), r.ws,
-                    max(all, kept), kept);
+    mine = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) w[q] = i0 + q < keep ? sh.w[i0 + q] : 0, mine += w[q];
+    u64 run = block_scan<kThreads>(mine, 0, sh.part, sh.part_n).v;
+    u64 drawn = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        if (run <= target && target < run + w[q]) drawn = sh.order[i0 + q];
+        run += w[q];
     }
+    if (drawn != 0)
+        write_drawn(a, row_i, int(0xffffffffu - uint32_t(drawn >> 32)),
+                    key_value(uint32_t(drawn)), r.ws, max(all, kept), kept);
     return true;
 }
 
-__host__ __device__ constexpr size_t scan_smem(int nch) {
-    return sizeof(Shared0) + size_t(nch) * 14 + 16;
+__host__ __device__ constexpr int segments_of(int nch, size_t esize) {
+    const int n = nch * (esize == 4 ? 4 : 2);
+    return n <= kMaxSegments ? n : 0;
+}
+__host__ __device__ constexpr size_t scan_smem(int nch, size_t esize) {
+    return sizeof(Shared0) + size_t(nch) * 12 + size_t(segments_of(nch, esize)) * 6 + 64;
 }
 
 template <typename T>
@@ -674,7 +739,9 @@ __global__ void __launch_bounds__(kThreads, 4)
     Shared0& sh = *reinterpret_cast<Shared0*>(smem);
     u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared0));
     float* cmax = reinterpret_cast<float*>(cw + nch);
-    uint16_t* ids = reinterpret_cast<uint16_t*>(cmax + nch);
+    const int nseg = segments_of(nch, sizeof(T));    // 0: too many to be kept
+    float* smax = reinterpret_cast<float*>(cw) + (nch * 3 + 3) / 4 * 4;
+    uint16_t* ids = reinterpret_cast<uint16_t*>(smax + (nseg + 3) / 4 * 4);
     const int64_t row_i = blockIdx.x / ranks;
     const int rank = blockIdx.x % ranks;             // = the block's rank in its cluster
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -702,6 +769,8 @@ __global__ void __launch_bounds__(kThreads, 4)
                              smem_u32(sh.table + 2 * i)),
                          "l"(kExpTable.v + 2 * i)
                          : "memory");
+    const bool cut = s.want_k || s.want_p || s.want_m;
+    float* segs = row_segs(a, row_i, nch);
     float best = -INFINITY;
     constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
 #pragma unroll 1
@@ -716,8 +785,19 @@ __global__ void __launch_bounds__(kThreads, 4)
         for (int q = 0; q < kAhead; ++q) {
             const int i = i0 + q * kWarps;
             if (i >= r.mine) break;
-            const float2 st = chunk_stats(c[q], r.ws.ch, best);
-            if (lane == 0) stats[r.first + i] = st;
+            float seg[Chunk<T>::LOADS];
+            if (cut) {
+                const float2 st = chunk_stats<true>(c[q], r.ws.ch, best, seg);
+                if (lane == 0) {
+                    stats[r.first + i] = st;
+#pragma unroll
+                    for (int j = 0; j < Chunk<T>::LOADS; ++j)
+                        segs[(r.first + i) * Chunk<T>::LOADS + j] = seg[j];
+                }
+            } else {
+                const float2 st = chunk_stats<false>(c[q], r.ws.ch, best, seg);
+                if (lane == 0) stats[r.first + i] = st;
+            }
         }
     }
     // the other blocks are done once their part is out
@@ -736,6 +816,16 @@ __global__ void __launch_bounds__(kThreads, 4)
         cw[i] = __float_as_uint(st.y);
         m = fmaxf(m, st.x);
         bad |= st.y != st.y;
+    }
+    if (cut) {                               // padded to whole groups of 4 with -inf
+#pragma unroll 2
+        for (int i = tid * 4; i < nseg; i += kThreads * 4) {
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (i + 3 < nseg) v = *reinterpret_cast<const float4*>(segs + i);
+            else v.x = segs[i], v.y = i + 1 < nseg ? segs[i + 1] : -INFINITY,
+                 v.z = i + 2 < nseg ? segs[i + 2] : -INFINITY;
+            *reinterpret_cast<float4*>(smax + i) = v;
+        }
     }
     m = warp_max(m);
     if (lane == 0) sh.part_n[warp] = __float_as_uint(m);
@@ -759,9 +849,8 @@ __global__ void __launch_bounds__(kThreads, 4)
         mine += w;
     }
     const u64 all = block_scan<kThreads>(mine, 0, sh.part, sh.part_n).tv;   // its barriers publish cw
-    const bool done = s.want_k || s.want_p || s.want_m
-                          ? short_draw(r, s, cmax, ids, all, a, row_i, sh)
-                          : fast_draw(r, cmax, cw, all, s, a, row_i, sh);
+    const bool done = !cut ? fast_draw(r, cmax, cw, all, s, a, row_i, sh)
+                           : nseg > 0 && short_draw(r, s, smax, ids, nseg, all, a, row_i, sh);
     if (tid == 0) {
         head->all = all;
         head->m = m;
@@ -1249,7 +1338,7 @@ __device__ __noinline__ void search_draw(const Row<T>& r, const Search& P, const
 // `inside`.  Returns the list's length, 0xffffffff if it does not fit.
 template <typename T>
 __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw, uint32_t* cn,
-                                       u64* own_w, uint32_t* own_n, int ranks, u64& above,
+                                       u64* own_w, uint32_t* own_n, int ranks, bool draws, u64& above,
                                        uint32_t& inside, Shared& sh) {
     u64 mine = 0;
     uint32_t n_mine = 0;
@@ -1262,6 +1351,10 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
         cn[c] = n;
         mine += w;
         n_mine += n;
+    }
+    if (draws) {
+        __syncthreads();
+        return 0;
     }
     const Scanned s = block_scan<kSearch>(mine, n_mine, sh.part, sh.part_n);
     above = s.tv;
@@ -1297,9 +1390,9 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
                                            uint32_t* cn, u64* own_w, uint32_t* own_n, int ranks,
                                            const SampleArgs& a, int64_t row_i, SampleFraction u,
                                            Shared& sh) {
-    u64 above;
-    uint32_t inside;
-    const uint32_t n = merge(r, cmd, cw, cn, own_w, own_n, ranks, above, inside, sh);
+    u64 above = 0;
+    uint32_t inside = 0;
+    const uint32_t n = merge(r, cmd, cw, cn, own_w, own_n, ranks, P.draw, above, inside, sh);
     if (P.draw) {
         search_draw(r, P, cmd, cw, cn, a, row_i, u, sh);
         return true;
@@ -1491,7 +1584,7 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, kThreads,
-                                scan_smem(nch), false, stream);
+                                scan_smem(nch, sizeof(T)), false, stream);
     if (e != cudaSuccess) return e;
     return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, kSearch,
                        search_smem(nch, (nch + ranks - 1) / ranks), true, stream);
@@ -1500,7 +1593,8 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
 }  // namespace
 
 size_t sample_workspace(int64_t N, int64_t V) {
-    return stats_offset(N) + size_t(N) * size_t((V + kChunk - 1) / kChunk) * sizeof(float2);
+    const int nch = static_cast<int>((V + kChunk - 1) / kChunk);
+    return segs_offset(N, nch) + size_t(N) * nch * kSegsPerChunk * sizeof(float);
 }
 
 cudaError_t launch_sample(const void* logits, bool bf16, const SampleArgs& args,
