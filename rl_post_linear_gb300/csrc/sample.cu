@@ -59,7 +59,8 @@ constexpr int kSearch = 512;             // of a search block
 constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
-constexpr int kList = 1024;              // elements of the search's list
+constexpr int kSelect = 1024;            // bins of the selection in it
+constexpr int kList = 1920;              // elements of the search's list
 constexpr int kShort = 1024;             // of the scan's list, sorted in place
 constexpr int kMaxSegments = 8192;       // of a row whose truncation the scan tries itself
 constexpr float kRange = 48.f;           // weights below 2^-47 round to 0 (bits <= 46)
@@ -155,10 +156,11 @@ struct Scanned {
 };
 template <int THREADS>
 __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_t* part_n) {
+    constexpr int kParts = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     u64 iv = v;
     uint32_t in = n;
-#pragma unroll 1
+#pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const u64 ov = __shfl_up_sync(0xffffffffu, iv, off);
         const uint32_t on = __shfl_up_sync(0xffffffffu, in, off);
@@ -167,14 +169,22 @@ __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_
     __syncthreads();
     if (lane == 31) part[warp] = iv, part_n[warp] = in;
     __syncthreads();
-    Scanned r{0, 0, 0, 0};
+    // every warp scans the warps' sums for itself
+    u64 pv = lane < kParts ? part[lane] : 0;
+    uint32_t pn = lane < kParts ? part_n[lane] : 0;
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i == warp) r.v = r.tv, r.n = r.tn;
-        r.tv += part[i], r.tn += part_n[i];
+    for (int off = 1; off < kParts; off <<= 1) {
+        const u64 ov = __shfl_up_sync(0xffffffffu, pv, off);
+        const uint32_t on = __shfl_up_sync(0xffffffffu, pn, off);
+        if (lane >= off) pv += ov, pn += on;
     }
-    r.v += iv - v;
-    r.n += in - n;
+    Scanned r;
+    r.tv = __shfl_sync(0xffffffffu, pv, kParts - 1);
+    r.tn = __shfl_sync(0xffffffffu, pn, kParts - 1);
+    const u64 bv = __shfl_sync(0xffffffffu, pv, warp - 1);
+    const uint32_t bn = __shfl_sync(0xffffffffu, pn, warp - 1);
+    r.v = (warp == 0 ? 0 : bv) + iv - v;
+    r.n = (warp == 0 ? 0 : bn) + in - n;
     return r;
 }
 
@@ -875,15 +885,16 @@ struct Cmd {
 // Shared memory of the search.
 struct Shared {
     u64 table[kExpEntries];
-    u64 w[kList];                        // block 0: the merged list
-    uint32_t key[kList], idx[kList];
+    uint32_t key[kList], idx[kList];     // block 0: the merged list
     union {                              // of one step or the other
         uint32_t hist[kBins];
         struct {
             uint32_t own_key[kList], own_idx[kList];   // this block's part of the list
         };
+        struct {
+            uint32_t cnt[kSelect], lo[kSelect], hi[kSelect];   // block 0, after the merge
+        };
     };
-    uint32_t cnt[256], lo[256], hi[256];
     u64 part[kSearch / 32];
     uint32_t part_n[kSearch / 32];
     u64 own_above, own_total;            // exact weights, all own chunks
@@ -927,12 +938,15 @@ __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, co
     float lo, hi;
     window_of(cmd, lo, hi);
     u64 above = 0, all = 0;
+    Chunk<T> next;                           // on its way while the one before is worked on
+    if (warp < r.mine) next.load(r.x, r.V, r.first + warp, lane, r.vec);
 #pragma unroll 1
     for (int i = warp; i < r.mine; i += kSearch / 32) {
+        Chunk<T> c = next;
+        if (i + kSearch / 32 < r.mine)
+            next.load(r.x, r.V, r.first + i + kSearch / 32, lane, r.vec);
         const float top = cmax[r.first + i];
         if (distance(top, r) >= kBins || (cmd.shift >= 0 && !cmd.total && top < lo)) continue;
-        Chunk<T> c;
-        c.load(r.x, r.V, r.first + i, lane, r.vec);
         if (cmd.shift < 0) {
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
@@ -984,14 +998,17 @@ __device__ __noinline__ void step_collect(const Row<T>& row, const Cmd& command,
     window_of(cmd, lo, hi);
     const bool everything = hi == -INFINITY;
     u64 all = 0;
+    Chunk<T> next;                           // on its way while the one before is worked on
+    if (warp < r.mine) next.load(r.x, r.V, r.first + warp, lane, r.vec);
 #pragma unroll 1
     for (int i = warp; i < r.mine; i += kSearch / 32) {
+        Chunk<T> c = next;
+        if (i + kSearch / 32 < r.mine)
+            next.load(r.x, r.V, r.first + i + kSearch / 32, lane, r.vec);
         const float top = cmax[r.first + i];
         u64 w = 0;
         uint32_t n = 0;
         if (top >= lo || ((cmd.total || everything) && distance(top, r) < kBins)) {
-            Chunk<T> c;
-            c.load(r.x, r.V, r.first + i, lane, r.vec);
             u64 sum = 0;
 #pragma unroll 1
             for (int j = 0; j < Chunk<T>::kQuads; ++j) {
@@ -1028,56 +1045,62 @@ __device__ __noinline__ void step_collect(const Row<T>& row, const Cmd& command,
     __syncthreads();
 }
 
-// Radix selection in the merged list: the key at which the count (or weight) of the
-// elements from the top reaches `need` >= 1, and count and weight above that key.
+// Selection in the merged list, whose keys lie in [lo, hi]: the key at which the count (or
+// weight) of the elements from the top reaches `need` >= 1, and count and weight above that
+// key.  Histograms of 1024 bins of the keys' range, then of the bin's: equal parts of the
+// range keep the atomics of one bin few, where digits of the keys would not.
 struct Selected {
     uint32_t key;
     u64 n, w;
 };
-__device__ __noinline__ Selected list_select(bool by_weight, u64 need, const Cmd& cmd,
-                                             Shared& sh) {
-    // the window's keys differ in their low bytes alone
-    const int levels = (39 - __clz(cmd.klo ^ cmd.khi)) / 8;
-    uint32_t prefix = levels > 3 ? 0u : cmd.khi >> (8 * levels) << (8 * levels);
+template <typename T>
+__device__ __noinline__ Selected list_select(const Row<T>& row, bool by_weight, u64 need,
+                                             uint32_t lo, uint32_t hi, Shared& sh) {
+    const WeightScale ws = row.ws;
     u64 n_up = 0, w_up = 0;
+    int shift;
 #pragma unroll 1
-    for (int level = levels - 1; level >= 0; --level) {
+    do {
+        shift = max(0, 22 - __clz(hi - lo));         // (hi - lo) >> shift < 1024
         __syncthreads();
-        if (threadIdx.x < 256) sh.cnt[threadIdx.x] = sh.lo[threadIdx.x] = sh.hi[threadIdx.x] = 0;
+        for (int i = threadIdx.x; i < kSelect; i += kSearch) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
         __syncthreads();
-        const uint32_t mask = level == 3 ? 0u : 0xffffffffu << (8 * (level + 1));
 #pragma unroll 1
         for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSearch) {
             const uint32_t k = sh.key[i];
-            if ((k & mask) != prefix) continue;
-            const uint32_t b = (k >> (8 * level)) & 255u;
+            if (k < lo || k > hi) continue;
+            const uint32_t b = (hi - k) >> shift;
             atomicAdd(&sh.cnt[b], 1u);
-            const u64 w = sh.w[i];
+            const u64 w = fixed_weight(key_value(k), ws, sh.table);
             const uint32_t wl = static_cast<uint32_t>(w);
             const uint32_t old = atomicAdd(&sh.lo[b], wl);
             atomicAdd(&sh.hi[b], static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u));
         }
         __syncthreads();
-        // thread t holds bin 255 - t, from the top down
-        const int b = 255 - int(threadIdx.x);
-        const u64 w = b >= 0 ? (u64(sh.hi[b]) << 32) | sh.lo[b] : 0;
-        const uint32_t n = b >= 0 ? sh.cnt[b] : 0;
-        const Scanned s = block_scan<kSearch>(w, n, sh.part, sh.part_n);
-        const u64 before = by_weight ? w_up + s.v : n_up + s.n;
-        const u64 after = before + (by_weight ? w : u64(n));
-        // the first bin to reach the need; the lowest one if none does
-        if (b >= 0 && ((before < need && after >= need) || (b == 0 && after < need))) {
-            sh.at = b;
-            sh.at_w = w_up + s.v;
-            sh.at_n = static_cast<uint32_t>(n_up) + s.n;
-        }
+        // thread t holds bins 2 t and 2 t + 1, from the top down
+        static_assert(kSelect == 2 * kSearch, "two bins a thread");
+        const int b = 2 * threadIdx.x;
+        const u64 w0 = (u64(sh.hi[b]) << 32) | sh.lo[b];
+        const u64 w1 = (u64(sh.hi[b + 1]) << 32) | sh.lo[b + 1];
+        const uint32_t n0 = sh.cnt[b], n1 = sh.cnt[b + 1];
+        const Scanned s = block_scan<kSearch>(w0 + w1, n0 + n1, sh.part, sh.part_n);
+        const u64 c0 = by_weight ? w_up + s.v : n_up + s.n;
+        const u64 c1 = c0 + (by_weight ? w0 : u64(n0)), c2 = c1 + (by_weight ? w1 : u64(n1));
+        if (c0 < need && c1 >= need)
+            sh.at = b, sh.at_w = w_up + s.v, sh.at_n = static_cast<uint32_t>(n_up) + s.n;
+        else if (c1 < need && c2 >= need)
+            sh.at = b + 1, sh.at_w = w_up + s.v + w0,
+            sh.at_n = static_cast<uint32_t>(n_up) + s.n + n0;
         __syncthreads();
-        prefix |= uint32_t(sh.at) << (8 * level);
+        const uint32_t at = sh.at;
         w_up = sh.at_w;
         n_up = sh.at_n;
-    }
+        const uint32_t top = hi - (at << shift);
+        lo = max(lo, top - ((1u << shift) - 1));
+        hi = top;
+    } while (shift > 0);
     __syncthreads();
-    return Selected{prefix, n_up, w_up};
+    return Selected{hi, n_up, w_up};
 }
 
 // What block 0 carries from step to step (uniform over its threads).
@@ -1231,7 +1254,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     if (first_may < kBins && first_may == sh.at) sh.at_w = at_before;
     __syncthreads();
     const int at = sh.at, at2 = sh.at2;
-    const u64 skipped = sh.at_w;
+    u64 skipped = sh.at_w;
     const int j1 = min(at, kBins - 1), j2 = max(j1, min(at2, kBins - 1));
     // elements of the new window (codes of a window are near 4096 unless it is wide)
     u64 est = 0;
@@ -1252,14 +1275,17 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         }
         return;
     }
+    // the first top_k altogether, where the list holds them: top_p is then settled in it too
+    const bool whole = P.want_k && !keys && skipped + est <= kList;
+    if (whole) skipped = 0;
     if (P.want_k) P.n_above += skipped;
     if (!keys) {
         // the keys of exactly these bins: the lowest of bin j2 or above, and the highest of
         // bin j1 or below
         if (threadIdx.x < 32) {
             const uint32_t lo = first_key(r, kKeyNegInf + 1, order_key(r.ws.m), j2);
-            const uint32_t hi = j1 == 0 ? order_key(r.ws.m)
-                                        : first_key(r, lo, order_key(r.ws.m), j1 - 1) - 1;
+            const uint32_t hi = j1 == 0 || whole ? order_key(r.ws.m)
+                                                 : first_key(r, lo, order_key(r.ws.m), j1 - 1) - 1;
             if (threadIdx.x == 0) sh.at = static_cast<int>(lo), sh.at2 = static_cast<int>(hi);
         }
         __syncthreads();
@@ -1291,7 +1317,8 @@ __device__ __noinline__ void search_draw(const Row<T>& r, const Search& P, const
 #pragma unroll 1
         for (uint32_t i = tid; i < sh.n_list; i += kSearch) {
             const int c = sh.idx[i] / kChunk;
-            if (sh.key[i] > P.key) atomicAdd(&cw[c], sh.w[i]);
+            if (sh.key[i] > P.key)
+                atomicAdd(&cw[c], fixed_weight(key_value(sh.key[i]), r.ws, sh.table));
             else if (sh.key[i] == P.key) atomicAdd(&cn[c], 1u);
         }
         __syncthreads();
@@ -1367,7 +1394,7 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
     const uint32_t n = start[8];
     const bool over = n > kList;
     if (!over)
-#pragma unroll 1
+#pragma unroll 2
         for (uint32_t i = threadIdx.x; i < n; i += kSearch) {
             int k = 0;
             uint32_t from = 0;
@@ -1377,7 +1404,6 @@ __device__ __noinline__ uint32_t merge(const Row<T>& r, const Cmd& cmd, u64* cw,
             const uint32_t key = peer(sh.own_key, k)[i - from];
             sh.key[i] = key;
             sh.idx[i] = peer(sh.own_idx, k)[i - from];
-            sh.w[i] = fixed_weight(key_value(key), r.ws, sh.table);
         }
     if (threadIdx.x == 0) sh.n_list = over ? 0 : n;
     __syncthreads();
@@ -1402,14 +1428,17 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
         next_hist(cmd);
         return false;
     }
-    u64 list_w;
-    if (cmd.list) {
+    const uint32_t key_top = min(cmd.khi, order_key(r.ws.m));
+    u64 list_w = 0;
+    if (cmd.list && (!P.want_k || P.top_k - P.n_above > n)) {
         u64 mine = 0;
-        for (uint32_t i = threadIdx.x; i < n; i += kSearch) mine += sh.w[i];
+        for (uint32_t i = threadIdx.x; i < n; i += kSearch)
+            mine += fixed_weight(key_value(sh.key[i]), r.ws, sh.table);
         list_w = block_scan<kSearch>(mine, 0, sh.part, sh.part_n).tv;
-    } else {
+    } else if (!cmd.list) {
         list_w = inside * fixed_weight(key_value(cmd.klo), r.ws, sh.table);
     }
+    bool settled = false;                // the need lies in this window
     if (P.want_k) {
         const u64 left = P.top_k - P.n_above;
         u64 up_w = 0;
@@ -1418,7 +1447,7 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
             P.ties = 0;
             up_w = list_w;
         } else if (cmd.list) {
-            const Selected at = list_select(false, left, cmd, sh);
+            const Selected at = list_select(r, false, left, cmd.klo, key_top, sh);
             P.key = at.key;
             P.ties = left - at.n;
             up_w = at.w;
@@ -1435,11 +1464,12 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
                 start_p(P, cmd);
                 return false;
             }
+            settled = true;
         }
     }
     if (P.want_p) {
         const u64 need = P.need(P.s_lo);     // exact by now
-        if (need <= above || need > above + list_w) {
+        if (need <= above || (!settled && need > above + list_w)) {
             // cannot be: the window was drawn around every total within its bounds
             P.key = kKeyNegInf;
             P.ties = 0;
@@ -1447,7 +1477,7 @@ __device__ __noinline__ bool after_collect(const Row<T>& r, Search& P, Cmd& cmd,
             return false;
         }
         Selected at{cmd.klo, 0, 0};
-        if (cmd.list) at = list_select(true, need - above, cmd, sh);
+        if (cmd.list) at = list_select(r, true, need - above, cmd.klo, key_top, sh);
         const u64 wt = fixed_weight(key_value(at.key), r.ws, sh.table);
         P.key = at.key;
         P.ties = wt == 0 ? 0 : (need - above - at.w + wt - 1) / wt;
