@@ -41,6 +41,7 @@
 // cluster decides each step; the blocks work on their own chunks in between.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "ptx.cuh"
@@ -56,6 +57,7 @@ typedef unsigned long long u64;
 constexpr int kThreads = 256;            // of a scan block
 constexpr int kWarps = kThreads / 32;
 constexpr int kSearch = 512;             // of a search block
+constexpr int kExact = 1024;             // of a block that weighs rows exactly
 constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
@@ -381,20 +383,25 @@ struct Shared0 {
     int at;
 };
 
-// Workspace: a header a row, then the chunks' maxima and sums, then the segments' maxima
-// (room for them as if logits were fp32).
+// Workspace: a header a row, whether the row goes on to the search, the chunks' maxima and
+// sums, the segments' maxima (room for them as if logits were fp32).
 enum : uint32_t { kRowDone, kRowSearch };
 struct RowHeader {
     u64 all;                             // fast total of the weights
     float m;                             // maximum
-    uint32_t mode;
 };
+__host__ __device__ constexpr size_t modes_offset(int64_t N) {
+    return (size_t(N) * sizeof(RowHeader) + 255) / 256 * 256;
+}
 constexpr int kSegsPerChunk = kChunk / 128;
 __host__ __device__ constexpr size_t stats_offset(int64_t N) {
-    return (size_t(N) * sizeof(RowHeader) + 255) / 256 * 256;
+    return (modes_offset(N) + size_t(N) * sizeof(uint32_t) + 255) / 256 * 256;
 }
 __host__ __device__ constexpr size_t segs_offset(int64_t N, int nch) {
     return (stats_offset(N) + size_t(N) * nch * sizeof(float2) + 255) / 256 * 256;
+}
+__device__ __forceinline__ uint32_t* row_modes(const SampleArgs& a) {
+    return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) + modes_offset(a.N));
 }
 __device__ __forceinline__ float2* row_stats(const SampleArgs& a, int64_t row, int nch) {
     return reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + stats_offset(a.N)) +
@@ -760,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (a.mask != nullptr && a.mask[row_i] == 0) {
         if (rank == 0 && tid == 0) {
             write_row(a, row_i, -1, 0.f, 0.f);
-            head->mode = kRowDone;
+            row_modes(a)[row_i] = kRowDone;
         }
         return;
     }
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (!s.ok) {
         if (rank == 0 && tid == 0) {
             write_failed(a, row_i, RLK_DEVERR_SAMPLE_PARAM);
-            head->mode = kRowDone;
+            row_modes(a)[row_i] = kRowDone;
         }
         return;
     }
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (bad || m == -INFINITY) {
         if (tid == 0) {
             write_failed(a, row_i, RLK_DEVERR_LOGITS);
-            head->mode = kRowDone;
+            row_modes(a)[row_i] = kRowDone;
         }
         return;
     }
@@ -864,11 +871,40 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (tid == 0) {
         head->all = all;
         head->m = m;
-        head->mode = done ? kRowDone : kRowSearch;
+        row_modes(a)[row_i] = done ? kRowDone : kRowSearch;
     }
 }
 
 // ----------------------------------------------------------------------------- search
+
+// Cluster c of `clusters` takes the rows to search whose number among them is c modulo
+// clusters: every block counts them out of the rows' modes, so the rows are spread evenly
+// without a counter.  The rows of the batch base .. base + THREADS - 1 that are this
+// cluster's: their number, places in queue.
+struct Queue {
+    uint32_t n;
+    uint16_t at[kExact];
+};
+template <int THREADS>
+__device__ uint32_t queue_rows(const uint32_t* modes, int N, int base, uint32_t cluster,
+                               uint32_t clusters, uint32_t& seen, Queue& queue, u64* part,
+                               uint32_t* part_n) {
+    const int tid = threadIdx.x;
+    const bool hard = base + tid < N && modes[base + tid] == kRowSearch;
+    if (!__syncthreads_or(hard)) return 0;
+    if (tid == 0) queue.n = 0;
+    const Scanned s = block_scan<THREADS>(0, hard ? 1 : 0, part, part_n);
+    const uint32_t number = seen + s.n;
+    if (hard && number % clusters == cluster) {
+        // the first of the batch's numbers that are this cluster's comes first
+        const uint32_t first = (seen + clusters - 1 - cluster) / clusters;
+        queue.at[(number - cluster) / clusters - first] = static_cast<uint16_t>(tid);
+        atomicAdd(&queue.n, 1u);
+    }
+    seen += s.tn;
+    __syncthreads();
+    return queue.n;
+}
 
 // A step that block 0 asks of all blocks.  Elements are above, inside or below a window of
 // values [key_value(klo), key_value(khi)].
@@ -900,6 +936,7 @@ struct Shared {
     u64 own_above, own_total;            // exact weights, all own chunks
     uint32_t own_count;
     uint32_t n_list, key_m;
+    Queue queue;
     // results of block-wide searches
     u64 at_w;
     uint32_t at_n;
@@ -1503,29 +1540,17 @@ __host__ __device__ constexpr size_t search_smem(int nch, int own) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSearch, 2)
-    sample_search_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
-                         int ranks) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem);
-    u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared));     // all chunks: weight
-    u64* own_w = cw + nch;                                       // own chunks
-    float* cmax = reinterpret_cast<float*>(own_w + own);         // all chunks: maximum
-    uint32_t* cn = reinterpret_cast<uint32_t*>(cmax + nch);      //             ties
-    uint32_t* own_n = cn + nch;
-    const int64_t row_i = blockIdx.x / ranks;
-    const int rank = blockIdx.x % ranks;
+__device__ __forceinline__ void search_row(const T* logits, const SampleArgs& a, int64_t row_i,
+                                           int rank, int ranks, int nch, int own, u64* cw,
+                                           u64* own_w, float* cmax, uint32_t* cn, uint32_t* own_n,
+                                           Shared& sh) {
     const int tid = threadIdx.x;
-    // the scan's results are complete
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const RowHeader* head = static_cast<const RowHeader*>(a.workspace) + row_i;
-    if (head->mode != kRowSearch) return;
     const Settings s = read_settings(a, row_i);
     Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
     r.ws.m = head->m;
     const float2* stats = row_stats(a, row_i, nch);
     for (int i = tid; i < nch; i += kSearch) cmax[i] = stats[i].x;
-    for (int i = tid; i < kExpEntries; i += kSearch) sh.table[i] = kExpTable.v[i];
     if (tid == 0) sh.key_m = s.want_m ? min_p_key(a, row_i, r.ws.m) : 0;
     __syncthreads();
 
@@ -1549,7 +1574,6 @@ __global__ void __launch_bounds__(kSearch, 2)
     } else {
         cmd = make_hist0(!P.want_k);
     }
-
     cmd.total = P.want_p && !P.want_k && cmd.type == kCollect;
     // the blocks work on their chunks, block 0 decides what comes next
     for (int step = 0; step < kMaxSteps; ++step) {
@@ -1581,9 +1605,149 @@ __global__ void __launch_bounds__(kSearch, 2)
 }
 
 template <typename T>
+__global__ void __launch_bounds__(kSearch, 2)
+    sample_search_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
+                         int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared));     // all chunks: weight
+    u64* own_w = cw + nch;                                       // own chunks
+    float* cmax = reinterpret_cast<float*>(own_w + own);         // all chunks: maximum
+    uint32_t* cn = reinterpret_cast<uint32_t*>(cmax + nch);      //             ties
+    uint32_t* own_n = cn + nch;
+    const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+    const int rank = blockIdx.x % ranks, tid = threadIdx.x;
+    // the scan's results are complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t* modes = row_modes(a);
+    bool table = false;
+    uint32_t seen = 0;                   // rows to search before this batch
+    for (int base = 0; base < a.N; base += kSearch) {
+        const uint32_t n = queue_rows<kSearch>(modes, a.N, base, cluster, clusters, seen, sh.queue,
+                                               sh.part, sh.part_n);
+        if (n > 0 && !table) {
+            for (int i = tid; i < kExpEntries; i += kSearch) sh.table[i] = kExpTable.v[i];
+            table = true;
+        }
+        for (uint32_t i = 0; i < n; ++i)
+            search_row(logits, a, int64_t(base) + sh.queue.at[i], rank, ranks, nch, own, cw, own_w,
+                       cmax, cn, own_n, sh);
+        __syncthreads();
+    }
+}
+
+// ----------------------------------------------------------------------------- exact draw
+
+// The search of a call without any truncation: its rows are those whose target lies near a
+// border, few of them, and what counts is how soon each is done.  Every weight of the row is
+// formed exactly; a warp takes 128 columns at a time.
+struct Shared1 {
+    u64 table[kExpEntries];
+    u64 part[kExact / 32];
+    uint32_t part_n[kExact / 32];
+    u64 at_w;
+    int at;
+    Queue queue;
+};
+__host__ __device__ constexpr size_t exact_smem(int own) {
+    return sizeof(Shared1) + size_t(own) * 8 + 16;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kExact, 1)
+    sample_exact_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
+                        int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared1& sh = *reinterpret_cast<Shared1*>(smem);
+    u64* own_w = reinterpret_cast<u64*>(smem + sizeof(Shared1));
+    const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+    const int rank = blockIdx.x % ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < kExpEntries; i += kExact) sh.table[i] = kExpTable.v[i];
+    // the scan's results are complete
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kUnit = 128, kPerChunk = kChunk / kUnit, kAhead = 5, kUnits = kExact / 32;
+    uint32_t seen = 0;
+    for (int base = 0; base < a.N; base += kExact) {
+        const uint32_t n = queue_rows<kExact>(row_modes(a), a.N, base, cluster, clusters, seen,
+                                              sh.queue, sh.part, sh.part_n);
+        for (uint32_t q = 0; q < n; ++q) {
+            const int64_t row_i = int64_t(base) + sh.queue.at[q];
+            const Settings s = read_settings(a, row_i);
+            Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
+            r.ws.m = (static_cast<const RowHeader*>(a.workspace) + row_i)->m;
+            for (int i = tid; i < own; i += kExact) own_w[i] = 0;
+            __syncthreads();
+            const int units = r.mine * kPerChunk;
+#pragma unroll 1
+            for (int u0 = warp; u0 < units; u0 += kAhead * kUnits) {
+                float x[kAhead][4];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int u = u0 + k * kUnits;
+                    if (u >= units) break;
+                    const int c = r.first * kChunk + u * kUnit + lane * 4;
+                    if (sizeof(T) == 4 && r.vec && c + 4 <= r.V) {
+                        const float4 v = __ldg(reinterpret_cast<const float4*>(r.x + c));
+                        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+                    } else if (sizeof(T) == 2 && r.vec && c + 4 <= r.V) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(r.x + c));
+                        x[k][0] = __uint_as_float(v.x << 16);
+                        x[k][1] = __uint_as_float(v.x & 0xffff0000u);
+                        x[k][2] = __uint_as_float(v.y << 16);
+                        x[k][3] = __uint_as_float(v.y & 0xffff0000u);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[k][e] = c + e < r.V ? load_one(r.x + c + e) : -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int u = u0 + k * kUnits;
+                    if (u >= units) break;
+                    u64 w[4];
+                    fixed_weights(make_float2(x[k][0], x[k][1]), r.ws, sh.table, w[0], w[1]);
+                    fixed_weights(make_float2(x[k][2], x[k][3]), r.ws, sh.table, w[2], w[3]);
+                    const u64 sum = warp_sum((w[0] + w[1]) + (w[2] + w[3]));
+                    if (lane == 0) atomicAdd(&own_w[u / kPerChunk], sum);
+                }
+            }
+            __syncthreads();
+            cluster_join();
+            if (rank == 0) {
+                // the chunk, then the column, that u times the total falls on
+                const int each = (nch + kExact - 1) / kExact;
+                const int c0 = min(nch, tid * each), c1 = min(nch, c0 + each);
+                u64 w = 0;
+                for (int c = c0; c < c1; ++c) w += peer(own_w, c / own)[c % own];
+                const Scanned t = block_scan<kExact>(w, 0, sh.part, sh.part_n);
+                const u64 target = part_of(s.u, t.tv, false);
+                if (tid == 0) sh.at = 0, sh.at_w = 0;
+                __syncthreads();
+                u64 run = t.v;
+                for (int c = c0; c < c1; ++c) {
+                    const u64 cw = peer(own_w, c / own)[c % own];
+                    if (run <= target && target < run + cw) sh.at = c, sh.at_w = run;
+                    run += cw;
+                }
+                __syncthreads();
+                const int col = sh.at * kChunk + tid;
+                const float x = tid < kChunk && col < r.V ? load_one(r.x + col) : -INFINITY;
+                const u64 we = fixed_weight(x, r.ws, sh.table);
+                const u64 lo = sh.at_w + block_scan<kExact>(we, 0, sh.part, sh.part_n).v;
+                if (lo <= target && target < lo + we)
+                    write_drawn(a, row_i, col, x, r.ws, t.tv, t.tv);
+            }
+            cluster_join();              // the blocks' sums are read until here
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T>
 cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int),
-                        const T* logits, const SampleArgs& a, int nch, int ranks, int threads,
-                        size_t smem, bool dependent, cudaStream_t stream) {
+                        const T* logits, const SampleArgs& a, int nch, int ranks, int clusters,
+                        int threads, size_t smem, bool dependent, cudaStream_t stream) {
     const int own = (nch + ranks - 1) / ranks;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -1592,7 +1756,7 @@ cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * ranks);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * ranks);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -1613,10 +1777,18 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int nch = (a.V + kChunk - 1) / kChunk;
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, kThreads,
+    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, a.N, kThreads,
                                 scan_smem(nch, sizeof(T)), false, stream);
     if (e != cudaSuccess) return e;
-    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, kSearch,
+    if (a.top_k_rows == nullptr && a.top_p_rows == nullptr && a.min_p_rows == nullptr &&
+        (a.top_k == 0 || a.top_k >= a.V) && a.top_p_value >= 1.f && a.min_p_value == 0.f)
+        // one block on each of 152 SMs
+        return launch_rows(sample_exact_kernel<T>, logits, a, nch, ranks,
+                           std::min(a.N, 152 / ranks), kExact,
+                           exact_smem((nch + ranks - 1) / ranks), true, stream);
+    // two blocks of the search on each of 152 SMs
+    const int clusters = std::min(a.N, 304 / ranks);
+    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, clusters, kSearch,
                        search_smem(nch, (nch + ranks - 1) / ranks), true, stream);
 }
 
