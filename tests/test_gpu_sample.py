@@ -338,3 +338,55 @@ def test_frequencies():
     got = np.bincount(tok.cpu().numpy(), minlength=v)
     assert np.abs(got - n * p).max() <= 1.0 + 1e-3
     assert bool((tok[1:] >= tok[:-1]).all())
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("setting", [{"top_k": 50}, {"top_p": 0.9}, {"top_k": 900, "top_p": 0.9},
+                                     {"min_p": 0.001}, {"top_k": 50, "min_p": 0.3}, {}], ids=str)
+def test_rows_in_order_of_the_tokens(setting, order):
+    # the largest elements side by side: they fill a few segments, so a value that as many
+    # segment maxima reach is reached by far more elements than the short list holds
+    z = normal(8, 40000, 48, 1.5).sort(dim=1, descending=order < 0).values
+    check(z.contiguous(), uniforms(8, 49), **setting)
+    check(z.bfloat16(), uniforms(8, 50), **setting)
+
+
+@pytest.mark.parametrize("setting", [{"top_p": 0.95}, {"top_k": 1500}], ids=str)
+def test_many_rows_to_search(setting):
+    # every row has a wide nucleus, and there are more of them than blocks, or than a batch
+    check(normal(1400, 2050, 51, 0.4, torch.bfloat16), uniforms(1400, 52), **setting)
+
+
+def test_many_rows_on_a_border():
+    # equal tokens and uniforms on the borders between them: u V is a whole number, exactly
+    n, v = 2100, 2048
+    z = torch.full((n, v), -3.25, device=dev())
+    z[::3] = 11.0
+    u = (torch.arange(n) % v).float().div(v).to(dev())
+    tok = check(z, u)
+    assert np.array_equal(tok, np.arange(n) % v)
+    mask = (torch.arange(n) % 4 != 2).to(device=dev(), dtype=torch.uint8)
+    check(z, u, mask=mask)
+
+
+def test_few_rows_to_search_among_many():
+    # the searched rows lie far apart, the others are done by the first pass
+    n, v = 1300, 3000
+    z = zipf(n, v, 53, power=(1.5, 1.6))
+    z[[3, 511, 512, 513, 1023, 1024, 1299]] = normal(7, v, 54, 0.3)
+    check(z, uniforms(n, 55), top_p=0.9)
+
+
+def test_workspace_size_is_enough_at_its_edge():
+    # the byte count asked for, in a buffer with a guard behind it
+    for n, v in ((1, 1), (3, 700), (40, 5003), (600, 1030), (2, 151936)):
+        for dtype in (torch.float32, torch.bfloat16):
+            z, u = normal(n, v, n, 0.7, dtype), uniforms(n, v)
+            need = rlk.rlk_sample_logits_workspace_bytes(n, v)
+            buf = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device=dev())
+            for p in (1.0, 0.9):
+                want = rlk.sample_logits(z, u, 0.8, 0, p)
+                out = tuple(torch.empty_like(t) for t in want)
+                rlk.rlk_sample_logits(z, u, None, 0.8, 0, p, 0.0, *out, buf[:need])
+                assert bool((buf[need:] == 0xA5).all())
+                assert all(torch.equal(a, b) for a, b in zip(out, want))
