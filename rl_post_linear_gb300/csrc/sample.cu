@@ -534,8 +534,9 @@ __device__ float reach_value(const Row<T>& r, const float* smax, int nseg, int c
         __syncthreads();
         if (lane == 0) sh.part_n[warp] = enough ? 1u : 0u;
         __syncthreads();
-        int first = 0;                               // the highest trial that is enough
-        while (first < kWarps && sh.part_n[first] == 0) ++first;
+        // the highest trial that is enough
+        const unsigned who = __ballot_sync(0xffffffffu, lane < kWarps && sh.part_n[lane] != 0);
+        const int first = who == 0 ? kWarps : __ffs(who) - 1;
         if (round == 0 && first >= kWarps - 1) {
             found = first < kWarps;
             if (!found) return low;
@@ -847,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     m = warp_max(m);
     if (lane == 0) sh.part_n[warp] = __float_as_uint(m);
     bad = __syncthreads_or(bad);
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, __uint_as_float(sh.part_n[i]));
+    m = warp_max(lane < kWarps ? __uint_as_float(sh.part_n[lane]) : -INFINITY);
     if (bad || m == -INFINITY) {
         if (tid == 0) {
             write_failed(a, row_i, RLK_DEVERR_LOGITS);
