@@ -324,8 +324,8 @@ __device__ __forceinline__ Raw<float> Ring<float>::group(int stage, int i) const
 }
 
 // mask byte of a row: 0 past the end
-__device__ __forceinline__ int mask_byte(const NormArgs& a, int row) {
-    return row >= a.N ? 0 : a.mask == nullptr ? 1 : __ldg(a.mask + row);
+__device__ __forceinline__ int mask_byte(const uint8_t* mask, int row, int N) {
+    return row >= N ? 0 : mask == nullptr ? 1 : __ldg(mask + row);
 }
 
 // FULL: H is 16 columns for each thread and every row starts on 16 bytes, so no column needs
@@ -341,6 +341,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     const bool out_vec = FULL || a.out_vec;
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.out);
+    const uint8_t* mask = a.mask;
+    const void *weight = a.weight, *bias = a.bias;
+    wait_previous(x, mask, weight, bias);
     const Ring<T> ring{ring_smem};
     // Row indices leave room for S more steps below 2^31.  S - 1 rows are on their way before
     // the first is waited for; `bits` says which of them are active, `next` whether the row
@@ -352,24 +355,24 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     T* yr = y + row * a.out_stride;
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-        if (mask_byte(a, row + k * step)) {
+        if (mask_byte(mask, row + k * step, a.N)) {
             ring.fetch(ahead, k, H, x_mode, FULL);
             bits |= 1u << k;
         }
         cp_commit();
         ahead += step * a.x_stride;
     }
-    next = mask_byte(a, row + (S - 1) * step);
+    next = mask_byte(mask, row + (S - 1) * step, a.N);
     float2 w[kGroups][4], b[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         const int c = (tid + i * blockDim.x) * kGroup;
         float v[8];
-        param_group(a.weight, a.w_bf16, a.w_vec, c, H, v);
+        param_group(weight, a.w_bf16, a.w_vec, c, H, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[i][e] = make_float2(v[2 * e], v[2 * e + 1]), b[i][e] = both(0.f);
-        if (a.bias != nullptr) {
-            param_group(a.bias, a.w_bf16, a.w_vec, c, H, v);
+        if (bias != nullptr) {
+            param_group(bias, a.w_bf16, a.w_vec, c, H, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) b[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
         }
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
         }
         cp_commit();
         ahead += step * a.x_stride;
-        next = mask_byte(a, row + S * step);
+        next = mask_byte(mask, row + S * step, a.N);
         const bool on = bits & 1u;
         bits >>= 1;
         const int at = stage;
@@ -515,6 +518,9 @@ __global__ void __launch_bounds__(MAXT, 1)
     const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.out);
+    const uint8_t* mask = a.mask;
+    const void* weight = a.weight;
+    wait_previous(x, dy, mask, weight);
     const Ring<T> rx{ring_smem}, rg{ring_smem + S * Ring<T>::kPieces * blockDim.x};
     const int step = gridDim.x;
     int row = blockIdx.x, next;
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     T* dxr = dx + row * a.out_stride;
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-        if (mask_byte(a, row + k * step)) {
+        if (mask_byte(mask, row + k * step, a.N)) {
             rx.fetch(x_ahead, k, H, x_mode, FULL);
             rg.fetch(g_ahead, k, H, dy_mode, FULL);
             bits |= 1u << k;
@@ -533,12 +539,12 @@ __global__ void __launch_bounds__(MAXT, 1)
         x_ahead += step * a.x_stride;
         g_ahead += step * a.dy_stride;
     }
-    next = mask_byte(a, row + (S - 1) * step);
+    next = mask_byte(mask, row + (S - 1) * step, a.N);
     float2 w[kGroups][4], dw[kGroups][4], db[kGroups][4];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
         float v[8];
-        param_group(a.weight, a.w_bf16, a.w_vec, (tid + i * blockDim.x) * kGroup, H, v);
+        param_group(weight, a.w_bf16, a.w_vec, (tid + i * blockDim.x) * kGroup, H, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w[i][e] = make_float2(v[2 * e], v[2 * e + 1]);
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(MAXT, 1)
         cp_commit();
         x_ahead += step * a.x_stride;
         g_ahead += step * a.dy_stride;
-        next = mask_byte(a, row + S * step);
+        next = mask_byte(mask, row + S * step, a.N);
         const bool on = bits & 1u;
         bits >>= 1;
         const int at = stage;
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(1024)
     norm_dw_merge_kernel(const float* __restrict__ dw_part, const float* __restrict__ db_part,
                          int P, int len, int threads, int H, bool bf16,
                          void* __restrict__ dweight, void* __restrict__ dbias) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(dw_part, db_part);
     const float* part = blockIdx.y == 0 ? dw_part : db_part;
     void* out = blockIdx.y == 0 ? dweight : dbias;
     if (out == nullptr) return;
@@ -781,9 +787,8 @@ cudaError_t run_fwd(const NormArgs& a, int threads, cudaStream_t stream) {
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(threads));
-    kernel<<<blocks, threads, smem, stream>>>(a, copy_mode(a.x, a.x_stride, sizeof(T)),
-                                              1.f / static_cast<float>(a.H));
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(blocks), threads, smem, stream, nullptr, a,
+                        copy_mode(a.x, a.x_stride, sizeof(T)), 1.f / static_cast<float>(a.H));
 }
 
 template <typename T, bool CENTER>
@@ -808,10 +813,10 @@ cudaError_t run_bwd(const NormArgs& a, int threads, int blocks, float* dwp, floa
         size_t(threads) * kGroups * kGroup * sizeof(T) * 2 * stages_of<T, MAXT, 2>();
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, threads, smem, stream>>>(a, copy_mode(a.x, a.x_stride, sizeof(T)),
-                                              copy_mode(a.dy, a.dy_stride, sizeof(T)),
-                                              1.f / static_cast<float>(a.H), dwp, dbp);
-    return cudaGetLastError();
+    return launch_early(kernel, dim3(blocks), threads, smem, stream, nullptr, a,
+                        copy_mode(a.x, a.x_stride, sizeof(T)),
+                        copy_mode(a.dy, a.dy_stride, sizeof(T)), 1.f / static_cast<float>(a.H), dwp,
+                        dbp);
 }
 
 template <typename T, bool CENTER>
@@ -861,19 +866,11 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool center, cudaStream_t stream)
         if (e != cudaSuccess) return e;
     }
     if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.len / 32), a.dbias != nullptr ? 2 : 1);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_dw_merge_kernel, static_cast<const float*>(dwp),
-                              static_cast<const float*>(dbp), a.N > 0 ? p.blocks : 0,
-                              static_cast<int>(p.len), p.threads, a.H, a.w_bf16, a.dweight,
-                              a.dbias);
+    const dim3 grid(static_cast<unsigned>(p.len / 32), a.dbias != nullptr ? 2 : 1);
+    return launch_early(norm_dw_merge_kernel, grid, 1024, 0, stream, nullptr,
+                        static_cast<const float*>(dwp), static_cast<const float*>(dbp),
+                        a.N > 0 ? p.blocks : 0, static_cast<int>(p.len), p.threads, a.H, a.w_bf16,
+                        a.dweight, a.dbias);
 }
 
 }  // namespace rlk

@@ -19,6 +19,14 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
+// Waits for what the stream did before a kernel that is launched early.  The pointers to read
+// through pass the wait too, so that no read-only load is moved ahead of it.
+template <typename... P>
+__device__ __forceinline__ void wait_previous(P&... pointers) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    ([&pointers] { asm volatile("" : "+l"(pointers)::"memory"); }(), ...);
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

@@ -277,6 +277,26 @@ cudaError_t launch_audit_ext(const float* logp_new, const float* logp_old, const
                              rlk_audit_ext_t* result, void* workspace, bool vec_ok, int sms,
                              cudaStream_t stream);
 
+// Launches a kernel that waits itself (wait_previous) for what the stream did before, so its
+// blocks are already there when that ends: 2 us of a call in a row of such calls.  `more` is one
+// further attribute or nullptr.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, const cudaLaunchAttribute* more, Args... args) {
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (more != nullptr) attr[1] = *more;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = more != nullptr ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // Layer norm / RMS norm.  *_vec: the rows' starts allow 16-byte accesses.
 struct NormArgs {
     const void* x;
