@@ -43,6 +43,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "ptx.cuh"
 #include "rlk_internal.h"
@@ -242,6 +243,54 @@ struct Chunk {
     }
 };
 
+// A warp's part of a ring of chunks in shared memory, on their way while another is worked on.
+// Each lane copies just what it reads itself, so this needs no barrier: group j of slot s lies
+// at (LOADS s + j) 32 + lane.  Two chunks of fp32: with three, an SM holds fewer blocks (the pass
+// alone 38.2 instead of 36.6 us at [256, 151936]).
+constexpr int kRing = 4096;              // bytes of a warp
+template <typename T>
+struct Ring {
+    static constexpr int LOADS = Chunk<T>::LOADS, VEC = Chunk<T>::VEC;
+    static constexpr int S = kRing / (kChunk * int(sizeof(T)));
+    uint4* lane_base;
+
+    __device__ __forceinline__ void fetch(int slot, const T* row, int V, int chunk, int lane,
+                                          bool vec) const {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            uint4* to = lane_base + (slot * LOADS + j) * 32;
+            const int c = Chunk<T>::column(chunk, j, lane);
+            if (vec && c + VEC <= V) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                             "l"(row + c)
+                             : "memory");
+            } else if (sizeof(T) == 4) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (c + e < V)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                         smem_u32(to) + 4 * e),
+                                     "l"(row + c + e)
+                                     : "memory");
+                    else
+                        reinterpret_cast<float*>(to)[e] = -INFINITY;
+            } else {
+                *to = load_group(row, V, c, false);
+            }
+        }
+    }
+    __device__ __forceinline__ void read(int slot, Chunk<T>& c) const {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) c.raw[j] = lane_base[(slot * LOADS + j) * 32];
+    }
+};
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest LEFT groups have arrived
+template <int LEFT>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
@@ -375,12 +424,14 @@ __device__ __noinline__ void write_drawn(const SampleArgs& a, int64_t row, int v
 // Shared memory of the scan.
 struct Shared0 {
     u64 table[kExpEntries];
-    u64 order[kShort], w[kShort];        // the list, then sorted
     u64 part[kWarps];
     uint32_t part_n[kWarps];
     u64 at_w;
     uint32_t n_list, n_ids, flag, key_m;
     int at;
+    // from here on first the ring of the pass over the row
+    __align__(16) u64 order[kShort];     // the list, then sorted
+    u64 w[kShort];
 };
 
 // Workspace: a header a row, whether the row goes on to the search, the chunks' maxima and
@@ -746,7 +797,10 @@ __host__ __device__ constexpr int segments_of(int nch, size_t esize) {
     return n <= kMaxSegments ? n : 0;
 }
 __host__ __device__ constexpr size_t scan_smem(int nch, size_t esize) {
-    return sizeof(Shared0) + size_t(nch) * 12 + size_t(segments_of(nch, esize)) * 6 + 64;
+    const size_t ring = offsetof(Shared0, order) + kWarps * kRing;
+    const size_t tail =
+        sizeof(Shared0) + size_t(nch) * 12 + size_t(segments_of(nch, esize)) * 6 + 64;
+    return ring > tail ? ring : tail;
 }
 
 template <typename T>
@@ -762,66 +816,82 @@ __global__ void __launch_bounds__(kThreads, 4)
     uint16_t* ids = reinterpret_cast<uint16_t*>(smax + (nseg + 3) / 4 * 4);
     const int64_t row_i = blockIdx.x / ranks;
     const int rank = blockIdx.x % ranks;             // = the block's rank in its cluster
+    // The block that finishes the row.  Not always the same one of its cluster: clusters that
+    // follow each other on the same SMs would then finish their rows on the same few of them
+    // (31.0 instead of 26.6 us at [64, 151936] with top_k and top_p).
+    const bool lead = rank == static_cast<int>(row_i % ranks);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     RowHeader* head = static_cast<RowHeader*>(a.workspace) + row_i;
     float2* stats = row_stats(a, row_i, nch);
+    if (lead)
+        for (int i = tid; i < kExpEntries / 2; i += kThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(sh.table + 2 * i)),
+                         "l"(kExpTable.v + 2 * i)
+                         : "memory");
+    cp_commit();
+    // what the stream did before is complete: the logits, and the last call's use of the workspace
+    wait_previous(logits);
     if (a.mask != nullptr && a.mask[row_i] == 0) {
-        if (rank == 0 && tid == 0) {
+        cp_wait<0>();
+        if (lead && tid == 0) {
             write_row(a, row_i, -1, 0.f, 0.f);
             row_modes(a)[row_i] = kRowDone;
         }
         return;
     }
+    // the row is on its way while its settings are read
+    const T* x = logits + row_i * a.stride;
+    const int first = rank * own, share = max(0, min(own, nch - first));
+    const Ring<T> ring{reinterpret_cast<uint4*>(sh.order) + warp * (kRing / 16) + lane};
+    constexpr int S = Ring<T>::S;
+#pragma unroll
+    for (int q = 0; q < S; ++q) {
+        if (warp + q * kWarps < share)
+            ring.fetch(q, x, a.V, first + warp + q * kWarps, lane, a.vec_ok);
+        cp_commit();
+    }
     const Settings s = read_settings(a, row_i);
     if (!s.ok) {
-        if (rank == 0 && tid == 0) {
+        cp_wait<0>();
+        if (lead && tid == 0) {
             write_failed(a, row_i, RLK_DEVERR_SAMPLE_PARAM);
             row_modes(a)[row_i] = kRowDone;
         }
         return;
     }
     Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
-    if (rank == 0)
-        for (int i = tid; i < kExpEntries / 2; i += kThreads)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             smem_u32(sh.table + 2 * i)),
-                         "l"(kExpTable.v + 2 * i)
-                         : "memory");
     const bool cut = s.want_k || s.want_p || s.want_m;
     float* segs = row_segs(a, row_i, nch);
     float best = -INFINITY;
-    constexpr int kAhead = sizeof(T) == 4 ? 2 : 4;
+    int slot = 0;
 #pragma unroll 1
-    for (int i0 = warp; i0 < r.mine; i0 += kAhead * kWarps) {
-        Chunk<T> c[kAhead];
+    for (int i = warp; i < r.mine; i += kWarps) {
+        cp_wait<S - 1>();
+        Chunk<T> c;
+        ring.read(slot, c);
+        float seg[Chunk<T>::LOADS];
+        if (cut) {
+            const float2 st = chunk_stats<true>(c, r.ws.ch, best, seg);
+            if (lane == 0) {
+                stats[r.first + i] = st;
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * kWarps;
-            if (i < r.mine) c[q].load(r.x, r.V, r.first + i, lane, r.vec);
-        }
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * kWarps;
-            if (i >= r.mine) break;
-            float seg[Chunk<T>::LOADS];
-            if (cut) {
-                const float2 st = chunk_stats<true>(c[q], r.ws.ch, best, seg);
-                if (lane == 0) {
-                    stats[r.first + i] = st;
-#pragma unroll
-                    for (int j = 0; j < Chunk<T>::LOADS; ++j)
-                        segs[(r.first + i) * Chunk<T>::LOADS + j] = seg[j];
-                }
-            } else {
-                const float2 st = chunk_stats<false>(c[q], r.ws.ch, best, seg);
-                if (lane == 0) stats[r.first + i] = st;
+                for (int j = 0; j < Chunk<T>::LOADS; ++j)
+                    segs[(r.first + i) * Chunk<T>::LOADS + j] = seg[j];
             }
+        } else {
+            const float2 st = chunk_stats<false>(c, r.ws.ch, best, seg);
+            if (lane == 0) stats[r.first + i] = st;
         }
+        if (i + S * kWarps < r.mine)
+            ring.fetch(slot, r.x, r.V, r.first + i + S * kWarps, lane, r.vec);
+        cp_commit();
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
     // the other blocks are done once their part is out
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    if (rank != 0) return;
+    if (!lead) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1618,8 +1688,7 @@ __global__ void __launch_bounds__(kSearch, 2)
     uint32_t* own_n = cn + nch;
     const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int rank = blockIdx.x % ranks, tid = threadIdx.x;
-    // the scan's results are complete
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(logits);               // the scan's results are complete
     const uint32_t* modes = row_modes(a);
     bool table = false;
     uint32_t seen = 0;                   // rows to search before this batch
@@ -1664,8 +1733,7 @@ __global__ void __launch_bounds__(kExact, 1)
     const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int rank = blockIdx.x % ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kExpEntries; i += kExact) sh.table[i] = kExpTable.v[i];
-    // the scan's results are complete
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(logits);               // the scan's results are complete
     constexpr int kUnit = 128, kPerChunk = kChunk / kUnit, kAhead = 5, kUnits = kExact / 32;
     uint32_t seen = 0;
     for (int base = 0; base < a.N; base += kExact) {
@@ -1748,7 +1816,7 @@ __global__ void __launch_bounds__(kExact, 1)
 template <typename T>
 cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int),
                         const T* logits, const SampleArgs& a, int nch, int ranks, int clusters,
-                        int threads, size_t smem, bool dependent, cudaStream_t stream) {
+                        int threads, size_t smem, cudaStream_t stream) {
     const int own = (nch + ranks - 1) / ranks;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -1756,21 +1824,13 @@ cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * ranks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, logits, a, nch, own, ranks);
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = ranks;
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    return launch_early(kernel, dim3(static_cast<unsigned>(clusters) * ranks), threads, smem,
+                        stream, &cluster, logits, a, nch, own, ranks);
 }
 
 template <typename T>
@@ -1779,18 +1839,18 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
     cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, a.N, kThreads,
-                                scan_smem(nch, sizeof(T)), false, stream);
+                                scan_smem(nch, sizeof(T)), stream);
     if (e != cudaSuccess) return e;
     if (a.top_k_rows == nullptr && a.top_p_rows == nullptr && a.min_p_rows == nullptr &&
         (a.top_k == 0 || a.top_k >= a.V) && a.top_p_value >= 1.f && a.min_p_value == 0.f)
         // one block on each of 152 SMs
         return launch_rows(sample_exact_kernel<T>, logits, a, nch, ranks,
                            std::min(a.N, 152 / ranks), kExact,
-                           exact_smem((nch + ranks - 1) / ranks), true, stream);
+                           exact_smem((nch + ranks - 1) / ranks), stream);
     // two blocks of the search on each of 152 SMs
     const int clusters = std::min(a.N, 304 / ranks);
     return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, clusters, kSearch,
-                       search_smem(nch, (nch + ranks - 1) / ranks), true, stream);
+                       search_smem(nch, (nch + ranks - 1) / ranks), stream);
 }
 
 }  // namespace
