@@ -71,12 +71,13 @@ constexpr int kMaxSteps = 32;            // far more than any row takes
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
 
 // The fast weights' relative error, in units of 2^-24: 4 for ex2.approx, 9 roundings of a
-// chunk's sum, and log(2) t_i (1 for x - max, 2 for the product with a rounded c) for each
-// element: the weighted mean of t over 512 elements with sum s >= 1 is at most
-// log2(512 / s) <= 9, so 19; another 9 between a chunk's sum and the sums of its parts.
-// 42 in all, with the factor 2 u (1 - u) that a relative error of all weights leaves of
-// sum(prefix) - u sum(all) at its zero.
-constexpr float kFastErr = 42.f / 16777216.f;
+// chunk's sum, and log(2) t_i (1 for x - max, 1 for its product with c) for each element: the
+// weighted mean of t over 512 elements with sum s >= 1 is at most log2(512 / s) <= 9, so 12.5.
+// A relative error e of all weights leaves 2 u (1 - u) e of sum(prefix) - u sum(all) at its
+// zero.  The prefix inside a chunk is summed exactly: there up to kSumErr of the chunk's weight
+// comes on top.
+constexpr float kFastErr = 26.f / 16777216.f;
+constexpr float kSumErr = 9.f / 16777216.f;
 constexpr float kBinErr = 1.f / 4096.f;  // of a histogram's weight: 12-bit codes
 
 // Unsigned integers in the order of the floats; -0 and +0 get the same one.
@@ -463,11 +464,18 @@ __device__ __forceinline__ float* row_segs(const SampleArgs& a, int64_t row, int
            row * nch * kSegsPerChunk;
 }
 
+// log2(e) / T in two positive floats: a distance of -inf then stays one, where a negative or zero
+// second part would make it NaN.
+__device__ __forceinline__ float2 fast_scale(const Settings& s) {
+    const float below = __int_as_float(__float_as_int(s.ch) - 1);
+    return s.cl > 0.f ? make_float2(s.ch, s.cl) : make_float2(below, s.cl + (s.ch - below));
+}
+
 // Maximum and sum of a chunk.  The sum of 2^((x - max) c) leaves out one element of the
 // maximum (and has its sign bit set) where the chunk may hold the row's maximum: a total is
 // a sum of such parts plus the maximum's own weight.
 template <bool SEGMENTS, typename T>
-__device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float& best,
+__device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float2 scale, float& best,
                                               float (&seg)[Chunk<T>::LOADS]) {
     constexpr int VEC = Chunk<T>::VEC, LOADS = Chunk<T>::LOADS;
     float ml = -INFINITY, m = -INFINITY;
@@ -482,9 +490,15 @@ __device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float
     if (!SEGMENTS) m = warp_max(ml);
     // a chunk of -inf has sum 0; NaN or +inf make it NaN
     const float mm = fmaxf(m, -3.402823466e38f);
-    float s[kLane];
+    float2 s[kLane / 2];
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) s[e] = ex2_approx((c.get(e) - mm) * ch);
+    for (int e = 0; e < kLane / 2; ++e) {
+        const float2 d = __fadd2_rn(make_float2(c.get(2 * e), c.get(2 * e + 1)),
+                                    make_float2(-mm, -mm));
+        const float2 t = __ffma2_rn(d, make_float2(scale.x, scale.x),
+                                    __fmul2_rn(d, make_float2(scale.y, scale.y)));
+        s[e] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    }
     // only a chunk that holds the warp's largest so far can hold the row's maximum
     const bool apart = m >= best && m < INFINITY && m > -INFINITY;
     if (apart) {
@@ -492,16 +506,17 @@ __device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float ch, float
         bool lead = (threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, ml == m)) - 1;
 #pragma unroll
         for (int e = 0; e < kLane; ++e) {
+            float& w = e % 2 == 0 ? s[e / 2].x : s[e / 2].y;
             const bool hit = lead && c.get(e) == m;
-            s[e] = hit ? 0.f : s[e];
+            w = hit ? 0.f : w;
             lead = lead && !hit;
         }
     }
 #pragma unroll
-    for (int w = kLane / 2; w > 0; w >>= 1)
+    for (int w = kLane / 4; w > 0; w >>= 1)
 #pragma unroll
-        for (int e = 0; e < w; ++e) s[e] += s[e + w];
-    const float sum = warp_sum(s[0]);
+        for (int e = 0; e < w; ++e) s[e] = __fadd2_rn(s[e], s[e + w]);
+    const float sum = warp_sum(s[0].x + s[0].y);
     return make_float2(m, apart ? -sum : sum);
 }
 
@@ -530,12 +545,15 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
     const float x1 = col + 1 < r.V ? load_one(r.x + col + 1) : -INFINITY;
     const float m = cmax[chunk];
     const u64 top = fixed_weight(m, r.ws, sh.table);
-    const u64 w0 = scale_weight(ex2_approx((x0 - m) * r.ws.ch), top);
-    const u64 w1 = scale_weight(ex2_approx((x1 - m) * r.ws.ch), top);
+    const float2 scale = fast_scale(s);
+    const float d0 = x0 - m, d1 = x1 - m;
+    const u64 w0 = scale_weight(ex2_approx(fmaf(d0, scale.x, d0 * scale.y)), top);
+    const u64 w1 = scale_weight(ex2_approx(fmaf(d1, scale.x, d1 * scale.y)), top);
     const u64 lo = sh.at_w + block_scan<kThreads>(w0 + w1, 0, sh.part, sh.part_n).v;
     const u64 mid = lo + w0, hi = mid + w1;
     const float part = 2.f * s.u_value * (1.f - s.u_value) * kFastErr + 1.5e-11f;
-    const u64 err = static_cast<u64>(static_cast<float>(all) * part) + 8192;
+    const u64 err = static_cast<u64>(static_cast<float>(all) * part) +
+                    static_cast<u64>(static_cast<float>(cw[chunk]) * kSumErr) + 8192;
     const bool hit0 = lo <= target && (lo == 0 || lo + err <= target) && target + err < mid;
     const bool hit1 = mid <= target && (mid == 0 || mid + err <= target) && target + err < hi;
     if (hit0 || hit1) {
@@ -863,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
     const bool cut = s.want_k || s.want_p || s.want_m;
     float* segs = row_segs(a, row_i, nch);
+    const float2 scale = fast_scale(s);
     float best = -INFINITY;
     int slot = 0;
 #pragma unroll 1
@@ -872,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 4)
         ring.read(slot, c);
         float seg[Chunk<T>::LOADS];
         if (cut) {
-            const float2 st = chunk_stats<true>(c, r.ws.ch, best, seg);
+            const float2 st = chunk_stats<true>(c, scale, best, seg);
             if (lane == 0) {
                 stats[r.first + i] = st;
 #pragma unroll
@@ -880,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 4)
                     segs[(r.first + i) * Chunk<T>::LOADS + j] = seg[j];
             }
         } else {
-            const float2 st = chunk_stats<false>(c, r.ws.ch, best, seg);
+            const float2 st = chunk_stats<false>(c, scale, best, seg);
             if (lane == 0) stats[r.first + i] = st;
         }
         if (i + S * kWarps < r.mine)
@@ -948,33 +967,33 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ----------------------------------------------------------------------------- search
 
-// Cluster c of `clusters` takes the rows to search whose number among them is c modulo
-// clusters: every block counts them out of the rows' modes, so the rows are spread evenly
-// without a counter.  The rows of the batch base .. base + THREADS - 1 that are this
-// cluster's: their number, places in queue.
+// The rows to search of the batch base .. base + THREADS - 1 are dealt to groups of `group`
+// blocks: every block counts them out of the rows' modes, and group g of G takes those whose
+// number among them is g modulo G.  So they are spread evenly without a counter.  A group is a
+// cluster, or (PARTED) a part of one where there are more rows than clusters.
 struct Queue {
-    uint32_t n;
-    uint16_t at[kExact];
+    uint32_t n;                          // rows of this block's group
+    uint16_t at[kExact];                 // their places in the batch
 };
-template <int THREADS>
-__device__ uint32_t queue_rows(const uint32_t* modes, int N, int base, uint32_t cluster,
-                               uint32_t clusters, uint32_t& seen, Queue& queue, u64* part,
-                               uint32_t* part_n) {
+// Returns the most rows that a group has.
+template <int THREADS, bool PARTED>
+__device__ uint32_t queue_rows(const uint32_t* modes, int N, int base, uint32_t ranks,
+                               uint32_t& group, Queue& queue, u64* part, uint32_t* part_n) {
     const int tid = threadIdx.x;
     const bool hard = base + tid < N && modes[base + tid] == kRowSearch;
     if (!__syncthreads_or(hard)) return 0;
     if (tid == 0) queue.n = 0;
     const Scanned s = block_scan<THREADS>(0, hard ? 1 : 0, part, part_n);
-    const uint32_t number = seen + s.n;
-    if (hard && number % clusters == cluster) {
-        // the first of the batch's numbers that are this cluster's comes first
-        const uint32_t first = (seen + clusters - 1 - cluster) / clusters;
-        queue.at[(number - cluster) / clusters - first] = static_cast<uint16_t>(tid);
+    group = ranks;
+    if (PARTED)
+        while (group > 1 && s.tn > gridDim.x / group) group /= 2;
+    const uint32_t groups = gridDim.x / group;
+    if (hard && s.n % groups == blockIdx.x / group) {
+        queue.at[s.n / groups] = static_cast<uint16_t>(tid);
         atomicAdd(&queue.n, 1u);
     }
-    seen += s.tn;
     __syncthreads();
-    return queue.n;
+    return (s.tn + groups - 1) / groups;
 }
 
 // A step that block 0 asks of all blocks.  Elements are above, inside or below a window of
@@ -1390,11 +1409,13 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     if (!keys) {
         // the keys of exactly these bins: the lowest of bin j2 or above, and the highest of
         // bin j1 or below
+        const uint32_t bottom = kKeyNegInf + 1, top = order_key(r.ws.m);
         if (threadIdx.x < 32) {
-            const uint32_t lo = first_key(r, kKeyNegInf + 1, order_key(r.ws.m), j2);
-            const uint32_t hi = j1 == 0 || whole ? order_key(r.ws.m)
-                                                 : first_key(r, lo, order_key(r.ws.m), j1 - 1) - 1;
-            if (threadIdx.x == 0) sh.at = static_cast<int>(lo), sh.at2 = static_cast<int>(hi);
+            const uint32_t lo = first_key(r, bottom, top, j2);
+            if (threadIdx.x == 0) sh.at = static_cast<int>(lo);
+        } else if (threadIdx.x < 64) {
+            const uint32_t hi = j1 == 0 || whole ? top : first_key(r, bottom, top, j1 - 1) - 1;
+            if (threadIdx.x == 32) sh.at2 = static_cast<int>(hi);
         }
         __syncthreads();
         cmd.klo = static_cast<uint32_t>(sh.at);
@@ -1686,15 +1707,15 @@ __global__ void __launch_bounds__(kSearch, 2)
     float* cmax = reinterpret_cast<float*>(own_w + own);         // all chunks: maximum
     uint32_t* cn = reinterpret_cast<uint32_t*>(cmax + nch);      //             ties
     uint32_t* own_n = cn + nch;
-    const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int rank = blockIdx.x % ranks, tid = threadIdx.x;
     wait_previous(logits);               // the scan's results are complete
     const uint32_t* modes = row_modes(a);
     bool table = false;
-    uint32_t seen = 0;                   // rows to search before this batch
     for (int base = 0; base < a.N; base += kSearch) {
-        const uint32_t n = queue_rows<kSearch>(modes, a.N, base, cluster, clusters, seen, sh.queue,
-                                               sh.part, sh.part_n);
+        uint32_t group;
+        const bool any = queue_rows<kSearch, false>(modes, a.N, base, ranks, group, sh.queue, sh.part,
+                                                    sh.part_n) > 0;
+        const uint32_t n = any ? sh.queue.n : 0;
         if (n > 0 && !table) {
             for (int i = tid; i < kExpEntries; i += kSearch) sh.table[i] = kExpTable.v[i];
             table = true;
@@ -1719,27 +1740,34 @@ struct Shared1 {
     int at;
     Queue queue;
 };
-__host__ __device__ constexpr size_t exact_smem(int own) {
-    return sizeof(Shared1) + size_t(own) * 8 + 16;
+__host__ __device__ constexpr size_t exact_smem(int nch) {
+    return sizeof(Shared1) + size_t(nch) * 8 + 16;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kExact, 1)
-    sample_exact_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int own,
-                        int ranks) {
+    sample_exact_kernel(const T* __restrict__ logits, const SampleArgs a, int nch, int, int ranks) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared1& sh = *reinterpret_cast<Shared1*>(smem);
     u64* own_w = reinterpret_cast<u64*>(smem + sizeof(Shared1));
-    const uint32_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
-    const int rank = blockIdx.x % ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < kExpEntries; i += kExact) sh.table[i] = kExpTable.v[i];
     wait_previous(logits);               // the scan's results are complete
     constexpr int kUnit = 128, kPerChunk = kChunk / kUnit, kAhead = 5, kUnits = kExact / 32;
-    uint32_t seen = 0;
     for (int base = 0; base < a.N; base += kExact) {
-        const uint32_t n = queue_rows<kExact>(row_modes(a), a.N, base, cluster, clusters, seen,
-                                              sh.queue, sh.part, sh.part_n);
+        uint32_t group = 1;
+        const uint32_t n = queue_rows<kExact, true>(row_modes(a), a.N, base, ranks, group, sh.queue,
+                                                    sh.part, sh.part_n);
+        const int own = (nch + group - 1) / group;
+        const uint32_t rank = blockIdx.x % group, first = blockIdx.x % ranks - rank;
+        // the blocks of a cluster keep step: the last time a group may be without a row
         for (uint32_t q = 0; q < n; ++q) {
+            const bool on = q < sh.queue.n;
+            if (!on) {
+                cluster_join();
+                cluster_join();
+                continue;
+            }
             const int64_t row_i = int64_t(base) + sh.queue.at[q];
             const Settings s = read_settings(a, row_i);
             Row<T> r = make_row(logits, a, row_i, s, nch, own, rank);
@@ -1788,14 +1816,14 @@ __global__ void __launch_bounds__(kExact, 1)
                 const int each = (nch + kExact - 1) / kExact;
                 const int c0 = min(nch, tid * each), c1 = min(nch, c0 + each);
                 u64 w = 0;
-                for (int c = c0; c < c1; ++c) w += peer(own_w, c / own)[c % own];
+                for (int c = c0; c < c1; ++c) w += peer(own_w, first + c / own)[c % own];
                 const Scanned t = block_scan<kExact>(w, 0, sh.part, sh.part_n);
                 const u64 target = part_of(s.u, t.tv, false);
                 if (tid == 0) sh.at = 0, sh.at_w = 0;
                 __syncthreads();
                 u64 run = t.v;
                 for (int c = c0; c < c1; ++c) {
-                    const u64 cw = peer(own_w, c / own)[c % own];
+                    const u64 cw = peer(own_w, first + c / own)[c % own];
                     if (run <= target && target < run + cw) sh.at = c, sh.at_w = run;
                     run += cw;
                 }
@@ -1838,19 +1866,35 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int nch = (a.V + kChunk - 1) / kChunk;
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, ranks, a.N, kThreads,
+    // As many blocks a row as run at the same time, four on each of 152 SMs: more of them, one
+    // after the other, start anew with nothing on its way (at V = 151936, [256] fp32 61.8 instead
+    // of 58.9 us, [1024] 196.8 instead of 186.7; [1024] bf16 with top_k and top_p 146 instead of 98).
+    int scan_ranks = ranks;
+    while (scan_ranks > 1 && int64_t(a.N) * scan_ranks > 608) scan_ranks /= 2;
+    cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, scan_ranks, a.N, kThreads,
                                 scan_smem(nch, sizeof(T)), stream);
     if (e != cudaSuccess) return e;
     if (a.top_k_rows == nullptr && a.top_p_rows == nullptr && a.min_p_rows == nullptr &&
-        (a.top_k == 0 || a.top_k >= a.V) && a.top_p_value >= 1.f && a.min_p_value == 0.f)
-        // one block on each of 152 SMs
+        (a.top_k == 0 || a.top_k >= a.V) && a.top_p_value >= 1.f && a.min_p_value == 0.f) {
+        // One block on each of 152 SMs, which may come to weigh a whole row.
         return launch_rows(sample_exact_kernel<T>, logits, a, nch, ranks,
-                           std::min(a.N, 152 / ranks), kExact,
-                           exact_smem((nch + ranks - 1) / ranks), stream);
-    // two blocks of the search on each of 152 SMs
-    const int clusters = std::min(a.N, 304 / ranks);
-    return launch_rows(sample_search_kernel<T>, logits, a, nch, ranks, clusters, kSearch,
-                       search_smem(nch, (nch + ranks - 1) / ranks), stream);
+                           std::min(a.N, 152 / ranks), kExact, exact_smem(nch), stream);
+    }
+    // The search: two blocks on each of 152 SMs, and smaller clusters where more rows than clusters
+    // are to be expected: nearly all rows where a wide nucleus is all that cuts, about a fifth where
+    // each row brings its own settings, few otherwise.  fp32, V = 151936, top_p alone, with 8, 4, 2
+    // and 1 blocks a row: [1] 56, 67, 93, 141 us; [64] 208, 173, 195, 282; [256] 764, 483, 431, 464;
+    // bf16 [256] 724, 535, 544, 724.
+    const bool own_settings =
+        a.top_k_rows != nullptr || a.top_p_rows != nullptr || a.min_p_rows != nullptr;
+    const bool listed =
+        a.min_p_value > 0.f || (a.top_k > 0 && a.top_k <= segments_of(nch, sizeof(T)) / 2);
+    const int64_t expected = own_settings ? a.N / 4 : listed ? 0 : a.N;
+    int search_ranks = ranks;
+    while (search_ranks > 2 && expected * search_ranks > 304) search_ranks /= 2;
+    return launch_rows(sample_search_kernel<T>, logits, a, nch, search_ranks,
+                       std::min(a.N, 304 / search_ranks), kSearch,
+                       search_smem(nch, (nch + search_ranks - 1) / search_ranks), stream);
 }
 
 }  // namespace
