@@ -269,14 +269,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# the current stream's handle without building a torch Stream object (2.8 us a call)
+# the current stream's handle without building a torch Stream object (2.8 us a call); the
+# device's number as torch.cuda.current_device() gives it once a CUDA tensor exists
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -686,7 +688,10 @@ def _dtype_code(t, name):
 
 
 def _need_rows(t, name, shape=None, dtype=None):
-    """Row stride of a 2-D CUDA tensor with contiguous rows (any stride between them)."""
+    """(n, h, row stride) of a 2-D CUDA tensor with contiguous rows, at any distance."""
+    if (shape is not None and t.shape == shape and t.dtype is dtype and t.is_cuda
+            and t.is_contiguous()):
+        return shape[0], shape[1], shape[1]
     if dtype is not None and t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_cuda or t.dim() != 2:
@@ -695,25 +700,24 @@ def _need_rows(t, name, shape=None, dtype=None):
     if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), (n, h)))
     if t.is_contiguous():
-        return h                                  # also a single row, whose stride says nothing
+        return n, h, h                            # also a single row, whose stride says nothing
     sn, sh = t.stride()
     if h > 1 and sh != 1:
         raise ValueError("%s must have contiguous rows" % name)
     if n == 1:
-        return h
+        return n, h, h
     if sn < h:
         raise ValueError("%s must not have overlapping rows" % name)
-    return sn
+    return n, h, sn
 
 
 def _need_norm(x, weight, active_mask):
     """(n, h, x's row stride) of the arguments that every norm call has."""
-    stride = _need_rows(x, "x")
-    n, h = x.shape
-    _need(weight, weight.dtype, "weight", (h,))
+    rows = _need_rows(x, "x")
+    _need(weight, weight.dtype, "weight", rows[1:2])
     if active_mask is not None:
-        _need(active_mask, torch.uint8, "active_mask", (n,))
-    return n, h, stride
+        _need(active_mask, torch.uint8, "active_mask", rows[:1])
+    return rows
 
 
 def rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd, stream=None):
@@ -722,7 +726,7 @@ def rlk_layer_norm_fwd(x, weight, bias, active_mask, eps, y, mean, rstd, stream=
     n, h, sx = _need_norm(x, weight, active_mask)
     if bias is not None:
         _need(bias, weight.dtype, "bias", (h,))
-    sy = _need_rows(y, "y", (n, h), x.dtype)
+    sy = _need_rows(y, "y", (n, h), x.dtype)[2]
     if mean is not None:
         _need(mean, torch.float32, "mean", (n,))
     if rstd is not None:
@@ -738,8 +742,8 @@ def rlk_layer_norm_bwd(x, weight, dy, mean, rstd, active_mask, dx, dweight, dbia
                        stream=None):
     """Enqueue the layer norm's backward; dweight and dbias may be None.  See include/rlk.h."""
     n, h, sx = _need_norm(x, weight, active_mask)
-    sg = _need_rows(dy, "dy", (n, h), x.dtype)
-    sd = _need_rows(dx, "dx", (n, h), x.dtype)
+    sg = _need_rows(dy, "dy", (n, h), x.dtype)[2]
+    sd = _need_rows(dx, "dx", (n, h), x.dtype)[2]
     _need(mean, torch.float32, "mean", (n,))
     _need(rstd, torch.float32, "rstd", (n,))
     for t, name in ((dweight, "dweight"), (dbias, "dbias")):
@@ -757,7 +761,7 @@ def rlk_layer_norm_bwd(x, weight, dy, mean, rstd, active_mask, dx, dweight, dbia
 def rlk_rms_norm_fwd(x, weight, active_mask, eps, y, rstd, stream=None):
     """Enqueue the RMS norm of x [N, H]; active_mask and rstd may be None.  See include/rlk.h."""
     n, h, sx = _need_norm(x, weight, active_mask)
-    sy = _need_rows(y, "y", (n, h), x.dtype)
+    sy = _need_rows(y, "y", (n, h), x.dtype)[2]
     if rstd is not None:
         _need(rstd, torch.float32, "rstd", (n,))
     st = load().rlk_rms_norm_fwd(_ptr(x), _dtype_code(x, "x"), sx, _ptr(weight),
@@ -769,8 +773,8 @@ def rlk_rms_norm_fwd(x, weight, active_mask, eps, y, rstd, stream=None):
 def rlk_rms_norm_bwd(x, weight, dy, rstd, active_mask, dx, dweight, workspace, stream=None):
     """Enqueue the RMS norm's backward; dweight may be None.  See include/rlk.h."""
     n, h, sx = _need_norm(x, weight, active_mask)
-    sg = _need_rows(dy, "dy", (n, h), x.dtype)
-    sd = _need_rows(dx, "dx", (n, h), x.dtype)
+    sg = _need_rows(dy, "dy", (n, h), x.dtype)[2]
+    sd = _need_rows(dx, "dx", (n, h), x.dtype)[2]
     _need(rstd, torch.float32, "rstd", (n,))
     if dweight is not None:
         _need(dweight, weight.dtype, "dweight", (h,))
@@ -813,8 +817,7 @@ def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, 
     """Draw one token a row of logits [N, V] (fp32 or bf16, rows contiguous, any row stride).
     temperature, top_p, min_p: a number or a float32 tensor [N]; top_k: a number or an int32
     tensor [N].  active_mask, logp, kept_logp may be None.  See include/rlk.h."""
-    stride = _need_rows(logits, "logits")
-    n, v = logits.shape
+    n, v, stride = _need_rows(logits, "logits")
     _need(uniforms, torch.float32, "uniforms", (n,))
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
