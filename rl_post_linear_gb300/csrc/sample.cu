@@ -1025,10 +1025,10 @@ struct Shared {
     uint32_t part_n[kSearch / 32];
     u64 own_above, own_total;            // exact weights, all own chunks
     uint32_t own_count;
-    uint32_t n_list, key_m;
+    uint32_t n_list, n_few, key_m;
     Queue queue;
     // results of block-wide searches
-    u64 at_w;
+    u64 at_w, width;
     uint32_t at_n;
     int at, at2;
     Cmd cmd;
@@ -1174,8 +1174,9 @@ __device__ __noinline__ void step_collect(const Row<T>& row, const Cmd& command,
 
 // Selection in the merged list, whose keys lie in [lo, hi]: the key at which the count (or
 // weight) of the elements from the top reaches `need` >= 1, and count and weight above that
-// key.  Histograms of 1024 bins of the keys' range, then of the bin's: equal parts of the
-// range keep the atomics of one bin few, where digits of the keys would not.
+// key.  A histogram of 1024 bins of the keys' range, then of the bin's, until a warp can order
+// what is left (at once, nearly always): equal parts of the range keep the atomics of one bin
+// few, where digits of the keys would not.
 struct Selected {
     uint32_t key;
     u64 n, w;
@@ -1186,6 +1187,7 @@ __device__ __noinline__ Selected list_select(const Row<T>& row, bool by_weight, 
     const WeightScale ws = row.ws;
     u64 n_up = 0, w_up = 0;
     int shift;
+    if (threadIdx.x == 0) sh.n_few = 0;
 #pragma unroll 1
     do {
         shift = max(0, 22 - __clz(hi - lo));         // (hi - lo) >> shift < 1024
@@ -1225,9 +1227,46 @@ __device__ __noinline__ Selected list_select(const Row<T>& row, bool by_weight, 
         const uint32_t top = hi - (at << shift);
         lo = max(lo, top - ((1u << shift) - 1));
         hi = top;
-    } while (shift > 0);
+    } while (shift > 0 && sh.cnt[sh.at] > 32);
+    if (shift == 0) {
+        __syncthreads();
+        return Selected{hi, n_up, w_up};
+    }
+    uint32_t* few = sh.lo;
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSearch) {
+        const uint32_t k = sh.key[i];
+        if (k >= lo && k <= hi) few[atomicAdd(&sh.n_few, 1u)] = k;
+    }
     __syncthreads();
-    return Selected{hi, n_up, w_up};
+    if (threadIdx.x < 32) {
+        const uint32_t n = sh.n_few;
+        const uint32_t k = threadIdx.x < n ? few[threadIdx.x] : 0;
+        const u64 w = threadIdx.x < n ? fixed_weight(key_value(k), ws, sh.table) : 0;
+        uint32_t n_above = 0, n_to = 0;
+        u64 w_above = 0, w_to = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < n; ++j) {
+            const uint32_t kj = __shfl_sync(0xffffffffu, k, j);
+            const u64 wj = __shfl_sync(0xffffffffu, w, j);
+            n_above += kj > k ? 1u : 0u;
+            n_to += kj >= k ? 1u : 0u;
+            w_above += kj > k ? wj : 0;
+            w_to += kj >= k ? wj : 0;
+        }
+        const u64 c0 = by_weight ? w_up + w_above : n_up + n_above;
+        const u64 c1 = by_weight ? w_up + w_to : n_up + n_to;
+        // lanes of equal keys write the same
+        if (threadIdx.x < n && c0 < need && c1 >= need) {
+            sh.at = static_cast<int>(k);
+            sh.at_w = w_up + w_above;
+            sh.at_n = static_cast<uint32_t>(n_up) + n_above;
+        }
+    }
+    __syncthreads();
+    const Selected r{static_cast<uint32_t>(sh.at), sh.at_n, sh.at_w};
+    __syncthreads();
+    return r;
 }
 
 // What block 0 carries from step to step (uniform over its threads).
@@ -1352,7 +1391,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     const u64 before = block_scan<kSearch>(mine, 0, sh.part, sh.part_n).v;
     // the first bins at which the running sum surely may, and surely must, have reached the
     // need
-    if (threadIdx.x == 0) sh.at = sh.at2 = kBins, sh.at_w = 0;
+    if (threadIdx.x == 0) sh.at = sh.at2 = kBins, sh.at_w = sh.width = 0;
     __syncthreads();
     u64 need_lo = P.top_k, need_hi = P.top_k, base = P.n_above;
     float err = 0.f;
@@ -1388,7 +1427,9 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
         if (b0 + i >= j1 && b0 + i <= j2) est += q[i];
-    est = block_scan<kSearch>(est, 0, sh.part, sh.part_n).tv;
+    if (est != 0) atomicAdd(&sh.width, est);         // by few threads
+    __syncthreads();
+    est = sh.width;
     if (cmd.by_weight) est = est / 3600 + 1;
     if (at == kBins) {
         // fewer elements of weight > 0 than top_k: nothing is cut (a weight is reached)
