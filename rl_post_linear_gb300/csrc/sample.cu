@@ -18,27 +18,35 @@
 // is sorted.  Sums that decide are integers (weight_exp.cuh), so the token depends on the
 // row alone: not on the batch, on how the row is split, or on the alignment.
 //
-// Two launches.  The scan: a cluster of up to 8 blocks a row, a warp a chunk of 512
-// columns; per chunk its maximum and an fp32 sum of 2^((x - chunk max) c), c = log2(e)/T,
-// go to the workspace.  This is the only pass over HBM.  The cluster's block 0 then forms
-// the chunks' weights as integers, in the same order whatever the split, and finishes the
-// rows that need no further pass over all columns:
+// Two launches.  The scan: up to 8 blocks a row (a cluster), a warp a chunk of 512 columns;
+// per chunk its maximum and an fp32 sum of 2^((x - chunk max) c), c = log2(e)/T, and with
+// truncation the maxima of its segments of 128 or 256 columns, go to the workspace.  This is
+// the only pass over HBM.  One block of the cluster then forms the chunks' weights as
+// integers, in the same order whatever the split, and finishes the rows that need no further
+// pass over all columns:
 //
 //   no truncation: the chunk and the element that u times the total falls on come from the
 //   fast weights, together with a bound on their error (kFastErr); only when the target lies
-//   within it of a border of the running sums -- some percent of the rows at V ~ 150k --
-//   does the row go on to the search, which weighs it exactly.
+//   within it of a border of the running sums -- one row in twenty at V ~ 150k -- is the row
+//   left open.
 //
-//   truncation: elements from some value on are gathered from the chunks whose maximum
-//   reaches it, and their order is counted out in place.  The value is one that K chunk
-//   maxima reach (top_k), that chunk maxima of top_p of the total reach, or min_p's own; in
-//   rows in no particular order few other elements reach it.
+//   truncation: elements from some value on are gathered from the segments whose maximum
+//   reaches it, and their order is counted out.  The value is one that top_k segment maxima
+//   reach, that segment maxima of top_p of the total reach, or min_p's own; in rows in no
+//   particular order few other elements reach it.
 //
-// The search takes the rows that are left (a wide nucleus, a large top_k, a row sorted by
-// token, a target near a border), again a cluster a row: histograms of 2048 bins of the
-// scaled distance from the maximum, then of the keys inside the remaining window, close in
-// on the boundary until its window fits a list or is a single value.  Block 0 of the
-// cluster decides each step; the blocks work on their own chunks in between.
+// The second launch takes the rows that are left.  Without truncation they are weighed
+// exactly.  With it (a wide nucleus, a large top_k, a row sorted by token) they are searched:
+// histograms of 2048 bins of the scaled distance from the maximum, then of the keys inside
+// the remaining window, close in on the boundary until its window fits a list or is a single
+// value.  One block of the cluster decides each step; the blocks work on their own chunks in
+// between.
+//
+// Measured at V = 151936, fp32 (HBM's floor in brackets): one row 10.2 us; [256] 54 us (23),
+// of which the scan takes 33 and the rows weighed exactly 17; [64] with top_k = 50 and top_p
+// 24 us (5.7); [1024] 139 us (92).  A row with a wide nucleus takes 55 us by itself, 256 of
+// them 426 us: 168 instructions an element in all, and block 0's decisions, for which the
+// other blocks wait, bind the search, not memory.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -62,9 +70,9 @@ constexpr int kExact = 1024;             // of a block that weighs rows exactly
 constexpr int kChunk = 512;              // columns of a chunk
 constexpr int kLane = kChunk / 32;       // of a lane
 constexpr int kBins = 2048;
-constexpr int kSelect = 1024;            // bins of the selection in it
 constexpr int kList = 1920;              // elements of the search's list
-constexpr int kShort = 1024;             // of the scan's list, sorted in place
+constexpr int kSelect = 1024;            // bins of the selection in it
+constexpr int kShort = 1024;             // of the scan's list
 constexpr int kMaxSegments = 8192;       // of a row whose truncation the scan tries itself
 constexpr float kRange = 48.f;           // weights below 2^-47 round to 0 (bits <= 46)
 constexpr int kMaxSteps = 32;            // far more than any row takes
@@ -246,8 +254,8 @@ struct Chunk {
 
 // A warp's part of a ring of chunks in shared memory, on their way while another is worked on.
 // Each lane copies just what it reads itself, so this needs no barrier: group j of slot s lies
-// at (LOADS s + j) 32 + lane.  Two chunks of fp32: with three, an SM holds fewer blocks (the pass
-// alone 38.2 instead of 36.6 us at [256, 151936]).
+// at (LOADS s + j) 32 + lane.  Two chunks of fp32: with three, an SM holds three blocks instead of
+// four (67 instead of 54 us at [256, 151936]).
 constexpr int kRing = 4096;              // bytes of a warp
 template <typename T>
 struct Ring {
@@ -396,7 +404,7 @@ __device__ __noinline__ void write_row(const SampleArgs& a, int64_t row, int64_t
     if (a.kept_logp != nullptr) a.kept_logp[row] = kept_logp;
 }
 
-// a row without a result, by one thread of block 0
+// a row without a result, by one thread
 __device__ __forceinline__ void write_failed(const SampleArgs& a, int64_t row, uint32_t bit) {
     write_row(a, row, -1, quiet_nan(), quiet_nan());
     if (a.err != nullptr) atomicOr(a.err, bit);
@@ -836,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const int rank = blockIdx.x % ranks;             // = the block's rank in its cluster
     // The block that finishes the row.  Not always the same one of its cluster: clusters that
     // follow each other on the same SMs would then finish their rows on the same few of them
-    // (31.0 instead of 26.6 us at [64, 151936] with top_k and top_p).
+    // (28.4 instead of 23.9 us at [64, 151936] with top_k and top_p).
     const bool lead = rank == static_cast<int>(row_i % ranks);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     RowHeader* head = static_cast<RowHeader*>(a.workspace) + row_i;
@@ -1050,7 +1058,8 @@ __device__ __forceinline__ void window_of(const Cmd& cmd, float& lo, float& hi) 
     hi = none ? -INFINITY : khi > order_key(INFINITY) ? INFINITY : key_value(khi);
 }
 
-// Histogram of the window; for windows of keys also the exact weight above it.
+// Histogram of the window; for windows of keys also the exact weight above it.  About 9 us over 8
+// blocks at V = 151936: shared-memory atomics and conversions bind it.
 template <typename T>
 __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, const float* cmax,
                                        Shared& sh) {
@@ -1112,7 +1121,8 @@ __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, co
     __syncthreads();
 }
 
-// Exact weight above the window, per chunk, and the elements inside it.
+// Exact weight above the window, per chunk, and the elements inside it.  About 13 us over 8 blocks
+// at V = 151936: the 64-bit arithmetic of the weights binds it.
 template <typename T>
 __device__ __noinline__ void step_collect(const Row<T>& row, const Cmd& command, const float* cmax,
                                           u64* own_w, uint32_t* own_n, Shared& sh) {
@@ -1770,8 +1780,10 @@ __global__ void __launch_bounds__(kSearch, 2)
 
 // ----------------------------------------------------------------------------- exact draw
 
-// The search of a call without any truncation: its rows are those whose target lies near a
-// border, few of them, and what counts is how soon each is done.  Every weight of the row is
+// The second launch of a call without any truncation: its rows are those whose target lies near
+// a border, few of them, and what counts is how soon each is done: 1024 threads a block, up to 8
+// blocks a row (17 us for the 12 rows or so of [256, 151936]).  With more rows than clusters, a
+// row gets fewer blocks ([1024, 151936] 139 us, 168 with 8 each).  Every weight of the row is
 // formed exactly; a warp takes 128 columns at a time.
 struct Shared1 {
     u64 table[kExpEntries];
@@ -1908,8 +1920,9 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
     // As many blocks a row as run at the same time, four on each of 152 SMs: more of them, one
-    // after the other, start anew with nothing on its way (at V = 151936, [256] fp32 61.8 instead
-    // of 58.9 us, [1024] 196.8 instead of 186.7; [1024] bf16 with top_k and top_p 146 instead of 98).
+    // after the other, start anew with nothing on its way (with 8 at V = 151936, [256] fp32 takes
+    // 56.5 instead of 53.8 us, [1024] 148 instead of 139, [1024] bf16 with top_k and top_p 145
+    // instead of 96).
     int scan_ranks = ranks;
     while (scan_ranks > 1 && int64_t(a.N) * scan_ranks > 608) scan_ranks /= 2;
     cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, scan_ranks, a.N, kThreads,
@@ -1923,9 +1936,9 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     }
     // The search: two blocks on each of 152 SMs, and smaller clusters where more rows than clusters
     // are to be expected: nearly all rows where a wide nucleus is all that cuts, about a fifth where
-    // each row brings its own settings, few otherwise.  fp32, V = 151936, top_p alone, with 8, 4, 2
-    // and 1 blocks a row: [1] 56, 67, 93, 141 us; [64] 208, 173, 195, 282; [256] 764, 483, 431, 464;
-    // bf16 [256] 724, 535, 544, 724.
+    // each row brings its own settings, few otherwise.  V = 151936, top_p alone, with 8, 4, 2 and 1
+    // blocks a row: fp32 [1] 55, 66, 92, 140 us; [64] 205, 171, 192, 280; [256] 744, 476, 426, 461;
+    // bf16 [256] 653, 420, 352, 396.
     const bool own_settings =
         a.top_k_rows != nullptr || a.top_p_rows != nullptr || a.min_p_rows != nullptr;
     const bool listed =
