@@ -343,6 +343,7 @@ struct SampleArgs {
     int N, V;
     int bits;                  // weights are scaled by 2^bits; V 2^bits < 2^64
     bool vec_ok;               // rows start on 16 bytes
+    int parts;                 // segments of a chunk of the scan (the launcher sets it)
     int64_t* tokens;
     float* logp;               // or nullptr
     float* kept_logp;          // or nullptr

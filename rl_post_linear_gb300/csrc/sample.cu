@@ -74,6 +74,7 @@ constexpr int kList = 1920;              // elements of the search's list
 constexpr int kSelect = 1024;            // bins of the selection in it
 constexpr int kShort = 1024;             // of the scan's list
 constexpr int kMaxSegments = 8192;       // of a row whose truncation the scan tries itself
+constexpr int kMaxShortK = 700;          // and its top_k, with finer segments
 constexpr float kRange = 48.f;           // weights below 2^-47 round to 0 (bits <= 46)
 constexpr int kMaxSteps = 32;            // far more than any row takes
 constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
@@ -202,15 +203,21 @@ __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_
 
 // ----------------------------------------------------------------------------- rows
 
-// 16 bytes of a row from column c on, -inf past its end.
+// 16 bytes of a row from column c on, -inf past its end.  Not inlined where they come one by
+// one: there are many such loads in code that is better short.
 template <typename T>
-__device__ __forceinline__ uint4 load_group(const T* row, int V, int c, bool vec) {
+__device__ __noinline__ uint4 load_single(const T* row, int V, int c) {
     constexpr int VEC = 16 / sizeof(T);
-    if (vec && c + VEC <= V) return __ldg(reinterpret_cast<const uint4*>(row + c));
     T v[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = c + e < V ? row[c + e] : T(-INFINITY);
     return *reinterpret_cast<const uint4*>(v);
+}
+template <typename T>
+__device__ __forceinline__ uint4 load_group(const T* row, int V, int c, bool vec) {
+    constexpr int VEC = 16 / sizeof(T);
+    if (vec && c + VEC <= V) return __ldg(reinterpret_cast<const uint4*>(row + c));
+    return load_single(row, V, c);
 }
 template <typename T>
 __device__ __forceinline__ float group_value(const uint4& g, int i) {
@@ -225,8 +232,6 @@ template <typename T>
 struct Chunk {
     static constexpr int VEC = 16 / sizeof(T);
     static constexpr int LOADS = kLane / VEC;
-    // columns of a segment: what one load of the warp covers
-    static constexpr int SEG = 32 * VEC;
     uint4 raw[LOADS];
 
     __device__ __forceinline__ static int column(int chunk, int j, int lane) {
@@ -453,7 +458,26 @@ struct RowHeader {
 __host__ __device__ constexpr size_t modes_offset(int64_t N) {
     return (size_t(N) * sizeof(RowHeader) + 255) / 256 * 256;
 }
-constexpr int kSegsPerChunk = kChunk / 128;
+// Segments of a row: parts of a chunk each.  What one load of the warp covers (parts 0: one
+// reduction gives their maximum), or, where top_k is more than half their number, what 32 / parts
+// neighbouring lanes hold, with parts the power of two that makes twice top_k of them.  So the
+// list has up to 1.4 top_k elements in rows in no particular order ([196, 32660] bf16 with top_k
+// 279: 44 us, 97 with a search for each row; [64, 151936] fp32 with 600: 61 and 100).  Finer
+// segments for all calls cost time ([256, 151936] bf16 with top_k 50 and top_p: 46.5 instead of
+// 41.5 us with 32 parts).
+__host__ __device__ constexpr int segments_of(int nch, int parts, size_t esize) {
+    const int64_t n = int64_t(nch) * (parts > 0 ? parts : esize == 4 ? 4 : 2);
+    return n <= kMaxSegments ? static_cast<int>(n) : 0;
+}
+int parts_of(int nch, int64_t top_k, size_t esize) {
+    const int n = segments_of(nch, 0, esize);
+    if (n == 0 || top_k <= n / 2 || top_k > kMaxShortK) return 0;
+    int parts = esize == 4 ? 8 : 4;
+    while (parts < 32 && int64_t(nch) * parts < 2 * top_k) parts *= 2;
+    return parts;
+}
+// floats between two rows' maxima of segments, a multiple of 4
+constexpr int kSegsPerChunk = 32;
 __host__ __device__ constexpr size_t stats_offset(int64_t N) {
     return (modes_offset(N) + size_t(N) * sizeof(uint32_t) + 255) / 256 * 256;
 }
@@ -482,20 +506,22 @@ __device__ __forceinline__ float2 fast_scale(const Settings& s) {
 // Maximum and sum of a chunk.  The sum of 2^((x - max) c) leaves out one element of the
 // maximum (and has its sign bit set) where the chunk may hold the row's maximum: a total is
 // a sum of such parts plus the maximum's own weight.
-template <bool SEGMENTS, typename T>
+// ml: the lane's maximum; seg (GROUPS): the maxima of the warp's loads.
+template <bool GROUPS, typename T>
 __device__ __forceinline__ float2 chunk_stats(const Chunk<T>& c, float2 scale, float& best,
-                                              float (&seg)[Chunk<T>::LOADS]) {
+                                              float (&seg)[Chunk<T>::LOADS], float& ml) {
     constexpr int VEC = Chunk<T>::VEC, LOADS = Chunk<T>::LOADS;
-    float ml = -INFINITY, m = -INFINITY;
+    ml = -INFINITY;
+    float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
         float v = c.get(j * VEC);
 #pragma unroll
         for (int e = 1; e < VEC; ++e) v = fmaxf(v, c.get(j * VEC + e));
         ml = fmaxf(ml, v);
-        if (SEGMENTS) m = fmaxf(m, seg[j] = warp_max(v));
+        if (GROUPS) m = fmaxf(m, seg[j] = warp_max(v));
     }
-    if (!SEGMENTS) m = warp_max(ml);
+    if (!GROUPS) m = warp_max(ml);
     // a chunk of -inf has sum 0; NaN or +inf make it NaN
     const float mm = fmaxf(m, -3.402823466e38f);
     float2 s[kLane / 2];
@@ -627,10 +653,15 @@ __device__ float reach_value(const Row<T>& r, const float* smax, int nseg, int c
     return lo;
 }
 
-// Sorts the first n <= kShort of (order, w) by descending order (all different), each
-// element's place counted out by a thread: at these lengths quicker than a sorting network,
-// whose steps each wait for the one before.  `order` is padded to a multiple of 4.
-__device__ __noinline__ void sort_list(uint32_t n, u64* order, u64* w) {
+// Sorts the first n <= kShort of (order, w) by descending order (all different): each element's
+// place in its run is counted out by a thread, and its places in the other runs, sorted by then,
+// are searched.  One run of all where they are few (to 512: 19.5 us instead of 22.5 for [16, 151936]
+// with min_p 0.02), runs of 128 where they are many (68 instead of 102 us for [64, 151936] with top_k
+// 700).  At these lengths that is quicker than a sorting network, whose steps each wait for the one
+// before.  `order` is padded to a multiple of 4.
+constexpr uint32_t kRun = 128;
+template <bool RUNS>
+__device__ __noinline__ void sort_by(uint32_t n, u64* order, u64* w) {
     constexpr int kPer = kShort / kThreads;
     const uint32_t padded = (n + 3) / 4 * 4;
     if (threadIdx.x < padded - n) order[n + threadIdx.x] = 0;
@@ -639,14 +670,15 @@ __device__ __noinline__ void sort_list(uint32_t n, u64* order, u64* w) {
     uint32_t place[kPer];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-        const uint32_t i = threadIdx.x + q * kThreads;
+        const uint32_t i = threadIdx.x + q * kThreads, run = RUNS ? i / kRun * kRun : 0;
         me[q] = i < n ? order[i] : 0;
         mw[q] = i < n ? w[i] : 0;
-        place[q] = 0;
+        place[q] = run;
         // warps without elements of their own have nothing to count
         if ((i & ~31u) < n) {
+            const uint32_t end = RUNS ? min(run + kRun, padded) : padded;
 #pragma unroll 2
-            for (uint32_t j = 0; j < padded; j += 4) {
+            for (uint32_t j = run; j < end; j += 4) {
                 const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(order + j);
                 const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(order + j + 2);
                 place[q] += (a.x > me[q] ? 1u : 0u) + (a.y > me[q] ? 1u : 0u) +
@@ -659,13 +691,93 @@ __device__ __noinline__ void sort_list(uint32_t n, u64* order, u64* w) {
     for (int q = 0; q < kPer; ++q)
         if (threadIdx.x + q * kThreads < n) order[place[q]] = me[q], w[place[q]] = mw[q];
     __syncthreads();
+    if constexpr (RUNS) {
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) place[q] %= kRun;
+#pragma unroll 1
+        for (uint32_t run = 0; run < n; run += kRun) {
+            uint32_t at[kPer] = {0, 0, 0, 0};            // elements of the run that come before
+#pragma unroll 1
+            for (uint32_t step = kRun; step > 0; step >>= 1)
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    const uint32_t k = run + at[q] + step - 1;
+                    if (at[q] + step <= kRun && k < n && order[k] > me[q]) at[q] += step;
+                }
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if ((threadIdx.x + q * kThreads) / kRun * kRun != run) place[q] += at[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            if (threadIdx.x + q * kThreads < n) order[place[q]] = me[q], w[place[q]] = mw[q];
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ void sort_list(uint32_t n, u64* order, u64* w) {
+    if (n > 512)
+        sort_by<true>(n, order, w);
+    else
+        sort_by<false>(n, order, w);
+}
+
+// Lists the columns of the elements from a value on, out of the segments whose maximum reaches it:
+// 16 bytes a thread, of a segment that is a load of the warp or (LANES) the groups of some lanes.
+template <bool LANES, typename T>
+__device__ __noinline__ void gather(const T* x, int V, bool vec, const uint16_t* ids, int n_ids,
+                                    int parts, float tau_x, Shared0& sh) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int VEC = Chunk<T>::VEC, LOADS = Chunk<T>::LOADS, kAhead = 8;
+    const int lg_wide = LANES ? 6 - __ffs(parts) : 5;
+    const int lg_pieces = LANES ? lg_wide + __ffs(LOADS) - 1 : 5;
+    const int total = n_ids << lg_pieces;
+    const auto column = [&](int t) {
+        const int seg = ids[t >> lg_pieces], k = t & ((1 << lg_pieces) - 1);
+        if (!LANES) return (seg * 32 + k) * VEC;
+        return Chunk<T>::column(seg >> (5 - lg_wide), k >> lg_wide,
+                                ((seg & (parts - 1)) << lg_wide) + (k & ((1 << lg_wide) - 1)));
+    };
+#pragma unroll 1
+    for (int t0 = tid & ~31; t0 < total; t0 += kAhead * kThreads) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int t = t0 + lane + q * kThreads;
+            if (t < total) raw[q] = load_group(x, V, column(t), vec);
+        }
+        // bit q VEC + e: element e of group q
+        u64 hits = 0;
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                hits |= u64(t0 + lane + q * kThreads < total && group_value<T>(raw[q], e) >= tau_x)
+                        << (q * VEC + e);
+        const uint32_t mine = __popcll(hits);
+        uint32_t at = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, at, off);
+            if (lane >= off) at += o;
+        }
+        uint32_t first = 0;
+        if (lane == 31) first = atomicAdd(&sh.n_list, at);
+        at += __shfl_sync(0xffffffffu, first, 31) - mine;
+#pragma unroll 1
+        for (; hits != 0; hits &= hits - 1, ++at) {
+            const int e = __ffsll(hits) - 1;
+            if (at < kShort) sh.order[at] = column(t0 + lane + e / VEC * kThreads) + e % VEC;
+        }
+    }
 }
 
 // Draws from the elements at or above a value, if they settle the boundary and are few.
 template <typename T>
 __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* smax, uint16_t* ids,
                            int nseg, u64 all, const SampleArgs& a, int64_t row_i, Shared0& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     if (tid == 0) {
         sh.n_list = 0, sh.n_ids = 0;
         sh.key_m = s.want_m ? min_p_key(a, row_i, r.ws.m) : 0;
@@ -695,42 +807,17 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* smax
     if (by_m) tau = max(tau, key_m);
     const float tau_x = key_value(tau);
     for (int c = tid; c < nseg; c += kThreads)
-        if (smax[c] >= tau_x) ids[atomicAdd(&sh.n_ids, 1u)] = static_cast<uint16_t>(c);
+        if (smax[c] >= tau_x) {
+            const uint32_t at = atomicAdd(&sh.n_ids, 1u);
+            if (at < kShort) ids[at] = static_cast<uint16_t>(c);
+        }
     __syncthreads();
     const int n_ids = sh.n_ids;
-    constexpr int VEC = Chunk<T>::VEC, SEG = Chunk<T>::SEG, kAhead = 8;
-#pragma unroll 1
-    for (int i0 = warp; i0 < n_ids; i0 += kAhead * kWarps) {
-        uint4 raw[kAhead];
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            const int i = i0 + q * kWarps;
-            if (i < n_ids) raw[q] = load_group(r.x, r.V, ids[i] * SEG + lane * VEC, r.vec);
-        }
-        // bit q VEC + e: element e of group q
-        u64 hits = 0;
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                hits |= u64(i0 + q * kWarps < n_ids && group_value<T>(raw[q], e) >= tau_x ? 1 : 0)
-                        << (q * VEC + e);
-        const uint32_t mine = __popcll(hits);
-        uint32_t at = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, at, off);
-            if (lane >= off) at += o;
-        }
-        uint32_t first = 0;
-        if (lane == 31) first = atomicAdd(&sh.n_list, at);
-        at += __shfl_sync(0xffffffffu, first, 31) - mine;
-#pragma unroll 1
-        for (; hits != 0; hits &= hits - 1, ++at) {
-            const int e = __ffsll(hits) - 1;
-            if (at < kShort) sh.order[at] = ids[i0 + e / VEC * kWarps] * SEG + lane * VEC + e % VEC;
-        }
-    }
+    if (n_ids > kShort) return false;
+    if (a.parts == 0)
+        gather<false>(r.x, r.V, r.vec, ids, n_ids, 0, tau_x, sh);
+    else
+        gather<true>(r.x, r.V, r.vec, ids, n_ids, a.parts, tau_x, sh);
     __syncthreads();
     const uint32_t n = sh.n_list;
     if (n > kShort) return false;
@@ -818,14 +905,10 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* smax
     return true;
 }
 
-__host__ __device__ constexpr int segments_of(int nch, size_t esize) {
-    const int n = nch * (esize == 4 ? 4 : 2);
-    return n <= kMaxSegments ? n : 0;
-}
-__host__ __device__ constexpr size_t scan_smem(int nch, size_t esize) {
+__host__ __device__ constexpr size_t scan_smem(int nch, int nseg) {
     const size_t ring = offsetof(Shared0, order) + kWarps * kRing;
     const size_t tail =
-        sizeof(Shared0) + size_t(nch) * 12 + size_t(segments_of(nch, esize)) * 6 + 64;
+        sizeof(Shared0) + size_t(nch) * 12 + size_t(nseg) * 4 + kShort * 2 + 64;
     return ring > tail ? ring : tail;
 }
 
@@ -837,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     Shared0& sh = *reinterpret_cast<Shared0*>(smem);
     u64* cw = reinterpret_cast<u64*>(smem + sizeof(Shared0));
     float* cmax = reinterpret_cast<float*>(cw + nch);
-    const int nseg = segments_of(nch, sizeof(T));    // 0: too many to be kept
+    const int nseg = segments_of(nch, a.parts, sizeof(T));   // 0: too many to be kept
     float* smax = reinterpret_cast<float*>(cw) + (nch * 3 + 3) / 4 * 4;
     uint16_t* ids = reinterpret_cast<uint16_t*>(smax + (nseg + 3) / 4 * 4);
     const int64_t row_i = blockIdx.x / ranks;
@@ -897,9 +980,9 @@ __global__ void __launch_bounds__(kThreads, 4)
         cp_wait<S - 1>();
         Chunk<T> c;
         ring.read(slot, c);
-        float seg[Chunk<T>::LOADS];
-        if (cut) {
-            const float2 st = chunk_stats<true>(c, scale, best, seg);
+        float seg[Chunk<T>::LOADS], ml;
+        if (cut && a.parts == 0) {
+            const float2 st = chunk_stats<true>(c, scale, best, seg, ml);
             if (lane == 0) {
                 stats[r.first + i] = st;
 #pragma unroll
@@ -907,8 +990,15 @@ __global__ void __launch_bounds__(kThreads, 4)
                     segs[(r.first + i) * Chunk<T>::LOADS + j] = seg[j];
             }
         } else {
-            const float2 st = chunk_stats<false>(c, scale, best, seg);
+            const float2 st = chunk_stats<false>(c, scale, best, seg, ml);
             if (lane == 0) stats[r.first + i] = st;
+            if (cut) {
+                const int wide = 32 / a.parts;       // lanes of a segment
+#pragma unroll 1
+                for (int off = wide >> 1; off > 0; off >>= 1)
+                    ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, off));
+                if (lane % wide == 0) segs[(r.first + i) * a.parts + lane / wide] = ml;
+            }
         }
         if (i + S * kWarps < r.mine)
             ring.fetch(slot, r.x, r.V, r.first + i + S * kWarps, lane, r.vec);
@@ -1915,8 +2005,11 @@ cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int
 }
 
 template <typename T>
-cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stream) {
-    const int nch = (a.V + kChunk - 1) / kChunk;
+cudaError_t launch_typed(const T* logits, const SampleArgs& args, cudaStream_t stream) {
+    const int nch = (args.V + kChunk - 1) / kChunk;
+    SampleArgs a = args;
+    a.parts = parts_of(nch, a.top_k_rows != nullptr ? 0 : a.top_k, sizeof(T));
+    const int nseg = segments_of(nch, a.parts, sizeof(T));
     const int ranks = nch >= 128 ? 8 : nch >= 64 ? 4 : nch >= 32 ? 2 : 1;
     if (int64_t(a.N) * ranks > 0x7fffffff) return cudaErrorInvalidValue;
     // As many blocks a row as run at the same time, four on each of 152 SMs: more of them, one
@@ -1926,7 +2019,7 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     int scan_ranks = ranks;
     while (scan_ranks > 1 && int64_t(a.N) * scan_ranks > 608) scan_ranks /= 2;
     cudaError_t e = launch_rows(sample_scan_kernel<T>, logits, a, nch, scan_ranks, a.N, kThreads,
-                                scan_smem(nch, sizeof(T)), stream);
+                                scan_smem(nch, nseg), stream);
     if (e != cudaSuccess) return e;
     if (a.top_k_rows == nullptr && a.top_p_rows == nullptr && a.min_p_rows == nullptr &&
         (a.top_k == 0 || a.top_k >= a.V) && a.top_p_value >= 1.f && a.min_p_value == 0.f) {
@@ -1942,7 +2035,7 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& a, cudaStream_t stre
     const bool own_settings =
         a.top_k_rows != nullptr || a.top_p_rows != nullptr || a.min_p_rows != nullptr;
     const bool listed =
-        a.min_p_value > 0.f || (a.top_k > 0 && a.top_k <= segments_of(nch, sizeof(T)) / 2);
+        a.min_p_value > 0.f || (a.top_k > 0 && a.top_k <= nseg / 2);
     const int64_t expected = own_settings ? a.N / 4 : listed ? 0 : a.N;
     int search_ranks = ranks;
     while (search_ranks > 2 && expected * search_ranks > 304) search_ranks /= 2;
