@@ -240,9 +240,11 @@ __host__ __device__ constexpr int64_t part_len(int64_t H, int threads) {
 enum : int { kCopy16, kCopy4, kCopyPlain };
 
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes, bool wide) {
-    // the rest of the 16 (4) bytes is filled with zeros
+    // The rest of the 16 (4) bytes is filled with zeros.  Through L1: the two halves of a group of
+    // fp32 come one after the other, and the second finds its sectors there (fp32 [4096, 4096] 22.9
+    // instead of 30.4 us past L1, bf16 the same either way).
     if (wide)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                      : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -277,17 +279,26 @@ struct Ring {
     __device__ __forceinline__ uint4* piece(int stage, int p) const {
         return base + (stage * kPieces + p) * blockDim.x + threadIdx.x;
     }
-    // full: 16 bytes at a time, and every column of every group is there
+    // fit: as at the forward kernel below
     __device__ __forceinline__ void fetch(const T* row, int stage, int H, int mode,
-                                          bool full) const {
+                                          int fit) const {
         constexpr int kPerGroup = kPieces / kGroups, kElems = kGroup / kPerGroup;
-        if (full) {
+        if (fit == 2) {
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
                 cp_async(smem_u32(piece(stage, p)),
                          row + (threadIdx.x + p / kPerGroup * blockDim.x) * kGroup +
                              p % kPerGroup * kElems,
                          16, true);
+            return;
+        }
+        if (fit == 1) {
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p) {
+                const int c = (threadIdx.x + p / kPerGroup * blockDim.x) * kGroup;
+                cp_async(smem_u32(piece(stage, p)), c < H ? row + c + p % kPerGroup * kElems : row,
+                         c < H ? 16 : 0, true);
+            }
             return;
         }
 #pragma unroll
@@ -334,9 +345,10 @@ __device__ __forceinline__ int mask_byte(const uint8_t* mask, int row, int N) {
 
 // The forward of a row in registers: two block reductions for layer norm, one for RMS norm, and
 // two blocks or more of up to 512 threads on an SM, so that one reduces while another moves data.
-// FULL: H is 16 columns for each thread and every row starts on 16 bytes, so no column needs
-// a test (a third of the instructions of a row; the arithmetic is the same).
-template <typename T, bool CENTER, int MAXT, bool FULL>
+// FIT: every row starts on 16 bytes and H is 16 columns for each thread (2), so that no column
+// needs a test, or whole groups (1), so that a group does; otherwise (0) each column.  The
+// arithmetic is the same (bf16 [8000, 1664] 13.5 us with 1, 15.1 with 0).
+template <typename T, bool CENTER, int MAXT, int FIT>
 __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     norm_fwd_kernel(const NormArgs a, int x_mode, float inv_h) {
     constexpr int S = stages_of<T, MAXT, 1>();
@@ -344,7 +356,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     __shared__ float2 slots[2][32];
     int slot = 0;
     const int tid = threadIdx.x, H = a.H;
-    const bool out_vec = FULL || a.out_vec;
+    const bool out_vec = FIT > 0 || a.out_vec;
     const T* x = static_cast<const T*>(a.x);
     T* y = static_cast<T*>(a.out);
     const uint8_t* mask = a.mask;
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
         if (mask_byte(mask, row + k * step, a.N)) {
-            ring.fetch(ahead, k, H, x_mode, FULL);
+            ring.fetch(ahead, k, H, x_mode, FIT);
             bits |= 1u << k;
         }
         cp_commit();
@@ -386,7 +398,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
     int stage = 0;
     for (; row < a.N; row += step, yr += step * a.out_stride) {
         if (next) {
-            ring.fetch(ahead, stage == 0 ? S - 1 : stage - 1, H, x_mode, FULL);
+            ring.fetch(ahead, stage == 0 ? S - 1 : stage - 1, H, x_mode, FIT);
             bits |= 1u << (S - 1);
         }
         cp_commit();
@@ -423,8 +435,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
             for (int e = 0; e < 4; ++e) {
                 if (CENTER) {
                     f[i][e] = __fadd2_rn(f[i][e], both(-mean));
-                    if (!FULL && 2 * e >= n) f[i][e].x = 0.f;
-                    if (!FULL && 2 * e + 1 >= n) f[i][e].y = 0.f;
+                    if (FIT == 1 && n == 0) f[i][e] = both(0.f);
+                    if (FIT == 0 && 2 * e >= n) f[i][e].x = 0.f;
+                    if (FIT == 0 && 2 * e + 1 >= n) f[i][e].y = 0.f;
                 }
                 q = __ffma2_rn(f[i][e], f[i][e], q);
             }
@@ -437,7 +450,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 1024 ? 1 : 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 f[i][e] = __ffma2_rn(__fmul2_rn(f[i][e], both(rstd)), w[i][e], b[i][e]);
-            if (FULL || c < H) store_group(yr, c, FULL ? c + kGroup : H, out_vec, f[i]);
+            if (FIT == 2 || c < H) store_group(yr, c, FIT > 0 ? c + kGroup : H, out_vec, f[i]);
         }
         if (tid == 0) {
             if (a.mean_out != nullptr) a.mean_out[row] = mean;
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(1024)
 // The backward of a row in registers, with the block's part of dw and db: 64 floats a thread for
 // the two tensors' groups, w and the sums, hence one block of 512 threads (or two of 256) on an
 // SM.  One reduction of both means.
-template <typename T, bool CENTER, int MAXT, bool FULL>
+template <typename T, bool CENTER, int MAXT, int FIT>
 __global__ void __launch_bounds__(MAXT, 1)
     norm_bwd_kernel(const NormArgs a, int x_mode, int dy_mode, float inv_h,
                     float* __restrict__ dw_part, float* __restrict__ db_part) {
@@ -524,7 +537,7 @@ __global__ void __launch_bounds__(MAXT, 1)
     __shared__ float2 slots[2][32];
     int slot = 0;
     const int tid = threadIdx.x, H = a.H;
-    const bool out_vec = FULL || a.out_vec;
+    const bool out_vec = FIT > 0 || a.out_vec;
     const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
     T* dx = static_cast<T*>(a.out);
@@ -541,8 +554,8 @@ __global__ void __launch_bounds__(MAXT, 1)
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
         if (mask_byte(mask, row + k * step, a.N)) {
-            rx.fetch(x_ahead, k, H, x_mode, FULL);
-            rg.fetch(g_ahead, k, H, dy_mode, FULL);
+            rx.fetch(x_ahead, k, H, x_mode, FIT);
+            rg.fetch(g_ahead, k, H, dy_mode, FIT);
             bits |= 1u << k;
         }
         cp_commit();
@@ -567,8 +580,8 @@ __global__ void __launch_bounds__(MAXT, 1)
     for (; row < a.N; row += step, dxr += step * a.out_stride) {
         if (next) {
             const int to = stage == 0 ? S - 1 : stage - 1;
-            rx.fetch(x_ahead, to, H, x_mode, FULL);
-            rg.fetch(g_ahead, to, H, dy_mode, FULL);
+            rx.fetch(x_ahead, to, H, x_mode, FIT);
+            rg.fetch(g_ahead, to, H, dy_mode, FIT);
             bits |= 1u << (S - 1);
         }
         cp_commit();
@@ -619,7 +632,7 @@ __global__ void __launch_bounds__(MAXT, 1)
                 if (CENTER) g[i][e] = __fadd2_rn(g[i][e], both(-m1));
                 g[i][e] = __fmul2_rn(__ffma2_rn(xh[i][e], both(-m2), g[i][e]), both(rstd));
             }
-            if (FULL || c < H) store_group(dxr, c, FULL ? c + kGroup : H, out_vec, g[i]);
+            if (FIT == 2 || c < H) store_group(dxr, c, FIT > 0 ? c + kGroup : H, out_vec, g[i]);
         }
     }
     // the block's partial row, in the order of part_len: neighbouring threads write
@@ -789,14 +802,17 @@ cudaError_t allow_smem(F kernel, size_t smem) {
                                 static_cast<int>(smem));
 }
 
-bool is_full(const NormArgs& a, int threads) {
-    return a.H == threads * kGroups * kGroup && a.in_vec && a.out_vec;
+int fit_of(const NormArgs& a, int threads) {
+    if (!a.in_vec || !a.out_vec || a.H % kGroup != 0) return 0;
+    return a.H == threads * kGroups * kGroup ? 2 : 1;
 }
 
 template <typename T, bool CENTER, int MAXT>
 cudaError_t run_fwd(const NormArgs& a, int threads, cudaStream_t stream) {
-    auto kernel = is_full(a, threads) ? norm_fwd_kernel<T, CENTER, MAXT, true>
-                                : norm_fwd_kernel<T, CENTER, MAXT, false>;
+    const int fit = fit_of(a, threads);
+    auto kernel = fit == 2   ? norm_fwd_kernel<T, CENTER, MAXT, 2>
+                  : fit == 1 ? norm_fwd_kernel<T, CENTER, MAXT, 1>
+                             : norm_fwd_kernel<T, CENTER, MAXT, 0>;
     const size_t smem = size_t(threads) * kGroups * kGroup * sizeof(T) * stages_of<T, MAXT, 1>();
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -821,8 +837,10 @@ cudaError_t fwd_dispatch(const NormArgs& a, cudaStream_t stream) {
 template <typename T, bool CENTER, int MAXT>
 cudaError_t run_bwd(const NormArgs& a, int threads, int blocks, float* dwp, float* dbp,
                     cudaStream_t stream) {
-    auto kernel = is_full(a, threads) ? norm_bwd_kernel<T, CENTER, MAXT, true>
-                                : norm_bwd_kernel<T, CENTER, MAXT, false>;
+    const int fit = fit_of(a, threads);
+    auto kernel = fit == 2   ? norm_bwd_kernel<T, CENTER, MAXT, 2>
+                  : fit == 1 ? norm_bwd_kernel<T, CENTER, MAXT, 1>
+                             : norm_bwd_kernel<T, CENTER, MAXT, 0>;
     const size_t smem =
         size_t(threads) * kGroups * kGroup * sizeof(T) * 2 * stages_of<T, MAXT, 2>();
     const cudaError_t e = allow_smem(kernel, smem);
