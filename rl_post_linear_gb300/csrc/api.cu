@@ -917,7 +917,10 @@ const char* rlk_contract_string(void) {
                               "audit: 4096-element slices dealt round-robin to min(slices, 608) "
                               "blocks, fixed trees, float-pair (two-sum) partials; "
                               "data-parallel dW: fp32 partials merged in rank order, one "
-                              "rounding";
+                              "rounding; norms: fp32, a row's sums ordered by H alone, dweight "
+                              "and dbias summed per block in ascending rows and merged in a "
+                              "fixed tree; sampling: weights as 64-bit integers of 40 or more "
+                              "correct bits, ties to the lowest index";
 }
 
 const char* rlk_status_string(rlk_status_t status) {
