@@ -476,8 +476,12 @@ int parts_of(int nch, int64_t top_k, size_t esize) {
     while (parts < 32 && int64_t(nch) * parts < 2 * top_k) parts *= 2;
     return parts;
 }
-// floats between two rows' maxima of segments, a multiple of 4
-constexpr int kSegsPerChunk = 32;
+// Floats between two rows' maxima of segments, a multiple of 4: one a load, or fewer than 4
+// kMaxShortK parts (parts_of doubles them only below 2 top_k).
+__host__ __device__ constexpr int64_t segs_stride(int64_t nch) {
+    const int64_t most = nch * 4 > 4 * kMaxShortK ? nch * 4 : 4 * kMaxShortK;
+    return ((nch * 32 < most ? nch * 32 : most) + 3) / 4 * 4;
+}
 __host__ __device__ constexpr size_t stats_offset(int64_t N) {
     return (modes_offset(N) + size_t(N) * sizeof(uint32_t) + 255) / 256 * 256;
 }
@@ -493,7 +497,7 @@ __device__ __forceinline__ float2* row_stats(const SampleArgs& a, int64_t row, i
 }
 __device__ __forceinline__ float* row_segs(const SampleArgs& a, int64_t row, int nch) {
     return reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + segs_offset(a.N, nch)) +
-           row * nch * kSegsPerChunk;
+           row * segs_stride(nch);
 }
 
 // log2(e) / T in two positive floats: a distance of -inf then stays one, where a negative or zero
@@ -2048,7 +2052,7 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& args, cudaStream_t s
 
 size_t sample_workspace(int64_t N, int64_t V) {
     const int nch = static_cast<int>((V + kChunk - 1) / kChunk);
-    return segs_offset(N, nch) + size_t(N) * nch * kSegsPerChunk * sizeof(float);
+    return segs_offset(N, nch) + size_t(N) * segs_stride(nch) * sizeof(float);
 }
 
 cudaError_t launch_sample(const void* logits, bool bf16, const SampleArgs& args,

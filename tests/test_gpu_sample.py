@@ -390,3 +390,15 @@ def test_workspace_size_is_enough_at_its_edge():
                 rlk.rlk_sample_logits(z, u, None, 0.8, 0, p, 0.0, *out, buf[:need])
                 assert bool((buf[need:] == 0xA5).all())
                 assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("v,dtype", [(32660, torch.bfloat16), (70001, torch.float32),
+                                     (151936, torch.float32), (151936, torch.bfloat16)])
+@pytest.mark.parametrize("k", [150, 300, 450, 600, 700, 701])
+def test_top_k_of_hundreds(k, v, dtype):
+    # lists of a few hundred to a thousand elements, from segments of every width
+    check(zipf(5, v, k), uniforms(5, k + 1), top_k=k, temperature=0.8)
+    check(normal(4, v, k + 2, 2.0, dtype), uniforms(4, k + 3), top_k=k, top_p=0.97)
+    z = normal(4, v, k + 4, 1.0, dtype)
+    z[:, ::3] = -math.inf
+    check(z, uniforms(4, k + 5), top_k=k, min_p=1e-4)
