@@ -139,6 +139,14 @@ __device__ __forceinline__ void store_group(__nv_bfloat16* row, int c, int H, bo
 __device__ __forceinline__ void store_group(float* row, int c, int H, bool vec,
                                             const float (&f)[8]) {
     const int n = valid_cols(c, H);
+    // whole sectors at once where the rows allow it ([4096, 4096] RMS norm 21.4 instead of 22.9 us)
+    if (n == kGroup && (reinterpret_cast<uintptr_t>(row) & 31) == 0) {
+        asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + c),
+                     "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]),
+                     "f"(f[7])
+                     : "memory");
+        return;
+    }
     if (n == kGroup && vec) {
         __stcs(reinterpret_cast<float4*>(row + c), make_float4(f[0], f[1], f[2], f[3]));
         __stcs(reinterpret_cast<float4*>(row + c) + 1, make_float4(f[4], f[5], f[6], f[7]));
@@ -241,8 +249,8 @@ enum : int { kCopy16, kCopy4, kCopyPlain };
 
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes, bool wide) {
     // The rest of the 16 (4) bytes is filled with zeros.  Through L1: the two halves of a group of
-    // fp32 come one after the other, and the second finds its sectors there (fp32 [4096, 4096] 22.9
-    // instead of 30.4 us past L1, bf16 the same either way).
+    // fp32 come one after the other, and the second finds its sectors there (fp32 [4096, 4096] a
+    // quarter less time than past L1, bf16 the same either way).
     if (wide)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                      : "memory");
