@@ -1876,7 +1876,7 @@ __global__ void __launch_bounds__(kSearch, 2)
 
 // The second launch of a call without any truncation: its rows are those whose target lies near
 // a border, few of them, and what counts is how soon each is done: 1024 threads a block, up to 8
-// blocks a row (17 us for the 12 rows or so of [256, 151936]).  With more rows than clusters, a
+// blocks a row (12 to 22 us for the 10 to 25 rows of [256, 151936]).  With more rows than clusters, a
 // row gets fewer blocks ([1024, 151936] 139 us, 168 with 8 each).  Every weight of the row is
 // formed exactly; a warp takes 128 columns at a time.
 struct Shared1 {
