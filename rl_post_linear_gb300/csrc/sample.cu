@@ -87,7 +87,9 @@ constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
 // comes on top.
 constexpr float kFastErr = 26.f / 16777216.f;
 constexpr float kSumErr = 9.f / 16777216.f;
-constexpr float kBinErr = 1.f / 4096.f;  // of a histogram's weight: 12-bit codes
+// Of the weight of a histogram of the distance: 12-bit codes relative to the weight at the bin's
+// start, in bins of 0.023 powers of 2 (half a code of 4030, and 2^-17 for distance and exponential).
+constexpr float kBinErr = 1.f / 4096.f;
 
 // Unsigned integers in the order of the floats; -0 and +0 get the same one.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -1105,7 +1107,7 @@ struct Cmd {
     int type;
     uint32_t klo, khi;
     int shift;        // kHist: bins of the keys, (khi - key) >> shift; -1: of the distance
-    int by_weight;    // kHist: 12-bit weights instead of counts
+    int by_weight;    // kHist: weights instead of counts, in bins of the distance 12-bit ones
     int list;         // kCollect: 1 lists the elements inside, 0 counts them per chunk
     int total;        // also the exact weight of all elements
 };
@@ -1115,7 +1117,9 @@ struct Shared {
     u64 table[kExpEntries];
     uint32_t key[kList], idx[kList];     // block 0: the merged list
     union {                              // of one step or the other
-        uint32_t hist[kBins];
+        struct {                         // the upper words: weights of keys
+            uint32_t hist[kBins], hist_hi[kBins];
+        };
         struct {
             uint32_t own_key[kList], own_idx[kList];   // this block's part of the list
         };
@@ -1152,7 +1156,16 @@ __device__ __forceinline__ void window_of(const Cmd& cmd, float& lo, float& hi) 
     hi = none ? -INFINITY : khi > order_key(INFINITY) ? INFINITY : key_value(khi);
 }
 
-// Histogram of the window; for windows of keys also the exact weight above it.  About 9 us over 8
+// a weight onto a sum in two words
+__device__ __forceinline__ void add_weight(uint32_t* lo, uint32_t* hi, u64 w) {
+    const uint32_t wl = static_cast<uint32_t>(w);
+    const uint32_t old = atomicAdd(lo, wl);
+    atomicAdd(hi, static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u));
+}
+
+// Histogram of the window.  Of keys: with the weights as integers, in the bins and above the window,
+// so that the boundary's bin is certain however far apart its elements lie (codes relative to one
+// value lose what is 13 bits below it: a window that spans a gap never closed).  About 9 us over 8
 // blocks at V = 151936: shared-memory atomics and conversions bind it.
 template <typename T>
 __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, const float* cmax,
@@ -1160,11 +1173,10 @@ __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, co
     const Row<T> r = row;                    // in registers for the loops
     const Cmd cmd = command;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kBins; i += kSearch) sh.hist[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += kSearch) sh.hist[i] = sh.hist_hi[i] = 0;
     if (threadIdx.x == 0) sh.own_above = sh.own_total = 0;
     __syncthreads();
     const float unit = kRange / kBins;
-    const float x_hi = key_value(cmd.khi);
     float lo, hi;
     window_of(cmd, lo, hi);
     u64 above = 0, all = 0;
@@ -1200,11 +1212,12 @@ __device__ __noinline__ void step_hist(const Row<T>& row, const Cmd& command, co
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 above += x[e] > hi ? w[e] : 0;
-                const float q =
-                    cmd.by_weight ? rintf(4096.f * ex2_approx((x[e] - x_hi) * r.ws.ch)) : 1.f;
-                if (x[e] >= lo && x[e] <= hi)
-                    atomicAdd(&sh.hist[(cmd.khi - order_key(x[e])) >> cmd.shift],
-                              static_cast<uint32_t>(q));
+                if (!(x[e] >= lo && x[e] <= hi)) continue;
+                const uint32_t b = (cmd.khi - order_key(x[e])) >> cmd.shift;
+                if (cmd.by_weight)
+                    add_weight(&sh.hist[b], &sh.hist_hi[b], w[e]);
+                else
+                    atomicAdd(&sh.hist[b], 1u);
             }
         }
     }
@@ -1304,10 +1317,7 @@ __device__ __noinline__ Selected list_select(const Row<T>& row, bool by_weight, 
             if (k < lo || k > hi) continue;
             const uint32_t b = (hi - k) >> shift;
             atomicAdd(&sh.cnt[b], 1u);
-            const u64 w = fixed_weight(key_value(k), ws, sh.table);
-            const uint32_t wl = static_cast<uint32_t>(w);
-            const uint32_t old = atomicAdd(&sh.lo[b], wl);
-            atomicAdd(&sh.hi[b], static_cast<uint32_t>(w >> 32) + (old + wl < old ? 1u : 0u));
+            add_weight(&sh.lo[b], &sh.hi[b], fixed_weight(key_value(k), ws, sh.table));
         }
         __syncthreads();
         // thread t holds bins 2 t and 2 t + 1, from the top down
@@ -1450,46 +1460,30 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     constexpr int kPer = kBins / kSearch;
     static_assert(kPer == 4, "a thread takes 16 bytes of each histogram");
     const int b0 = threadIdx.x * kPer;
-    u64 q[kPer] = {0, 0, 0, 0};
+    const bool keys = cmd.shift >= 0;
+    u64 q[kPer] = {0, 0, 0, 0}, weight[kPer];
     u64 above = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if (k >= ranks) break;
         const uint4 h = *reinterpret_cast<const uint4*>(peer(sh.hist, k) + b0);
         q[0] += h.x, q[1] += h.y, q[2] += h.z, q[3] += h.w;
-        if (cmd.shift >= 0) above += *peer(&sh.own_above, k);
+        if (!keys) continue;
+        above += *peer(&sh.own_above, k);
+        if (!cmd.by_weight) continue;
+        const uint4 hi = *reinterpret_cast<const uint4*>(peer(sh.hist_hi, k) + b0);
+        q[0] += u64(hi.x) << 32, q[1] += u64(hi.y) << 32;
+        q[2] += u64(hi.z) << 32, q[3] += u64(hi.w) << 32;
     }
-    if (cmd.shift >= 0) take_total(P, cmd, ranks, sh);
+    if (keys) take_total(P, cmd, ranks, sh);
     u64 mine = 0;
-    const bool keys = cmd.shift >= 0, single = cmd.shift == 0;
     const float unit = kRange / kBins;
-    const float x_hi = key_value(cmd.khi);
-    const u64 w_hi = keys ? fixed_weight(fminf(x_hi, r.ws.m), r.ws, sh.table) : 0;
-    u64 weight[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        if (!cmd.by_weight) {
-            weight[i] = q[i];
-        } else if (!keys) {
-            weight[i] = __float2ull_rn(static_cast<float>(q[i]) *
-                                       ex2_approx(-(b0 + i) * unit + (r.bits - 12)));
-        } else {
-            weight[i] = scale_weight(static_cast<float>(q[i]) * (1.f / 4096.f / 4096.f), w_hi)
-                        << 12;
-        }
-    }
-    if (cmd.by_weight && single) {
-        // one value a bin: its code tells the count, and the weight is exact
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (q[i] != 0) {
-                const float x = key_value(cmd.khi - (b0 + i));
-                const float code = rintf(4096.f * ex2_approx((x - x_hi) * r.ws.ch));
-                // the count is below 2^22 and the quotient off by less than 2^-23 of it
-                weight[i] = __float2ull_rn(__fdiv_rn(static_cast<float>(q[i]), code)) *
-                            fixed_weight(x, r.ws, sh.table);
-            }
-    }
+    for (int i = 0; i < kPer; ++i)
+        weight[i] = keys || !cmd.by_weight
+                        ? q[i]
+                        : __float2ull_rn(static_cast<float>(q[i]) *
+                                         ex2_approx(-(b0 + i) * unit + (r.bits - 12)));
 #pragma unroll
     for (int i = 0; i < kPer; ++i) mine += weight[i];
     const u64 before = block_scan<kSearch>(mine, 0, sh.part, sh.part_n).v;
@@ -1503,7 +1497,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         need_lo = P.need(P.s_lo);
         need_hi = P.need(P.s_hi);
         base = above;
-        err = single ? 0.f : kBinErr;
+        err = keys ? 0.f : kBinErr;
     }
     u64 run = before, at_before = 0;
     int first_may = kBins, first_must = kBins;
@@ -1526,7 +1520,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     const int at = sh.at, at2 = sh.at2;
     u64 skipped = sh.at_w;
     const int j1 = min(at, kBins - 1), j2 = max(j1, min(at2, kBins - 1));
-    // elements of the new window (codes of a window are near 4096 unless it is wide)
+    // elements of the new window, or their weight
     u64 est = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -1534,9 +1528,9 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
     if (est != 0) atomicAdd(&sh.width, est);         // by few threads
     __syncthreads();
     est = sh.width;
-    if (cmd.by_weight) est = est / 3600 + 1;
     if (at == kBins) {
-        // fewer elements of weight > 0 than top_k: nothing is cut (a weight is reached)
+        // fewer elements of weight > 0 than top_k: nothing is cut.  (A weight is reached: the
+        // bounds of total and bins hold.)
         P.key = kKeyNegInf;
         P.ties = 0;
         if (P.want_k) {
@@ -1548,6 +1542,7 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         return;
     }
     // the first top_k altogether, where the list holds them: top_p is then settled in it too
+    if (cmd.by_weight && !keys) est = est / 3600 + 1;    // codes of the distance lie near 4096
     const bool whole = P.want_k && !keys && skipped + est <= kList;
     if (whole) skipped = 0;
     if (P.want_k) P.n_above += skipped;
@@ -1571,6 +1566,10 @@ __device__ __noinline__ void after_hist(const Row<T>& r, Search& P, Cmd& cmd, in
         const int64_t lo = int64_t(cmd.khi) - (int64_t(j2 + 1) << cmd.shift) + 1;
         cmd.klo = static_cast<uint32_t>(max(int64_t(cmd.klo), lo));
         cmd.khi = static_cast<uint32_t>(hi);
+        if (cmd.by_weight) {             // at most so many of the least weight in it
+            const u64 least = fixed_weight(key_value(cmd.klo), r.ws, sh.table);
+            est = least > 0 ? est / least : u64(kList) + 1;
+        }
     }
     if (cmd.klo == cmd.khi || est <= kList) {
         cmd.type = kCollect;

@@ -1,0 +1,101 @@
+"""Sampling near its borders: gaps in the logits at top_p's boundary.
+
+Compared with the definition in float64, one row at a time.  The kernel's weights carry a relative
+error of 2^-40 and a rounding to whole units of 2^-bits of the largest, V 2^bits < 2^64: sums are
+within 2^-39 + V 2^-(bits + 1) / S of themselves (S: the sum in units of the largest weight), and a
+row whose target or top_p boundary is nearer than that to a border is left out.
+logp and kept_logp: 2^-19 + 2^-22 |logp|, as the fp32 exponentials, logarithm and difference give.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rl_post_linear_gb300 as rlk
+from helpers import dev
+from test_gpu_sample import ref_row
+
+pytestmark = pytest.mark.gpu
+
+
+def weight_bits(v):
+    bits = 46
+    while 1 << (64 - bits) <= v:
+        bits -= 1
+    return bits
+
+
+def check(logits, u, temperature=1.0, top_k=0, top_p=1.0):
+    """Compares each row; returns how many were far enough from a border to be compared."""
+    n, v = logits.shape
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    out = rlk.sample_logits(logits, u, temperature, top_k, top_p, error_word=err)
+    assert int(err.item()) == 0
+    tok, logp, kept = (t.cpu().double().numpy() for t in out)
+    x, uu = logits.float().cpu().double().numpy(), u.cpu().double().numpy()
+    done = 0
+    for i in range(n):
+        s = np.exp((x[i] - x[i].max()) / temperature).sum()
+        want, lp, kl, margin = ref_row(x[i], temperature, top_k, top_p, 0.0, uu[i])
+        if margin <= 2.0 ** -39 + v * 2.0 ** -(weight_bits(v) + 1) / s:
+            continue
+        done += 1
+        assert tok[i] == want, (i, tok[i], want, margin)
+        assert abs(logp[i] - lp) <= 2.0 ** -19 + 2.0 ** -22 * abs(lp)
+        assert abs(kept[i] - kl) <= 2.0 ** -19 + 2.0 ** -22 * abs(kl)
+    return done
+
+
+def two_levels(n, v, heavy, gap, spread_top, spread_tail, dtype, seed):
+    """Rows with `heavy` logits in [-spread_top, 0], in the last columns, and the others in
+    [-gap - spread_tail, -gap]."""
+    g = torch.Generator().manual_seed(seed)
+    z = -gap - spread_tail * torch.rand(n, v, generator=g)
+    z[:, v - heavy:] = -spread_top * torch.rand(n, heavy, generator=g)
+    z[:, v - 1] = 0.0
+    return z.to(dtype).to(dev())
+
+
+def check_nuclei(z, heavy, where, **setting):
+    """Nuclei that end at `where` of the tail's weight, drawn from over the tail's part of them."""
+    n, v = z.shape
+    w = torch.exp(z[:1].double().cpu())[0]
+    tail, top = float(w[:v - heavy].sum()), float(w[v - heavy:].sum())
+    p = (top + where * tail) / (top + tail)
+    u = (torch.arange(n, dtype=torch.float64) + 0.5) / n * (where * tail / (top + where * tail))
+    return check(z, u.float().to(dev()), top_p=p, **setting)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heavy,spread_top,gaps", [(1, 0.0, (2, 5, 8, 10, 12, 14, 17, 20)),
+                                                   (300, 0.0, (1, 3, 6, 9, 10, 12, 15)),
+                                                   (300, 2.0, (1, 4, 7, 9, 11, 11.5, 13, 15)),
+                                                   (2500, 3.0, (1, 6, 9, 11, 13))])
+def test_nuclei_that_end_behind_a_gap(heavy, spread_top, gaps, dtype):
+    done = 0
+    for i, gap in enumerate(gaps):
+        for spread_tail in (0.0, 0.05, 1.0):
+            z = two_levels(6, 8003, heavy, gap, spread_top, spread_tail, dtype, 100 * i + heavy)
+            for where in (0.003, 0.17, 0.5, 0.93):
+                done += check_nuclei(z, heavy, where)
+    assert done >= 6 * len(gaps)
+
+
+@pytest.mark.parametrize("top_p", [0.99915, 0.9992, 0.9993, 0.99945, 0.9995, 0.99953, 0.9997])
+def test_nuclei_of_a_flat_top_and_a_far_tail(top_p):
+    for v, gap, spread in ((5003, 10.0, 0.0), (8003, 11.5, 2.0)):
+        for k in (0, 4000):
+            z = two_levels(16, v, 300, gap, spread, 0.05, torch.float32, 5)
+            u = (torch.arange(16) + 0.5) / 16 * (3e-4 if k == 0 else 1e-4)
+            assert check(z, u.to(dev()), top_p=top_p, top_k=k) >= 8
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nuclei_of_a_staircase(dtype):
+    # steps of 200 tokens, each 2 to 5 nats below the one before: a gap inside every window
+    g = torch.Generator().manual_seed(3)
+    for step in (2.0, 3.5, 5.0):
+        z = -step * (torch.arange(8001) // 200).clamp(max=9) - 0.01 * torch.rand(8, 8001, generator=g)
+        z = z.flip(1).contiguous().to(dtype).to(dev())
+        for p in (0.5, 0.9, 0.99, 0.9999, 1 - 1e-6, 1 - 1e-8):
+            u = 10.0 ** -torch.arange(8, dtype=torch.float32)
+            assert check(z, u.clamp(max=0.9999).to(dev()), top_p=p) >= 4
