@@ -84,9 +84,11 @@ constexpr uint32_t kKeyNegInf = 0x007fffffu;   // order_key(-inf)
 // weighted mean of t over 512 elements with sum s >= 1 is at most log2(512 / s) <= 9, so 12.5.
 // A relative error e of all weights leaves 2 u (1 - u) e of sum(prefix) - u sum(all) at its
 // zero.  The prefix inside a chunk is summed exactly: there up to kSumErr of the chunk's weight
-// comes on top.
+// comes on top, and whole units: half a unit of a chunk's largest weight, 512 times, and one for
+// each product, are below one for each column (kFastUnits for the columns past V).
 constexpr float kFastErr = 26.f / 16777216.f;
 constexpr float kSumErr = 9.f / 16777216.f;
+constexpr u64 kFastUnits = 8192;
 // Of the weight of a histogram of the distance: 12-bit codes relative to the weight at the bin's
 // start, in bins of 0.023 powers of 2 (half a code of 4030, and 2^-17 for distance and exponential).
 constexpr float kBinErr = 1.f / 4096.f;
@@ -125,13 +127,15 @@ __device__ __forceinline__ SampleFraction fraction(float f) {
     r.shift = 150 - static_cast<int>(max(e, 1u));
     return r;
 }
-// floor(w * f) of a float 0 <= w <= 512 and an integer f <= 2^46, to 2^-40 of itself
+// floor(w f) of a float 0 <= w <= 512 and an integer f <= 2^46.  The product has up to 70 bits, of
+// which the 14 that are always behind the point go first; bits cut off f instead would be much of
+// the weight of a light chunk, whose f is small.
 __device__ __forceinline__ u64 scale_weight(float w, u64 f) {
-    const uint32_t b = __float_as_uint(w);
-    const int e = int(b >> 23);
-    const int shift = 150 - e - 6;             // w = mant 2^-(150 - e)
-    if (e == 0 || shift > 63) return 0;
-    return ((f >> 6) * u64((b & 0x7fffffu) | 0x800000u)) >> shift;
+    const uint32_t b = __float_as_uint(w), mant = (b & 0x7fffffu) | 0x800000u;
+    const u64 hi = u64(static_cast<uint32_t>(f >> 24)) * mant;
+    const u64 lo = u64(static_cast<uint32_t>(f) & 0xffffffu) * mant;
+    // w = mant 2^-(150 - e); what has no such mantissa is below 2^-126
+    return ((hi << 10) + (lo >> 14)) >> min(136 - static_cast<int>(b >> 23), 63);
 }
 
 // the same shared object in block `rank` of the cluster (generic address)
@@ -395,9 +399,10 @@ __device__ __forceinline__ Row<T> make_row(const T* logits, const SampleArgs& a,
     return r;
 }
 
-// bounds of the exact total from the fast one
-__device__ __forceinline__ void total_bounds(u64 all, u64& lo, u64& hi) {
-    const u64 err = static_cast<u64>(static_cast<float>(all) * (kFastErr + 1.5e-11f)) + 8192;
+// bounds of the exact total from the fast one; half a unit of each exact weight's own on top
+__device__ __forceinline__ void total_bounds(u64 all, int V, u64& lo, u64& hi) {
+    const u64 err =
+        static_cast<u64>(static_cast<float>(all) * (kFastErr + 1.5e-11f)) + 2 * V + kFastUnits;
     lo = all > err ? all - err : 1;
     hi = all + err;
 }
@@ -593,7 +598,7 @@ __device__ bool fast_draw(const Row<T>& r, const float* cmax, const u64* cw, u64
     const u64 mid = lo + w0, hi = mid + w1;
     const float part = 2.f * s.u_value * (1.f - s.u_value) * kFastErr + 1.5e-11f;
     const u64 err = static_cast<u64>(static_cast<float>(all) * part) +
-                    static_cast<u64>(static_cast<float>(cw[chunk]) * kSumErr) + 8192;
+                    static_cast<u64>(static_cast<float>(cw[chunk]) * kSumErr) + r.V + kFastUnits;
     const bool hit0 = lo <= target && (lo == 0 || lo + err <= target) && target + err < mid;
     const bool hit1 = mid <= target && (mid == 0 || mid + err <= target) && target + err < hi;
     if (hit0 || hit1) {
@@ -858,7 +863,7 @@ __device__ bool short_draw(const Row<T>& r, const Settings& s, const float* smax
     if (s.want_p) {
         u64 lo = s_k, hi = s_k;                      // exact, where the list holds all that counts
         const bool whole = s.want_k || (r.V <= kShort && !by_m);
-        if (!whole) total_bounds(all, lo, hi);
+        if (!whole) total_bounds(all, r.V, lo, hi);
         const u64 need_lo = max(u64(1), part_of(s.top_p, lo, true));
         const u64 need_hi = whole ? need_lo : max(u64(1), part_of(s.top_p, hi, true));
         if (need_hi > sum.tv && !by_m) return false;
@@ -1796,7 +1801,7 @@ __device__ __forceinline__ void search_row(const T* logits, const SampleArgs& a,
     P.draw = P.exact = false;
     P.n_above = 0;
     P.all = head->all;
-    total_bounds(P.all, P.s_lo, P.s_hi);
+    total_bounds(P.all, a.V, P.s_lo, P.s_hi);
     P.key = kKeyNegInf;
     P.ties = 0;
     P.key_m = sh.key_m;

@@ -1,4 +1,5 @@
-"""Sampling near its borders: gaps in the logits at top_p's boundary.
+"""Sampling near its borders: gaps in the logits at top_p's boundary, rows with one
+dominant token.
 
 Compared with the definition in float64, one row at a time.  The kernel's weights carry a relative
 error of 2^-40 and a rounding to whole units of 2^-bits of the largest, V 2^bits < 2^64: sums are
@@ -99,3 +100,36 @@ def test_nuclei_of_a_staircase(dtype):
         for p in (0.5, 0.9, 0.99, 0.9999, 1 - 1e-6, 1 - 1e-8):
             u = 10.0 ** -torch.arange(8, dtype=torch.float32)
             assert check(z, u.clamp(max=0.9999).to(dev()), top_p=p) >= 4
+
+
+@pytest.mark.parametrize("v,n,gap", [(8003, 128, gap) for gap in (8.0, 14.0, 18.0003, 20.0, 21.5)] +
+                         [(151936, 48, gap) for gap in (8.0, 14.0, 16.5, 18.0003, 19.0)])
+def test_draws_from_the_tail_of_a_peaked_row(v, n, gap):
+    # one token holds nearly all weight, in the last column; u over the others' part
+    z = torch.full((1, v), -gap)
+    z[0, v - 1] = 0.0
+    tail = (v - 1) * float(np.exp(-np.float64(np.float32(gap))))
+    u = (torch.arange(n, dtype=torch.float64) + 0.37) / n * (tail / (1 + tail))
+    z = z.expand(n, v).contiguous()
+    assert check(z.to(dev()), u.float().to(dev())) >= n // 2
+    z += 0.3 * torch.randn(n, v, generator=torch.Generator().manual_seed(1)) * (z < 0)
+    assert check(z.to(dev()), u.float().to(dev())) >= n // 2
+
+
+def test_draws_next_to_a_long_light_tail():
+    # 2^20 columns of 127 units, between a token of weight 1 and one of weight 1/2: uniforms on both
+    # sides of the last one's border.  In the tail a token may be off by what the sums may.
+    v, n = 1 << 20, 64
+    z = torch.full((1, v), -float(np.log(2.0 ** weight_bits(v) / 127.0)))
+    z[0, 0], z[0, v - 1] = 0.0, -float(np.log(2.0))
+    w = np.exp(z[0].double().numpy())
+    c = np.cumsum(w)
+    u = np.float32(c[-2] / c[-1]) + np.arange(-n // 2, n // 2, dtype=np.float32) * np.float32(2.0 ** -24)
+    want = np.searchsorted(c, u.astype(np.float64) * c[-1], side="right")
+    units = (2.0 ** -39 * c[-1] + v * 2.0 ** -(weight_bits(v) + 1)) / w[1]
+    z, u = z.expand(8, v).contiguous().to(dev()), torch.from_numpy(u).to(dev())
+    tok = torch.cat([rlk.sample_logits(z, u[a:a + 8])[0] for a in range(0, n, 8)]).cpu().numpy()
+    assert (want[:n // 2 - 2] < v - 1).all() and (want[n // 2 + 2:] == v - 1).all()
+    far = np.abs(np.arange(n) - n // 2) > 2
+    assert (np.abs(tok - want)[far] <= units).all()
+    assert ((tok == v - 1) == (want == v - 1))[far].all()
