@@ -2045,8 +2045,12 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& args, cudaStream_t s
     const bool listed =
         a.min_p_value > 0.f || (a.top_k > 0 && a.top_k <= nseg / 2);
     const int64_t expected = own_settings ? a.N / 4 : listed ? 0 : a.N;
+    // A block's share stays below 2^20 columns, whose codes of 4096 would overflow a bin.
+    const auto share = [nch](int blocks) { return (nch + blocks - 1) / blocks * kChunk; };
     int search_ranks = ranks;
-    while (search_ranks > 2 && expected * search_ranks > 304) search_ranks /= 2;
+    while (search_ranks > 2 && expected * search_ranks > 304 &&
+           share(search_ranks / 2) < (1 << 20))
+        search_ranks /= 2;
     return launch_rows(sample_search_kernel<T>, logits, a, nch, search_ranks,
                        std::min(a.N, 304 / search_ranks), kSearch,
                        search_smem(nch, (nch + search_ranks - 1) / search_ranks), stream);

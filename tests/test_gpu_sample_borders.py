@@ -1,5 +1,5 @@
 """Sampling near its borders: gaps in the logits at top_p's boundary, rows with one
-dominant token.
+dominant token, the largest vocabularies.
 
 Compared with the definition in float64, one row at a time.  The kernel's weights carry a relative
 error of 2^-40 and a rounding to whole units of 2^-bits of the largest, V 2^bits < 2^64: sums are
@@ -133,3 +133,16 @@ def test_draws_next_to_a_long_light_tail():
     far = np.abs(np.arange(n) - n // 2) > 2
     assert (np.abs(tok - want)[far] <= units).all()
     assert ((tok == v - 1) == (want == v - 1))[far].all()
+
+
+@pytest.mark.parametrize("v,n", [(1 << 21, 78), (1 << 22, 40)])
+def test_flat_rows_of_the_largest_vocabularies(v, n):
+    # All tokens alike but one, which takes 5e-7 of a weight out of the total: a quarter of V is
+    # kept, and u times that gives the token exactly.
+    z = torch.full((n, v), -2.5, dtype=torch.bfloat16, device=dev())
+    z[:, v // 2] = -3.0
+    u = torch.arange(n, dtype=torch.float32, device=dev()) / n
+    tok, _, kept = rlk.sample_logits(z, u, 1e6, 0, 0.25)
+    assert torch.equal(tok, torch.floor(u.double() * (v // 4)).long())
+    want = -float(np.log(v // 4))
+    assert bool(((kept.double() - want).abs() <= 2.0 ** -19 - 2.0 ** -22 * want).all())
