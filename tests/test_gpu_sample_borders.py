@@ -1,5 +1,5 @@
-"""Sampling near its borders: gaps in the logits at top_p's boundary, rows with one
-dominant token, the largest vocabularies.
+"""Sampling near its borders: gaps in the logits at top_p's boundary, rows with one dominant token,
+the largest vocabularies, and batches that divide a row differently.
 
 Compared with the definition in float64, one row at a time.  The kernel's weights carry a relative
 error of 2^-40 and a rounding to whole units of 2^-bits of the largest, V 2^bits < 2^64: sums are
@@ -13,7 +13,7 @@ import torch
 
 import rl_post_linear_gb300 as rlk
 from helpers import dev
-from test_gpu_sample import ref_row
+from test_gpu_sample import ref_row, uniforms, zipf
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,24 @@ def test_flat_rows_of_the_largest_vocabularies(v, n):
     assert torch.equal(tok, torch.floor(u.double() * (v // 4)).long())
     want = -float(np.log(v // 4))
     assert bool(((kept.double() - want).abs() <= 2.0 ** -19 - 2.0 ** -22 * want).all())
+
+
+@pytest.mark.parametrize("setting", [{}, {"temperature": 0.7}, {"top_k": 50}, {"top_p": 0.9},
+                                     {"top_k": 2000, "top_p": 0.95}, {"min_p": 0.01}], ids=str)
+@pytest.mark.parametrize("v,dtype", [(151936, torch.float32), (151936, torch.bfloat16),
+                                     (70001, torch.float32)])
+def test_values_do_not_depend_on_the_batch(v, dtype, setting):
+    # 1, 64, 100, 256 and 700 rows: 8, 8, 4, 2 and 1 blocks a row at the larger size
+    g = torch.Generator().manual_seed(9)
+    base = torch.cat([zipf(48, v, 7, dtype), (2 * torch.randn(16, v, generator=g)).to(dtype).to(dev())])
+    u = uniforms(64, 8)
+    want = rlk.sample_logits(base, u, **setting)
+    for n in (100, 256, 700):
+        at = torch.arange(n, device=dev()) % 64
+        got = rlk.sample_logits(base[at], u[at], **setting)
+        for a, b in zip(want, got):
+            assert torch.equal(a[at], b)
+    for i in (0, 17, 63):
+        one = rlk.sample_logits(base[i:i + 1], u[i:i + 1], **setting)
+        for a, b in zip(want, one):
+            assert torch.equal(a[i:i + 1], b)
