@@ -802,12 +802,13 @@ int copy_mode(const void* p, int64_t stride, size_t esize) {
     return esize == 4 ? kCopy4 : kCopyPlain;
 }
 
-// a block's shared memory beyond 48 KB is asked for
+// A block's shared memory beyond 48 KB is asked for: always the most that the kernel may need, as
+// another thread's call with narrower rows may come between this and the launch.
 template <typename F>
-cudaError_t allow_smem(F kernel, size_t smem) {
+cudaError_t allow_smem(F kernel, size_t smem, size_t most) {
     if (smem <= 47 * 1024) return cudaSuccess;      // with the static part below 48 KB
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(smem));
+                                static_cast<int>(most));
 }
 
 int fit_of(const NormArgs& a, int threads) {
@@ -821,8 +822,9 @@ cudaError_t run_fwd(const NormArgs& a, int threads, cudaStream_t stream) {
     auto kernel = fit == 2   ? norm_fwd_kernel<T, CENTER, MAXT, 2>
                   : fit == 1 ? norm_fwd_kernel<T, CENTER, MAXT, 1>
                              : norm_fwd_kernel<T, CENTER, MAXT, 0>;
-    const size_t smem = size_t(threads) * kGroups * kGroup * sizeof(T) * stages_of<T, MAXT, 1>();
-    const cudaError_t e = allow_smem(kernel, smem);
+    constexpr size_t each = kGroups * kGroup * sizeof(T) * stages_of<T, MAXT, 1>();
+    const size_t smem = threads * each;
+    const cudaError_t e = allow_smem(kernel, smem, MAXT * each);
     if (e != cudaSuccess) return e;
     const int blocks = std::min(a.N, a.sms * fwd_blocks_per_sm(threads));
     return launch_early(kernel, dim3(blocks), threads, smem, stream, nullptr, a,
@@ -849,9 +851,9 @@ cudaError_t run_bwd(const NormArgs& a, int threads, int blocks, float* dwp, floa
     auto kernel = fit == 2   ? norm_bwd_kernel<T, CENTER, MAXT, 2>
                   : fit == 1 ? norm_bwd_kernel<T, CENTER, MAXT, 1>
                              : norm_bwd_kernel<T, CENTER, MAXT, 0>;
-    const size_t smem =
-        size_t(threads) * kGroups * kGroup * sizeof(T) * 2 * stages_of<T, MAXT, 2>();
-    const cudaError_t e = allow_smem(kernel, smem);
+    constexpr size_t each = kGroups * kGroup * sizeof(T) * 2 * stages_of<T, MAXT, 2>();
+    const size_t smem = threads * each;
+    const cudaError_t e = allow_smem(kernel, smem, MAXT * each);
     if (e != cudaSuccess) return e;
     return launch_early(kernel, dim3(blocks), threads, smem, stream, nullptr, a,
                         copy_mode(a.x, a.x_stride, sizeof(T)),

@@ -2000,10 +2000,16 @@ cudaError_t launch_rows(void (*kernel)(const T*, const SampleArgs, int, int, int
                         const T* logits, const SampleArgs& a, int nch, int ranks, int clusters,
                         int threads, size_t smem, cudaStream_t stream) {
     const int own = (nch + ranks - 1) / ranks;
+    // Always the most that any vocabulary needs: another thread's call with a smaller one may come
+    // between this and the launch.
+    constexpr int kMaxChunks = (1 << 22) / kChunk, kMost = 227 * 1024;
+    static_assert(scan_smem(kMaxChunks, kMaxSegments) <= kMost && exact_smem(kMaxChunks) <= kMost &&
+                      search_smem(kMaxChunks, (1 << 20) / kChunk) <= kMost,
+                  "a block's shared memory");
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        const cudaError_t e =
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute cluster;
