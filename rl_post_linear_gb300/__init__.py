@@ -1106,10 +1106,46 @@ def _as_rows(t, like=None):
     if like is not None:
         t = t.to(like.dtype)
     rows = t.reshape(-1, t.shape[-1])
+    return rows if _rows_apart(rows) else rows.contiguous()   # an expanded gradient, for instance
+
+
+def _rows_apart(rows):
     n, h = rows.shape
-    if (h > 1 and rows.stride(1) != 1) or (n > 1 and rows.stride(0) < h):
-        rows = rows.contiguous()                  # an expanded gradient, for instance
-    return rows
+    return (h == 1 or rows.stride(1) == 1) and (n <= 1 or rows.stride(0) >= h)
+
+
+def _with_row_view(x):
+    """x, or where its rows cannot be a view a copy that the forward and the backward share."""
+    if x.is_contiguous():
+        return x
+    try:
+        rows = x.detach().view(-1, x.shape[-1])
+    except RuntimeError:                          # no such view
+        return x.contiguous()
+    return x if _rows_apart(rows) else x.contiguous()
+
+
+class _FirstDerivatives(torch.autograd.Function):
+    """Gradients as they are; differentiating them is an error."""
+
+    @staticmethod
+    def forward(ctx, count, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the norms can be differentiated once: there is no kernel for the "
+                           "derivative of their gradients")
+
+
+def _once(grads, *inputs):
+    """The gradients of a backward, tied to what they depend on where autograd records it
+    (create_graph): as constants they would drop their part of a second derivative."""
+    if not torch.is_grad_enabled():
+        return grads
+    given = [g for g in grads if g is not None]
+    tied = iter(_FirstDerivatives.apply(len(given), *given, *inputs))
+    return tuple(None if g is None else next(tied) for g in grads)
 
 
 class LayerNorm(torch.autograd.Function):
@@ -1119,30 +1155,31 @@ class LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, active_mask):
         rows = _as_rows(x)
         y, mean, rstd = layer_norm_fwd(rows, weight, bias, eps, active_mask)
-        ctx.save_for_backward(rows, weight, mean, rstd, active_mask)
+        ctx.save_for_backward(x, weight, mean, rstd, active_mask)
         return y.view(x.shape)
 
     @staticmethod
     def backward(ctx, grad):
-        x, weight, mean, rstd, active_mask = ctx.saved_tensors
+        x_in, weight, mean, rstd, active_mask = ctx.saved_tensors
+        x = _as_rows(x_in)
         n, h = x.shape
         dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
         dw = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
         db = torch.empty_like(weight) if ctx.needs_input_grad[2] else None
         ws = _workspace(rlk_layer_norm_bwd_workspace_bytes(n, h), x.device)
         rlk_layer_norm_bwd(x, weight, _as_rows(grad, x), mean, rstd, active_mask, dx, dw, db, ws)
-        return dx.view(grad.shape), dw, db, None, None
+        return _once((dx.view(grad.shape), dw, db, None, None), x_in, weight, grad)
 
 
 def layer_norm(x, weight, bias=None, eps=1e-6, active_mask=None):
-    """Differentiable layer norm over the last axis of x [..., H]; active_mask: uint8, one byte
-    a row, in the order of x's leading axes.
+    """Differentiable layer norm over the last axis of x [..., H] (once: a second derivative is an
+    error); active_mask: uint8, one byte a row, in the order of x's leading axes.
 
     A training step can be captured in a CUDA graph.  As for every autograd operator, an eager
     graph of the same leaves that is still alive then has to come from the captured stream:
     autograd joins a leaf's gradient on the stream of the first live graph that used it, and a
     join with a stream outside the capture ends the capture."""
-    return LayerNorm.apply(x, weight, bias, eps, active_mask)
+    return LayerNorm.apply(_with_row_view(x), weight, bias, eps, active_mask)
 
 
 class RmsNorm(torch.autograd.Function):
@@ -1152,20 +1189,21 @@ class RmsNorm(torch.autograd.Function):
     def forward(ctx, x, weight, eps, active_mask):
         rows = _as_rows(x)
         y, rstd = rms_norm_fwd(rows, weight, eps, active_mask)
-        ctx.save_for_backward(rows, weight, rstd, active_mask)
+        ctx.save_for_backward(x, weight, rstd, active_mask)
         return y.view(x.shape)
 
     @staticmethod
     def backward(ctx, grad):
-        x, weight, rstd, active_mask = ctx.saved_tensors
+        x_in, weight, rstd, active_mask = ctx.saved_tensors
+        x = _as_rows(x_in)
         n, h = x.shape
         dx = torch.empty(n, h, dtype=x.dtype, device=x.device)
         dw = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
         ws = _workspace(rlk_rms_norm_bwd_workspace_bytes(n, h), x.device)
         rlk_rms_norm_bwd(x, weight, _as_rows(grad, x), rstd, active_mask, dx, dw, ws)
-        return dx.view(grad.shape), dw, None, None
+        return _once((dx.view(grad.shape), dw, None, None), x_in, weight, grad)
 
 
 def rms_norm(x, weight, eps=1e-6, active_mask=None):
-    """Differentiable RMS norm over the last axis of x [..., H]."""
-    return RmsNorm.apply(x, weight, eps, active_mask)
+    """Differentiable RMS norm over the last axis of x [..., H] (once, like layer_norm)."""
+    return RmsNorm.apply(_with_row_view(x), weight, eps, active_mask)

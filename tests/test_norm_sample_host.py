@@ -133,3 +133,28 @@ def test_binding_refuses_what_it_cannot_pass_on(lib):
         rlk.sample_logits(x, torch.zeros(4))
     with pytest.raises(ValueError):
         rlk.rms_norm_fwd(x, w)
+
+
+@pytest.mark.parametrize("wrt", ["x", "weight", "grad"])
+@pytest.mark.parametrize("norm", ["layer_norm", "rms_norm"])
+def test_second_derivatives_are_refused(monkeypatch, lib, norm, wrt):
+    # the launches stood in for; a gradient of the gradient has no kernel, so it must not read as 0
+    def forward(x, weight, *_):
+        return (x * weight,) + (torch.ones(x.shape[0]),) * (2 if norm == "layer_norm" else 1)
+
+    def backward(*args):
+        args[6 if norm == "layer_norm" else 5].fill_(1.0)           # dx
+
+    monkeypatch.setattr(rlk, norm + "_fwd", forward)
+    monkeypatch.setattr(rlk, "rlk_%s_bwd" % norm, backward)
+    t = {"x": torch.randn(2, 3, 8), "weight": torch.ones(8), "grad": torch.randn(2, 3, 8)}
+    t["x"].requires_grad_()
+    t[wrt].requires_grad_()
+    y = getattr(rlk, norm)(t["x"], t["weight"])
+    dx, = torch.autograd.grad(y, t["x"], t["grad"], retain_graph=True)
+    assert bool((dx == 1.0).all()) and not dx.requires_grad
+    dx, = torch.autograd.grad(y, t["x"], t["grad"], create_graph=True)
+    assert bool((dx == 1.0).all())
+    loss = dx.square().sum() + (t[wrt] ** 3).sum()
+    with pytest.raises(RuntimeError, match="differentiated once"):
+        torch.autograd.grad(loss, t[wrt])
