@@ -323,7 +323,7 @@ struct Ring {
                 for (int e = 0; e < kElems; ++e)
                     cp_async(dst + 4 * e, e < n ? src + e : row, e < n ? 4 : 0, false);
             } else {
-                T v[kElems];
+                alignas(16) T v[kElems];             // read as one piece
 #pragma unroll
                 for (int e = 0; e < kElems; ++e) v[e] = e < n ? src[e] : T(0.f);
                 *piece(stage, p) = *reinterpret_cast<const uint4*>(v);

@@ -214,7 +214,7 @@ __device__ __noinline__ Scanned block_scan(u64 v, uint32_t n, u64* part, uint32_
 template <typename T>
 __device__ __noinline__ uint4 load_single(const T* row, int V, int c) {
     constexpr int VEC = 16 / sizeof(T);
-    T v[VEC];
+    alignas(16) T v[VEC];                // read as one
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = c + e < V ? row[c + e] : T(-INFINITY);
     return *reinterpret_cast<const uint4*>(v);
