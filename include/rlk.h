@@ -528,6 +528,7 @@ rlk_status_t rlk_dlogp_audit_noalloc(const float* logp_new, const float* logp_ol
  *               statistics are 0, and they add nothing to dweight and dbias
  *   eps         finite, >= 0
  *   mean_out, rstd_out  [N] fp32 or NULL: what the backward takes back
+ *   (every array aligned to its element: RLK_ERR_INVALID_VALUE otherwise)
  *   dweight, dbias [H] w_dtype, overwritten; either may be NULL
  *   workspace   rlk_*_norm_bwd_workspace_bytes(N, H), 256-aligned (needed when dweight or
  *               dbias is asked for); its contents on entry do not matter
@@ -593,6 +594,7 @@ typedef struct {
  *   uniforms    [N] fp32
  *   active_mask [N] uint8 or NULL; inactive rows give token -1, logp 0, and are never read
  *   tokens_out  [N] int64; logp_out, kept_logp_out [N] fp32 or NULL
+ *   (every array, the settings' too, aligned to its element: RLK_ERR_INVALID_VALUE otherwise)
  *   workspace   rlk_sample_logits_workspace_bytes(N, V) bytes, 256-aligned (may be NULL when
  *               that is 0); its contents on entry do not matter
  * Sums of weights are 64-bit integers of about 40 correct bits, so the token is that of

@@ -727,7 +727,8 @@ rlk_status_t norm_fwd(bool center, const void* x, int32_t x_dtype, int64_t x_str
     if (N == 0) return RLK_OK;
     const size_t es = x_dtype == RLK_DTYPE_F32 ? 4 : 2, wes = w_dtype == RLK_DTYPE_F32 ? 4 : 2;
     if (x == nullptr || weight == nullptr || y == nullptr) return RLK_ERR_INVALID_VALUE;
-    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, wes) || !aligned(bias, wes))
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, wes) || !aligned(bias, wes) ||
+        !aligned(mean_out, 4) || !aligned(rstd_out, 4))
         return RLK_ERR_INVALID_VALUE;
     DeviceInfo dev;
     RLK_TRY(current_device(dev));
@@ -759,7 +760,7 @@ rlk_status_t norm_bwd(bool center, const void* x, int32_t x_dtype, int64_t x_str
                   rstd == nullptr || (center && mean == nullptr)))
         return RLK_ERR_INVALID_VALUE;
     if (!aligned(x, es) || !aligned(dy, es) || !aligned(dx, es) || !aligned(weight, wes) ||
-        !aligned(dweight, wes) || !aligned(dbias, wes))
+        !aligned(dweight, wes) || !aligned(dbias, wes) || !aligned(mean, 4) || !aligned(rstd, 4))
         return RLK_ERR_INVALID_VALUE;
     if (params && (workspace == nullptr || !aligned(workspace, 256) ||
                    workspace_bytes < rlk::norm_bwd_workspace(N, H, center)))
@@ -858,7 +859,11 @@ rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int
     if (logits == nullptr || uniforms == nullptr || tokens_out == nullptr)
         return RLK_ERR_INVALID_VALUE;
     const size_t es = dtype == RLK_DTYPE_F32 ? 4 : 2;
-    if (!aligned(logits, es)) return RLK_ERR_INVALID_VALUE;
+    if (!aligned(logits, es) || !aligned(uniforms, 4) || !aligned(tokens_out, 8) ||
+        !aligned(logp_out, 4) || !aligned(kept_logp_out, 4) || !aligned(p.temperature_rows, 4) ||
+        !aligned(p.top_k_rows, 4) || !aligned(p.top_p_rows, 4) || !aligned(p.min_p_rows, 4) ||
+        !aligned(device_error_word, 4))
+        return RLK_ERR_INVALID_VALUE;
     const size_t need = rlk::sample_workspace(N, V);
     if (need > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need))
         return RLK_ERR_WORKSPACE;

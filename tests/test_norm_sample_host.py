@@ -158,3 +158,22 @@ def test_second_derivatives_are_refused(monkeypatch, lib, norm, wrt):
     loss = dx.square().sum() + (t[wrt] ** 3).sum()
     with pytest.raises(RuntimeError, match="differentiated once"):
         torch.autograd.grad(loss, t[wrt])
+
+
+def test_arrays_have_to_be_aligned_to_their_elements(lib):
+    # a kernel that reads or writes them would fault
+    for name in ("mean", "rstd"):
+        for at in (1, 2, 3):
+            assert call(lib.rlk_layer_norm_fwd, FWD, **{name: FAKE + at}) == INVALID
+            assert call(lib.rlk_layer_norm_bwd, BWD, **{name: FAKE + at}) == INVALID
+    assert call(lib.rlk_rms_norm_fwd, FWD, ("bias", "mean"), rstd=FAKE + 2) == INVALID
+    assert call(lib.rlk_rms_norm_bwd, BWD, ("mean", "db"), rstd=FAKE + 2) == INVALID
+    for name in ("u", "tokens", "logp", "kept", "err"):
+        assert sample(lib, **{name: FAKE + 2}) == INVALID
+    assert sample(lib, tokens=FAKE + 4) == INVALID
+    for i in range(4):
+        rows = [None] * 4
+        rows[i] = FAKE + 2
+        p = rlk.SampleParams(*rows, 1.0, 0, 1.0, 0.0)
+        assert lib.rlk_sample_logits(FAKE, F32, 4, 1000, 1000, FAKE, None, ctypes.byref(p), FAKE,
+                                     FAKE, FAKE, FAKE, 1 << 40, None, None) == INVALID
