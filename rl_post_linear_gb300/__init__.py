@@ -798,7 +798,10 @@ def _sample_params(n, temperature, top_k, top_p, min_p):
         _need(top_k, torch.int32, "top_k", (n,))
         p.top_k_rows = top_k.data_ptr()
     else:
-        p.top_k = int(top_k)
+        k = int(top_k)
+        if k != top_k:
+            raise ValueError("top_k must be a whole number, got %r" % (top_k,))
+        p.top_k = max(-1, min(k, 1 << 62))        # not wrapped into 64 bits
     if isinstance(top_p, torch.Tensor):
         _need(top_p, torch.float32, "top_p", (n,))
         p.top_p_rows = top_p.data_ptr()

@@ -177,3 +177,15 @@ def test_arrays_have_to_be_aligned_to_their_elements(lib):
         p = rlk.SampleParams(*rows, 1.0, 0, 1.0, 0.0)
         assert lib.rlk_sample_logits(FAKE, F32, 4, 1000, 1000, FAKE, None, ctypes.byref(p), FAKE,
                                      FAKE, FAKE, FAKE, 1 << 40, None, None) == INVALID
+
+
+def test_scalar_top_k_reaches_the_kernel_as_it_is():
+    def passed(top_k):
+        return rlk._sample_params(4, 1.0, top_k, 1.0, 0.0).top_k
+
+    assert passed(50) == passed(50.0) == passed(torch.tensor([50])[0].item()) == 50
+    assert passed(1 << 64) >= 1 << 22 and passed((1 << 64) + 5) >= 1 << 22       # off
+    assert passed(-(1 << 64) + 5) < 0                                           # refused
+    for bad in (2.7, math.nan, math.inf):
+        with pytest.raises((ValueError, OverflowError)):
+            passed(bad)
