@@ -588,7 +588,8 @@ typedef struct {
  *   logp = x_token/T - log sum_v exp(x_v/T)        (all v: rlk_logp_from_logits' value)
  *   kept_logp = the same with the sum over the kept tokens (the truncated distribution's)
  *
- * Greedy decoding is top_k = 1.  -inf entries (banned tokens) are never drawn.
+ * Greedy decoding is top_k = 1.  -inf entries (banned tokens) are never drawn, nor are tokens of a
+ * weight below 2^-(b + 1) (b below): u = 0 gives the first token of that weight or more.
  *
  *   logits      [N, row_stride] (V <= row_stride used), fp32 or bf16, aligned to the element
  *   uniforms    [N] fp32
@@ -597,9 +598,13 @@ typedef struct {
  *   (every array, the settings' too, aligned to its element: RLK_ERR_INVALID_VALUE otherwise)
  *   workspace   rlk_sample_logits_workspace_bytes(N, V) bytes, 256-aligned (may be NULL when
  *               that is 0); its contents on entry do not matter
- * Sums of weights are 64-bit integers of about 40 correct bits, so the token is that of
- * exact arithmetic unless u times the total lies within about 1e-12 of a border, and it
- * depends on the row alone (not on the batch, the mask or alignment).  V <= 2^22
+ * Weights are held as integers in units of 2^-b, each off by 2^-39 of itself and half a unit; b is
+ * the largest up to 46 with V 2^b < 2^64 (46 for V < 2^18, 41 at V = 2^22).  Sums of them are exact.
+ * So the token is that of exact arithmetic unless u times the kept total, or top_p's boundary, lies
+ * within 2^-39 S + V 2^-(b + 1) of a border, S = sum w_v.  (The second part is for tokens that are
+ * all rounded the same way, 1e-9 for 150k of them.)  Token, logp and kept_logp depend on the row and
+ * its settings alone, not on the batch, the mask or alignment; the last bits of logp may differ
+ * between settings given as scalars and the same ones given as arrays.  V <= 2^22
  * (RLK_ERR_UNSUPPORTED above).  A row with NaN or +inf, or with nothing above -inf, gives
  * token -1, logp NaN and RLK_DEVERR_LOGITS; a row whose own settings or uniform are out of
  * range gives the same with RLK_DEVERR_SAMPLE_PARAM.  Scalar settings out of range are

@@ -924,8 +924,9 @@ const char* rlk_contract_string(void) {
                               "data-parallel dW: fp32 partials merged in rank order, one "
                               "rounding; norms: fp32, a row's sums ordered by H alone, dweight "
                               "and dbias summed per block in ascending rows and merged in a "
-                              "fixed tree; sampling: weights as 64-bit integers of 40 or more "
-                              "correct bits, ties to the lowest index";
+                              "fixed tree; sampling: weights as integers in units of 2^-46 (2^-41 "
+                              "at V = 2^22) of the row's largest, off by 2^-39 and half a unit, "
+                              "64-bit sums, ties to the lowest index";
 }
 
 const char* rlk_status_string(rlk_status_t status) {

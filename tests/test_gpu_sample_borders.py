@@ -135,6 +135,20 @@ def test_draws_next_to_a_long_light_tail():
     assert ((tok == v - 1) == (want == v - 1))[far].all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tokens_below_half_a_unit_are_not_drawn(dtype):
+    # weights of 2^-57.7 in front, one of 2^-45 behind them, the largest last: u = 0 draws the second
+    for v in (700, 30011):
+        z = torch.full((3, v), -40.0)
+        z[:, v - 2], z[:, v - 1] = -45.0 * float(np.log(2.0)), 0.0
+        u = torch.tensor([0.0, 2.0 ** -60, 2.0 ** -24], device=dev())
+        for setting in ({}, {"top_p": 1 - 2.0 ** -20}, {"top_k": 5}):
+            tok, logp, kept = rlk.sample_logits(z.to(dtype).to(dev()), u, **setting)
+            last = v - 1 if "top_p" in setting else v - 2        # all but the largest is cut
+            assert tok.tolist() == [last, last, v - 1]
+            assert bool((kept >= logp).all())
+
+
 @pytest.mark.parametrize("v,n", [(1 << 21, 78), (1 << 22, 40)])
 def test_flat_rows_of_the_largest_vocabularies(v, n):
     # All tokens alike but one, which takes 5e-7 of a weight out of the total: a quarter of V is
