@@ -38,14 +38,14 @@
 // The second launch takes the rows that are left.  Without truncation they are weighed
 // exactly.  With it (a wide nucleus, a large top_k, a row sorted by token) they are searched:
 // histograms of 2048 bins of the scaled distance from the maximum, then of the keys inside
-// the remaining window, close in on the boundary until its window fits a list or is a single
-// value.  One block of the cluster decides each step; the blocks work on their own chunks in
+// the remaining window (with the weights as integers, so each leaves one bin of it), close in on
+// the boundary until its window fits a list or is a single value.  One block of the cluster decides each step; the blocks work on their own chunks in
 // between.
 //
-// Measured at V = 151936, fp32 (HBM's floor in brackets): one row 10.2 us; [256] 54 us (23),
+// Measured at V = 151936, fp32 (HBM's floor in brackets): one row 10.7 us; [256] 54 us (23),
 // of which the scan takes 33 and the rows weighed exactly 17; [64] with top_k = 50 and top_p
-// 24 us (5.7); [1024] 139 us (92).  A row with a wide nucleus takes 55 us by itself, 256 of
-// them 426 us: 168 instructions an element in all, and block 0's decisions, for which the
+// 24 us (5.7); [1024] 141 us (92).  A row with a wide nucleus takes 56 us by itself, 256 of
+// them 420 us: 168 instructions an element in all, and block 0's decisions, for which the
 // other blocks wait, bind the search, not memory.
 #include <cuda_bf16.h>
 
@@ -2047,8 +2047,8 @@ cudaError_t launch_typed(const T* logits, const SampleArgs& args, cudaStream_t s
     // The search: two blocks on each of 152 SMs, and smaller clusters where more rows than clusters
     // are to be expected: nearly all rows where a wide nucleus is all that cuts, about a fifth where
     // each row brings its own settings, few otherwise.  V = 151936, top_p alone, with 8, 4, 2 and 1
-    // blocks a row: fp32 [1] 55, 66, 92, 140 us; [64] 205, 171, 192, 280; [256] 744, 476, 426, 461;
-    // bf16 [256] 653, 420, 352, 396.
+    // blocks a row: fp32 [1] 56, 67, 94, 143 us; [64] 200, 164, 188, 276; [256] 735, 463, 420, 449;
+    // bf16 [256] 672, 421, 355, 390.
     const bool own_settings =
         a.top_k_rows != nullptr || a.top_p_rows != nullptr || a.min_p_rows != nullptr;
     const bool listed =
