@@ -618,6 +618,129 @@ rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int
                                void* workspace, size_t workspace_bytes,
                                uint32_t* device_error_word, cudaStream_t stream);
 
+/* Settings of rlk_process_logits (a host structure, read during the call).  Pointers are device
+ * arrays or NULL.  A *_rows member has one value a row; NULL: the scalar holds for every row. */
+typedef struct {
+    const int64_t* tokens;          /* [N, tokens_stride]: a row's prompt, then what it drew */
+    const int64_t* lengths;         /* [N] how many of them count; NULL: tokens_width */
+    const int64_t* prompt_lengths;  /* [N] how many of those are the prompt; NULL: 0 */
+    int64_t tokens_width, tokens_stride;
+    const float* repetition_rows;
+    const float* frequency_rows;
+    const float* presence_rows;
+    double repetition;              /* > 0, finite; 1: off */
+    double frequency;               /* finite; 0: off */
+    double presence;                /* finite; 0: off */
+    const int64_t* bias_ids;        /* [N, bias_count] */
+    const float* bias_values;       /* [N, bias_count] */
+    int64_t bias_count;             /* 0 .. 4096 */
+    const int32_t* allowed;         /* [N, allowed_stride]: bit v % 32 of word v / 32 */
+    int64_t allowed_stride;         /* words, >= ceil(V / 32) */
+} rlk_process_params_t;
+
+/*
+ * Penalties for repeated tokens, biases and masks on logits: what a rollout does to the head's
+ * logits before it draws from them with rlk_sample_logits.  "RL-Kernel integration roadmap for
+ * vime", Consistency Contract (the settings a rollout draws with).  For an active row x_v, with
+ * c_v how often v stands among its drawn tokens:
+ *
+ *   x = x > 0 ? x / repetition : x repetition    for v among its tokens, prompt and drawn
+ *   x = x - frequency c_v - presence             for c_v > 0
+ *   x = x + b                                    for each slot of bias_ids that names v
+ *   x = -inf                                     where the bit of v in allowed is 0
+ *
+ *   logits, out [N, row stride] (V used), dtype fp32 or bf16, rows contiguous, aligned to the
+ *               element.  out may be logits itself (the same pointer and stride); otherwise
+ *               they must not overlap.
+ *   active_mask [N] uint8 or NULL: rows of mask 0 are neither read nor written
+ *   tokens, bias_ids: a negative id is an empty slot.  An id named by several slots of bias_ids
+ *               gets their sum, in ascending slots.
+ *   (every array aligned to its element: RLK_ERR_INVALID_VALUE otherwise)
+ * Arithmetic is fp32 with one rounding to dtype; columns that nothing names keep their bits
+ * (unless masked).  Token counts are whole numbers: results depend on the row alone.
+ * A row with an id >= V (RLK_DEVERR_TARGET_RANGE), with lengths outside 0 <= prompt <= length <=
+ * tokens_width or with a row's setting out of its range (RLK_DEVERR_SAMPLE_PARAM) becomes NaN.
+ * Scalar settings out of range are RLK_ERR_INVALID_VALUE; tokens_width > 2^29, bias_count > 4096
+ * or V > 2^22 is RLK_ERR_UNSUPPORTED.
+ */
+rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                                int64_t row_stride, const uint8_t* active_mask,
+                                const rlk_process_params_t* params, void* out,
+                                int64_t out_stride, uint32_t* device_error_word,
+                                cudaStream_t stream);
+
+/*
+ * The K largest log-probs of each row of logits with their tokens: what a teacher sends to a
+ * student (rlk_linear_topk_kl_fwd), or a server with a token.  For an active row x_v:
+ *
+ *   lse = log sum_v exp(x_v / T);  order: x descending, lowest index first among equals
+ *   ids[j], logp[j] = the order's j-th v and x_v / T - lse
+ *
+ *   logits      [N, row_stride] (V used), fp32 or bf16, aligned to the element
+ *   temperature finite, > 0
+ *   K           1 .. 1024
+ *   active_mask [N] uint8 or NULL; inactive rows are never read and give ids -1, logp 0, lse 0
+ *   ids_out     [N, K] int64; logp_out [N, K] fp32; lse_out [N] fp32 or NULL
+ * Entries of -inf (banned tokens) are not listed: slots that are left have id -1 and logp -inf.
+ * A row with NaN or +inf, or with nothing above -inf, gives ids -1, logp and lse NaN and
+ * RLK_DEVERR_LOGITS.  A row's results depend on the row alone.  V <= 2^22.
+ */
+rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                           int64_t row_stride, const uint8_t* active_mask, int64_t K,
+                           double temperature, int64_t* ids_out, float* logp_out, float* lse_out,
+                           uint32_t* device_error_word, cudaStream_t stream);
+
+/*
+ * KL of the LM head against a teacher's top tokens, forward and backward.  "RL-Kernel Roadmap
+ * (2026)", backlog: distillation KL fused with lm_head; here the teacher is not a head but K
+ * tokens a row with their log-weights a (rlk_topk_logp's, say).  For an active row, with
+ * p = softmax(hidden W^T / T):
+ *
+ *   A = renormalize ? log sum_k exp a_k : 0,  q_k = exp(a_k - A),  Q = sum_k q_k
+ *   logp[k] = log p[id_k],  kl = sum_k q_k (a_k - A - logp[k])
+ *   dL/ds[t,v] = grad_kl[t] (Q_t p[t,v] - sum_{k: id_k = v} q_k) / T    (s = hidden W^T)
+ *
+ * So without renormalize the teacher's mass outside its K tokens counts 0; with it the K are the
+ * whole distribution.  The [N,V] logits are never materialised.
+ *
+ *   hidden [N,H], weight [V,H]  bf16, row-major, 16-byte aligned; H a multiple of 64
+ *   teacher_ids  [N,K] int64, in any order; a negative id is an empty slot, an id that a row
+ *                names more than once counts with the sum of its weights (1 <= K <= 1024)
+ *   teacher_logp [N,K] fp32, a: -inf counts 0, values of empty slots are not used.  Without
+ *                renormalize exp(a) has to be within fp32.
+ *   active_mask  [N] uint8 or NULL; hidden rows of inactive tokens are never read, and they
+ *                give kl, lse, logp and dhidden 0
+ *   kl_out, lse_out [N] fp32; logp_out [N,K] fp32 (0 in empty slots): the backward takes lse
+ *                and logp back
+ *   grad_kl      [N] fp32, dL/dkl
+ *   dhidden [N,H], dweight [V,H]  bf16, overwritten, 16-byte aligned
+ *   (every other array aligned to its element: RLK_ERR_INVALID_VALUE otherwise)
+ *   workspace    the matching query's bytes, 256-aligned; its contents on entry do not matter
+ * A row without any weight gives kl 0 and no gradient.  A row with an id >= V
+ * (RLK_DEVERR_TARGET_RANGE), or with NaN or +inf as log-weight of an id (RLK_DEVERR_LOGITS),
+ * gives kl and logp NaN; the backward gives it no gradient.  Accumulation is fp32, with the mean
+ * of what the tensor cores cut off a logit given back (lse may differ from rlk_linear_logp_fwd's
+ * by that, 1e-9 H of a logit); dhidden and dweight are rounded once.  kl, lse, logp and dhidden rows do not depend on the batch; dweight
+ * is reproducible bit for bit.
+ */
+size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K);
+rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
+                                    const int64_t* teacher_ids, const float* teacher_logp,
+                                    const uint8_t* active_mask, int64_t N, int64_t H, int64_t V,
+                                    int64_t K, double temperature, int32_t renormalize,
+                                    float* kl_out, float* lse_out, float* logp_out,
+                                    void* workspace, size_t workspace_bytes,
+                                    uint32_t* device_error_word, cudaStream_t stream);
+size_t rlk_linear_topk_kl_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K);
+rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
+                                    const int64_t* teacher_ids, const float* teacher_logp,
+                                    const uint8_t* active_mask, const float* grad_kl,
+                                    const float* lse, const float* logp, int64_t N, int64_t H,
+                                    int64_t V, int64_t K, double temperature, int32_t renormalize,
+                                    void* dhidden, void* dweight, void* workspace,
+                                    size_t workspace_bytes, uint32_t* device_error_word,
+                                    cudaStream_t stream);
+
 /* Build fingerprint and the fixed numeric contract (tile shapes, chunk widths,
  * accumulation and rounding points).  Static string, never NULL. */
 const char* rlk_contract_string(void);

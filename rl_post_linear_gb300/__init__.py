@@ -102,6 +102,18 @@ class SampleParams(ctypes.Structure):
     ]
 
 
+class ProcessParams(ctypes.Structure):
+    """Mirror of rlk_process_params_t (a host structure)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("tokens", "lengths", "prompt_lengths")] + \
+               [(n, ctypes.c_int64) for n in ("tokens_width", "tokens_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("repetition_rows", "frequency_rows",
+                                               "presence_rows")] + \
+               [(n, ctypes.c_double) for n in ("repetition", "frequency", "presence")] + \
+               [(n, ctypes.c_void_p) for n in ("bias_ids", "bias_values")] + \
+               [("bias_count", ctypes.c_int64), ("allowed", ctypes.c_void_p),
+                ("allowed_stride", ctypes.c_int64)]
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load librlk.so (built by ``rl_post_linear_gb300.build``); raise if it is missing."""
     global _lib
@@ -193,13 +205,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             ("rlk_rms_norm_bwd", [_vp, i32, _i64, _vp, i32, _vp, _i64, _vp, _vp, _i64, _i64, _vp,
                                   _i64, _vp, _vp, _sz, _vp]),
             ("rlk_sample_logits", [_vp, i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                   _sz, _vp, _vp])):
+                                   _sz, _vp, _vp]),
+            ("rlk_process_logits", [_vp, i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp]),
+            ("rlk_topk_logp", [_vp, i32, _i64, _i64, _i64, _vp, _i64, f64, _vp, _vp, _vp, _vp,
+                               _vp]),
+            ("rlk_linear_topk_kl_fwd", [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, f64, i32,
+                                        _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+            ("rlk_linear_topk_kl_bwd", [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                        _i64, f64, i32, _vp, _vp, _vp, _sz, _vp, _vp])):
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name).argtypes = args
     for name in ("rlk_layer_norm_bwd_workspace_bytes", "rlk_rms_norm_bwd_workspace_bytes",
                  "rlk_sample_logits_workspace_bytes"):
         getattr(lib, name).restype = _sz
         getattr(lib, name).argtypes = [_i64, _i64]
+    for name in ("rlk_linear_topk_kl_fwd_workspace_bytes", "rlk_linear_topk_kl_bwd_workspace_bytes"):
+        getattr(lib, name).restype = _sz
+        getattr(lib, name).argtypes = [_i64, _i64, _i64, _i64]
     lib.rlk_contract_string.restype = ctypes.c_char_p
     lib.rlk_contract_string.argtypes = []
     lib.rlk_status_string.restype = ctypes.c_char_p
@@ -261,6 +283,14 @@ def rlk_rms_norm_bwd_workspace_bytes(N: int, H: int) -> int:
 
 def rlk_sample_logits_workspace_bytes(N: int, V: int) -> int:
     return int(load().rlk_sample_logits_workspace_bytes(N, V))
+
+
+def rlk_linear_topk_kl_fwd_workspace_bytes(N: int, H: int, V: int, K: int) -> int:
+    return int(load().rlk_linear_topk_kl_fwd_workspace_bytes(N, H, V, K))
+
+
+def rlk_linear_topk_kl_bwd_workspace_bytes(N: int, H: int, V: int, K: int) -> int:
+    return int(load().rlk_linear_topk_kl_bwd_workspace_bytes(N, H, V, K))
 
 
 # ----------------------------------------------------------------------------- marshalling
@@ -838,6 +868,143 @@ def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, 
     _check("rlk_sample_logits", st)
 
 
+def _number_or_rows(p, name, value, n):
+    """A setting of a row: a number into p.name, or a CUDA tensor [n] into p.name_rows."""
+    if isinstance(value, torch.Tensor):
+        _need(value, torch.float32, name, (n,))
+        setattr(p, name + "_rows", value.data_ptr())
+    else:
+        setattr(p, name, float(value))
+
+
+def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence,
+                       bias_ids, bias_values, allowed, active_mask, out, device_error_word=None,
+                       stream=None):
+    """Penalties, biases and masks on logits [N, V] (fp32 or bf16, rows contiguous, any row
+    stride) into out (the same dtype and shape; may be logits itself).  repetition, frequency,
+    presence: a number or a float32 tensor [N].  tokens [N, L] int64 (rows contiguous), lengths
+    and prompt_lengths [N] int64, bias_ids [N, B] int64 with bias_values [N, B] float32, allowed
+    [N, >= ceil(V / 32)] int32 bits, active_mask: or None.  See include/rlk.h."""
+    n, v, stride = _need_rows(logits, "logits")
+    out_stride = _need_rows(out, "out", (n, v), logits.dtype)[2]
+    p = ProcessParams(repetition=1.0)
+    if tokens is not None:
+        if tokens.dtype is not torch.int64:
+            raise TypeError("tokens must be int64, got %s" % tokens.dtype)
+        rows, p.tokens_width, p.tokens_stride = _need_rows(tokens, "tokens")
+        if rows != n:
+            raise ValueError("tokens must have %d rows, got %d" % (n, rows))
+        p.tokens = tokens.data_ptr()
+        if lengths is not None:
+            _need(lengths, torch.int64, "lengths", (n,))
+            p.lengths = lengths.data_ptr()
+        if prompt_lengths is not None:
+            _need(prompt_lengths, torch.int64, "prompt_lengths", (n,))
+            p.prompt_lengths = prompt_lengths.data_ptr()
+    elif lengths is not None or prompt_lengths is not None:
+        raise ValueError("lengths and prompt_lengths are of tokens")
+    _number_or_rows(p, "repetition", repetition, n)
+    _number_or_rows(p, "frequency", frequency, n)
+    _number_or_rows(p, "presence", presence, n)
+    if (bias_ids is None) != (bias_values is None):
+        raise ValueError("bias_ids and bias_values belong together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise ValueError("bias_ids must be [N, B]")
+        b = bias_ids.shape[1]
+        _need(bias_ids, torch.int64, "bias_ids", (n, b))
+        _need(bias_values, torch.float32, "bias_values", (n, b))
+        if b > 0:
+            p.bias_ids, p.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
+            p.bias_count = b
+    if allowed is not None:
+        if allowed.dtype is not torch.int32:
+            raise TypeError("allowed must be int32, got %s" % allowed.dtype)
+        rows, words, p.allowed_stride = _need_rows(allowed, "allowed")
+        if rows != n or words < (v + 31) // 32:
+            raise ValueError("allowed must be [%d, >= %d], got %s"
+                             % (n, (v + 31) // 32, tuple(allowed.shape)))
+        p.allowed = allowed.data_ptr()
+    if active_mask is not None:
+        _need(active_mask, torch.uint8, "active_mask", (n,))
+    st = load().rlk_process_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
+                                   _ptr(active_mask), ctypes.byref(p), _ptr(out), out_stride,
+                                   _ptr(device_error_word), _stream(stream))
+    _check("rlk_process_logits", st)
+
+
+def rlk_topk_logp(logits, active_mask, temperature, ids, logp, lse, device_error_word=None,
+                  stream=None):
+    """The K largest log-probs of each row of logits [N, V] (fp32 or bf16, rows contiguous, any
+    row stride) into ids [N, K] int64 and logp [N, K] float32; active_mask and lse may be None.
+    See include/rlk.h."""
+    n, v, stride = _need_rows(logits, "logits")
+    if ids.dim() != 2:
+        raise ValueError("ids must be [N, K]")
+    k = ids.shape[1]
+    _need(ids, torch.int64, "ids", (n, k))
+    _need(logp, torch.float32, "logp", (n, k))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (n,))
+    if active_mask is not None:
+        _need(active_mask, torch.uint8, "active_mask", (n,))
+    st = load().rlk_topk_logp(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
+                              _ptr(active_mask), k, float(temperature), _ptr(ids), _ptr(logp),
+                              _ptr(lse), _ptr(device_error_word), _stream(stream))
+    _check("rlk_topk_logp", st)
+
+
+def _need_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask, lse, logp, workspace):
+    """(n, h, v, k) of the arguments that both directions have."""
+    n, h = hidden.shape
+    v = weight.shape[0]
+    k = teacher_ids.shape[1]
+    _need(hidden, torch.bfloat16, "hidden")
+    _need(weight, torch.bfloat16, "weight", (v, h))
+    _need(teacher_ids, torch.int64, "teacher_ids", (n, k))
+    _need(teacher_logp, torch.float32, "teacher_logp", (n, k))
+    if active_mask is not None:
+        _need(active_mask, torch.uint8, "active_mask", (n,))
+    _need(lse, torch.float32, "lse", (n,))
+    _need(logp, torch.float32, "logp", (n, k))
+    _need(workspace, torch.uint8, "workspace")
+    return n, h, v, k
+
+
+def rlk_linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask, temperature,
+                           renormalize, kl_out, lse_out, logp_out, workspace,
+                           device_error_word=None, stream=None):
+    """KL of the head against a teacher's top tokens [N, K]; see include/rlk.h."""
+    n, h, v, k = _need_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask, lse_out,
+                               logp_out, workspace)
+    _need(kl_out, torch.float32, "kl_out", (n,))
+    st = load().rlk_linear_topk_kl_fwd(_ptr(hidden), _ptr(weight), _ptr(teacher_ids),
+                                       _ptr(teacher_logp), _ptr(active_mask), n, h, v, k,
+                                       float(temperature), int(bool(renormalize)), _ptr(kl_out),
+                                       _ptr(lse_out), _ptr(logp_out), _ptr(workspace),
+                                       workspace.numel(), _ptr(device_error_word),
+                                       _stream(stream))
+    _check("rlk_linear_topk_kl_fwd", st)
+
+
+def rlk_linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse,
+                           logp, temperature, renormalize, dhidden, dweight, workspace,
+                           device_error_word=None, stream=None):
+    """Its backward for hidden and weight; lse and logp are the forward's.  See include/rlk.h."""
+    n, h, v, k = _need_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask, lse, logp,
+                               workspace)
+    _need(grad_kl, torch.float32, "grad_kl", (n,))
+    _need(dhidden, torch.bfloat16, "dhidden", (n, h))
+    _need(dweight, torch.bfloat16, "dweight", (v, h))
+    st = load().rlk_linear_topk_kl_bwd(_ptr(hidden), _ptr(weight), _ptr(teacher_ids),
+                                       _ptr(teacher_logp), _ptr(active_mask), _ptr(grad_kl),
+                                       _ptr(lse), _ptr(logp), n, h, v, k, float(temperature),
+                                       int(bool(renormalize)), _ptr(dhidden), _ptr(dweight),
+                                       _ptr(workspace), workspace.numel(),
+                                       _ptr(device_error_word), _stream(stream))
+    _check("rlk_linear_topk_kl_bwd", st)
+
+
 # ----------------------------------------------------------------------------- conveniences
 
 def _workspace(nbytes, device):
@@ -1023,6 +1190,59 @@ def sample_logits(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     return tokens, logp, kept
 
 
+def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repetition=1.0,
+                   frequency=0.0, presence=0.0, bias_ids=None, bias_values=None, allowed=None,
+                   active_mask=None, out=None, error_word=None):
+    """Logits [N,V] after penalties for repeated tokens, biases and a mask, to draw from with
+    sample_logits.  tokens [N,L]: each row's prompt (prompt_lengths of them) and what it drew (up
+    to lengths); a negative id is an empty slot.  allowed: int32 bits, one a column.  out may be
+    logits itself; rows of active_mask 0 are left as they are (0 where out is made here)."""
+    if out is None:
+        make = torch.empty if active_mask is None else torch.zeros
+        out = make(logits.shape, dtype=logits.dtype, device=logits.device)
+    rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence,
+                       bias_ids, bias_values, allowed, active_mask, out, error_word)
+    return out
+
+
+def topk_logp(logits, k, temperature=1.0, active_mask=None, error_word=None):
+    """(ids [N,k] int64, logp [N,k], lse [N]): the k most likely tokens of each row, the likeliest
+    first, the lowest index first among equals.  Slots past the tokens above -inf: -1 and -inf."""
+    n = logits.shape[0]
+    ids = torch.empty(n, k, dtype=torch.int64, device=logits.device)
+    logp = torch.empty(n, k, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+    rlk_topk_logp(logits, active_mask, temperature, ids, logp, lse, error_word)
+    return ids, logp, lse
+
+
+def linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask=None,
+                       temperature=1.0, renormalize=False, error_word=None):
+    """(kl [N], lse [N], logp [N,K]) fp32: KL of the teacher's top tokens against the head, and
+    the head's log-probs of them."""
+    n, h = hidden.shape
+    v, k = weight.shape[0], teacher_ids.shape[1]
+    kl, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
+    logp = torch.empty(n, k, dtype=torch.float32, device=hidden.device)
+    ws = _workspace(rlk_linear_topk_kl_fwd_workspace_bytes(n, h, v, k), hidden.device)
+    rlk_linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask, temperature,
+                           renormalize, kl, lse, logp, ws, error_word)
+    return kl, lse, logp
+
+
+def linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse, logp,
+                       temperature=1.0, renormalize=False, error_word=None):
+    """(dhidden[N,H], dweight[V,H]) bf16."""
+    n, h = hidden.shape
+    v, k = weight.shape[0], teacher_ids.shape[1]
+    dh = torch.empty_like(hidden)
+    dw = torch.empty_like(weight)
+    ws = _workspace(rlk_linear_topk_kl_bwd_workspace_bytes(n, h, v, k), hidden.device)
+    rlk_linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse,
+                           logp, temperature, renormalize, dh, dw, ws, error_word)
+    return dh, dw
+
+
 class LinearLogp(torch.autograd.Function):
     """logp = LinearLogp.apply(hidden, weight, targets, active_mask, temperature)."""
 
@@ -1102,6 +1322,36 @@ def linear_kl(hidden, weight, hidden_ref, weight_ref, active_mask=None, temperat
     temperature_ref = temperature if temperature_ref is None else temperature_ref
     return LinearKl.apply(hidden, weight, hidden_ref.detach(), weight_ref.detach(), active_mask,
                           temperature, temperature_ref)
+
+
+class LinearTopkKl(torch.autograd.Function):
+    """kl = LinearTopkKl.apply(hidden, weight, teacher_ids, teacher_logp, active_mask, T,
+    renormalize); gradients flow to the student's head (hidden, weight) only."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, teacher_ids, teacher_logp, active_mask, temperature,
+                renormalize):
+        kl, lse, logp = linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask,
+                                           temperature, renormalize)
+        ctx.save_for_backward(hidden, weight, teacher_ids, teacher_logp, active_mask, lse, logp)
+        ctx.settings = (temperature, renormalize)
+        return kl
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_kl):
+        hidden, weight, teacher_ids, teacher_logp, active_mask, lse, logp = ctx.saved_tensors
+        dh, dw = linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask,
+                                    grad_kl.float().contiguous(), lse, logp, *ctx.settings)
+        return dh, dw, None, None, None, None, None
+
+
+def linear_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask=None, temperature=1.0,
+                   renormalize=False):
+    """Differentiable KL [N] of a teacher's top tokens (topk_logp's ids and logp) against the
+    student's head (once: a second derivative is an error)."""
+    return LinearTopkKl.apply(hidden, weight, teacher_ids, teacher_logp.detach(), active_mask,
+                              temperature, renormalize)
 
 
 def _as_rows(t, like=None):

@@ -902,6 +902,245 @@ rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int
     return RLK_OK;
 }
 
+rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                                int64_t row_stride, const uint8_t* active_mask,
+                                const rlk_process_params_t* params, void* out,
+                                int64_t out_stride, uint32_t* device_error_word,
+                                cudaStream_t stream) {
+    if (dtype != RLK_DTYPE_F32 && dtype != RLK_DTYPE_BF16) return RLK_ERR_UNSUPPORTED;
+    if (N < 0 || N > kMaxDim || V < 1 || row_stride < V || out_stride < V || params == nullptr)
+        return RLK_ERR_INVALID_VALUE;
+    if (V > (int64_t(1) << 22)) return RLK_ERR_UNSUPPORTED;
+    const rlk_process_params_t& p = *params;
+    // as the kernel holds them
+    const float rep = static_cast<float>(p.repetition), freq = static_cast<float>(p.frequency),
+                pres = static_cast<float>(p.presence);
+    if (p.repetition_rows == nullptr && !(rep > 0.f && std::isfinite(rep)))
+        return RLK_ERR_INVALID_VALUE;
+    if (p.frequency_rows == nullptr && !std::isfinite(freq)) return RLK_ERR_INVALID_VALUE;
+    if (p.presence_rows == nullptr && !std::isfinite(pres)) return RLK_ERR_INVALID_VALUE;
+    const bool history = p.tokens != nullptr;
+    if (history && (p.tokens_width < 0 || p.tokens_stride < p.tokens_width))
+        return RLK_ERR_INVALID_VALUE;
+    if (!history && (p.lengths != nullptr || p.prompt_lengths != nullptr))
+        return RLK_ERR_INVALID_VALUE;
+    if (history && p.tokens_width > (int64_t(1) << 29)) return RLK_ERR_UNSUPPORTED;
+    if (p.bias_count < 0) return RLK_ERR_INVALID_VALUE;
+    if (p.bias_count > rlk::kMaxBias) return RLK_ERR_UNSUPPORTED;
+    if (p.bias_count > 0 && (p.bias_ids == nullptr || p.bias_values == nullptr))
+        return RLK_ERR_INVALID_VALUE;
+    if (p.allowed != nullptr && p.allowed_stride < (V + 31) / 32) return RLK_ERR_INVALID_VALUE;
+    if (N == 0) return RLK_OK;
+    if (logits == nullptr || out == nullptr) return RLK_ERR_INVALID_VALUE;
+    if (logits == out && row_stride != out_stride) return RLK_ERR_INVALID_VALUE;
+    const size_t es = dtype == RLK_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, es) || !aligned(out, es) || !aligned(p.tokens, 8) ||
+        !aligned(p.lengths, 8) || !aligned(p.prompt_lengths, 8) ||
+        !aligned(p.repetition_rows, 4) || !aligned(p.frequency_rows, 4) ||
+        !aligned(p.presence_rows, 4) || !aligned(p.bias_ids, 8) || !aligned(p.bias_values, 4) ||
+        !aligned(p.allowed, 4) || !aligned(device_error_word, 4))
+        return RLK_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    rlk::ProcessArgs a{};
+    a.x = logits, a.out = out, a.x_stride = row_stride, a.out_stride = out_stride;
+    a.mask = active_mask;
+    a.tokens = p.tokens, a.lengths = p.lengths, a.prompt_lengths = p.prompt_lengths;
+    a.tokens_stride = p.tokens_stride;
+    a.repetition_rows = p.repetition_rows, a.frequency_rows = p.frequency_rows;
+    a.presence_rows = p.presence_rows;
+    a.repetition = rep, a.frequency = freq, a.presence = pres;
+    a.bias_ids = p.bias_ids, a.bias_values = p.bias_values;
+    a.allowed = p.allowed, a.allowed_stride = p.allowed_stride;
+    a.N = static_cast<int>(N), a.V = static_cast<int>(V);
+    a.width = history ? static_cast<int>(p.tokens_width) : 0;
+    a.bias = static_cast<int>(p.bias_count);
+    a.x_vec = rows_vec(logits, row_stride, es), a.out_vec = rows_vec(out, out_stride, es);
+    a.err = device_error_word;
+    RLK_CUDA(rlk::launch_process(a, dtype == RLK_DTYPE_BF16, stream));
+    return RLK_OK;
+}
+
+rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t V,
+                           int64_t row_stride, const uint8_t* active_mask, int64_t K,
+                           double temperature, int64_t* ids_out, float* logp_out, float* lse_out,
+                           uint32_t* device_error_word, cudaStream_t stream) {
+    if (dtype != RLK_DTYPE_F32 && dtype != RLK_DTYPE_BF16) return RLK_ERR_UNSUPPORTED;
+    if (N < 0 || N > kMaxDim || V < 1 || row_stride < V || K < 1) return RLK_ERR_INVALID_VALUE;
+    const float k = static_cast<float>(1.4426950408889634074 / temperature);
+    if (!(k > 0.f && std::isfinite(k))) return RLK_ERR_INVALID_VALUE;
+    if (V > rlk::kMaxTopkColumns || K > rlk::kMaxTopK) return RLK_ERR_UNSUPPORTED;
+    if (N == 0) return RLK_OK;
+    if (logits == nullptr || ids_out == nullptr || logp_out == nullptr)
+        return RLK_ERR_INVALID_VALUE;
+    const size_t es = dtype == RLK_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, es) || !aligned(ids_out, 8) || !aligned(logp_out, 4) ||
+        !aligned(lse_out, 4) || !aligned(device_error_word, 4))
+        return RLK_ERR_INVALID_VALUE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    rlk::TopkArgs a{};
+    a.stride = row_stride, a.mask = active_mask;
+    a.N = static_cast<int>(N), a.V = static_cast<int>(V), a.K = static_cast<int>(K);
+    a.k = k, a.inv_t = static_cast<float>(1.0 / temperature);
+    a.vec_ok = rows_vec(logits, row_stride, es);
+    a.ids = ids_out, a.logp = logp_out, a.lse = lse_out, a.err = device_error_word;
+    RLK_CUDA(rlk::launch_topk(logits, dtype == RLK_DTYPE_BF16, a, stream));
+    return RLK_OK;
+}
+
+size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K) {
+    if (N < 0 || H < 0 || V < 1 || K < 1) return 0;
+    return rlk::TopkKlFwdLayout(N, H, V, K).total;
+}
+
+size_t rlk_linear_topk_kl_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K) {
+    if (N < 0 || H < 0 || V < 1 || K < 1) return 0;
+    return rlk::TopkKlBwdLayout(N, H, K).total;
+}
+
+rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
+                                    const int64_t* teacher_ids, const float* teacher_logp,
+                                    const uint8_t* active_mask, int64_t N, int64_t H, int64_t V,
+                                    int64_t K, double temperature, int32_t renormalize,
+                                    float* kl_out, float* lse_out, float* logp_out,
+                                    void* workspace, size_t workspace_bytes,
+                                    uint32_t* device_error_word, cudaStream_t stream) {
+    RLK_TRY(check_shape(N, H, V, temperature));
+    if (K < 1) return RLK_ERR_INVALID_VALUE;
+    if (K > rlk::kMaxTopK) return RLK_ERR_UNSUPPORTED;
+    if (N == 0) return RLK_OK;
+    if (hidden == nullptr || weight == nullptr || teacher_ids == nullptr ||
+        teacher_logp == nullptr || kl_out == nullptr || lse_out == nullptr || logp_out == nullptr)
+        return RLK_ERR_INVALID_VALUE;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(teacher_ids, 8) ||
+        !aligned(teacher_logp, 4) || !aligned(kl_out, 4) || !aligned(lse_out, 4) ||
+        !aligned(logp_out, 4) || !aligned(device_error_word, 4))
+        return RLK_ERR_INVALID_VALUE;
+    const rlk::TopkKlFwdLayout lay(N, H, V, K);
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < lay.total)
+        return RLK_ERR_WORKSPACE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int n = static_cast<int>(N), h = static_cast<int>(H), v = static_cast<int>(V);
+    int* rows = nullptr;
+    int* pos_of = nullptr;
+    int* n_rows = nullptr;
+    const void* gemm_rows = hidden;
+    if (active_mask != nullptr) {
+        rows = reinterpret_cast<int*>(ws + lay.rows_off);
+        pos_of = reinterpret_cast<int*>(ws + lay.pos_off);
+        n_rows = reinterpret_cast<int*>(ws + lay.count_off);
+        RLK_CUDA(rlk::launch_compact(active_mask, n, h, hidden, ws + lay.hc_off,
+                                     reinterpret_cast<int*>(ws + lay.blk_off), rows, pos_of,
+                                     n_rows, stream));
+        gemm_rows = ws + lay.hc_off;
+    }
+    CUtensorMap map_h, map_w;
+    RLK_TRY(make_map(&map_h, gemm_rows, H, N, H * 2, 64, rlk::kTileM));
+    RLK_TRY(make_map(&map_w, weight, H, V, H * 2, 64, rlk::kPairBRows));
+    const float k = rlk::topk_kl_scale(temperature, H);
+    float2* partials = reinterpret_cast<float2*>(ws + lay.partial_off);
+    const rlk::TopkSlots slots{teacher_ids, teacher_logp, active_mask, n, static_cast<int>(K), v,
+                               renormalize != 0};
+    int2* list = reinterpret_cast<int2*>(ws + lay.list_off);
+    uint16_t* first = reinterpret_cast<uint16_t*>(ws + lay.first_off);
+    RLK_CUDA(rlk::launch_topk_list(slots, rows, n_rows, static_cast<int>(lay.num_chunks), list,
+                                   first, stream));
+    RLK_CUDA(rlk::launch_list_partials(map_h, map_w, n, h, v, static_cast<int>(K), k, partials,
+                                       list, first, logp_out, rows, n_rows, device_error_word,
+                                       dev.sms, stream));
+    RLK_CUDA(rlk::launch_topk_merge(slots, partials, static_cast<int>(lay.num_chunks), pos_of, k,
+                                    kl_out, lse_out, logp_out, device_error_word, stream));
+    return RLK_OK;
+}
+
+rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
+                                    const int64_t* teacher_ids, const float* teacher_logp,
+                                    const uint8_t* active_mask, const float* grad_kl,
+                                    const float* lse, const float* logp, int64_t N, int64_t H,
+                                    int64_t V, int64_t K, double temperature, int32_t renormalize,
+                                    void* dhidden, void* dweight, void* workspace,
+                                    size_t workspace_bytes, uint32_t* device_error_word,
+                                    cudaStream_t stream) {
+    RLK_TRY(check_shape(N, H, V, temperature));
+    if (K < 1) return RLK_ERR_INVALID_VALUE;
+    if (K > rlk::kMaxTopK) return RLK_ERR_UNSUPPORTED;
+    if (N == 0) return RLK_OK;
+    if (hidden == nullptr || weight == nullptr || teacher_ids == nullptr ||
+        teacher_logp == nullptr || grad_kl == nullptr || lse == nullptr || logp == nullptr ||
+        dhidden == nullptr || dweight == nullptr)
+        return RLK_ERR_INVALID_VALUE;
+    if (!aligned(hidden, 16) || !aligned(weight, 16) || !aligned(dhidden, 16) ||
+        !aligned(dweight, 16) || !aligned(teacher_ids, 8) || !aligned(teacher_logp, 4) ||
+        !aligned(grad_kl, 4) || !aligned(lse, 4) || !aligned(logp, 4) ||
+        !aligned(device_error_word, 4))
+        return RLK_ERR_INVALID_VALUE;
+    const rlk::TopkKlBwdLayout lay(N, H, K);
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < lay.total)
+        return RLK_ERR_WORKSPACE;
+    DeviceInfo dev;
+    RLK_TRY(current_device(dev));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int n = static_cast<int>(N), h = static_cast<int>(H), v = static_cast<int>(V);
+    rlk::BwdStep st{};
+    const void* gemm_rows = hidden;
+    if (active_mask != nullptr) {
+        int* rows = reinterpret_cast<int*>(ws + lay.rows_off);
+        int* n_rows = reinterpret_cast<int*>(ws + lay.count_off);
+        RLK_CUDA(rlk::launch_compact(active_mask, n, h, hidden, ws + lay.hc_off,
+                                     reinterpret_cast<int*>(ws + lay.blk_off), rows,
+                                     reinterpret_cast<int*>(ws + lay.pos_off), n_rows, stream));
+        RLK_CUDA(rlk::launch_zero_inactive_rows(active_mask, n, static_cast<size_t>(H) * 2,
+                                                dhidden, stream));
+        st.rows = rows;
+        st.n_rows = n_rows;
+        gemm_rows = ws + lay.hc_off;
+    }
+    rlk::BwdStepMaps maps;
+    RLK_TRY(make_map(&maps.h_kmajor, gemm_rows, H, N, H * 2, 64, rlk::kTileM));
+    RLK_TRY(make_map(&maps.w_kmajor_pair, weight, H, V, H * 2, 64, rlk::kPairBRows));
+    RLK_TRY(make_map(&maps.w_mnmajor, weight, H, V, H * 2, 64, 64));
+    RLK_TRY(make_map(&maps.h_mnmajor, gemm_rows, H, N, H * 2, 64, 64));
+    st.mask = active_mask;
+    st.grad = grad_kl;
+    st.lse = lse;
+    st.hidden = hidden;
+    st.weight = weight;
+    st.N = n;
+    st.H = h;
+    st.V = v;
+    st.num_chunks = static_cast<int>((V + rlk::kBwdChunk - 1) / rlk::kBwdChunk);
+    st.k = rlk::topk_kl_scale(temperature, H);
+    st.temp = static_cast<float>(temperature);
+    st.V_global = v;
+    st.round_last = true;
+    st.hilo = true;
+    st.topk = true;
+    st.K = static_cast<int>(K);
+    int* ids = reinterpret_cast<int*>(ws + lay.ids_off);
+    float* val = reinterpret_cast<float*>(ws + lay.val_off);
+    st.topk_ids = ids;
+    st.topk_val = val;
+    st.dh_acc = reinterpret_cast<float*>(ws + lay.dhacc_off);
+    st.ycoef = reinterpret_cast<float*>(ws + lay.ycoef_off);
+    st.dom = reinterpret_cast<int*>(ws + lay.dom_off);
+    st.dom_flags = reinterpret_cast<int*>(ws + lay.flags_off);
+    st.dcoef = reinterpret_cast<float*>(ws + lay.dcoef_off);
+    st.dhidden = dhidden;
+    st.dweight = dweight;
+    const rlk::TopkSlots slots{teacher_ids, teacher_logp, active_mask, n, static_cast<int>(K), v,
+                               renormalize != 0};
+    RLK_CUDA(rlk::launch_topk_coef(slots, grad_kl, logp, st.rows, st.n_rows, st.temp, st.ycoef,
+                                   ids, val, device_error_word, stream));
+    // no entry is split off as a row's dominant class (all bits set: -1)
+    RLK_CUDA(cudaMemsetAsync(st.dom, 0xff, static_cast<size_t>(N) * sizeof(int), stream));
+    RLK_CUDA(cudaMemsetAsync(st.dom_flags, 0, static_cast<size_t>(st.num_chunks) * sizeof(int),
+                             stream));
+    return bwd_chunks(maps, st, ws + lay.ds_off, N, V, dev.sms, device_error_word, stream);
+}
+
 #define RLK_STR2(x) #x
 #define RLK_STR(x) RLK_STR2(x)
 

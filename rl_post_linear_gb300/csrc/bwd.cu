@@ -521,6 +521,90 @@ struct DsKlPolicy {
     __device__ void epi_end(int, int, int, EpiState&) const {}
 };
 
+// ----------------------------------------------------------------------------- dS_c for top-K KL
+//
+// dS[t,v] = (g_t / T) (Q_t p[t,v] - q[t,v]): this GEMM writes the first term, with
+// coef_t = g_t Q_t / T from the launch before it, as hi and lo bf16 planes.  The entries
+// at the teacher's tokens, at most K a row, are then overwritten (launch_topk_scatter):
+// near a student that agrees with its teacher they are differences of near numbers, so
+// they are formed whole in fp32 and rounded once.
+struct DsTopkPolicy : SingleRole<false, false> {
+    static constexpr bool kCtaPair = true;
+    static constexpr int kLd = 2 * kBwdChunk;
+
+    const float* lse;         // [N] by token
+    const float* coef;        // [N] by GEMM row
+    __nv_bfloat16* ds;
+    RowMap rm;
+    int N, V, c0, num_m, num_n, kblocks;
+    float k;
+
+    __device__ int num_units() const { return rm.tiles(N) * num_n; }
+    __device__ int k_blocks(int) const { return kblocks; }
+    __device__ int tiles_in_unit(int) const { return 1; }
+    __device__ void unit(int u, int& m, int& n) const {
+        grouped_unit(u, rm.tiles(N), num_n, kRasterTokenRows / kUnitM, m, n);
+    }
+    __device__ void coords(int u, int, int& a_mn, int& a_k, int& b_mn, int& b_k) const {
+        int m, n;
+        unit(u, m, n);
+        a_mn = m * kUnitM;
+        a_k = 0;
+        b_mn = c0 + n * kTileV;
+        b_k = 0;
+    }
+
+    struct EpiState {
+        float coef, lse2;
+        bool live;
+    };
+
+    __device__ void epi_begin(int u, int row, EpiState& st) const {
+        int m, n;
+        unit(u, m, n);
+        const int i = m * kUnitM + row;
+        st.coef = i < rm.count(N) ? coef[i] : 0.f;
+        st.live = st.coef != 0.f;        // rows without weight stay 0, whatever their logits
+        st.lse2 = st.live ? lse[rm.token(i)] * kLog2e : 0.f;
+    }
+
+    __device__ void epi_tile(int u, int, int row, uint32_t taddr, EpiState& st) const {
+        int m, n;
+        unit(u, m, n);
+        const int i = m * kUnitM + row;
+#pragma unroll 1
+        for (int cc = 0; cc < kTileV / 32; ++cc) {
+            uint32_t r[32];
+            tmem_load_32(taddr + cc * 32, r);
+            if (i >= N) continue;
+            const int col = n * kTileV + cc * 32;   // column inside the chunk
+            const int vb = c0 + col;
+            uint32_t packed[16], packed_lo[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float d0 = st.coef * ex2_approx(fmaf(__uint_as_float(r[2 * j]), k, -st.lse2));
+                float d1 = st.coef * ex2_approx(fmaf(__uint_as_float(r[2 * j + 1]), k, -st.lse2));
+                if (!st.live || vb + 2 * j >= V) d0 = 0.f;
+                if (!st.live || vb + 2 * j + 1 >= V) d1 = 0.f;
+                packed[j] = pack_bf16x2(d0, d1);
+                packed_lo[j] = pack_lo_bf16x2(d0, d1, packed[j]);
+            }
+            uint4* hi = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + col);
+            uint4* lo = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + kBwdChunk +
+                                                 col);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                hi[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
+                                   packed[4 * w + 3]);
+                lo[w] = make_uint4(packed_lo[4 * w], packed_lo[4 * w + 1], packed_lo[4 * w + 2],
+                                   packed_lo[4 * w + 3]);
+            }
+        }
+    }
+
+    __device__ void epi_end(int, int, EpiState&) const {}
+};
+
 // ----------------------------------------------------------------------------- dh
 
 // dS_c [N, width]: K (vocab) contiguous; W_c [width, H]: N (hidden) contiguous.
@@ -1049,6 +1133,25 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         return launch_dom_sort(st.dom, N, V, c0, c0 + width, st.dom_flags + st.chunk, st.tiles,
                                st.sorted_dy, st.sorted_dt, stream);
     }
+    if (st.role == kRoleDs && st.topk) {
+        DsTopkPolicy ps;
+        ps.lse = st.lse;
+        ps.coef = st.ycoef;
+        ps.ds = static_cast<__nv_bfloat16*>(st.ds);
+        ps.rm = RowMap{st.rows, st.n_rows};
+        ps.N = N;
+        ps.V = V;
+        ps.c0 = c0;
+        ps.num_m = (N + kUnitM - 1) / kUnitM;
+        ps.num_n = (width + kTileV - 1) / kTileV;
+        ps.kblocks = H / 64;
+        ps.k = st.k;
+        const cudaError_t e = launch_gemm(maps.h_kmajor, maps.w_kmajor_pair, ps,
+                                          ps.num_m * ps.num_n, num_sms, err, stream);
+        if (e != cudaSuccess) return e;
+        return launch_topk_scatter(st.topk_ids, st.topk_val, st.n_rows, N, st.K, c0, width, st.ds,
+                                   stream);
+    }
     if (st.role == kRoleDs) {
         const cudaError_t e =
             st.grad_ent != nullptr ? launch_ds<true>(maps, st, c0, width, num_sms, err, stream)
@@ -1084,7 +1187,7 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pd.first = st.chunk == 0;
         pd.last = st.chunk == st.num_chunks - 1;
         pd.temp = st.temp;
-        pd.terms = !st.kl;
+        pd.terms = !st.kl && !st.topk;
         pd.hilo = st.hilo;
         // the dW GEMM that follows overlaps this one's last wave (with 6.7 waves of dh
         // units at N = 8192, a quarter of the CTA pairs would otherwise idle for a unit)
@@ -1112,7 +1215,7 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
     pw.num_n = (H + kTileV - 1) / kTileV;
     pw.kblocks = (N + 63) / 64;
     pw.temp = st.temp;
-    pw.terms = !st.kl;
+    pw.terms = !st.kl && !st.topk;
     pw.hilo = st.hilo;
     // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
     // writes only dW, which the dh GEMM does not touch

@@ -44,8 +44,10 @@ namespace rlk {
 constexpr float kMaskedLogit = -3.0e38f;
 
 // ENT adds the running sum a = sum_j 2^((S_j - m) k) S_j per row, from which
-// the merge forms E[S] = a / s and the entropy lse - E[S]/T.
-template <bool ENT>
+// the merge forms E[S] = a / s and the entropy lse - E[S]/T.  LIST takes, instead of a
+// target logit, the logits of the columns that the row lists in ascending order, from the
+// same accumulator; nothing else of the row's arithmetic differs.
+template <bool ENT, bool LIST = false>
 struct FwdPolicyT : SingleRole<false, false> {   // h [N,H] and W [V,H]: K-major
     static constexpr bool kCtaPair = true;       // 256-token tiles on a CTA pair
 
@@ -59,6 +61,11 @@ struct FwdPolicyT : SingleRole<false, false> {   // h [N,H] and W [V,H]: K-major
     int64_t vocab_start;  // global id of this weight block's first row
     int N, V, num_m, num_vt, num_chunks, kblocks;   // V: rows of this weight block
     float k;              // log2(e) / T
+    // LIST only
+    const int2* list;     // [N][K] by GEMM row: (column, place in out), columns ascending
+    const uint16_t* first;   // [N][num_chunks]: the list's first entry in or behind a chunk
+    float* out;           // [N][K] by token
+    int K;
 
     __device__ int valid_rows() const { return n_rows != nullptr ? *n_rows : N; }
     __device__ int token_tiles() const {
@@ -89,19 +96,39 @@ struct FwdPolicyT : SingleRole<false, false> {   // h [N,H] and W [V,H]: K-major
         float m, s, a, sy;
         int64_t y;
         bool found;
+        // LIST: the entry that comes next and the one after it (fetched ahead), past the
+        // last one {kNoColumn, -}
+        int2 next, ahead;
+        const int2* from;        // where `ahead` came from
+        const int2* end;
+        float* out;
     };
+    static constexpr int kNoColumn = 0x7fffffff;
 
     __device__ void epi_begin(int u, int row, EpiState& st) const {
         int m, c;
         unit(u, m, c);
         const int i = m * kUnitM + row;
+        if constexpr (LIST) {
+            st.next = st.ahead = make_int2(kNoColumn, 0);
+            st.from = st.end = nullptr;
+            if (i < valid_rows()) {
+                const int2* mine = list + static_cast<size_t>(i) * K;
+                st.out = out + static_cast<size_t>(rows != nullptr ? rows[i] : i) * K;
+                st.end = mine + K;
+                const int2* at = mine + first[static_cast<size_t>(i) * num_chunks + c];
+                if (at < st.end) st.next = *at;
+                st.from = at + 1;
+                if (st.from < st.end) st.ahead = *st.from;
+            }
+        }
         st.m = -INFINITY;
         st.s = 0.f;
         st.a = 0.f;
         st.sy = 0.f;
         st.found = false;
         st.y = -1;
-        if (i < valid_rows()) {
+        if (!LIST && i < valid_rows()) {
             const int t = rows != nullptr ? rows[i] : i;
             if (mask == nullptr || mask[t] != 0) st.y = targets[t];
         }
@@ -126,10 +153,22 @@ struct FwdPolicyT : SingleRole<false, false> {   // h [N,H] and W [V,H]: K-major
                 for (int j = 0; j < 32; ++j)
                     if (j >= nv) x[j] = kMaskedLogit;
             }
-            const int64_t dy = st.y - vocab_start - vb;
-            if (dy >= 0 && dy < 32) {
-                st.sy = select32(x, static_cast<int>(dy));
-                st.found = true;
+            if constexpr (LIST) {
+                while (st.next.x < vb + 32) {
+                    st.out[st.next.y] = select32(x, st.next.x - vb);
+                    st.next = st.ahead;
+                    ++st.from;
+                    if (st.from < st.end)
+                        st.ahead = *st.from;
+                    else
+                        st.ahead.x = kNoColumn;
+                }
+            } else {
+                const int64_t dy = st.y - vocab_start - vb;
+                if (dy >= 0 && dy < 32) {
+                    st.sy = select32(x, static_cast<int>(dy));
+                    st.found = true;
+                }
             }
             const float cm = max32(x);
             const float nm = fmaxf(st.m, cm);
@@ -240,7 +279,7 @@ static cudaError_t launch_partials_t(const CUtensorMap& map_h, const CUtensorMap
                                      float* partials_a, float* s_target, const int* rows,
                                      const int* n_rows, uint32_t* err, int num_sms,
                                      cudaStream_t stream) {
-    FwdPolicyT<ENT> p;
+    FwdPolicyT<ENT> p{};
     p.targets = targets;
     p.mask = mask;
     p.partials = partials;
@@ -267,6 +306,30 @@ cudaError_t launch_fwd_partials(const CUtensorMap& map_h, const CUtensorMap& map
     return launch_partials_t<false>(map_h, map_w, targets, mask, N, H, V_local, vocab_start, k,
                                     partials, nullptr, s_target, nullptr, nullptr, err, num_sms,
                                     stream);
+}
+
+cudaError_t launch_list_partials(const CUtensorMap& map_h, const CUtensorMap& map_w, int N, int H,
+                                 int V, int K, float k, float2* partials, const int2* list,
+                                 const uint16_t* first, float* out, const int* rows,
+                                 const int* n_rows, uint32_t* err, int num_sms,
+                                 cudaStream_t stream) {
+    FwdPolicyT<false, true> p{};
+    p.partials = partials;
+    p.rows = rows;
+    p.n_rows = n_rows;
+    p.N = N;
+    p.V = V;
+    p.num_m = (N + kUnitM - 1) / kUnitM;
+    p.num_vt = (V + kTileV - 1) / kTileV;
+    p.num_chunks = (p.num_vt + kFwdTilesPerChunk - 1) / kFwdTilesPerChunk;
+    p.kblocks = H / 64;
+    p.k = k;
+    p.list = list;
+    p.first = first;
+    p.out = out;
+    p.K = K;
+    const long long units = static_cast<long long>(p.num_m) * p.num_chunks;
+    return launch_persistent(TwoMaps{map_h, map_w}, p, units, num_sms, err, stream);
 }
 
 cudaError_t launch_fwd_merge(const float2* partials, int num_chunks, const float* s_target,

@@ -96,6 +96,16 @@ struct BwdLayout {
     }
 };
 
+// The same with the entries of dS at the teacher's K tokens of each row behind it.
+struct TopkKlBwdLayout : BwdLayout {
+    size_t ids_off, val_off;
+    TopkKlBwdLayout(int64_t N, int64_t H, int64_t K) : BwdLayout(N, H, true) {
+        ids_off = total;
+        val_off = align_up(ids_off + static_cast<size_t>(N) * K * 4, 256);
+        total = align_up(val_off + static_cast<size_t>(N) * K * 4, 256);
+    }
+};
+
 // A sum carried as an unevaluated pair of floats (hi + lo, about 48 significant
 // bits), added with Knuth's two-sum: the audit's cross-block accumulation.  The
 // fp64 units of this GPU are few and slow; pairs of fp32 operations are not.
@@ -227,7 +237,12 @@ struct BwdStep {
     const float* grad_rev;     // d loss / d KL(q || p), or nullptr
     const float* lse_ref;
     const float* kl_val;       // the forward's KL(p || q)
-    bool hilo;                 // dS as hi and lo bf16 planes [N, 2 kBwdChunk] (entropy, KL)
+    bool hilo;                 // dS as hi and lo bf16 planes [N, 2 kBwdChunk] (entropy, KL, top-K)
+    // KL against a teacher's top tokens (topk = true): ycoef holds g Q / T by GEMM row
+    bool topk;
+    int K;
+    const int* topk_ids;       // [N][K] by GEMM row: distinct token ids, -1: no entry
+    const float* topk_val;     // [N][K] their whole entries of dS
     void* ds;                  // dS [N, kBwdChunk] bf16 of the chunk (hilo: [N, 2 kBwdChunk])
     float* dh_acc;
     const int* sorted_y;
@@ -353,6 +368,103 @@ struct SampleArgs {
 size_t sample_workspace(int64_t N, int64_t V);
 cudaError_t launch_sample(const void* logits, bool bf16, const SampleArgs& args,
                           cudaStream_t stream);
+
+// Top-K log-probs of logits.
+constexpr int kMaxTopK = 1024;
+constexpr int kMaxTopkColumns = 1 << 22;
+struct TopkArgs {
+    int64_t stride;
+    const uint8_t* mask;
+    int N, V, K;
+    float k, inv_t;            // log2(e) / T, 1 / T
+    bool vec_ok;               // rows start on 16 bytes
+    int64_t* ids;
+    float* logp;
+    float* lse;                // or nullptr
+    uint32_t* err;
+};
+cudaError_t launch_topk(const void* logits, bool bf16, const TopkArgs& args, cudaStream_t stream);
+
+// Penalties, biases and masks on logits.
+constexpr int kMaxBias = 4096;
+struct ProcessArgs {
+    const void* x;
+    void* out;
+    int64_t x_stride, out_stride;
+    const uint8_t* mask;
+    const int64_t* tokens;     // or nullptr
+    const int64_t* lengths;    // or nullptr: width
+    const int64_t* prompt_lengths;   // or nullptr: 0
+    int64_t tokens_stride;
+    const float* repetition_rows;    // *_rows: or nullptr, then the scalar
+    const float* frequency_rows;
+    const float* presence_rows;
+    float repetition, frequency, presence;
+    const int64_t* bias_ids;   // or nullptr
+    const float* bias_values;
+    const int32_t* allowed;    // or nullptr
+    int64_t allowed_stride;
+    int N, V, width, bias;
+    bool x_vec, out_vec;       // rows start on 16 bytes
+    uint32_t* err;
+};
+cudaError_t launch_process(const ProcessArgs& args, bool bf16, cudaStream_t stream);
+
+// KL of the head against a teacher's top tokens.
+struct TopkKlFwdLayout {
+    int64_t num_chunks;
+    size_t partial_off, rows_off, pos_off, blk_off, count_off, hc_off, list_off, first_off, total;
+    TopkKlFwdLayout(int64_t N, int64_t H, int64_t V, int64_t K) {
+        num_chunks = fwd_num_chunks(V);
+        partial_off = 0;
+        rows_off = align_up(static_cast<size_t>(num_chunks) * N * 8, 256);
+        pos_off = align_up(rows_off + static_cast<size_t>(N) * 4, 256);
+        blk_off = align_up(pos_off + static_cast<size_t>(N) * 4, 256);
+        count_off = align_up(blk_off + static_cast<size_t>((N + kCompactBlock - 1) / kCompactBlock) * 4, 256);
+        hc_off = align_up(count_off + 4, 256);
+        // the rows' tokens in ascending order, and where each vocabulary chunk's begin
+        list_off = align_up(hc_off + static_cast<size_t>(N) * H * 2, 256);
+        first_off = align_up(list_off + static_cast<size_t>(N) * K * 8, 256);
+        total = align_up(first_off + static_cast<size_t>(num_chunks) * N * 2, 256);
+    }
+};
+// What the tensor cores lose of a logit: each of the H/16 steps of the accumulation cuts the sum
+// off towards zero, a mean of 2^-25.8 of a logit that builds up evenly (a sum that grows to S loses
+// half an ulp of its present value a step, about 0.35 2^-24 S in the mean).  Measured over H = 1024
+// .. 7168: a share of 1.037e-9 H (logits of 12 at H = 7168: 9e-5 low; 1e-5 scatter about that).  The
+// kernels of the top-K KL scale it back with the temperature, which costs nothing: a weighted mean
+// of a few large logits is where it shows.
+constexpr double kAccumulatorLoss = 1.037e-9;
+inline float topk_kl_scale(double temperature, int64_t H) {
+    return static_cast<float>(1.4426950408889634074 / temperature *
+                              (1.0 + kAccumulatorLoss * static_cast<double>(H)));
+}
+struct TopkSlots {
+    const int64_t* ids;        // [N][K] by token
+    const float* teacher;      // [N][K] the teacher's log-weights
+    const uint8_t* mask;
+    int N, K, V;
+    bool renormalize;
+};
+// The log-prob's GEMM: the partials of lse, and s[t, column] of each row's list into out.
+cudaError_t launch_list_partials(const CUtensorMap& map_h, const CUtensorMap& map_w, int N, int H,
+                                 int V, int K, float k, float2* partials, const int2* list,
+                                 const uint16_t* first, float* out, const int* rows,
+                                 const int* n_rows, uint32_t* err, int num_sms,
+                                 cudaStream_t stream);
+// by GEMM row: the listed tokens (id, slot) in ascending order, and the chunks' first ones
+cudaError_t launch_topk_list(const TopkSlots& slots, const int* rows, const int* n_rows,
+                             int num_chunks, int2* list, uint16_t* first, cudaStream_t stream);
+// lse, then logp in place of the logits, and kl
+cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, int num_chunks,
+                              const int* pos_of, float k, float* kl, float* lse, float* logp,
+                              uint32_t* err, cudaStream_t stream);
+// by GEMM row: coef = g Q / T, and the entries of dS at the listed tokens
+cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const float* logp,
+                             const int* rows, const int* n_rows, float temp, float* coef,
+                             int* ids, float* val, uint32_t* err, cudaStream_t stream);
+cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,
+                                int c0, int width, void* ds, cudaStream_t stream);
 
 // Device address (current device and context) of the library-owned audit scratch.
 cudaError_t audit_noalloc_scratch(void** parts);

@@ -1,0 +1,263 @@
+"""Penalties, biases and masks on logits against the definition in float64, one row at a time.
+
+A listed column goes through at most a division, a multiply-add, a subtraction, the sum of its B
+biases and their addition, each rounded to fp32 (2^-24 of a value no larger than the sum of the
+magnitudes that enter), then once to the output's type (2^-8 for bf16).  All others keep their
+bits.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rl_post_linear_gb300 as rlk
+from helpers import dev, same_bits
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16]
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def logits(n, v, seed, dtype, pad=0):
+    x = 4.0 * torch.randn(n, v + pad, generator=gen(seed))
+    return x.to(dtype).to(dev())[:, :v]
+
+
+def pack(allow):
+    """int32 words [N, ceil(V / 32)] of a boolean [N, V]; bits past V are 0."""
+    n, v = allow.shape
+    b = np.zeros((n, (v + 31) // 32 * 32), np.uint8)
+    b[:, :v] = allow.cpu().numpy()
+    return torch.from_numpy(np.packbits(b, axis=1, bitorder="little").view(np.int32).copy()).to(dev())
+
+
+def at(value, i):
+    return float(value[i]) if isinstance(value, torch.Tensor) else float(np.float32(value))
+
+
+def check(x, tokens=None, lengths=None, prompt_lengths=None, repetition=1.0, frequency=0.0,
+          presence=0.0, bias_ids=None, bias_values=None, allowed=None, mask=None, out=None):
+    n, v = x.shape
+    before = x.clone()
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    y = rlk.process_logits(x, tokens, lengths, prompt_lengths, repetition, frequency, presence,
+                           bias_ids, bias_values, None if allowed is None else pack(allowed), mask,
+                           out, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and y.dtype == x.dtype
+    for i in range(n):
+        if mask is not None and int(mask[i]) == 0:
+            continue
+        z = before[i].float().cpu().double().numpy()
+        mag, ops = np.abs(z), np.zeros(v)
+        if tokens is not None:
+            row = tokens[i].cpu().numpy()
+            end = row.size if lengths is None else int(lengths[i])
+            first = 0 if prompt_lengths is None else int(prompt_lengths[i])
+            seen = np.unique(row[:end][row[:end] >= 0])
+            r, f, p = at(repetition, i), at(frequency, i), at(presence, i)
+            z[seen] = np.where(z[seen] > 0, z[seen] / r, z[seen] * r)
+            mag[seen] = np.abs(z[seen])
+            drawn, c = np.unique(row[first:end][row[first:end] >= 0], return_counts=True)
+            z[drawn] -= f * c + p
+            mag[drawn] += np.abs(f * c) + abs(p)
+            ops[seen] += 3
+        if bias_ids is not None:
+            ids, b = bias_ids[i].cpu().numpy(), bias_values[i].cpu().double().numpy()
+            ids, b = ids[ids >= 0], b[ids >= 0]
+            np.add.at(z, ids, b)
+            np.add.at(mag, ids, np.abs(b))
+            np.add.at(ops, ids, 2)
+        if allowed is not None:
+            z[~allowed[i].cpu().numpy()] = -np.inf
+        got = y[i].float().cpu().double().numpy()
+        plain = (ops == 0) & np.isfinite(z)
+        assert same_bits(y[i][torch.from_numpy(plain)], before[i][torch.from_numpy(plain)])
+        off = np.isinf(z)
+        assert np.array_equal(got[off], z[off])
+        on = (ops > 0) & ~off
+        tol = ops * 2.0 ** -24 * mag
+        if x.dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -8 * (np.abs(z) + tol)
+        assert np.all(np.abs(got - z)[on] <= tol[on])
+    return y
+
+
+def history(n, v, length, seed, holes=0.0):
+    g = gen(seed)
+    t = (v * torch.rand(n, length, generator=g) ** 3).long().clamp(max=v - 1)
+    t[torch.rand(n, length, generator=g) < holes] = -1
+    full = (torch.rand(n, generator=g) * (length + 1)).long().clamp(max=length)
+    full[0] = length
+    if n > 2:
+        full[1], full[2] = 0, min(1, length)
+    prompt = (full * torch.rand(n, generator=g)).long()
+    prompt[-1] = full[-1]
+    return t.to(dev()), full.to(dev()), prompt.to(dev())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("v", [1, 2, 7, 31, 32, 33, 255, 1000, 4097, 8191, 8192, 8193, 16400, 50021])
+def test_vocabulary_sizes(v, dtype):
+    n = 5
+    t, full, prompt = history(n, v, 97, v, 0.1)
+    g = gen(v + 1)
+    ids = torch.randint(-1, v, (n, 9), generator=g).to(dev())
+    vals = torch.randn(n, 9, generator=g).to(dev())
+    allow = (torch.rand(n, v, generator=g) < 0.6).to(dev())
+    x = logits(n, v, v + 2, dtype)
+    check(x, t, full, prompt, 1.3, 0.4, -0.7)
+    check(x, bias_ids=ids, bias_values=vals)
+    check(x, allowed=allow)
+    check(x, t, full, prompt, 0.8, -0.2, 0.5, ids, vals, allow)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", [0, 1, 3, 8])
+def test_strides_and_in_place(pad, dtype):
+    n, v = 4, 9001
+    t, full, prompt = history(n, v, 300, 3)
+    allow = (torch.rand(n, v, generator=gen(4)) < 0.5).to(dev())
+    x = logits(n, v, 5, dtype, pad)
+    want = check(x, t, full, prompt, 1.2, 0.1, 0.3, allowed=allow)
+    wide = torch.full((n, v + 5), 7.0, dtype=dtype, device=dev())
+    got = check(x, t, full, prompt, 1.2, 0.1, 0.3, allowed=allow, out=wide[:, 2:v + 2])
+    assert same_bits(got, want)
+    assert bool((wide[:, :2] == 7.0).all()) and bool((wide[:, v + 2:] == 7.0).all())
+    same = x.clone() if pad == 0 else x
+    assert same_bits(check(same, t, full, prompt, 1.2, 0.1, 0.3, allowed=allow, out=same), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_settings_of_each_row(dtype):
+    n, v = 40, 3001
+    t, full, prompt = history(n, v, 700, 6)
+    g = gen(7)
+
+    def pick(values):
+        return torch.tensor(values)[torch.randint(len(values), (n,), generator=g)].to(dev())
+
+    x = logits(n, v, 8, dtype)
+    r, f, p = pick([1.0, 1.1, 2.0, 0.5]), pick([0.0, 0.3, -0.4]), pick([0.0, 1.0, -0.5])
+    y = check(x, t, full, prompt, r, f, p)
+    # a row's result is its own, whatever the batch
+    for i in (0, 7, 39):
+        one = check(x[i:i + 1].clone(), t[i:i + 1], full[i:i + 1], prompt[i:i + 1],
+                    float(r[i]), float(f[i]), float(p[i]))
+        assert same_bits(one[0], y[i])
+
+
+def test_long_histories_and_repeats():
+    v = 12000
+    t = torch.zeros(3, 50000, dtype=torch.int64, device=dev())
+    t[1] = 8191
+    t[2] = torch.arange(50000, device=dev()) % v
+    check(logits(3, v, 9, torch.float32), t, None, None, 1.1, 0.01, 0.2)
+    check(logits(3, v, 10, torch.float32), t, None,
+          torch.tensor([50000, 0, 25000], device=dev()), 1.1, 0.01, 0.2)
+
+
+def test_many_biases_of_one_token():
+    n, v = 2, 5000
+    ids = torch.randint(0, 3, (n, 4096), generator=gen(11)).to(dev()) * 2000
+    vals = torch.randn(n, 4096, generator=gen(12)).to(dev())
+    x = logits(n, v, 13, torch.float32)
+    a = check(x, bias_ids=ids, bias_values=vals)
+    for _ in range(3):                                   # the sum's order is fixed
+        assert same_bits(rlk.process_logits(x, bias_ids=ids, bias_values=vals), a)
+
+
+def test_values_at_the_ends():
+    x = torch.tensor([[0.0, -0.0, np.inf, -np.inf, np.nan, 3.0e38, -3.0e38, 1.0]], device=dev())
+    t = torch.arange(8, device=dev())[None]
+    y = rlk.process_logits(x, t, repetition=2.0)[0].cpu().numpy()
+    assert y[0] == 0 and y[1] == 0 and y[2] == np.inf and y[3] == -np.inf and np.isnan(y[4])
+    assert y[5] == np.float32(1.5e38) and y[6] == -np.inf and y[7] == 0.5
+    none = torch.zeros(1, 1, dtype=torch.int32, device=dev())
+    assert bool((rlk.process_logits(x, allowed=none) == -np.inf).all())
+    lowest = torch.full((1, 8), torch.finfo(torch.float32).min, device=dev())
+    assert same_bits(rlk.process_logits(lowest, t, frequency=0.0), lowest)
+    ban = torch.full((1, 1), -np.inf, device=dev())
+    y = rlk.process_logits(lowest, bias_ids=t[:, 3:4].clone(), bias_values=ban)
+    assert y[0, 3] == -np.inf and bool((y[0, :3] > -np.inf).all())
+
+
+def test_inactive_rows_are_left_as_they_are():
+    n, v = 6, 2000
+    x = logits(n, v, 14, torch.float32).clone()
+    x[1], x[4] = np.nan, np.inf
+    mask = torch.tensor([1, 0, 1, 1, 0, 1], dtype=torch.uint8, device=dev())
+    t = torch.full((n, 3), 5, dtype=torch.int64, device=dev())
+    t[1] = 1 << 40                                        # never looked at
+    out = torch.full((n, v), 9.0, device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    rlk.process_logits(x, t, presence=1.0, active_mask=mask, out=out, error_word=err)
+    assert int(err.item()) == 0 and bool((out[1] == 9.0).all()) and bool((out[4] == 9.0).all())
+    assert out[0, 5] == x[0, 5] - 1.0 and bool((out[0, 6:] == x[0, 6:]).all())
+
+
+@pytest.mark.parametrize("kind", ["token", "bias", "length", "prompt", "negative", "repetition",
+                                  "frequency", "presence"])
+def test_rows_that_cannot_be(kind):
+    n, v = 3, 20000
+    x = logits(n, v, 15, torch.float32)
+    t = torch.full((n, 4), 3, dtype=torch.int64, device=dev())
+    full = torch.full((n,), 4, device=dev())
+    prompt = torch.full((n,), 2, device=dev())
+    ids, vals = t.clone(), torch.zeros(n, 4, device=dev())
+    r, f, p = (torch.full((n,), w, device=dev()) for w in (1.0, 0.0, 0.0))
+    flag = rlk.RLK_DEVERR_SAMPLE_PARAM
+    if kind == "token":
+        t[1, 3], flag = v, rlk.RLK_DEVERR_TARGET_RANGE
+    elif kind == "bias":
+        ids[1, 0], flag = 1 << 33, rlk.RLK_DEVERR_TARGET_RANGE
+    elif kind == "length":
+        full[1] = 5
+    elif kind == "prompt":
+        prompt[1] = 5
+    elif kind == "negative":
+        prompt[1] = -1
+    elif kind == "repetition":
+        r[1] = 0.0
+    elif kind == "frequency":
+        f[1] = np.nan
+    else:
+        p[1] = np.inf
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    y = rlk.process_logits(x, t, full, prompt, r, f, p, ids, vals, error_word=err)
+    assert int(err.item()) == flag
+    assert bool(torch.isnan(y[1]).all()) and same_bits(y[0], x[0]) and same_bits(y[2], x[2])
+
+
+def test_captured_with_the_draw():
+    n, v = 8, 30000
+    x = logits(n, v, 16, torch.float32)
+    t, full, prompt = history(n, v, 64, 17)
+    u = torch.rand(n, generator=gen(18)).to(dev())
+    y = torch.empty_like(x)
+    ws = torch.empty(max(256, rlk.rlk_sample_logits_workspace_bytes(n, v)), dtype=torch.uint8,
+                     device=dev())
+    tok = torch.empty(n, dtype=torch.int64, device=dev())
+
+    def step():
+        rlk.rlk_process_logits(x, t, full, prompt, 1.2, 0.1, 0.1, None, None, None, None, y)
+        rlk.rlk_sample_logits(y, u, None, 0.8, 0, 0.9, 0.0, tok, None, None, ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (19, 20):
+        x.copy_(logits(n, v, seed, torch.float32))
+        graph.replay()
+        got = tok.clone()
+        want = rlk.sample_logits(rlk.process_logits(x, t, full, prompt, 1.2, 0.1, 0.1), u, 0.8,
+                                 top_p=0.9)[0]
+        assert torch.equal(got, want)
