@@ -6,18 +6,21 @@
 //   lse = log sum_v exp(x_v / T);  order: x descending, lowest index first among equals
 //   ids, logp = the order's first K v, x_v / T - lse
 //
-// One pass over the row: a warp takes units of 1024 columns, of which each lane holds 32 (its
-// segment).  A unit leaves its maximum and an fp32 sum of 2^((x - max) k), k = log2(e)/T; each
-// segment leaves its maximum.  K segments reach the K-th largest of the segments' maxima, so
-// every element of the answer reaches it too, and lies in a segment that does.  One block of the
-// row's cluster takes such a bound from a histogram of the maxima, reads the few segments that
-// reach it again, and sorts what it finds there.  A row where more is found than the list holds
-// (ties in great number, a row sorted by token) is searched by its keys' digits instead.
+// One pass over the row, in units of four 16-byte loads a lane of a warp.  Units are dealt to a
+// number of streams that depends on V alone; of a stream each lane carries its maximum and an fp32
+// sum of 2^((x - max) k), k = log2(e)/T.  Each segment of a unit (a lane's columns, or those of a
+// few lanes) leaves the key of its maximum.  K segments reach the K-th largest of the segments'
+// maxima, so every element of the answer reaches it too, and lies in a segment that does.  One
+// block of the row's cluster takes such a bound from a histogram of the maxima, reads the few
+// segments that reach it again, and puts what it finds there in order by a second histogram.  A
+// row where more is found than the list holds (ties in great number, a row sorted by token) is
+// searched by its keys' digits instead.
 //
 // Order and ties go by whole numbers: keys in the order of the floats, over the column.  Sums
 // run in an order that depends on V alone, so a row's results do not depend on the batch.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "ptx.cuh"
@@ -29,12 +32,11 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnit = 1024;              // columns of a unit
+constexpr int kLoads = 4;                // 16-byte loads a lane of a unit
 constexpr int kBins = 2048;
-constexpr int kList = 2048;              // elements of the list, a power of two
+constexpr int kQueue = 2048;             // segments that are read again
 constexpr int kMaxSegments = 8192;
+constexpr int kMaxStreams = 128;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -49,11 +51,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// maximum over the warp, by an integer reduction of order-preserving bits
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    const int b = __float_as_int(v);
+    const int k = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+    return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -68,39 +70,118 @@ __device__ __forceinline__ P* peer(P* p, uint32_t rank) {
     return reinterpret_cast<P*>(a);
 }
 
-// How a row's units are divided into segments: `halves` of a lane's columns, or `lanes` of them
-// together.
-struct Segments {
-    int halves, lanes;
-    __host__ __device__ int per_unit() const { return 32 * halves / lanes; }
+template <typename T>
+struct Unit {
+    static constexpr int VEC = 16 / sizeof(T), WORDS = 4 * kLoads;
+    static constexpr int kColumns = 32 * kLoads * VEC;
+    uint32_t w[WORDS];                   // as they lie in memory
+
+    __device__ __forceinline__ static int column(int unit, int load, int lane) {
+        return unit * kColumns + (load * 32 + lane) * VEC;
+    }
+    // A lane's part of a unit into its place of a warp's ring in shared memory, on its way while
+    // others are worked on; -inf past the row's end.  Each lane copies just what it reads itself,
+    // so this needs no barrier.
+    __device__ __forceinline__ static void fetch(uint4* slot, const T* row, int V, int unit,
+                                                 int lane, bool vec) {
+        if (vec && (unit + 1) * kColumns <= V) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(slot + j * 32)),
+                             "l"(row + column(unit, j, lane))
+                             : "memory");
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < kLoads; ++j)
+                load_edge(row, V, column(unit, j, lane), reinterpret_cast<uint32_t*>(slot + j * 32));
+        }
+    }
+    __device__ __forceinline__ void read(const uint4* slot) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const uint4 v = slot[j * 32];
+            w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        }
+    }
+    __device__ __noinline__ static void load_edge(const T* row, int V, int c, uint32_t* to) {
+        alignas(16) T v[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = c + e < V ? row[c + e] : T(-INFINITY);
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = p[i];
+    }
+    // the largest of words [4 * first, 4 * (first + loads))
+    __device__ __forceinline__ float largest(int first, int loads) const {
+        if constexpr (sizeof(T) == 2) {
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w + 4 * first);
+            __nv_bfloat162 m = p[0];
+#pragma unroll
+            for (int i = 1; i < 4 * loads; ++i) m = __hmax2(m, p[i]);
+            return fmaxf(__low2float(m), __high2float(m));
+        } else {
+            float m = __uint_as_float(w[4 * first]);
+#pragma unroll
+            for (int i = 1; i < 4 * loads; ++i) m = fmaxf(m, __uint_as_float(w[4 * first + i]));
+            return m;
+        }
+    }
+    // sum of 2^((x - m) k), pairs of columns at a time
+    __device__ __forceinline__ float weight(float m, float k) const {
+        const float2 mm = make_float2(-m, -m), kk = make_float2(k, k);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < WORDS; i += sizeof(T) == 2 ? 1 : 2) {
+            float2 x;
+            if constexpr (sizeof(T) == 2)
+                x = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            else
+                x = make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+            x = __fmul2_rn(__fadd2_rn(x, mm), kk);
+            sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+        }
+        return sum.x + sum.y;
+    }
 };
 
 // VEC consecutive columns from c on, as floats; -inf past the row's end.
 template <typename T>
-__device__ __forceinline__ void load_piece(const T* row, int V, int c, bool vec,
-                                           float (&x)[16 / sizeof(T)]) {
-    constexpr int VEC = 16 / sizeof(T);
-    alignas(16) T v[VEC];
-    if (vec && c + VEC <= V) {
-        *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(row + c));
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = to_f32(v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = c + e < V ? to_f32(row[c + e]) : -INFINITY;
-    }
+__device__ __forceinline__ uint4 load_piece(const T* row, int V, int c, bool vec) {
+    if (vec && c + Unit<T>::VEC <= V) return __ldg(reinterpret_cast<const uint4*>(row + c));
+    uint32_t w[4];
+    Unit<T>::load_edge(row, V, c, w);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ float piece_value(const uint4& v, int e) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(&v);
+    if (sizeof(T) == 4) return __uint_as_float(p[e]);
+    return __uint_as_float((e & 1) ? (p[e / 2] & 0xffff0000u) : (p[e / 2] << 16));
 }
 
+// What a stream leaves: maximum, sum, the least of its segments' maxima (a lower bound of it) and
+// how many lanes' are above -inf.
+struct Stream {
+    float m, s, low;
+    uint32_t count;
+};
+
+// Behind it the list.  While the row is read the warps' rings take the place of both.
 struct Shared {
     uint32_t hist[kBins];
-    u64 list[kList];
-    float warp_f[kWarps];
-    uint32_t warp_n[kWarps];
+    uint16_t queue[kQueue];
+    uint32_t warp_n[32];
     uint32_t n, queued;
     uint32_t bin, below, through;        // of the histogram: the bin K falls on, counts to it
 };
 
+// Elements the list holds: about K are found where segments are many, and never more than
+// twice as many that a histogram would let through.
+__host__ __device__ constexpr int list_size(int K) { return K <= 256 ? 1024 : 2048; }
+
 // Exclusive prefix of n over the block, and the total.
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_prefix(uint32_t n, Shared& sh, uint32_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t inc = n;
@@ -115,7 +196,7 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t n, Shared& sh, uint32_
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += sh.warp_n[w];
         total += sh.warp_n[w];
     }
@@ -123,12 +204,14 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t n, Shared& sh, uint32_
 }
 
 // The first bin at which the running count, `base` before the first, reaches `want`.
+template <int THREADS>
 __device__ __forceinline__ void find_bin(Shared& sh, int bins, uint32_t base, uint32_t want) {
-    const int each = bins / kThreads;
+    const int each = max(1, bins / THREADS);
     uint32_t own = 0;
-    for (int b = 0; b < each; ++b) own += sh.hist[threadIdx.x * each + b];
+    if (threadIdx.x * each < bins)
+        for (int b = 0; b < each; ++b) own += sh.hist[threadIdx.x * each + b];
     uint32_t total;
-    uint32_t run = base + block_prefix(own, sh, total);
+    uint32_t run = base + block_prefix<THREADS>(own, sh, total);
     if (run < want && run + own >= want) {
         for (int b = 0; b < each; ++b) {
             const uint32_t n = sh.hist[threadIdx.x * each + b];
@@ -145,21 +228,23 @@ __device__ __forceinline__ void find_bin(Shared& sh, int bins, uint32_t base, ui
 }
 
 // A key that at least `want` segments reach, and not many more: the histogram's window closes
-// in on it.  All segments above -inf have one; `want` of them at least.
-__device__ __noinline__ uint32_t segment_bound(const float* segmax, int nseg, uint32_t lo,
+// in on it.  `want` segments at least are above -inf; the histogram is 0 on entry.
+template <int THREADS>
+__device__ __noinline__ uint32_t segment_bound(const uint32_t* segkey, int nseg, uint32_t lo,
                                                uint32_t hi, uint32_t want, Shared& sh) {
     const uint32_t slack = max(32u, want / 4);
     uint32_t base = 0;
     while (true) {
         const int shift = max(0, 21 - __clz((hi - lo) | 1u));      // (hi - lo) >> shift < 2048
-        for (int b = threadIdx.x; b < kBins; b += kThreads) sh.hist[b] = 0;
-        __syncthreads();
-        for (int s = threadIdx.x; s < nseg; s += kThreads) {
-            const uint32_t key = order_key(segmax[s]);
-            if (key >= lo && key <= hi) atomicAdd(&sh.hist[(hi - key) >> shift], 1u);
+        for (int i = threadIdx.x * 4; i < nseg; i += THREADS * 4) {   // keys of 0 behind the last
+            const uint4 v = *reinterpret_cast<const uint4*>(segkey + i);
+            const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (key[e] >= lo && key[e] <= hi) atomicAdd(&sh.hist[(hi - key[e]) >> shift], 1u);
         }
         __syncthreads();
-        find_bin(sh, kBins, base, want);
+        find_bin<THREADS>(sh, kBins, base, want);
         const uint32_t bin = sh.bin, through = sh.through;
         base = sh.below;
         const u64 edge = (u64(bin) + 1) << shift;                  // keys of bins 0 .. bin
@@ -167,30 +252,8 @@ __device__ __noinline__ uint32_t segment_bound(const float* segmax, int nseg, ui
         if (through <= want + slack || shift == 0) return bound;
         hi -= bin << shift;
         lo = bound;
+        for (int b = threadIdx.x; b < kBins; b += THREADS) sh.hist[b] = 0;
         __syncthreads();
-    }
-}
-
-// Sorts sh.list[0, n) descending; n <= kList.
-__device__ __noinline__ void sort_list(Shared& sh, int n) {
-    int size = 2;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = 0;
-    __syncthreads();
-    for (int run = 2; run <= size; run <<= 1) {
-        for (int d = run >> 1; d > 0; d >>= 1) {
-            for (int i = threadIdx.x; i < size; i += kThreads) {
-                const int j = i ^ d;
-                if (j > i) {
-                    const u64 p = sh.list[i], q = sh.list[j];
-                    if ((p < q) == ((i & run) == 0)) {
-                        sh.list[i] = q;
-                        sh.list[j] = p;
-                    }
-                }
-            }
-            __syncthreads();
-        }
     }
 }
 
@@ -199,15 +262,16 @@ __device__ __forceinline__ u64 element(uint32_t key, int col) {
 }
 
 // The K largest of the row into the list, by the digits of their keys: for rows whose segments
-// say too little.  Leaves sh.n.
-template <typename T>
-__device__ __noinline__ void select_digits(const T* row, int V, uint32_t K, Shared& sh) {
+// say too little.  Leaves sh.n; returns a key that all of them reach.
+template <typename T, int THREADS>
+__device__ __noinline__ uint32_t select_digits(const T* row, int V, uint32_t K, Shared& sh,
+                                            u64* list) {
     const int tid = threadIdx.x, lane = tid & 31;
     uint32_t prefix = 0, above = 0;          // above: keys larger than the prefix's
     for (int shift = 24; shift >= 0; shift -= 8) {
-        sh.hist[tid] = 0;
+        if (tid < 256) sh.hist[tid] = 0;
         __syncthreads();
-        for (int c0 = 0; c0 < V; c0 += kThreads) {
+        for (int c0 = 0; c0 < V; c0 += THREADS) {
             const int c = c0 + tid;
             const uint32_t key = c < V ? order_key(to_f32(row[c])) : 0;
             // bins in descending order of the digit; -inf is never counted
@@ -218,7 +282,7 @@ __device__ __noinline__ void select_digits(const T* row, int V, uint32_t K, Shar
         }
         if (tid == 0) sh.through = 0;
         __syncthreads();
-        find_bin(sh, 256, above, K);
+        find_bin<THREADS>(sh, 256, above, K);
         if (sh.through == 0) break;          // fewer than K above -inf (in the first step only)
         prefix = (prefix << 8) | (255 - sh.bin);
         above = sh.below;
@@ -228,37 +292,52 @@ __device__ __noinline__ void select_digits(const T* row, int V, uint32_t K, Shar
     const bool all = sh.through == 0;
     const uint32_t kth = all ? kKeyNegInf : prefix;
     uint32_t n = 0, ties = all ? 0 : K - above;
-    for (int c0 = 0; c0 < V && n < K; c0 += kThreads) {
+    for (int c0 = 0; c0 < V && n < K; c0 += THREADS) {
         const int c = c0 + tid;
         const uint32_t key = c < V ? order_key(to_f32(row[c])) : 0;
         uint32_t total_tie = 0, total;
-        const uint32_t before = block_prefix(key == kth && !all ? 1 : 0, sh, total_tie);
+        const uint32_t before = block_prefix<THREADS>(key == kth && !all ? 1 : 0, sh, total_tie);
         const bool take = key > kth || (!all && key == kth && before < ties);
-        const uint32_t at = block_prefix(take ? 1 : 0, sh, total);
-        if (take) sh.list[n + at] = element(key, c);
+        const uint32_t at = block_prefix<THREADS>(take ? 1 : 0, sh, total);
+        if (take) list[n + at] = element(key, c);
         n += total;
         ties -= min(ties, total_tie);
     }
     __syncthreads();
     if (tid == 0) sh.n = n;
     __syncthreads();
+    return all ? kKeyNegInf + 1 : kth;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    topk_kernel(const T* logits, const TopkArgs a, const Segments seg, int units, int ranks) {
-    constexpr int VEC = 16 / sizeof(T), LOADS = kUnit / 32 / VEC;
+// How the row is divided, and the shares of shared memory: where the segments' keys were, the
+// list is put in order.
+constexpr int kSlots = 2;
+constexpr size_t kListOff = (sizeof(Shared) + 15) / 16 * 16;
+struct Plan {
+    int units, streams, ranks, lanes, log_lanes, halves, nseg, list;
+    size_t stream_off, seg_off, bytes;
+};
+
+template <typename T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
+    topk_kernel(const T* logits, const TopkArgs args, const Plan plan) {
+    typedef Unit<T> U;
+    constexpr int VEC = U::VEC;
     extern __shared__ uint4 smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
-    float2* unit_ms = reinterpret_cast<float2*>(&sh + 1);
-    float* segmax = reinterpret_cast<float*>(unit_ms + units);
-    const int nseg = units * seg.per_unit();
+    uint8_t* base = reinterpret_cast<uint8_t*>(smem);
+    u64* list = reinterpret_cast<u64*>(base + kListOff);
+    Stream* of_stream = reinterpret_cast<Stream*>(base + plan.stream_off);
+    uint32_t* segkey = reinterpret_cast<uint32_t*>(base + plan.seg_off);
+    TopkArgs a = args;
+    const int units = plan.units, ranks = plan.ranks, nseg = plan.nseg, streams = plan.streams;
     const int row = blockIdx.x / ranks;
     const uint32_t rank = ranks > 1 ? cluster_ctarank() : 0u;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    wait_previous(logits, a.mask);
     if (a.mask != nullptr && a.mask[row] == 0) {
         if (rank == 0) {
-            for (int j = tid; j < a.K; j += kThreads) {
+            for (int j = tid; j < a.K; j += THREADS) {
                 a.ids[static_cast<int64_t>(row) * a.K + j] = -1;
                 a.logp[static_cast<int64_t>(row) * a.K + j] = 0.f;
             }
@@ -267,45 +346,74 @@ __global__ void __launch_bounds__(kThreads)
         return;
     }
     const T* x_row = logits + row * a.stride;
-    float2* to_ms = unit_ms;
-    float* to_seg = segmax;
-    if (ranks > 1) {
-        cluster_sync();                          // the first block is there
-        to_ms = peer(unit_ms, 0);
-        to_seg = peer(segmax, 0);
-    }
-    for (int u = static_cast<int>(rank) * kWarps + warp; u < units; u += ranks * kWarps) {
-        float x[LOADS][VEC];
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j)
-            load_piece(x_row, a.V, u * kUnit + (j * 32 + lane) * VEC, a.vec_ok, x[j]);
-        float half[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                half[2 * j / LOADS] = fmaxf(half[2 * j / LOADS], x[j][e]);
-        float m = fmaxf(half[0], half[1]);
-        if (seg.halves == 2) {
-            to_seg[u * 64 + lane * 2] = half[0];
-            to_seg[u * 64 + lane * 2 + 1] = half[1];
-            m = warp_max(m);
-        } else {
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                if (off == seg.lanes && lane % off == 0) to_seg[(u * 32 + lane) / off] = m;
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            }
-            if (seg.lanes == 32 && lane == 0) to_seg[u] = m;
+    // this warp's streams, one after the other, and its ring: units i, i + 1 on their way
+    const int step = ranks * (THREADS / 32), last = min(streams, units);
+    int stream = static_cast<int>(rank) * (THREADS / 32) + warp;
+    int u = stream, ahead = stream, ahead_stream = stream;
+    uint4* ring = smem + warp * kSlots * kLoads * 32 + lane;
+    const auto fetch_next = [&](uint4* slot) {
+        if (ahead_stream < last) {
+            U::fetch(slot, x_row, a.V, ahead, lane, a.vec_ok);
+            ahead += streams;
+            if (ahead >= units) ahead = ahead_stream += step;
         }
-        const float mm = m == -INFINITY ? 0.f : m;
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) s += ex2_approx((x[j][e] - mm) * a.k);
-        s = warp_sum(s);
-        if (lane == 0) to_ms[u] = make_float2(m, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int q = 0; q < kSlots; ++q) fetch_next(ring + q * kLoads * 32);
+    Stream* to_stream = of_stream;
+    uint32_t* to_seg = segkey;
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();                          // the first block is there
+        to_stream = peer(to_stream, 0);
+        to_seg = peer(to_seg, 0);
+    }
+    int slot = 0;
+    float m = -INFINITY, s = 0.f, low = INFINITY;
+    uint32_t count = 0;
+    while (stream < last) {
+        U now;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+        now.read(ring + slot * kLoads * 32);
+        fetch_next(ring + slot * kLoads * 32);
+        slot = slot + 1 == kSlots ? 0 : slot + 1;
+        const int at = u;
+        const bool ends = u + streams >= units;
+        const int to = ends ? stream + step : stream;
+        u = ends ? to : u + streams;
+        float mu;
+        if (plan.halves == 2) {
+            const float m0 = now.largest(0, kLoads / 2), m1 = now.largest(kLoads / 2, kLoads / 2);
+            *reinterpret_cast<uint2*>(to_seg + (at * 32 + lane) * 2) =
+                make_uint2(order_key(m0), order_key(m1));
+            mu = fmaxf(m0, m1);
+            low = fminf(low, fminf(m0 > -INFINITY ? m0 : INFINITY, m1 > -INFINITY ? m1 : INFINITY));
+            count += (m0 > -INFINITY) + (m1 > -INFINITY);
+        } else {
+            mu = now.largest(0, kLoads);
+            float g = mu;
+            for (int off = 1; off < plan.lanes; off <<= 1)
+                g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, off));
+            if (lane % plan.lanes == 0) to_seg[(at * 32 + lane) >> plan.log_lanes] = order_key(g);
+            if (mu > -INFINITY) ++count, low = fminf(low, mu);
+        }
+        // the lane's running maximum and sum; 0 stands in for a maximum of -inf
+        const float nm = fmaxf(m, mu), zero = nm == -INFINITY ? 0.f : nm;
+        const float su = now.weight(mu == -INFINITY ? 0.f : mu, a.k);
+        s = fmaf(s, ex2_approx((m - zero) * a.k), su * (mu == -INFINITY ? 1.f : ex2_approx((mu - zero) * a.k)));
+        m = nm;
+        if (ends) {
+            const float top = warp_max(m), ref = top == -INFINITY ? 0.f : top;
+            s = warp_sum(s * (m == -INFINITY ? 1.f : ex2_approx((m - ref) * a.k)));
+            low = -warp_max(-low);
+            count = __reduce_add_sync(0xffffffffu, count);
+            if (lane == 0) to_stream[stream] = Stream{top, s, low, count};
+            m = -INFINITY, s = 0.f, low = INFINITY, count = 0;
+            stream = to;
+        }
+    }
+    if (rank == 0) {
+        if (tid < 4 && (nseg & ~3) + tid >= nseg && nseg % 4 != 0) segkey[(nseg & ~3) + tid] = 0;
     }
     if (ranks > 1) {
         __syncwarp();
@@ -314,46 +422,31 @@ __global__ void __launch_bounds__(kThreads)
     } else {
         __syncthreads();
     }
-
-    // the row's maximum and sum; the range of the segments' maxima
-    float m = -INFINITY, low = INFINITY;
-    for (int u = tid; u < units; u += kThreads) m = fmaxf(m, unit_ms[u].x);
-    uint32_t finite = 0;
-    for (int s = tid; s < nseg; s += kThreads) {
-        const float v = segmax[s];
-        if (v > -INFINITY) ++finite, low = fminf(low, v);
-    }
-    m = warp_max(m);
-    if (lane == 0) sh.warp_f[warp] = m;
-    uint32_t total;
-    block_prefix(finite, sh, total);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.warp_f[w]);
-    __syncthreads();
-    low = -warp_max(-low);
-    if (lane == 0) sh.warp_f[warp] = low;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) low = fminf(low, sh.warp_f[w]);
-    const float mm = m == -INFINITY ? 0.f : m;
-    float s = 0.f;
-    for (int u = tid; u < units; u += kThreads) {
-        const float2 p = unit_ms[u];
-        if (!(p.x == -INFINITY && p.y == 0.f))   // nothing in it (but not NaN)
-            s = fmaf(p.y, ex2_approx((p.x - mm) * a.k), s);
-    }
-    s = warp_sum(s);
-    __syncthreads();
-    if (lane == 0) sh.warp_f[warp] = s;
+    for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
     if (tid == 0) sh.n = sh.queued = 0;
     __syncthreads();
-    s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sh.warp_f[w];
+
+    // the row's maximum and sum; the least of the segments' maxima, and how many are above -inf
+    // (each warp for itself, in one order)
+    for (int i = lane; i < last; i += 32) {
+        m = fmaxf(m, of_stream[i].m);
+        low = fminf(low, of_stream[i].low);
+        count += of_stream[i].count;
+    }
+    m = warp_max(m);
+    low = -warp_max(-low);
+    count = __reduce_add_sync(0xffffffffu, count) / plan.lanes;
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < last; i += 32) {
+        const Stream p = of_stream[i];
+        s = fmaf(p.s, p.m == -INFINITY ? 1.f : ex2_approx((p.m - ref) * a.k), s);
+    }
+    s = warp_sum(s);
+    const uint32_t K = static_cast<uint32_t>(a.K);
     int64_t* ids = a.ids + static_cast<int64_t>(row) * a.K;
     float* logp = a.logp + static_cast<int64_t>(row) * a.K;
     if (!(s > 0.f && s < INFINITY && fabsf(m) < INFINITY)) {
-        for (int j = tid; j < a.K; j += kThreads) {
+        for (int j = tid; j < a.K; j += THREADS) {
             ids[j] = -1;
             logp[j] = __int_as_float(0x7fc00000);
         }
@@ -366,88 +459,164 @@ __global__ void __launch_bounds__(kThreads)
     const float ln_s = lg2_approx(s) * kLn2;
     if (tid == 0 && a.lse != nullptr) a.lse[row] = fmaf(m, a.inv_t, ln_s);
 
-    const uint32_t K = static_cast<uint32_t>(a.K);
-    const uint32_t bound =
-        total < K ? kKeyNegInf + 1
-                  : segment_bound(segmax, nseg, order_key(low), order_key(m), K, sh);
-    __syncthreads();
-    // the segments that reach it (their numbers take the histogram's place), then their elements
-    for (int g = tid; g < nseg; g += kThreads)
-        if (order_key(segmax[g]) >= bound) {
-            const uint32_t at = atomicAdd(&sh.queued, 1u);
-            if (at < kBins) sh.hist[at] = g;
-        }
+    // the segments that reach the bound, then their elements
+    uint32_t bound = kKeyNegInf + 1;
+    if (count >= K)
+        bound = segment_bound<THREADS>(segkey, nseg, order_key(low), order_key(m), K, sh);
+    for (int i = tid * 4; i < nseg; i += THREADS * 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(segkey + i);
+        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (key[e] >= bound) {
+                const uint32_t at = atomicAdd(&sh.queued, 1u);
+                if (at < kQueue) sh.queue[at] = static_cast<uint16_t>(i + e);
+            }
+    }
     __syncthreads();
     const uint32_t queued = sh.queued;
-    if (queued <= kBins) {
-        const int loads = LOADS / seg.halves, pieces = loads * seg.lanes;
-        const int per_unit = seg.per_unit();
-        for (int i = tid; i < static_cast<int>(queued) * pieces; i += kThreads) {
-            const int g = sh.hist[i / pieces], p = i % pieces;
-            const int u = g / per_unit, in = g % per_unit;
-            const int j = p / seg.lanes + (seg.halves == 2 ? (in & 1) * loads : 0);
-            const int l = seg.halves == 2 ? in / 2 : in * seg.lanes + p % seg.lanes;
-            const int c = u * kUnit + (j * 32 + l) * VEC;
-            float x[VEC];
-            load_piece(x_row, a.V, c, a.vec_ok, x);
+    if (queued <= kQueue) {
+        // pieces of 16 bytes of a segment: 2, 4, 8 .. 128
+        const int log_pieces = (plan.halves == 2 ? 1 : 2) + plan.log_lanes;
+        const int pieces = static_cast<int>(queued) << log_pieces;
+        constexpr int kAhead = 4;
+        for (int i0 = tid; i0 < pieces; i0 += kAhead * THREADS) {
+            uint4 v[kAhead];
+            int col[kAhead];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const uint32_t key = order_key(x[e]);
-                if (key < bound) continue;
-                const uint32_t at = atomicAdd(&sh.n, 1u);
-                if (at < kList) sh.list[at] = element(key, c + e);
+            for (int q = 0; q < kAhead; ++q) {
+                const int i = i0 + q * THREADS;
+                if (i >= pieces) continue;
+                const int g = sh.queue[i >> log_pieces], p = i & ((1 << log_pieces) - 1);
+                int unit, load, l;
+                if (plan.halves == 2) {
+                    unit = g >> 6, l = (g & 63) >> 1, load = (g & 1) * (kLoads / 2) + p;
+                } else {
+                    const int first = g << plan.log_lanes;       // unit * 32 + its first lane
+                    unit = first >> 5, l = (first & 31) + (p & (plan.lanes - 1));
+                    load = p >> plan.log_lanes;
+                }
+                col[q] = U::column(unit, load, l);
+                v[q] = load_piece(x_row, a.V, col[q], a.vec_ok);
+            }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                if (i0 + q * THREADS >= pieces) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const uint32_t key = order_key(piece_value<T>(v[q], e));
+                    if (key < bound) continue;
+                    const uint32_t at = atomicAdd(&sh.n, 1u);
+                    if (at < static_cast<uint32_t>(plan.list)) list[at] = element(key, col[q] + e);
+                }
             }
         }
     }
+    for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
     __syncthreads();
-    if (queued > kBins || sh.n > kList) select_digits(x_row, a.V, K, sh);
+    if (queued > kQueue || sh.n > static_cast<uint32_t>(plan.list)) {
+        bound = select_digits<T, THREADS>(x_row, a.V, K, sh, list);
+        for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
+        __syncthreads();
+    }
+
+    // in order: bins of the key from the largest on, then among the few of a bin
     const int n = static_cast<int>(sh.n);
-    sort_list(sh, n);
-    for (int j = tid; j < a.K; j += kThreads) {
-        if (j < n) {
-            const u64 el = sh.list[j];
-            ids[j] = static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(el));
-            logp[j] = fmaf(key_value(static_cast<uint32_t>(el >> 32)) - m, a.inv_t, -ln_s);
-        } else {
-            ids[j] = -1;
-            logp[j] = -INFINITY;
+    const uint32_t top = order_key(m);
+    const int shift = max(0, 21 - __clz((top - bound) | 1u));
+    constexpr int kEach = 2048 / THREADS;
+    uint32_t arrived[kEach];
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        const int i = tid + q * THREADS;
+        if (i < n)
+            arrived[q] = atomicAdd(&sh.hist[(top - static_cast<uint32_t>(list[i] >> 32)) >> shift], 1u);
+    }
+    __syncthreads();
+    {
+        uint32_t own[kBins / THREADS], sum = 0, all;
+#pragma unroll
+        for (int b = 0; b < kBins / THREADS; ++b) {
+            own[b] = sh.hist[tid * (kBins / THREADS) + b];
+            sum += own[b];
+        }
+        uint32_t run = block_prefix<THREADS>(sum, sh, all);
+#pragma unroll
+        for (int b = 0; b < kBins / THREADS; ++b) {
+            sh.hist[tid * (kBins / THREADS) + b] = run;
+            run += own[b];
         }
     }
+    __syncthreads();
+    u64* ordered = reinterpret_cast<u64*>(segkey);
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        const int i = tid + q * THREADS;
+        if (i < n) {
+            const u64 el = list[i];
+            ordered[sh.hist[(top - static_cast<uint32_t>(el >> 32)) >> shift] + arrived[q]] = el;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += THREADS) {
+        const u64 el = ordered[i];
+        const uint32_t key = static_cast<uint32_t>(el >> 32), bin = (top - key) >> shift;
+        const int from = static_cast<int>(sh.hist[bin]);
+        const int end = bin + 1 < kBins ? static_cast<int>(sh.hist[bin + 1]) : n;
+        if (from >= a.K) continue;
+        int place = from;
+        for (int j = from; j < end; ++j) place += ordered[j] > el;
+        if (place >= a.K) continue;
+        ids[place] = static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(el));
+        logp[place] = fmaf(key_value(key) - m, a.inv_t, -ln_s);
+    }
+    for (int j = n + tid; j < a.K; j += THREADS) {
+        ids[j] = -1;
+        logp[j] = -INFINITY;
+    }
+}
+
+template <typename T, int THREADS>
+cudaError_t launch_threads(const T* logits, const TopkArgs& a, const Plan& p,
+                           cudaStream_t stream) {
+    constexpr size_t kMost = 100 * 1024;     // of any vocabulary
+    static_assert(std::max(kListOff + 2048 * 8, size_t(THREADS) * kSlots * kLoads * 16) +
+                          kMaxStreams * sizeof(Stream) + kMaxSegments * 4 <= kMost,
+                  "a block's shared memory");
+    if (p.bytes > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(topk_kernel<T, THREADS>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = p.ranks;
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    return launch_early(topk_kernel<T, THREADS>, dim3(static_cast<unsigned>(a.N) * p.ranks),
+                        THREADS, p.bytes, stream, &cluster, logits, a, p);
 }
 
 template <typename T>
 cudaError_t launch_typed(const T* logits, const TopkArgs& a, cudaStream_t stream) {
-    const int units = (a.V + kUnit - 1) / kUnit;
-    Segments seg{1, 1};
-    if (units * 32 < 4 * a.K) seg.halves = 2;
-    while (units * seg.per_unit() > kMaxSegments) seg.lanes *= 2;
-    int ranks = units >= 64 ? 8 : units >= 32 ? 4 : units >= 16 ? 2 : 1;
-    while (ranks > 1 && static_cast<int64_t>(a.N) * ranks > 608) ranks /= 2;
-    const size_t smem = sizeof(Shared) + units * sizeof(float2) +
-                        static_cast<size_t>(units) * seg.per_unit() * sizeof(float);
-    constexpr int kMost = 100 * 1024;        // of any vocabulary
-    static_assert(sizeof(Shared) + kMaxTopkColumns / kUnit * 8 + kMaxSegments * 4 <= kMost,
-                  "a block's shared memory");
-    void (*kernel)(const T*, const TopkArgs, const Segments, int, int) = topk_kernel<T>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-        if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.N) * ranks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, logits, a, seg, units, ranks);
+    Plan p{};
+    p.units = (a.V + Unit<T>::kColumns - 1) / Unit<T>::kColumns;
+    p.streams = p.units >= 256 ? 128 : 64;
+    p.lanes = p.halves = 1;
+    if (p.units * 32 < 4 * a.K) p.halves = 2;
+    while (p.units * 32 * p.halves / p.lanes > kMaxSegments) p.lanes *= 2, ++p.log_lanes;
+    p.nseg = p.units * 32 * p.halves / p.lanes;
+    p.list = list_size(a.K);
+    p.ranks = p.units >= 64 ? 8 : p.units >= 32 ? 4 : p.units >= 16 ? 2 : 1;
+    while (p.ranks > 1 && static_cast<int64_t>(a.N) * p.ranks > 608) p.ranks /= 2;
+    const int threads = static_cast<int64_t>(a.N) * p.ranks <= 304 ? 512 : 256;
+    p.stream_off = std::max(kListOff + p.list * sizeof(u64), size_t(threads) * kSlots * kLoads * 16);
+    p.seg_off = p.stream_off + p.streams * sizeof(Stream);
+    p.bytes = p.seg_off + std::max((p.nseg + 3) / 4 * 4 * sizeof(uint32_t), p.list * sizeof(u64));
+    if (threads == 512)
+        return launch_threads<T, 512>(logits, a, p, stream);
+    return launch_threads<T, 256>(logits, a, p, stream);
 }
 
 }  // namespace
