@@ -35,7 +35,9 @@ typedef unsigned long long u64;
 constexpr int kLoads = 4;                // 16-byte loads a lane of a unit
 constexpr int kBins = 2048;
 constexpr int kQueue = 2048;             // segments that are read again
-constexpr int kMaxSegments = 8192;
+constexpr int kPieces = 8192;            // and 16-byte pieces of them
+constexpr int kList = 2048;              // elements of the longest list
+constexpr int kMaxSegments = 10240;
 constexpr int kMaxStreams = 128;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 constexpr float kLn2 = 0.693147180559945309f;
@@ -79,29 +81,65 @@ struct Unit {
     __device__ __forceinline__ static int column(int unit, int load, int lane) {
         return unit * kColumns + (load * 32 + lane) * VEC;
     }
-    // A lane's part of a unit into its place of a warp's ring in shared memory, on its way while
-    // others are worked on; -inf past the row's end.  Each lane copies just what it reads itself,
-    // so this needs no barrier.
+    // A unit into a slot of a warp's ring in shared memory, on its way while others are worked
+    // on; -inf past the row's end.  `off` is how many bytes behind a 16-byte border the row
+    // starts: the copies start on the border, so a slot holds one piece more than a unit.  At 0
+    // each lane copies just what it reads itself and no barrier is needed.  A unit whose last
+    // piece reaches past the row is read by its elements.
+    __device__ __forceinline__ static bool whole(int V, int unit, int off) {
+        return (unit + 1) * kColumns + (off != 0 ? VEC : 0) <= V;
+    }
     __device__ __forceinline__ static void fetch(uint4* slot, const T* row, int V, int unit,
-                                                 int lane, bool vec) {
-        if (vec && (unit + 1) * kColumns <= V) {
+                                                 int lane, int off) {
+        if (whole(V, unit, off)) {
+            const uint8_t* from = reinterpret_cast<const uint8_t*>(row + column(unit, 0, 0)) - off;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(slot + j * 32)),
-                             "l"(row + column(unit, j, lane))
-                             : "memory");
+            for (int j = 0; j < kLoads; ++j) copy16(slot + j * 32 + lane, from + (j * 32 + lane) * 16);
+            if (off != 0 && lane == 0) copy16(slot + kLoads * 32, from + kLoads * 512);
         } else {
-#pragma unroll 1
-            for (int j = 0; j < kLoads; ++j)
-                load_edge(row, V, column(unit, j, lane), reinterpret_cast<uint32_t*>(slot + j * 32));
+            fetch_edge(slot + lane, row, V, unit, lane);
         }
     }
-    __device__ __forceinline__ void read(const uint4* slot) {
+    // all loads on their way at once
+    __device__ __noinline__ static void fetch_edge(uint4* slot, const T* row, int V, int unit,
+                                                   int lane) {
+        alignas(16) T v[kLoads][VEC];
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const uint4 v = slot[j * 32];
-            w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int c = column(unit, j, lane) + e;
+                v[j][e] = c < V ? row[c] : T(-INFINITY);
+            }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) slot[j * 32] = *reinterpret_cast<const uint4*>(v[j]);
+    }
+    __device__ __forceinline__ static void copy16(uint4* to, const uint8_t* from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                     : "memory");
+    }
+    __device__ __forceinline__ void read(const uint4* slot, int lane, int off) {
+        if (off == 0) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const uint4 v = slot[j * 32 + lane];
+                w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(slot + j * 32 + lane) + off / 4;
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t v[5] = {p[0], p[1], p[2], p[3], p[4]};
+                    const int half = (off & 2) * 8;              // 0 or 16
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[4 * j + i] = __funnelshift_r(v[i], v[i + 1], half);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[4 * j + i] = p[i];
+                }
+            }
         }
     }
     __device__ __noinline__ static void load_edge(const T* row, int V, int c, uint32_t* to) {
@@ -112,18 +150,18 @@ struct Unit {
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = p[i];
     }
-    // the largest of words [4 * first, 4 * (first + loads))
-    __device__ __forceinline__ float largest(int first, int loads) const {
+    // the largest of 4 * loads words
+    __device__ __forceinline__ static float largest(const uint32_t* w, int loads) {
         if constexpr (sizeof(T) == 2) {
-            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w + 4 * first);
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(w);
             __nv_bfloat162 m = p[0];
 #pragma unroll
             for (int i = 1; i < 4 * loads; ++i) m = __hmax2(m, p[i]);
             return fmaxf(__low2float(m), __high2float(m));
         } else {
-            float m = __uint_as_float(w[4 * first]);
+            float m = __uint_as_float(w[0]);
 #pragma unroll
-            for (int i = 1; i < 4 * loads; ++i) m = fmaxf(m, __uint_as_float(w[4 * first + i]));
+            for (int i = 1; i < 4 * loads; ++i) m = fmaxf(m, __uint_as_float(w[i]));
             return m;
         }
     }
@@ -145,12 +183,26 @@ struct Unit {
     }
 };
 
-// VEC consecutive columns from c on, as floats; -inf past the row's end.
-template <typename T>
-__device__ __forceinline__ uint4 load_piece(const T* row, int V, int c, bool vec) {
-    if (vec && c + Unit<T>::VEC <= V) return __ldg(reinterpret_cast<const uint4*>(row + c));
-    uint32_t w[4];
-    Unit<T>::load_edge(row, V, c, w);
+// VEC consecutive columns from c < V on; -inf past the row's end.  A row that does not start on 16
+// bytes is read by words: each holds an element of the row.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ uint4 load_piece(const T* row, int V, int c) {
+    uint32_t w[5];
+    if (c + Unit<T>::VEC > V) {
+        Unit<T>::load_edge(row, V, c, w);
+    } else if (ALIGNED) {
+        return __ldg(reinterpret_cast<const uint4*>(row + c));
+    } else {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(p + i);
+        if (sizeof(T) == 2 && (at & 2) != 0) {
+            w[4] = __ldg(p + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        }
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename T>
@@ -171,6 +223,7 @@ struct Stream {
 struct Shared {
     uint32_t hist[kBins];
     uint16_t queue[kQueue];
+    alignas(4) uint8_t bits[kPieces + 4];
     uint32_t warp_n[32];
     uint32_t n, queued;
     uint32_t bin, below, through;        // of the histogram: the bin K falls on, counts to it
@@ -178,7 +231,7 @@ struct Shared {
 
 // Elements the list holds: about K are found where segments are many, and never more than
 // twice as many that a histogram would let through.
-__host__ __device__ constexpr int list_size(int K) { return K <= 256 ? 1024 : 2048; }
+__host__ __device__ constexpr int list_size(int K) { return K <= 256 ? 1024 : kList; }
 
 // Exclusive prefix of n over the block, and the total.
 template <int THREADS>
@@ -311,14 +364,15 @@ __device__ __noinline__ uint32_t select_digits(const T* row, int V, uint32_t K, 
 
 // How the row is divided, and the shares of shared memory: where the segments' keys were, the
 // list is put in order.
-constexpr int kSlots = 2;
+constexpr int kSlots = 2, kSlot = kLoads * 32 + 1;         // of a ring, and 16-byte pieces of one
 constexpr size_t kListOff = (sizeof(Shared) + 15) / 16 * 16;
 struct Plan {
     int units, streams, ranks, lanes, log_lanes, halves, nseg, list;
     size_t stream_off, seg_off, bytes;
 };
 
-template <typename T, int THREADS>
+// ALIGNED: all rows start on 16 bytes.
+template <typename T, int THREADS, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     topk_kernel(const T* logits, const TopkArgs args, const Plan plan) {
     typedef Unit<T> U;
@@ -350,16 +404,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     const int step = ranks * (THREADS / 32), last = min(streams, units);
     int stream = static_cast<int>(rank) * (THREADS / 32) + warp;
     int u = stream, ahead = stream, ahead_stream = stream;
-    uint4* ring = smem + warp * kSlots * kLoads * 32 + lane;
+    uint4* ring = smem + warp * kSlots * kSlot;
+    const int off = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(x_row) & 15);
     const auto fetch_next = [&](uint4* slot) {
         if (ahead_stream < last) {
-            U::fetch(slot, x_row, a.V, ahead, lane, a.vec_ok);
+            U::fetch(slot, x_row, a.V, ahead, lane, off);
             ahead += streams;
             if (ahead >= units) ahead = ahead_stream += step;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int q = 0; q < kSlots; ++q) fetch_next(ring + q * kLoads * 32);
+    for (int q = 0; q < kSlots; ++q) fetch_next(ring + q * kSlot);
     Stream* to_stream = of_stream;
     uint32_t* to_seg = segkey;
     if (ranks > 1) {
@@ -374,8 +429,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     while (stream < last) {
         U now;
         asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
-        now.read(ring + slot * kLoads * 32);
-        fetch_next(ring + slot * kLoads * 32);
+        if (!ALIGNED) __syncwarp();              // the other lanes' copies too
+        now.read(ring + slot * kSlot, lane, U::whole(a.V, u, off) ? off : 0);
+        if (!ALIGNED) __syncwarp();              // read before it is written again
+        fetch_next(ring + slot * kSlot);
         slot = slot + 1 == kSlots ? 0 : slot + 1;
         const int at = u;
         const bool ends = u + streams >= units;
@@ -383,14 +440,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         u = ends ? to : u + streams;
         float mu;
         if (plan.halves == 2) {
-            const float m0 = now.largest(0, kLoads / 2), m1 = now.largest(kLoads / 2, kLoads / 2);
+            const float m0 = U::largest(now.w, kLoads / 2),
+                        m1 = U::largest(now.w + 2 * kLoads, kLoads / 2);
             *reinterpret_cast<uint2*>(to_seg + (at * 32 + lane) * 2) =
                 make_uint2(order_key(m0), order_key(m1));
             mu = fmaxf(m0, m1);
             low = fminf(low, fminf(m0 > -INFINITY ? m0 : INFINITY, m1 > -INFINITY ? m1 : INFINITY));
             count += (m0 > -INFINITY) + (m1 > -INFINITY);
         } else {
-            mu = now.largest(0, kLoads);
+            mu = U::largest(now.w, kLoads);
             float g = mu;
             for (int off = 1; off < plan.lanes; off <<= 1)
                 g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, off));
@@ -424,7 +482,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
     for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
     if (tid == 0) sh.n = sh.queued = 0;
-    __syncthreads();
 
     // the row's maximum and sum; the least of the segments' maxima, and how many are above -inf
     // (each warp for itself, in one order)
@@ -460,6 +517,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     if (tid == 0 && a.lse != nullptr) a.lse[row] = fmaf(m, a.inv_t, ln_s);
 
     // the segments that reach the bound, then their elements
+    __syncthreads();
     uint32_t bound = kKeyNegInf + 1;
     if (count >= K)
         bound = segment_bound<THREADS>(segkey, nseg, order_key(low), order_key(m), K, sh);
@@ -475,62 +533,81 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     }
     __syncthreads();
     const uint32_t queued = sh.queued;
-    if (queued <= kQueue) {
-        // pieces of 16 bytes of a segment: 2, 4, 8 .. 128
-        const int log_pieces = (plan.halves == 2 ? 1 : 2) + plan.log_lanes;
+    // pieces of 16 bytes of a segment: 2, 4, 8 .. 128
+    const int log_pieces = (plan.halves == 2 ? 1 : 2) + plan.log_lanes;
+    const auto piece_column = [&](int i) {
+        const int g = sh.queue[i >> log_pieces], p = i & ((1 << log_pieces) - 1);
+        if (plan.halves == 2)
+            return U::column(g >> 6, (g & 1) * (kLoads / 2) + p, (g & 63) >> 1);
+        const int first = g << plan.log_lanes;   // unit * 32 + its first lane
+        return U::column(first >> 5, p >> plan.log_lanes, (first & 31) + (p & (plan.lanes - 1)));
+    };
+    uint32_t* columns = segkey;                  // read until here
+    uint32_t n = kList + 1;
+    if (queued <= static_cast<uint32_t>(min(kQueue, kPieces >> log_pieces))) {
+        // which columns of each piece reach the bound, a bit each
         const int pieces = static_cast<int>(queued) << log_pieces;
+        const float least = key_value(bound);    // x >= least where its key reaches the bound
         constexpr int kAhead = 4;
         for (int i0 = tid; i0 < pieces; i0 += kAhead * THREADS) {
             uint4 v[kAhead];
-            int col[kAhead];
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) {
-                const int i = i0 + q * THREADS;
-                if (i >= pieces) continue;
-                const int g = sh.queue[i >> log_pieces], p = i & ((1 << log_pieces) - 1);
-                int unit, load, l;
-                if (plan.halves == 2) {
-                    unit = g >> 6, l = (g & 63) >> 1, load = (g & 1) * (kLoads / 2) + p;
-                } else {
-                    const int first = g << plan.log_lanes;       // unit * 32 + its first lane
-                    unit = first >> 5, l = (first & 31) + (p & (plan.lanes - 1));
-                    load = p >> plan.log_lanes;
-                }
-                col[q] = U::column(unit, load, l);
-                v[q] = load_piece(x_row, a.V, col[q], a.vec_ok);
+                const int i = i0 + q * THREADS, c = i < pieces ? piece_column(i) : a.V;
+                // past the row: NaN, which reaches nothing
+                v[q] = make_uint4(~0u, ~0u, ~0u, ~0u);
+                if (c < a.V) v[q] = load_piece<T, ALIGNED>(x_row, a.V, c);
             }
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) {
-                if (i0 + q * THREADS >= pieces) continue;
+                uint32_t bits = 0;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const uint32_t key = order_key(piece_value<T>(v[q], e));
-                    if (key < bound) continue;
-                    const uint32_t at = atomicAdd(&sh.n, 1u);
-                    if (at < static_cast<uint32_t>(plan.list)) list[at] = element(key, col[q] + e);
-                }
+                for (int e = 0; e < VEC; ++e)
+                    bits |= piece_value<T>(v[q], e) >= least ? 1u << e : 0u;
+                if (i0 + q * THREADS < pieces) sh.bits[i0 + q * THREADS] = static_cast<uint8_t>(bits);
             }
         }
+        if (tid < 3) sh.bits[pieces + tid] = 0;
+        __syncthreads();
+        // the columns, in the pieces' order: four pieces at a time
+        const uint32_t* bits4 = reinterpret_cast<const uint32_t*>(sh.bits);
+        const int words = (pieces + 3) / 4, each = (words + THREADS - 1) / THREADS;
+        const int w0 = min(words, tid * each), w1 = min(words, w0 + each);
+        uint32_t own = 0;
+        for (int w = w0; w < w1; ++w) own += __popc(bits4[w]);
+        uint32_t at = block_prefix<THREADS>(own, sh, n);
+        if (n <= static_cast<uint32_t>(plan.list))
+            for (int w = w0; w < w1; ++w)
+                for (uint32_t b = bits4[w]; b != 0; b &= b - 1) {
+                    const int bit = __ffs(b) - 1;
+                    columns[at++] = piece_column(4 * w + bit / 8) + bit % 8;
+                }
     }
     for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
     __syncthreads();
-    if (queued > kQueue || sh.n > static_cast<uint32_t>(plan.list)) {
+    const bool searched = n > static_cast<uint32_t>(plan.list);
+    if (searched) {
         bound = select_digits<T, THREADS>(x_row, a.V, K, sh, list);
+        n = sh.n;
         for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
         __syncthreads();
     }
 
     // in order: bins of the key from the largest on, then among the few of a bin
-    const int n = static_cast<int>(sh.n);
     const uint32_t top = order_key(m);
     const int shift = max(0, 21 - __clz((top - bound) | 1u));
     constexpr int kEach = 2048 / THREADS;
     uint32_t arrived[kEach];
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-        const int i = tid + q * THREADS;
-        if (i < n)
+        const uint32_t i = tid + q * THREADS;
+        if (i < n) {
+            if (!searched) {
+                const int c = static_cast<int>(columns[i]);
+                list[i] = element(order_key(to_f32(x_row[c])), c);
+            }
             arrived[q] = atomicAdd(&sh.hist[(top - static_cast<uint32_t>(list[i] >> 32)) >> shift], 1u);
+        }
     }
     __syncthreads();
     {
@@ -551,18 +628,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     u64* ordered = reinterpret_cast<u64*>(segkey);
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
-        const int i = tid + q * THREADS;
+        const uint32_t i = tid + q * THREADS;
         if (i < n) {
             const u64 el = list[i];
             ordered[sh.hist[(top - static_cast<uint32_t>(el >> 32)) >> shift] + arrived[q]] = el;
         }
     }
     __syncthreads();
-    for (int i = tid; i < n; i += THREADS) {
+    for (uint32_t i = tid; i < n; i += THREADS) {
         const u64 el = ordered[i];
         const uint32_t key = static_cast<uint32_t>(el >> 32), bin = (top - key) >> shift;
         const int from = static_cast<int>(sh.hist[bin]);
-        const int end = bin + 1 < kBins ? static_cast<int>(sh.hist[bin + 1]) : n;
+        const int end = bin + 1 < kBins ? static_cast<int>(sh.hist[bin + 1]) : static_cast<int>(n);
         if (from >= a.K) continue;
         int place = from;
         for (int j = from; j < end; ++j) place += ordered[j] > el;
@@ -570,22 +647,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         ids[place] = static_cast<int64_t>(0xffffffffu - static_cast<uint32_t>(el));
         logp[place] = fmaf(key_value(key) - m, a.inv_t, -ln_s);
     }
-    for (int j = n + tid; j < a.K; j += THREADS) {
+    for (int j = static_cast<int>(n) + tid; j < a.K; j += THREADS) {
         ids[j] = -1;
         logp[j] = -INFINITY;
     }
 }
 
-template <typename T, int THREADS>
+template <typename T, int THREADS, bool ALIGNED>
 cudaError_t launch_threads(const T* logits, const TopkArgs& a, const Plan& p,
                            cudaStream_t stream) {
-    constexpr size_t kMost = 100 * 1024;     // of any vocabulary
-    static_assert(std::max(kListOff + 2048 * 8, size_t(THREADS) * kSlots * kLoads * 16) +
+    constexpr size_t kMost = 112 * 1024;     // of any vocabulary
+    static_assert(std::max(kListOff + 2048 * 8, size_t(THREADS / 32) * kSlots * kSlot * 16) +
                           kMaxStreams * sizeof(Stream) + kMaxSegments * 4 <= kMost,
                   "a block's shared memory");
     if (p.bytes > 48 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(topk_kernel<T, THREADS>),
+            cudaFuncSetAttribute(reinterpret_cast<const void*>(topk_kernel<T, THREADS, ALIGNED>),
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
         if (e != cudaSuccess) return e;
     }
@@ -594,7 +671,7 @@ cudaError_t launch_threads(const T* logits, const TopkArgs& a, const Plan& p,
     cluster.val.clusterDim.x = p.ranks;
     cluster.val.clusterDim.y = 1;
     cluster.val.clusterDim.z = 1;
-    return launch_early(topk_kernel<T, THREADS>, dim3(static_cast<unsigned>(a.N) * p.ranks),
+    return launch_early(topk_kernel<T, THREADS, ALIGNED>, dim3(static_cast<unsigned>(a.N) * p.ranks),
                         THREADS, p.bytes, stream, &cluster, logits, a, p);
 }
 
@@ -605,18 +682,29 @@ cudaError_t launch_typed(const T* logits, const TopkArgs& a, cudaStream_t stream
     p.streams = p.units >= 256 ? 128 : 64;
     p.lanes = p.halves = 1;
     if (p.units * 32 < 4 * a.K) p.halves = 2;
-    while (p.units * 32 * p.halves / p.lanes > kMaxSegments) p.lanes *= 2, ++p.log_lanes;
+    // 16 segments for each element that is looked for leave few others among the K largest of
+    // their maxima; more of them cost more than they save (K = 64 of [2048, 151936] bf16: 4768
+    // segments 129 us, 1192 of them 118).
+    while (p.units * 32 * p.halves / p.lanes > kMaxSegments ||
+           (p.halves == 1 && p.lanes < 32 &&
+            p.units * 32 / (2 * p.lanes) >= std::max(1024, 32 * a.K)))
+        p.lanes *= 2, ++p.log_lanes;
     p.nseg = p.units * 32 * p.halves / p.lanes;
     p.list = list_size(a.K);
+    // 512 threads a block while two of them on each of 152 SMs hold all rows, with as many blocks
+    // a row as that leaves; else four of 256 on an SM, a row each
+    const int threads = a.N <= 304 ? 512 : 256;
     p.ranks = p.units >= 64 ? 8 : p.units >= 32 ? 4 : p.units >= 16 ? 2 : 1;
-    while (p.ranks > 1 && static_cast<int64_t>(a.N) * p.ranks > 608) p.ranks /= 2;
-    const int threads = static_cast<int64_t>(a.N) * p.ranks <= 304 ? 512 : 256;
-    p.stream_off = std::max(kListOff + p.list * sizeof(u64), size_t(threads) * kSlots * kLoads * 16);
+    while (p.ranks > 1 && static_cast<int64_t>(a.N) * p.ranks > (threads == 512 ? 304 : 608))
+        p.ranks /= 2;
+    p.stream_off = std::max(kListOff + p.list * sizeof(u64), size_t(threads / 32) * kSlots * kSlot * 16);
     p.seg_off = p.stream_off + p.streams * sizeof(Stream);
     p.bytes = p.seg_off + std::max((p.nseg + 3) / 4 * 4 * sizeof(uint32_t), p.list * sizeof(u64));
     if (threads == 512)
-        return launch_threads<T, 512>(logits, a, p, stream);
-    return launch_threads<T, 256>(logits, a, p, stream);
+        return a.vec_ok ? launch_threads<T, 512, true>(logits, a, p, stream)
+                        : launch_threads<T, 512, false>(logits, a, p, stream);
+    return a.vec_ok ? launch_threads<T, 256, true>(logits, a, p, stream)
+                    : launch_threads<T, 256, false>(logits, a, p, stream);
 }
 
 }  // namespace
