@@ -868,13 +868,12 @@ def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, 
     _check("rlk_sample_logits", st)
 
 
-def _number_or_rows(p, name, value, n):
-    """A setting of a row: a number into p.name, or a CUDA tensor [n] into p.name_rows."""
+def _number_or_rows(name, value, n, off):
+    """(address, number) of a row's setting: a float32 CUDA tensor [n], or a number."""
     if isinstance(value, torch.Tensor):
         _need(value, torch.float32, name, (n,))
-        setattr(p, name + "_rows", value.data_ptr())
-    else:
-        setattr(p, name, float(value))
+        return value.data_ptr(), off
+    return None, float(value)
 
 
 def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence,
@@ -886,26 +885,27 @@ def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, freq
     and prompt_lengths [N] int64, bias_ids [N, B] int64 with bias_values [N, B] float32, allowed
     [N, >= ceil(V / 32)] int32 bits, active_mask: or None.  See include/rlk.h."""
     n, v, stride = _need_rows(logits, "logits")
-    out_stride = _need_rows(out, "out", (n, v), logits.dtype)[2]
-    p = ProcessParams(repetition=1.0)
+    out_stride = _need_rows(out, "out", logits.shape, logits.dtype)[2]
+    tok = full = prompt = bias = values = words = None
+    width = tok_stride = biases = words_stride = 0
     if tokens is not None:
         if tokens.dtype is not torch.int64:
             raise TypeError("tokens must be int64, got %s" % tokens.dtype)
-        rows, p.tokens_width, p.tokens_stride = _need_rows(tokens, "tokens")
+        rows, width, tok_stride = _need_rows(tokens, "tokens")
         if rows != n:
             raise ValueError("tokens must have %d rows, got %d" % (n, rows))
-        p.tokens = tokens.data_ptr()
+        tok = tokens.data_ptr()
         if lengths is not None:
             _need(lengths, torch.int64, "lengths", (n,))
-            p.lengths = lengths.data_ptr()
+            full = lengths.data_ptr()
         if prompt_lengths is not None:
             _need(prompt_lengths, torch.int64, "prompt_lengths", (n,))
-            p.prompt_lengths = prompt_lengths.data_ptr()
+            prompt = prompt_lengths.data_ptr()
     elif lengths is not None or prompt_lengths is not None:
         raise ValueError("lengths and prompt_lengths are of tokens")
-    _number_or_rows(p, "repetition", repetition, n)
-    _number_or_rows(p, "frequency", frequency, n)
-    _number_or_rows(p, "presence", presence, n)
+    rep_rows, rep = _number_or_rows("repetition", repetition, n, 1.0)
+    freq_rows, freq = _number_or_rows("frequency", frequency, n, 0.0)
+    pres_rows, pres = _number_or_rows("presence", presence, n, 0.0)
     if (bias_ids is None) != (bias_values is None):
         raise ValueError("bias_ids and bias_values belong together")
     if bias_ids is not None:
@@ -915,20 +915,21 @@ def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, freq
         _need(bias_ids, torch.int64, "bias_ids", (n, b))
         _need(bias_values, torch.float32, "bias_values", (n, b))
         if b > 0:
-            p.bias_ids, p.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
-            p.bias_count = b
+            bias, values, biases = bias_ids.data_ptr(), bias_values.data_ptr(), b
     if allowed is not None:
         if allowed.dtype is not torch.int32:
             raise TypeError("allowed must be int32, got %s" % allowed.dtype)
-        rows, words, p.allowed_stride = _need_rows(allowed, "allowed")
-        if rows != n or words < (v + 31) // 32:
+        rows, have, words_stride = _need_rows(allowed, "allowed")
+        if rows != n or have < (v + 31) // 32:
             raise ValueError("allowed must be [%d, >= %d], got %s"
                              % (n, (v + 31) // 32, tuple(allowed.shape)))
-        p.allowed = allowed.data_ptr()
+        words = allowed.data_ptr()
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
+    params = ProcessParams(tok, full, prompt, width, tok_stride, rep_rows, freq_rows, pres_rows,
+                           rep, freq, pres, bias, values, biases, words, words_stride)
     st = load().rlk_process_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
-                                   _ptr(active_mask), ctypes.byref(p), _ptr(out), out_stride,
+                                   _ptr(active_mask), ctypes.byref(params), _ptr(out), out_stride,
                                    _ptr(device_error_word), _stream(stream))
     _check("rlk_process_logits", st)
 

@@ -955,7 +955,6 @@ rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, in
     a.N = static_cast<int>(N), a.V = static_cast<int>(V);
     a.width = history ? static_cast<int>(p.tokens_width) : 0;
     a.bias = static_cast<int>(p.bias_count);
-    a.x_vec = rows_vec(logits, row_stride, es), a.out_vec = rows_vec(out, out_stride, es);
     a.err = device_error_word;
     RLK_CUDA(rlk::launch_process(a, dtype == RLK_DTYPE_BF16, stream));
     return RLK_OK;

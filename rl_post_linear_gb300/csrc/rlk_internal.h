@@ -405,7 +405,6 @@ struct ProcessArgs {
     const int32_t* allowed;    // or nullptr
     int64_t allowed_stride;
     int N, V, width, bias;
-    bool x_vec, out_vec;       // rows start on 16 bytes
     uint32_t* err;
 };
 cudaError_t launch_process(const ProcessArgs& args, bool bf16, cudaStream_t stream);

@@ -132,6 +132,57 @@ def test_strides_and_in_place(pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("length", [90, 4091, 4096, 9000])
+def test_many_rows(length, dtype):
+    # a copy and a launch for the listed columns: by hashing for short rows, in ranges for others
+    n, v = 400, 70001
+    t, full, prompt = history(n, v, length, length, 0.05)
+    if length > 5000:
+        full[7:390] %= 97
+        prompt = torch.minimum(prompt, full)
+    g = gen(length + 1)
+    ids = torch.randint(-1, v, (n, 5), generator=g).to(dev())
+    vals = torch.randn(n, 5, generator=g).to(dev())
+    x = logits(n, v, 30, dtype)
+    mask = (torch.arange(n) % 5 != 4).to(torch.uint8).to(dev())
+    mask[10:380] = 0
+    mask[100] = 1
+    allow = (torch.rand(n, v, generator=g) < 0.5).to(dev())
+    out = torch.full((n, v), 3.0, dtype=dtype, device=dev())
+    want = check(x, t, full, prompt, 1.2, 0.3, -0.1, ids, vals, allow, mask, out)
+    assert bool((want[mask == 0] == 3.0).all())
+    same = x.clone()
+    check(same, t, full, prompt, 1.2, 0.3, -0.1, ids, vals, allow, mask, same)
+    assert same_bits(same[mask != 0], want[mask != 0]) and same_bits(same[mask == 0], x[mask == 0])
+    # as each row by itself
+    for i in (0, 1, 2, 3, 100, n - 1):
+        if int(mask[i]):
+            one = rlk.process_logits(x[i:i + 1].clone(), t[i:i + 1], full[i:i + 1],
+                                     prompt[i:i + 1], 1.2, 0.3, -0.1, ids[i:i + 1],
+                                     vals[i:i + 1], pack(allow[i:i + 1]))
+            assert same_bits(one[0], want[i])
+    again = rlk.process_logits(x, t, full, prompt, 1.2, 0.3, -0.1, ids, vals, None, mask)
+    in_place = x.clone()
+    rlk.process_logits(in_place, t, full, prompt, 1.2, 0.3, -0.1, ids, vals, None, mask, in_place)
+    assert same_bits(in_place[mask != 0], again[mask != 0])
+
+
+def test_a_row_that_cannot_be_among_many():
+    n, v = 500, 60000
+    x = logits(n, v, 31, torch.float32)
+    t = torch.randint(0, v, (n, 50), generator=gen(32)).to(dev())
+    full = torch.full((n,), 50, device=dev())
+    t[3, 49], full[400] = v, 51
+    for out in (None, x.clone()):
+        err = torch.zeros(1, dtype=torch.int32, device=dev())
+        src = x if out is None else out
+        y = rlk.process_logits(src, t, full, presence=1.0, out=out, error_word=err)
+        assert int(err.item()) == rlk.RLK_DEVERR_TARGET_RANGE | rlk.RLK_DEVERR_SAMPLE_PARAM
+        bad = torch.isnan(y).any(1)
+        assert bad.nonzero()[:, 0].tolist() == [3, 400] and bool(torch.isnan(y[[3, 400]]).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_settings_of_each_row(dtype):
     n, v = 40, 3001
     t, full, prompt = history(n, v, 700, 6)
@@ -158,6 +209,17 @@ def test_long_histories_and_repeats():
     check(logits(3, v, 9, torch.float32), t, None, None, 1.1, 0.01, 0.2)
     check(logits(3, v, 10, torch.float32), t, None,
           torch.tensor([50000, 0, 25000], device=dev()), 1.1, 0.01, 0.2)
+
+
+@pytest.mark.parametrize("b", [1, 2, 3, 64, 255, 256, 257, 300, 512, 513, 1025, 4096])
+def test_numbers_of_biases(b):
+    n, v = 3, 30011
+    g = gen(b)
+    ids = torch.randint(-1, v, (n, b), generator=g).to(dev())
+    vals = torch.randn(n, b, generator=g).to(dev())
+    t, full, prompt = history(n, v, 50, b + 1)
+    for dtype in DTYPES:
+        check(logits(n, v, b + 2, dtype), t, full, prompt, 1.1, 0.2, 0.1, ids, vals)
 
 
 def test_many_biases_of_one_token():
