@@ -995,7 +995,7 @@ size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, i
 
 size_t rlk_linear_topk_kl_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K) {
     if (N < 0 || H < 0 || V < 1 || K < 1) return 0;
-    return rlk::TopkKlBwdLayout(N, H, K).total;
+    return rlk::TopkKlBwdLayout(N, H, V, K).total;
 }
 
 rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
@@ -1065,7 +1065,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
                                     cudaStream_t stream) {
     RLK_TRY(check_shape(N, H, V, temperature));
     if (K < 1) return RLK_ERR_INVALID_VALUE;
-    if (K > rlk::kMaxTopK) return RLK_ERR_UNSUPPORTED;
+    if (K > rlk::kMaxTopK || N * K > kMaxDim) return RLK_ERR_UNSUPPORTED;
     if (N == 0) return RLK_OK;
     if (hidden == nullptr || weight == nullptr || teacher_ids == nullptr ||
         teacher_logp == nullptr || grad_kl == nullptr || lse == nullptr || logp == nullptr ||
@@ -1076,7 +1076,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
         !aligned(grad_kl, 4) || !aligned(lse, 4) || !aligned(logp, 4) ||
         !aligned(device_error_word, 4))
         return RLK_ERR_INVALID_VALUE;
-    const rlk::TopkKlBwdLayout lay(N, H, K);
+    const rlk::TopkKlBwdLayout lay(N, H, V, K);
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < lay.total)
         return RLK_ERR_WORKSPACE;
     DeviceInfo dev;
@@ -1115,13 +1115,16 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
     st.temp = static_cast<float>(temperature);
     st.V_global = v;
     st.round_last = true;
-    st.hilo = true;
     st.topk = true;
     st.K = static_cast<int>(K);
     int* ids = reinterpret_cast<int*>(ws + lay.ids_off);
     float* val = reinterpret_cast<float*>(ws + lay.val_off);
     st.topk_ids = ids;
     st.topk_val = val;
+    st.gemm_rows = gemm_rows;
+    st.sorted_dy = reinterpret_cast<int*>(ws + lay.sorted_dy_off);
+    st.sorted_dt = reinterpret_cast<int*>(ws + lay.sorted_dt_off);
+    st.tiles = reinterpret_cast<uint64_t*>(ws + lay.tiles_off);
     st.dh_acc = reinterpret_cast<float*>(ws + lay.dhacc_off);
     st.ycoef = reinterpret_cast<float*>(ws + lay.ycoef_off);
     st.dom = reinterpret_cast<int*>(ws + lay.dom_off);
@@ -1133,7 +1136,17 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
                                renormalize != 0};
     RLK_CUDA(rlk::launch_topk_coef(slots, grad_kl, logp, st.rows, st.n_rows, st.temp, st.ycoef,
                                    ids, val, device_error_word, stream));
-    // no entry is split off as a row's dominant class (all bits set: -1)
+    // dh depends on V here, not on N: its rows are those of any batch
+    st.hilo = lay.lo;
+    st.dh_started = V > rlk::kTopkSmallV;
+    if (st.dh_started)
+        RLK_CUDA(rlk::launch_topk_dh(ids, val, st.n_rows, n, st.K, weight, h, st.dh_acc, stream));
+    rlk::TopkRows rows_of{};
+    if (!lay.lo) {
+        RLK_CUDA(rlk::launch_topk_sort(lay, ws, st.n_rows, n, st.K, v, &rows_of, stream));
+        st.rows_of = &rows_of;
+    }
+    // no dominant class yet (all bits set: -1), and none in any chunk
     RLK_CUDA(cudaMemsetAsync(st.dom, 0xff, static_cast<size_t>(N) * sizeof(int), stream));
     RLK_CUDA(cudaMemsetAsync(st.dom_flags, 0, static_cast<size_t>(st.num_chunks) * sizeof(int),
                              stream));

@@ -524,19 +524,27 @@ struct DsKlPolicy {
 // ----------------------------------------------------------------------------- dS_c for top-K KL
 //
 // dS[t,v] = (g_t / T) (Q_t p[t,v] - q[t,v]): this GEMM writes the first term, with
-// coef_t = g_t Q_t / T from the launch before it, as hi and lo bf16 planes.  The entries
-// at the teacher's tokens, at most K a row, are then overwritten (launch_topk_scatter):
-// near a student that agrees with its teacher they are differences of near numbers, so
-// they are formed whole in fp32 and rounded once.
-struct DsTopkPolicy : SingleRole<false, false> {
+// coef_t = g_t Q_t / T from the launch before it, in bf16.  The entries at the teacher's tokens, at
+// most K a row and most of its gradient, are then overwritten whole (launch_topk_scatter), and what
+// their rounding to bf16 leaves goes into dh, and as a sum for each vocabulary row into dW, in fp32
+// (topk_kl.cu): without it the rounding costs as much accuracy as that of the outputs.  So would a
+// class with p > 1/2 that the teacher does not list; it takes the logp backward's way for dominant
+// classes.  LO: a second plane holds what the rounding leaves of every entry (as for the entropy),
+// for dW where that costs less, for both where V is small.
+template <bool LO>
+struct DsTopkPolicyT : SingleRole<false, false> {
     static constexpr bool kCtaPair = true;
-    static constexpr int kLd = 2 * kBwdChunk;
+    static constexpr int kLd = LO ? 2 * kBwdChunk : kBwdChunk;   // dS row stride
 
     const float* lse;         // [N] by token
     const float* coef;        // [N] by GEMM row
+    const int* ids;           // [N][K] by GEMM row, -1: none
     __nv_bfloat16* ds;
+    int* dom;                 // [N] by token
+    float* dcoef;
+    int* dom_flag;
     RowMap rm;
-    int N, V, c0, num_m, num_n, kblocks;
+    int N, V, K, c0, num_m, num_n, kblocks;
     float k;
 
     __device__ int num_units() const { return rm.tiles(N) * num_n; }
@@ -556,6 +564,7 @@ struct DsTopkPolicy : SingleRole<false, false> {
 
     struct EpiState {
         float coef, lse2;
+        int t;
         bool live;
     };
 
@@ -565,7 +574,8 @@ struct DsTopkPolicy : SingleRole<false, false> {
         const int i = m * kUnitM + row;
         st.coef = i < rm.count(N) ? coef[i] : 0.f;
         st.live = st.coef != 0.f;        // rows without weight stay 0, whatever their logits
-        st.lse2 = st.live ? lse[rm.token(i)] * kLog2e : 0.f;
+        st.t = st.live ? rm.token(i) : 0;
+        st.lse2 = st.live ? lse[st.t] * kLog2e : 0.f;
     }
 
     __device__ void epi_tile(int u, int, int row, uint32_t taddr, EpiState& st) const {
@@ -579,25 +589,68 @@ struct DsTopkPolicy : SingleRole<false, false> {
             if (i >= N) continue;
             const int col = n * kTileV + cc * 32;   // column inside the chunk
             const int vb = c0 + col;
-            uint32_t packed[16], packed_lo[16];
+            const bool full = vb + 32 <= V;         // no column of the slice is past V
+            float x[32];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float d0 = st.coef * ex2_approx(fmaf(__uint_as_float(r[2 * j]), k, -st.lse2));
-                float d1 = st.coef * ex2_approx(fmaf(__uint_as_float(r[2 * j + 1]), k, -st.lse2));
-                if (!st.live || vb + 2 * j >= V) d0 = 0.f;
-                if (!st.live || vb + 2 * j + 1 >= V) d1 = 0.f;
-                packed[j] = pack_bf16x2(d0, d1);
-                packed_lo[j] = pack_lo_bf16x2(d0, d1, packed[j]);
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            int ai = 32;                            // a dominant class that is not listed
+            if (st.live) {
+                float cm = -INFINITY;
+                if (full) {
+                    cm = fmaxf(cm, max32(x));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) cm = (vb + j < V) ? fmaxf(cm, x[j]) : cm;
+                }
+                const float l2 = fmaf(cm, k, -st.lse2);
+                if (l2 > -0.99f) {                  // at most one entry of a row
+                    int idx = 31;
+#pragma unroll
+                    for (int j = 31; j >= 0; --j) idx = (x[j] == cm && vb + j < V) ? j : idx;
+                    bool listed = false;
+                    const int* mine = ids + static_cast<size_t>(i) * K;
+                    for (int j = 0; j < K; ++j) listed |= mine[j] == vb + idx;
+                    if (!listed) {
+                        ai = idx;
+                        dom[st.t] = vb + idx;
+                        dcoef[st.t] = st.coef * ex2_approx(l2);
+                        atomicOr(dom_flag, 1);
+                    }
+                }
             }
-            uint4* hi = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + col);
-            uint4* lo = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + kBwdChunk +
-                                                 col);
+            uint32_t packed[16], packed_lo[LO ? 16 : 1];
+            if (full && ai == 32 && st.live) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                hi[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
-                                   packed[4 * w + 3]);
-                lo[w] = make_uint4(packed_lo[4 * w], packed_lo[4 * w + 1], packed_lo[4 * w + 2],
-                                   packed_lo[4 * w + 3]);
+                for (int j = 0; j < 16; ++j) {
+                    const float d0 = st.coef * ex2_approx(fmaf(x[2 * j], k, -st.lse2));
+                    const float d1 = st.coef * ex2_approx(fmaf(x[2 * j + 1], k, -st.lse2));
+                    packed[j] = pack_bf16x2(d0, d1);
+                    if constexpr (LO) packed_lo[j] = pack_lo_bf16x2(d0, d1, packed[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float d[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int at = 2 * j + e;
+                        d[e] = st.live && vb + at < V && ai != at
+                                   ? st.coef * ex2_approx(fmaf(x[at], k, -st.lse2)) : 0.f;
+                    }
+                    packed[j] = pack_bf16x2(d[0], d[1]);
+                    if constexpr (LO) packed_lo[j] = pack_lo_bf16x2(d[0], d[1], packed[j]);
+                }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + col);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                dst[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
+                                    packed[4 * w + 3]);
+            if constexpr (LO) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    dst[kBwdChunk / 8 + w] = make_uint4(packed_lo[4 * w], packed_lo[4 * w + 1],
+                                                        packed_lo[4 * w + 2], packed_lo[4 * w + 3]);
             }
         }
     }
@@ -778,7 +831,10 @@ struct DhPolicy : SingleRole<false, true> {
 // dS_c^T: vocab (M) contiguous, tokens along K; h: hidden (N) contiguous.
 // hilo: the K loop runs over the tokens of the hi plane of dS, then over the
 // same tokens of the lo plane (kBwdChunk columns further on), against h twice.
-struct DwPolicy : SingleRole<true, true> {
+// ROWS: rows of the chunk may have a sum that is added before the rounding (of what bf16 left of
+// entries of dS, 2^-9 of them, so bf16 itself).
+template <bool ROWS>
+struct DwPolicyT : SingleRole<true, true> {
     static constexpr bool kKRemap = true;
     static constexpr bool kCtaPair = true;       // 256-vocab-row tiles on a CTA pair
 
@@ -793,6 +849,8 @@ struct DwPolicy : SingleRole<true, true> {
     const int* dom_flag;           // 0: no dominant class in this chunk (the list was not built)
     const float* dcoef;            // [N] fp32 coefficient of each token's dominant class
     float* dw_out32;               // non-null: dW rows go here in fp32, unrounded [V][H]
+    const int* row_at;             // ROWS: [V] a row's place in row_sum, or -1
+    const __nv_bfloat16* row_sum;  // ROWS: [places][H]
     RowMap rm;                     // compaction: K runs over the compacted rows only
     int N, H, c0, width, num_m, num_n, kblocks;
     float temp;
@@ -829,6 +887,7 @@ struct DwPolicy : SingleRole<true, true> {
     struct EpiState {
         int lo, hi, dlo, dhi, v;
         bool valid;
+        const uint4* sum;          // ROWS: the row's sum, or nullptr
     };
 
     // [lo, hi): the entries of an ascending list equal to v
@@ -851,7 +910,12 @@ struct DwPolicy : SingleRole<true, true> {
         st.valid = vl < width;
         st.v = c0 + vl;
         st.lo = st.hi = st.dlo = st.dhi = 0;
+        st.sum = nullptr;
         if (!st.valid) return;
+        if constexpr (ROWS) {
+            const int at = row_at[st.v];
+            if (at >= 0) st.sum = reinterpret_cast<const uint4*>(row_sum + static_cast<size_t>(at) * H);
+        }
         if (terms) equal_range(sorted_y, N, st.v, st.lo, st.hi);
         if (*dom_flag != 0) equal_range(sorted_dy, N, st.v, st.dlo, st.dhi);
     }
@@ -859,6 +923,15 @@ struct DwPolicy : SingleRole<true, true> {
     __device__ void epi_tile(int u, int, int, uint32_t taddr, EpiState& st) const {
         int m, n;
         unit(u, m, n);
+        uint4 sum[ROWS ? 4 : 1];                   // of the next slice, on its way
+        const auto fetch = [&](int col) {
+            if constexpr (ROWS) {
+                if (st.sum == nullptr || col >= H) return;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
+            }
+        };
+        fetch(n * kTileV);
 #pragma unroll 1
         for (int cc = 0; cc < kTileV / 32; ++cc) {
             uint32_t r[32];
@@ -868,6 +941,18 @@ struct DwPolicy : SingleRole<true, true> {
             float x[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            if constexpr (ROWS) {
+                if (st.sum != nullptr) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float add[8];
+                        bf16x8_to_f32(sum[q], add);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[8 * q + j] += add[j];
+                    }
+                }
+                if (cc + 1 < kTileV / 32) fetch(col + 32);
+            }
             for (int i = st.lo; i < st.hi; ++i) {
                 const int t = sorted_t[i];
                 const float coef = __fdiv_rn(grad[t], temp) * ycoef[t];
@@ -1098,6 +1183,65 @@ static cudaError_t launch_ds(const BwdStepMaps& maps, const BwdStep& st, int c0,
                        stream);
 }
 
+template <bool ROWS>
+static cudaError_t launch_dw(const BwdStepMaps& maps, const BwdStep& st, int c0, int width,
+                             int num_sms, uint32_t* err, cudaStream_t stream) {
+    const int N = st.N, H = st.H;
+    DwPolicyT<ROWS> pw;
+    pw.grad = st.grad;
+    pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
+    pw.dw = static_cast<__nv_bfloat16*>(st.dweight);
+    pw.sorted_y = st.sorted_y;
+    pw.sorted_t = st.sorted_t;
+    pw.ycoef = st.ycoef;
+    pw.sorted_dy = st.sorted_dy;
+    pw.sorted_dt = st.sorted_dt;
+    pw.dom_flag = st.dom_flags + st.chunk;
+    pw.dcoef = st.dcoef;
+    pw.dw_out32 = st.dw_out32;
+    pw.row_at = ROWS ? st.rows_of->row_at : nullptr;
+    pw.row_sum = ROWS ? static_cast<const __nv_bfloat16*>(st.rows_of->sums) : nullptr;
+    pw.rm = RowMap{st.rows, st.n_rows};
+    pw.N = N;
+    pw.H = H;
+    pw.c0 = c0;
+    pw.width = width;
+    pw.num_m = (width + kUnitM - 1) / kUnitM;
+    pw.num_n = (H + kTileV - 1) / kTileV;
+    pw.kblocks = (N + 63) / 64;
+    pw.temp = st.temp;
+    pw.terms = !st.kl && !st.topk;
+    pw.hilo = st.hilo;
+    // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
+    // writes only dW, which the dh GEMM does not touch
+    return launch_gemm(maps.ds_mnmajor, maps.h_mnmajor, pw, pw.num_m * pw.num_n, num_sms, err,
+                       stream, kPdlOverlap);
+}
+
+template <bool LO>
+static cudaError_t launch_ds_topk(const BwdStepMaps& maps, const BwdStep& st, int c0, int width,
+                                  int num_sms, uint32_t* err, cudaStream_t stream) {
+    DsTopkPolicyT<LO> ps;
+    ps.lse = st.lse;
+    ps.coef = st.ycoef;
+    ps.ids = st.topk_ids;
+    ps.dom = st.dom;
+    ps.dcoef = st.dcoef;
+    ps.dom_flag = st.dom_flags + st.chunk;
+    ps.K = st.K;
+    ps.ds = static_cast<__nv_bfloat16*>(st.ds);
+    ps.rm = RowMap{st.rows, st.n_rows};
+    ps.N = st.N;
+    ps.V = st.V;
+    ps.c0 = c0;
+    ps.num_m = (st.N + kUnitM - 1) / kUnitM;
+    ps.num_n = (width + kTileV - 1) / kTileV;
+    ps.kblocks = st.H / 64;
+    ps.k = st.k;
+    return launch_gemm(maps.h_kmajor, maps.w_kmajor_pair, ps, ps.num_m * ps.num_n, num_sms, err,
+                       stream);
+}
+
 cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_sms, uint32_t* err,
                             cudaStream_t stream) {
     const int N = st.N, H = st.H, V = st.V;
@@ -1134,23 +1278,18 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
                                st.sorted_dy, st.sorted_dt, stream);
     }
     if (st.role == kRoleDs && st.topk) {
-        DsTopkPolicy ps;
-        ps.lse = st.lse;
-        ps.coef = st.ycoef;
-        ps.ds = static_cast<__nv_bfloat16*>(st.ds);
-        ps.rm = RowMap{st.rows, st.n_rows};
-        ps.N = N;
-        ps.V = V;
-        ps.c0 = c0;
-        ps.num_m = (N + kUnitM - 1) / kUnitM;
-        ps.num_n = (width + kTileV - 1) / kTileV;
-        ps.kblocks = H / 64;
-        ps.k = st.k;
-        const cudaError_t e = launch_gemm(maps.h_kmajor, maps.w_kmajor_pair, ps,
-                                          ps.num_m * ps.num_n, num_sms, err, stream);
+        cudaError_t e = st.hilo ? launch_ds_topk<true>(maps, st, c0, width, num_sms, err, stream)
+                                : launch_ds_topk<false>(maps, st, c0, width, num_sms, err, stream);
         if (e != cudaSuccess) return e;
-        return launch_topk_scatter(st.topk_ids, st.topk_val, st.n_rows, N, st.K, c0, width, st.ds,
-                                   stream);
+        e = launch_topk_scatter(st.topk_ids, st.topk_val, st.n_rows, N, st.K, c0, width, st.ds,
+                                st.hilo, stream);
+        if (e != cudaSuccess) return e;
+        if (st.rows_of != nullptr) {
+            e = launch_topk_rows(*st.rows_of, st.chunk, st.gemm_rows, H, stream);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_dom_sort(st.dom, N, V, c0, c0 + width, st.dom_flags + st.chunk, st.tiles,
+                               st.sorted_dy, st.sorted_dt, stream);
     }
     if (st.role == kRoleDs) {
         const cudaError_t e =
@@ -1184,43 +1323,18 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pd.num_m = (N + kUnitM - 1) / kUnitM;
         pd.num_n = (H + kTileV - 1) / kTileV;
         pd.kblocks = (width + 63) / 64;
-        pd.first = st.chunk == 0;
+        pd.first = st.chunk == 0 && !st.dh_started;
         pd.last = st.chunk == st.num_chunks - 1;
         pd.temp = st.temp;
         pd.terms = !st.kl && !st.topk;
-        pd.hilo = st.hilo;
+        pd.hilo = st.hilo && !st.dh_started;
         // the dW GEMM that follows overlaps this one's last wave (with 6.7 waves of dh
         // units at N = 8192, a quarter of the CTA pairs would otherwise idle for a unit)
         return launch_gemm(maps.ds_kmajor, maps.w_mnmajor, pd, pd.num_m * pd.num_n, num_sms, err,
                            stream, kPdlTrigger);
     }
-    DwPolicy pw;
-    pw.grad = st.grad;
-    pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
-    pw.dw = static_cast<__nv_bfloat16*>(st.dweight);
-    pw.sorted_y = st.sorted_y;
-    pw.sorted_t = st.sorted_t;
-    pw.ycoef = st.ycoef;
-    pw.sorted_dy = st.sorted_dy;
-    pw.sorted_dt = st.sorted_dt;
-    pw.dom_flag = st.dom_flags + st.chunk;
-    pw.dcoef = st.dcoef;
-    pw.dw_out32 = st.dw_out32;
-    pw.rm = RowMap{st.rows, st.n_rows};
-    pw.N = N;
-    pw.H = H;
-    pw.c0 = c0;
-    pw.width = width;
-    pw.num_m = (width + kUnitM - 1) / kUnitM;
-    pw.num_n = (H + kTileV - 1) / kTileV;
-    pw.kblocks = (N + 63) / 64;
-    pw.temp = st.temp;
-    pw.terms = !st.kl && !st.topk;
-    pw.hilo = st.hilo;
-    // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
-    // writes only dW, which the dh GEMM does not touch
-    return launch_gemm(maps.ds_mnmajor, maps.h_mnmajor, pw, pw.num_m * pw.num_n, num_sms, err,
-                       stream, kPdlOverlap);
+    return st.rows_of != nullptr ? launch_dw<true>(maps, st, c0, width, num_sms, err, stream)
+                                 : launch_dw<false>(maps, st, c0, width, num_sms, err, stream);
 }
 
 // ----------------------------------------------------------------------------- dh merge

@@ -96,13 +96,52 @@ struct BwdLayout {
     }
 };
 
-// The same with the entries of dS at the teacher's K tokens of each row behind it.
+// Top-K KL: the entries of dS at the teacher's tokens (coefficient by slot).  What their rounding to
+// bf16 leaves reaches dW either as a second plane of dS (lo) or as a sum for each vocabulary row:
+// then also their list by token id, radix-sorted (id, slot) pairs, of which come each entry's GEMM
+// row and remainder; a vocabulary row's range of the list; each chunk's rows that have one, those
+// with many apart, and their sums.
+constexpr int kRadixBits = 9, kRadixTile = 2048;
+constexpr int kTopkSmallV = 8192;
+// The lo plane doubles the dW GEMM, 2 N H V at 1.7 PFLOP/s.  The sums move 4 bytes a column of each
+// row that has any at 6 TB/s, read 2 of h for each entry at 8 TB/s from L2, and take 70 us of
+// launches for their list (H = 4096, V = 151936, K = 64: equal at N = 500; N = 2048: XXX).  A small
+// vocabulary, of which a few classes that are not listed may carry much of a row, has the plane
+// for dh too.
+inline bool topk_lo_plane(int64_t N, int64_t H, int64_t V, int64_t K) {
+    if (V <= kTopkSmallV) return true;
+    const double e = static_cast<double>(N) * static_cast<double>(K);
+    const double rows = e < static_cast<double>(V) ? e : static_cast<double>(V);
+    const double sums = (rows * 4 / 6e12 + e * 2 / 8e12) * static_cast<double>(H) + 70e-6;
+    return 2.0 * static_cast<double>(N) * static_cast<double>(H) * static_cast<double>(V) / 1.7e15 < sums;
+}
 struct TopkKlBwdLayout : BwdLayout {
-    size_t ids_off, val_off;
-    TopkKlBwdLayout(int64_t N, int64_t H, int64_t K) : BwdLayout(N, H, true) {
+    bool lo;
+    int64_t tiles, places;
+    size_t ids_off, val_off, key_off[2], slot_off[2], hist_off, first_off, last_off, at_off,
+        list_off, many_off, counts_off, sums_off;
+    TopkKlBwdLayout(int64_t N, int64_t H, int64_t V, int64_t K)
+        : BwdLayout(N, H, topk_lo_plane(N, H, V, K)), lo(topk_lo_plane(N, H, V, K)) {
+        const size_t e = static_cast<size_t>(N) * K, v = static_cast<size_t>(V);
+        tiles = static_cast<int64_t>((e + kRadixTile - 1) / kRadixTile);
+        places = static_cast<int64_t>(e < kBwdChunk ? e : kBwdChunk);
         ids_off = total;
-        val_off = align_up(ids_off + static_cast<size_t>(N) * K * 4, 256);
-        total = align_up(val_off + static_cast<size_t>(N) * K * 4, 256);
+        val_off = align_up(ids_off + e * 4, 256);
+        total = align_up(val_off + e * 4, 256);
+        if (lo) return;
+        key_off[0] = total;
+        key_off[1] = align_up(key_off[0] + e * 4, 256);
+        slot_off[0] = align_up(key_off[1] + e * 4, 256);
+        slot_off[1] = align_up(slot_off[0] + e * 4, 256);
+        hist_off = align_up(slot_off[1] + e * 4, 256);
+        first_off = align_up(hist_off + static_cast<size_t>(tiles) * 4 * (1 << kRadixBits), 256);
+        last_off = align_up(first_off + v * 4, 256);
+        at_off = align_up(last_off + v * 4, 256);
+        list_off = align_up(at_off + v * 4, 256);
+        many_off = align_up(list_off + v * 4, 256);
+        counts_off = align_up(many_off + v * 4, 256);
+        sums_off = align_up(counts_off + static_cast<size_t>(kMaxBwdChunks) * 8, 256);
+        total = align_up(sums_off + static_cast<size_t>(places) * H * 2, 256);
     }
 };
 
@@ -211,6 +250,19 @@ struct BwdStepMaps {
 // One launch of the backward: a role (the dS recompute, the dh GEMM or the dW
 // GEMM) over one vocabulary chunk.
 constexpr int kRoleDs = 0, kRoleDh = 1, kRoleDw = 2;
+// The listed entries by vocabulary row, for dW.
+struct TopkRows {
+    const int* entry_row;      // [E] GEMM row of each entry, by token id and row
+    const float* entry_rest;   // [E] what bf16 leaves of it
+    const int* first;          // [V] a row's range of them (empty: last = 0)
+    const int* last;
+    const int* row_at;         // [V] its place in sums, or -1
+    const int* list;           // [V] each chunk's rows that have entries
+    const int* many;           // [V] and places of those that have many
+    const int2* counts;        // [chunks] of both
+    void* sums;                // [places][H] bf16, of one chunk at a time
+    int places;
+};
 struct BwdStep {
     const int64_t* targets;
     const uint8_t* mask;
@@ -240,9 +292,12 @@ struct BwdStep {
     bool hilo;                 // dS as hi and lo bf16 planes [N, 2 kBwdChunk] (entropy, KL, top-K)
     // KL against a teacher's top tokens (topk = true): ycoef holds g Q / T by GEMM row
     bool topk;
+    bool dh_started;           // dh_acc holds what bf16 leaves of the listed entries; dh takes one plane
     int K;
     const int* topk_ids;       // [N][K] by GEMM row: distinct token ids, -1: no entry
     const float* topk_val;     // [N][K] their whole entries of dS
+    const void* gemm_rows;     // [N][H]
+    const TopkRows* rows_of;   // or nullptr: dS has a lo plane
     void* ds;                  // dS [N, kBwdChunk] bf16 of the chunk (hilo: [N, 2 kBwdChunk])
     float* dh_acc;
     const int* sorted_y;
@@ -462,8 +517,18 @@ cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, in
 cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const float* logp,
                              const int* rows, const int* n_rows, float temp, float* coef,
                              int* ids, float* val, uint32_t* err, cudaStream_t stream);
+// what bf16 leaves of the entries in dh: dh_acc[i] = sum_k rest(val[i,k]) W[id[i,k]]
+cudaError_t launch_topk_dh(const int* ids, const float* val, const int* n_rows, int N, int K,
+                           const void* weight, int H, float* dh_acc, cudaStream_t stream);
+// the entries by token id
+cudaError_t launch_topk_sort(const TopkKlBwdLayout& lay, uint8_t* ws, const int* n_rows, int N, int K,
+                             int V, TopkRows* out, cudaStream_t stream);
+// sums[row_at[v]] = sum of rest h over the entries of v, for the chunk's rows
+cudaError_t launch_topk_rows(const TopkRows& rows, int chunk, const void* hidden, int H,
+                             cudaStream_t stream);
+// the entries of dS at the listed tokens (lo: and what bf16 leaves of them in its second plane)
 cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,
-                                int c0, int width, void* ds, cudaStream_t stream);
+                                int c0, int width, void* ds, bool lo, cudaStream_t stream);
 
 // Device address (current device and context) of the library-owned audit scratch.
 cudaError_t audit_noalloc_scratch(void** parts);
