@@ -331,6 +331,7 @@ struct DsKlMaps {
 struct DsKlPolicy {
     using Maps = DsKlMaps;
     static constexpr bool kPairTiles = true;
+    static constexpr bool kTileK = false;
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = true;    // 256-token units on a CTA pair
     static constexpr int kEpiWarps = 8;       // two column halves per row
@@ -826,6 +827,177 @@ struct DhPolicy : SingleRole<false, true> {
     __device__ void epi_end(int, int, EpiState&) const {}
 };
 
+// ----------------------------------------------------------------------------- dh for top-K KL
+//
+// The chunk's product in sub-chunks of kDhSub vocabulary columns, each accumulated by itself from
+// 0 and added to dh_acc in fp32, ascending: a fixed order.  With many tiles a unit is a tile of dh
+// and walks its sub-chunks (the additions overlap the next one's MMAs).  With few, most CTA pairs
+// would idle: a unit is then one sub-chunk of a tile, written to `part`, and dh_sum_kernel adds them
+// in the same order, so that a row's bits do not depend on the batch (a step of [200, 2048] against
+// V = 32003: 242 instead of 341 us).
+constexpr int kDhSub = kBwdChunk / kDhSubs;       // 4096
+struct DhTopkPolicy : SingleRole<false, true> {
+    static constexpr bool kKRemap = true;
+    static constexpr bool kTileK = true;
+    static constexpr bool kCtaPair = true;
+
+    float* dh_acc;                 // [N][H]
+    float* part;                   // split: [sub-chunks][N][H]
+    __nv_bfloat16* dh;             // [N][H] by token
+    const __nv_bfloat16* weight;   // [V][H]
+    const int* dom;                // [N] by token
+    const float* dcoef;
+    RowMap rm;
+    int N, H, c0, width, num_n, subs;
+    bool first, last, hilo, split;
+
+    __device__ int num_units() const { return rm.tiles(N) * num_n * (split ? subs : 1); }
+    __device__ int tiles_in_unit(int) const { return split ? 1 : subs; }
+    // unit -> (token tile m, hidden tile n, its first sub-chunk)
+    __device__ void unit(int u, int& m, int& n, int& s) const {
+        const int tiles = rm.tiles(N) * num_n;
+        s = u / tiles;
+        const int t = u - s * tiles;
+        m = t / num_n;
+        n = t - m * num_n;
+    }
+    __device__ int sub_blocks(int s) const { return (min(kDhSub, width - s * kDhSub) + 63) / 64; }
+    __device__ int tile_k_blocks(int u, int q) const {
+        int m, n, s;
+        unit(u, m, n, s);
+        return sub_blocks(s + q) * (hilo ? 2 : 1);
+    }
+    __device__ int k_blocks(int u) const { return tile_k_blocks(u, 0); }
+    __device__ void coords(int u, int q, int& a_mn, int& a_k, int& b_mn, int& b_k) const {
+        int m, n, s;
+        unit(u, m, n, s);
+        a_mn = m * kUnitM;
+        a_k = (s + q) * kDhSub;
+        b_mn = n * kTileV;
+        b_k = c0 + (s + q) * kDhSub;
+    }
+    // the lo plane behind the hi plane, against the same rows of W
+    __device__ void k_remap(int kb, int nkb, int&, int& a_k, int&, int& b_k) const {
+        if (hilo && kb >= nkb / 2) {
+            a_k += kBwdChunk - nkb / 2 * kBK;
+            b_k -= nkb / 2 * kBK;
+        }
+    }
+
+    struct EpiState {
+        int t, s, dom;
+        float coef_dom;
+    };
+
+    __device__ void epi_begin(int u, int row, EpiState& st) const {
+        int m, n;
+        unit(u, m, n, st.s);
+        const int i = m * kUnitM + row;
+        st.t = i < rm.count(N) ? rm.token(i) : N;
+        st.dom = st.t < N && last && !split ? dom[st.t] : -1;
+        st.coef_dom = st.dom >= 0 ? dcoef[st.t] : 0.f;
+    }
+
+    __device__ void epi_tile(int u, int q, int row, uint32_t taddr, EpiState& st) const {
+        int m, n, s;
+        unit(u, m, n, s);
+        const int i = m * kUnitM + row;
+        const bool start = split || (first && q == 0), end = !split && last && q == subs - 1;
+        float* to = (split ? part + static_cast<size_t>(s) * N * H : dh_acc) +
+                    static_cast<size_t>(i) * H;
+        float4 old[8];                             // of the next slice, on its way
+        const auto fetch = [&](int col) {
+            if (start || st.t >= N || col >= H) return;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) old[j] = reinterpret_cast<const float4*>(to + col)[j];
+        };
+        fetch(n * kTileV);
+#pragma unroll 1
+        for (int cc = 0; cc < kTileV / 32; ++cc) {
+            uint32_t r[32];
+            tmem_load_32(taddr + cc * 32, r);
+            const int col = n * kTileV + cc * 32;
+            if (st.t >= N || col >= H) continue;
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            float4* acc = reinterpret_cast<float4*>(to + col);
+            if (!start) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[4 * j] = old[j].x + x[4 * j];
+                    x[4 * j + 1] = old[j].y + x[4 * j + 1];
+                    x[4 * j + 2] = old[j].z + x[4 * j + 2];
+                    x[4 * j + 3] = old[j].w + x[4 * j + 3];
+                }
+            }
+            if (cc + 1 < kTileV / 32) fetch(col + 32);
+            if (!end) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    acc[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                continue;
+            }
+            if (st.dom >= 0) {
+                const uint4* wa = reinterpret_cast<const uint4*>(
+                    weight + static_cast<size_t>(st.dom) * H + col);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float wv[8];
+                    bf16x8_to_f32(wa[g], wv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[8 * g + j] = fmaf(st.coef_dom, wv[j], x[8 * g + j]);
+                }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(dh + static_cast<size_t>(st.t) * H + col);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                dst[g] = make_uint4(pack_bf16x2(x[8 * g], x[8 * g + 1]),
+                                    pack_bf16x2(x[8 * g + 2], x[8 * g + 3]),
+                                    pack_bf16x2(x[8 * g + 4], x[8 * g + 5]),
+                                    pack_bf16x2(x[8 * g + 6], x[8 * g + 7]));
+        }
+    }
+
+    __device__ void epi_end(int, int, EpiState&) const {}
+};
+
+// dh_acc += the chunk's parts, ascending; the last chunk adds the dominant class and rounds.  Four
+// columns a thread.
+__global__ void __launch_bounds__(256)
+    dh_sum_kernel(const float4* __restrict__ part, int subs, RowMap rm, int N, int H, bool first,
+                  bool last, const uint2* __restrict__ weight, const int* __restrict__ dom,
+                  const float* __restrict__ dcoef, float4* __restrict__ dh_acc,
+                  uint2* __restrict__ dh) {
+    const int vecs = H / 4;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int i = static_cast<int>(e / vecs), c = static_cast<int>(e % vecs);
+    if (i >= rm.count(N)) return;
+    const size_t plane = static_cast<size_t>(N) * vecs;
+    float4 x = first ? part[e] : dh_acc[e];
+    for (int s = first ? 1 : 0; s < subs; ++s) {
+        const float4 v = part[s * plane + e];
+        x.x += v.x;
+        x.y += v.y;
+        x.z += v.z;
+        x.w += v.w;
+    }
+    if (!last) {
+        dh_acc[e] = x;
+        return;
+    }
+    const int t = rm.token(i), a = dom[t];
+    if (a >= 0) {
+        const uint2 w = weight[static_cast<size_t>(a) * vecs + c];
+        const float d = dcoef[t];
+        x.x = fmaf(d, __uint_as_float(w.x << 16), x.x);
+        x.y = fmaf(d, __uint_as_float(w.x & 0xffff0000u), x.y);
+        x.z = fmaf(d, __uint_as_float(w.y << 16), x.z);
+        x.w = fmaf(d, __uint_as_float(w.y & 0xffff0000u), x.w);
+    }
+    dh[static_cast<size_t>(t) * vecs + c] = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
+
 // ----------------------------------------------------------------------------- dW
 
 // dS_c^T: vocab (M) contiguous, tokens along K; h: hidden (N) contiguous.
@@ -1214,6 +1386,7 @@ static cudaError_t launch_dw(const BwdStepMaps& maps, const BwdStep& st, int c0,
     pw.hilo = st.hilo;
     // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
     // writes only dW, which the dh GEMM does not touch
+    // (behind dh_sum_kernel, which does not trigger it, it just starts when that ends)
     return launch_gemm(maps.ds_mnmajor, maps.h_mnmajor, pw, pw.num_m * pw.num_n, num_sms, err,
                        stream, kPdlOverlap);
 }
@@ -1300,6 +1473,37 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         return launch_dom_sort(st.dom, N, V, c0, c0 + width, st.dom_flags + st.chunk, st.tiles,
                                st.sorted_dy, st.sorted_dt, stream);
     }
+    if (st.role == kRoleDh && st.topk) {
+        DhTopkPolicy pd;
+        pd.dh_acc = st.dh_acc;
+        pd.part = st.dh_part;
+        pd.dh = static_cast<__nv_bfloat16*>(st.dhidden);
+        pd.weight = static_cast<const __nv_bfloat16*>(st.weight);
+        pd.dom = st.dom;
+        pd.dcoef = st.dcoef;
+        pd.rm = RowMap{st.rows, st.n_rows};
+        pd.N = N;
+        pd.H = H;
+        pd.c0 = c0;
+        pd.width = width;
+        pd.num_n = (H + kTileV - 1) / kTileV;
+        pd.subs = (width + kDhSub - 1) / kDhSub;
+        pd.first = st.chunk == 0 && !st.dh_started;
+        pd.last = st.chunk == st.num_chunks - 1;
+        pd.hilo = st.hilo && !st.dh_started;
+        pd.split = st.dh_part != nullptr;
+        const int tiles = (N + kUnitM - 1) / kUnitM * pd.num_n;
+        const cudaError_t e =
+            launch_gemm(maps.ds_kmajor, maps.w_mnmajor, pd, pd.split ? tiles * pd.subs : tiles,
+                        num_sms, err, stream, pd.split ? 0 : kPdlTrigger);
+        if (e != cudaSuccess || !pd.split) return e;
+        const int64_t vecs = static_cast<int64_t>(N) * H / 4;
+        dh_sum_kernel<<<static_cast<unsigned>((vecs + 255) / 256), 256, 0, stream>>>(
+            reinterpret_cast<const float4*>(st.dh_part), pd.subs, pd.rm, N, H, pd.first, pd.last,
+            reinterpret_cast<const uint2*>(st.weight), st.dom, st.dcoef,
+            reinterpret_cast<float4*>(st.dh_acc), reinterpret_cast<uint2*>(st.dhidden));
+        return cudaGetLastError();
+    }
     if (st.role == kRoleDh) {
         DhPolicy pd;
         pd.targets = st.targets;
@@ -1323,11 +1527,11 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pd.num_m = (N + kUnitM - 1) / kUnitM;
         pd.num_n = (H + kTileV - 1) / kTileV;
         pd.kblocks = (width + 63) / 64;
-        pd.first = st.chunk == 0 && !st.dh_started;
+        pd.first = st.chunk == 0;
         pd.last = st.chunk == st.num_chunks - 1;
         pd.temp = st.temp;
-        pd.terms = !st.kl && !st.topk;
-        pd.hilo = st.hilo && !st.dh_started;
+        pd.terms = !st.kl;
+        pd.hilo = st.hilo;
         // the dW GEMM that follows overlaps this one's last wave (with 6.7 waves of dh
         // units at N = 8192, a quarter of the CTA pairs would otherwise idle for a unit)
         return launch_gemm(maps.ds_kmajor, maps.w_mnmajor, pd, pd.num_m * pd.num_n, num_sms, err,

@@ -150,6 +150,8 @@ __device__ __forceinline__ uint64_t operand_desc_rt(bool mn_major, uint32_t stag
 //                                         true: the coordinates of K block kb
 //                                         (of nkb) are the policy's, not the
 //                                         plain ascending walk along K
+//   kTileK                                true: tile_k_blocks(u, q) gives each tile's
+//                                         K extent, as with kPairTiles
 //   kCtaPair                              true: units are 256-row tiles of a
 //                                         CTA pair; coords() gives the tile's
 //                                         origin, the mainloop adds the CTA's
@@ -178,6 +180,7 @@ template <bool AMN, bool BMN>
 struct SingleRole {
     using Maps = TwoMaps;
     static constexpr bool kPairTiles = false;
+    static constexpr bool kTileK = false;
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = false;
     static constexpr int kEpiWarps = 4;
@@ -344,8 +347,8 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                     if constexpr (P::kPairTiles) {
                         qa = p.tile_a_map(maps, u, q);
                         qb = p.tile_b_map(maps, u, q);
-                        qk = p.tile_k_blocks(u, q);
                     }
+                    if constexpr (P::kPairTiles || P::kTileK) qk = p.tile_k_blocks(u, q);
                     for (int kb = 0; kb < qk; ++kb) {
                         const bool got = PAIR
                             ? mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag, kWaitTimeoutNs)
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + buf * kBN;
                     int qk = kblocks;
-                    if constexpr (P::kPairTiles) qk = p.tile_k_blocks(u, q);
+                    if constexpr (P::kPairTiles || P::kTileK) qk = p.tile_k_blocks(u, q);
                     for (int kb = 0; kb < qk; ++kb) {
                         const bool landed = PAIR
                             ? mbar_wait_cluster(&full[stage], phase, abort_flag, kWaitTimeoutNs)

@@ -104,27 +104,44 @@ struct BwdLayout {
 constexpr int kRadixBits = 9, kRadixTile = 2048;
 constexpr int kTopkSmallV = 8192;
 // The lo plane doubles the dW GEMM, 2 N H V at 1.7 PFLOP/s.  The sums move 4 bytes a column of each
-// row that has any at 6 TB/s, read 2 of h for each entry at 8 TB/s from L2, and take 70 us of
-// launches for their list (H = 4096, V = 151936, K = 64: equal at N = 500; N = 2048: XXX).  A small
-// vocabulary, of which a few classes that are not listed may carry much of a row, has the plane
-// for dh too.
+// row that has any at 6 TB/s, read 2 of h for each entry at 8 TB/s from L2, and take 60 us a chunk for
+// their list, their launches and the reads that dW waits for.  Measured for steps at H = 4096, V =
+// 151936, lo and sums: N = 600, K = 64 2922 and 3027 us; N = 600, K = 512 3251 and 3992; N = 1200, K =
+// 256 5253 and 5172; N = 2048, K = 64 7900 and 6820.  A small vocabulary, of which a few classes that
+// are not listed may carry much of a row, has the plane for dh too.
 inline bool topk_lo_plane(int64_t N, int64_t H, int64_t V, int64_t K) {
     if (V <= kTopkSmallV) return true;
     const double e = static_cast<double>(N) * static_cast<double>(K);
     const double rows = e < static_cast<double>(V) ? e : static_cast<double>(V);
-    const double sums = (rows * 4 / 6e12 + e * 2 / 8e12) * static_cast<double>(H) + 70e-6;
+    const double sums = (rows * 4 / 6e12 + e * 2 / 8e12) * static_cast<double>(H) +
+                        60e-6 * static_cast<double>((V + kBwdChunk - 1) / kBwdChunk);
     return 2.0 * static_cast<double>(N) * static_cast<double>(H) * static_cast<double>(V) / 1.7e15 < sums;
+}
+// Whether the dh GEMM takes the sub-chunks of a vocabulary chunk side by side, in parts that are
+// summed after it (DhTopkPolicy): where that fills the waves of 76 CTA pairs better by more than the
+// parts cost, with a tenth to spare (dW fills part of an idle wave).  A tile takes 192 us for a whole
+// chunk, the parts move at 6.5 TB/s.  Measured for steps of [45, 4096] and V = 151936: 1391 us, one
+// after the other 1791; [500, 4096] 2520 and 2708; [2048, 4096] 6887 and 6822 (not split).
+constexpr int kDhSubs = 4;
+inline bool topk_dh_split(int64_t N, int64_t H) {
+    const int64_t tiles = (N + kUnitM - 1) / kUnitM * ((H + kTileV - 1) / kTileV);
+    const int64_t waves = (tiles + 75) / 76, part_waves = (tiles * kDhSubs + 75) / 76;
+    const double parts = static_cast<double>(N) * static_cast<double>(H) * 8 * kDhSubs / 6.5e12;
+    return 1.1 * (static_cast<double>(part_waves) / kDhSubs * 192e-6 + parts) <
+           static_cast<double>(waves) * 192e-6;
 }
 struct TopkKlBwdLayout : BwdLayout {
     bool lo;
     int64_t tiles, places;
-    size_t ids_off, val_off, key_off[2], slot_off[2], hist_off, first_off, last_off, at_off,
+    size_t part_off, ids_off, val_off, key_off[2], slot_off[2], hist_off, first_off, last_off, at_off,
         list_off, many_off, counts_off, sums_off;
     TopkKlBwdLayout(int64_t N, int64_t H, int64_t V, int64_t K)
         : BwdLayout(N, H, topk_lo_plane(N, H, V, K)), lo(topk_lo_plane(N, H, V, K)) {
         const size_t e = static_cast<size_t>(N) * K, v = static_cast<size_t>(V);
         tiles = static_cast<int64_t>((e + kRadixTile - 1) / kRadixTile);
         places = static_cast<int64_t>(e < kBwdChunk ? e : kBwdChunk);
+        part_off = total;
+        if (topk_dh_split(N, H)) total = align_up(part_off + static_cast<size_t>(kDhSubs) * N * H * 4, 256);
         ids_off = total;
         val_off = align_up(ids_off + e * 4, 256);
         total = align_up(val_off + e * 4, 256);
@@ -298,6 +315,7 @@ struct BwdStep {
     const float* topk_val;     // [N][K] their whole entries of dS
     const void* gemm_rows;     // [N][H]
     const TopkRows* rows_of;   // or nullptr: dS has a lo plane
+    float* dh_part;            // or nullptr: dh's sub-chunks one after the other
     void* ds;                  // dS [N, kBwdChunk] bf16 of the chunk (hilo: [N, 2 kBwdChunk])
     float* dh_acc;
     const int* sorted_y;
@@ -469,7 +487,7 @@ struct TopkKlFwdLayout {
     int64_t num_chunks;
     size_t partial_off, rows_off, pos_off, blk_off, count_off, hc_off, list_off, first_off, total;
     TopkKlFwdLayout(int64_t N, int64_t H, int64_t V, int64_t K) {
-        num_chunks = fwd_num_chunks(V);
+        num_chunks = (V + kTileV - 1) / kTileV;
         partial_off = 0;
         rows_off = align_up(static_cast<size_t>(num_chunks) * N * 8, 256);
         pos_off = align_up(rows_off + static_cast<size_t>(N) * 4, 256);

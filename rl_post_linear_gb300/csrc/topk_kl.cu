@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kListThreads)
         list[static_cast<size_t>(i) * s.K + j] =
             make_int2(static_cast<int>(key[j] >> 32), static_cast<int>(key[j] & 0xffffffffu));
     for (int c = threadIdx.x; c < num_chunks; c += kListThreads) {
-        const uint64_t from = static_cast<uint64_t>(c) * kFwdChunk << 32;
+        const uint64_t from = static_cast<uint64_t>(c) * kTileV << 32;
         int lo = 0, hi = s.K;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -124,65 +124,59 @@ __global__ void __launch_bounds__(kListThreads)
 
 // ----------------------------------------------------------------------------- lse, logp, kl
 
-// lse as the log-prob's merge forms it (chunk c to group c mod 8, ascending; then the groups in
-// order), 32 rows a block; then the rows' slots, four rows a warp.
-constexpr int kRows = 32, kGroups = 8;
+// lse of eight rows a block, a tile's partial to group tile mod 32 and ascending in it, then the
+// groups in order; then a warp for each row's slots.
+constexpr int kRows = 8, kGroups = 32;
 
 __global__ void __launch_bounds__(kRows * kGroups)
     topk_merge_kernel(const TopkSlots s, const float2* __restrict__ partials, int num_chunks,
                       const int* __restrict__ pos_of, float k, float* __restrict__ kl,
                       float* __restrict__ lse, float* __restrict__ logp, uint32_t* err) {
-    __shared__ float s_m[kGroups][kRows];
-    __shared__ float s_s[kGroups][kRows];
-    __shared__ float s_max[kRows];               // the row's largest logit
-    __shared__ float s_log[kRows];               // log2 sum 2^((s - max) k)
-    const int r = threadIdx.x % kRows, g = threadIdx.x / kRows;
+    __shared__ float s_m[kRows][kGroups + 1];
+    __shared__ float s_s[kRows][kGroups + 1];
     const int t0 = blockIdx.x * kRows;
-    const int tr = t0 + r;
-    const bool live = tr < s.N && (s.mask == nullptr || s.mask[tr] != 0);
-    const int i = !live ? 0 : (pos_of != nullptr ? pos_of[tr] : tr);
-    float m = -INFINITY, sigma = 0.f;
-    if (live) {
-        for (int c = g; c < num_chunks; c += kGroups)
-            m = fmaxf(m, partials[static_cast<size_t>(c) * s.N + i].x);
-        for (int c = g; c < num_chunks; c += kGroups) {
-            const float2 pc = partials[static_cast<size_t>(c) * s.N + i];
-            sigma += pc.y * ex2_approx((pc.x - m) * k);
+    {
+        const int r = threadIdx.x % kRows, g = threadIdx.x / kRows;
+        const int t = t0 + r;
+        const bool live = t < s.N && (s.mask == nullptr || s.mask[t] != 0);
+        const int i = !live ? 0 : (pos_of != nullptr ? pos_of[t] : t);
+        float m = -INFINITY, sigma = 0.f;
+        if (live) {
+#pragma unroll 4
+            for (int c = g; c < num_chunks; c += kGroups)
+                m = fmaxf(m, partials[static_cast<size_t>(c) * s.N + i].x);
+#pragma unroll 4
+            for (int c = g; c < num_chunks; c += kGroups) {
+                const float2 pc = partials[static_cast<size_t>(c) * s.N + i];
+                sigma += pc.y * ex2_approx((pc.x - m) * k);
+            }
         }
-    }
-    s_m[g][r] = m;
-    s_s[g][r] = sigma;
-    __syncthreads();
-    if (g == 0) {
-        float mm = -INFINITY, sg = 0.f;
-#pragma unroll
-        for (int q = 0; q < kGroups; ++q) mm = fmaxf(mm, s_m[q][r]);
-#pragma unroll
-        for (int q = 0; q < kGroups; ++q) sg += s_s[q][r] * ex2_approx((s_m[q][r] - mm) * k);
-        s_max[r] = mm;
-        s_log[r] = log2f(sg);
-        if (tr < s.N) lse[tr] = live ? (mm * k + lg2_approx(sg)) * kLn2 : 0.f;
+        s_m[r][g] = m;
+        s_s[r][g] = sigma;
     }
     __syncthreads();
-    const int lane = r;
-    for (int a = g; a < kRows; a += kGroups) {
+    const int lane = threadIdx.x & 31, a = threadIdx.x >> 5;
+    {
         const int t = t0 + a;
         if (t >= s.N) return;
         float* lp = logp + static_cast<size_t>(t) * s.K;
         if (s.mask != nullptr && s.mask[t] == 0) {
             for (int j = lane; j < s.K; j += 32) lp[j] = 0.f;
-            if (lane == 0) kl[t] = 0.f;
-            continue;
+            if (lane == 0) kl[t] = 0.f, lse[t] = 0.f;
+            return;
         }
+        // the row's largest logit, and log2 sum 2^((s - top) k)
+        const float top = warp_max(s_m[a][lane]);
+        const float log_sum = log2f(warp_sum(s_s[a][lane] * ex2_approx((s_m[a][lane] - top) * k)));
+        if (lane == 0) lse[t] = fmaf(top, k, log_sum) * kLn2;
         const RowSlots slots(s, t, lane);
-        const float top = s_max[a], log_sum = s_log[a];
         if (slots.bad != 0) {
             for (int j = lane; j < s.K; j += 32) lp[j] = __int_as_float(0x7fc00000);
             if (lane == 0) {
                 kl[t] = __int_as_float(0x7fc00000);
                 if (err != nullptr) atomicOr(err, slots.bad);
             }
-            continue;
+            return;
         }
         float sum = 0.f;
         for (int j = lane; j < s.K; j += 32) {
@@ -590,28 +584,43 @@ __global__ void __launch_bounds__(1024)
                       int2* __restrict__ counts) {
     __shared__ uint32_t part[32];
     __shared__ uint32_t s_total, s_many;
-    constexpr int kEach = kBwdChunk / 1024;
-    const int c0 = blockIdx.x * kBwdChunk, v0 = c0 + threadIdx.x * kEach;
+    const int c0 = blockIdx.x * kBwdChunk, c1 = min(V, c0 + kBwdChunk);
     if (threadIdx.x == 0) s_many = 0;
-    uint32_t has = 0;                            // bit j: row v0 + j
-#pragma unroll 8
-    for (int j = 0; j < kEach; ++j)
-        if (v0 + j < V && last[v0 + j] > 0) has |= 1u << j;
-    const uint32_t inc = block_sum_scan<1024>(__popc(has), part);
-    if (threadIdx.x == 1023) s_total = inc;
-    uint32_t at = inc - __popc(has);
-    for (int j = 0; j < kEach && v0 + j < V; ++j) {
-        const bool on = (has >> j) & 1u;
-        row_at[v0 + j] = on ? static_cast<int>(at) : -1;
-        if (!on) continue;
-        list[c0 + at] = v0 + j;
-        if (last[v0 + j] - first[v0 + j] > kMany)
-            many[c0 + atomicAdd(&s_many, 1u)] = static_cast<int>(at);   // in no order: each by itself
-        ++at;
+    uint32_t base = 0;
+    for (int b0 = c0; b0 < c1; b0 += 4096) {
+        const int v0 = b0 + threadIdx.x * 4;
+        int4 end = make_int4(0, 0, 0, 0);
+        if (v0 + 3 < c1) {
+            end = *reinterpret_cast<const int4*>(last + v0);
+        } else {
+            if (v0 < c1) end.x = last[v0];
+            if (v0 + 1 < c1) end.y = last[v0 + 1];
+            if (v0 + 2 < c1) end.z = last[v0 + 2];
+        }
+        const int ends[4] = {end.x, end.y, end.z, end.w};
+        uint32_t own = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) own += ends[j] > 0;
+        const uint32_t inc = base + block_sum_scan<1024>(own, part);
+        if (threadIdx.x == 1023) s_total = inc;
+        uint32_t at = inc - own;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (v0 + j >= c1) continue;
+            const bool on = ends[j] > 0;
+            row_at[v0 + j] = on ? static_cast<int>(at) : -1;
+            if (!on) continue;
+            list[c0 + at] = v0 + j;
+            if (ends[j] - first[v0 + j] > kMany)
+                many[c0 + atomicAdd(&s_many, 1u)] = static_cast<int>(at);   // in no order: each by itself
+            ++at;
+        }
+        __syncthreads();
+        base = s_total;
     }
     __syncthreads();
     if (threadIdx.x == 0)
-        counts[blockIdx.x] = make_int2(static_cast<int>(s_total), static_cast<int>(s_many));
+        counts[blockIdx.x] = make_int2(static_cast<int>(base), static_cast<int>(s_many));
 }
 
 }  // namespace

@@ -233,6 +233,47 @@ def test_a_row_does_not_depend_on_its_batch_and_dweight_is_reproducible():
         assert same_bits(got, want[131:260])
 
 
+def test_few_tiles_and_many_give_the_same_bits():
+    # dh of few rows takes a vocabulary chunk's parts side by side, of many one after the other
+    n, h, v, k = 10000, 64, 45000, 3
+    hid, w, ids, a = (x.to(dev()) for x in problem(500, h, v, k, 22))
+    reps = n // 500
+    g = torch.randn(500, generator=gen(23)).to(dev())
+
+    def both(hid, ids, a, g):
+        kl, lse, lp = rlk.linear_topk_kl_fwd(hid, w, ids, a)
+        return kl, lp, rlk.linear_topk_kl_bwd(hid, w, ids, a, None, g, lse, lp)[0]
+
+    few = both(hid, ids, a, g)
+    many = both(hid.repeat(reps, 1), ids.repeat(reps, 1), a.repeat(reps, 1), g.repeat(reps))
+    for x, y in zip(few, many):
+        for part in y.split(500):
+            assert same_bits(x, part.contiguous())
+
+
+@pytest.mark.parametrize("n,h,v,k", [(700, 128, 70000, 16), (1200, 64, 40000, 40),
+                                     (3000, 64, 9000, 8)])
+def test_tokens_that_many_rows_list(n, h, v, k):
+    # dweight's sums over many entries of a vocabulary row, some of them in every row
+    hid, w, ids, a = problem(n, h, v, k, 24)
+    ids = (ids.double() / v).pow(6).mul(v).long()
+    for j in range(k):                                  # distinct in a row
+        ids[:, j] = (ids[:, j] // k) * k + j
+    ids.clamp_(max=v - 1)
+    ids[:, 0] = v - 1
+    mask = (torch.arange(n) % 7 != 2).to(torch.uint8)
+    check(hid, w, ids, a, mask, t=1.1)
+
+
+def test_a_confident_student_that_the_teacher_does_not_follow():
+    # a class with p near 1 that no slot names
+    n, h, v, k = 200, 128, 20000, 6
+    hid, w, ids, a = problem(n, h, v, k, 25)
+    other = torch.randint(0, v, (n,), generator=gen(26))
+    hid = (hid.float() + 14.0 * w[other].float()).to(torch.bfloat16)
+    check(hid, w, ids, a)
+
+
 def test_gradient_by_differences():
     # kl(h + d) - kl(h - d) = 2 dkl.d + R, |R| <= sum g Q max|ds|^3 / 3 (a third derivative of
     # logsumexp is a third central moment, at most max|ds|^3), with steps that bf16 holds exactly
