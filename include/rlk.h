@@ -621,7 +621,8 @@ rlk_status_t rlk_sample_logits(const void* logits, int32_t dtype, int64_t N, int
 /* Settings of rlk_process_logits (a host structure, read during the call).  Pointers are device
  * arrays or NULL.  A *_rows member has one value a row; NULL: the scalar holds for every row. */
 typedef struct {
-    const int64_t* tokens;          /* [N, tokens_stride]: a row's prompt, then what it drew */
+    const int64_t* tokens;          /* [N, tokens_stride]: a row's prompt, then what it drew; may be
+                                       NULL where tokens_width is 0 */
     const int64_t* lengths;         /* [N] how many of them count; NULL: tokens_width */
     const int64_t* prompt_lengths;  /* [N] how many of those are the prompt; NULL: 0 */
     int64_t tokens_width, tokens_stride;
@@ -720,7 +721,9 @@ rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t
  * (RLK_DEVERR_TARGET_RANGE), or with NaN or +inf as log-weight of an id (RLK_DEVERR_LOGITS),
  * gives kl and logp NaN; the backward gives it no gradient.  Accumulation is fp32, with the mean
  * of what the tensor cores cut off a logit given back (lse may differ from rlk_linear_logp_fwd's
- * by that, 1e-9 H of a logit); dhidden and dweight are rounded once.  kl, lse, logp and dhidden rows do not depend on the batch; dweight
+ * by that, 1e-9 H of a logit); dhidden and dweight are rounded once.  Of dL/ds the entries at the
+ * teacher's tokens, and one with p > 1/2, enter the products in fp32 accuracy, the others rounded to
+ * bf16 (2^-8 of themselves at most; in about 16 bits for V <= 8192).  kl, lse, logp and dhidden rows do not depend on the batch; dweight
  * is reproducible bit for bit.
  */
 size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K);

@@ -329,6 +329,15 @@ def _need(t, dtype, name, shape=None):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+def _here(*tensors):
+    """Refuses tensors of another device than the current one, on which the call is launched."""
+    device = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("a tensor on %s with cuda:%d as the current device"
+                             % (t.device, device))
+
+
 def _check(fn, status):
     if status != RLK_OK:
         raise RlkError(fn, status)
@@ -926,6 +935,9 @@ def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, freq
         words = allowed.data_ptr()
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
+    _here(logits, tokens, lengths, prompt_lengths, bias_ids, bias_values, allowed, active_mask, out,
+          device_error_word, *[t for t in (repetition, frequency, presence)
+                               if isinstance(t, torch.Tensor)])
     params = ProcessParams(tok, full, prompt, width, tok_stride, rep_rows, freq_rows, pres_rows,
                            rep, freq, pres, bias, values, biases, words, words_stride)
     st = load().rlk_process_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
@@ -949,6 +961,7 @@ def rlk_topk_logp(logits, active_mask, temperature, ids, logp, lse, device_error
         _need(lse, torch.float32, "lse", (n,))
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
+    _here(logits, active_mask, ids, logp, lse, device_error_word)
     st = load().rlk_topk_logp(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
                               _ptr(active_mask), k, float(temperature), _ptr(ids), _ptr(logp),
                               _ptr(lse), _ptr(device_error_word), _stream(stream))
@@ -979,6 +992,8 @@ def rlk_linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mas
     n, h, v, k = _need_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask, lse_out,
                                logp_out, workspace)
     _need(kl_out, torch.float32, "kl_out", (n,))
+    _here(hidden, weight, teacher_ids, teacher_logp, active_mask, kl_out, lse_out, logp_out,
+          workspace, device_error_word)
     st = load().rlk_linear_topk_kl_fwd(_ptr(hidden), _ptr(weight), _ptr(teacher_ids),
                                        _ptr(teacher_logp), _ptr(active_mask), n, h, v, k,
                                        float(temperature), int(bool(renormalize)), _ptr(kl_out),
@@ -997,6 +1012,8 @@ def rlk_linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mas
     _need(grad_kl, torch.float32, "grad_kl", (n,))
     _need(dhidden, torch.bfloat16, "dhidden", (n, h))
     _need(dweight, torch.bfloat16, "dweight", (v, h))
+    _here(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse, logp, dhidden,
+          dweight, workspace, device_error_word)
     st = load().rlk_linear_topk_kl_bwd(_ptr(hidden), _ptr(weight), _ptr(teacher_ids),
                                        _ptr(teacher_logp), _ptr(active_mask), _ptr(grad_kl),
                                        _ptr(lse), _ptr(logp), n, h, v, k, float(temperature),

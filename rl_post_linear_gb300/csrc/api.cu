@@ -919,12 +919,10 @@ rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, in
         return RLK_ERR_INVALID_VALUE;
     if (p.frequency_rows == nullptr && !std::isfinite(freq)) return RLK_ERR_INVALID_VALUE;
     if (p.presence_rows == nullptr && !std::isfinite(pres)) return RLK_ERR_INVALID_VALUE;
-    const bool history = p.tokens != nullptr;
-    if (history && (p.tokens_width < 0 || p.tokens_stride < p.tokens_width))
-        return RLK_ERR_INVALID_VALUE;
-    if (!history && (p.lengths != nullptr || p.prompt_lengths != nullptr))
-        return RLK_ERR_INVALID_VALUE;
-    if (history && p.tokens_width > (int64_t(1) << 29)) return RLK_ERR_UNSUPPORTED;
+    // no tokens yet: their array may be missing where its width is 0
+    if (p.tokens_width < 0 || p.tokens_stride < p.tokens_width) return RLK_ERR_INVALID_VALUE;
+    if (p.tokens == nullptr && p.tokens_width > 0) return RLK_ERR_INVALID_VALUE;
+    if (p.tokens_width > (int64_t(1) << 29)) return RLK_ERR_UNSUPPORTED;
     if (p.bias_count < 0) return RLK_ERR_INVALID_VALUE;
     if (p.bias_count > rlk::kMaxBias) return RLK_ERR_UNSUPPORTED;
     if (p.bias_count > 0 && (p.bias_ids == nullptr || p.bias_values == nullptr))
@@ -945,7 +943,8 @@ rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, in
     rlk::ProcessArgs a{};
     a.x = logits, a.out = out, a.x_stride = row_stride, a.out_stride = out_stride;
     a.mask = active_mask;
-    a.tokens = p.tokens, a.lengths = p.lengths, a.prompt_lengths = p.prompt_lengths;
+    a.tokens = p.tokens_width > 0 ? p.tokens : nullptr;
+    a.lengths = p.lengths, a.prompt_lengths = p.prompt_lengths;
     a.tokens_stride = p.tokens_stride;
     a.repetition_rows = p.repetition_rows, a.frequency_rows = p.frequency_rows;
     a.presence_rows = p.presence_rows;
@@ -953,7 +952,7 @@ rlk_status_t rlk_process_logits(const void* logits, int32_t dtype, int64_t N, in
     a.bias_ids = p.bias_ids, a.bias_values = p.bias_values;
     a.allowed = p.allowed, a.allowed_stride = p.allowed_stride;
     a.N = static_cast<int>(N), a.V = static_cast<int>(V);
-    a.width = history ? static_cast<int>(p.tokens_width) : 0;
+    a.width = static_cast<int>(p.tokens_width);
     a.bias = static_cast<int>(p.bias_count);
     a.err = device_error_word;
     RLK_CUDA(rlk::launch_process(a, dtype == RLK_DTYPE_BF16, stream));

@@ -835,7 +835,7 @@ struct DhPolicy : SingleRole<false, true> {
 // would idle: a unit is then one sub-chunk of a tile, written to `part`, and dh_sum_kernel adds them
 // in the same order, so that a row's bits do not depend on the batch (a step of [200, 2048] against
 // V = 32003: 242 instead of 341 us).
-constexpr int kDhSub = kBwdChunk / kDhSubs;       // 4096
+constexpr int kDhSub = kBwdChunk / kDhSubs;       // 8192
 struct DhTopkPolicy : SingleRole<false, true> {
     static constexpr bool kKRemap = true;
     static constexpr bool kTileK = true;

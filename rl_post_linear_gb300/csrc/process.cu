@@ -184,7 +184,7 @@ struct Row {
         pres = a.presence_rows != nullptr ? a.presence_rows[row] : a.presence;
         if (!(rep > 0.f && rep < INFINITY) || !(fabsf(freq) < INFINITY) || !(fabsf(pres) < INFINITY))
             bad = RLK_DEVERR_SAMPLE_PARAM;
-        if (a.tokens != nullptr) {
+        if (a.tokens != nullptr || a.lengths != nullptr || a.prompt_lengths != nullptr) {
             const int64_t n = a.lengths != nullptr ? a.lengths[row] : a.width;
             const int64_t m = a.prompt_lengths != nullptr ? a.prompt_lengths[row] : 0;
             if (m < 0 || n < m || n > a.width)
@@ -586,8 +586,11 @@ cudaError_t launch_rows(const ProcessArgs& a, cudaStream_t stream) {
             return launch(process_kernel<T, 1024, true>, 1024, a, r, kWords, stream);
     }
     const bool copied = a.x != a.out || a.allowed != nullptr;
-    if (copied || (!listed && (a.repetition_rows != nullptr || a.frequency_rows != nullptr ||
-                               a.presence_rows != nullptr))) {
+    // a row that cannot be is found out even where nothing is changed
+    const bool checked = a.repetition_rows != nullptr || a.frequency_rows != nullptr ||
+                         a.presence_rows != nullptr || a.lengths != nullptr ||
+                         a.prompt_lengths != nullptr;
+    if (copied || (!listed && checked)) {
         const cudaError_t e =
             launch(process_kernel<T, 256, false>, 256, a, Ranges(a.V, 8192), 0, stream);
         if (e != cudaSuccess) return e;

@@ -294,8 +294,26 @@ def test_rows_that_cannot_be(kind):
     assert bool(torch.isnan(y[1]).all()) and same_bits(y[0], x[0]) and same_bits(y[2], x[2])
 
 
-def test_captured_with_the_draw():
-    n, v = 8, 30000
+def test_no_tokens_yet():
+    n, v = 3, 4000
+    x = logits(n, v, 40, torch.float32)
+    none = torch.empty(n, 0, dtype=torch.int64, device=dev())
+    zero = torch.zeros(n, dtype=torch.int64, device=dev())
+    assert same_bits(check(x, none, zero, zero, 1.5, 0.5, 0.5), x)
+    assert same_bits(check(x, none, None, None, 1.5), x)
+    one = zero.clone()
+    one[1] = 1
+    for out in (None, x.clone()):
+        err = torch.zeros(1, dtype=torch.int32, device=dev())
+        src = x if out is None else out
+        y = rlk.process_logits(src, none, one, out=out, error_word=err)
+        assert int(err.item()) == rlk.RLK_DEVERR_SAMPLE_PARAM
+        assert bool(torch.isnan(y[1]).all()) and same_bits(y[0], x[0]) and same_bits(y[2], x[2])
+
+
+@pytest.mark.parametrize("n", [8, 400])
+def test_captured_with_the_draw(n):
+    v = 30000
     x = logits(n, v, 16, torch.float32)
     t, full, prompt = history(n, v, 64, 17)
     u = torch.rand(n, generator=gen(18)).to(dev())
@@ -316,8 +334,9 @@ def test_captured_with_the_draw():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
-    for seed in (19, 20):
+    for seed in (19, 20, 21):
         x.copy_(logits(n, v, seed, torch.float32))
+        t.copy_(history(n, v, 64, seed + 30)[0])         # by the launch just before
         graph.replay()
         got = tok.clone()
         want = rlk.sample_logits(rlk.process_logits(x, t, full, prompt, 1.2, 0.1, 0.1), u, 0.8,

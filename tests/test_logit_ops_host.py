@@ -53,8 +53,8 @@ def test_processing_refusals(lib, kw, status):
     ({"presence": math.nan}, INVALID), ({"presence": -1e60}, INVALID),
     ({"tokens_width": -1}, INVALID), ({"tokens_stride": 7}, INVALID),
     ({"tokens_width": (1 << 29) + 1, "tokens_stride": 1 << 30}, UNSUPPORTED),
-    ({"tokens": None, "lengths": FAKE}, INVALID),
-    ({"tokens": None, "prompt_lengths": FAKE}, INVALID), ({"bias_count": -1}, INVALID),
+    ({"tokens": None}, INVALID), ({"tokens": None, "lengths": FAKE}, INVALID),
+    ({"bias_count": -1}, INVALID),
     ({"bias_count": 4097, "bias_ids": FAKE, "bias_values": FAKE}, UNSUPPORTED),
     ({"bias_count": 1, "bias_ids": FAKE}, INVALID),
     ({"bias_count": 1, "bias_values": FAKE}, INVALID),
@@ -135,6 +135,21 @@ def test_workspace_queries(lib):
                rlk.rlk_linear_topk_kl_bwd_workspace_bytes):
         assert fn(-1, 64, 10, 2) == fn(4, 64, 0, 2) == fn(4, 64, 10, 0) == 0
     assert ctypes.sizeof(rlk.ProcessParams) == 128
+
+
+def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    class On:
+        def __init__(self, device):
+            self.at, self.device = device, "cuda:%d" % device
+
+        def get_device(self):
+            return self.at
+
+    monkeypatch.setattr(rlk, "_device", lambda: 1)
+    rlk._here(On(1), None, On(1))
+    for bad in ((On(0),), (On(1), On(2)), (On(1), None, On(0))):
+        with pytest.raises(ValueError, match="current device"):
+            rlk._here(*bad)
 
 
 def test_binding_refuses_what_it_cannot_pass_on(lib):
