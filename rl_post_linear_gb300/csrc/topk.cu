@@ -167,19 +167,41 @@ struct Unit {
     }
     // sum of 2^((x - m) k), pairs of columns at a time
     __device__ __forceinline__ float weight(float m, float k) const {
-        const float2 mm = make_float2(-m, -m), kk = make_float2(k, k);
+        const float mk = m * k;
         float2 sum = make_float2(0.f, 0.f);
+        const float2 kk = make_float2(k, k);
+        if (fabsf(mk) < 65536.f) {
+            // one fma a column; what the product m k was rounded by (at most 2^-9) comes off the sum
+            const float2 by = make_float2(-mk, -mk);
 #pragma unroll
-        for (int i = 0; i < WORDS; i += sizeof(T) == 2 ? 1 : 2) {
-            float2 x;
+            for (int i = 0; i < WORDS / kWordsPair; ++i) {
+                const float2 t = __ffma2_rn(pair(i), kk, by);
+                sum = __fadd2_rn(sum, make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+            }
+            return (sum.x + sum.y) * ex2_approx(-fmaf(m, k, -mk));
+        }
+        const float2 by = make_float2(-m, -m);
+#pragma unroll 1
+        for (int i = 0; i < WORDS; ++i) {
+            float2 t = make_float2(0.f, -INFINITY);
+            uint32_t word = w[0];
+#pragma unroll
+            for (int j = 1; j < WORDS; ++j) word = i == j ? w[j] : word;
             if constexpr (sizeof(T) == 2)
-                x = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                t = make_float2(__uint_as_float(word << 16), __uint_as_float(word & 0xffff0000u));
             else
-                x = make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-            x = __fmul2_rn(__fadd2_rn(x, mm), kk);
-            sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                t.x = __uint_as_float(word);
+            t = __fmul2_rn(__fadd2_rn(t, by), kk);
+            sum = __fadd2_rn(sum, make_float2(ex2_approx(t.x), ex2_approx(t.y)));
         }
         return sum.x + sum.y;
+    }
+    static constexpr int kWordsPair = sizeof(T) == 2 ? 1 : 2;
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 2)
+            return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else
+            return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     }
 };
 
@@ -212,19 +234,17 @@ __device__ __forceinline__ float piece_value(const uint4& v, int e) {
     return __uint_as_float((e & 1) ? (p[e / 2] & 0xffff0000u) : (p[e / 2] << 16));
 }
 
-// What a stream leaves: maximum, sum, the least of its segments' maxima (a lower bound of it) and
-// how many lanes' are above -inf.
+// What a stream leaves: its maximum and the sum of its weights.
 struct Stream {
-    float m, s, low;
-    uint32_t count;
+    float m, s;
 };
 
 // Behind it the list.  While the row is read the warps' rings take the place of both.
 struct Shared {
-    uint32_t hist[kBins];
+    alignas(16) uint32_t hist[kBins];
     uint16_t queue[kQueue];
     alignas(4) uint8_t bits[kPieces + 4];
-    uint32_t warp_n[32];
+    uint32_t warp_n[32], warp_low[32];
     uint32_t n, queued;
     uint32_t bin, below, through;        // of the histogram: the bin K falls on, counts to it
 };
@@ -232,6 +252,12 @@ struct Shared {
 // Elements the list holds: about K are found where segments are many, and never more than
 // twice as many that a histogram would let through.
 __host__ __device__ constexpr int list_size(int K) { return K <= 256 ? 1024 : kList; }
+
+template <int THREADS>
+__device__ __forceinline__ void clear_hist(Shared& sh) {
+    uint4* h = reinterpret_cast<uint4*>(sh.hist);
+    for (int b = threadIdx.x; b < kBins / 4; b += THREADS) h[b] = make_uint4(0, 0, 0, 0);
+}
 
 // Exclusive prefix of n over the block, and the total.
 template <int THREADS>
@@ -305,7 +331,7 @@ __device__ __noinline__ uint32_t segment_bound(const uint32_t* segkey, int nseg,
         if (through <= want + slack || shift == 0) return bound;
         hi -= bin << shift;
         lo = bound;
-        for (int b = threadIdx.x; b < kBins; b += THREADS) sh.hist[b] = 0;
+        clear_hist<THREADS>(sh);
         __syncthreads();
     }
 }
@@ -424,8 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         to_seg = peer(to_seg, 0);
     }
     int slot = 0;
-    float m = -INFINITY, s = 0.f, low = INFINITY;
-    uint32_t count = 0;
+    float m = -INFINITY, s = 0.f;
     while (stream < last) {
         U now;
         asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
@@ -445,28 +470,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             *reinterpret_cast<uint2*>(to_seg + (at * 32 + lane) * 2) =
                 make_uint2(order_key(m0), order_key(m1));
             mu = fmaxf(m0, m1);
-            low = fminf(low, fminf(m0 > -INFINITY ? m0 : INFINITY, m1 > -INFINITY ? m1 : INFINITY));
-            count += (m0 > -INFINITY) + (m1 > -INFINITY);
         } else {
             mu = U::largest(now.w, kLoads);
             float g = mu;
             for (int off = 1; off < plan.lanes; off <<= 1)
                 g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, off));
             if (lane % plan.lanes == 0) to_seg[(at * 32 + lane) >> plan.log_lanes] = order_key(g);
-            if (mu > -INFINITY) ++count, low = fminf(low, mu);
         }
         // the lane's running maximum and sum; 0 stands in for a maximum of -inf
-        const float nm = fmaxf(m, mu), zero = nm == -INFINITY ? 0.f : nm;
-        const float su = now.weight(mu == -INFINITY ? 0.f : mu, a.k);
-        s = fmaf(s, ex2_approx((m - zero) * a.k), su * (mu == -INFINITY ? 1.f : ex2_approx((mu - zero) * a.k)));
+        const float nm = fmaxf(m, mu), ref = nm == -INFINITY ? 0.f : nm;
+        s = fmaf(s, ex2_approx((m - ref) * a.k), now.weight(ref, a.k));
         m = nm;
         if (ends) {
-            const float top = warp_max(m), ref = top == -INFINITY ? 0.f : top;
-            s = warp_sum(s * (m == -INFINITY ? 1.f : ex2_approx((m - ref) * a.k)));
-            low = -warp_max(-low);
-            count = __reduce_add_sync(0xffffffffu, count);
-            if (lane == 0) to_stream[stream] = Stream{top, s, low, count};
-            m = -INFINITY, s = 0.f, low = INFINITY, count = 0;
+            const float top = warp_max(m), at_top = top == -INFINITY ? 0.f : top;
+            s = warp_sum(s * (m == -INFINITY ? 1.f : ex2_approx((m - at_top) * a.k)));
+            if (lane == 0) to_stream[stream] = Stream{top, s};
+            m = -INFINITY, s = 0.f;
             stream = to;
         }
     }
@@ -480,25 +499,30 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     } else {
         __syncthreads();
     }
-    for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
+    clear_hist<THREADS>(sh);
     if (tid == 0) sh.n = sh.queued = 0;
 
-    // the row's maximum and sum; the least of the segments' maxima, and how many are above -inf
-    // (each warp for itself, in one order)
-    for (int i = lane; i < last; i += 32) {
-        m = fmaxf(m, of_stream[i].m);
-        low = fminf(low, of_stream[i].low);
-        count += of_stream[i].count;
-    }
+    // the row's maximum and sum, each warp for itself, in one order; the least of the segments' keys
+    // above -inf, and how many there are
+    for (int i = lane; i < last; i += 32) m = fmaxf(m, of_stream[i].m);
     m = warp_max(m);
-    low = -warp_max(-low);
-    count = __reduce_add_sync(0xffffffffu, count) / plan.lanes;
     const float ref = m == -INFINITY ? 0.f : m;
     for (int i = lane; i < last; i += 32) {
         const Stream p = of_stream[i];
         s = fmaf(p.s, p.m == -INFINITY ? 1.f : ex2_approx((p.m - ref) * a.k), s);
     }
     s = warp_sum(s);
+    uint32_t low = ~0u, count = 0;
+    for (int i = tid * 4; i < nseg; i += THREADS * 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(segkey + i);
+        const uint32_t key[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (key[e] > kKeyNegInf) low = min(low, key[e]), ++count;
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (lane == 0) sh.warp_n[warp] = count, sh.warp_low[warp] = low;
     const uint32_t K = static_cast<uint32_t>(a.K);
     int64_t* ids = a.ids + static_cast<int64_t>(row) * a.K;
     float* logp = a.logp + static_cast<int64_t>(row) * a.K;
@@ -518,9 +542,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
     // the segments that reach the bound, then their elements
     __syncthreads();
+    count = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) count += sh.warp_n[w], low = min(low, sh.warp_low[w]);
     uint32_t bound = kKeyNegInf + 1;
-    if (count >= K)
-        bound = segment_bound<THREADS>(segkey, nseg, order_key(low), order_key(m), K, sh);
+    if (count >= K) bound = segment_bound<THREADS>(segkey, nseg, low, order_key(m), K, sh);
     for (int i = tid * 4; i < nseg; i += THREADS * 4) {
         const uint4 v = *reinterpret_cast<const uint4*>(segkey + i);
         const uint32_t key[4] = {v.x, v.y, v.z, v.w};
@@ -583,13 +609,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                     columns[at++] = piece_column(4 * w + bit / 8) + bit % 8;
                 }
     }
-    for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
+    clear_hist<THREADS>(sh);
     __syncthreads();
     const bool searched = n > static_cast<uint32_t>(plan.list);
     if (searched) {
         bound = select_digits<T, THREADS>(x_row, a.V, K, sh, list);
         n = sh.n;
-        for (int b = tid; b < kBins; b += THREADS) sh.hist[b] = 0;
+        clear_hist<THREADS>(sh);
         __syncthreads();
     }
 
@@ -600,6 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     uint32_t arrived[kEach];
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
+        if (q * THREADS >= n) break;
         const uint32_t i = tid + q * THREADS;
         if (i < n) {
             if (!searched) {
@@ -628,6 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     u64* ordered = reinterpret_cast<u64*>(segkey);
 #pragma unroll
     for (int q = 0; q < kEach; ++q) {
+        if (q * THREADS >= n) break;
         const uint32_t i = tid + q * THREADS;
         if (i < n) {
             const u64 el = list[i];
