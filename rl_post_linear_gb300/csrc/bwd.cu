@@ -332,6 +332,7 @@ struct DsKlPolicy {
     using Maps = DsKlMaps;
     static constexpr bool kPairTiles = true;
     static constexpr bool kTileK = false;
+    static constexpr bool kStagedEpi = false;
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = true;    // 256-token units on a CTA pair
     static constexpr int kEpiWarps = 8;       // two column halves per row
@@ -1003,10 +1004,7 @@ __global__ void __launch_bounds__(256)
 // dS_c^T: vocab (M) contiguous, tokens along K; h: hidden (N) contiguous.
 // hilo: the K loop runs over the tokens of the hi plane of dS, then over the
 // same tokens of the lo plane (kBwdChunk columns further on), against h twice.
-// ROWS: rows of the chunk may have a sum that is added before the rounding (of what bf16 left of
-// entries of dS, 2^-9 of them, so bf16 itself).
-template <bool ROWS>
-struct DwPolicyT : SingleRole<true, true> {
+struct DwPolicy : SingleRole<true, true> {
     static constexpr bool kKRemap = true;
     static constexpr bool kCtaPair = true;       // 256-vocab-row tiles on a CTA pair
 
@@ -1021,8 +1019,6 @@ struct DwPolicyT : SingleRole<true, true> {
     const int* dom_flag;           // 0: no dominant class in this chunk (the list was not built)
     const float* dcoef;            // [N] fp32 coefficient of each token's dominant class
     float* dw_out32;               // non-null: dW rows go here in fp32, unrounded [V][H]
-    const int* row_at;             // ROWS: [V] a row's place in row_sum, or -1
-    const __nv_bfloat16* row_sum;  // ROWS: [places][H]
     RowMap rm;                     // compaction: K runs over the compacted rows only
     int N, H, c0, width, num_m, num_n, kblocks;
     float temp;
@@ -1059,7 +1055,6 @@ struct DwPolicyT : SingleRole<true, true> {
     struct EpiState {
         int lo, hi, dlo, dhi, v;
         bool valid;
-        const uint4* sum;          // ROWS: the row's sum, or nullptr
     };
 
     // [lo, hi): the entries of an ascending list equal to v
@@ -1082,12 +1077,7 @@ struct DwPolicyT : SingleRole<true, true> {
         st.valid = vl < width;
         st.v = c0 + vl;
         st.lo = st.hi = st.dlo = st.dhi = 0;
-        st.sum = nullptr;
         if (!st.valid) return;
-        if constexpr (ROWS) {
-            const int at = row_at[st.v];
-            if (at >= 0) st.sum = reinterpret_cast<const uint4*>(row_sum + static_cast<size_t>(at) * H);
-        }
         if (terms) equal_range(sorted_y, N, st.v, st.lo, st.hi);
         if (*dom_flag != 0) equal_range(sorted_dy, N, st.v, st.dlo, st.dhi);
     }
@@ -1095,15 +1085,6 @@ struct DwPolicyT : SingleRole<true, true> {
     __device__ void epi_tile(int u, int, int, uint32_t taddr, EpiState& st) const {
         int m, n;
         unit(u, m, n);
-        uint4 sum[ROWS ? 4 : 1];                   // of the next slice, on its way
-        const auto fetch = [&](int col) {
-            if constexpr (ROWS) {
-                if (st.sum == nullptr || col >= H) return;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
-            }
-        };
-        fetch(n * kTileV);
 #pragma unroll 1
         for (int cc = 0; cc < kTileV / 32; ++cc) {
             uint32_t r[32];
@@ -1113,18 +1094,6 @@ struct DwPolicyT : SingleRole<true, true> {
             float x[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
-            if constexpr (ROWS) {
-                if (st.sum != nullptr) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float add[8];
-                        bf16x8_to_f32(sum[q], add);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[8 * q + j] += add[j];
-                    }
-                }
-                if (cc + 1 < kTileV / 32) fetch(col + 32);
-            }
             for (int i = st.lo; i < st.hi; ++i) {
                 const int t = sorted_t[i];
                 const float coef = __fdiv_rn(grad[t], temp) * ycoef[t];
@@ -1171,6 +1140,165 @@ struct DwPolicyT : SingleRole<true, true> {
     }
 
     __device__ void epi_end(int, int, EpiState&) const {}
+};
+
+// ----------------------------------------------------------------------------- dW for top-K KL
+//
+// The same product (with a lo plane or without), to which rows of the chunk may have a sum that is
+// added before the rounding (what bf16 left of entries of dS, 2^-9 of them, so bf16 itself), and
+// dominant classes.  With few tokens a tile is a few MMAs and the epilogue decides: eight warps, each
+// staging 32 rows x 32 columns in shared memory for a TMA store, instead of four whose threads write
+// their rows themselves (a step of [45, 4096] against V = 151936: 1219 instead of 1390 us).
+struct DwTopkMaps {
+    CUtensorMap a, b;             // dS and h, MN-major
+    CUtensorMap dw;               // dW [V, H], box {32, 32}, no swizzle
+};
+struct DwTopkPolicy : SingleRole<true, true> {
+    using Maps = DwTopkMaps;
+    static constexpr bool kKRemap = true;
+    static constexpr bool kCtaPair = true;
+    static constexpr bool kStagedEpi = true;
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kEpiSmemPerWarp = 4096;   // two slices
+
+    const __nv_bfloat16* hidden;   // [N][H] by token
+    const int* sorted_dy;          // dominant classes of this chunk, ascending
+    const int* sorted_dt;
+    const int* dom_flag;
+    const float* dcoef;
+    const int* row_at;             // [V] a row's place in row_sum, or -1; or nullptr: no sums
+    const __nv_bfloat16* row_sum;  // [places][H]
+    RowMap rm;
+    int N, H, c0, width, num_m, num_n, kblocks;
+    bool hilo;
+
+    __device__ static void prefetch(const Maps& m) {
+        prefetch_tensormap(&m.a);
+        prefetch_tensormap(&m.b);
+        prefetch_tensormap(&m.dw);
+    }
+    __device__ static const CUtensorMap* a_map(const Maps& m, int) { return &m.a; }
+    __device__ static const CUtensorMap* b_map(const Maps& m, int) { return &m.b; }
+    __device__ int num_units() const { return num_m * num_n; }
+    __device__ int k_blocks(int) const {
+        const int kb = rm.n_rows != nullptr ? (max(*rm.n_rows, 1) + 63) / 64 : kblocks;
+        return hilo ? 2 * kb : kb;
+    }
+    __device__ void k_remap(int kb, int nkb, int& a_mn, int& a_k, int&, int& b_k) const {
+        if (hilo && kb >= nkb / 2) {
+            const int j = kb - nkb / 2;
+            a_mn += kBwdChunk;
+            a_k = j * 64;
+            b_k = j * 64;
+        }
+    }
+    __device__ int tiles_in_unit(int) const { return 1; }
+    __device__ void unit(int u, int& m, int& n) const {
+        grouped_unit(u, num_n, num_m, kRasterHiddenTiles, n, m);
+    }
+    __device__ void coords(int u, int, int& a_mn, int& a_k, int& b_mn, int& b_k) const {
+        int m, n;
+        unit(u, m, n);
+        a_mn = m * kUnitM;
+        a_k = 0;
+        b_mn = n * kTileV;
+        b_k = 0;
+    }
+
+    struct EpiState {
+        int dlo, dhi, v;
+        const uint4* sum;          // the row's sum, or nullptr
+    };
+
+    __device__ void epi_begin(int u, int row, int, EpiState& st) const {
+        int m, n;
+        unit(u, m, n);
+        const int vl = m * kUnitM + row;
+        st.v = c0 + vl;
+        st.dlo = st.dhi = 0;
+        st.sum = nullptr;
+        if (vl >= width) return;
+        if (row_at != nullptr) {
+            const int at = row_at[st.v];
+            if (at >= 0)
+                st.sum = reinterpret_cast<const uint4*>(row_sum + static_cast<size_t>(at) * H);
+        }
+        if (*dom_flag != 0) DwPolicy::equal_range(sorted_dy, N, st.v, st.dlo, st.dhi);
+    }
+
+    __device__ void epi_staged(const Maps& maps, int u, int, int row, int half, uint32_t taddr,
+                               EpiState& st, uint8_t* stage) const {
+        int m, n;
+        unit(u, m, n);
+        const int lane = row & 31;
+        const int first = c0 + m * kUnitM + row - lane;     // the warp's first vocabulary row
+        const int begin = half * (kTileV / 64), end = begin + kTileV / 64;
+        uint4 sum[4];                                        // of the next slice, on its way
+        const auto fetch = [&](int col) {
+            if (st.sum == nullptr || col >= H) return;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
+        };
+        fetch(n * kTileV + begin * 32);
+#pragma unroll 1
+        for (int cc = begin; cc < end; ++cc) {
+            uint32_t r[32];
+            tmem_load_32(taddr + cc * 32, r);
+            const int col = n * kTileV + cc * 32;
+            if (col >= H) continue;                          // the whole warp
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            if (st.sum != nullptr) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float add[8];
+                    bf16x8_to_f32(sum[q], add);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[8 * q + j] += add[j];
+                }
+            }
+            if (cc + 1 < end) fetch(col + 32);
+            // tokens whose dominant class that is not listed is v, ascending
+            for (int i = st.dlo; i < st.dhi; ++i) {
+                const int t = sorted_dt[i];
+                const float coef = dcoef[t];
+                const uint4* hr = reinterpret_cast<const uint4*>(
+                    hidden + static_cast<size_t>(t) * H + col);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float hv[8];
+                    bf16x8_to_f32(hr[q], hv);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[8 * q + j] = fmaf(coef, hv[j], x[8 * q + j]);
+                }
+            }
+            // the slot is free once the store before the last has read it; a tile begins with the
+            // first one, whichever the tile before ended with
+            uint8_t* slot = stage + (cc & 1) * 2048;
+            if (lane == 0) {
+                if (cc == begin)
+                    bulk_wait_group_read0();
+                else
+                    bulk_wait_group_read<1>();
+            }
+            __syncwarp();
+            uint4* to = reinterpret_cast<uint4*>(slot + lane * 64);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                to[q] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]),
+                                   pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                                   pack_bf16x2(x[8 * q + 4], x[8 * q + 5]),
+                                   pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(&maps.dw, slot, col, first);    // rows past V are dropped
+                bulk_commit_group();
+            }
+        }
+    }
+    __device__ void epi_end(int, int, int, EpiState&) const {}
 };
 
 // ----------------------------------------------------------------------------- target list
@@ -1355,42 +1483,6 @@ static cudaError_t launch_ds(const BwdStepMaps& maps, const BwdStep& st, int c0,
                        stream);
 }
 
-template <bool ROWS>
-static cudaError_t launch_dw(const BwdStepMaps& maps, const BwdStep& st, int c0, int width,
-                             int num_sms, uint32_t* err, cudaStream_t stream) {
-    const int N = st.N, H = st.H;
-    DwPolicyT<ROWS> pw;
-    pw.grad = st.grad;
-    pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
-    pw.dw = static_cast<__nv_bfloat16*>(st.dweight);
-    pw.sorted_y = st.sorted_y;
-    pw.sorted_t = st.sorted_t;
-    pw.ycoef = st.ycoef;
-    pw.sorted_dy = st.sorted_dy;
-    pw.sorted_dt = st.sorted_dt;
-    pw.dom_flag = st.dom_flags + st.chunk;
-    pw.dcoef = st.dcoef;
-    pw.dw_out32 = st.dw_out32;
-    pw.row_at = ROWS ? st.rows_of->row_at : nullptr;
-    pw.row_sum = ROWS ? static_cast<const __nv_bfloat16*>(st.rows_of->sums) : nullptr;
-    pw.rm = RowMap{st.rows, st.n_rows};
-    pw.N = N;
-    pw.H = H;
-    pw.c0 = c0;
-    pw.width = width;
-    pw.num_m = (width + kUnitM - 1) / kUnitM;
-    pw.num_n = (H + kTileV - 1) / kTileV;
-    pw.kblocks = (N + 63) / 64;
-    pw.temp = st.temp;
-    pw.terms = !st.kl && !st.topk;
-    pw.hilo = st.hilo;
-    // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
-    // writes only dW, which the dh GEMM does not touch
-    // (behind dh_sum_kernel, which does not trigger it, it just starts when that ends)
-    return launch_gemm(maps.ds_mnmajor, maps.h_mnmajor, pw, pw.num_m * pw.num_n, num_sms, err,
-                       stream, kPdlOverlap);
-}
-
 template <bool LO>
 static cudaError_t launch_ds_topk(const BwdStepMaps& maps, const BwdStep& st, int c0, int width,
                                   int num_sms, uint32_t* err, cudaStream_t stream) {
@@ -1537,8 +1629,56 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         return launch_gemm(maps.ds_kmajor, maps.w_mnmajor, pd, pd.num_m * pd.num_n, num_sms, err,
                            stream, kPdlTrigger);
     }
-    return st.rows_of != nullptr ? launch_dw<true>(maps, st, c0, width, num_sms, err, stream)
-                                 : launch_dw<false>(maps, st, c0, width, num_sms, err, stream);
+    if (st.topk) {
+        DwTopkPolicy pw;
+        pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
+        pw.sorted_dy = st.sorted_dy;
+        pw.sorted_dt = st.sorted_dt;
+        pw.dom_flag = st.dom_flags + st.chunk;
+        pw.dcoef = st.dcoef;
+        pw.row_at = st.rows_of != nullptr ? st.rows_of->row_at : nullptr;
+        pw.row_sum = st.rows_of != nullptr ? static_cast<const __nv_bfloat16*>(st.rows_of->sums)
+                                           : nullptr;
+        pw.rm = RowMap{st.rows, st.n_rows};
+        pw.N = N;
+        pw.H = H;
+        pw.c0 = c0;
+        pw.width = width;
+        pw.num_m = (width + kUnitM - 1) / kUnitM;
+        pw.num_n = (H + kTileV - 1) / kTileV;
+        pw.kblocks = (N + 63) / 64;
+        pw.hilo = st.hilo;
+        // (behind dh_sum_kernel, which does not trigger it, it just starts when that ends)
+        return launch_persistent(DwTopkMaps{maps.ds_mnmajor, maps.h_mnmajor, maps.dw_store}, pw,
+                                 pw.num_m * pw.num_n, num_sms, err, stream, kPdlOverlap);
+    }
+    DwPolicy pw;
+    pw.grad = st.grad;
+    pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
+    pw.dw = static_cast<__nv_bfloat16*>(st.dweight);
+    pw.sorted_y = st.sorted_y;
+    pw.sorted_t = st.sorted_t;
+    pw.ycoef = st.ycoef;
+    pw.sorted_dy = st.sorted_dy;
+    pw.sorted_dt = st.sorted_dt;
+    pw.dom_flag = st.dom_flags + st.chunk;
+    pw.dcoef = st.dcoef;
+    pw.dw_out32 = st.dw_out32;
+    pw.rm = RowMap{st.rows, st.n_rows};
+    pw.N = N;
+    pw.H = H;
+    pw.c0 = c0;
+    pw.width = width;
+    pw.num_m = (width + kUnitM - 1) / kUnitM;
+    pw.num_n = (H + kTileV - 1) / kTileV;
+    pw.kblocks = (N + 63) / 64;
+    pw.temp = st.temp;
+    pw.terms = !st.kl;
+    pw.hilo = st.hilo;
+    // dW reads dS, h and the target lists, all complete before the dh GEMM started, and
+    // writes only dW, which the dh GEMM does not touch
+    return launch_gemm(maps.ds_mnmajor, maps.h_mnmajor, pw, pw.num_m * pw.num_n, num_sms, err,
+                       stream, kPdlOverlap);
 }
 
 // ----------------------------------------------------------------------------- dh merge

@@ -165,7 +165,8 @@ __device__ __forceinline__ uint64_t operand_desc_rt(bool mn_major, uint32_t stag
 // CTA pairs: each CTA's epilogue warps take its 128 rows of both accumulators and
 // arrive on the leader's barriers.  Pair policies may set
 // kEpiWarps = 8: two warps per TMEM lane quarter, each given half of the
-// tile's columns (epi_begin / epi_pair / epi_end take the half), so that the
+// tile's columns (epi_begin / epi_pair / epi_end take the half; kStagedEpi does
+// the same for single tiles: epi_staged), so that the
 // epilogue, which the MMA waits for, takes half as long.  epi_pair also gets the
 // kernel's tensor maps and, for a policy with kEpiSmemPerWarp > 0, this warp's
 // slot of that many bytes of shared memory (after the ring), e.g. to stage a tile
@@ -181,6 +182,7 @@ struct SingleRole {
     using Maps = TwoMaps;
     static constexpr bool kPairTiles = false;
     static constexpr bool kTileK = false;
+    static constexpr bool kStagedEpi = false;
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = false;
     static constexpr int kEpiWarps = 4;
@@ -485,7 +487,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
         bool ok = true;
         for (int u = wg; ok && u < units; u += num_wg) {
             typename P::EpiState st;
-            if constexpr (P::kPairTiles)
+            if constexpr (P::kPairTiles || P::kStagedEpi)
                 p.epi_begin(u, prow, half, st);
             else
                 p.epi_begin(u, prow, st);
@@ -521,7 +523,11 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                     }
                 } else {
                     tc_fence_after();
-                    p.epi_tile(u, q, prow, taddr_row + buf * kBN, st);
+                    if constexpr (P::kStagedEpi)
+                        p.epi_staged(maps, u, q, prow, half, taddr_row + buf * kBN, st,
+                                     epi_smem + (warp - 2) * P::kEpiSmemPerWarp);
+                    else
+                        p.epi_tile(u, q, prow, taddr_row + buf * kBN, st);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                 }
             }
             if (!ok) break;
-            if constexpr (P::kPairTiles)
+            if constexpr (P::kPairTiles || P::kStagedEpi)
                 p.epi_end(u, prow, half, st);
             else
                 p.epi_end(u, prow, st);

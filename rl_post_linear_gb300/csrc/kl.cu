@@ -50,6 +50,7 @@ struct KlFwdPolicy {
     using Maps = KlMaps;
     static constexpr bool kPairTiles = true;
     static constexpr bool kTileK = false;
+    static constexpr bool kStagedEpi = false;
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = false;
     static constexpr int kEpiWarps = 8;       // two column halves per row
