@@ -433,11 +433,15 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 6)
 // copy runs before.
 template <typename T, int THREADS, int WORDS>
 __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
-    process_listed_kernel(const ProcessArgs a, int ranges, int share, int bias_slots, bool copied) {
+    process_listed_kernel(const ProcessArgs args, int ranges, int share, int bias_slots,
+                          bool copied) {
     extern __shared__ uint4 smem[];
     const int r = blockIdx.x / ranges, range = blockIdx.x % ranges, tid = threadIdx.x;
+    ProcessArgs a = args;
     const auto wait = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
-    if (!copied) wait();
+    if (!copied)
+        wait_previous(a.mask, a.tokens, a.lengths, a.prompt_lengths, a.repetition_rows,
+                      a.frequency_rows, a.presence_rows, a.bias_ids, a.bias_values, a.allowed);
     const Row row(a, r);
     const bool few = WORDS == kFewWords || row.len + a.bias <= kFew;
     if ((a.mask != nullptr && a.mask[r] == 0) || (few && range > 0)) {

@@ -81,10 +81,12 @@ constexpr int kListThreads = 128;
 // A block a GEMM row: its tokens in ascending order (Batcher's bitonic network), empty slots
 // behind them, so that the GEMM's epilogue meets them as it walks the columns.
 __global__ void __launch_bounds__(kListThreads)
-    topk_list_kernel(const TopkSlots s, const int* __restrict__ rows,
+    topk_list_kernel(const TopkSlots slots, const int* __restrict__ rows,
                      const int* __restrict__ n_rows, int num_chunks, int size,
                      int2* __restrict__ list, uint16_t* __restrict__ first) {
     __shared__ uint64_t key[kMaxTopK];
+    TopkSlots s = slots;
+    wait_previous(s.ids, rows, n_rows);
     const int i = blockIdx.x;
     if (n_rows != nullptr && i >= *n_rows) return;
     const int64_t* ids = s.ids + static_cast<size_t>(rows != nullptr ? rows[i] : i) * s.K;
@@ -129,9 +131,11 @@ __global__ void __launch_bounds__(kListThreads)
 constexpr int kRows = 8, kGroups = 32;
 
 __global__ void __launch_bounds__(kRows * kGroups)
-    topk_merge_kernel(const TopkSlots s, const float2* __restrict__ partials, int num_chunks,
+    topk_merge_kernel(const TopkSlots args, const float2* __restrict__ partials, int num_chunks,
                       const int* __restrict__ pos_of, float k, float* __restrict__ kl,
                       float* __restrict__ lse, float* __restrict__ logp, uint32_t* err) {
+    TopkSlots s = args;
+    wait_previous(s.ids, s.teacher, s.mask, partials, pos_of, logp);
     __shared__ float s_m[kRows][kGroups + 1];
     __shared__ float s_s[kRows][kGroups + 1];
     const int t0 = blockIdx.x * kRows;
@@ -203,11 +207,13 @@ constexpr int kCoefWarps = 4;
 // near 1 and q near Q: 1 - p comes from expm1, and for the largest q of the row (no other can be
 // near Q) Q - q is the sum of the others.
 __global__ void __launch_bounds__(kCoefWarps * 32)
-    topk_coef_kernel(const TopkSlots s, const float* __restrict__ grad,
+    topk_coef_kernel(const TopkSlots args, const float* __restrict__ grad,
                      const float* __restrict__ logp, const int* __restrict__ rows,
                      const int* __restrict__ n_rows, float temp, float* __restrict__ coef,
                      int* __restrict__ ids_out, float* __restrict__ val, uint32_t* err) {
     extern __shared__ int s_all[];
+    TopkSlots s = args;
+    wait_previous(s.ids, s.teacher, grad, logp, rows, n_rows);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* s_id = s_all + warp * 3 * s.K;
     float* s_q = reinterpret_cast<float*>(s_id + s.K);
@@ -280,6 +286,7 @@ __global__ void __launch_bounds__(256)
     topk_scatter_kernel(const int* __restrict__ ids, const float* __restrict__ val,
                         const int* __restrict__ n_rows, int N, int K, int c0, int width,
                         __nv_bfloat16* __restrict__ ds) {
+    wait_previous(ids, val, n_rows, ds);
     const size_t count = static_cast<size_t>(n_rows != nullptr ? *n_rows : N) * K;
     const size_t step = static_cast<size_t>(gridDim.x) * 256;
     for (size_t e = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; e < count; e += step) {
@@ -318,6 +325,7 @@ __global__ void __launch_bounds__(kRowThreads)
                    int vecs, float* __restrict__ dh_acc) {
     __shared__ int s_id[kMaxTopK + kRowAhead];
     __shared__ float s_rest[kMaxTopK + kRowAhead];
+    wait_previous(ids, val, n_rows, weight);
     const int i = blockIdx.x;
     if (i >= (n_rows != nullptr ? *n_rows : N)) return;
     for (int j = threadIdx.x; j < K + kRowAhead; j += kRowThreads) {
@@ -629,27 +637,24 @@ cudaError_t launch_topk_list(const TopkSlots& slots, const int* rows, const int*
                              int num_chunks, int2* list, uint16_t* first, cudaStream_t stream) {
     int size = 2;
     while (size < slots.K) size *= 2;
-    topk_list_kernel<<<slots.N, kListThreads, 0, stream>>>(slots, rows, n_rows, num_chunks, size,
-                                                           list, first);
-    return cudaGetLastError();
+    return launch_early(topk_list_kernel, dim3(slots.N), kListThreads, 0, stream, nullptr, slots,
+                        rows, n_rows, num_chunks, size, list, first);
 }
 
 cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, int num_chunks,
                               const int* pos_of, float k, float* kl, float* lse, float* logp,
                               uint32_t* err, cudaStream_t stream) {
-    topk_merge_kernel<<<(slots.N + kRows - 1) / kRows, kRows * kGroups, 0, stream>>>(
-        slots, partials, num_chunks, pos_of, k, kl, lse, logp, err);
-    return cudaGetLastError();
+    return launch_early(topk_merge_kernel, dim3((slots.N + kRows - 1) / kRows), kRows * kGroups, 0,
+                        stream, nullptr, slots, partials, num_chunks, pos_of, k, kl, lse, logp, err);
 }
 
 cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const float* logp,
                              const int* rows, const int* n_rows, float temp, float* coef,
                              int* ids, float* val, uint32_t* err, cudaStream_t stream) {
     static_assert(kCoefWarps * 12 * kMaxTopK <= 48 * 1024, "a block's shared memory");
-    topk_coef_kernel<<<(slots.N + kCoefWarps - 1) / kCoefWarps, kCoefWarps * 32,
-                       static_cast<size_t>(kCoefWarps) * 12 * slots.K, stream>>>(
-        slots, grad, logp, rows, n_rows, temp, coef, ids, val, err);
-    return cudaGetLastError();
+    return launch_early(topk_coef_kernel, dim3((slots.N + kCoefWarps - 1) / kCoefWarps),
+                        kCoefWarps * 32, static_cast<size_t>(kCoefWarps) * 12 * slots.K, stream,
+                        nullptr, slots, grad, logp, rows, n_rows, temp, coef, ids, val, err);
 }
 
 cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,
@@ -657,20 +662,16 @@ cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_r
     const size_t blocks = (static_cast<size_t>(N) * K + 255) / 256, most = 152 * 8;
     const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
     __nv_bfloat16* to = static_cast<__nv_bfloat16*>(ds);
-    if (lo)
-        topk_scatter_kernel<true><<<grid, 256, 0, stream>>>(ids, val, n_rows, N, K, c0, width, to);
-    else
-        topk_scatter_kernel<false><<<grid, 256, 0, stream>>>(ids, val, n_rows, N, K, c0, width, to);
-    return cudaGetLastError();
+    return launch_early(lo ? topk_scatter_kernel<true> : topk_scatter_kernel<false>, dim3(grid), 256,
+                        0, stream, nullptr, ids, val, n_rows, N, K, c0, width, to);
 }
 
 cudaError_t launch_topk_dh(const int* ids, const float* val, const int* n_rows, int N, int K,
                            const void* weight, int H, float* dh_acc, cudaStream_t stream) {
     const int vecs = H / 8;
     const dim3 grid(N, (vecs + kRowThreads - 1) / kRowThreads);
-    topk_dh_kernel<<<grid, kRowThreads, 0, stream>>>(ids, val, n_rows, N, K,
-                                                     static_cast<const uint4*>(weight), vecs, dh_acc);
-    return cudaGetLastError();
+    return launch_early(topk_dh_kernel, grid, kRowThreads, 0, stream, nullptr, ids, val, n_rows, N, K,
+                        static_cast<const uint4*>(weight), vecs, dh_acc);
 }
 
 cudaError_t launch_topk_rows(const TopkRows& rows, int chunk, const void* hidden, int H,
