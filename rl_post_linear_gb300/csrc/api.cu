@@ -1178,7 +1178,11 @@ const char* rlk_contract_string(void) {
                               "and dbias summed per block in ascending rows and merged in a "
                               "fixed tree; sampling: weights as integers in units of 2^-46 (2^-41 "
                               "at V = 2^22) of the row's largest, off by 2^-39 and half a unit, "
-                              "64-bit sums, ties to the lowest index";
+                              "64-bit sums, ties to the lowest index; logit processing: fp32, "
+                              "counts as whole numbers, biases in ascending slots; top-k: order "
+                              "by value, then index, sums ordered by V alone; top-K KL: logits "
+                              "scaled by 1 + 1.037e-9 H, dS bf16 with the remainders of listed "
+                              "entries, dh in sub-chunks of 8192 columns, ascending";
 }
 
 const char* rlk_status_string(rlk_status_t status) {
