@@ -705,8 +705,10 @@ rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t
  * whole distribution.  The [N,V] logits are never materialised.
  *
  *   hidden [N,H], weight [V,H]  bf16, row-major, 16-byte aligned; H a multiple of 64
+ *   temperature  1e-4 .. 1e30
  *   teacher_ids  [N,K] int64, in any order; a negative id is an empty slot, an id that a row
- *                names more than once counts with the sum of its weights (1 <= K <= 1024)
+ *                names more than once counts with the sum of its weights (1 <= K <= 1024,
+ *                N K < 2^31 - 2^16)
  *   teacher_logp [N,K] fp32, a: -inf counts 0, values of empty slots are not used.  Without
  *                renormalize exp(a) has to be within fp32.
  *   active_mask  [N] uint8 or NULL; hidden rows of inactive tokens are never read, and they
@@ -723,8 +725,9 @@ rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t
  * of what the tensor cores cut off a logit given back (lse may differ from rlk_linear_logp_fwd's
  * by that, 1e-9 H of a logit); dhidden and dweight are rounded once.  Of dL/ds the entries at the
  * teacher's tokens, and one with p > 1/2, enter the products in fp32 accuracy, the others rounded to
- * bf16 (2^-8 of themselves at most; in about 16 bits for V <= 8192).  kl, lse, logp and dhidden rows do not depend on the batch; dweight
- * is reproducible bit for bit.
+ * bf16 (2^-8 of themselves at most; in about 16 bits for V <= 8192).  kl, lse, logp and dhidden rows
+ * do not depend on the batch; dweight is reproducible bit for bit.  N = 0 returns RLK_OK and writes
+ * nothing, dweight neither.
  */
 size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K);
 rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,

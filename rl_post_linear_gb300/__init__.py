@@ -968,11 +968,15 @@ def rlk_topk_logp(logits, active_mask, temperature, ids, logp, lse, device_error
     _check("rlk_topk_logp", st)
 
 
+def _topk_kl_sizes(hidden, weight, teacher_ids):
+    if hidden.dim() != 2 or weight.dim() != 2 or teacher_ids.dim() != 2:
+        raise ValueError("hidden must be [N, H], weight [V, H] and teacher_ids [N, K]")
+    return *hidden.shape, weight.shape[0], teacher_ids.shape[1]
+
+
 def _need_topk_kl(hidden, weight, teacher_ids, teacher_logp, active_mask, lse, logp, workspace):
     """(n, h, v, k) of the arguments that both directions have."""
-    n, h = hidden.shape
-    v = weight.shape[0]
-    k = teacher_ids.shape[1]
+    n, h, v, k = _topk_kl_sizes(hidden, weight, teacher_ids)
     _need(hidden, torch.bfloat16, "hidden")
     _need(weight, torch.bfloat16, "weight", (v, h))
     _need(teacher_ids, torch.int64, "teacher_ids", (n, k))
@@ -1226,7 +1230,7 @@ def process_logits(logits, tokens=None, lengths=None, prompt_lengths=None, repet
 def topk_logp(logits, k, temperature=1.0, active_mask=None, error_word=None):
     """(ids [N,k] int64, logp [N,k], lse [N]): the k most likely tokens of each row, the likeliest
     first, the lowest index first among equals.  Slots past the tokens above -inf: -1 and -inf."""
-    n = logits.shape[0]
+    n = _need_rows(logits, "logits")[0]
     ids = torch.empty(n, k, dtype=torch.int64, device=logits.device)
     logp = torch.empty(n, k, dtype=torch.float32, device=logits.device)
     lse = torch.empty(n, dtype=torch.float32, device=logits.device)
@@ -1238,8 +1242,7 @@ def linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask=No
                        temperature=1.0, renormalize=False, error_word=None):
     """(kl [N], lse [N], logp [N,K]) fp32: KL of the teacher's top tokens against the head, and
     the head's log-probs of them."""
-    n, h = hidden.shape
-    v, k = weight.shape[0], teacher_ids.shape[1]
+    n, h, v, k = _topk_kl_sizes(hidden, weight, teacher_ids)
     kl, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
     logp = torch.empty(n, k, dtype=torch.float32, device=hidden.device)
     ws = _workspace(rlk_linear_topk_kl_fwd_workspace_bytes(n, h, v, k), hidden.device)
@@ -1251,10 +1254,9 @@ def linear_topk_kl_fwd(hidden, weight, teacher_ids, teacher_logp, active_mask=No
 def linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse, logp,
                        temperature=1.0, renormalize=False, error_word=None):
     """(dhidden[N,H], dweight[V,H]) bf16."""
-    n, h = hidden.shape
-    v, k = weight.shape[0], teacher_ids.shape[1]
+    n, h, v, k = _topk_kl_sizes(hidden, weight, teacher_ids)
     dh = torch.empty_like(hidden)
-    dw = torch.empty_like(weight)
+    dw = torch.empty_like(weight) if n > 0 else torch.zeros_like(weight)
     ws = _workspace(rlk_linear_topk_kl_bwd_workspace_bytes(n, h, v, k), hidden.device)
     rlk_linear_topk_kl_bwd(hidden, weight, teacher_ids, teacher_logp, active_mask, grad_kl, lse,
                            logp, temperature, renormalize, dh, dw, ws, error_word)

@@ -987,6 +987,16 @@ rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t
     return RLK_OK;
 }
 
+// What both directions of the top-K KL check first.  At temperatures above the range the columns that
+// fill up the last tile (logits of -3e38) would count; below it 2^-24 of a logit over T, which the
+// exponents are rounded by, would be many bits, and infinite from 2^31 on (logits of 1.5e5 at 1e-4).
+static rlk_status_t check_topk_kl(int64_t N, int64_t H, int64_t V, int64_t K, double temperature) {
+    RLK_TRY(check_shape(N, H, V, temperature));
+    if (K < 1 || temperature < 1e-4 || temperature > 1e30) return RLK_ERR_INVALID_VALUE;
+    if (K > rlk::kMaxTopK || N * K > kMaxDim) return RLK_ERR_UNSUPPORTED;
+    return RLK_OK;
+}
+
 size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K) {
     if (N < 0 || H < 0 || V < 1 || K < 1) return 0;
     return rlk::TopkKlFwdLayout(N, H, V, K).total;
@@ -1004,9 +1014,7 @@ rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
                                     float* kl_out, float* lse_out, float* logp_out,
                                     void* workspace, size_t workspace_bytes,
                                     uint32_t* device_error_word, cudaStream_t stream) {
-    RLK_TRY(check_shape(N, H, V, temperature));
-    if (K < 1) return RLK_ERR_INVALID_VALUE;
-    if (K > rlk::kMaxTopK) return RLK_ERR_UNSUPPORTED;
+    RLK_TRY(check_topk_kl(N, H, V, K, temperature));
     if (N == 0) return RLK_OK;
     if (hidden == nullptr || weight == nullptr || teacher_ids == nullptr ||
         teacher_logp == nullptr || kl_out == nullptr || lse_out == nullptr || logp_out == nullptr)
@@ -1062,9 +1070,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
                                     void* dhidden, void* dweight, void* workspace,
                                     size_t workspace_bytes, uint32_t* device_error_word,
                                     cudaStream_t stream) {
-    RLK_TRY(check_shape(N, H, V, temperature));
-    if (K < 1) return RLK_ERR_INVALID_VALUE;
-    if (K > rlk::kMaxTopK || N * K > kMaxDim) return RLK_ERR_UNSUPPORTED;
+    RLK_TRY(check_topk_kl(N, H, V, K, temperature));
     if (N == 0) return RLK_OK;
     if (hidden == nullptr || weight == nullptr || teacher_ids == nullptr ||
         teacher_logp == nullptr || grad_kl == nullptr || lse == nullptr || logp == nullptr ||

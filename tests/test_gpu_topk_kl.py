@@ -348,3 +348,56 @@ def test_captured_step():
     torch.cuda.synchronize()
     for got, want in zip(out, step()):
         assert same_bits(got, want)
+
+
+def test_no_rows():
+    hid, w, ids, a = (x.to(dev()) for x in problem(3, 64, 300, 4, 22))
+    hid = hid[:0].clone().requires_grad_()
+    w.requires_grad_()
+    kl = rlk.linear_topk_kl(hid, w, ids[:0], a[:0])
+    kl.sum().backward()
+    assert kl.shape == (0,) and hid.grad.shape == (0, 64) and not bool(w.grad.any())
+
+
+def test_temperatures_at_the_ends_of_their_range():
+    hid, w, ids, a = (x.to(dev()) for x in problem(5, 64, 300, 4, 23))
+    kl, lse, lp = rlk.linear_topk_kl_fwd(hid, w, ids, a, None, 1e30)
+    # every logit is 0: p = 1/300, and the columns that fill the last tile up do not count
+    assert torch.all((lse - np.log(300)).abs() <= LOGP_ATOL)
+    assert torch.all((lp + np.log(300)).abs() <= LOGP_ATOL)
+    g = torch.rand(5, generator=gen(24)).to(dev())
+    for t in (1e30, 1e-4):         # below, 1e-30 too, is refused
+        kl, lse, lp = rlk.linear_topk_kl_fwd(hid, w, ids, a, None, t)
+        dh, dw = rlk.linear_topk_kl_bwd(hid, w, ids, a, None, g, lse, lp, t)
+        for x in (kl, lse, lp, dh, dw):
+            assert bool(torch.isfinite(x.float()).all())
+
+
+def test_two_streams():
+    # odd sizes and a mask, each on a stream of its own, against the same calls by themselves
+    many = []
+    for n, v, seed in ((130, 9001, 25), (70, 20000, 26)):
+        hid, w, ids, a = (x.to(dev()) for x in problem(n, 128, v, 9, seed))
+        g = torch.rand(n, generator=gen(seed)).to(dev())
+        mask = (torch.rand(n, generator=gen(seed + 2)) < 0.7).to(torch.uint8).to(dev())
+        many.append((hid, w, ids, a, mask, g))
+
+    def step(hid, w, ids, a, mask, g):
+        kl, lse, lp = rlk.linear_topk_kl_fwd(hid, w, ids, a, mask)
+        return (kl, *rlk.linear_topk_kl_bwd(hid, w, ids, a, mask, g, lse, lp))
+
+    want = [step(*x) for x in many]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in many]
+    got = []
+    for _ in range(5):
+        for x, s in zip(many, streams):
+            with torch.cuda.stream(s):
+                got.append(step(*x))
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(same_bits(p, q) for p, q in zip(out, want[i % 2]))
+
+
+def test_offsets_past_32_bits():
+    check(*problem(70000, 64, 300, 2, 27))       # dS alone: 70000 rows of 2^16 entries

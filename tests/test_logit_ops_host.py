@@ -102,7 +102,8 @@ def test_topk_refusals(lib, kw, status):
 
 
 BOTH = [({"H": 100}, UNSUPPORTED), ({"H": 0}, INVALID), ({"N": -1}, INVALID), ({"V": 0}, INVALID),
-        ({"K": 0}, INVALID), ({"K": 1025}, UNSUPPORTED), ({"T": 0.0}, INVALID),
+        ({"K": 0}, INVALID), ({"K": 1025}, UNSUPPORTED), ({"N": 1 << 21, "K": 1024}, UNSUPPORTED),
+        ({"T": 0.0}, INVALID), ({"T": 9e-5}, INVALID), ({"T": 1e-30}, INVALID), ({"T": 1e31}, INVALID),
         ({"T": math.nan}, INVALID), ({"hidden": None}, INVALID), ({"weight": None}, INVALID),
         ({"ids": None}, INVALID), ({"teacher": None}, INVALID), ({"lse": None}, INVALID),
         ({"logp": None}, INVALID), ({"hidden": FAKE + 8}, INVALID),
@@ -160,3 +161,10 @@ def test_binding_refuses_what_it_cannot_pass_on(lib):
         rlk.topk_logp(x, 3)
     with pytest.raises((TypeError, ValueError)):
         rlk.linear_topk_kl(x.bfloat16(), x.bfloat16(), ids, torch.zeros(4, 3))
+    h = x.bfloat16()
+    for bad in ((h, h, ids[0], torch.zeros(3)), (h[0], h, ids, torch.zeros(4, 3)),
+                (h, h[0], ids, torch.zeros(4, 3))):
+        with pytest.raises(ValueError, match=r"hidden must be \[N, H\]"):
+            rlk.linear_topk_kl(*bad)
+    with pytest.raises(ValueError):
+        rlk.topk_logp(x[0], 3)
