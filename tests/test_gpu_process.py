@@ -342,3 +342,41 @@ def test_captured_with_the_draw(n):
         want = rlk.sample_logits(rlk.process_logits(x, t, full, prompt, 1.2, 0.1, 0.1), u, 0.8,
                                  top_p=0.9)[0]
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_offsets_past_32_bits(dtype, many):
+    # many: more than 152 ranges, so two launches, of rows that the mask leaves out but for four
+    n, v = (200 if many else 4), 5003
+    apart = (1 << 32) // n
+    room = torch.empty((n - 1) * apart + v, dtype=dtype, device=dev())
+    x = room.as_strided((n, v), (apart, 1))
+    dense = logits(n, v, 62, dtype)
+    x.copy_(dense)
+    mask = torch.zeros(n, dtype=torch.uint8, device=dev())
+    mask[[0, 1, n - 2, n - 1]] = 1
+    t, full, prompt = history(n, v, 90, 63)
+    want = rlk.process_logits(dense, t, full, prompt, 1.2, 0.1, 0.3, active_mask=mask)
+    assert same_bits(rlk.process_logits(x, t, full, prompt, 1.2, 0.1, 0.3, active_mask=mask), want)
+    rlk.process_logits(x, t, full, prompt, 1.2, 0.1, 0.3, active_mask=mask, out=x)
+    assert same_bits(x[mask != 0], want[mask != 0]) and same_bits(x[mask == 0], dense[mask == 0])
+
+
+def test_two_streams():
+    calls = []
+    for n, v, seed in ((300, 9001, 64), (40, 50021, 65)):
+        x = logits(n, v, seed, torch.bfloat16)
+        t, full, prompt = history(n, v, 200, seed)
+        calls.append((x, t, full, prompt, 1.3, 0.2, 0.1))
+    want = [rlk.process_logits(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(10):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                got.append(rlk.process_logits(*c))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert same_bits(y, want[i % 2])

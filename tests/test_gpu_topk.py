@@ -169,3 +169,14 @@ def test_two_streams_and_a_captured_call():
     graph.replay()
     ref = rlk.topk_logp(x, 20)
     assert torch.equal(out[0], ref[0]) and same_bits(out[1], ref[1]) and same_bits(out[2], ref[2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_offsets_past_32_bits(dtype):
+    v, apart = 5003, 1 << 30
+    room = torch.empty(3 * apart + v, dtype=dtype, device=dev())
+    x = room.as_strided((4, v), (apart, 1))
+    x.copy_(torch.randn(4, v, generator=gen(61)))
+    want = rlk.topk_logp(x.clone(), 20)
+    for got, w in zip(rlk.topk_logp(x, 20), want):
+        assert same_bits(got, w)
