@@ -710,9 +710,9 @@ cudaError_t launch_typed(const T* logits, const TopkArgs& a, cudaStream_t stream
     p.streams = p.units >= 256 ? 128 : 64;
     p.lanes = p.halves = 1;
     if (p.units * 32 < 4 * a.K) p.halves = 2;
-    // 16 segments for each element that is looked for leave few others among the K largest of
-    // their maxima; more of them cost more than they save (K = 64 of [2048, 151936] bf16: 4768
-    // segments 129 us, 1192 of them 118).
+    // 32 segments and more for each element that is looked for leave few others among the K
+    // largest of their maxima; more of them cost more than they save (K = 64 of [2048, 151936] bf16:
+    // 4768 segments 131 us, 2384 of them 125, 1192 126).
     while (p.units * 32 * p.halves / p.lanes > kMaxSegments ||
            (p.halves == 1 && p.lanes < 32 &&
             p.units * 32 / (2 * p.lanes) >= std::max(1024, 32 * a.K)))
