@@ -9,27 +9,29 @@
 //   x = x + sum of the biases of v   (ascending slots)
 //   x = -inf                         where the mask's bit of v is 0
 //
-// Bound by HBM for many rows.  The logits are copied through the mask, and then the listed columns
-// alone are changed in the output: a copy that tests each column took 102 us for [256, 151936] fp32
-// with 3000 tokens a row, a copy alone 48.  A call in place reads and writes no more than what
-// changes.
+// Bound by HBM for many rows, by latency for few.  A block copies a range of columns through the
+// mask; it counts the row's tokens that fall into the range in a table in shared memory (16 bits a
+// column) while its first loads are on their way.  Where tokens and biases are few (1 to kSparse
+// columns, at most), the first to name a column also puts it on a list, and the block reads the
+// list's logits while it copies, and changes them behind a barrier: [64, 129280] bf16 with a mask,
+// 512 tokens and 64 biases 11.7 us, by a look into the table for each column 13.9.  Where they are
+// many that look costs less, and the changed value is taken from the loaded ones: [33, 50021] with
+// 20000 tokens 16 us, by the list 31.
 //
-// Few rows take one launch: a block copies a range of columns, counts the row's tokens that fall
-// into it in a table in shared memory (16 bits a column), and changes its listed columns.  Rows of
-// which two ranges do not fit the SMs at a time take two launches, the copy and a block for each
-// row's listed columns, which counts while the copy ends ([256, 151936] fp32 with 3000 tokens a row
-// 70 us; in one launch, in turns, 87; a block that copies a row and changes it, 89).  A row of up to
-// kFew tokens and biases is counted in a hash table of the columns; a longer one in a table of 16
-// bits a column, part by part of the row, where the thread that takes a column's word out of the
-// table changes that column.  Each block reads all of its row's tokens: counting a share of them
-// into the tables of a cluster's blocks was slower, since a text's few common tokens all fall into
-// one table.  Counts are whole numbers, so the order of the atomics does not matter.  A row with
-// more drawn tokens than 14 bits count gets 32 bits a column.
+// Few rows get ranges for all SMs and 1024 threads a block.  Many rows get ranges of kRange columns
+// and 256 threads: [1024, 32003] fp32 with 1000 tokens 62 us.  Each block reads all of its row's
+// tokens, so a long vocabulary with few tokens takes two launches, the copy and a block for each
+// row's listed columns, which counts while the copy ends: [256, 151936] fp32 with 500 tokens 55 us, in
+// ranges 60; with 4096 71 and 70; with 15000 121 and 100; [1024, 32003] with 500 61 and 52.  The
+// same launch changes rows in place, where nothing else is copied.  It counts up to kFew tokens
+// and biases in a hash table of the columns; more in a table of 16 bits a column, part by part of
+// the row, where the thread that takes a column's word out of the table changes that column.
+// Counting a share of the tokens into the tables of a cluster's blocks was slower, since a text's few
+// common tokens all fall into one table.  Counts are whole numbers, so the order of the atomics does
+// not matter.  A row with more drawn tokens than 14 bits count gets 32 bits a column.
 //
-// Measured: [1, 151936] fp32 with 2000 tokens 7.6 us; [64, 129280] bf16 with a mask, 512 tokens and
-// 64 biases 14.4 (HBM's floor 5); [33, 50021] with 15000 tokens 25, most of it the tokens' rounds
-// through one block; the 70 above are the copy's 48 and the listed columns' 22, whose lines have
-// left L2.
+// Measured: [1, 151936] fp32 with 2000 tokens 6.9 us; the 71 above are the copy's 48 and the listed
+// columns' 22, whose lines have left L2.
 //
 // Groups of 16 bytes follow the alignment of the output row.
 #include <cuda_bf16.h>
@@ -47,9 +49,13 @@ namespace {
 constexpr int kFew = 4096;               // tokens and biases that the hash table takes
 constexpr int kFewWords = 4 * kFew;      // for two slots each
 constexpr int kWords = 40960;            // of any other table: a block has an SM to itself
+constexpr int kRoom = 16;                // columns of a table in front of a range and behind it
+constexpr int kRange = 24576;            // columns of a block where there are many rows
+constexpr int kSparse = 32;              // columns for each token and bias, where these are few
 constexpr int kMaxNarrow = 0x3fff;       // drawn tokens that 16 bits a column count
 constexpr int kUnroll = 4;               // groups a thread has on their way
 constexpr int kTokens = 4;               // and tokens
+constexpr int kHeld = 2;                 // and listed columns
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -65,14 +71,39 @@ struct Table {
     __device__ __forceinline__ int width() const { return wide ? 32 : 16; }
     __device__ __forceinline__ uint32_t* word(int i) const { return words + (wide ? i : i >> 1); }
     __device__ __forceinline__ int shift(int i) const { return wide ? 0 : (i & 1) * 16; }
-    __device__ __forceinline__ void add(int i, bool drawn) const {
-        if (drawn)
-            atomicAdd(word(i), 1u << shift(i));
-        else
-            atomicOr(word(i), 1u << (shift(i) + width() - 1));
+    // whether nothing had named the column
+    __device__ __forceinline__ bool add(int i, bool drawn) const {
+        const uint32_t old = drawn ? atomicAdd(word(i), 1u << shift(i))
+                                   : atomicOr(word(i), 1u << (shift(i) + width() - 1));
+        return (wide ? old : old >> shift(i) & 0xffffu) == 0;
     }
-    __device__ __forceinline__ void mark_biased(int i) const {
-        atomicOr(word(i), 1u << (shift(i) + width() - 2));
+    __device__ __forceinline__ bool mark_biased(int i) const {
+        const uint32_t old = atomicOr(word(i), 1u << (shift(i) + width() - 2));
+        return (wide ? old : old >> shift(i) & 0xffffu) == 0;
+    }
+    __device__ __forceinline__ uint32_t get(int i) const {
+        return wide ? words[i] : reinterpret_cast<const uint16_t*>(words)[i];
+    }
+    // bit i: column at + i of VEC is listed; at is a multiple of VEC
+    template <int VEC>
+    __device__ __forceinline__ uint32_t listed(int at) const {
+        uint32_t bits = 0;
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) bits |= words[at + i] != 0 ? 1u << i : 0u;
+        } else {
+            uint32_t w[VEC / 2];
+            if constexpr (VEC == 4)
+                *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(words + at / 2);
+            else
+                *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(words + at / 2);
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                bits |= (w[i] & 0xffffu) != 0 ? 1u << 2 * i : 0u;
+                bits |= (w[i] >> 16) != 0 ? 2u << 2 * i : 0u;
+            }
+        }
+        return bits;
     }
     // the column's word, which is 0 from then on
     __device__ __forceinline__ uint32_t take(int i) const {
@@ -252,8 +283,12 @@ struct Copy {
             }
         }
     }
-    __device__ __forceinline__ void store(int g0) {
+    // and to the output; LISTED: with what the table and the biases change
+    template <bool LISTED>
+    __device__ __forceinline__ void store(int g0, const Row& row, const Table& table,
+                                          const Biases& biases) {
         uint32_t bits[kUnroll];                  // bit i: column i of the group is open
+        uint32_t listed = 0;                     // bit q VEC + i
 #pragma unroll
         for (int q = 0; q < kUnroll; ++q) {
             const int g = g0 + q * THREADS, c = lo - pad + g * VEC;
@@ -263,6 +298,26 @@ struct Copy {
             const uint32_t w1 = static_cast<uint32_t>(allowed[c1 >> 5]);
             const uint32_t w2 = pad != 0 ? static_cast<uint32_t>(allowed[c2 >> 5]) : w1;
             bits[q] = c >= 0 ? __funnelshift_r(w1, w2, c & 31) : w1 << -c;
+        }
+        constexpr uint32_t kAll = (1u << VEC) - 1;
+        if constexpr (LISTED) {
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int g = g0 + q * THREADS;
+                if (g < groups)
+                    listed |= (table.template listed<VEC>(g * VEC) & bits[q] & kAll) << q * VEC;
+            }
+        }
+        // in place a group that is open in part is read here; others are not needed
+        const auto loaded = [&](int q) {
+            const int g = g0 + q * THREADS;
+            return g < groups && (bits[q] & kAll) != 0 && (bits[q] & kAll) != kAll && whole(g);
+        };
+        if (in_place && allowed != nullptr) {
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q)
+                if (loaded(q))
+                    v[q] = *reinterpret_cast<const uint4*>(x + (lo - pad + (g0 + q * THREADS) * VEC));
         }
 #pragma unroll
         for (int q = 0; q < kUnroll; ++q) {
@@ -275,8 +330,7 @@ struct Copy {
                 for (int i = 0; i < VEC; ++i)
                     if (!((bits[q] >> i) & 1u)) put(e[i], -INFINITY);
             }
-            constexpr uint32_t kAll = (1u << VEC) - 1;
-            const bool all = !in_place || (bits[q] & kAll) == 0;
+            const bool all = !in_place || (bits[q] & kAll) == 0 || loaded(q);
             if (all && whole(g)) {
                 *reinterpret_cast<uint4*>(to) = v[q];
             } else {
@@ -287,6 +341,35 @@ struct Copy {
                 }
             }
         }
+        if constexpr (LISTED) {
+            for (; listed != 0; listed &= listed - 1) {
+                const int b = __ffs(listed) - 1;
+                const int at = (g0 + b / VEC * THREADS) * VEC + b % VEC;
+                change(at, in_place ? to_f32(out[lo - pad + at]) : value(b), row, table, biases);
+            }
+        }
+    }
+    // the column at `at` of the table, whose logit is f
+    __device__ __forceinline__ void change(int at, float f, const Row& row, const Table& table,
+                                           const Biases& biases) {
+        const uint32_t biased = 1u << (table.width() - 2), w = table.get(at);
+        const int c = lo - pad + at;
+        put(out[c], row.change(f, w & (biased - 1), (w & ~biased) != 0,
+                               (w & biased) ? biases.find(c) : 0.f));
+    }
+    // the loaded value of column b % VEC of group b / VEC, by selection
+    __device__ __forceinline__ float value(int b) const {
+        const int i = b * int(sizeof(T)) / 4;
+        uint32_t w[4 * kUnroll];
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q)
+            w[4 * q] = v[q].x, w[4 * q + 1] = v[q].y, w[4 * q + 2] = v[q].z, w[4 * q + 3] = v[q].w;
+#pragma unroll
+        for (int half = 2 * kUnroll; half > 0; half >>= 1)
+#pragma unroll
+            for (int j = 0; j < half; ++j) w[j] = (i & half) ? w[j + half] : w[j];
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[0]);
+        return __uint_as_float((b & 1) ? w[0] & 0xffff0000u : w[0] << 16);
     }
     // begin() has the first loads on their way
     __device__ __forceinline__ void begin(int from, int to) {
@@ -294,10 +377,12 @@ struct Copy {
         groups = lo < hi ? (hi - lo + pad + VEC - 1) / VEC : 0;
         if (!in_place) load(threadIdx.x);
     }
-    __device__ __forceinline__ void finish() {
-        if (in_place && allowed == nullptr) return;
+    template <bool LISTED>
+    __device__ __forceinline__ void finish(const Row& row, const Table& table,
+                                           const Biases& biases) {
+        if (!LISTED && in_place && allowed == nullptr) return;
         for (int g0 = threadIdx.x; g0 < groups; g0 += kUnroll * THREADS) {
-            store(g0);
+            store<LISTED>(g0, row, table, biases);
             if (!in_place && g0 + kUnroll * THREADS < groups) load(g0 + kUnroll * THREADS);
         }
     }
@@ -306,21 +391,26 @@ struct Copy {
     }
 };
 
-// The listed columns of [lo, hi), by a table that has room for them.
+// The listed columns of [lo, hi), by a table that has room for them, column lo at `pad`.
 template <typename T, int THREADS>
 struct Listed {
     const Row& row;
     Table table;
     Biases biases;
-    int slots, V, num_biases, lo, hi;
+    int slots, V, num_biases, pad, lo, hi;
+    uint32_t* list;                      // which columns have been named, by their places in the
+    uint32_t* listed;                    // table, and how many
 
+    // and for what a group reads past the last column
     __device__ __forceinline__ void clear() {
-        const int words = table.wide ? hi - lo : (hi - lo + 1) / 2;
+        const int room = hi - lo + pad + 7, words = table.wide ? room : (room + 1) / 2;
         for (int i = threadIdx.x; i < (words + 3) / 4; i += THREADS)
             reinterpret_cast<uint4*>(table.words)[i] = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; i < slots; i += THREADS) biases.key[i] = kFree;
+        if (listed != nullptr && threadIdx.x == 0) *listed = 0;
     }
-    // counts the tokens and enters the biases; the thread's error bits
+    // counts the tokens and enters the biases; the thread's error bits.  LIST: with a list
+    template <bool LIST>
     __device__ __forceinline__ uint32_t count() {
         uint32_t bad = 0;
         for (int i0 = threadIdx.x; i0 < row.len; i0 += 2 * kTokens * THREADS) {
@@ -331,22 +421,27 @@ struct Listed {
 #pragma unroll
             for (int q = 0; q < 2 * kTokens; ++q) {
                 if (id[q] >= V) bad |= RLK_DEVERR_TARGET_RANGE;
-                if (id[q] >= lo && id[q] < hi)
-                    table.add(static_cast<int>(id[q]) - lo, i0 + q * THREADS >= row.prompt);
+                if (id[q] >= lo && id[q] < hi) {
+                    const int at = static_cast<int>(id[q]) - lo + pad;
+                    const bool first = table.add(at, i0 + q * THREADS >= row.prompt);
+                    if (LIST && first) list[atomicAdd(listed, 1u)] = at;
+                }
             }
         }
         for (int i = threadIdx.x; i < num_biases; i += THREADS) {
             const int64_t id = row.bias_ids[i];
             if (id >= V) bad |= RLK_DEVERR_TARGET_RANGE;
             if (id < lo || id >= hi) continue;
-            table.mark_biased(static_cast<int>(id) - lo);
+            const bool first = table.mark_biased(static_cast<int>(id) - lo + pad);
+            if (LIST && first)
+                list[atomicAdd(listed, 1u)] = static_cast<int>(id) - lo + pad;
             biases.insert(static_cast<uint32_t>(id), row.bias[i]);
         }
         return bad;
     }
-    // after a barrier
+    // after a barrier; pad = 0
     __device__ __forceinline__ void change(T* out) {
-        biases.add_up<THREADS>(slots, row, num_biases);
+        biases.template add_up<THREADS>(slots, row, num_biases);
         visit(out, row.tokens, row.len);
         visit(out, row.bias_ids, num_biases);
     }
@@ -379,12 +474,14 @@ struct Listed {
     }
 };
 
-// A block copies a range of a row and, LISTED, changes its listed columns.  share: columns of a
-// block, a multiple of 32.
+// A block copies a range of a row, LISTED: with its listed columns changed.  share: columns of a
+// block, a multiple of 32; words: of its table; few_most: tokens and biases with which it lists them.
 template <typename T, int THREADS, bool LISTED>
-__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 6)
-    process_kernel(const ProcessArgs args, int ranges, int share, int bias_slots) {
-    extern __shared__ uint4 smem[];              // the table, then the biases
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : LISTED ? 4 : 6)
+    process_kernel(const ProcessArgs args, int ranges, int share, int bias_slots, int words,
+                   int few_most) {
+    extern __shared__ uint4 smem[];              // the table, the biases, the list
+    __shared__ uint32_t s_listed;
     ProcessArgs a = args;
     const int r = blockIdx.x / ranges, range = blockIdx.x % ranges;
     wait_previous(a.x, a.mask, a.tokens, a.lengths, a.prompt_lengths, a.repetition_rows,
@@ -396,32 +493,59 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 6)
     const Row row(a, r);
     Copy<T, THREADS> copy(a, r, row.allowed);
     const int first = range * share, end = min(a.V, first + share);
+    uint32_t* own = reinterpret_cast<uint32_t*>(smem);
+    const Table table{own, row.len - row.prompt > kMaxNarrow};
+    const Biases biases(own + words, bias_slots);
     if constexpr (!LISTED) {
         copy.begin(first, end);
         if (row.bad == 0) {
-            copy.finish();
+            copy.template finish<false>(row, table, biases);
         } else {
             if (range == 0 && threadIdx.x == 0 && a.err != nullptr) atomicOr(a.err, row.bad);
             copy.fill_nan();
         }
     } else {
-        uint32_t* words = reinterpret_cast<uint32_t*>(smem);
-        Listed<T, THREADS> listed{row, Table{words, row.len - row.prompt > kMaxNarrow},
-                                  Biases(words + kWords, bias_slots), bias_slots, a.V, a.bias, 0, 0};
-        const int part = listed.table.wide ? kWords : 2 * kWords;
-        for (int lo = first; lo < first + share; lo += part) {
+        uint32_t* list = own + words + 2 * bias_slots;
+        Listed<T, THREADS> listed{row, table, biases, bias_slots, a.V, a.bias, copy.pad, 0, 0,
+                                  list, &s_listed};
+        const bool few = row.len + a.bias <= few_most;
+        const int part = ((table.wide ? words : 2 * words) - kRoom) / 32 * 32;
+        for (int lo = first; lo < end; lo += part) {
             listed.lo = lo, listed.hi = min(end, lo + part);
             copy.begin(lo, listed.hi);
             listed.clear();
             __syncthreads();
-            const uint32_t bad = row.bad | listed.count();
-            copy.finish();
-            // all tokens are counted, and the columns are there
+            const uint32_t bad = row.bad | (few ? listed.template count<true>()
+                                                : listed.template count<false>());
             if (__syncthreads_or(bad != 0)) {
                 if (bad != 0 && range == 0 && a.err != nullptr) atomicOr(a.err, bad);
                 copy.fill_nan();
             } else {
-                listed.change(copy.out);
+                biases.template add_up<THREADS>(bias_slots, row, a.bias);
+                if (few) {
+                    const int n = static_cast<int>(s_listed);
+                    // a thread's first kHeld are read while the row is copied
+                    int at[kHeld];
+                    float f[kHeld];
+#pragma unroll
+                    for (int q = 0; q < kHeld; ++q) {
+                        const int i = threadIdx.x + q * THREADS;
+                        at[q] = i < n ? list[i] : -1;
+                        if (at[q] >= 0 && !row.open(lo - copy.pad + at[q])) at[q] = -1;
+                        if (at[q] >= 0) f[q] = to_f32(copy.x[lo - copy.pad + at[q]]);
+                    }
+                    copy.template finish<false>(row, table, biases);
+                    __syncthreads();
+#pragma unroll
+                    for (int q = 0; q < kHeld; ++q)
+                        if (at[q] >= 0) copy.change(at[q], f[q], row, table, biases);
+                    for (int i = threadIdx.x + kHeld * THREADS; i < n; i += THREADS) {
+                        const int at = list[i], c = lo - copy.pad + at;
+                        if (row.open(c)) copy.change(at, to_f32(copy.x[c]), row, table, biases);
+                    }
+                } else {
+                    copy.template finish<true>(row, table, biases);
+                }
             }
             __syncthreads();
         }
@@ -518,14 +642,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
         }
     } else {
         Listed<T, THREADS> listed{row, Table{words, row.len - row.prompt > kMaxNarrow}, biases,
-                                  bias_slots, a.V, a.bias, 0, 0};
-        const int part = listed.table.wide ? WORDS : 2 * WORDS;
+                                  bias_slots, a.V, a.bias, 0, 0, 0, nullptr, nullptr};
+        const int part = ((listed.table.wide ? WORDS : 2 * WORDS) - kRoom) / 32 * 32;
         bool waited = !copied;
         for (; lo < end; lo += part) {
             listed.lo = lo, listed.hi = min(end, lo + part);
             listed.clear();
             __syncthreads();
-            bad |= listed.count();
+            bad |= listed.template count<false>();
             broken = __syncthreads_or(bad != 0) != 0;
             if (!waited) wait();
             waited = true;
@@ -552,7 +676,8 @@ struct Ranges {
     }
 };
 
-static_assert(kWords * 4 + 2 * kMaxBias * 8 <= 227 * 1024, "a block's shared memory");
+constexpr int kMostShared = 227 * 1024 - 256;    // of a block, behind what is static
+static_assert(kWords * 4 + 2 * kMaxBias * 8 <= kMostShared, "a block's shared memory");
 int bias_slots(const ProcessArgs& a) {
     if (a.bias == 0) return 0;
     int slots = 2;
@@ -562,19 +687,38 @@ int bias_slots(const ProcessArgs& a) {
 
 template <typename... Params, typename... Args>
 cudaError_t launch(void (*kernel)(const ProcessArgs, int, int, int, Params...), int threads,
-                   const ProcessArgs& a, const Ranges& r, size_t words, cudaStream_t stream,
+                   const ProcessArgs& a, const Ranges& r, size_t words, size_t list, cudaStream_t stream,
                    Args... args) {
     const int64_t blocks = static_cast<int64_t>(a.N) * r.count;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const size_t smem = words * 4 + static_cast<size_t>(words > 0 ? bias_slots(a) : 0) * 8;
+    const size_t smem =
+        words * 4 + static_cast<size_t>(words > 0 ? bias_slots(a) : 0) * 8 + list * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-            static_cast<int>(words * 4 + 2 * kMaxBias * 8));
+            kMostShared);
         if (e != cudaSuccess) return e;
     }
     return launch_early(kernel, dim3(static_cast<unsigned>(blocks)), threads, smem, stream, nullptr,
                         a, r.count, r.share, bias_slots(a), args...);
+}
+
+// Columns that a table of kWords has room for.
+constexpr int kMostColumns = (2 * kWords - kRoom) / 32 * 32;
+
+// few_most: tokens and biases with which a row's listed columns are listed; the list has room for
+// them, or for all of the range's columns.
+template <typename T, int THREADS>
+cudaError_t launch_listed(const ProcessArgs& a, const Ranges& r, cudaStream_t stream) {
+    // a table of 32 bits takes 32 columns at least, all of them where a block has the SM to itself
+    const int narrow = std::max(48, (r.share + kRoom + 31) / 32 * 16);
+    const int words = THREADS == 1024 && a.width > kMaxNarrow
+                          ? std::max(narrow, std::min(kWords, r.share + kRoom)) : narrow;
+    const int room = std::min(THREADS == 1024 ? 4096 : 1024,
+                              (kMostShared - words * 4 - bias_slots(a) * 8) / 4);
+    const int list = std::min(std::min(a.V / kSparse, r.share), room);
+    const int few_most = list == room ? room : a.V / kSparse;
+    return launch(process_kernel<T, THREADS, true>, THREADS, a, r, words, list, stream, words, few_most);
 }
 
 template <typename T>
@@ -583,29 +727,37 @@ cudaError_t launch_rows(const ProcessArgs& a, cudaStream_t stream) {
     if (listed) {
         // as many ranges as give each of 152 SMs one, of 4096 columns at least and the table's size
         // at most
-        const int ranges = std::max((a.V + 2 * kWords - 1) / (2 * kWords),
+        const int ranges = std::max((a.V + kMostColumns - 1) / kMostColumns,
                                     std::min(152 / a.N, (a.V + 4095) / 4096));
         const Ranges r(a.V, (a.V + ranges - 1) / ranges);
         if (static_cast<int64_t>(a.N) * r.count <= 152)
-            return launch(process_kernel<T, 1024, true>, 1024, a, r, kWords, stream);
+            return launch_listed<T, 1024>(a, r, stream);
     }
-    const bool copied = a.x != a.out || a.allowed != nullptr;
+    // ranges, and blocks for all of 152 SMs four times
+    if (listed && a.x != a.out &&
+        (a.V <= 2 * kRange || kSparse * (int64_t(a.width) + a.bias) >= a.V)) {
+        const int ranges = std::max((a.V + kRange - 1) / kRange,
+                                    std::min(608 / a.N, (a.V + 4095) / 4096));
+        const Ranges r(a.V, (a.V + ranges - 1) / ranges);
+        return launch_listed<T, 256>(a, r, stream);
+    }
     // a row that cannot be is found out even where nothing is changed
     const bool checked = a.repetition_rows != nullptr || a.frequency_rows != nullptr ||
                          a.presence_rows != nullptr || a.lengths != nullptr ||
                          a.prompt_lengths != nullptr;
+    const bool copied = a.x != a.out || a.allowed != nullptr;
     if (copied || (!listed && checked)) {
         const cudaError_t e =
-            launch(process_kernel<T, 256, false>, 256, a, Ranges(a.V, 8192), 0, stream);
+            launch(process_kernel<T, 256, false>, 256, a, Ranges(a.V, 8192), 0, 0, stream, 0, 0);
         if (e != cudaSuccess) return e;
     }
     if (!listed) return cudaSuccess;
     if (a.width + a.bias <= kFew)
-        return launch(process_listed_kernel<T, 512, kFewWords>, 512, a, Ranges(a.V, a.V), kFewWords,
+        return launch(process_listed_kernel<T, 512, kFewWords>, 512, a, Ranges(a.V, a.V), kFewWords, 0,
                       stream, copied);
     // a block a row where that is enough of them
-    const Ranges r(a.V, a.N > 152 ? a.V : 2 * kWords);
-    return launch(process_listed_kernel<T, 1024, kWords>, 1024, a, r, kWords, stream, copied);
+    const Ranges r(a.V, a.N > 152 ? a.V : kMostColumns);
+    return launch(process_listed_kernel<T, 1024, kWords>, 1024, a, r, kWords, 0, stream, copied);
 }
 
 }  // namespace

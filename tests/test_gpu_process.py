@@ -380,3 +380,30 @@ def test_two_streams():
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert same_bits(y, want[i % 2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,v,length", [(200, 8001, 90), (200, 8003, 700), (200, 40000, 20000),
+                                        (170, 300001, 5000), (3, 60001, 50), (3, 60001, 3000),
+                                        (160, 31, 40), (160, 33, 40)])
+def test_listed_columns_few_and_many(n, v, length, dtype):
+    # few and many rows, with few tokens for their columns (lists) and many (looks at each column),
+    # counts past 14 bits, tables in parts; a copy, in place, and rows of other alignments
+    t, full, prompt = history(n, v, length, v + length, 0.02)
+    g = gen(length)
+    ids = torch.randint(-1, v, (n, 3), generator=g).to(dev())
+    vals = torch.randn(n, 3, generator=g).to(dev())
+    if length > 16384:
+        prompt[0], t[0, 1::2] = 0, 5                      # 5 is drawn often
+        t[3] = 7
+        full[3], prompt[3] = length, 1
+    mask = torch.zeros(n, dtype=torch.uint8, device=dev())
+    mask[[0, 1, 2, 3 % n, n // 2, n - 2, n - 1]] = 1
+    allow = (torch.rand(n, v, generator=g) < 0.7).to(dev())
+    for a in (None, allow):
+        x = logits(n, v, 70, dtype, pad=3)
+        want = check(x, t, full, prompt, 1.3, 0.2, 0.1, ids, vals, a, mask)
+        same = x.clone()
+        check(same, t, full, prompt, 1.3, 0.2, 0.1, ids, vals, a, mask, same)
+        assert same_bits(same[mask != 0], want[mask != 0])
+        assert same_bits(same[mask == 0], x[mask == 0])
