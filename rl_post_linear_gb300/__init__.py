@@ -879,8 +879,11 @@ def rlk_sample_logits(logits, uniforms, active_mask, temperature, top_k, top_p, 
 
 def _number_or_rows(name, value, n, off):
     """(address, number) of a row's setting: a float32 CUDA tensor [n], or a number."""
+    if type(value) is float:
+        return None, value
     if isinstance(value, torch.Tensor):
         _need(value, torch.float32, name, (n,))
+        _here(value)
         return value.data_ptr(), off
     return None, float(value)
 
@@ -936,8 +939,7 @@ def rlk_process_logits(logits, tokens, lengths, prompt_lengths, repetition, freq
     if active_mask is not None:
         _need(active_mask, torch.uint8, "active_mask", (n,))
     _here(logits, tokens, lengths, prompt_lengths, bias_ids, bias_values, allowed, active_mask, out,
-          device_error_word, *[t for t in (repetition, frequency, presence)
-                               if isinstance(t, torch.Tensor)])
+          device_error_word)
     params = ProcessParams(tok, full, prompt, width, tok_stride, rep_rows, freq_rows, pres_rows,
                            rep, freq, pres, bias, values, biases, words, words_stride)
     st = load().rlk_process_logits(_ptr(logits), _dtype_code(logits, "logits"), n, v, stride,
