@@ -1107,7 +1107,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
     RLK_TRY(make_map(&maps.w_kmajor_pair, weight, H, V, H * 2, 64, rlk::kPairBRows));
     RLK_TRY(make_map(&maps.w_mnmajor, weight, H, V, H * 2, 64, 64));
     RLK_TRY(make_map(&maps.h_mnmajor, gemm_rows, H, N, H * 2, 64, 64));
-    RLK_TRY(make_map(&maps.dw_store, dweight, H, V, H * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE));
+    RLK_TRY(make_map(&maps.dw_store, dweight, H, V, H * 2, 64, 32));
     st.mask = active_mask;
     st.grad = grad_kl;
     st.lse = lse;

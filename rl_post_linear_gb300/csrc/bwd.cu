@@ -333,6 +333,7 @@ struct DsKlPolicy {
     static constexpr bool kPairTiles = true;
     static constexpr bool kTileK = false;
     static constexpr bool kStagedEpi = false;
+    struct EpiCarry {};
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = true;    // 256-token units on a CTA pair
     static constexpr int kEpiWarps = 8;       // two column halves per row
@@ -1151,7 +1152,7 @@ struct DwPolicy : SingleRole<true, true> {
 // their rows themselves (a step of [45, 4096] against V = 151936: 1219 instead of 1390 us).
 struct DwTopkMaps {
     CUtensorMap a, b;             // dS and h, MN-major
-    CUtensorMap dw;               // dW [V, H], box {32, 32}, no swizzle
+    CUtensorMap dw;               // dW [V, H], box {64, 32}, 128-byte swizzle
 };
 struct DwTopkPolicy : SingleRole<true, true> {
     using Maps = DwTopkMaps;
@@ -1159,7 +1160,8 @@ struct DwTopkPolicy : SingleRole<true, true> {
     static constexpr bool kCtaPair = true;
     static constexpr bool kStagedEpi = true;
     static constexpr int kEpiWarps = 8;
-    static constexpr int kEpiSmemPerWarp = 4096;   // two slices
+    static constexpr int kSlice = 64;              // columns that a warp stages at a time
+    static constexpr int kEpiSmemPerWarp = 4096;
 
     const __nv_bfloat16* hidden;   // [N][H] by token
     const int* sorted_dy;          // dominant classes of this chunk, ascending
@@ -1205,25 +1207,37 @@ struct DwTopkPolicy : SingleRole<true, true> {
         b_k = 0;
     }
 
+    // loaded ahead: a unit's wait for its own took as long as a slice
+    struct EpiCarry {
+        bool dominant;             // any class of this chunk
+        int at;                    // the next unit's place in row_sum
+    };
+    __device__ int place(int u, int row) const {
+        if (u < 0 || row_at == nullptr) return -1;
+        int m, n;
+        unit(u, m, n);
+        return m * kUnitM + row < width ? row_at[c0 + m * kUnitM + row] : -1;
+    }
+    __device__ void epi_init(int u, int row, EpiCarry& carry) const {
+        carry.dominant = *dom_flag != 0;
+        carry.at = place(u, row);
+    }
+
     struct EpiState {
-        int dlo, dhi, v;
+        int dlo, dhi;
         const uint4* sum;          // the row's sum, or nullptr
     };
 
-    __device__ void epi_begin(int u, int row, int, EpiState& st) const {
+    __device__ void epi_begin(int u, int next, int row, EpiCarry& carry, EpiState& st) const {
+        st.dlo = st.dhi = 0;
+        st.sum = carry.at < 0 ? nullptr : reinterpret_cast<const uint4*>(
+                                              row_sum + static_cast<size_t>(carry.at) * H);
+        carry.at = place(next, row);
+        if (!carry.dominant) return;
         int m, n;
         unit(u, m, n);
         const int vl = m * kUnitM + row;
-        st.v = c0 + vl;
-        st.dlo = st.dhi = 0;
-        st.sum = nullptr;
-        if (vl >= width) return;
-        if (row_at != nullptr) {
-            const int at = row_at[st.v];
-            if (at >= 0)
-                st.sum = reinterpret_cast<const uint4*>(row_sum + static_cast<size_t>(at) * H);
-        }
-        if (*dom_flag != 0) DwPolicy::equal_range(sorted_dy, N, st.v, st.dlo, st.dhi);
+        if (vl < width) DwPolicy::equal_range(sorted_dy, N, c0 + vl, st.dlo, st.dhi);
     }
 
     __device__ void epi_staged(const Maps& maps, int u, int, int row, int half, uint32_t taddr,
@@ -1232,33 +1246,34 @@ struct DwTopkPolicy : SingleRole<true, true> {
         unit(u, m, n);
         const int lane = row & 31;
         const int first = c0 + m * kUnitM + row - lane;     // the warp's first vocabulary row
-        const int begin = half * (kTileV / 64), end = begin + kTileV / 64;
-        uint4 sum[4];                                        // of the next slice, on its way
+        const int n0 = n * kTileV + half * (kTileV / 2);
+        taddr += half * (kTileV / 2);
+        uint4 sum[8];                                        // of the next slice, on its way
         const auto fetch = [&](int col) {
             if (st.sum == nullptr || col >= H) return;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
+            for (int q = 0; q < 8; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
         };
-        fetch(n * kTileV + begin * 32);
+        fetch(n0);
 #pragma unroll 1
-        for (int cc = begin; cc < end; ++cc) {
-            uint32_t r[32];
-            tmem_load_32(taddr + cc * 32, r);
-            const int col = n * kTileV + cc * 32;
+        for (int cc = 0; cc < kTileV / 2; cc += kSlice) {
+            uint32_t r[2][32];
+            tmem_load_32x2(taddr + cc, r[0], taddr + cc + 32, r[1]);
+            const int col = n0 + cc;
             if (col >= H) continue;                          // the whole warp
-            float x[32];
+            float x[kSlice];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(r[j]);
+            for (int j = 0; j < kSlice; ++j) x[j] = __uint_as_float(r[j / 32][j % 32]);
             if (st.sum != nullptr) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 8; ++q) {
                     float add[8];
                     bf16x8_to_f32(sum[q], add);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[8 * q + j] += add[j];
                 }
             }
-            if (cc + 1 < end) fetch(col + 32);
+            if (cc + kSlice < kTileV / 2) fetch(col + kSlice);
             // tokens whose dominant class that is not listed is v, ascending
             for (int i = st.dlo; i < st.dhi; ++i) {
                 const int t = sorted_dt[i];
@@ -1266,39 +1281,32 @@ struct DwTopkPolicy : SingleRole<true, true> {
                 const uint4* hr = reinterpret_cast<const uint4*>(
                     hidden + static_cast<size_t>(t) * H + col);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 8; ++q) {
                     float hv[8];
                     bf16x8_to_f32(hr[q], hv);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) x[8 * q + j] = fmaf(coef, hv[j], x[8 * q + j]);
                 }
             }
-            // the slot is free once the store before the last has read it; a tile begins with the
-            // first one, whichever the tile before ended with
-            uint8_t* slot = stage + (cc & 1) * 2048;
-            if (lane == 0) {
-                if (cc == begin)
-                    bulk_wait_group_read0();
-                else
-                    bulk_wait_group_read<1>();
-            }
+            if (lane == 0) bulk_wait_group_read0();          // the slot is free
             __syncwarp();
-            uint4* to = reinterpret_cast<uint4*>(slot + lane * 64);
+            // the map's swizzle: a row's 16-byte pieces by its number mod 8
+            uint4* to = reinterpret_cast<uint4*>(stage + lane * 128);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                to[q] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]),
-                                   pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
-                                   pack_bf16x2(x[8 * q + 4], x[8 * q + 5]),
-                                   pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+            for (int q = 0; q < 8; ++q)
+                to[q ^ (lane & 7)] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]),
+                                                pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                                                pack_bf16x2(x[8 * q + 4], x[8 * q + 5]),
+                                                pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(&maps.dw, slot, col, first);    // rows past V are dropped
+                tma_store_2d(&maps.dw, stage, col, first);   // rows past V are dropped
                 bulk_commit_group();
             }
         }
     }
-    __device__ void epi_end(int, int, int, EpiState&) const {}
+    __device__ void epi_end(int, int, EpiState&) const {}
 };
 
 // ----------------------------------------------------------------------------- target list

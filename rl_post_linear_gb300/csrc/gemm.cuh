@@ -166,7 +166,8 @@ __device__ __forceinline__ uint64_t operand_desc_rt(bool mn_major, uint32_t stag
 // arrive on the leader's barriers.  Pair policies may set
 // kEpiWarps = 8: two warps per TMEM lane quarter, each given half of the
 // tile's columns (epi_begin / epi_pair / epi_end take the half; kStagedEpi does
-// the same for single tiles: epi_staged), so that the
+// the same for single tiles: epi_staged, whose epi_begin also gets the next unit and an
+// EpiCarry that epi_init or the unit before loaded ahead), so that the
 // epilogue, which the MMA waits for, takes half as long.  epi_pair also gets the
 // kernel's tensor maps and, for a policy with kEpiSmemPerWarp > 0, this warp's
 // slot of that many bytes of shared memory (after the ring), e.g. to stage a tile
@@ -183,6 +184,7 @@ struct SingleRole {
     static constexpr bool kPairTiles = false;
     static constexpr bool kTileK = false;
     static constexpr bool kStagedEpi = false;
+    struct EpiCarry {};
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = false;
     static constexpr int kEpiWarps = 4;
@@ -247,9 +249,13 @@ constexpr int gemm_threads() {
     return 64 + 32 * P::kEpiWarps;
 }
 
+// where the epilogue warps' slots begin behind the ring (staged: on 1024 bytes, for a swizzle)
+template <class P>
+constexpr uint32_t kEpiOffset = P::kStagedEpi ? 1024 : kBarrierBytes;
+
 template <class P>
 __host__ __device__ constexpr uint32_t gemm_smem_bytes() {
-    return RingShape<P::kCtaPair>::smem_bytes +
+    return RingShape<P::kCtaPair>::smem_bytes - kBarrierBytes + kEpiOffset<P> +
            static_cast<uint32_t>(P::kEpiWarps * P::kEpiSmemPerWarp);
 }
 
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
     uint8_t* a_stages = smem;
     uint8_t* b_stages = smem + S * Ring::a_bytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * Ring::stage_bytes);
-    uint8_t* epi_smem = smem + S * Ring::stage_bytes + kBarrierBytes;   // [kEpiWarps] slots
+    uint8_t* epi_smem = smem + S * Ring::stage_bytes + kEpiOffset<P>;   // [kEpiWarps] slots
     static_assert(gemm_smem_bytes<P>() <= 227 * 1024, "shared memory of the launch");
     uint64_t* full = bars;                    // [S] TMA -> MMA (pair: the even CTA's counts both CTAs' bytes)
     uint64_t* empty = bars + S;               // [S] MMA -> TMA
@@ -485,9 +491,13 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
         const uint32_t taddr_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
         uint32_t tile_i = 0;
         bool ok = true;
+        typename P::EpiCarry carry;
+        if constexpr (P::kStagedEpi) p.epi_init(wg < units ? wg : -1, prow, carry);
         for (int u = wg; ok && u < units; u += num_wg) {
             typename P::EpiState st;
-            if constexpr (P::kPairTiles || P::kStagedEpi)
+            if constexpr (P::kStagedEpi)
+                p.epi_begin(u, u + num_wg < units ? u + num_wg : -1, prow, carry, st);
+            else if constexpr (P::kPairTiles)
                 p.epi_begin(u, prow, half, st);
             else
                 p.epi_begin(u, prow, st);
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                 }
             }
             if (!ok) break;
-            if constexpr (P::kPairTiles || P::kStagedEpi)
+            if constexpr (P::kPairTiles)
                 p.epi_end(u, prow, half, st);
             else
                 p.epi_end(u, prow, st);

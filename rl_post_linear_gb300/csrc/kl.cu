@@ -51,6 +51,7 @@ struct KlFwdPolicy {
     static constexpr bool kPairTiles = true;
     static constexpr bool kTileK = false;
     static constexpr bool kStagedEpi = false;
+    struct EpiCarry {};
     static constexpr bool kKRemap = false;
     static constexpr bool kCtaPair = false;
     static constexpr int kEpiWarps = 8;       // two column halves per row

@@ -262,7 +262,7 @@ struct BwdStepMaps {
     CUtensorMap hr_kmajor;     // KL only: reference hidden [N,Hr], box {64, 128}
     CUtensorMap wr_kmajor;     // KL only: reference weight [V,Hr], box {64, 128} (pair)
     CUtensorMap ds_store;      // KL only: dS [N, width] written by TMA stores, box {32, 32}
-    CUtensorMap dw_store;      // top-K KL only: dW [V, H] written by TMA stores, box {32, 32}
+    CUtensorMap dw_store;      // top-K KL only: dW [V, H] written by TMA stores, box {64, 32}
 };
 
 // One launch of the backward: a role (the dS recompute, the dh GEMM or the dW
