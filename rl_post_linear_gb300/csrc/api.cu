@@ -134,7 +134,8 @@ static rlk_status_t bwd_chunks(rlk::BwdStepMaps& maps, rlk::BwdStep& st, void* d
     for (int c = 0; c < st.num_chunks; ++c) {
         const int64_t width = std::min<int64_t>(rlk::kBwdChunk, V - int64_t(c) * rlk::kBwdChunk);
         const uint64_t inner = uint64_t(width) + (st.hilo ? uint64_t(rlk::kBwdChunk) : 0);
-        RLK_TRY(make_map(&maps.ds_kmajor, ds, inner, N, ld * 2, 64, rlk::kTileM));
+        RLK_TRY(make_map(&maps.ds_kmajor, ds, inner, st.topk ? rlk::map_rows(N) : N, ld * 2, 64,
+                         rlk::kTileM));
         RLK_TRY(make_map(&maps.ds_mnmajor, ds, inner, N, ld * 2, 64, 64));
         if (st.kl)   // the KL dS epilogue writes its tiles with TMA stores
             RLK_TRY(make_map(&maps.ds_store, ds, inner, N, ld * 2, 32, 32,
@@ -1043,8 +1044,13 @@ rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
                                      n_rows, stream));
         gemm_rows = ws + lay.hc_off;
     }
+    rlk::CopyRows copy{};
+    if (active_mask == nullptr && N < rlk::kMinMapRows) {
+        copy = rlk::CopyRows{hidden, ws + lay.hc_off, h};
+        gemm_rows = copy.h_to;
+    }
     CUtensorMap map_h, map_w;
-    RLK_TRY(make_map(&map_h, gemm_rows, H, N, H * 2, 64, rlk::kTileM));
+    RLK_TRY(make_map(&map_h, gemm_rows, H, rlk::map_rows(N), H * 2, 64, rlk::kTileM));
     RLK_TRY(make_map(&map_w, weight, H, V, H * 2, 64, rlk::kPairBRows));
     const float k = rlk::topk_kl_scale(temperature, H);
     float2* partials = reinterpret_cast<float2*>(ws + lay.partial_off);
@@ -1053,7 +1059,7 @@ rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,
     int2* list = reinterpret_cast<int2*>(ws + lay.list_off);
     uint16_t* first = reinterpret_cast<uint16_t*>(ws + lay.first_off);
     RLK_CUDA(rlk::launch_topk_list(slots, rows, n_rows, static_cast<int>(lay.num_chunks), list,
-                                   first, stream));
+                                   first, copy, stream));
     RLK_CUDA(rlk::launch_list_partials(map_h, map_w, n, h, v, static_cast<int>(K), k, partials,
                                        list, first, logp_out, rows, n_rows, device_error_word,
                                        dev.sms, stream));
@@ -1102,8 +1108,13 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
         st.n_rows = n_rows;
         gemm_rows = ws + lay.hc_off;
     }
+    // for the K-major map alone: dW's operands have rows past N as zeros
+    rlk::CopyRows copy{};
+    if (active_mask == nullptr && N < rlk::kMinMapRows)
+        copy = rlk::CopyRows{hidden, ws + lay.hc_off, h};
     rlk::BwdStepMaps maps;
-    RLK_TRY(make_map(&maps.h_kmajor, gemm_rows, H, N, H * 2, 64, rlk::kTileM));
+    RLK_TRY(make_map(&maps.h_kmajor, copy.h_to != nullptr ? copy.h_to : gemm_rows, H,
+                     rlk::map_rows(N), H * 2, 64, rlk::kTileM));
     RLK_TRY(make_map(&maps.w_kmajor_pair, weight, H, V, H * 2, 64, rlk::kPairBRows));
     RLK_TRY(make_map(&maps.w_mnmajor, weight, H, V, H * 2, 64, 64));
     RLK_TRY(make_map(&maps.h_mnmajor, gemm_rows, H, N, H * 2, 64, 64));
@@ -1141,7 +1152,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
     const rlk::TopkSlots slots{teacher_ids, teacher_logp, active_mask, n, static_cast<int>(K), v,
                                renormalize != 0};
     RLK_CUDA(rlk::launch_topk_coef(slots, grad_kl, logp, st.rows, st.n_rows, st.temp, st.ycoef,
-                                   ids, val, device_error_word, stream));
+                                   ids, val, copy, device_error_word, stream));
     // dh depends on V here, not on N: its rows are those of any batch
     st.hilo = lay.lo;
     st.dh_started = V > rlk::kTopkSmallV;

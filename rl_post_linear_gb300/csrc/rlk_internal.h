@@ -130,13 +130,19 @@ inline bool topk_dh_split(int64_t N, int64_t H) {
     return 1.1 * (static_cast<double>(part_waves) / kDhSubs * 192e-6 + parts) <
            static_cast<double>(waves) * 192e-6;
 }
+// Rows that the K-major maps of h and dS have at least: a load of 128 rows of which a map has fewer
+// than 16 takes half as long again (forward of [14, 4096] against V = 151936: 268 us, with two more
+// rows 207).  What is behind the N rows in the workspace does not matter: a row of the products
+// depends on its own row alone, and only N are kept.
+constexpr int64_t kMinMapRows = 16;
+inline int64_t map_rows(int64_t N) { return N < kMinMapRows ? kMinMapRows : N; }
 struct TopkKlBwdLayout : BwdLayout {
     bool lo;
     int64_t tiles, places;
     size_t part_off, ids_off, val_off, key_off[2], slot_off[2], hist_off, first_off, last_off, at_off,
         list_off, many_off, counts_off, sums_off;
     TopkKlBwdLayout(int64_t N, int64_t H, int64_t V, int64_t K)
-        : BwdLayout(N, H, topk_lo_plane(N, H, V, K)), lo(topk_lo_plane(N, H, V, K)) {
+        : BwdLayout(map_rows(N), H, topk_lo_plane(N, H, V, K)), lo(topk_lo_plane(N, H, V, K)) {
         const size_t e = static_cast<size_t>(N) * K, v = static_cast<size_t>(V);
         tiles = static_cast<int64_t>((e + kRadixTile - 1) / kRadixTile);
         places = static_cast<int64_t>(e < kBwdChunk ? e : kBwdChunk);
@@ -496,7 +502,7 @@ struct TopkKlFwdLayout {
         count_off = align_up(blk_off + static_cast<size_t>((N + kCompactBlock - 1) / kCompactBlock) * 4, 256);
         hc_off = align_up(count_off + 4, 256);
         // the rows' tokens in ascending order, and where each vocabulary chunk's begin
-        list_off = align_up(hc_off + static_cast<size_t>(N) * H * 2, 256);
+        list_off = align_up(hc_off + static_cast<size_t>(map_rows(N)) * H * 2, 256);
         first_off = align_up(list_off + static_cast<size_t>(N) * K * 8, 256);
         total = align_up(first_off + static_cast<size_t>(num_chunks) * N * 2, 256);
     }
@@ -525,9 +531,16 @@ cudaError_t launch_list_partials(const CUtensorMap& map_h, const CUtensorMap& ma
                                  const uint16_t* first, float* out, const int* rows,
                                  const int* n_rows, uint32_t* err, int num_sms,
                                  cudaStream_t stream);
+// rows of h that a launch copies (h_to = nullptr: none)
+struct CopyRows {
+    const void* h;
+    void* h_to;
+    int H;
+};
 // by GEMM row: the listed tokens (id, slot) in ascending order, and the chunks' first ones
 cudaError_t launch_topk_list(const TopkSlots& slots, const int* rows, const int* n_rows,
-                             int num_chunks, int2* list, uint16_t* first, cudaStream_t stream);
+                             int num_chunks, int2* list, uint16_t* first, const CopyRows& copy,
+                             cudaStream_t stream);
 // lse, then logp in place of the logits, and kl
 cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, int num_chunks,
                               const int* pos_of, float k, float* kl, float* lse, float* logp,
@@ -535,7 +548,8 @@ cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, in
 // by GEMM row: coef = g Q / T, and the entries of dS at the listed tokens
 cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const float* logp,
                              const int* rows, const int* n_rows, float temp, float* coef,
-                             int* ids, float* val, uint32_t* err, cudaStream_t stream);
+                             int* ids, float* val, const CopyRows& copy, uint32_t* err,
+                             cudaStream_t stream);
 // what bf16 leaves of the entries in dh: dh_acc[i] = sum_k rest(val[i,k]) W[id[i,k]]
 cudaError_t launch_topk_dh(const int* ids, const float* val, const int* n_rows, int N, int K,
                            const void* weight, int H, float* dh_acc, cudaStream_t stream);

@@ -74,6 +74,15 @@ struct RowSlots {
     __device__ __forceinline__ float log_weight(int j) const { return teacher[j] - shift; }
 };
 
+// row i, by `threads` threads
+__device__ __forceinline__ void copy_row(const CopyRows& c, int i, int thread, int threads) {
+    if (c.h_to == nullptr) return;
+    const int vecs = c.H / 8;
+    const size_t from = static_cast<size_t>(i) * vecs;
+    for (int j = thread; j < vecs; j += threads)
+        static_cast<uint4*>(c.h_to)[from + j] = static_cast<const uint4*>(c.h)[from + j];
+}
+
 // ----------------------------------------------------------------------------- list
 
 constexpr int kListThreads = 128;
@@ -83,12 +92,14 @@ constexpr int kListThreads = 128;
 __global__ void __launch_bounds__(kListThreads)
     topk_list_kernel(const TopkSlots slots, const int* __restrict__ rows,
                      const int* __restrict__ n_rows, int num_chunks, int size,
-                     int2* __restrict__ list, uint16_t* __restrict__ first) {
+                     int2* __restrict__ list, uint16_t* __restrict__ first, const CopyRows args) {
     __shared__ uint64_t key[kMaxTopK];
     TopkSlots s = slots;
-    wait_previous(s.ids, rows, n_rows);
+    CopyRows copy = args;
+    wait_previous(s.ids, rows, n_rows, copy.h);
     const int i = blockIdx.x;
     if (n_rows != nullptr && i >= *n_rows) return;
+    copy_row(copy, i, threadIdx.x, kListThreads);
     const int64_t* ids = s.ids + static_cast<size_t>(rows != nullptr ? rows[i] : i) * s.K;
     for (int j = threadIdx.x; j < size; j += kListThreads) {
         const int64_t id = j < s.K ? ids[j] : -1;
@@ -210,16 +221,19 @@ __global__ void __launch_bounds__(kCoefWarps * 32)
     topk_coef_kernel(const TopkSlots args, const float* __restrict__ grad,
                      const float* __restrict__ logp, const int* __restrict__ rows,
                      const int* __restrict__ n_rows, float temp, float* __restrict__ coef,
-                     int* __restrict__ ids_out, float* __restrict__ val, uint32_t* err) {
+                     int* __restrict__ ids_out, float* __restrict__ val, const CopyRows copy_args,
+                     uint32_t* err) {
     extern __shared__ int s_all[];
     TopkSlots s = args;
-    wait_previous(s.ids, s.teacher, grad, logp, rows, n_rows);
+    CopyRows copy = copy_args;
+    wait_previous(s.ids, s.teacher, grad, logp, rows, n_rows, copy.h);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int* s_id = s_all + warp * 3 * s.K;
     float* s_q = reinterpret_cast<float*>(s_id + s.K);
     float* s_sum = s_q + s.K;                    // an id's weights together, at its first slot
     const int i = blockIdx.x * kCoefWarps + warp;
     if (i >= (n_rows != nullptr ? *n_rows : s.N)) return;
+    copy_row(copy, i, lane, 32);
     const int t = rows != nullptr ? rows[i] : i;
     int* out_id = ids_out + static_cast<size_t>(i) * s.K;
     float* out_val = val + static_cast<size_t>(i) * s.K;
@@ -634,11 +648,12 @@ __global__ void __launch_bounds__(1024)
 }  // namespace
 
 cudaError_t launch_topk_list(const TopkSlots& slots, const int* rows, const int* n_rows,
-                             int num_chunks, int2* list, uint16_t* first, cudaStream_t stream) {
+                             int num_chunks, int2* list, uint16_t* first, const CopyRows& copy,
+                             cudaStream_t stream) {
     int size = 2;
     while (size < slots.K) size *= 2;
     return launch_early(topk_list_kernel, dim3(slots.N), kListThreads, 0, stream, nullptr, slots,
-                        rows, n_rows, num_chunks, size, list, first);
+                        rows, n_rows, num_chunks, size, list, first, copy);
 }
 
 cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, int num_chunks,
@@ -650,11 +665,12 @@ cudaError_t launch_topk_merge(const TopkSlots& slots, const float2* partials, in
 
 cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const float* logp,
                              const int* rows, const int* n_rows, float temp, float* coef,
-                             int* ids, float* val, uint32_t* err, cudaStream_t stream) {
+                             int* ids, float* val, const CopyRows& copy, uint32_t* err,
+                             cudaStream_t stream) {
     static_assert(kCoefWarps * 12 * kMaxTopK <= 48 * 1024, "a block's shared memory");
     return launch_early(topk_coef_kernel, dim3((slots.N + kCoefWarps - 1) / kCoefWarps),
                         kCoefWarps * 32, static_cast<size_t>(kCoefWarps) * 12 * slots.K, stream,
-                        nullptr, slots, grad, logp, rows, n_rows, temp, coef, ids, val, err);
+                        nullptr, slots, grad, logp, rows, n_rows, temp, coef, ids, val, copy, err);
 }
 
 cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,

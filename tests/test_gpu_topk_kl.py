@@ -401,3 +401,23 @@ def test_two_streams():
 
 def test_offsets_past_32_bits():
     check(*problem(70000, 64, 300, 2, 27))       # dS alone: 70000 rows of 2^16 entries
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("n,v", [(1, 700), (3, 9001), (15, 40000), (16, 700), (17, 9001)])
+def test_whatever_the_workspace_holds(n, v, masked):
+    # NaN everywhere on entry: nothing of it reaches the results (rows of maps past N, planes of dS)
+    hid, w, ids, a = problem(n, 128, v, 6, 28)
+    mask = (torch.arange(n) % 3 != 1).to(torch.uint8) if masked else None
+    g = torch.randn(n, generator=gen(29)) / n
+    kl, lse, lp, dh, dw = check(hid, w, ids, a, mask, 1.1, False, g)
+    d = [x if x is None else x.to(dev()) for x in (hid, w, ids, a, mask)]
+    for fill in (255, 0):
+        out = [torch.full_like(x, float("nan")) for x in (kl, lse, lp, dh, dw)]
+        ws = [torch.full((max(q(n, 128, v, 6), 256),), fill, dtype=torch.uint8, device=dev())
+              for q in (rlk.rlk_linear_topk_kl_fwd_workspace_bytes,
+                        rlk.rlk_linear_topk_kl_bwd_workspace_bytes)]
+        rlk.rlk_linear_topk_kl_fwd(*d, 1.1, False, *out[:3], ws[0])
+        rlk.rlk_linear_topk_kl_bwd(*d, g.to(dev()), out[1], out[2], 1.1, False, *out[3:], ws[1])
+        for got, want in zip(out, (kl, lse, lp, dh, dw)):
+            assert same_bits(got, want)
