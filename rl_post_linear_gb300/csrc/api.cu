@@ -1156,7 +1156,7 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
     // dh depends on V here, not on N: its rows are those of any batch
     st.hilo = lay.lo;
     st.dh_started = V > rlk::kTopkSmallV;
-    if (rlk::topk_dh_split(N, H)) st.dh_part = reinterpret_cast<float*>(ws + lay.part_off);
+    if (rlk::topk_dh_split(N, H, V)) st.dh_part = reinterpret_cast<float*>(ws + lay.part_off);
     if (st.dh_started)
         RLK_CUDA(rlk::launch_topk_dh(ids, val, st.n_rows, n, st.K, weight, h, st.dh_acc, stream));
     rlk::TopkRows rows_of{};

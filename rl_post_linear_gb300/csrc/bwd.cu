@@ -831,13 +831,12 @@ struct DhPolicy : SingleRole<false, true> {
 
 // ----------------------------------------------------------------------------- dh for top-K KL
 //
-// The chunk's product in sub-chunks of kDhSub vocabulary columns, each accumulated by itself from
+// The chunk's product in sub-chunks of `sub` vocabulary columns, each accumulated by itself from
 // 0 and added to dh_acc in fp32, ascending: a fixed order.  With many tiles a unit is a tile of dh
 // and walks its sub-chunks (the additions overlap the next one's MMAs).  With few, most CTA pairs
 // would idle: a unit is then one sub-chunk of a tile, written to `part`, and dh_sum_kernel adds them
 // in the same order, so that a row's bits do not depend on the batch (a step of [200, 2048] against
 // V = 32003: 242 instead of 341 us).
-constexpr int kDhSub = kBwdChunk / kDhSubs;       // 8192
 struct DhTopkPolicy : SingleRole<false, true> {
     static constexpr bool kKRemap = true;
     static constexpr bool kTileK = true;
@@ -850,7 +849,7 @@ struct DhTopkPolicy : SingleRole<false, true> {
     const int* dom;                // [N] by token
     const float* dcoef;
     RowMap rm;
-    int N, H, c0, width, num_n, subs;
+    int N, H, c0, width, num_n, sub, subs;
     bool first, last, hilo, split;
 
     __device__ int num_units() const { return rm.tiles(N) * num_n * (split ? subs : 1); }
@@ -863,7 +862,7 @@ struct DhTopkPolicy : SingleRole<false, true> {
         m = t / num_n;
         n = t - m * num_n;
     }
-    __device__ int sub_blocks(int s) const { return (min(kDhSub, width - s * kDhSub) + 63) / 64; }
+    __device__ int sub_blocks(int s) const { return (min(sub, width - s * sub) + 63) / 64; }
     __device__ int tile_k_blocks(int u, int q) const {
         int m, n, s;
         unit(u, m, n, s);
@@ -874,9 +873,9 @@ struct DhTopkPolicy : SingleRole<false, true> {
         int m, n, s;
         unit(u, m, n, s);
         a_mn = m * kUnitM;
-        a_k = (s + q) * kDhSub;
+        a_k = (s + q) * sub;
         b_mn = n * kTileV;
-        b_k = c0 + (s + q) * kDhSub;
+        b_k = c0 + (s + q) * sub;
     }
     // the lo plane behind the hi plane, against the same rows of W
     __device__ void k_remap(int kb, int nkb, int&, int& a_k, int&, int& b_k) const {
@@ -1587,7 +1586,8 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pd.c0 = c0;
         pd.width = width;
         pd.num_n = (H + kTileV - 1) / kTileV;
-        pd.subs = (width + kDhSub - 1) / kDhSub;
+        pd.sub = topk_dh_sub(st.V);
+        pd.subs = (width + pd.sub - 1) / pd.sub;
         pd.first = st.chunk == 0 && !st.dh_started;
         pd.last = st.chunk == st.num_chunks - 1;
         pd.hilo = st.hilo && !st.dh_started;

@@ -117,18 +117,36 @@ inline bool topk_lo_plane(int64_t N, int64_t H, int64_t V, int64_t K) {
                         60e-6 * static_cast<double>((V + kBwdChunk - 1) / kBwdChunk);
     return 2.0 * static_cast<double>(N) * static_cast<double>(H) * static_cast<double>(V) / 1.7e15 < sums;
 }
+// The columns of a sub-chunk of dh (DhTopkPolicy), by V alone: a chunk's quarters; the eighths of a
+// vocabulary of one chunk, of which few rows have few tiles to share out, or its quarters where dS
+// has two planes there.  Measured for steps at H = 2048 with these and with 8192 columns: V = 32003, N
+// = 200 189 and 200 us, N = 600 335 and 344, N = 2048 788 and 784; V = 8000, N = 3 93 and 137, N = 4000
+// 518 and 504.
+inline int topk_dh_sub(int64_t V) {
+    if (V > kBwdChunk) return kBwdChunk / 4;
+    const int64_t parts = V > kTopkSmallV ? 8 : 4;
+    const int64_t sub = (V + 64 * parts - 1) / (64 * parts) * 64;
+    return static_cast<int>(sub > 1024 ? sub : 1024);
+}
+inline int topk_dh_subs(int64_t V) {     // of the first chunk, the most
+    const int64_t width = V < kBwdChunk ? V : kBwdChunk;
+    return static_cast<int>((width + topk_dh_sub(V) - 1) / topk_dh_sub(V));
+}
 // Whether the dh GEMM takes the sub-chunks of a vocabulary chunk side by side, in parts that are
-// summed after it (DhTopkPolicy): where that fills the waves of 76 CTA pairs better by more than the
-// parts cost, with a tenth to spare (dW fills part of an idle wave).  A tile takes 192 us for a whole
-// chunk, the parts move at 6.5 TB/s.  Measured for steps of [45, 4096] and V = 151936: 1391 us, one
-// after the other 1791; [500, 4096] 2520 and 2708; [2048, 4096] 6887 and 6822 (not split).
-constexpr int kDhSubs = 4;
-inline bool topk_dh_split(int64_t N, int64_t H) {
+// summed after it: where that fills the waves of 76 CTA pairs better by more than the parts cost, with
+// a tenth to spare (dW fills part of an idle wave).  A tile takes 192 us for a whole chunk of one
+// plane, the parts move at 6.5 TB/s and their sum takes a launch of 3 us.  Measured for steps of [45,
+// 4096] and V = 151936: 1391 us, one after the other 1791; [500, 4096] 2520 and 2708; [2048, 4096]
+// 6887 and 6822 (not split).
+inline bool topk_dh_split(int64_t N, int64_t H, int64_t V) {
+    const int subs = topk_dh_subs(V);
+    const double width = static_cast<double>(V < kBwdChunk ? V : kBwdChunk) / kBwdChunk;
+    const double tile = 192e-6 * width * (V <= kTopkSmallV ? 2 : 1);
     const int64_t tiles = (N + kUnitM - 1) / kUnitM * ((H + kTileV - 1) / kTileV);
-    const int64_t waves = (tiles + 75) / 76, part_waves = (tiles * kDhSubs + 75) / 76;
-    const double parts = static_cast<double>(N) * static_cast<double>(H) * 8 * kDhSubs / 6.5e12;
-    return 1.1 * (static_cast<double>(part_waves) / kDhSubs * 192e-6 + parts) <
-           static_cast<double>(waves) * 192e-6;
+    const int64_t waves = (tiles + 75) / 76, part_waves = (tiles * subs + 75) / 76;
+    const double parts = static_cast<double>(N) * static_cast<double>(H) * 8 * subs / 6.5e12 + 3e-6;
+    return subs > 1 && 1.1 * (static_cast<double>(part_waves) / subs * tile + parts) <
+                           static_cast<double>(waves) * tile;
 }
 // Rows that the K-major maps of h and dS have at least: a load of 128 rows of which a map has fewer
 // than 16 takes half as long again (forward of [14, 4096] against V = 151936: 268 us, with two more
@@ -147,7 +165,8 @@ struct TopkKlBwdLayout : BwdLayout {
         tiles = static_cast<int64_t>((e + kRadixTile - 1) / kRadixTile);
         places = static_cast<int64_t>(e < kBwdChunk ? e : kBwdChunk);
         part_off = total;
-        if (topk_dh_split(N, H)) total = align_up(part_off + static_cast<size_t>(kDhSubs) * N * H * 4, 256);
+        if (topk_dh_split(N, H, V))
+            total = align_up(part_off + static_cast<size_t>(topk_dh_subs(V)) * N * H * 4, 256);
         ids_off = total;
         val_off = align_up(ids_off + e * 4, 256);
         total = align_up(val_off + e * 4, 256);
