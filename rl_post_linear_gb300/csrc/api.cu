@@ -1199,7 +1199,7 @@ const char* rlk_contract_string(void) {
                               "counts as whole numbers, biases in ascending slots; top-k: order "
                               "by value, then index, sums ordered by V alone; top-K KL: logits "
                               "scaled by 1 + 1.037e-9 H, dS bf16 with the remainders of listed "
-                              "entries, dh in sub-chunks of 8192 columns, ascending";
+                              "entries, dh in sub-chunks by V, ascending";
 }
 
 const char* rlk_status_string(rlk_status_t status) {
