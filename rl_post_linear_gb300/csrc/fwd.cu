@@ -331,7 +331,7 @@ cudaError_t launch_list_partials(const CUtensorMap& map_h, const CUtensorMap& ma
     p.out = out;
     p.K = K;
     const long long units = static_cast<long long>(p.num_m) * p.num_chunks;
-    return launch_persistent(TwoMaps{map_h, map_w}, p, units, num_sms, err, stream);
+    return launch_persistent(TwoMaps{map_h, map_w}, p, units, num_sms, err, stream, kPdlEarly);
 }
 
 cudaError_t launch_fwd_merge(const float2* partials, int num_chunks, const float* s_target,
