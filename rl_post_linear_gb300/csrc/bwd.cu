@@ -1605,6 +1605,39 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
             reinterpret_cast<float4*>(st.dh_acc), reinterpret_cast<uint2*>(st.dhidden));
         return cudaGetLastError();
     }
+    if (st.role == kRoleDh) {
+        DhPolicy pd;
+        pd.targets = st.targets;
+        pd.mask = st.mask;
+        pd.grad = st.grad;
+        pd.weight = static_cast<const __nv_bfloat16*>(st.weight);
+        pd.dh_acc = st.dh_acc;
+        pd.dh = static_cast<__nv_bfloat16*>(st.dhidden);
+        pd.ycoef = st.ycoef;
+        pd.dom = st.dom;
+        pd.dcoef = st.dcoef;
+        pd.y_off = st.y_off;
+        pd.V_global = st.V_global;
+        pd.round_last = st.round_last;
+        pd.rm = RowMap{st.rows, st.n_rows};
+        pd.dh_out32 = st.dh_out32;
+        pd.N = N;
+        pd.V = V;
+        pd.H = H;
+        pd.c0 = c0;
+        pd.num_m = (N + kUnitM - 1) / kUnitM;
+        pd.num_n = (H + kTileV - 1) / kTileV;
+        pd.kblocks = (width + 63) / 64;
+        pd.first = st.chunk == 0;
+        pd.last = st.chunk == st.num_chunks - 1;
+        pd.temp = st.temp;
+        pd.terms = !st.kl;
+        pd.hilo = st.hilo;
+        // the dW GEMM that follows overlaps this one's last wave (with 6.7 waves of dh
+        // units at N = 8192, a quarter of the CTA pairs would otherwise idle for a unit)
+        return launch_gemm(maps.ds_kmajor, maps.w_mnmajor, pd, pd.num_m * pd.num_n, num_sms, err,
+                           stream, kPdlTrigger);
+    }
     if (st.topk) {
         DwTopkPolicy pw;
         pw.hidden = static_cast<const __nv_bfloat16*>(st.hidden);
