@@ -676,7 +676,8 @@ struct Ranges {
     }
 };
 
-constexpr int kMostShared = 227 * 1024 - 256;    // of a block, behind what is static
+constexpr int kStaticShared = 256;               // more than what is static in any kernel
+constexpr int kMostShared = 227 * 1024 - kStaticShared;
 static_assert(kWords * 4 + 2 * kMaxBias * 8 <= kMostShared, "a block's shared memory");
 int bias_slots(const ProcessArgs& a) {
     if (a.bias == 0) return 0;
@@ -693,7 +694,8 @@ cudaError_t launch(void (*kernel)(const ProcessArgs, int, int, int, Params...), 
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     const size_t smem =
         words * 4 + static_cast<size_t>(words > 0 ? bias_slots(a) : 0) * 8 + list * 4;
-    if (smem > 48 * 1024) {
+    // without the attribute a block has 48 KB, of which what is static takes its part
+    if (smem > 48 * 1024 - kStaticShared) {
         const cudaError_t e = cudaFuncSetAttribute(
             reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
             kMostShared);
