@@ -35,6 +35,9 @@ class Rollout:
 
     def __init__(self, student, prompts, room, hidden, allowed=None, active_mask=None,
                  repetition=1.1, frequency=0.1, presence=0.0, temperature=0.8, top_p=0.95):
+        if room < 1:
+            raise ValueError("room must be 1 or more, got %d" % room)
+        self.left = room                          # tokens that may still be drawn
         device = student.head.device
         n, p = prompts.shape
         self.tokens = torch.full((n, p + room), -1, dtype=torch.int64, device=device)
@@ -66,6 +69,9 @@ class Rollout:
 
     def __call__(self, x, uniforms):
         """One token of each sequence from its state: (tokens, logp)."""
+        if self.left < 1:
+            raise RuntimeError("the sequences' buffer is full")
+        self.left -= 1
         self.x.copy_(x)
         self.uniforms.copy_(uniforms)
         self.graph.replay()
@@ -99,6 +105,8 @@ def update(student, x, ids, logp, temperature, active_mask=None, lr=1.0, renorma
 def run(rows=256, hidden=512, vocab=1000, prompt=16, steps=8, top_k=32, temperature=1.0, lr=10.0,
         seed=0, log=print):
     """One dict a step: the mean KL and the share of draws that the sequence had drawn before."""
+    if steps < 1:
+        raise ValueError("steps must be 1 or more, got %d" % steps)
     student = PolicyHead(hidden, vocab, seed=seed)
     teacher = PolicyHead(hidden, vocab, seed=seed + 1)
     with torch.no_grad():
