@@ -723,11 +723,10 @@ rlk_status_t rlk_topk_logp(const void* logits, int32_t dtype, int64_t N, int64_t
  * (RLK_DEVERR_TARGET_RANGE), or with NaN or +inf as log-weight of an id (RLK_DEVERR_LOGITS),
  * gives kl and logp NaN; the backward gives it no gradient.  Accumulation is fp32, with the mean
  * of what the tensor cores cut off a logit given back (lse may differ from rlk_linear_logp_fwd's
- * by that, 1e-9 H of a logit); dhidden and dweight are rounded once.  Of dL/ds the entries at the
- * teacher's tokens, and one with p > 1/2, enter the products in fp32 accuracy, the others rounded to
- * bf16 (2^-8 of themselves at most; in about 16 bits for V <= 8192).  kl, lse, logp and dhidden rows
- * do not depend on the batch; dweight is reproducible bit for bit.  N = 0 returns RLK_OK and writes
- * nothing, dweight neither.
+ * by that, 1e-9 H of a logit).  dL/ds enters the products in two bf16 planes (about 16 bits), an
+ * entry with p > 1/2 that no slot names in fp32; dhidden and dweight are rounded once.  kl, lse, logp
+ * and dhidden rows do not depend on the batch; dweight is reproducible bit for bit.  N = 0 returns
+ * RLK_OK and writes nothing, dweight neither.
  */
 size_t rlk_linear_topk_kl_fwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int64_t K);
 rlk_status_t rlk_linear_topk_kl_fwd(const void* hidden, const void* weight,

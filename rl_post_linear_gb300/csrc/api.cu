@@ -1138,7 +1138,6 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
     float* val = reinterpret_cast<float*>(ws + lay.val_off);
     st.topk_ids = ids;
     st.topk_val = val;
-    st.gemm_rows = gemm_rows;
     st.sorted_dy = reinterpret_cast<int*>(ws + lay.sorted_dy_off);
     st.sorted_dt = reinterpret_cast<int*>(ws + lay.sorted_dt_off);
     st.tiles = reinterpret_cast<uint64_t*>(ws + lay.tiles_off);
@@ -1153,17 +1152,8 @@ rlk_status_t rlk_linear_topk_kl_bwd(const void* hidden, const void* weight,
                                renormalize != 0};
     RLK_CUDA(rlk::launch_topk_coef(slots, grad_kl, logp, st.rows, st.n_rows, st.temp, st.ycoef,
                                    ids, val, copy, device_error_word, stream));
-    // dh depends on V here, not on N: its rows are those of any batch
-    st.hilo = lay.lo;
-    st.dh_started = V > rlk::kTopkSmallV;
+    st.hilo = true;
     if (rlk::topk_dh_split(N, H, V)) st.dh_part = reinterpret_cast<float*>(ws + lay.part_off);
-    if (st.dh_started)
-        RLK_CUDA(rlk::launch_topk_dh(ids, val, st.n_rows, n, st.K, weight, h, st.dh_acc, stream));
-    rlk::TopkRows rows_of{};
-    if (!lay.lo) {
-        RLK_CUDA(rlk::launch_topk_sort(lay, ws, st.n_rows, n, st.K, v, &rows_of, stream));
-        st.rows_of = &rows_of;
-    }
     // no dominant class yet (all bits set: -1), and none in any chunk
     RLK_CUDA(cudaMemsetAsync(st.dom, 0xff, static_cast<size_t>(N) * sizeof(int), stream));
     RLK_CUDA(cudaMemsetAsync(st.dom_flags, 0, static_cast<size_t>(st.num_chunks) * sizeof(int),
@@ -1198,8 +1188,8 @@ const char* rlk_contract_string(void) {
                               "64-bit sums, ties to the lowest index; logit processing: fp32, "
                               "counts as whole numbers, biases in ascending slots; top-k: order "
                               "by value, then index, sums ordered by V alone; top-K KL: logits "
-                              "scaled by 1 + 1.037e-9 H, dS bf16 with the remainders of listed "
-                              "entries, dh in sub-chunks by V, ascending";
+                              "scaled by 1 + 1.037e-9 H, dS in two bf16 planes, dh in "
+                              "sub-chunks by V, ascending";
 }
 
 const char* rlk_status_string(rlk_status_t status) {

@@ -528,16 +528,16 @@ struct DsKlPolicy {
 //
 // dS[t,v] = (g_t / T) (Q_t p[t,v] - q[t,v]): this GEMM writes the first term, with
 // coef_t = g_t Q_t / T from the launch before it, in bf16.  The entries at the teacher's tokens, at
-// most K a row and most of its gradient, are then overwritten whole (launch_topk_scatter), and what
-// their rounding to bf16 leaves goes into dh, and as a sum for each vocabulary row into dW, in fp32
-// (topk_kl.cu): without it the rounding costs as much accuracy as that of the outputs.  So would a
-// class with p > 1/2 that the teacher does not list; it takes the logp backward's way for dominant
-// classes.  LO: a second plane holds what the rounding leaves of every entry (as for the entropy),
-// for dW where that costs less, for both where V is small.
-template <bool LO>
-struct DsTopkPolicyT : SingleRole<false, false> {
+// most K a row, are then overwritten whole (launch_topk_scatter).  A second plane holds what the
+// rounding leaves of every entry, as for the entropy: any of them may carry a row, the listed ones or,
+// where the student does not follow the teacher, a few others, and in one plane the rounding costs as
+// much accuracy as that of the outputs, together more than 2e-3 (dh of a student with five unlisted
+// classes near 0.2: 2.06e-3, of entries halfway between two numbers of bf16 3.97e-3; with two planes
+// 1.66e-3).  A class with p > 1/2 that the teacher does not
+// list takes the logp backward's way for dominant classes.
+struct DsTopkPolicy : SingleRole<false, false> {
     static constexpr bool kCtaPair = true;
-    static constexpr int kLd = LO ? 2 * kBwdChunk : kBwdChunk;   // dS row stride
+    static constexpr int kLd = 2 * kBwdChunk;   // dS row stride: hi plane, lo plane
 
     const float* lse;         // [N] by token
     const float* coef;        // [N] by GEMM row
@@ -621,14 +621,14 @@ struct DsTopkPolicyT : SingleRole<false, false> {
                     }
                 }
             }
-            uint32_t packed[16], packed_lo[LO ? 16 : 1];
+            uint32_t packed[16], packed_lo[16];
             if (full && ai == 32 && st.live) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float d0 = st.coef * ex2_approx(fmaf(x[2 * j], k, -st.lse2));
                     const float d1 = st.coef * ex2_approx(fmaf(x[2 * j + 1], k, -st.lse2));
                     packed[j] = pack_bf16x2(d0, d1);
-                    if constexpr (LO) packed_lo[j] = pack_lo_bf16x2(d0, d1, packed[j]);
+                    packed_lo[j] = pack_lo_bf16x2(d0, d1, packed[j]);
                 }
             } else {
 #pragma unroll
@@ -641,7 +641,7 @@ struct DsTopkPolicyT : SingleRole<false, false> {
                                    ? st.coef * ex2_approx(fmaf(x[at], k, -st.lse2)) : 0.f;
                     }
                     packed[j] = pack_bf16x2(d[0], d[1]);
-                    if constexpr (LO) packed_lo[j] = pack_lo_bf16x2(d[0], d[1], packed[j]);
+                    packed_lo[j] = pack_lo_bf16x2(d[0], d[1], packed[j]);
                 }
             }
             uint4* dst = reinterpret_cast<uint4*>(ds + static_cast<size_t>(i) * kLd + col);
@@ -649,12 +649,10 @@ struct DsTopkPolicyT : SingleRole<false, false> {
             for (int w = 0; w < 4; ++w)
                 dst[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
                                     packed[4 * w + 3]);
-            if constexpr (LO) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    dst[kBwdChunk / 8 + w] = make_uint4(packed_lo[4 * w], packed_lo[4 * w + 1],
-                                                        packed_lo[4 * w + 2], packed_lo[4 * w + 3]);
-            }
+            for (int w = 0; w < 4; ++w)
+                dst[kBwdChunk / 8 + w] = make_uint4(packed_lo[4 * w], packed_lo[4 * w + 1],
+                                                    packed_lo[4 * w + 2], packed_lo[4 * w + 3]);
         }
     }
 
@@ -836,7 +834,7 @@ struct DhPolicy : SingleRole<false, true> {
 // and walks its sub-chunks (the additions overlap the next one's MMAs).  With few, most CTA pairs
 // would idle: a unit is then one sub-chunk of a tile, written to `part`, and dh_sum_kernel adds them
 // in the same order, so that a row's bits do not depend on the batch (a step of [200, 2048] against
-// V = 32003: 242 instead of 341 us).
+// V = 32003: 208 instead of 425 us).
 struct DhTopkPolicy : SingleRole<false, true> {
     static constexpr bool kKRemap = true;
     static constexpr bool kTileK = true;
@@ -850,7 +848,7 @@ struct DhTopkPolicy : SingleRole<false, true> {
     const float* dcoef;
     RowMap rm;
     int N, H, c0, width, num_n, sub, subs;
-    bool first, last, hilo, split;
+    bool first, last, split;
 
     __device__ int num_units() const { return rm.tiles(N) * num_n * (split ? subs : 1); }
     __device__ int tiles_in_unit(int) const { return split ? 1 : subs; }
@@ -866,7 +864,7 @@ struct DhTopkPolicy : SingleRole<false, true> {
     __device__ int tile_k_blocks(int u, int q) const {
         int m, n, s;
         unit(u, m, n, s);
-        return sub_blocks(s + q) * (hilo ? 2 : 1);
+        return 2 * sub_blocks(s + q);
     }
     __device__ int k_blocks(int u) const { return tile_k_blocks(u, 0); }
     __device__ void coords(int u, int q, int& a_mn, int& a_k, int& b_mn, int& b_k) const {
@@ -879,7 +877,7 @@ struct DhTopkPolicy : SingleRole<false, true> {
     }
     // the lo plane behind the hi plane, against the same rows of W
     __device__ void k_remap(int kb, int nkb, int&, int& a_k, int&, int& b_k) const {
-        if (hilo && kb >= nkb / 2) {
+        if (kb >= nkb / 2) {
             a_k += kBwdChunk - nkb / 2 * kBK;
             b_k -= nkb / 2 * kBK;
         }
@@ -1144,12 +1142,9 @@ struct DwPolicy : SingleRole<true, true> {
 
 // ----------------------------------------------------------------------------- dW for top-K KL
 //
-// The same product (with a lo plane or without), to which rows of the chunk may have a sum that is
-// added before the rounding (what bf16 left of entries of dS, 2^-9 of them, so bf16 itself), and
-// dominant classes.  With few tokens a tile is a few MMAs and the epilogue decides: eight warps, each
-// staging 32 rows x 64 columns in shared memory for a TMA store, instead of four whose threads write
-// their rows themselves (a step of [45, 4096] against V = 151936: 1390 us; by stores of 32 columns,
-// unswizzled, 1219; now 1030, dW 231 of them, 5.4 TB/s).
+// The product over both planes of dS, and dominant classes.  With few tokens a tile is a few MMAs and
+// the epilogue decides: eight warps, each staging 32 rows x 64 columns in shared memory for a TMA
+// store, instead of four whose threads write their rows themselves.
 struct DwTopkMaps {
     CUtensorMap a, b;             // dS and h, MN-major
     CUtensorMap dw;               // dW [V, H], box {64, 32}, 128-byte swizzle
@@ -1168,11 +1163,8 @@ struct DwTopkPolicy : SingleRole<true, true> {
     const int* sorted_dt;
     const int* dom_flag;
     const float* dcoef;
-    const int* row_at;             // [V] a row's place in row_sum, or -1; or nullptr: no sums
-    const __nv_bfloat16* row_sum;  // [places][H]
     RowMap rm;
     int N, H, c0, width, num_m, num_n, kblocks;
-    bool hilo;
 
     __device__ static void prefetch(const Maps& m) {
         prefetch_tensormap(&m.a);
@@ -1184,10 +1176,10 @@ struct DwTopkPolicy : SingleRole<true, true> {
     __device__ int num_units() const { return num_m * num_n; }
     __device__ int k_blocks(int) const {
         const int kb = rm.n_rows != nullptr ? (max(*rm.n_rows, 1) + 63) / 64 : kblocks;
-        return hilo ? 2 * kb : kb;
+        return 2 * kb;
     }
     __device__ void k_remap(int kb, int nkb, int& a_mn, int& a_k, int&, int& b_k) const {
-        if (hilo && kb >= nkb / 2) {
+        if (kb >= nkb / 2) {
             const int j = kb - nkb / 2;
             a_mn += kBwdChunk;
             a_k = j * 64;
@@ -1210,29 +1202,15 @@ struct DwTopkPolicy : SingleRole<true, true> {
     // loaded ahead: a unit's wait for its own took as long as a slice
     struct EpiCarry {
         bool dominant;             // any class of this chunk
-        int at;                    // the next unit's place in row_sum
     };
-    __device__ int place(int u, int row) const {
-        if (u < 0 || row_at == nullptr) return -1;
-        int m, n;
-        unit(u, m, n);
-        return m * kUnitM + row < width ? row_at[c0 + m * kUnitM + row] : -1;
-    }
-    __device__ void epi_init(int u, int row, EpiCarry& carry) const {
-        carry.dominant = *dom_flag != 0;
-        carry.at = place(u, row);
-    }
+    __device__ void epi_init(EpiCarry& carry) const { carry.dominant = *dom_flag != 0; }
 
     struct EpiState {
         int dlo, dhi;
-        const uint4* sum;          // the row's sum, or nullptr
     };
 
-    __device__ void epi_begin(int u, int next, int row, EpiCarry& carry, EpiState& st) const {
+    __device__ void epi_begin(int u, int row, const EpiCarry& carry, EpiState& st) const {
         st.dlo = st.dhi = 0;
-        st.sum = carry.at < 0 ? nullptr : reinterpret_cast<const uint4*>(
-                                              row_sum + static_cast<size_t>(carry.at) * H);
-        carry.at = place(next, row);
         if (!carry.dominant) return;
         int m, n;
         unit(u, m, n);
@@ -1248,13 +1226,6 @@ struct DwTopkPolicy : SingleRole<true, true> {
         const int first = c0 + m * kUnitM + row - lane;     // the warp's first vocabulary row
         const int n0 = n * kTileV + half * (kTileV / 2);
         taddr += half * (kTileV / 2);
-        uint4 sum[8];                                        // of the next slice, on its way
-        const auto fetch = [&](int col) {
-            if (st.sum == nullptr || col >= H) return;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) sum[q] = __ldcs(st.sum + col / 8 + q);
-        };
-        fetch(n0);
 #pragma unroll 1
         for (int cc = 0; cc < kTileV / 2; cc += kSlice) {
             uint32_t r[2][32];
@@ -1264,16 +1235,6 @@ struct DwTopkPolicy : SingleRole<true, true> {
             float x[kSlice];
 #pragma unroll
             for (int j = 0; j < kSlice; ++j) x[j] = __uint_as_float(r[j / 32][j % 32]);
-            if (st.sum != nullptr) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    float add[8];
-                    bf16x8_to_f32(sum[q], add);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[8 * q + j] += add[j];
-                }
-            }
-            if (cc + kSlice < kTileV / 2) fetch(col + kSlice);
             // tokens whose dominant class that is not listed is v, ascending
             for (int i = st.dlo; i < st.dhi; ++i) {
                 const int t = sorted_dt[i];
@@ -1491,10 +1452,9 @@ static cudaError_t launch_ds(const BwdStepMaps& maps, const BwdStep& st, int c0,
                        stream);
 }
 
-template <bool LO>
 static cudaError_t launch_ds_topk(const BwdStepMaps& maps, const BwdStep& st, int c0, int width,
                                   int num_sms, uint32_t* err, cudaStream_t stream) {
-    DsTopkPolicyT<LO> ps;
+    DsTopkPolicy ps;
     ps.lse = st.lse;
     ps.coef = st.ycoef;
     ps.ids = st.topk_ids;
@@ -1551,16 +1511,10 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
                                st.sorted_dy, st.sorted_dt, stream);
     }
     if (st.role == kRoleDs && st.topk) {
-        cudaError_t e = st.hilo ? launch_ds_topk<true>(maps, st, c0, width, num_sms, err, stream)
-                                : launch_ds_topk<false>(maps, st, c0, width, num_sms, err, stream);
+        cudaError_t e = launch_ds_topk(maps, st, c0, width, num_sms, err, stream);
         if (e != cudaSuccess) return e;
-        e = launch_topk_scatter(st.topk_ids, st.topk_val, st.n_rows, N, st.K, c0, width, st.ds,
-                                st.hilo, stream);
+        e = launch_topk_scatter(st.topk_ids, st.topk_val, st.n_rows, N, st.K, c0, width, st.ds, stream);
         if (e != cudaSuccess) return e;
-        if (st.rows_of != nullptr) {
-            e = launch_topk_rows(*st.rows_of, st.chunk, st.gemm_rows, H, stream);
-            if (e != cudaSuccess) return e;
-        }
         return launch_dom_sort(st.dom, N, V, c0, c0 + width, st.dom_flags + st.chunk, st.tiles,
                                st.sorted_dy, st.sorted_dt, stream);
     }
@@ -1589,9 +1543,8 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pd.num_n = (H + kTileV - 1) / kTileV;
         pd.sub = topk_dh_sub(st.V);
         pd.subs = (width + pd.sub - 1) / pd.sub;
-        pd.first = st.chunk == 0 && !st.dh_started;
+        pd.first = st.chunk == 0;
         pd.last = st.chunk == st.num_chunks - 1;
-        pd.hilo = st.hilo && !st.dh_started;
         pd.split = st.dh_part != nullptr;
         const int tiles = (N + kUnitM - 1) / kUnitM * pd.num_n;
         const cudaError_t e =
@@ -1645,9 +1598,6 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pw.sorted_dt = st.sorted_dt;
         pw.dom_flag = st.dom_flags + st.chunk;
         pw.dcoef = st.dcoef;
-        pw.row_at = st.rows_of != nullptr ? st.rows_of->row_at : nullptr;
-        pw.row_sum = st.rows_of != nullptr ? static_cast<const __nv_bfloat16*>(st.rows_of->sums)
-                                           : nullptr;
         pw.rm = RowMap{st.rows, st.n_rows};
         pw.N = N;
         pw.H = H;
@@ -1656,7 +1606,6 @@ cudaError_t launch_bwd_step(const BwdStepMaps& maps, const BwdStep& st, int num_
         pw.num_m = (width + kUnitM - 1) / kUnitM;
         pw.num_n = (H + kTileV - 1) / kTileV;
         pw.kblocks = (N + 63) / 64;
-        pw.hilo = st.hilo;
         // (behind dh_sum_kernel, which does not trigger it, it just starts when that ends)
         return launch_persistent(DwTopkMaps{maps.ds_mnmajor, maps.h_mnmajor, maps.dw_store}, pw,
                                  pw.num_m * pw.num_n, num_sms, err, stream, kPdlOverlap);

@@ -166,8 +166,8 @@ __device__ __forceinline__ uint64_t operand_desc_rt(bool mn_major, uint32_t stag
 // arrive on the leader's barriers.  Pair policies may set
 // kEpiWarps = 8: two warps per TMEM lane quarter, each given half of the
 // tile's columns (epi_begin / epi_pair / epi_end take the half; kStagedEpi does
-// the same for single tiles: epi_staged, whose epi_begin also gets the next unit and an
-// EpiCarry that epi_init or the unit before loaded ahead), so that the
+// the same for single tiles: epi_staged, whose epi_begin also gets an EpiCarry that
+// epi_init loaded ahead), so that the
 // epilogue, which the MMA waits for, takes half as long.  epi_pair also gets the
 // kernel's tensor maps and, for a policy with kEpiSmemPerWarp > 0, this warp's
 // slot of that many bytes of shared memory (after the ring), e.g. to stage a tile
@@ -497,11 +497,11 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
         uint32_t tile_i = 0;
         bool ok = true;
         typename P::EpiCarry carry;
-        if constexpr (P::kStagedEpi) p.epi_init(wg < units ? wg : -1, prow, carry);
+        if constexpr (P::kStagedEpi) p.epi_init(carry);
         for (int u = wg; ok && u < units; u += num_wg) {
             typename P::EpiState st;
             if constexpr (P::kStagedEpi)
-                p.epi_begin(u, u + num_wg < units ? u + num_wg : -1, prow, carry, st);
+                p.epi_begin(u, prow, carry, st);
             else if constexpr (P::kPairTiles)
                 p.epi_begin(u, prow, half, st);
             else

@@ -96,35 +96,13 @@ struct BwdLayout {
     }
 };
 
-// Top-K KL: the entries of dS at the teacher's tokens (coefficient by slot).  What their rounding to
-// bf16 leaves reaches dW either as a second plane of dS (lo) or as a sum for each vocabulary row:
-// then also their list by token id, radix-sorted (id, slot) pairs, of which come each entry's GEMM
-// row and remainder; a vocabulary row's range of the list; each chunk's rows that have one, those
-// with many apart, and their sums.
-constexpr int kRadixBits = 9, kRadixTile = 2048;
-constexpr int kTopkSmallV = 8192;
-// The lo plane doubles the dW GEMM, 2 N H V at 1.7 PFLOP/s.  The sums move 4 bytes a column of each
-// row that has any at 6 TB/s, read 2 of h for each entry at 8 TB/s from L2, and take 60 us a chunk for
-// their list, their launches and the reads that dW waits for.  Measured for steps at H = 4096, V =
-// 151936, lo and sums: N = 600, K = 64 2922 and 3027 us; N = 600, K = 512 3251 and 3992; N = 1200, K =
-// 256 5253 and 5172; N = 2048, K = 64 7900 and 6820.  A small vocabulary, of which a few classes that
-// are not listed may carry much of a row, has the plane for dh too.
-inline bool topk_lo_plane(int64_t N, int64_t H, int64_t V, int64_t K) {
-    if (V <= kTopkSmallV) return true;
-    const double e = static_cast<double>(N) * static_cast<double>(K);
-    const double rows = e < static_cast<double>(V) ? e : static_cast<double>(V);
-    const double sums = (rows * 4 / 6e12 + e * 2 / 8e12) * static_cast<double>(H) +
-                        60e-6 * static_cast<double>((V + kBwdChunk - 1) / kBwdChunk);
-    return 2.0 * static_cast<double>(N) * static_cast<double>(H) * static_cast<double>(V) / 1.7e15 < sums;
-}
-// The columns of a sub-chunk of dh (DhTopkPolicy), by V alone: a chunk's quarters; the eighths of a
-// vocabulary of one chunk, of which few rows have few tiles to share out, or its quarters where dS
-// has two planes there.  Measured for steps at H = 2048 with these and with 8192 columns: V = 32003, N
-// = 200 189 and 200 us, N = 600 335 and 344, N = 2048 788 and 784; V = 8000, N = 3 93 and 137, N = 4000
-// 518 and 504.
+// The columns of a sub-chunk of dh (DhTopkPolicy), by V alone: a chunk's quarters; of a vocabulary of
+// one chunk the eighths, of which few rows have few tiles to share out, or of a small one the quarters.
+// Measured for steps at H = 2048 in eighths and in quarters: V = 32003, N = 200 210 and 233 us, N = 2048
+// 981 and 1003; V = 8000, N = 3 84 and 92, N = 4000 563 and 523.
 inline int topk_dh_sub(int64_t V) {
     if (V > kBwdChunk) return kBwdChunk / 4;
-    const int64_t parts = V > kTopkSmallV ? 8 : 4;
+    const int64_t parts = V > 8192 ? 8 : 4;
     const int64_t sub = (V + 64 * parts - 1) / (64 * parts) * 64;
     return static_cast<int>(sub > 1024 ? sub : 1024);
 }
@@ -134,14 +112,14 @@ inline int topk_dh_subs(int64_t V) {     // of the first chunk, the most
 }
 // Whether the dh GEMM takes the sub-chunks of a vocabulary chunk side by side, in parts that are
 // summed after it: where that fills the waves of 76 CTA pairs better by more than the parts cost, with
-// a tenth to spare (dW fills part of an idle wave).  A tile takes 192 us for a whole chunk of one
-// plane, the parts move at 6.5 TB/s and their sum takes a launch of 3 us.  Measured for steps of [45,
-// 4096] and V = 151936: 1391 us, one after the other 1791; [500, 4096] 2520 and 2708; [2048, 4096]
-// 6887 and 6822 (not split).
+// a tenth to spare (dW fills part of an idle wave).  A tile takes 384 us for a whole chunk of two
+// planes, the parts move at 6.5 TB/s and their sum takes a launch of 3 us.  Measured for steps of [45,
+// 4096] and V = 151936: 1231 us, one after the other 2133; [500, 4096] 2600 and 3012; [768, 7168] and V
+// = 129280 5597 and 6058.
 inline bool topk_dh_split(int64_t N, int64_t H, int64_t V) {
     const int subs = topk_dh_subs(V);
     const double width = static_cast<double>(V < kBwdChunk ? V : kBwdChunk) / kBwdChunk;
-    const double tile = 192e-6 * width * (V <= kTopkSmallV ? 2 : 1);
+    const double tile = 384e-6 * width;
     const int64_t tiles = (N + kUnitM - 1) / kUnitM * ((H + kTileV - 1) / kTileV);
     const int64_t waves = (tiles + 75) / 76, part_waves = (tiles * subs + 75) / 76;
     const double parts = static_cast<double>(N) * static_cast<double>(H) * 8 * subs / 6.5e12 + 3e-6;
@@ -154,36 +132,18 @@ inline bool topk_dh_split(int64_t N, int64_t H, int64_t V) {
 // depends on its own row alone, and only N are kept.
 constexpr int64_t kMinMapRows = 16;
 inline int64_t map_rows(int64_t N) { return N < kMinMapRows ? kMinMapRows : N; }
+// dS in two planes, the parts of dh where there are any, and the entries of dS at the teacher's tokens.
 struct TopkKlBwdLayout : BwdLayout {
-    bool lo;
-    int64_t tiles, places;
-    size_t part_off, ids_off, val_off, key_off[2], slot_off[2], hist_off, first_off, last_off, at_off,
-        list_off, many_off, counts_off, sums_off;
+    size_t part_off, ids_off, val_off;
     TopkKlBwdLayout(int64_t N, int64_t H, int64_t V, int64_t K)
-        : BwdLayout(map_rows(N), H, topk_lo_plane(N, H, V, K)), lo(topk_lo_plane(N, H, V, K)) {
-        const size_t e = static_cast<size_t>(N) * K, v = static_cast<size_t>(V);
-        tiles = static_cast<int64_t>((e + kRadixTile - 1) / kRadixTile);
-        places = static_cast<int64_t>(e < kBwdChunk ? e : kBwdChunk);
+        : BwdLayout(map_rows(N), H, true) {
+        const size_t e = static_cast<size_t>(N) * K;
         part_off = total;
         if (topk_dh_split(N, H, V))
             total = align_up(part_off + static_cast<size_t>(topk_dh_subs(V)) * N * H * 4, 256);
         ids_off = total;
         val_off = align_up(ids_off + e * 4, 256);
         total = align_up(val_off + e * 4, 256);
-        if (lo) return;
-        key_off[0] = total;
-        key_off[1] = align_up(key_off[0] + e * 4, 256);
-        slot_off[0] = align_up(key_off[1] + e * 4, 256);
-        slot_off[1] = align_up(slot_off[0] + e * 4, 256);
-        hist_off = align_up(slot_off[1] + e * 4, 256);
-        first_off = align_up(hist_off + static_cast<size_t>(tiles) * 4 * (1 << kRadixBits), 256);
-        last_off = align_up(first_off + v * 4, 256);
-        at_off = align_up(last_off + v * 4, 256);
-        list_off = align_up(at_off + v * 4, 256);
-        many_off = align_up(list_off + v * 4, 256);
-        counts_off = align_up(many_off + v * 4, 256);
-        sums_off = align_up(counts_off + static_cast<size_t>(kMaxBwdChunks) * 8, 256);
-        total = align_up(sums_off + static_cast<size_t>(places) * H * 2, 256);
     }
 };
 
@@ -293,19 +253,6 @@ struct BwdStepMaps {
 // One launch of the backward: a role (the dS recompute, the dh GEMM or the dW
 // GEMM) over one vocabulary chunk.
 constexpr int kRoleDs = 0, kRoleDh = 1, kRoleDw = 2;
-// The listed entries by vocabulary row, for dW.
-struct TopkRows {
-    const int* entry_row;      // [E] GEMM row of each entry, by token id and row
-    const float* entry_rest;   // [E] what bf16 leaves of it
-    const int* first;          // [V] a row's range of them (empty: last = 0)
-    const int* last;
-    const int* row_at;         // [V] its place in sums, or -1
-    const int* list;           // [V] each chunk's rows that have entries
-    const int* many;           // [V] and places of those that have many
-    const int2* counts;        // [chunks] of both
-    void* sums;                // [places][H] bf16, of one chunk at a time
-    int places;
-};
 struct BwdStep {
     const int64_t* targets;
     const uint8_t* mask;
@@ -335,12 +282,9 @@ struct BwdStep {
     bool hilo;                 // dS as hi and lo bf16 planes [N, 2 kBwdChunk] (entropy, KL, top-K)
     // KL against a teacher's top tokens (topk = true): ycoef holds g Q / T by GEMM row
     bool topk;
-    bool dh_started;           // dh_acc holds what bf16 leaves of the listed entries; dh takes one plane
     int K;
     const int* topk_ids;       // [N][K] by GEMM row: distinct token ids, -1: no entry
     const float* topk_val;     // [N][K] their whole entries of dS
-    const void* gemm_rows;     // [N][H]
-    const TopkRows* rows_of;   // or nullptr: dS has a lo plane
     float* dh_part;            // or nullptr: dh's sub-chunks one after the other
     void* ds;                  // dS [N, kBwdChunk] bf16 of the chunk (hilo: [N, 2 kBwdChunk])
     float* dh_acc;
@@ -569,18 +513,9 @@ cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const fl
                              const int* rows, const int* n_rows, float temp, float* coef,
                              int* ids, float* val, const CopyRows& copy, uint32_t* err,
                              cudaStream_t stream);
-// what bf16 leaves of the entries in dh: dh_acc[i] = sum_k rest(val[i,k]) W[id[i,k]]
-cudaError_t launch_topk_dh(const int* ids, const float* val, const int* n_rows, int N, int K,
-                           const void* weight, int H, float* dh_acc, cudaStream_t stream);
-// the entries by token id
-cudaError_t launch_topk_sort(const TopkKlBwdLayout& lay, uint8_t* ws, const int* n_rows, int N, int K,
-                             int V, TopkRows* out, cudaStream_t stream);
-// sums[row_at[v]] = sum of rest h over the entries of v, for the chunk's rows
-cudaError_t launch_topk_rows(const TopkRows& rows, int chunk, const void* hidden, int H,
-                             cudaStream_t stream);
-// the entries of dS at the listed tokens (lo: and what bf16 leaves of them in its second plane)
+// the entries of dS at the listed tokens, in both planes
 cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,
-                                int c0, int width, void* ds, bool lo, cudaStream_t stream);
+                                int c0, int width, void* ds, cudaStream_t stream);
 
 // Device address (current device and context) of the library-owned audit scratch.
 cudaError_t audit_noalloc_scratch(void** parts);

@@ -11,9 +11,7 @@
 // leaves the partials of lse and takes the listed logits from the same accumulators
 // (launch_list_partials), and launch_topk_merge forms lse, logp and kl.  Backward: launch_topk_coef
 // forms the coefficients; then per vocabulary chunk the dS GEMM, launch_topk_scatter for the listed
-// entries, and the dh and dW GEMMs.  What bf16 leaves of the listed entries is taken along:
-// launch_topk_dh starts dh with it, launch_topk_sort lists the entries by token and launch_topk_rows
-// sums them for dW.
+// entries, and the dh and dW GEMMs.
 //
 // A slot with a negative id is empty.  A row with an id >= V, or a log-weight that is NaN or
 // +inf at an id, gives NaN and sets an error bit; the backward gives it no gradient.
@@ -289,13 +287,7 @@ __global__ void __launch_bounds__(kCoefWarps * 32)
     }
 }
 
-// What rounding to bf16 leaves, exactly.
-__device__ __forceinline__ float rest_of(float d) {
-    return d - __bfloat162float(__float2bfloat16_rn(d));
-}
-
 // The chunk's listed entries, over what the GEMM wrote there.
-template <bool LO>
 __global__ void __launch_bounds__(256)
     topk_scatter_kernel(const int* __restrict__ ids, const float* __restrict__ val,
                         const int* __restrict__ n_rows, int N, int K, int c0, int width,
@@ -307,342 +299,11 @@ __global__ void __launch_bounds__(256)
         const int id = ids[e];
         if (id < c0 || id - c0 >= width) continue;
         const float d = val[e];
-        __nv_bfloat16* at = ds + (e / K) * ((LO ? 2 : 1) * kBwdChunk) + (id - c0);
-        at[0] = __float2bfloat16_rn(d);
-        if (LO) at[kBwdChunk] = __float2bfloat16_rn(rest_of(d));
+        const __nv_bfloat16 hi = __float2bfloat16_rn(d);
+        __nv_bfloat16* at = ds + (e / K) * (2 * kBwdChunk) + (id - c0);
+        at[0] = hi;
+        at[kBwdChunk] = __float2bfloat16_rn(d - __bfloat162float(hi));
     }
-}
-
-// ----------------------------------------------------------------------------- what bf16 leaves
-
-// acc += coef row, 8 columns
-__device__ __forceinline__ void add_row(float coef, uint4 v, float (&acc)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(coef, __uint_as_float(w[i] << 16), acc[2 * i]);
-        acc[2 * i + 1] = fmaf(coef, __uint_as_float(w[i] & 0xffff0000u), acc[2 * i + 1]);
-    }
-}
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-constexpr int kRowThreads = 256, kRowAhead = 8;
-
-// dh_acc[i] = sum over the slots, ascending, of rest W[id]: a block a row and 2048 columns.  Bound by
-// the rows of W it reads: N K H 2 bytes ([2048, 4096], K = 64: 1.07 GB in 132 us, 8.1 TB/s, some of
-// them from L2).
-__global__ void __launch_bounds__(kRowThreads)
-    topk_dh_kernel(const int* __restrict__ ids, const float* __restrict__ val,
-                   const int* __restrict__ n_rows, int N, int K, const uint4* __restrict__ weight,
-                   int vecs, float* __restrict__ dh_acc) {
-    __shared__ int s_id[kMaxTopK + kRowAhead];
-    __shared__ float s_rest[kMaxTopK + kRowAhead];
-    wait_previous(ids, val, n_rows, weight);
-    const int i = blockIdx.x;
-    if (i >= (n_rows != nullptr ? *n_rows : N)) return;
-    for (int j = threadIdx.x; j < K + kRowAhead; j += kRowThreads) {
-        const size_t at = static_cast<size_t>(i) * K + j;
-        const int id = j < K ? ids[at] : -1;
-        s_id[j] = id;
-        s_rest[j] = id >= 0 ? rest_of(val[at]) : 0.f;
-    }
-    __syncthreads();
-    const int c = blockIdx.y * kRowThreads + threadIdx.x;
-    if (c >= vecs) return;
-    float acc[8] = {};
-    for (int j0 = 0; j0 < K; j0 += kRowAhead) {
-        uint4 v[kRowAhead];
-#pragma unroll
-        for (int q = 0; q < kRowAhead; ++q)
-            if (s_id[j0 + q] >= 0) v[q] = __ldg(weight + static_cast<size_t>(s_id[j0 + q]) * vecs + c);
-#pragma unroll
-        for (int q = 0; q < kRowAhead; ++q)
-            if (s_id[j0 + q] >= 0) add_row(s_rest[j0 + q], v[q], acc);
-    }
-    float4* to = reinterpret_cast<float4*>(dh_acc + (static_cast<size_t>(i) * vecs + c) * 8);
-    to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-}
-
-// The same by vocabulary row: sums[place] = sum of rest h over its entries in ascending rows.  The h
-// rows of some thousand tokens stay in L2.  Most rows have an entry or a few: a warp each, its
-// entries fetched together.  Rows with more than kMany: a block for 256 columns, whose warps take an
-// eighth of the entries each, added up in order.
-constexpr int kMany = 32;
-
-__global__ void __launch_bounds__(kRowThreads)
-    topk_rows_kernel(const TopkRows r, int chunk, const uint4* __restrict__ hidden, int vecs) {
-    const int lane = threadIdx.x & 31;
-    const int count = r.counts[chunk].x, warps = gridDim.x * (kRowThreads / 32);
-    uint4* sums = static_cast<uint4*>(r.sums);
-    for (int p = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); p < count; p += warps) {
-        const int v = r.list[chunk * kBwdChunk + p];
-        const int e0 = r.first[v], n = r.last[v] - e0;
-        if (n > kMany) continue;
-        const int row = lane < n ? r.entry_row[e0 + lane] : 0;
-        const float rest = lane < n ? r.entry_rest[e0 + lane] : 0.f;
-        constexpr int kWide = 4;                 // groups of 256 columns at a time
-        for (int cb = 0; cb < vecs; cb += 32 * kWide) {
-            const int c0 = cb + lane;
-            float acc[kWide][8] = {};
-            for (int e = 0; e < n; e += 2) {
-                uint4 h[2][kWide];
-                float coef[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int er = __shfl_sync(0xffffffffu, row, min(e + q, n - 1));
-                    coef[q] = __shfl_sync(0xffffffffu, rest, min(e + q, n - 1));
-                    const uint4* from = hidden + static_cast<size_t>(er) * vecs;
-#pragma unroll
-                    for (int w = 0; w < kWide; ++w)
-                        if (e + q < n && c0 + 32 * w < vecs) h[q][w] = __ldg(from + c0 + 32 * w);
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int w = 0; w < kWide; ++w)
-                        if (e + q < n && c0 + 32 * w < vecs) add_row(coef[q], h[q][w], acc[w]);
-            }
-#pragma unroll
-            for (int w = 0; w < kWide; ++w)
-                if (c0 + 32 * w < vecs)
-                    sums[static_cast<size_t>(p) * vecs + c0 + 32 * w] =
-                        make_uint4(pack(acc[w][0], acc[w][1]), pack(acc[w][2], acc[w][3]),
-                                   pack(acc[w][4], acc[w][5]), pack(acc[w][6], acc[w][7]));
-        }
-    }
-}
-
-__global__ void __launch_bounds__(kRowThreads)
-    topk_many_kernel(const TopkRows r, int chunk, const uint4* __restrict__ hidden, int vecs) {
-    constexpr int kWarps = kRowThreads / 32;
-    __shared__ float part[kWarps][32][8 + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int count = r.counts[chunk].y, groups = (vecs + 31) / 32;
-    for (int64_t job = blockIdx.x; job < static_cast<int64_t>(count) * groups; job += gridDim.x) {
-        const int p = r.many[chunk * kBwdChunk + job / groups];
-        const int c = static_cast<int>(job % groups) * 32 + lane;
-        const int v = r.list[chunk * kBwdChunk + p];
-        const int e0 = r.first[v], n = r.last[v] - e0;
-        const int each = (n + kWarps - 1) / kWarps;
-        const int from = e0 + min(n, warp * each), to = e0 + min(n, (warp + 1) * each);
-        float acc[8] = {};
-        if (c < vecs)
-            for (int e = from; e < to; e += kRowAhead) {
-                uint4 h[kRowAhead];
-#pragma unroll
-                for (int q = 0; q < kRowAhead; ++q)
-                    if (e + q < to)
-                        h[q] = __ldg(hidden + static_cast<size_t>(r.entry_row[e + q]) * vecs + c);
-#pragma unroll
-                for (int q = 0; q < kRowAhead; ++q)
-                    if (e + q < to) add_row(r.entry_rest[e + q], h[q], acc);
-            }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) part[warp][lane][i] = acc[i];
-        __syncthreads();
-        if (warp == 0 && c < vecs) {
-            for (int w = 1; w < kWarps; ++w)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += part[w][lane][i];
-            static_cast<uint4*>(r.sums)[static_cast<size_t>(p) * vecs + c] =
-                make_uint4(pack(acc[0], acc[1]), pack(acc[2], acc[3]), pack(acc[4], acc[5]),
-                           pack(acc[6], acc[7]));
-        }
-        __syncthreads();
-    }
-}
-
-// ----------------------------------------------------------------------------- entries by token id
-//
-// A stable radix sort of (id, slot number) by id, 9 bits at a time from the lowest on: equal ids
-// stay in ascending rows, so the sums of dW have one order.  A tile of 2048 pairs a block; each of
-// its warps takes 256 consecutive ones, 32 at a time, and counts digits in its own row of shared
-// memory, so that a pair's place follows from whole numbers alone.
-
-constexpr int kRadix = 1 << kRadixBits, kSortThreads = 256, kSortWarps = kSortThreads / 32;
-constexpr int kWarpPairs = kRadixTile / kSortWarps;
-
-struct Pairs {
-    const int* ids;                      // first pass: [E] by slot, -1: none
-    const uint32_t* key;                 // later passes
-    const uint32_t* slot;
-    const int* n_rows;
-    int64_t entries;
-    int N, K, V;
-
-    // entries without an id sort behind all others
-    __device__ __forceinline__ uint32_t key_of(int64_t e) const {
-        if (key != nullptr) return key[e];
-        const int64_t live = static_cast<int64_t>(n_rows != nullptr ? *n_rows : N) * K;
-        const int id = e < live ? ids[e] : -1;
-        return static_cast<uint32_t>(id >= 0 ? id : V);
-    }
-};
-
-__global__ void __launch_bounds__(kSortThreads)
-    radix_count_kernel(const Pairs in, int shift, uint32_t* __restrict__ hist, int tiles) {
-    __shared__ uint32_t s_n[kRadix];
-    for (int d = threadIdx.x; d < kRadix; d += kSortThreads) s_n[d] = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < kRadixTile; j += kSortThreads) {
-        const int64_t e = static_cast<int64_t>(blockIdx.x) * kRadixTile + j;
-        if (e < in.entries) atomicAdd(&s_n[(in.key_of(e) >> shift) & (kRadix - 1)], 1u);
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < kRadix; d += kSortThreads)
-        hist[static_cast<size_t>(d) * tiles + blockIdx.x] = s_n[d];
-}
-
-// inclusive sum over the block's threads
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_sum_scan(uint32_t v, uint32_t* part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, v, off);
-        if (lane >= off) v += o;
-    }
-    if (lane == 31) part[warp] = v;
-    __syncthreads();
-    uint32_t before = 0;
-    for (int w = 0; w < warp; ++w) before += part[w];
-    __syncthreads();
-    return before + v;
-}
-
-// exclusive sums of n counts, in place, by one block
-__global__ void __launch_bounds__(1024) radix_scan_kernel(uint32_t* hist, int64_t n) {
-    __shared__ uint32_t part[32];
-    __shared__ uint32_t s_total;
-    uint32_t base = 0;
-    for (int64_t i0 = 0; i0 < n; i0 += 4096) {
-        const int64_t i = i0 + threadIdx.x * 4;      // n is a multiple of 512
-        uint4 v = i < n ? *reinterpret_cast<const uint4*>(hist + i) : uint4{};
-        const uint32_t own = v.x + v.y + v.z + v.w;
-        const uint32_t inc = base + block_sum_scan<1024>(own, part);
-        if (threadIdx.x == 1023) s_total = inc;
-        uint32_t run = inc - own;
-        uint4 out;
-        out.x = run, run += v.x;
-        out.y = run, run += v.y;
-        out.z = run, run += v.z;
-        out.w = run;
-        if (i < n) *reinterpret_cast<uint4*>(hist + i) = out;
-        __syncthreads();
-        base = s_total;
-    }
-}
-
-__global__ void __launch_bounds__(kSortThreads)
-    radix_place_kernel(const Pairs in, int shift, const uint32_t* __restrict__ hist, int tiles,
-                       uint32_t* __restrict__ key_out, uint32_t* __restrict__ slot_out) {
-    __shared__ uint32_t s_n[kSortWarps][kRadix];     // a warp's counts, then where its first goes
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int d = threadIdx.x; d < kRadix * kSortWarps; d += kSortThreads) (&s_n[0][0])[d] = 0;
-    __syncthreads();
-    constexpr int kRounds = kWarpPairs / 32;
-    uint32_t key[kRounds], rank[kRounds];
-    const int64_t e0 = static_cast<int64_t>(blockIdx.x) * kRadixTile + warp * kWarpPairs + lane;
-#pragma unroll
-    for (int q = 0; q < kRounds; ++q) key[q] = e0 + q * 32 < in.entries ? in.key_of(e0 + q * 32) : 0;
-#pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        const bool there = e0 + q * 32 < in.entries;
-        const uint32_t d = there ? (key[q] >> shift) & (kRadix - 1) : kRadix;
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
-        const int leader = __ffs(same) - 1;
-        uint32_t before = 0;
-        if (there && lane == leader) {
-            before = s_n[warp][d];
-            s_n[warp][d] = before + __popc(same);
-        }
-        rank[q] = __shfl_sync(0xffffffffu, before, leader) + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < kRadix; d += kSortThreads) {
-        uint32_t run = hist[static_cast<size_t>(d) * tiles + blockIdx.x];
-        for (int w = 0; w < kSortWarps; ++w) {
-            const uint32_t n = s_n[w][d];
-            s_n[w][d] = run;
-            run += n;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
-        const int64_t e = e0 + q * 32;
-        if (e >= in.entries) continue;
-        const uint32_t to = s_n[warp][(key[q] >> shift) & (kRadix - 1)] + rank[q];
-        key_out[to] = key[q];
-        slot_out[to] = in.slot != nullptr ? in.slot[e] : static_cast<uint32_t>(e);
-    }
-}
-
-// Each entry's GEMM row and remainder, in place of the sort's other buffers; where each token id's
-// entries begin and end.
-__global__ void __launch_bounds__(256)
-    topk_entries_kernel(const uint32_t* __restrict__ key, const uint32_t* __restrict__ slot,
-                        const float* __restrict__ val, int64_t entries, int K, uint32_t V,
-                        int* __restrict__ row, float* __restrict__ rest, int* __restrict__ first,
-                        int* __restrict__ last) {
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= entries) return;
-    const uint32_t v = key[e];
-    if (v >= V) return;
-    row[e] = static_cast<int>(slot[e] / static_cast<uint32_t>(K));
-    rest[e] = rest_of(val[slot[e]]);
-    if (e == 0 || key[e - 1] != v) first[v] = static_cast<int>(e);
-    if (e + 1 == entries || key[e + 1] != v) last[v] = static_cast<int>(e) + 1;
-}
-
-// A block a vocabulary chunk: its rows that have entries, ascending; the places of those with many.
-__global__ void __launch_bounds__(1024)
-    topk_index_kernel(const int* __restrict__ first, const int* __restrict__ last, int V,
-                      int* __restrict__ row_at, int* __restrict__ list, int* __restrict__ many,
-                      int2* __restrict__ counts) {
-    __shared__ uint32_t part[32];
-    __shared__ uint32_t s_total, s_many;
-    const int c0 = blockIdx.x * kBwdChunk, c1 = min(V, c0 + kBwdChunk);
-    if (threadIdx.x == 0) s_many = 0;
-    uint32_t base = 0;
-    for (int b0 = c0; b0 < c1; b0 += 4096) {
-        const int v0 = b0 + threadIdx.x * 4;
-        int4 end = make_int4(0, 0, 0, 0);
-        if (v0 + 3 < c1) {
-            end = *reinterpret_cast<const int4*>(last + v0);
-        } else {
-            if (v0 < c1) end.x = last[v0];
-            if (v0 + 1 < c1) end.y = last[v0 + 1];
-            if (v0 + 2 < c1) end.z = last[v0 + 2];
-        }
-        const int ends[4] = {end.x, end.y, end.z, end.w};
-        uint32_t own = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) own += ends[j] > 0;
-        const uint32_t inc = base + block_sum_scan<1024>(own, part);
-        if (threadIdx.x == 1023) s_total = inc;
-        uint32_t at = inc - own;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (v0 + j >= c1) continue;
-            const bool on = ends[j] > 0;
-            row_at[v0 + j] = on ? static_cast<int>(at) : -1;
-            if (!on) continue;
-            list[c0 + at] = v0 + j;
-            if (ends[j] - first[v0 + j] > kMany)
-                many[c0 + atomicAdd(&s_many, 1u)] = static_cast<int>(at);   // in no order: each by itself
-            ++at;
-        }
-        __syncthreads();
-        base = s_total;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0)
-        counts[blockIdx.x] = make_int2(static_cast<int>(base), static_cast<int>(s_many));
 }
 
 }  // namespace
@@ -674,73 +335,11 @@ cudaError_t launch_topk_coef(const TopkSlots& slots, const float* grad, const fl
 }
 
 cudaError_t launch_topk_scatter(const int* ids, const float* val, const int* n_rows, int N, int K,
-                                int c0, int width, void* ds, bool lo, cudaStream_t stream) {
+                                int c0, int width, void* ds, cudaStream_t stream) {
     const size_t blocks = (static_cast<size_t>(N) * K + 255) / 256, most = 152 * 8;
     const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(ds);
-    return launch_early(lo ? topk_scatter_kernel<true> : topk_scatter_kernel<false>, dim3(grid), 256,
-                        0, stream, nullptr, ids, val, n_rows, N, K, c0, width, to);
-}
-
-cudaError_t launch_topk_dh(const int* ids, const float* val, const int* n_rows, int N, int K,
-                           const void* weight, int H, float* dh_acc, cudaStream_t stream) {
-    const int vecs = H / 8;
-    const dim3 grid(N, (vecs + kRowThreads - 1) / kRowThreads);
-    return launch_early(topk_dh_kernel, grid, kRowThreads, 0, stream, nullptr, ids, val, n_rows, N, K,
-                        static_cast<const uint4*>(weight), vecs, dh_acc);
-}
-
-cudaError_t launch_topk_rows(const TopkRows& rows, int chunk, const void* hidden, int H,
-                             cudaStream_t stream) {
-    const int vecs = H / 8, blocks = (rows.places + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    const uint4* h = static_cast<const uint4*>(hidden);
-    topk_rows_kernel<<<blocks < 152 * 8 ? blocks : 152 * 8, kRowThreads, 0, stream>>>(rows, chunk, h,
-                                                                                      vecs);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    topk_many_kernel<<<152 * 8, kRowThreads, 0, stream>>>(rows, chunk, h, vecs);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_topk_sort(const TopkKlBwdLayout& lay, uint8_t* ws, const int* n_rows, int N, int K,
-                             int V, TopkRows* out, cudaStream_t stream) {
-    const int64_t entries = static_cast<int64_t>(N) * K;
-    const int tiles = static_cast<int>(lay.tiles);
-    uint32_t* key[2];
-    uint32_t* slot[2];
-    for (int i = 0; i < 2; ++i) {
-        key[i] = reinterpret_cast<uint32_t*>(ws + lay.key_off[i]);
-        slot[i] = reinterpret_cast<uint32_t*>(ws + lay.slot_off[i]);
-    }
-    uint32_t* hist = reinterpret_cast<uint32_t*>(ws + lay.hist_off);
-    Pairs in{reinterpret_cast<const int*>(ws + lay.ids_off), nullptr, nullptr, n_rows, entries, N, K, V};
-    int at = 0;
-    for (int shift = 0; shift < 32 && (V >> shift) != 0; shift += kRadixBits, at ^= 1) {
-        radix_count_kernel<<<tiles, kSortThreads, 0, stream>>>(in, shift, hist, tiles);
-        radix_scan_kernel<<<1, 1024, 0, stream>>>(hist, static_cast<int64_t>(tiles) * kRadix);
-        radix_place_kernel<<<tiles, kSortThreads, 0, stream>>>(in, shift, hist, tiles, key[at],
-                                                               slot[at]);
-        in.key = key[at];
-        in.slot = slot[at];
-    }
-    int* first = reinterpret_cast<int*>(ws + lay.first_off);
-    int* last = reinterpret_cast<int*>(ws + lay.last_off);
-    int* row = reinterpret_cast<int*>(key[at]);          // the buffers that the last pass read
-    float* rest = reinterpret_cast<float*>(slot[at]);
-    const int chunks = (V + kBwdChunk - 1) / kBwdChunk;
-    cudaError_t e = cudaMemsetAsync(last, 0, static_cast<size_t>(V) * 4, stream);
-    if (e != cudaSuccess) return e;
-    topk_entries_kernel<<<static_cast<unsigned>((entries + 255) / 256), 256, 0, stream>>>(
-        in.key, in.slot, reinterpret_cast<const float*>(ws + lay.val_off), entries, K,
-        static_cast<uint32_t>(V), row, rest, first, last);
-    int* row_at = reinterpret_cast<int*>(ws + lay.at_off);
-    int* list = reinterpret_cast<int*>(ws + lay.list_off);
-    int* many = reinterpret_cast<int*>(ws + lay.many_off);
-    int2* counts = reinterpret_cast<int2*>(ws + lay.counts_off);
-    topk_index_kernel<<<chunks, 1024, 0, stream>>>(first, last, V, row_at, list, many, counts);
-    *out = TopkRows{row, rest, first, last, row_at, list, many, counts, ws + lay.sums_off,
-                    static_cast<int>(lay.places)};
-    return cudaGetLastError();
+    return launch_early(topk_scatter_kernel, dim3(grid), 256, 0, stream, nullptr, ids, val, n_rows, N,
+                        K, c0, width, static_cast<__nv_bfloat16*>(ds));
 }
 
 }  // namespace rlk
