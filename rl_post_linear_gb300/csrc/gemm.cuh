@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (PAIR) {
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[buf ^ 1u]), 0));
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[buf]), 0));
+                            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[buf ^ 1u]), 0));
+                            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[buf]), 0));
                         } else {
                             mbar_arrive(&tmem_empty[buf ^ 1u]);
                             mbar_arrive(&tmem_empty[buf]);
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(64 + 32 * P::kEpiWarps, 1)
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (PAIR)
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&tmem_empty[buf]), 0));
+                            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tmem_empty[buf]), 0));
                         else
                             mbar_arrive(&tmem_empty[buf]);
                     }

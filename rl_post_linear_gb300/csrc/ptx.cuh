@@ -283,23 +283,22 @@ __device__ __forceinline__ void cluster_sync() {
                      "memory");
 }
 
-// arrive on an mbarrier given by its shared::cluster address.  What it hands over to the peer CTA is
-// TMEM, whose reads are behind tcgen05.wait and tcgen05.fence, and nothing in memory: a release at
-// cluster scope would wait for all that the epilogue has stored so far, 1500 cycles and more a tile
+// arrive on an mbarrier given by its shared::cluster address, without ordering any memory: what it
+// hands over to the peer CTA is TMEM, whose reads are behind tcgen05.wait and tcgen05.fence.  A release
+// at cluster scope would wait for all that the epilogue has stored so far, 1500 cycles and more a tile
 // where HBM is busy (dW of [14, 4096] against V = 151936: 358 us, without 265).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                      bar_cluster_addr)
                  : "memory");
 }
 
-// try_wait on a barrier that receives arrivals from the peer CTA or its TMA loads; what these hand
-// over is TMEM, and shared memory that tcgen05.mma alone reads
+// try_wait with acquire at cluster scope (the barrier receives arrivals from the peer CTA)
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
         : "r"(smem_u32(bar)), "r"(parity)
