@@ -570,44 +570,55 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     };
     uint32_t* columns = segkey;                  // read until here
     uint32_t n = kList + 1;
-    if (queued <= static_cast<uint32_t>(min(kQueue, kPieces >> log_pieces))) {
-        // which columns of each piece reach the bound, a bit each
-        const int pieces = static_cast<int>(queued) << log_pieces;
+    if (queued <= kQueue) {
+        // as many segments at a time as there is room for their pieces: all of them up to V = 163840
+        // fp32 and 327680 bf16, 64 at V = 2^22 (a search by digits instead, K = 1024 of [16, 262144]
+        // fp32: 1307 us)
+        const uint32_t room = kPieces >> log_pieces;
         const float least = key_value(bound);    // x >= least where its key reaches the bound
-        constexpr int kAhead = 4;
-        for (int i0 = tid; i0 < pieces; i0 += kAhead * THREADS) {
-            uint4 v[kAhead];
+        n = 0;
+        for (uint32_t q0 = 0; q0 < queued && n <= static_cast<uint32_t>(plan.list); q0 += room) {
+            if (q0 > 0) __syncthreads();         // the bits are read until here
+            // which columns of each piece reach the bound, a bit each
+            const int first = static_cast<int>(q0) << log_pieces;
+            const int pieces = static_cast<int>(min(room, queued - q0)) << log_pieces;
+            constexpr int kAhead = 4;
+            for (int i0 = tid; i0 < pieces; i0 += kAhead * THREADS) {
+                uint4 v[kAhead];
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                const int i = i0 + q * THREADS, c = i < pieces ? piece_column(i) : a.V;
-                // past the row: NaN, which reaches nothing
-                v[q] = make_uint4(~0u, ~0u, ~0u, ~0u);
-                if (c < a.V) v[q] = load_piece<T, ALIGNED>(x_row, a.V, c);
-            }
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    bits |= piece_value<T>(v[q], e) >= least ? 1u << e : 0u;
-                if (i0 + q * THREADS < pieces) sh.bits[i0 + q * THREADS] = static_cast<uint8_t>(bits);
-            }
-        }
-        if (tid < 3) sh.bits[pieces + tid] = 0;
-        __syncthreads();
-        // the columns, in the pieces' order: four pieces at a time
-        const uint32_t* bits4 = reinterpret_cast<const uint32_t*>(sh.bits);
-        const int words = (pieces + 3) / 4, each = (words + THREADS - 1) / THREADS;
-        const int w0 = min(words, tid * each), w1 = min(words, w0 + each);
-        uint32_t own = 0;
-        for (int w = w0; w < w1; ++w) own += __popc(bits4[w]);
-        uint32_t at = block_prefix<THREADS>(own, sh, n);
-        if (n <= static_cast<uint32_t>(plan.list))
-            for (int w = w0; w < w1; ++w)
-                for (uint32_t b = bits4[w]; b != 0; b &= b - 1) {
-                    const int bit = __ffs(b) - 1;
-                    columns[at++] = piece_column(4 * w + bit / 8) + bit % 8;
+                for (int q = 0; q < kAhead; ++q) {
+                    const int i = i0 + q * THREADS, c = i < pieces ? piece_column(first + i) : a.V;
+                    // past the row: NaN, which reaches nothing
+                    v[q] = make_uint4(~0u, ~0u, ~0u, ~0u);
+                    if (c < a.V) v[q] = load_piece<T, ALIGNED>(x_row, a.V, c);
                 }
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    uint32_t bits = 0;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        bits |= piece_value<T>(v[q], e) >= least ? 1u << e : 0u;
+                    if (i0 + q * THREADS < pieces)
+                        sh.bits[i0 + q * THREADS] = static_cast<uint8_t>(bits);
+                }
+            }
+            if (tid < 3) sh.bits[pieces + tid] = 0;
+            __syncthreads();
+            // the columns, in the pieces' order: four pieces at a time
+            const uint32_t* bits4 = reinterpret_cast<const uint32_t*>(sh.bits);
+            const int words = (pieces + 3) / 4, each = (words + THREADS - 1) / THREADS;
+            const int w0 = min(words, tid * each), w1 = min(words, w0 + each);
+            uint32_t own = 0, found;
+            for (int w = w0; w < w1; ++w) own += __popc(bits4[w]);
+            uint32_t at = n + block_prefix<THREADS>(own, sh, found);
+            n += found;
+            if (n <= static_cast<uint32_t>(plan.list))
+                for (int w = w0; w < w1; ++w)
+                    for (uint32_t b = bits4[w]; b != 0; b &= b - 1) {
+                        const int bit = __ffs(b) - 1;
+                        columns[at++] = piece_column(first + 4 * w + bit / 8) + bit % 8;
+                    }
+        }
     }
     clear_hist<THREADS>(sh);
     __syncthreads();
